@@ -11,6 +11,10 @@ from .binding import (  # noqa: F401
     Lut,
     backward,
     build_lut,
+    cache_append,
+    cache_forward,
+    cache_resize,
+    cache_workspace,
     forward,
     forward_ext,
     library_path,

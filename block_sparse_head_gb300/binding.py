@@ -7,6 +7,7 @@ a call returns an error; there is no fallback path.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import threading
@@ -31,8 +32,12 @@ EXPORTED = (
     "bsa_wait_selftest",
     "bsa_status_string", "bsa_version", "bsa_forward_noalloc", "bsa_debug_expire_wait",
     "bsa_build_lut_rect", "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
-    "bsa_backward", "bsa_topk_forward",
+    "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
+    "bsa_cache_forward", "bsa_cache_workspace",
 )
+
+_ACTIVATIONS = {torch.bfloat16: 0, torch.float16: 1}          # BSA_BF16, BSA_FP16
+_CACHE_TYPES = {torch.float8_e4m3fn: 2, torch.int8: 3}        # BSA_E4M3, BSA_INT8
 
 
 class ExtArgs(ctypes.Structure):
@@ -40,6 +45,20 @@ class ExtArgs(ctypes.Structure):
     _fields_ = [("window_left", ctypes.c_int), ("window_right", ctypes.c_int),
                 ("softcap", ctypes.c_float), ("sinks", ctypes.c_void_p),
                 ("q_segment_ids", ctypes.c_void_p), ("kv_segment_ids", ctypes.c_void_p)]
+
+
+class Cache(ctypes.Structure):
+    """bsa_cache of include/bsa.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int),
+                ("kv_heads", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
+                ("dtype", ctypes.c_int)]
+
+
+class CacheArgs(ctypes.Structure):
+    """bsa_cache_args of include/bsa.h."""
+    _fields_ = [("window", ctypes.c_int), ("softcap", ctypes.c_float), ("sinks", ctypes.c_void_p),
+                ("lut", ctypes.c_void_p), ("block", ctypes.c_int)]
 
 _lib = None
 _lock = threading.Lock()
@@ -83,6 +102,13 @@ def load_library():
         lib.bsa_topk_forward.argtypes = [vp, vp, vp, vp, vp, vp, vp, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                          ctypes.c_float, vp]
+        ci, i64 = ctypes.c_int, ctypes.c_int64
+        lib.bsa_cache_resize.argtypes = [vp] * 10 + [ci] * 5 + [vp]
+        lib.bsa_cache_append.argtypes = [ctypes.POINTER(Cache), vp, vp, vp, ci, ci, i64, i64, i64,
+                                         i64, vp]
+        lib.bsa_cache_forward.argtypes = [ctypes.POINTER(Cache)] + [vp] * 8 + [i64] + [ci] * 6 + \
+            [i64, i64, ctypes.c_float, ctypes.POINTER(CacheArgs), vp]
+        lib.bsa_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(i64)]
         lib.bsa_lut_export_csc.argtypes = [vp, vp, vp, vp]
         lib.bsa_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
@@ -114,7 +140,8 @@ def load_library():
                      "bsa_forward", "bsa_device_status", "bsa_set_schedule", "bsa_set_wait_limit",
                      "bsa_wait_selftest", "bsa_debug_expire_wait", "bsa_build_lut_rect",
                      "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
-                     "bsa_backward", "bsa_topk_forward"):
+                     "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
+                     "bsa_cache_forward", "bsa_cache_workspace"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -353,6 +380,171 @@ def topk_forward(q: torch.Tensor, kv: torch.Tensor, sink: torch.Tensor, idx: tor
                                 idx.data_ptr(), out.data_ptr(), lse.data_ptr(), status.data_ptr(),
                                 B, M, N, H, D, K, float(scale), _stream_handle(stream)),
            "bsa_topk_forward")
+    return out, lse, status
+
+
+def _dev_ptr(t, name: str, dtype, shape) -> int:
+    """Pointer of a contiguous CUDA tensor of this type and shape on the current device.
+    The cache calls launch on the current device, so a tensor elsewhere is refused."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or \
+            not t.is_contiguous() or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    return t.data_ptr()
+
+
+def _rows_ptr(t, name: str, heads: int | None, d: int):
+    """Pointer and (token, head) strides of a [T, heads, d] activation tensor whose numbers
+    of one head are contiguous."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _ACTIVATIONS or \
+            t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [T, heads, {d}]")
+    if t.stride(2) != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    # The stride of a dimension of one is never used, whatever the tensor says.
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+
+
+def _on(stream):
+    """Context in which a call allocates what the caller did not give it: memory of the
+    stream that the call runs on, so that neither earlier nor later work of the current
+    stream touches it meanwhile."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream))
+    return torch.cuda.stream(stream)
+
+
+def _cache_view(k_cache, v_cache, k_scale, v_scale) -> Cache:
+    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or \
+            k_cache.dtype not in _CACHE_TYPES:
+        raise ValueError("k_cache must be float8_e4m3fn or int8 [pages, kv_heads, page, d]")
+    pages, heads, page, d = k_cache.shape
+    return Cache(_dev_ptr(k_cache, "k_cache", k_cache.dtype, k_cache.shape),
+                 _dev_ptr(v_cache, "v_cache", k_cache.dtype, k_cache.shape),
+                 _dev_ptr(k_scale, "k_scale", torch.float32, (pages, heads)),
+                 _dev_ptr(v_scale, "v_scale", torch.float32, (pages, heads)),
+                 pages, heads, page, d, _CACHE_TYPES[k_cache.dtype])
+
+
+def cache_resize(block_table: torch.Tensor, kv_len: torch.Tensor, new_len: torch.Tensor,
+                 free_pages: torch.Tensor, free_count: torch.Tensor, page: int, tokens: int,
+                 kv_len_out: torch.Tensor | None = None, free_count_out: torch.Tensor | None = None,
+                 cu_new: torch.Tensor | None = None, slots: torch.Tensor | None = None,
+                 status: torch.Tensor | None = None, stream=None):
+    """Block tables and slots from request lengths (bsa_cache_resize).  int32 on the current
+    device: block_table [B, max_pages], kv_len and new_len [B], free_pages [pages], free_count
+    [1]; ``tokens`` is the capacity of the packed new tokens.  kv_len and free_count are
+    updated in place unless other outputs are given.  Returns (cu_new [B + 1], slots
+    [tokens], status [1]); a nonzero status means that nothing was changed."""
+    lib = load_library()
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, max_pages]")
+    B, max_pages = block_table.shape
+    i32 = torch.int32
+    tokens = int(tokens)
+    if tokens < 0:
+        raise ValueError("tokens must not be negative")
+    dev = block_table.device
+    kv_len_out = kv_len if kv_len_out is None else kv_len_out
+    free_count_out = free_count if free_count_out is None else free_count_out
+    with _on(stream):
+        cu_new = torch.empty(B + 1, dtype=i32, device=dev) if cu_new is None else cu_new
+        slots = torch.empty(tokens, dtype=i32, device=dev) if slots is None else slots
+        status = torch.empty(1, dtype=i32, device=dev) if status is None else status
+    n_pages = free_pages.numel()
+    _check(lib.bsa_cache_resize(
+        _dev_ptr(block_table, "block_table", i32, (B, max_pages)),
+        _dev_ptr(kv_len, "kv_len", i32, (B,)), _dev_ptr(new_len, "new_len", i32, (B,)),
+        _dev_ptr(free_pages, "free_pages", i32, (n_pages,)),
+        _dev_ptr(free_count, "free_count", i32, (1,)), _dev_ptr(kv_len_out, "kv_len_out", i32, (B,)),
+        _dev_ptr(free_count_out, "free_count_out", i32, (1,)),
+        _dev_ptr(cu_new, "cu_new", i32, (B + 1,)), _dev_ptr(slots, "slots", i32, (tokens,)),
+        _dev_ptr(status, "status", i32, (1,)), B, max_pages, n_pages, int(page), tokens,
+        _stream_handle(stream)), "bsa_cache_resize")
+    return cu_new, slots, status
+
+
+def cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache: torch.Tensor,
+                 v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                 stream=None) -> None:
+    """Quantise new keys and values into the cache (bsa_cache_append).  k, v: bf16 or fp16
+    [T, kv_heads, d], any token and head stride; slots int32 [T] (cache_resize; -1: skip);
+    caches float8_e4m3fn or int8 [pages, kv_heads, page, d], scales fp32 [pages, kv_heads],
+    all on the current device and updated in place."""
+    lib = load_library()
+    c = _cache_view(k_cache, v_cache, k_scale, v_scale)
+    kp, kt, kh = _rows_ptr(k, "k", c.kv_heads, c.d)
+    vp, vt, vh = _rows_ptr(v, "v", c.kv_heads, c.d)
+    if v.dtype != k.dtype or v.shape != k.shape:
+        raise ValueError("k and v must have one type and shape")
+    T = k.shape[0]
+    _check(lib.bsa_cache_append(ctypes.byref(c), kp, vp, _dev_ptr(slots, "slots", torch.int32, (T,)),
+                                T, _ACTIVATIONS[k.dtype], kt, kh, vt, vh, _stream_handle(stream)),
+           "bsa_cache_append")
+
+
+def cache_workspace(heads: int, kv_heads: int, d: int, max_q: int) -> torch.Tensor:
+    """A workspace for cache_forward on the current device; calls that may overlap on the
+    GPU need one each."""
+    lib = load_library()
+    n = ctypes.c_int64()
+    _check(lib.bsa_cache_workspace(int(heads), int(kv_heads), int(d), int(max_q), ctypes.byref(n)),
+           "bsa_cache_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
+
+
+def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                  k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                  kv_len: torch.Tensor, cu_q: torch.Tensor, scale: float, max_q: int | None = None,
+                  window: int | None = None, softcap: float = 0.0,
+                  sinks: torch.Tensor | None = None, lut: Lut | None = None,
+                  block: int | None = None, out: torch.Tensor | None = None,
+                  lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Attention of the newest tokens of every request over its cache (bsa_cache_forward).
+    q: bf16 or fp16 [T, heads, d], any token and head stride, packed by cu_q int32 [B + 1];
+    caches and scales as in cache_append; block_table int32 [B, max_pages], kv_len int32 [B]
+    with the new tokens counted.  ``max_q``: the most queries of a request (T when None);
+    ``window``: keys further back than that are masked (None or negative: no bound); ``lut``
+    with ``block``: only the layout's active blocks, one layout head per kv head.  Returns
+    (out [T, heads, d], lse fp32 [T, heads], status int32 [1]); a nonzero status (read after
+    the stream is synchronized) means a bounded wait gave up."""
+    lib = load_library()
+    c = _cache_view(k_cache, v_cache, k_scale, v_scale)
+    qp, qt, qh = _rows_ptr(q, "q", None, c.d)
+    T, heads, d = q.shape
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, max_pages]")
+    B, max_pages = block_table.shape
+    if lut is not None and block is None:
+        raise ValueError("a lut needs its block")
+    max_q = max(T, 1) if max_q is None else int(max_q)
+    with _on(stream):
+        if out is None:
+            out = torch.empty(T, heads, d, dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.empty(T, heads, dtype=torch.float32, device=q.device)
+        if status is None:
+            status = torch.empty(1, dtype=torch.int32, device=q.device)
+        if workspace is None:
+            workspace = cache_workspace(heads, c.kv_heads, d, max_q)
+    x = CacheArgs(-1 if window is None else int(window), float(softcap),
+                  None if sinks is None else _dev_ptr(sinks, "sinks", torch.float32, (heads,)),
+                  None if lut is None else lut.handle, 0 if block is None else int(block))
+    i32 = torch.int32
+    _check(lib.bsa_cache_forward(
+        ctypes.byref(c), qp, _dev_ptr(block_table, "block_table", i32, (B, max_pages)),
+        _dev_ptr(kv_len, "kv_len", i32, (B,)), _dev_ptr(cu_q, "cu_q", i32, (B + 1,)),
+        _dev_ptr(out, "out", q.dtype, (T, heads, d)), _dev_ptr(lse, "lse", torch.float32, (T, heads)),
+        _dev_ptr(status, "status", i32, (1,)),
+        _dev_ptr(workspace, "workspace", torch.uint8, (workspace.numel(),)), workspace.numel(),
+        B, max_pages, T, heads, max_q, _ACTIVATIONS[q.dtype], qt, qh, float(scale), ctypes.byref(x),
+        _stream_handle(stream)), "bsa_cache_forward")
     return out, lse, status
 
 

@@ -210,8 +210,9 @@ bool bsa::schedule_by_head(int policy, int64_t B, int64_t H, int64_t L, int64_t 
 namespace {
 
 void free_device(bsa_lut* lut) {
+  if (lut->d_row_ptr) cudaFree(lut->d_row_ptr);
   if (lut->d_row_idx) cudaFree(lut->d_row_idx);
-  lut->d_row_idx = nullptr;
+  lut->d_row_ptr = lut->d_row_idx = nullptr;
   for (int o = 0; o < 2; ++o) {
     if (lut->d_items_t[o]) cudaFree(lut->d_items_t[o]);
     if (lut->d_sched_start_t[o]) cudaFree(lut->d_sched_start_t[o]);
@@ -410,7 +411,9 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
   const size_t nc = std::max<size_t>(lut->col_idx.size(), 1) * 4;
   const size_t ni = std::max<size_t>(lut->items.size(), 4) * 4;
   const size_t ns = lut->sched_start[0].size() * 4;
-  if (cudaMalloc(&lut->d_col_idx, nc) != cudaSuccess || cudaMalloc(&lut->d_items, ni) != cudaSuccess ||
+  const size_t np = lut->row_ptr.size() * 4;
+  if (cudaMalloc(&lut->d_col_idx, nc) != cudaSuccess ||
+      cudaMalloc(&lut->d_row_ptr, np) != cudaSuccess || cudaMalloc(&lut->d_items, ni) != cudaSuccess ||
       cudaMalloc(&lut->d_status, 16) != cudaSuccess ||
       cudaMalloc(&lut->d_sched_start, ns) != cudaSuccess ||
       cudaMalloc(&lut->d_items_g, ni) != cudaSuccess ||
@@ -422,6 +425,8 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
   bool ok = (lut->col_idx.empty() ||
              cudaMemcpyAsync(lut->d_col_idx, lut->col_idx.data(), lut->col_idx.size() * 4,
                              cudaMemcpyHostToDevice, st) == cudaSuccess) &&
+            cudaMemcpyAsync(lut->d_row_ptr, lut->row_ptr.data(), np, cudaMemcpyHostToDevice, st) ==
+                cudaSuccess &&
             (rec[0].empty() ||
              (cudaMemcpyAsync(lut->d_items, rec[0].data(), rec[0].size() * 4,
                               cudaMemcpyHostToDevice, st) == cudaSuccess &&
@@ -731,7 +736,7 @@ const char* bsa_status_string(int status) {
     case BSA_ERR_DEVICE_TIMEOUT: return "bounded wait timed out on the device";
     case BSA_ERR_STATE: return "LUT not uploaded to the current device";
     case BSA_ERR_ALLOC: return "allocation failed";
-    case BSA_ERR_TOO_LARGE: return "LUT too large for the fixed 4 MiB no-allocation scratch";
+    case BSA_ERR_TOO_LARGE: return "LUT or workspace need exceeds the scratch given";
     default: return "unknown status";
   }
 }

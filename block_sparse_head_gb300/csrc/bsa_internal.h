@@ -7,6 +7,8 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include "../../include/bsa.h"
+
 // The look-up table behind the opaque bsa_lut handle of bsa.h.
 struct bsa_lut {
   int H = 0, nb = 0, batch = 0, order = 0;
@@ -40,6 +42,7 @@ struct bsa_lut {
   int32_t* d_sched_start = nullptr;  // device copy of sched_start[0] (d_items: records of sched_items[0])
   int32_t* d_items_g = nullptr;        // records of sched_items[1]
   int32_t* d_sched_start_g = nullptr;  // sched_start[1]
+  int32_t* d_row_ptr = nullptr;        // row_ptr (attention over a cache looks rows up by position)
   int32_t* d_row_idx = nullptr;        // column view: row_idx
   int32_t* d_items_t[2] = {nullptr, nullptr};        // records of both column schedules
   int32_t* d_sched_start_t[2] = {nullptr, nullptr};
@@ -176,6 +179,66 @@ cudaError_t launch_bwd_b128_d128(bool kv, const BwdParams& p, const CUtensorMap&
                                  int grid, cudaStream_t stream);
 // delta[r] = sum_x dout[r,x] out[r,x] over `rows` rows of d bf16 (fp32 result).
 cudaError_t launch_bwd_delta(const void* out, const void* dout, float* delta, int64_t rows, int d,
+                             cudaStream_t stream);
+
+// Element types of the cache calls: bf16 / fp16 activations, e4m3 / int8 caches (BSA_* of
+// bsa.h).  kMaxResizeBatch: requests that one bsa_cache_resize takes (its prefix sums sit in
+// shared memory).
+constexpr int kMaxResizeBatch = 8192;
+
+struct CacheResizeParams {
+  int32_t* table;            // [B, max_pages]
+  const int32_t* kv_len;     // [B]
+  const int32_t* new_len;    // [B]
+  int32_t* free_pages;       // [n_pages], a stack
+  const int32_t* free_count; // [1]
+  int32_t* kv_len_out;       // [B], may be kv_len
+  int32_t* free_count_out;   // [1], may be free_count
+  int32_t* cu_new;           // [B + 1]
+  int32_t* slots;            // [tokens]
+  int32_t* status;           // [1]
+  int B, max_pages, n_pages, tokens;
+  int page_shift;            // log2(page)
+};
+cudaError_t launch_cache_resize(const CacheResizeParams& p, cudaStream_t stream);
+
+struct CacheAppendParams {
+  const void* x[2];          // new keys, new values: [T, heads, d]
+  int64_t token_stride[2], head_stride[2];  // in elements
+  void* cache[2];            // [n_pages, heads, page, d], 8 bits
+  float* scale[2];           // [n_pages, heads]
+  const int32_t* slots;      // [T]
+  int T, heads, n_pages;
+  int page_shift;
+};
+cudaError_t launch_cache_append(int d, int dtype, int cache_dtype, const CacheAppendParams& p,
+                                cudaStream_t stream);
+
+struct CacheFwdParams {
+  const void* q;             // [T, Hq, d] with strides
+  int64_t q_token_stride, q_head_stride;  // in elements
+  const uint8_t* k_cache;    // [n_pages, Hkv, page, d]
+  const uint8_t* v_cache;
+  const float* k_scale;      // [n_pages, Hkv]
+  const float* v_scale;
+  const int32_t* table;      // [B, max_pages]
+  const int32_t* kv_len;     // [B]
+  const int32_t* cu_q;       // [B + 1]
+  const int32_t* row_ptr;    // layout rows (null: dense)
+  const int32_t* col_idx;
+  void* out;                 // [T, Hq, d]
+  float* lse;                // [T, Hq]
+  int32_t* status;           // [1]
+  const float* sinks;        // [Hq] or null
+  int B, T, Hq, Hkv, group;  // group = Hq / Hkv
+  int n_pages, max_pages, page_shift;
+  int nb, block_shift;       // layout rows per head, log2 of its block
+  int window;                // keys before position - window are masked (< 0: no bound)
+  float scale_log2;          // scale * log2(e)
+  float softcap_log2;        // cap * log2(e); 0: no soft-cap
+  float softcap_inv;         // scale / cap
+};
+cudaError_t launch_cache_fwd(int d, int dtype, int cache_dtype, const CacheFwdParams& p,
                              cudaStream_t stream);
 
 // One-CTA kernel whose only wait never completes; it must give up after limit_ns.

@@ -53,7 +53,7 @@ typedef enum bsa_status {
   BSA_ERR_STATE = -9,          /* the LUT has not been uploaded to a device            */
   BSA_ERR_ALLOC = -10,         /* host or device allocation failed                     */
   BSA_ERR_TOO_LARGE = -11      /* LUT does not fit the fixed scratch of
-                                  bsa_forward_noalloc                                   */
+                                  bsa_forward_noalloc, or a workspace is too small      */
 } bsa_status;
 
 /* Work-list orders accepted by bsa_build_lut. */
@@ -328,6 +328,171 @@ int bsa_topk_forward(const void* q, const void* kv, const float* sink, const int
 int bsa_forward_noalloc(const void* q, const void* k, const void* v, const bsa_lut* lut,
                         void* out, float* lse, int B, int H, int L, int d, float scale, int block,
                         int causal_diag, void* stream, int sync_status);
+
+/*
+ * ---------------------------------------------------------------- paged 8-bit cache
+ *
+ * Answering with a trained model one token (or one chunk) at a time.  Keys and values of
+ * all requests live in pages of `page` tokens, 8 bits a number, with one fp32 scale for
+ * each page and key/value head; a block table lists each request's pages in order.  A
+ * serving step calls, on one stream:
+ *
+ *   bsa_cache_resize    the lengths that the requests are to have -> block tables, packed
+ *                       offsets and the cache slot of every new token
+ *   bsa_cache_append    the new tokens' keys and values -> the cache
+ *   bsa_cache_forward   the new tokens' queries -> attention over the cache, dense or over
+ *                       the active blocks of a LUT (the layout the model was trained with)
+ *
+ * All three are asynchronous, allocate nothing, keep nothing between calls and read every
+ * length on the device, so a step with fixed T and B can be captured in a CUDA graph once
+ * and replayed as the requests grow.  Packed tensors hold the new tokens of request 0, then
+ * of request 1 and so on ([T, heads, d]); T may exceed their number, and rows behind the
+ * last request are neither read nor written.
+ */
+
+/* Element types of the cache calls. */
+enum {
+  BSA_BF16 = 0, /* activations: queries, new keys and values, output */
+  BSA_FP16 = 1,
+  BSA_E4M3 = 2, /* cache: 8-bit floating point, 4 exponent and 3 mantissa bits, up to 448 */
+  BSA_INT8 = 3  /* cache: two's complement, used from -127 to 127 */
+};
+
+/* A cache.  Key c of the token page holds k_scale[page][head] * k[page][head][c][:]. */
+typedef struct bsa_cache {
+  void* k;        /* device, 8-bit [n_pages, kv_heads, page, d], 16-byte aligned */
+  void* v;        /* the same for values                                         */
+  float* k_scale; /* device, fp32 [n_pages, kv_heads]                            */
+  float* v_scale;
+  int n_pages;
+  int kv_heads;
+  int page;       /* tokens of a page: 16, 32, 64 or 128; n_pages * page < 2^31  */
+  int d;          /* head dim: 64 or 128                                         */
+  int dtype;      /* BSA_E4M3 or BSA_INT8                                        */
+} bsa_cache;
+
+/*
+ * bsa_cache_resize -- request b goes from kv_len[b] to new_len[b] tokens, b in [0, B).
+ * A growing request takes ceil(new / page) - ceil(old / page) pages, a shrinking one gives
+ * back those behind its new length (new_len 0 ends it; drafts that were turned down are
+ * taken back the same way).
+ *
+ *   block_table     device int32 [B, max_pages].  Entry (b, j) is the page of tokens
+ *                   [j*page, (j+1)*page) of request b.  Entries of new pages are written;
+ *                   all others, also those behind the end, stay as they are.
+ *   kv_len, new_len device int32 [B].
+ *   free_pages      device int32 [n_pages], free_count device int32 [1]: a stack of free
+ *                   pages.  Freed pages are pushed first, in the order of requests and
+ *                   pages; new pages are then popped in the same order.
+ *   kv_len_out      device int32 [B], receives the new lengths; may be kv_len itself.
+ *   free_count_out  device int32 [1]; may be free_count itself.
+ *   cu_new          device int32 [B + 1]: cu_new[b] = new tokens of requests before b.
+ *   slots           device int32 [tokens]: page * page_size + offset of each new token in
+ *                   packed order, -1 behind the last (NULL when tokens is 0).
+ *   status          device int32 [1], written: 0, or the call changed nothing (lengths and
+ *                   count come out as they went in, cu_new all 0, slots all -1) because
+ *                     > 0          that many pages are missing
+ *                     -1 - b       request b is the first with a length below 0 or above
+ *                                  max_pages * page
+ *                     INT32_MIN    there are more than `tokens` new tokens
+ *                     INT32_MIN+1  free_count is not in [0, n_pages], or the freed pages
+ *                                  do not fit the stack
+ *   B               1 to 8192.
+ *
+ * One kernel launch.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_UNSUPPORTED (page),
+ * BSA_ERR_ALIGN (4-byte), BSA_ERR_CUDA.
+ */
+int bsa_cache_resize(int32_t* block_table, const int32_t* kv_len, const int32_t* new_len,
+                     int32_t* free_pages, const int32_t* free_count, int32_t* kv_len_out,
+                     int32_t* free_count_out, int32_t* cu_new, int32_t* slots, int32_t* status,
+                     int B, int max_pages, int n_pages, int page, int tokens, void* stream);
+
+/*
+ * bsa_cache_append -- new keys and values into the cache.  A page's new tokens are a run
+ * of consecutive tokens with slots in that page, ascending by one; the run's first slot
+ * says how many of the page's tokens are kept (those before it; what lies behind the run
+ * is no longer valid).  For each run and head, and K and V each:
+ *
+ *   need = the smallest power of two in [2^-60, 2^60] with max |x| <= largest * need, over
+ *          the run's finite numbers; largest = 448 (e4m3) or 127 (int8)
+ *   s    = max(need, old scale if tokens are kept)
+ *   kept numbers:  y <- round(y * old / s)          new numbers:  round(x * (1 / s))
+ *
+ * rounding to the nearest stored number, ties to even, saturating.  Infinities saturate;
+ * NaN stays NaN in e4m3 and becomes 0 in int8.  A growing power of two costs a kept e4m3
+ * number nothing but underflow and a kept int8 number less than one step in all.
+ *
+ *   k, v    device, dtype BSA_BF16 or BSA_FP16, [T, kv_heads, d]: element (t, h, x) at
+ *           t * token_stride + h * head_stride + x (strides in elements, multiples of 8;
+ *           rows of a fused projection are passed as they are), 16-byte aligned.
+ *   slots   device int32 [T]; a slot outside [0, n_pages * page) skips its token.  No slot
+ *           may be listed twice in a call, and no page in two runs (the page's contents
+ *           are then undefined).
+ *
+ * One kernel launch.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN,
+ * BSA_ERR_UNSUPPORTED (page, d), BSA_ERR_CUDA.
+ */
+int bsa_cache_append(const bsa_cache* cache, const void* k, const void* v, const int32_t* slots,
+                     int T, int dtype, int64_t k_token_stride, int64_t k_head_stride,
+                     int64_t v_token_stride, int64_t v_head_stride, void* stream);
+
+/* Arguments of bsa_cache_forward that most calls leave out (zeroed with window -1: none). */
+typedef struct bsa_cache_args {
+  int window;         /* key c masked when c < position - window; < 0: no bound          */
+  float softcap;      /* > 0: each scaled score s becomes softcap*tanh(s / softcap)      */
+  const float* sinks; /* device fp32 [heads] or NULL: as in bsa_ext_args                 */
+  const bsa_lut* lut; /* uploaded LUT with one layout row per kv head, or NULL: dense    */
+  int block;          /* the LUT's block, 64 or 128 (both sides); unused without a LUT   */
+} bsa_cache_args;
+
+/*
+ * bsa_cache_forward -- attention of the newest tokens of every request over its cache.
+ * Request b has n_b = cu_q[b+1] - cu_q[b] queries; query i stands at position
+ * r = kv_len[b] - n_b + i (its own key is in the cache).  With kv head g = h / (heads /
+ * kv_heads) and page(c) = block_table[b][c / page]:
+ *
+ *   A(r)   = { c <= r : not masked by the window, page(c) in [0, n_pages), and with a LUT
+ *              layout[g][r / block][c / block] == 1 }
+ *   s_c    = scale * k_scale[page(c)][g] * <q, k8_c>, then softcap*tanh(s_c/softcap) if set
+ *   lse    = ln( sum_{c in A(r)} exp(s_c) + exp(sinks[h]) if sinks )   (-inf when empty)
+ *   out    = sum_{c in A(r)} exp(s_c - lse) * v_scale[page(c)][g] * v8_c    (0 when empty)
+ *
+ * A query whose position is negative (more queries than tokens) sees no key.  kv_len is
+ * taken as at most max_pages * page.  V scales count as lying in [2^-60, 2^60], which those
+ * of bsa_cache_append do.  What the cache holds behind a request's length is not used.
+ *
+ *   q         device, dtype BSA_BF16 or BSA_FP16, [T, heads, d] with strides as in
+ *             bsa_cache_append, 16-byte aligned.
+ *   block_table  device int32 [B, max_pages];  kv_len  device int32 [B];
+ *   cu_q      device int32 [B + 1], ascending, cu_q[B] <= T (bsa_cache_resize's cu_new).
+ *   out       device [T, heads, d] of dtype, 16-byte aligned;  lse  device fp32 [T, heads].
+ *   status    device int32 [1], written: 0, or 0x10000 | site when a bounded wait in the
+ *             kernel gave up (the outputs are then undefined).
+ *   workspace device, 16-byte aligned, of the size that bsa_cache_workspace gives for the
+ *             same heads, kv_heads, d and max_q; contents need not be kept.  Calls that may
+ *             overlap on the GPU need one each.
+ *   max_q     at least the queries of any request, as far as the caller knows: chooses the
+ *             kernel, results are right for any value >= 1.
+ *   heads     a multiple of kv_heads, at most 128 times it.
+ *   scale     any finite value.
+ *
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN, BSA_ERR_UNSUPPORTED
+ * (page, d, block, window or soft-cap out of range, non-finite scale), BSA_ERR_STATE (LUT
+ * not uploaded to the current device), BSA_ERR_TOO_LARGE (workspace too small),
+ * BSA_ERR_CUDA.  The LUT has kv_heads heads (its batch does not matter) and covers the
+ * block table: max_pages * page <= nb * block, and the same for its key blocks.
+ */
+int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* block_table,
+                      const int32_t* kv_len, const int32_t* cu_q, void* out, float* lse,
+                      int32_t* status, void* workspace, int64_t workspace_bytes, int B,
+                      int max_pages, int T, int heads, int max_q, int dtype,
+                      int64_t q_token_stride, int64_t q_head_stride, float scale,
+                      const bsa_cache_args* args, void* stream);
+
+/* bsa_cache_workspace -- bytes of workspace that bsa_cache_forward needs on the current
+ * device, for any batch and any lengths.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE,
+ * BSA_ERR_UNSUPPORTED (d), BSA_ERR_CUDA. */
+int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* bytes);
 
 /*
  * bsa_device_status -- synchronize `stream`, read and clear the LUT's device status
