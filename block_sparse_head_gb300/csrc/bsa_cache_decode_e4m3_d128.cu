@@ -1,0 +1,11 @@
+// Decode kernels over an e4m3 cache, head dim 128.
+#include "bsa_cache_decode.cuh"
+
+namespace bsa {
+
+cudaError_t launch_cache_decode_e4m3_d128(bool fp16, int rows, const CacheFwdParams& p,
+                                         void* workspace, int sms, cudaStream_t stream) {
+  return launch_decode<E4M3, 128>(fp16, rows, p, workspace, sms, stream);
+}
+
+}  // namespace bsa

@@ -1,0 +1,11 @@
+// Decode kernels over an int8 cache, head dim 64.
+#include "bsa_cache_decode.cuh"
+
+namespace bsa {
+
+cudaError_t launch_cache_decode_int8_d64(bool fp16, int rows, const CacheFwdParams& p,
+                                         void* workspace, int sms, cudaStream_t stream) {
+  return launch_decode<Int8, 64>(fp16, rows, p, workspace, sms, stream);
+}
+
+}  // namespace bsa

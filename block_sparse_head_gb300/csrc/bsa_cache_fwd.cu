@@ -110,11 +110,11 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_fwd_kernel(const CacheFwdP
       r.x += s_o[w][2 * threadIdx.x] * f[w];
       r.y += s_o[w][2 * threadIdx.x + 1] * f[w];
     }
-    const float inv = z > 0.f ? 1.f / z : 0.f;
+    const float inv = z == 0.f ? 0.f : 1.f / z;
     reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row * D)[threadIdx.x] =
         float2_to_act<A>(r.x * inv, r.y * inv);
   }
-  if (threadIdx.x == 0) p.lse[row] = z > 0.f ? (top + log2f(z)) * 0.6931471805599453f : -INFINITY;
+  if (threadIdx.x == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * 0.6931471805599453f;
 }
 
 template <class A, class C>

@@ -45,6 +45,13 @@ int check_heads(int heads, int kv_heads) {
              : BSA_OK;
 }
 
+// Rows of the decode kernel that a call takes, 0: too many for it.  All queries of a
+// request in one tile, else the cache would be read once for each tile.
+int decode_rows(int group, int max_q) {
+  const int64_t rows = static_cast<int64_t>(group) * max_q;
+  return rows <= 8 ? 8 : rows <= bsa::kDecodeRows ? 16 : 0;
+}
+
 }  // namespace
 
 extern "C" {
@@ -130,7 +137,13 @@ int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* byte
   *bytes = 0;
   if (d != 64 && d != 128) return BSA_ERR_UNSUPPORTED;
   if (check_heads(heads, kv_heads) != BSA_OK || max_q < 1) return BSA_ERR_SHAPE;
-  *bytes = 16;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+  const int sms = bsa::sm_count(dev);
+  if (sms <= 0) return BSA_ERR_CUDA;
+  // Two decode CTAs an SM; see cache_parts for what each leaves.
+  const int rows = decode_rows(heads / kv_heads, max_q);
+  *bytes = rows > 0 ? bsa::cache_parts_bytes(2 * sms, rows, d) : 16;
   return BSA_OK;
 }
 
@@ -209,8 +222,22 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
     p.softcap_log2 = static_cast<float>(static_cast<double>(x.softcap) * 1.4426950408889634);
     p.softcap_inv = static_cast<float>(static_cast<double>(scale) / x.softcap);
   }
-  return bsa::launch_cache_fwd(cache->d, dtype, cache->dtype, p, st) == cudaSuccess ? BSA_OK
-                                                                                   : BSA_ERR_CUDA;
+  cudaError_t e;
+  const int rows = decode_rows(p.group, max_q);
+  if (rows > 0) {
+    int dev = -1;
+    if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+    const int sms = bsa::sm_count(dev);
+    const bool fp16 = dtype == BSA_FP16, int8 = cache->dtype == BSA_INT8;
+    e = cache->d == 128
+            ? (int8 ? bsa::launch_cache_decode_int8_d128(fp16, rows, p, workspace, sms, st)
+                    : bsa::launch_cache_decode_e4m3_d128(fp16, rows, p, workspace, sms, st))
+            : (int8 ? bsa::launch_cache_decode_int8_d64(fp16, rows, p, workspace, sms, st)
+                    : bsa::launch_cache_decode_e4m3_d64(fp16, rows, p, workspace, sms, st));
+  } else {
+    e = bsa::launch_cache_fwd(cache->d, dtype, cache->dtype, p, st);
+  }
+  return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }
 
 }  // extern "C"

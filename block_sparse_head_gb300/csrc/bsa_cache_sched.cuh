@@ -1,0 +1,204 @@
+// bsa_cache_sched.cuh -- how the attention kernels over a cache share their work out.
+//
+// A unit is (request b, kv head h, query tile t): TQ consecutive queries of b, the rows of
+// all G query heads of h packed together, against the keys those queries can see.  Its keys
+// are taken in slices of 2^SL keys (of the dense range, or of the layout row's blocks).
+// Every length sits on the device, so the split is made there: all units are laid end to
+// end on one axis, a unit taking kOverhead + slices places, and CTA c takes the c-th piece
+// of equal length.  A CTA thus runs whole units and at most two cut ones; cut units leave
+// partial results (running maximum, sum, accumulator) in the workspace, and a second small
+// kernel joins them.  Any mix of lengths splits evenly, one long request over all CTAs as
+// well as a thousand short ones, and the result does not depend on which CTA is first.
+#pragma once
+
+#include "bsa_internal.h"
+
+namespace bsa {
+
+// One CTA's share of one unit.
+struct CacheSeg {
+  int b, h;
+  int q0, nq;       // first packed token and number of queries (0: no more segments)
+  int pos0;         // position of the first query
+  int lo_key;       // no query of the tile sees a key before it (window)
+  int s0, s1;       // slices [s0, s1): of the key axis (dense) or of the row's block list
+  int rp;           // layout row: first col_idx entry
+  int starts, ends; // whether the unit's first / last slice is in this segment
+  int more;         // CTAs after this one that the unit goes on in (if it does not end here)
+};
+
+// Joining kernel's record of a CTA: pieces (0: no cut unit starts here), q0, nq, h.
+using CacheMeta = int4;
+
+template <int SL>
+struct CacheUnits {
+  const CacheFwdParams& p;
+  int tq;  // queries of a tile (a power of two when there is a layout)
+  static constexpr int kOverhead = 2;  // places for a unit's fixed work
+
+  struct Request {
+    int q0, n, len, p0, o, tiles;
+  };
+  __device__ __forceinline__ Request request(int b) const {
+    Request r;
+    const int c0 = max(0, min(p.cu_q[b], p.T)), c1 = max(c0, min(p.cu_q[b + 1], p.T));
+    r.q0 = c0;
+    r.n = c1 - c0;
+    r.len = max(0, min(p.kv_len[b], p.max_pages << p.page_shift));
+    r.p0 = r.len - r.n;
+    // With a layout, tiles begin at multiples of tq (negative positions included), so that
+    // the queries of a tile share one layout row.
+    r.o = p.row_ptr != nullptr ? (r.p0 & ~(tq - 1)) : r.p0;
+    r.tiles = r.n > 0 ? (r.len - r.o + tq - 1) / tq : 0;
+    return r;
+  }
+  // Slices of tile t; fills the tile's part of s.
+  __device__ __forceinline__ int unit(const Request& r, int h, int t, CacheSeg& s) const {
+    const int a = max(r.p0, r.o + t * tq), e = min(r.len, r.o + (t + 1) * tq), last = e - 1;
+    s.h = h;
+    s.nq = e - a;
+    s.q0 = r.q0 + (a - r.p0);
+    s.pos0 = a;
+    s.lo_key = p.window >= 0 ? max(0, a - p.window) : 0;
+    s.rp = 0;
+    s.s0 = 0;
+    if (last < 0) return 0;
+    if (p.row_ptr != nullptr) {
+      const int32_t* row = p.row_ptr + h * p.nb + (last >> p.block_shift);
+      s.rp = row[0];
+      return (row[1] - row[0]) << (p.block_shift - SL);
+    }
+    s.s0 = s.lo_key >> SL;
+    return (last >> SL) + 1 - s.s0;
+  }
+  __device__ __forceinline__ long long head_places(const Request& r, int h) const {
+    long long n = 0;
+    CacheSeg s;
+    for (int t = 0; t < r.tiles; ++t) n += kOverhead + unit(r, h, t, s);
+    return n;
+  }
+};
+
+// Walks a CTA's segments; one thread runs it.
+template <int SL>
+struct CacheWalk {
+  int b, h, t;
+  long long off;   // places of unit (b, h, t) that lie before this CTA
+  long long left;  // places of this CTA still to hand out
+  long long chunk;
+
+  // Next segment into s (s.nq = 0 at the end).
+  __device__ void next(const CacheUnits<SL>& u, CacheSeg& s) {
+    s.nq = 0;
+    if (left <= 0) return;
+    for (; b < u.p.B; ++b, h = 0) {
+      const auto r = u.request(b);
+      if (r.tiles == 0) continue;
+      for (; h < u.p.Hkv; ++h, t = 0) {
+        if (t >= r.tiles) continue;
+        s.b = b;
+        const int slices = u.unit(r, h, t, s);
+        const long long size = u.kOverhead + slices;
+        const long long take = min(left, size - off), end = off + take;
+        // the unit's fixed places come first
+        s.s1 = s.s0 + static_cast<int>(max(0ll, end - u.kOverhead));
+        s.s0 += static_cast<int>(max(0ll, off - u.kOverhead));
+        s.starts = off == 0;
+        s.ends = end == size;
+        s.more = static_cast<int>((size - end + chunk - 1) / chunk);
+        left -= take;
+        off = 0;
+        ++t;
+        return;
+      }
+    }
+  }
+};
+
+// Splits the axis: every thread of the CTA calls it, thread 0 of the caller gets the walk
+// through `out` (shared memory).  scratch: kThreads / 32 + 1 long longs.
+template <int SL, int kThreads>
+__device__ __forceinline__ void cache_split(const CacheUnits<SL>& u, int min_chunk,
+                                            long long* scratch, CacheWalk<SL>* out) {
+  const CacheFwdParams& p = u.p;
+  // Without a layout the heads of a request have the same places, so the requests are
+  // scanned; with one, the (request, head) pairs are.
+  const bool lay = p.row_ptr != nullptr;
+  const int n = lay ? p.B * p.Hkv : p.B, mult = lay ? 1 : p.Hkv;
+  const int per = (n + kThreads - 1) / kThreads;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
+  auto places = [&](int i) {
+    const int b = lay ? i / p.Hkv : i;
+    return u.head_places(u.request(b), lay ? i - b * p.Hkv : 0);
+  };
+  long long mine = 0;
+  for (int i = i0; i < i1; ++i) mine += places(i) * mult;
+  long long inc = mine;
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) {
+    const long long up = __shfl_up_sync(0xffffffffu, inc, k);
+    if (lane >= k) inc += up;
+  }
+  if (lane == 31) scratch[warp] = inc;
+  if (tid == 0) {
+    out->b = p.B;
+    out->left = 0;
+  }
+  __syncthreads();
+  long long before = inc - mine, total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < warp) before += scratch[w];
+    total += scratch[w];
+  }
+  const long long chunk =
+      max(static_cast<long long>(min_chunk), (total + gridDim.x - 1) / gridDim.x);
+  const long long start = blockIdx.x * chunk;
+  if (start >= before && start < before + mine) {
+    // The thread whose items hold the start finds the item, the head and the tile.
+    long long at = before;
+    for (int i = i0; i < i1; ++i) {
+      const long long one = places(i);
+      if (start >= at + one * mult) {
+        at += one * mult;
+        continue;
+      }
+      CacheWalk<SL> w;
+      w.b = lay ? i / p.Hkv : i;
+      w.h = lay ? i - w.b * p.Hkv : static_cast<int>((start - at) / one);
+      w.off = start - at - (lay ? 0 : w.h * one);
+      w.chunk = chunk;
+      w.left = min(chunk, total - start);
+      const auto r = u.request(w.b);
+      CacheSeg s;
+      for (w.t = 0; w.t < r.tiles - 1; ++w.t) {
+        const long long size = u.kOverhead + u.unit(r, w.h, w.t, s);
+        if (w.off < size) break;
+        w.off -= size;
+      }
+      *out = w;
+      break;
+    }
+  }
+  __syncthreads();
+}
+
+// Partial results of a cut unit: slot 2c holds the piece at the start of CTA c's share (a
+// unit begun earlier), slot 2c + 1 the piece at its end.  Slot s: R rows of D fp32 at
+// o + s * R * D, and R (max, sum) pairs at ml + s * R.
+struct CacheParts {
+  float* o;
+  float2* ml;
+  CacheMeta* meta;
+};
+
+__device__ __forceinline__ CacheParts cache_parts(void* ws, int grid, int rows, int d) {
+  CacheParts c;
+  c.meta = static_cast<CacheMeta*>(ws);
+  c.o = reinterpret_cast<float*>(c.meta + grid);
+  c.ml = reinterpret_cast<float2*>(c.o + static_cast<int64_t>(grid) * 2 * rows * d);
+  return c;
+}
+
+}  // namespace bsa

@@ -63,7 +63,9 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int d, int bo
   return r == CUDA_SUCCESS;
 }
 
-int sm_count(int dev) {
+}  // namespace
+
+int bsa::sm_count(int dev) {
   static int cache[64] = {0};
   if (dev >= 0 && dev < 64 && cache[dev] > 0) return cache[dev];
   int n = 0;
@@ -72,6 +74,8 @@ int sm_count(int dev) {
   if (dev >= 0 && dev < 64) cache[dev] = n;
   return n;
 }
+
+namespace {
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
@@ -395,7 +399,7 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
   int dev = -1;
   if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
   free_device(lut);
-  const int sms = sm_count(dev);
+  const int sms = bsa::sm_count(dev);
   if (sms <= 0) return BSA_ERR_CUDA;
   lut->sched_grid = std::max(1, std::min(lut->n_items, sms));
   std::vector<int32_t>* rec = lut->sched_records;  // device records of both schedules

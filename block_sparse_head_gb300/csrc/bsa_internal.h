@@ -91,6 +91,9 @@ enum WaitSite : int {
   kSiteSelftest = 15,
 };
 
+// SMs of a device (0: the query failed).
+int sm_count(int dev);
+
 // Regroups lut's work list for `grid` CTAs: CTA c takes items[start[c] .. start[c+1]).
 // by_head: hand the items out (batch, head) by (batch, head) instead of in list order.
 void build_schedule(const bsa_lut& lut, int grid, bool by_head, std::vector<int32_t>& items,
@@ -240,6 +243,23 @@ struct CacheFwdParams {
 };
 cudaError_t launch_cache_fwd(int d, int dtype, int cache_dtype, const CacheFwdParams& p,
                              cudaStream_t stream);
+
+// Bytes of the partial results that `grid` CTAs of `rows` query rows may leave for the join
+// (bsa_cache_sched.cuh): a record of 16, and two pieces of rows * d numbers and rows pairs.
+inline int64_t cache_parts_bytes(int grid, int rows, int d) {
+  return static_cast<int64_t>(grid) * (16 + 2 * (static_cast<int64_t>(rows) * d * 4 + rows * 8));
+}
+
+// Few query rows (group * max_q <= kDecodeRows): the decode kernels, split over the keys.
+constexpr int kDecodeRows = 16;
+cudaError_t launch_cache_decode_e4m3_d64(bool fp16, int rows, const CacheFwdParams& p,
+                                         void* workspace, int sms, cudaStream_t stream);
+cudaError_t launch_cache_decode_e4m3_d128(bool fp16, int rows, const CacheFwdParams& p,
+                                          void* workspace, int sms, cudaStream_t stream);
+cudaError_t launch_cache_decode_int8_d64(bool fp16, int rows, const CacheFwdParams& p,
+                                         void* workspace, int sms, cudaStream_t stream);
+cudaError_t launch_cache_decode_int8_d128(bool fp16, int rows, const CacheFwdParams& p,
+                                          void* workspace, int sms, cudaStream_t stream);
 
 // One-CTA kernel whose only wait never completes; it must give up after limit_ns.
 cudaError_t launch_wait_selftest(int32_t* status, uint64_t limit_ns, cudaStream_t stream);
