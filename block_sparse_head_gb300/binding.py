@@ -489,13 +489,13 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache:
 
 
 def cache_workspace(heads: int, kv_heads: int, d: int, max_q: int) -> torch.Tensor:
-    """A workspace for cache_forward on the current device; calls that may overlap on the
-    GPU need one each."""
+    """A workspace for cache_forward on the current device, zeroed as its first call wants
+    it; calls that may overlap on the GPU need one each."""
     lib = load_library()
     n = ctypes.c_int64()
     _check(lib.bsa_cache_workspace(int(heads), int(kv_heads), int(d), int(max_q), ctypes.byref(n)),
            "bsa_cache_workspace")
-    return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
+    return torch.zeros(n.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
 
 
 def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,

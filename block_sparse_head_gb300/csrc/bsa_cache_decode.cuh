@@ -3,27 +3,28 @@
 //
 // Bound: memory.  A key costs 2 D bytes and 4 D R flops, R <= 16, so the kernel has to keep
 // the loads in flight and spend few instructions a byte.
-//   * Work is split evenly on the device (bsa_cache_sched.cuh); inside a CTA's segment the
-//     warps take 16-key slices in turn, each with a running maximum and sum of its own,
-//     joined when the segment ends.
-//   * A lane copies exactly the bytes that its matrix fragments need (cp.async, 16 bytes at
-//     a time, whole 32-byte sectors over the warp), into shared memory that only this lane
-//     reads: no barriers, no bank conflicts, kStages - 1 slices in flight a warp.
+//   * Work is split evenly on the device (bsa_cache_sched.cuh).  One CTA per SM: a producer
+//     warp walks its segments, looks pages and scales up and brings the keys and values in
+//     by TMA, 256 keys a stage, about 190 KB ahead of the eight consumer warps; joining a
+//     segment's warps thus stalls no load.
+//   * A consumer warp takes two 16-key slices of a stage (two chains that overlap), with a
+//     running maximum and sum of its own; the warps are joined when the segment ends.
 //   * Products on mma.m16n8k16 (fp16 inputs, fp32 sums), transposed so that the keys (then
 //     the head dim) fill the 16 rows and the few query rows the 8 columns: S^T = K Q^T and
 //     O^T = V^T P^T.  The order of d inside S and of the columns of V is free, so both
-//     fragments come from contiguous bytes: a lane's 16-byte piece of a key row gives it
-//     four k-steps of K, and its 16-byte pieces of four value rows, interleaved by byte
-//     permutes, give 8 row pairs of V^T.  The tensor pipe is nearly idle here; tcgen05
-//     would need the operands converted into shared memory first, a second trip for every
-//     byte.
+//     fragments come from contiguous bytes: a lane's 16-byte pieces of a key row give it
+//     four k-steps of K each, and its 16-byte pieces of four value rows, interleaved by byte
+//     permutes, give 8 row pairs of V^T.  With the 128-byte swizzle of the boxes all of these
+//     shared-memory reads are free of bank conflicts (d = 64: the values' are two-way).  The
+//     tensor pipe is nearly idle here; tcgen05 would need the operands converted into shared
+//     memory first, a second trip for every byte.
 //   * Stored numbers are exact in fp16.  bf16 queries are scaled per row by a power of two
 //     into fp16's range (exact but for numbers 2^-28 of the row's largest).  The V scale
 //     is folded into the exponent, w = exp2(s + log2 vs - m), so that weights are rounded
 //     to fp16 relative to the largest weight times scale, and the sum takes w / vs: both
 //     sums are held in fp32, with m the running maximum of s + log2 vs.
-//   * The running maximum moves only when a score passes it by 2^8 (one vote a slice; the
-//     weights stay below 256), so the usual slice needs no shuffles.
+//   * The running maximum moves only when a score passes it by 2^8 (one vote a stage; the
+//     weights stay below 256), so the usual stage needs no shuffles.
 #pragma once
 
 #include <type_traits>
@@ -95,178 +96,311 @@ __device__ __forceinline__ float log2_scale(float s) {
 
 template <int D, int NT>
 struct DecodeCfg {
-  static constexpr int kWarps = 8;
-  static constexpr int kThreads = 32 * kWarps;
+  static constexpr int kWarps = 8;                    // consumers; the producer comes after
+  static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 8 * NT;
-  static constexpr int kCtas = 2;               // per SM
-  static constexpr int kStages = 3;
-  static constexpr int kSL = 4;                 // log2 keys of a slice
-  static constexpr int kVB = D / 8;             // bytes of a value row per lane
-  static constexpr int kStageB = 2 * 16 * D;    // one warp's K and V slice
-  static constexpr int kRingB = kWarps * kStages * kStageB;
+  static constexpr int kSub = 2;                      // slices of a stage per warp
+  static constexpr int kSlices = kWarps * kSub;       // slices of a stage
+  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kVB = D / 8;                   // bytes of a value row per lane
+  static constexpr int kSliceB = 16 * D;              // one slice of K or of V
+  static constexpr int kSideB = kSlices * kSliceB;
+  static constexpr int kStageB = 2 * kSideB;          // K boxes, then V boxes
   static constexpr int kJoinB = (kWarps / 2) * 32 * (D / 4) * 4;  // half the warps' O, one NT
-  static constexpr int kOffJoin = kRingB;
-  static constexpr int kOffSeg = kOffJoin + kJoinB;
-  static constexpr int kOffScan = kOffSeg + 3 * 64;
-  static constexpr int kSmemB = kOffScan + 192;
+  static constexpr int kInfoB = 64 + 16 + kSlices * 16;  // DecodeStage
+  static_assert(kSlices == 16, "boxes of a DecodeStage");
+  static constexpr int kOffJoin = kStages * kStageB;
+  static constexpr int kOffSegs = kOffJoin + kJoinB;
+  static constexpr int kOffInfo = kOffSegs + 64 * static_cast<int>(sizeof(CacheSeg));
+  static constexpr int kOffBar = kOffInfo + kStages * kInfoB;  // full, empty
+  static constexpr int kOffScan = kOffBar + (2 * kStages + 1) * 8;  // and the consumers' barrier
+  static constexpr int kOffWalk = kOffScan + 16 * 8;
+  static constexpr int kOffCtl = kOffWalk + 96;       // status, abort flag
+  static constexpr int kSmemB = kOffCtl + 16 + 1024;  // + align slack
   static_assert(kWarps * kRows * 8 <= kJoinB, "row statistics share the join buffer");
-  static_assert(sizeof(CacheSeg) <= 64, "segment slots");
-  static_assert(kCtas * (kSmemB + 1024) <= 228 * 1024, "shared memory of an SM");
+  static_assert(sizeof(CacheSeg) <= 64 && sizeof(CacheWalk) <= 96, "slots");
+  static_assert(kThreads / 32 <= 16, "scan scratch");
+  static_assert(kOffInfo % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
+  static_assert(kSmemB <= 232448, "shared memory");
 };
 
-// Waiting slices of a warp: where the slice's keys start and what scales them.
-struct DecodeSlice {
-  int key0;  // >= 0: loaded; -1: nothing of it is seen; -2: none was left to load
+// A box of a stage: its first key (kNoKeys: nothing of it is seen), the scale of its
+// scores and log2 of its values' scale.
+struct DecodeBox {
+  int key0;
   float ks, lv;
+  int pad;
 };
+constexpr int kNoKeys = 1 << 30;  // past every position, so that the masks cover it
+
+enum DecodeFlags { kStageFirst = 1, kStageLast = 2, kStageEnd = 4 };
+
+// What the producer says about a stage.
+struct DecodeStage {
+  CacheSeg seg;
+  int seg_pad[(64 - sizeof(CacheSeg)) / 4];
+  int flags, pad[3];
+  DecodeBox boxes[16];
+};
+
+// Barriers of the consumer warps.  A warp whose wait on a copy gave up leaves the loop, so
+// the warps first meet with a bounded wait; once all are there none leaves before the end of
+// the join, and the hardware barrier does.
+template <int kThreads>
+__device__ __forceinline__ void consumer_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
+struct ConsumerBarrier {
+  uint32_t bar, phase;
+  __device__ __forceinline__ bool sync(int lane, const WaitCtl& ctl) {
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+    const bool ok = mbar_wait(bar, phase, ctl, kSiteCacheJoin);
+    phase ^= 1;
+    return __all_sync(0xffffffffu, ok);
+  }
+};
+
+template <class C, int D, int NT>
+__device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const CUtensorMap* tm_k,
+                                                const CUtensorMap* tm_v, uint8_t* smem,
+                                                const CacheUnits& units, const WaitCtl& ctl) {
+  using Cfg = DecodeCfg<D, NT>;
+  constexpr int S = Cfg::kStages;
+  const int lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  auto full = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
+  auto empty = [&](int i) { return sbase + Cfg::kOffBar + 8 * (S + i); };
+  CacheWalk walk = *reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk);
+  const int sl = units.sl, per_stage = (16 * Cfg::kSlices) >> sl;
+  const int box_b = D << sl;
+  CacheSeg* ring = reinterpret_cast<CacheSeg*>(smem + Cfg::kOffSegs);  // two batches' segments
+
+  // A box's lookups depend on one another (layout block, page, scales), each a trip to
+  // memory.  They are made for 32 boxes at a time, one a lane, over as many segments as
+  // those lie in, and a batch ahead of the copies: between two stages of one batch the next
+  // batch gets one lookup further, and none is waited for.
+  struct Batch {
+    int n;            // boxes (0: the share has ended)
+    int seg;          // this lane's box: place of its segment in the ring,
+    int first, last;  // whether it is the segment's first, last box
+    int key;          // first key (kNoKeys: nothing of it is seen)
+    int pid, tile;
+    float ks, vs;
+  };
+  CacheSeg seg;
+  int pos = 0, segs = 0;  // next piece of seg; segments so far
+  bool open = false;      // seg has pieces left
+  auto place = [&](Batch& x) {
+    x.n = 0;
+    x.key = kNoKeys;
+    while (x.n < 32) {
+      if (!open) {
+        walk.next(units, seg);  // every lane walks the same way
+        if (seg.nq == 0) break;
+        pos = seg.s0;
+        if (lane == 0) ring[segs % 64] = seg;
+        ++segs;
+      }
+      // A segment without a piece still takes a place: its rows are written.
+      const int left = max(1, seg.s1 - pos), take = min(left, 32 - x.n), i = lane - x.n;
+      if (i >= 0 && i < take) {
+        x.seg = (segs - 1) % 64;
+        x.first = pos + i == seg.s0;
+        x.last = i == left - 1;
+        if (pos + i < seg.s1)
+          x.key = p.row_ptr != nullptr ? p.col_idx[seg.rp + ((pos + i) >> (p.block_shift - sl))]
+                                       : (pos + i) << sl;
+        x.pid = pos + i;
+      }
+      x.n += take;
+      pos += take;
+      open = take < left;
+    }
+    __syncwarp();
+  };
+  auto find_page = [&](Batch& x) {
+    if (x.key == kNoKeys) return;
+    const CacheSeg& s = ring[x.seg];
+    if (p.row_ptr != nullptr) {
+      const int sub = p.block_shift - sl;
+      x.key = (x.key << p.block_shift) + ((x.pid & ((1 << sub) - 1)) << sl);
+    }
+    if (x.key > s.pos0 + s.nq - 1 || x.key + (1 << sl) <= s.lo_key) {
+      x.key = kNoKeys;
+      return;
+    }
+    x.pid = p.table[static_cast<int64_t>(s.b) * p.max_pages + (x.key >> p.page_shift)];
+  };
+  auto find_scales = [&](Batch& x) {
+    if (x.key == kNoKeys) return;
+    if (x.pid < 0 || x.pid >= p.n_pages) {
+      x.key = kNoKeys;
+      return;
+    }
+    x.tile = x.pid * p.Hkv + ring[x.seg].h;
+    x.ks = p.k_scale[x.tile];
+    x.vs = p.v_scale[x.tile];
+  };
+
+  Batch cur{}, next{};
+  place(cur);
+  find_page(cur);
+  find_scales(cur);
+  int at = 0, step = 0, issued = 0;  // boxes of cur that are copied; lookups of next made
+  for (int g = 0;; ++g) {
+    const int slot = g % S;
+    if (at >= cur.n && cur.n > 0) {
+      if (step < 1) place(next);
+      if (step < 2) find_page(next);
+      if (step < 3) find_scales(next);
+      cur = next;
+      at = step = 0;
+    } else if (cur.n > 0) {
+      if (step == 0) place(next);
+      else if (step == 1) find_page(next);
+      else if (step == 2) find_scales(next);
+      step = min(step + 1, 3);
+    }
+    const bool end = cur.n == 0;
+    // The stage: boxes [at, at + n) of the batch, of one segment.
+    const int who = __shfl_sync(0xffffffffu, cur.seg, at);
+    const uint32_t same = __ballot_sync(0xffffffffu, lane < cur.n && cur.seg == who) >> at;
+    const int n = end ? 0 : min(per_stage, __ffs(~same) == 0 ? 32 - at : __ffs(~same) - 1);
+    const bool mine = lane >= at && lane < at + n;
+    const int flags = end ? kStageEnd
+                          : (__any_sync(0xffffffffu, mine && cur.first) ? kStageFirst : 0) |
+                                (__any_sync(0xffffffffu, mine && cur.last) ? kStageLast : 0);
+    if (g >= S && !mbar_wait(empty(slot), (g / S - 1) & 1, ctl, kSiteProdKEmpty)) break;
+    DecodeStage& st = *reinterpret_cast<DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    const bool load = mine && cur.key != kNoKeys;
+    const int loads = __popc(__ballot_sync(0xffffffffu, load));
+    if (lane == 0) mbar_arrive_expect_tx(full(slot), loads * 2 * box_b);
+    __syncwarp();
+    if (load) {
+      const uint32_t dst = sbase + slot * Cfg::kStageB + (lane - at) * box_b;
+      const int row = cur.key & ((1 << p.page_shift) - 1);
+      tma_load_3d(dst, tm_k, full(slot), 0, row, cur.tile);
+      tma_load_3d(dst + Cfg::kSideB, tm_v, full(slot), 0, row, cur.tile);
+    }
+    // The scales may still be on their way: described after the copies have begun.
+    if (lane < Cfg::kSlices) st.boxes[lane] = DecodeBox{kNoKeys, 0.f, 0.f, 0};
+    __syncwarp();
+    if (mine) st.boxes[lane - at] = DecodeBox{cur.key, cur.ks, log2_scale(cur.vs), 0};
+    if (lane == 0) st.flags = flags;
+    if ((flags & kStageFirst) && lane < static_cast<int>(sizeof(CacheSeg) / 4))
+      reinterpret_cast<int*>(&st.seg)[lane] = reinterpret_cast<const int*>(&ring[who])[lane];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(full(slot));
+    issued = g + 1;
+    if (end) break;
+    at += n;
+  }
+  // Every copy lands before the CTA leaves (also when the consumers have given up).
+  for (int j = max(0, issued - S); j < issued; ++j) mbar_drain_wait(full(j % S), (j / S) & 1);
+}
+
+// Row r of a cut unit: pieces 0 .. more, the first at the end of CTA root's share, piece i at
+// the start of CTA root + i's.  One warp.
+template <class A, int D, int R>
+__device__ __forceinline__ void join_row(const CacheFwdParams& p, const CacheParts& parts,
+                                         const CacheSeg& s, int root, int more, int r, int lane) {
+  constexpr int E = D / 32;
+  auto slot = [&](int i) {
+    return static_cast<int64_t>(i == 0 ? 2 * root + 1 : 2 * (root + i)) * R + r;
+  };
+  const int qi = r / p.group, head = s.h * p.group + r - qi * p.group;
+  const float sink = p.sinks != nullptr ? p.sinks[head] * kLog2e : -INFINITY;
+  float top = sink;
+  for (int i = lane; i <= more; i += 32) top = fmaxf(top, __ldcg(&parts.ml[slot(i)]).x);
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+  float z = sink == -INFINITY ? 0.f : ex2_approx(sink - top), o[E] = {};
+#pragma unroll 8
+  for (int i = 0; i <= more; ++i) {
+    const int64_t at = slot(i);
+    const float2 x = __ldcg(&parts.ml[at]);
+    const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
+    const float* src = parts.o + at * D + lane * E;
+    if constexpr (E == 4) {
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+      o[0] += f * v.x;
+      o[1] += f * v.y;
+      o[2] += f * v.z;
+      o[3] += f * v.w;
+    } else {
+      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+      o[0] += f * v.x;
+      o[1] += f * v.y;
+    }
+    z += f * x.y;
+  }
+  const float inv = z == 0.f ? 0.f : 1.f / z;
+  const int64_t row = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
+  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row * D + lane * E);
+#pragma unroll
+  for (int i = 0; i < E / 2; ++i) dst[i] = float2_to_act<A>(o[2 * i] * inv, o[2 * i + 1] * inv);
+  if (lane == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * kLn2;
+}
 
 template <class A, class C, int D, int NT>
-__global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, DecodeCfg<D, NT>::kCtas)
-    bsa_cache_decode_kernel(const CacheFwdParams p, void* workspace) {
+__global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
+    bsa_cache_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
+                            const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p,
+                            void* workspace) {
   using Cfg = DecodeCfg<D, NT>;
   constexpr int W = Cfg::kWarps, R = Cfg::kRows, S = Cfg::kStages, VB = Cfg::kVB;
   constexpr int KT = D / 64;  // 16-byte pieces of a key row per lane
-  extern __shared__ __align__(16) uint8_t smem[];
-  asm volatile("griddepcontrol.launch_dependents;");
+  constexpr int SUB = Cfg::kSub;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~static_cast<uintptr_t>(1023));
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;  // fragment row and column of this lane
-  CacheSeg* segs = reinterpret_cast<CacheSeg*>(smem + Cfg::kOffSeg);  // 3 slots of 64 bytes
-  auto seg_at = [&](int i) -> CacheSeg& {
-    return *reinterpret_cast<CacheSeg*>(reinterpret_cast<uint8_t*>(segs) + 64 * (i % 3));
-  };
+  const uint32_t sbase = smem_u32(smem);
+  auto full = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
+  auto empty = [&](int i) { return sbase + Cfg::kOffBar + 8 * (S + i); };
+  int* err = reinterpret_cast<int*>(smem + Cfg::kOffCtl);
+  const WaitCtl ctl{err + 1, err, kCacheWaitNs, 0};
   const CacheParts parts = cache_parts(workspace, gridDim.x, R, D);
-  if (blockIdx.x == 0 && tid == 0) *p.status = 0;
 
   int tq = R / p.group;
   if (p.row_ptr != nullptr) tq = 1 << (31 - __clz(tq));
-  const CacheUnits<Cfg::kSL> units{p, tq};
-  CacheWalk<Cfg::kSL>* walk_slot = reinterpret_cast<CacheWalk<Cfg::kSL>*>(smem + Cfg::kOffScan + 128);
-  cache_split<Cfg::kSL, Cfg::kThreads>(units, W, reinterpret_cast<long long*>(smem + Cfg::kOffScan),
-                                       walk_slot);
-  CacheWalk<Cfg::kSL> walk;
+  const CacheUnits units{p, tq, p.box_shift, p.box_shift == 4 ? 2 : 1};
   if (tid == 0) {
-    walk = *walk_slot;
-    walk.next(units, seg_at(0));
-    if (seg_at(0).nq > 0) walk.next(units, seg_at(1));
-    else seg_at(1).nq = 0;
-    parts.meta[blockIdx.x] = make_int4(0, 0, 0, 0);
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full(i), 2);  // copies announced, boxes described
+      mbar_init(empty(i), W);
+    }
+    mbar_init(sbase + Cfg::kOffBar + 8 * (2 * S), W);
+    err[0] = err[1] = 0;
+    fence_mbar_init();
+    if (blockIdx.x == 0) *p.status = 0;
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
   }
-  __syncthreads();
+  cache_split<Cfg::kThreads>(units, 128 >> p.box_shift,
+                            reinterpret_cast<long long*>(smem + Cfg::kOffScan),
+                                       reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk));
 
-  // ---- this warp's stream of slices: those of the current segment, then of the next one
-  const uint32_t ring = smem_u32(smem) + warp * (S * Cfg::kStageB);
-  int f_seg = 0, f_idx = 0, f_n = 0;  // segment being loaded, next slice of it, its slices
-  int f_key0 = -1, f_pid = 0;         // this lane's slice of the current batch of 32
-  float f_ks = 0.f, f_lv = 0.f;
-  int stage_in = 0, stage_out = 0;
-  auto count_of = [&](const CacheSeg& s) {
-    return s.nq == 0 ? 0 : max(0, (s.s1 - s.s0 - warp + W - 1) / W);
-  };
-  f_n = count_of(seg_at(0));
-  // Loads the next slice (limit: the last segment that may be begun) and says which it is.
-  auto push = [&](int limit) -> DecodeSlice {
-    DecodeSlice r{-2, 0.f, 0.f};
-    while (f_idx >= f_n && f_seg < limit) {
-      ++f_seg;
-      f_idx = 0;
-      f_n = count_of(seg_at(f_seg));
-    }
-    if (f_idx < f_n) {
-      const CacheSeg& s = seg_at(f_seg);
-      if ((f_idx & 31) == 0) {
-        // The places of the next 32 slices, one a lane.
-        const int i = s.s0 + warp + (f_idx + lane) * W;
-        f_key0 = -1;
-        if (i < s.s1) {
-          const int last = s.pos0 + s.nq - 1;
-          int key = i << Cfg::kSL;
-          if (p.row_ptr != nullptr) {
-            const int sub = p.block_shift - Cfg::kSL;
-            key = (p.col_idx[s.rp + (i >> sub)] << p.block_shift) + ((i & ((1 << sub) - 1)) << Cfg::kSL);
-          }
-          if (key <= last && key + 15 >= s.lo_key) {
-            f_pid = p.table[static_cast<int64_t>(s.b) * p.max_pages + (key >> p.page_shift)];
-            if (f_pid >= 0 && f_pid < p.n_pages) {
-              f_key0 = key;
-              const int64_t tile = static_cast<int64_t>(f_pid) * p.Hkv + s.h;
-              f_ks = p.k_scale[tile];
-              f_lv = log2_scale(p.v_scale[tile]);
-            }
-          }
-        }
-      }
-      const int src = f_idx & 31;
-      r.key0 = __shfl_sync(0xffffffffu, f_key0, src);
-      const int pid = __shfl_sync(0xffffffffu, f_pid, src);
-      r.ks = __shfl_sync(0xffffffffu, f_ks, src);
-      r.lv = __shfl_sync(0xffffffffu, f_lv, src);
-      ++f_idx;
-      if (r.key0 >= 0) {
-        const int64_t base = (((static_cast<int64_t>(pid) * p.Hkv + s.h) << p.page_shift) +
-                              (r.key0 & ((1 << p.page_shift) - 1))) * D;
-        const uint32_t dst = ring + stage_in * Cfg::kStageB;
-        const uint8_t* k = p.k_cache + base + g * D + t * 16;
-#pragma unroll
-        for (int i = 0; i < 2 * KT; ++i)  // key g, then key g + 8; pieces t and t + 4
-          cp_async16(dst + i * 512 + lane * 16, k + (i / KT) * 8 * D + (i % KT) * 64);
-        const uint8_t* v = p.v_cache + base + g * VB;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // keys 2t, 2t + 1, 2t + 8, 2t + 9
-          const uint8_t* src_v = v + (2 * t + (i >> 1) * 8 + (i & 1)) * D;
-          const uint32_t dst_v = dst + 16 * D + i * (32 * VB) + lane * VB;
-          if constexpr (VB == 16) cp_async16(dst_v, src_v);
-          else cp_async8(dst_v, src_v);
-        }
-        stage_in = stage_in + 1 == S ? 0 : stage_in + 1;
-      }
-    }
-    cp_async_commit();
-    return r;
-  };
-  DecodeSlice fifo[S - 1];
-#pragma unroll
-  for (int i = 0; i < S - 1; ++i) fifo[i] = push(1);
-
-  for (int si = 0;; ++si) {
-    const CacheSeg s = seg_at(si);
-    if (s.nq == 0) break;
-    if (tid == 0) {  // read by the others after this segment's barriers
-      if (seg_at(si + 1).nq > 0) walk.next(units, seg_at(si + 2));
-      else seg_at(si + 2).nq = 0;
-    }
-    const int mine = count_of(s);
-    if (f_seg < si) {  // a warp without slices in the last segment
-      f_seg = si;
-      f_idx = 0;
-      f_n = mine;
-    }
-    const int last = s.pos0 + s.nq - 1;
+  if (warp == W) {
+    decode_producer<C, D, NT>(p, &tm_k, &tm_v, smem, units, ctl);
+  } else {
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
-#pragma unroll
-      for (int j = 0; j < D / 16; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
-    }
-    if (mine > 0) {
-      // Q fragments: row 8n + g, the columns of this lane's pieces of a key row.
-      uint32_t qf[NT][KT][8];
-      float rf[NT][2];      // factor of the scores of rows 8n + 2t, 8n + 2t + 1
-      int hi[NT][2];        // their positions (-1: no such row)
+    uint32_t qf[NT][KT][8];  // Q fragments: row 8n + g, the columns of this lane's pieces
+    float rf[NT][2];         // factor of the scores of rows 8n + 2t, 8n + 2t + 1
+    int hi[NT][2];           // their positions (-1: no such row)
+    auto load_q = [&](const CacheSeg& seg) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int row = 8 * n + g;
-        const bool live = row < s.nq * p.group;
-        const int qi = row / p.group;
-        float top = 0.f;
-        if (live) {
-          const A* q = static_cast<const A*>(p.q) + (s.q0 + qi) * p.q_token_stride +
-                       (s.h * p.group + row - qi * p.group) * p.q_head_stride + t * 16;
+        const int row = 8 * n + g, qi = row / p.group;
+        if (row < seg.nq * p.group) {
+          const A* q = static_cast<const A*>(p.q) + (seg.q0 + qi) * p.q_token_stride +
+                       (seg.h * p.group + row - qi * p.group) * p.q_head_stride + t * (16 * KT);
 #pragma unroll
           for (int c = 0; c < KT; ++c) {
-            const uint4 a = *reinterpret_cast<const uint4*>(q + c * 64);
-            const uint4 b = *reinterpret_cast<const uint4*>(q + c * 64 + 8);
+            const uint4 a = *reinterpret_cast<const uint4*>(q + c * 16);
+            const uint4 b = *reinterpret_cast<const uint4*>(q + c * 16 + 8);
             qf[n][c][0] = a.x; qf[n][c][1] = a.y; qf[n][c][2] = a.z; qf[n][c][3] = a.w;
             qf[n][c][4] = b.x; qf[n][c][5] = b.y; qf[n][c][6] = b.z; qf[n][c][7] = b.w;
           }
@@ -276,113 +410,129 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, DecodeCfg<D, NT>::
 #pragma unroll
             for (int i = 0; i < 8; ++i) qf[n][c][i] = 0;
         }
-        float back = 1.f;
-        if constexpr (sizeof(A) == 2 && !std::is_same<A, __half>::value) {
-          // bf16: largest magnitude of the row to [2^14, 2^15), then fp16.
-#pragma unroll
-          for (int c = 0; c < KT; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = act_to_float2<A>(qf[n][c][i]);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-            }
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-          const int k = max(-113, min(120, 14 - e));
-          const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-          back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-#pragma unroll
-          for (int c = 0; c < KT; ++c)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 f = act_to_float2<A>(qf[n][c][i]);
-              qf[n][c][i] = float2_to_act<__half>(f.x * up, f.y * up);
-            }
-        }
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int r = 8 * n + 2 * t + e;
-          rf[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e)) *
-                     (p.softcap_log2 > 0.f ? p.softcap_inv : p.scale_log2);
-          hi[n][e] = r < s.nq * p.group ? s.pos0 + r / p.group : -1;
-        }
       }
-      for (int done = 0; done < mine;) {
-        const DecodeSlice cur = fifo[0];
-#pragma unroll
-        for (int i = 0; i < S - 2; ++i) fifo[i] = fifo[i + 1];
-        cp_async_wait<S - 2>();
-        // The slice's fragments; then its stage is free for the slice after the next.
-        uint4 kw[2 * KT];
-        uint32_t vw[4][VB / 4];
-        if (cur.key0 >= 0) {
-          const uint8_t* src = smem + warp * (S * Cfg::kStageB) + stage_out * Cfg::kStageB;
-#pragma unroll
-          for (int i = 0; i < 2 * KT; ++i)
-            kw[i] = *reinterpret_cast<const uint4*>(src + i * 512 + lane * 16);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint8_t* sv = src + 16 * D + i * (32 * VB) + lane * VB;
-            if constexpr (VB == 16) {
-              const uint4 x = *reinterpret_cast<const uint4*>(sv);
-              vw[i][0] = x.x; vw[i][1] = x.y; vw[i][2] = x.z; vw[i][3] = x.w;
-            } else {
-              const uint2 x = *reinterpret_cast<const uint2*>(sv);
-              vw[i][0] = x.x; vw[i][1] = x.y;
-            }
-          }
-          stage_out = stage_out + 1 == S ? 0 : stage_out + 1;
-        }
-        fifo[S - 2] = push(si + 1);
-        if (cur.key0 == -2) continue;  // nothing was left to load when this place was filled
-        ++done;
-        if (cur.key0 < 0) continue;
-
-        // S^T: keys g and g + 8 (rows) by query rows 2t, 2t + 1 (columns).
-        float x[NT][4];
-#pragma unroll
-        for (int n = 0; n < NT; ++n) x[n][0] = x[n][1] = x[n][2] = x[n][3] = 0.f;
-#pragma unroll
-        for (int c = 0; c < KT; ++c) {
-          const uint32_t wa[4] = {kw[c].x, kw[c].y, kw[c].z, kw[c].w};
-          const uint32_t wb[4] = {kw[KT + c].x, kw[KT + c].y, kw[KT + c].z, kw[KT + c].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t a0, a1, a2, a3;
-            stored4_to_half2<C>(wa[i], a0, a2);
-            stored4_to_half2<C>(wb[i], a1, a3);
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma16816(x[n], a0, a1, a2, a3, qf[n][c][2 * i], qf[n][c][2 * i + 1]);
-          }
-        }
-        const bool whole = cur.key0 + 15 <= s.pos0 &&
-                           (p.window < 0 || cur.key0 >= last - p.window);
-        bool grow = false;
+    };
+    CacheSeg s{};
+    // The first segment's queries are requested before its keys have landed.
+    CacheWalk walk = *reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk);
+    walk.next(units, s);
+    load_q(s);
+    int last = 0;  // last position of the tile
+    ConsumerBarrier cb{sbase + Cfg::kOffBar + 8 * (2 * S), 0};
+    for (int gs = 0;; ++gs) {
+      const int slot = gs % S;
+      // A warp whose wait gave up leaves; the abort flag ends the others' waits too.
+      if (!__all_sync(0xffffffffu, mbar_wait(full(slot), (gs / S) & 1, ctl, kSiteMmaStage)))
+        break;
+      const DecodeStage& st =
+          *reinterpret_cast<const DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+      const int flags = st.flags;
+      if (flags & kStageEnd) break;
+      if (flags & kStageFirst) {
+        s = st.seg;
+        last = s.pos0 + s.nq - 1;
+        if (gs > 0) load_q(s);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+          m[n][0] = m[n][1] = -INFINITY;
+          l[n][0] = l[n][1] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float y = x[n][e] * (rf[n][e & 1] * cur.ks);
-            if (p.softcap_log2 > 0.f) y = softcap(y, p.softcap_log2);
-            y += cur.lv;
-            if (!whole) {
-              const int key = cur.key0 + g + (e >> 1) * 8, top = hi[n][e & 1];
-              if (key > top || (p.window >= 0 && key < top - p.window)) y = -INFINITY;
-            }
-            x[n][e] = y;
-            grow |= y > m[n][e & 1] + 8.f;
+          for (int j = 0; j < D / 16; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+          float back = 1.f;
+          if constexpr (!std::is_same<A, __half>::value) {
+            // bf16: largest magnitude of the row to [2^14, 2^15), then fp16.
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < KT; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 f = act_to_float2<A>(qf[n][c][i]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+            const int k = max(-113, min(120, 14 - e));
+            const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+            back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+            for (int c = 0; c < KT; ++c)
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float2 f = act_to_float2<A>(qf[n][c][i]);
+                qf[n][c][i] = float2_to_act<__half>(f.x * up, f.y * up);
+              }
+          }
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            rf[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e)) *
+                       (p.softcap_log2 > 0.f ? p.softcap_inv : p.scale_log2);
+            hi[n][e] = r < s.nq * p.group ? s.pos0 + r / p.group : -1;
           }
         }
-        if (!whole) {
-          // Values that no row sees may be anything, a NaN among it: zero.
+      }
+      // This warp's slices: warp and warp + W, so that few slices spread over the warps.
+      DecodeBox sl[SUB];
+      bool any = false;
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int key = cur.key0 + 2 * t + (i >> 1) * 8 + (i & 1);
-            if (key > last || key < s.lo_key)
+      for (int u = 0; u < SUB; ++u) {
+        const int i = warp + u * W, sub = p.box_shift - 4;
+        sl[u] = st.boxes[i >> sub];
+        any |= sl[u].key0 != kNoKeys;
+        sl[u].key0 += (i & ((1 << sub) - 1)) << 4;  // kNoKeys stays past every position
+      }
+      if (any) {
+        const uint8_t* kbox = smem + slot * Cfg::kStageB;
+        const uint8_t* vbox = kbox + Cfg::kSideB;
+        // S^T: keys g and g + 8 (rows) by query rows 2t, 2t + 1 (columns).
+        float x[SUB][NT][4];
 #pragma unroll
-              for (int w = 0; w < VB / 4; ++w) vw[i][w] = 0;
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n) x[u][n][0] = x[u][n][1] = x[u][n][2] = x[u][n][3] = 0.f;
+#pragma unroll
+        for (int c = 0; c < KT; ++c) {
+          uint32_t wa[SUB][4], wb[SUB][4];
+          const int piece = D == 128 ? ((2 * t + c) ^ g) : (t ^ (g >> 1));
+#pragma unroll
+          for (int u = 0; u < SUB; ++u) {
+            const uint8_t* src = kbox + (warp + u * W) * Cfg::kSliceB + g * D + piece * 16;
+            const uint4 a = *reinterpret_cast<const uint4*>(src);
+            const uint4 b = *reinterpret_cast<const uint4*>(src + 8 * D);
+            wa[u][0] = a.x; wa[u][1] = a.y; wa[u][2] = a.z; wa[u][3] = a.w;
+            wb[u][0] = b.x; wb[u][1] = b.y; wb[u][2] = b.z; wb[u][3] = b.w;
+          }
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int u = 0; u < SUB; ++u) {
+              uint32_t a0, a1, a2, a3;
+              stored4_to_half2<C>(wa[u][i], a0, a2);
+              stored4_to_half2<C>(wb[u][i], a1, a3);
+#pragma unroll
+              for (int n = 0; n < NT; ++n)
+                mma16816(x[u][n], a0, a1, a2, a3, qf[n][c][2 * i], qf[n][c][2 * i + 1]);
+            }
+        }
+        bool grow = false, whole[SUB];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) {
+          whole[u] = sl[u].key0 + 15 <= s.pos0 && (p.window < 0 || sl[u].key0 >= last - p.window);
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float y = x[u][n][e] * (rf[n][e & 1] * sl[u].ks);
+              if (p.softcap_log2 > 0.f) y = softcap(y, p.softcap_log2);
+              y += sl[u].lv;
+              if (!whole[u]) {
+                const int key = sl[u].key0 + g + (e >> 1) * 8, top = hi[n][e & 1];
+                if (key > top || (p.window >= 0 && key < top - p.window)) y = -INFINITY;
+              }
+              x[u][n][e] = y;
+              grow |= y > m[n][e & 1] + 8.f;
+            }
           }
         }
         if (__any_sync(0xffffffffu, grow)) {
@@ -390,7 +540,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, DecodeCfg<D, NT>::
           for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(x[n][e], x[n][e + 2]);
+              float top = fmaxf(x[0][n][e], x[0][n][e + 2]);
+#pragma unroll
+              for (int u = 1; u < SUB; ++u) top = fmaxf(top, fmaxf(x[u][n][e], x[u][n][e + 2]));
 #pragma unroll
               for (int k = 4; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
               top = fmaxf(top, m[n][e]);
@@ -404,220 +556,215 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, DecodeCfg<D, NT>::
               }
             }
         }
-        const float rv = ex2_approx(-cur.lv);
-        uint32_t pf[NT][2];
+        uint32_t pf[SUB][NT][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+        for (int u = 0; u < SUB; ++u) {
+          const float rv = ex2_approx(-sl[u].lv);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float top = m[n][e & 1];
-            x[n][e] = ex2_approx(x[n][e] - (top == -INFINITY ? 0.f : top));
+          for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float top = m[n][e & 1];
+              x[u][n][e] = ex2_approx(x[u][n][e] - (top == -INFINITY ? 0.f : top));
+            }
+            l[n][0] = fmaf(x[u][n][0] + x[u][n][2], rv, l[n][0]);
+            l[n][1] = fmaf(x[u][n][1] + x[u][n][3], rv, l[n][1]);
+            pf[u][n][0] = transpose8x8(float2_to_act<__half>(x[u][n][0], x[u][n][1]));
+            pf[u][n][1] = transpose8x8(float2_to_act<__half>(x[u][n][2], x[u][n][3]));
           }
-          l[n][0] = fmaf(x[n][0] + x[n][2], rv, l[n][0]);
-          l[n][1] = fmaf(x[n][1] + x[n][3], rv, l[n][1]);
-          pf[n][0] = transpose8x8(float2_to_act<__half>(x[n][0], x[n][1]));
-          pf[n][1] = transpose8x8(float2_to_act<__half>(x[n][2], x[n][3]));
         }
         // O^T: columns VB * g + 2j, 2j + 1 of the values (rows) by the query rows.
 #pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
-          const uint32_t w01 = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel);
-          const uint32_t w23 = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
-          uint32_t a0, a1, a2, a3;
-          stored4_to_half2<C>(w01, a0, a1);
-          stored4_to_half2<C>(w23, a2, a3);
+        for (int u = 0; u < SUB; ++u) {
+          uint32_t vw[4][VB / 4];  // keys 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
-          for (int n = 0; n < NT; ++n) mma16816(o[n][j], a0, a1, a2, a3, pf[n][0], pf[n][1]);
-        }
-      }
-    }
-
-    // ---- join the warps: row statistics, then the scaled accumulators, halves onto halves
-    float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffJoin);
+          for (int i = 0; i < 4; ++i) {
+            const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+            const uint8_t* src = vbox + (warp + u * W) * Cfg::kSliceB + r * D;
+            if constexpr (D == 128) {
+              const uint4 w = *reinterpret_cast<const uint4*>(src + (g ^ (2 * t + (i & 1))) * 16);
+              vw[i][0] = w.x; vw[i][1] = w.y; vw[i][2] = w.z; vw[i][3] = w.w;
+            } else {
+              const uint2 w =
+                  *reinterpret_cast<const uint2*>(src + ((g >> 1) ^ t) * 16 + (g & 1) * 8);
+              vw[i][0] = w.x; vw[i][1] = w.y;
+            }
+          }
+          if (!whole[u]) {
+            // Values that no row sees may be anything, a NaN among it: zero.
 #pragma unroll
-    for (int n = 0; n < NT; ++n)
+            for (int i = 0; i < 4; ++i) {
+              const int key = sl[u].key0 + 2 * t + (i >> 1) * 8 + (i & 1);
+              if (key > last || key < s.lo_key)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int k = 4; k < 32; k *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], k);
-        if (g == 0) ml[warp * R + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
-      }
-    __syncthreads();
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float top = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * R + 8 * n + 2 * t + e].x);
-#pragma unroll
-        for (int w = 0; w < W; ++w) {
-          const float2 x = ml[w * R + 8 * n + 2 * t + e];
-          sum += x.y * (x.x == -INFINITY ? 0.f : ex2_approx(x.x - top));  // a NaN stays
-        }
-        const float f = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - top);
-        m[n][e] = top;
-        l[n][e] = sum;
-#pragma unroll
-        for (int j = 0; j < D / 16; ++j) {
-          o[n][j][e] *= f;
-          o[n][j][e + 2] *= f;
-        }
-      }
-    float4* join = reinterpret_cast<float4*>(smem + Cfg::kOffJoin);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int half = W / 2; half >= 1; half /= 2) {
-        __syncthreads();
-        if (warp >= half && warp < 2 * half) {
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j)
-            join[((warp - half) * (D / 16) + j) * 32 + lane] =
-                make_float4(o[n][j][0], o[n][j][1], o[n][j][2], o[n][j][3]);
-        }
-        __syncthreads();
-        if (warp < half) {
+                for (int w = 0; w < VB / 4; ++w) vw[i][w] = 0;
+            }
+          }
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            const float4 x = join[(warp * (D / 16) + j) * 32 + lane];
-            o[n][j][0] += x.x;
-            o[n][j][1] += x.y;
-            o[n][j][2] += x.z;
-            o[n][j][3] += x.w;
+            const uint32_t sel = (j & 1) ? 0x7362u : 0x5140u;
+            const uint32_t w01 = __byte_perm(vw[0][j / 2], vw[1][j / 2], sel);
+            const uint32_t w23 = __byte_perm(vw[2][j / 2], vw[3][j / 2], sel);
+            uint32_t a0, a1, a2, a3;
+            stored4_to_half2<C>(w01, a0, a1);
+            stored4_to_half2<C>(w23, a2, a3);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+              mma16816(o[n][j], a0, a1, a2, a3, pf[u][n][0], pf[u][n][1]);
           }
         }
       }
-    // ---- warp 0 has the segment's sums: final rows, or a partial result of a cut unit
-    if (warp == 0) {
-      const bool whole_unit = s.starts && s.ends;
-      const int slot = 2 * blockIdx.x + (s.starts ? 1 : 0);
-      if (lane == 0 && s.starts && !s.ends)
-        parts.meta[blockIdx.x] = make_int4(s.more, s.q0, s.nq, s.h);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(empty(slot));
+      if (!(flags & kStageLast)) continue;
+
+      // ---- join the warps: row statistics, then the scaled accumulators, halves onto halves
+      float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffJoin);
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          const int r = 8 * n + 2 * t + e;
-          if (r >= s.nq * p.group) continue;
-          if (whole_unit) {
-            const int qi = r / p.group, head = s.h * p.group + r - qi * p.group;
-            const int64_t row = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
-            float top = m[n][e], z = l[n][e], f = 1.f;
-            if (p.sinks != nullptr) {
-              const float sink = p.sinks[head] * kLog2e;
-              const float mx = fmaxf(top, sink);
-              f = top == -INFINITY ? 0.f : ex2_approx(top - mx);
-              z = z * f + (sink == -INFINITY ? 0.f : ex2_approx(sink - mx));
-              top = mx;
-            }
-            const float inv = z == 0.f ? 0.f : f / z;
-            uint32_t w[D / 16];
 #pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-              w[j] = float2_to_act<A>(o[n][j][e] * inv, o[n][j][e + 2] * inv);
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<A*>(p.out) + row * D + g * VB);
+          for (int k = 4; k < 32; k *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], k);
+          if (g == 0) ml[warp * R + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
+        }
+      if (!cb.sync(lane, ctl)) break;
 #pragma unroll
-            for (int i = 0; i < D / 64; ++i)
-              dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            if (g == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * kLn2;
-          } else {
-            float4* dst = reinterpret_cast<float4*>(parts.o + (static_cast<int64_t>(slot) * R + r) * D + g * VB);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i)
-              dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][e + 2], o[n][2 * i + 1][e],
-                                   o[n][2 * i + 1][e + 2]);
-            if (g == 0) parts.ml[static_cast<int64_t>(slot) * R + r] = make_float2(m[n][e], l[n][e]);
+        for (int e = 0; e < 2; ++e) {
+          float top = -INFINITY, sum = 0.f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * R + 8 * n + 2 * t + e].x);
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            const float2 x = ml[w * R + 8 * n + 2 * t + e];
+            sum += x.y * (x.x == -INFINITY ? 0.f : ex2_approx(x.x - top));  // a NaN stays
+          }
+          const float f = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - top);
+          m[n][e] = top;
+          l[n][e] = sum;
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j) {
+            o[n][j][e] *= f;
+            o[n][j][e + 2] *= f;
           }
         }
-    }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
-}
-
-// Joins the pieces of the unit that was cut at the end of CTA blockIdx.x's share: one warp
-// a row.  Launched with every call and early (programmatic dependent launch): it waits for
-// the attention kernel's results on the device, and its CTAs leave at once where nothing
-// was cut.
-template <class A, int D, int R>
-__global__ void __launch_bounds__(128) bsa_cache_join_kernel(const CacheFwdParams p, void* workspace) {
-  constexpr int E = D / 32;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const CacheParts parts = cache_parts(workspace, gridDim.x, R, D);
-  const int4 unit = parts.meta[blockIdx.x];  // pieces that follow, q0, nq, h
-  const int r = blockIdx.y * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (unit.x == 0 || r >= unit.z * p.group) return;
-  // Piece 0 ends this CTA's share, piece i begins that of CTA blockIdx.x + i.
-  auto slot = [&](int i) {
-    return static_cast<int64_t>(i == 0 ? 2 * blockIdx.x + 1 : 2 * (blockIdx.x + i)) * R + r;
-  };
-  const int qi = r / p.group, head = unit.w * p.group + r - qi * p.group;
-  const float sink = p.sinks != nullptr ? p.sinks[head] * kLog2e : -INFINITY;
-  float top = sink;
-  for (int i = lane; i <= unit.x; i += 32) top = fmaxf(top, parts.ml[slot(i)].x);
+      float4* join = reinterpret_cast<float4*>(smem + Cfg::kOffJoin);
 #pragma unroll
-  for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  float z = sink == -INFINITY ? 0.f : ex2_approx(sink - top), o[E] = {};
-#pragma unroll 4
-  for (int i = 0; i <= unit.x; ++i) {
-    const int64_t s = slot(i);
-    const float2 x = parts.ml[s];
-    const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
-    const float* src = parts.o + s * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(src);
-      o[0] += f * v.x;
-      o[1] += f * v.y;
-      o[2] += f * v.z;
-      o[3] += f * v.w;
-    } else {
-      const float2 v = *reinterpret_cast<const float2*>(src);
-      o[0] += f * v.x;
-      o[1] += f * v.y;
-    }
-    z += f * x.y;
-  }
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  const int64_t row = static_cast<int64_t>(unit.y + qi) * p.Hq + head;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row * D + lane * E);
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) dst[i] = float2_to_act<A>(o[2 * i] * inv, o[2 * i + 1] * inv);
-  if (lane == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * kLn2;
+        for (int half = W / 2; half >= 1; half /= 2) {
+          consumer_sync<32 * W>();
+          if (warp >= half && warp < 2 * half) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+              join[((warp - half) * (D / 16) + j) * 32 + lane] =
+                  make_float4(o[n][j][0], o[n][j][1], o[n][j][2], o[n][j][3]);
+          }
+          consumer_sync<32 * W>();
+          if (warp < half) {
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              const float4 x = join[(warp * (D / 16) + j) * 32 + lane];
+              o[n][j][0] += x.x;
+              o[n][j][1] += x.y;
+              o[n][j][2] += x.z;
+              o[n][j][3] += x.w;
+            }
+          }
+        }
+      // ---- warp 0 has the segment's sums: final rows, or a partial result of a cut unit
+      const bool whole_unit = s.starts && s.ends;
+      if (warp == 0) {
+        const int piece = 2 * blockIdx.x + (s.starts ? 1 : 0);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            if (r >= s.nq * p.group) continue;
+            if (whole_unit) {
+              const int qi = r / p.group, head = s.h * p.group + r - qi * p.group;
+              const int64_t row = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
+              float top = m[n][e], z = l[n][e], f = 1.f;
+              if (p.sinks != nullptr) {
+                const float sink = p.sinks[head] * kLog2e;
+                const float mx = fmaxf(top, sink);
+                f = top == -INFINITY ? 0.f : ex2_approx(top - mx);
+                z = z * f + (sink == -INFINITY ? 0.f : ex2_approx(sink - mx));
+                top = mx;
+              }
+              const float inv = z == 0.f ? 0.f : f / z;
+              uint32_t w[D / 16];
+#pragma unroll
+              for (int j = 0; j < D / 16; ++j)
+                w[j] = float2_to_act<A>(o[n][j][e] * inv, o[n][j][e + 2] * inv);
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<A*>(p.out) + row * D + g * VB);
+#pragma unroll
+              for (int i = 0; i < D / 64; ++i)
+                dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              if (g == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * kLn2;
+            } else {
+              float4* dst = reinterpret_cast<float4*>(
+                  parts.o + (static_cast<int64_t>(piece) * R + r) * D + g * VB);
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i)
+                dst[i] = make_float4(o[n][2 * i][e], o[n][2 * i][e + 2], o[n][2 * i + 1][e],
+                                     o[n][2 * i + 1][e + 2]);
+              if (g == 0)
+                parts.ml[static_cast<int64_t>(piece) * R + r] = make_float2(m[n][e], l[n][e]);
+            }
+          }
+        if (!whole_unit) {
+          // The CTA that leaves a unit's last piece joins them (in their order, whoever it is).
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) {
+            int* count = parts.count + (blockIdx.x - s.before);
+            const int pieces = s.before + 1 + s.more;
+            const bool join_now = atomicAdd(count, 1) == pieces - 1;
+            if (join_now) *count = 0;  // as the next call wants it
+            err[2] = join_now;
+            __threadfence();
+          }
+        }
+      }
+      consumer_sync<32 * W>();  // the join buffer is free again
+      if (!whole_unit) {
+        if (err[2]) {
+          for (int r = warp; r < s.nq * p.group; r += W)
+            join_row<A, D, R>(p, parts, s, blockIdx.x - s.before, s.before + s.more, r, lane);
+        }
+        consumer_sync<32 * W>();  // err[2] has been read
+      }
+    }
+  }
+  __syncthreads();
+  // A wait gives up long after CTA 0 has cleared the word.
+  if (tid == 0 && err[0] != 0) atomicMax(p.status, err[0]);
 }
 
 template <class A, class C, int D, int NT>
-cudaError_t launch_decode(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
+cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const CacheFwdParams& p,
+                          void* workspace, int sms, cudaStream_t stream) {
   using Cfg = DecodeCfg<D, NT>;
   auto* kernel = bsa_cache_decode_kernel<A, C, D, NT>;
   cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemB);
   if (e != cudaSuccess) return e;
-  const int grid = Cfg::kCtas * sms;
-  kernel<<<grid, Cfg::kThreads, Cfg::kSmemB, stream>>>(p, workspace);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid, Cfg::kRows / 4);
-  cfg.blockDim = dim3(128);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr{};
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, bsa_cache_join_kernel<A, D, Cfg::kRows>, p, workspace);
+  kernel<<<sms, Cfg::kThreads, Cfg::kSmemB, stream>>>(k, v, p, workspace);
+  return cudaGetLastError();
 }
 
 template <class C, int D>
-cudaError_t launch_decode(bool fp16, int rows, const CacheFwdParams& p, void* workspace, int sms,
-                          cudaStream_t stream) {
+cudaError_t launch_decode(bool fp16, int rows, const CUtensorMap& k, const CUtensorMap& v,
+                          const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
   if (fp16)
-    return rows <= 8 ? launch_decode<__half, C, D, 1>(p, workspace, sms, stream)
-                     : launch_decode<__half, C, D, 2>(p, workspace, sms, stream);
-  return rows <= 8 ? launch_decode<__nv_bfloat16, C, D, 1>(p, workspace, sms, stream)
-                   : launch_decode<__nv_bfloat16, C, D, 2>(p, workspace, sms, stream);
+    return rows <= 8 ? launch_decode<__half, C, D, 1>(k, v, p, workspace, sms, stream)
+                     : launch_decode<__half, C, D, 2>(k, v, p, workspace, sms, stream);
+  return rows <= 8 ? launch_decode<__nv_bfloat16, C, D, 1>(k, v, p, workspace, sms, stream)
+                   : launch_decode<__nv_bfloat16, C, D, 2>(k, v, p, workspace, sms, stream);
 }
 
 }  // namespace bsa

@@ -3,9 +3,10 @@
 
 namespace bsa {
 
-cudaError_t launch_cache_decode_int8_d64(bool fp16, int rows, const CacheFwdParams& p,
+cudaError_t launch_cache_decode_int8_d64(bool fp16, int rows, const CUtensorMap& k,
+                                         const CUtensorMap& v, const CacheFwdParams& p,
                                          void* workspace, int sms, cudaStream_t stream) {
-  return launch_decode<Int8, 64>(fp16, rows, p, workspace, sms, stream);
+  return launch_decode<Int8, 64>(fp16, rows, k, v, p, workspace, sms, stream);
 }
 
 }  // namespace bsa

@@ -30,7 +30,8 @@ int check_cache(const bsa_cache* c) {
   if (shift_of(c->page, 16) < 0 || (c->d != 64 && c->d != 128)) return BSA_ERR_UNSUPPORTED;
   if (c->dtype != BSA_E4M3 && c->dtype != BSA_INT8) return BSA_ERR_DTYPE;
   if (c->n_pages < 1 || c->kv_heads < 1 || c->kv_heads > 65535 ||
-      static_cast<int64_t>(c->n_pages) * c->page > kInt32Max)
+      static_cast<int64_t>(c->n_pages) * c->page > kInt32Max ||
+      static_cast<int64_t>(c->n_pages) * c->kv_heads > kInt32Max)
     return BSA_ERR_SHAPE;
   if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(c->k_scale, 4) ||
       !aligned(c->v_scale, 4))
@@ -141,9 +142,8 @@ int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* byte
   if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
   const int sms = bsa::sm_count(dev);
   if (sms <= 0) return BSA_ERR_CUDA;
-  // Two decode CTAs an SM; see cache_parts for what each leaves.
   const int rows = decode_rows(heads / kv_heads, max_q);
-  *bytes = rows > 0 ? bsa::cache_parts_bytes(2 * sms, rows, d) : 16;
+  *bytes = rows > 0 ? bsa::cache_parts_bytes(sms, rows, d) : 16;
   return BSA_OK;
 }
 
@@ -229,11 +229,17 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
     if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
     const int sms = bsa::sm_count(dev);
     const bool fp16 = dtype == BSA_FP16, int8 = cache->dtype == BSA_INT8;
+    const int64_t tiles = static_cast<int64_t>(cache->n_pages) * cache->kv_heads;
+    p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
+    CUtensorMap k, v;
+    if (!bsa::encode_cache(&k, cache->k, tiles, cache->page, cache->d, 1 << p.box_shift) ||
+        !bsa::encode_cache(&v, cache->v, tiles, cache->page, cache->d, 1 << p.box_shift))
+      return BSA_ERR_CUDA;
     e = cache->d == 128
-            ? (int8 ? bsa::launch_cache_decode_int8_d128(fp16, rows, p, workspace, sms, st)
-                    : bsa::launch_cache_decode_e4m3_d128(fp16, rows, p, workspace, sms, st))
-            : (int8 ? bsa::launch_cache_decode_int8_d64(fp16, rows, p, workspace, sms, st)
-                    : bsa::launch_cache_decode_e4m3_d64(fp16, rows, p, workspace, sms, st));
+            ? (int8 ? bsa::launch_cache_decode_int8_d128(fp16, rows, k, v, p, workspace, sms, st)
+                    : bsa::launch_cache_decode_e4m3_d128(fp16, rows, k, v, p, workspace, sms, st))
+            : (int8 ? bsa::launch_cache_decode_int8_d64(fp16, rows, k, v, p, workspace, sms, st)
+                    : bsa::launch_cache_decode_e4m3_d64(fp16, rows, k, v, p, workspace, sms, st));
   } else {
     e = bsa::launch_cache_fwd(cache->d, dtype, cache->dtype, p, st);
   }

@@ -6,8 +6,8 @@
 // Every length sits on the device, so the split is made there: all units are laid end to
 // end on one axis, a unit taking kOverhead + slices places, and CTA c takes the c-th piece
 // of equal length.  A CTA thus runs whole units and at most two cut ones; cut units leave
-// partial results (running maximum, sum, accumulator) in the workspace, and a second small
-// kernel joins them.  Any mix of lengths splits evenly, one long request over all CTAs as
+// partial results (running maximum, sum, accumulator) in the workspace, and the CTA that
+// leaves the last one joins them.  Any mix of lengths splits evenly, one long request over all CTAs as
 // well as a thousand short ones, and the result does not depend on which CTA is first.
 #pragma once
 
@@ -21,20 +21,17 @@ struct CacheSeg {
   int q0, nq;       // first packed token and number of queries (0: no more segments)
   int pos0;         // position of the first query
   int lo_key;       // no query of the tile sees a key before it (window)
-  int s0, s1;       // slices [s0, s1): of the key axis (dense) or of the row's block list
+  int s0, s1;       // pieces [s0, s1): of the key axis (dense) or of the row's block list
   int rp;           // layout row: first col_idx entry
-  int starts, ends; // whether the unit's first / last slice is in this segment
-  int more;         // CTAs after this one that the unit goes on in (if it does not end here)
+  int starts, ends; // whether the unit's first / last piece is in this segment
+  int before, more; // CTAs before and after this one that have a piece of the unit
 };
 
-// Joining kernel's record of a CTA: pieces (0: no cut unit starts here), q0, nq, h.
-using CacheMeta = int4;
-
-template <int SL>
 struct CacheUnits {
   const CacheFwdParams& p;
-  int tq;  // queries of a tile (a power of two when there is a layout)
-  static constexpr int kOverhead = 2;  // places for a unit's fixed work
+  int tq;        // queries of a tile (a power of two when there is a layout)
+  int sl;        // log2 keys of a piece, at most those of a page and of a layout block
+  int overhead;  // places for a unit's fixed work
 
   struct Request {
     int q0, n, len, p0, o, tiles;
@@ -52,7 +49,7 @@ struct CacheUnits {
     r.tiles = r.n > 0 ? (r.len - r.o + tq - 1) / tq : 0;
     return r;
   }
-  // Slices of tile t; fills the tile's part of s.
+  // Pieces of tile t; fills the tile's part of s.
   __device__ __forceinline__ int unit(const Request& r, int h, int t, CacheSeg& s) const {
     const int a = max(r.p0, r.o + t * tq), e = min(r.len, r.o + (t + 1) * tq), last = e - 1;
     s.h = h;
@@ -66,45 +63,45 @@ struct CacheUnits {
     if (p.row_ptr != nullptr) {
       const int32_t* row = p.row_ptr + h * p.nb + (last >> p.block_shift);
       s.rp = row[0];
-      return (row[1] - row[0]) << (p.block_shift - SL);
+      return (row[1] - row[0]) << (p.block_shift - sl);
     }
-    s.s0 = s.lo_key >> SL;
-    return (last >> SL) + 1 - s.s0;
+    s.s0 = s.lo_key >> sl;
+    return (last >> sl) + 1 - s.s0;
   }
   __device__ __forceinline__ long long head_places(const Request& r, int h) const {
     long long n = 0;
     CacheSeg s;
-    for (int t = 0; t < r.tiles; ++t) n += kOverhead + unit(r, h, t, s);
+    for (int t = 0; t < r.tiles; ++t) n += overhead + unit(r, h, t, s);
     return n;
   }
 };
 
 // Walks a CTA's segments; one thread runs it.
-template <int SL>
 struct CacheWalk {
   int b, h, t;
   long long off;   // places of unit (b, h, t) that lie before this CTA
   long long left;  // places of this CTA still to hand out
   long long chunk;
+  CacheUnits::Request r;  // of request b
 
   // Next segment into s (s.nq = 0 at the end).
-  __device__ void next(const CacheUnits<SL>& u, CacheSeg& s) {
+  __device__ void next(const CacheUnits& u, CacheSeg& s) {
     s.nq = 0;
     if (left <= 0) return;
-    for (; b < u.p.B; ++b, h = 0) {
-      const auto r = u.request(b);
+    for (; b < u.p.B; h = 0, ++b < u.p.B ? (void)(r = u.request(b)) : (void)0) {
       if (r.tiles == 0) continue;
       for (; h < u.p.Hkv; ++h, t = 0) {
         if (t >= r.tiles) continue;
         s.b = b;
-        const int slices = u.unit(r, h, t, s);
-        const long long size = u.kOverhead + slices;
+        const int pieces = u.unit(r, h, t, s);
+        const long long size = u.overhead + pieces;
         const long long take = min(left, size - off), end = off + take;
         // the unit's fixed places come first
-        s.s1 = s.s0 + static_cast<int>(max(0ll, end - u.kOverhead));
-        s.s0 += static_cast<int>(max(0ll, off - u.kOverhead));
+        s.s1 = s.s0 + static_cast<int>(max(0ll, end - u.overhead));
+        s.s0 += static_cast<int>(max(0ll, off - u.overhead));
         s.starts = off == 0;
         s.ends = end == size;
+        s.before = static_cast<int>((off + chunk - 1) / chunk);
         s.more = static_cast<int>((size - end + chunk - 1) / chunk);
         left -= take;
         off = 0;
@@ -117,9 +114,9 @@ struct CacheWalk {
 
 // Splits the axis: every thread of the CTA calls it, thread 0 of the caller gets the walk
 // through `out` (shared memory).  scratch: kThreads / 32 + 1 long longs.
-template <int SL, int kThreads>
-__device__ __forceinline__ void cache_split(const CacheUnits<SL>& u, int min_chunk,
-                                            long long* scratch, CacheWalk<SL>* out) {
+template <int kThreads>
+__device__ __forceinline__ void cache_split(const CacheUnits& u, int min_chunk,
+                                            long long* scratch, CacheWalk* out) {
   const CacheFwdParams& p = u.p;
   // Without a layout the heads of a request have the same places, so the requests are
   // scanned; with one, the (request, head) pairs are.
@@ -164,16 +161,16 @@ __device__ __forceinline__ void cache_split(const CacheUnits<SL>& u, int min_chu
         at += one * mult;
         continue;
       }
-      CacheWalk<SL> w;
+      CacheWalk w;
       w.b = lay ? i / p.Hkv : i;
       w.h = lay ? i - w.b * p.Hkv : static_cast<int>((start - at) / one);
       w.off = start - at - (lay ? 0 : w.h * one);
       w.chunk = chunk;
       w.left = min(chunk, total - start);
-      const auto r = u.request(w.b);
+      w.r = u.request(w.b);
       CacheSeg s;
-      for (w.t = 0; w.t < r.tiles - 1; ++w.t) {
-        const long long size = u.kOverhead + u.unit(r, w.h, w.t, s);
+      for (w.t = 0; w.t < w.r.tiles - 1; ++w.t) {
+        const long long size = u.overhead + u.unit(w.r, w.h, w.t, s);
         if (w.off < size) break;
         w.off -= size;
       }
@@ -187,16 +184,18 @@ __device__ __forceinline__ void cache_split(const CacheUnits<SL>& u, int min_chu
 // Partial results of a cut unit: slot 2c holds the piece at the start of CTA c's share (a
 // unit begun earlier), slot 2c + 1 the piece at its end.  Slot s: R rows of D fp32 at
 // o + s * R * D, and R (max, sum) pairs at ml + s * R.
+// count[c]: pieces so far of the unit that was cut at the end of CTA c's share; zero before
+// and after every call.
 struct CacheParts {
+  int* count;
   float* o;
   float2* ml;
-  CacheMeta* meta;
 };
 
 __device__ __forceinline__ CacheParts cache_parts(void* ws, int grid, int rows, int d) {
   CacheParts c;
-  c.meta = static_cast<CacheMeta*>(ws);
-  c.o = reinterpret_cast<float*>(c.meta + grid);
+  c.count = static_cast<int*>(ws);
+  c.o = reinterpret_cast<float*>(c.count + (grid + 3) / 4 * 4);
   c.ml = reinterpret_cast<float2*>(c.o + static_cast<int64_t>(grid) * 2 * rows * d);
   return c;
 }

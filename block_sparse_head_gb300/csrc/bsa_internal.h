@@ -89,7 +89,11 @@ enum WaitSite : int {
   kSiteEpiStats = 13,
   kSiteSoftStatsFree = 14,
   kSiteSelftest = 15,
+  kSiteCacheJoin = 16,
 };
+
+// Limit of every wait of the attention kernels over a cache.
+constexpr uint64_t kCacheWaitNs = 10000000000ull;
 
 // SMs of a device (0: the query failed).
 int sm_count(int dev);
@@ -235,6 +239,7 @@ struct CacheFwdParams {
   const float* sinks;        // [Hq] or null
   int B, T, Hq, Hkv, group;  // group = Hq / Hkv
   int n_pages, max_pages, page_shift;
+  int box_shift;             // log2 keys of a box (decode): of a page, a block, at most 64
   int nb, block_shift;       // layout rows per head, log2 of its block
   int window;                // keys before position - window are masked (< 0: no bound)
   float scale_log2;          // scale * log2(e)
@@ -245,21 +250,27 @@ cudaError_t launch_cache_fwd(int d, int dtype, int cache_dtype, const CacheFwdPa
                              cudaStream_t stream);
 
 // Bytes of the partial results that `grid` CTAs of `rows` query rows may leave for the join
-// (bsa_cache_sched.cuh): a record of 16, and two pieces of rows * d numbers and rows pairs.
+// (bsa_cache_sched.cuh): a counter, and two pieces of rows * d numbers and rows pairs.
 inline int64_t cache_parts_bytes(int grid, int rows, int d) {
-  return static_cast<int64_t>(grid) * (16 + 2 * (static_cast<int64_t>(rows) * d * 4 + rows * 8));
+  return (grid + 3) / 4 * 16 +
+         static_cast<int64_t>(grid) * 2 * (static_cast<int64_t>(rows) * d * 4 + rows * 8);
 }
 
 // Few query rows (group * max_q <= kDecodeRows): the decode kernels, split over the keys.
 constexpr int kDecodeRows = 16;
-cudaError_t launch_cache_decode_e4m3_d64(bool fp16, int rows, const CacheFwdParams& p,
-                                         void* workspace, int sms, cudaStream_t stream);
-cudaError_t launch_cache_decode_e4m3_d128(bool fp16, int rows, const CacheFwdParams& p,
-                                          void* workspace, int sms, cudaStream_t stream);
-cudaError_t launch_cache_decode_int8_d64(bool fp16, int rows, const CacheFwdParams& p,
-                                         void* workspace, int sms, cudaStream_t stream);
-cudaError_t launch_cache_decode_int8_d128(bool fp16, int rows, const CacheFwdParams& p,
-                                          void* workspace, int sms, cudaStream_t stream);
+#define BSA_DECODE_LAUNCH(name)                                                              \
+  cudaError_t launch_cache_decode_##name(bool fp16, int rows, const CUtensorMap& k,          \
+                                         const CUtensorMap& v, const CacheFwdParams& p,      \
+                                         void* workspace, int sms, cudaStream_t stream)
+BSA_DECODE_LAUNCH(e4m3_d64);
+BSA_DECODE_LAUNCH(e4m3_d128);
+BSA_DECODE_LAUNCH(int8_d64);
+BSA_DECODE_LAUNCH(int8_d128);
+#undef BSA_DECODE_LAUNCH
+
+// A cache side [tiles, page, d] of 8-bit numbers for boxes of `rows` rows of one tile,
+// swizzled over their whole row (128 or 64 bytes).  false: the encoder refused.
+bool encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int page, int d, int rows);
 
 // One-CTA kernel whose only wait never completes; it must give up after limit_ns.
 cudaError_t launch_wait_selftest(int32_t* status, uint64_t limit_ns, cudaStream_t stream);

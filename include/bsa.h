@@ -343,8 +343,8 @@ int bsa_forward_noalloc(const void* q, const void* k, const void* v, const bsa_l
  *   bsa_cache_forward   the new tokens' queries -> attention over the cache, dense or over
  *                       the active blocks of a LUT (the layout the model was trained with)
  *
- * All three are asynchronous, allocate nothing, keep nothing between calls and read every
- * length on the device, so a step with fixed T and B can be captured in a CUDA graph once
+ * All three are asynchronous, one kernel each, allocate nothing and read every length on the
+ * device, so a step with fixed T and B can be captured in a CUDA graph once
  * and replayed as the requests grow.  Packed tensors hold the new tokens of request 0, then
  * of request 1 and so on ([T, heads, d]); T may exceed their number, and rows behind the
  * last request are neither read nor written.
@@ -365,7 +365,7 @@ typedef struct bsa_cache {
   float* k_scale; /* device, fp32 [n_pages, kv_heads]                            */
   float* v_scale;
   int n_pages;
-  int kv_heads;
+  int kv_heads;   /* n_pages * kv_heads < 2^31                                  */
   int page;       /* tokens of a page: 16, 32, 64 or 128; n_pages * page < 2^31  */
   int d;          /* head dim: 64 or 128                                         */
   int dtype;      /* BSA_E4M3 or BSA_INT8                                        */
@@ -469,8 +469,9 @@ typedef struct bsa_cache_args {
  *   status    device int32 [1], written: 0, or 0x10000 | site when a bounded wait in the
  *             kernel gave up (the outputs are then undefined).
  *   workspace device, 16-byte aligned, of the size that bsa_cache_workspace gives for the
- *             same heads, kv_heads, d and max_q; contents need not be kept.  Calls that may
- *             overlap on the GPU need one each.
+ *             same heads, kv_heads, d and max_q, all zero before its first use; a call that
+ *             ends with status 0 leaves it fit for any later call.  Calls that may overlap on
+ *             the GPU need one each.
  *   max_q     at least the queries of any request, as far as the caller knows: chooses the
  *             kernel, results are right for any value >= 1.
  *   heads     a multiple of kv_heads, at most 128 times it.
