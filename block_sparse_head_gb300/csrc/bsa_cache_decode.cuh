@@ -99,25 +99,26 @@ struct DecodeCfg {
   static constexpr int kWarps = 8;                    // consumers; the producer comes after
   static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 8 * NT;
-  static constexpr int kSub = 2;                      // slices of a stage per warp
+  // Slices of a stage per warp: two, or one where two would not fit the registers.
+  static constexpr int kSub = NT * D == 256 ? 1 : 2;
   static constexpr int kSlices = kWarps * kSub;       // slices of a stage
-  static constexpr int kStages = D == 128 ? 3 : 6;
+  static constexpr int kStages = 192 * 1024 / (2 * kSlices * 16 * D);
   static constexpr int kVB = D / 8;                   // bytes of a value row per lane
   static constexpr int kSliceB = 16 * D;              // one slice of K or of V
   static constexpr int kSideB = kSlices * kSliceB;
   static constexpr int kStageB = 2 * kSideB;          // K boxes, then V boxes
   static constexpr int kJoinB = (kWarps / 2) * 32 * (D / 4) * 4;  // half the warps' O, one NT
-  static constexpr int kInfoB = 64 + 16 + kSlices * 16;  // DecodeStage
-  static_assert(kSlices == 16, "boxes of a DecodeStage");
+  static constexpr int kInfoB = 64 + 16 + 16 * 16;  // DecodeStage
+  static_assert(kSlices <= 16, "boxes of a DecodeStage");
   static constexpr int kOffJoin = kStages * kStageB;
-  static constexpr int kOffSegs = kOffJoin + kJoinB;
+  static constexpr int kOffStats = kOffJoin + kJoinB;  // (max, sum) of each warp's rows
+  static constexpr int kOffSegs = kOffStats + kWarps * kRows * 8;
   static constexpr int kOffInfo = kOffSegs + 64 * static_cast<int>(sizeof(CacheSeg));
   static constexpr int kOffBar = kOffInfo + kStages * kInfoB;  // full, empty
   static constexpr int kOffScan = kOffBar + (2 * kStages + 1) * 8;  // and the consumers' barrier
   static constexpr int kOffWalk = kOffScan + 16 * 8;
   static constexpr int kOffCtl = kOffWalk + 96;       // status, abort flag
   static constexpr int kSmemB = kOffCtl + 16 + 1024;  // + align slack
-  static_assert(kWarps * kRows * 8 <= kJoinB, "row statistics share the join buffer");
   static_assert(sizeof(CacheSeg) <= 64 && sizeof(CacheWalk) <= 96, "slots");
   static_assert(kThreads / 32 <= 16, "scan scratch");
   static_assert(kOffInfo % 16 == 0 && kOffBar % 8 == 0 && kOffScan % 8 == 0, "alignment");
@@ -256,11 +257,6 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
       if (step < 3) find_scales(next);
       cur = next;
       at = step = 0;
-    } else if (cur.n > 0) {
-      if (step == 0) place(next);
-      else if (step == 1) find_page(next);
-      else if (step == 2) find_scales(next);
-      step = min(step + 1, 3);
     }
     const bool end = cur.n == 0;
     // The stage: boxes [at, at + n) of the batch, of one segment.
@@ -295,9 +291,24 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
     issued = g + 1;
     if (end) break;
     at += n;
+    if (step == 0) place(next);
+    else if (step == 1) find_page(next);
+    else if (step == 2) find_scales(next);
+    step = min(step + 1, 3);
   }
   // Every copy lands before the CTA leaves (also when the consumers have given up).
   for (int j = max(0, issued - S); j < issued; ++j) mbar_drain_wait(full(j % S), (j / S) & 1);
+}
+
+// Adds and returns what was there; the warp's earlier writes (after a __syncwarp) are seen by
+// whoever sees the sum, and this thread sees the others'.
+__device__ __forceinline__ int atomic_add_acq_rel(int* p, int x) {
+  int r;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
+               : "=r"(r)
+               : "l"(p), "r"(x)
+               : "memory");
+  return r;
 }
 
 // Row r of a cut unit: pieces 0 .. more, the first at the end of CTA root's share, piece i at
@@ -363,10 +374,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
   int* err = reinterpret_cast<int*>(smem + Cfg::kOffCtl);
   const WaitCtl ctl{err + 1, err, kCacheWaitNs, 0};
   const CacheParts parts = cache_parts(workspace, gridDim.x, R, D);
+  auto group_div = [&](int r) { return static_cast<int>((r * p.group_inv) >> 16); };
 
-  int tq = R / p.group;
-  if (p.row_ptr != nullptr) tq = 1 << (31 - __clz(tq));
-  const CacheUnits units{p, tq, p.box_shift, p.box_shift == 4 ? 2 : 1};
+  const CacheUnits units{p, 31 - __clz(group_div(R)), p.box_shift, p.box_shift == 4 ? 2 : 1};
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(full(i), 2);  // copies announced, boxes described
@@ -393,7 +403,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     auto load_q = [&](const CacheSeg& seg) {
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const int row = 8 * n + g, qi = row / p.group;
+        const int row = 8 * n + g, qi = group_div(row);
         if (row < seg.nq * p.group) {
           const A* q = static_cast<const A*>(p.q) + (seg.q0 + qi) * p.q_token_stride +
                        (seg.h * p.group + row - qi * p.group) * p.q_head_stride + t * (16 * KT);
@@ -419,6 +429,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     load_q(s);
     int last = 0;  // last position of the tile
     ConsumerBarrier cb{sbase + Cfg::kOffBar + 8 * (2 * S), 0};
+    bool gone = false;
     for (int gs = 0;; ++gs) {
       const int slot = gs % S;
       // A warp whose wait gave up leaves; the abort flag ends the others' waits too.
@@ -468,7 +479,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
             const int r = 8 * n + 2 * t + e;
             rf[n][e] = __shfl_sync(0xffffffffu, back, 4 * (2 * t + e)) *
                        (p.softcap_log2 > 0.f ? p.softcap_inv : p.scale_log2);
-            hi[n][e] = r < s.nq * p.group ? s.pos0 + r / p.group : -1;
+            hi[n][e] = r < s.nq * p.group ? s.pos0 + group_div(r) : -1;
           }
         }
       }
@@ -618,8 +629,27 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
       if (lane == 0) mbar_arrive(empty(slot));
       if (!(flags & kStageLast)) continue;
 
-      // ---- join the warps: row statistics, then the scaled accumulators, halves onto halves
-      float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffJoin);
+      // ---- join the warps: halves onto halves, each warp's accumulator scaled to the common
+      // maximum by its reader (round 1: the row statistics come with it).  Slot i of the
+      // buffer is read by warp i in round 1, so warp i may write it again after that.
+      float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffStats);
+      float4* join = reinterpret_cast<float4*>(smem + Cfg::kOffJoin);
+      auto give = [&](int n, int slot) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+          join[(slot * (D / 16) + j) * 32 + lane] =
+              make_float4(o[n][j][0], o[n][j][1], o[n][j][2], o[n][j][3]);
+      };
+      auto take = [&](int n, int slot, float f0, float f1) {
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j) {
+          const float4 x = join[(slot * (D / 16) + j) * 32 + lane];
+          o[n][j][0] = fmaf(x.x, f0, o[n][j][0]);
+          o[n][j][1] = fmaf(x.y, f1, o[n][j][1]);
+          o[n][j][2] = fmaf(x.z, f0, o[n][j][2]);
+          o[n][j][3] = fmaf(x.w, f1, o[n][j][3]);
+        }
+      };
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -628,52 +658,52 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
           for (int k = 4; k < 32; k *= 2) l[n][e] += __shfl_xor_sync(0xffffffffu, l[n][e], k);
           if (g == 0) ml[warp * R + 8 * n + 2 * t + e] = make_float2(m[n][e], l[n][e]);
         }
-      if (!cb.sync(lane, ctl)) break;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int n = 0; n < NT; ++n) {
+        if (n > 0) consumer_sync<32 * W>();  // the buffer of the columns before
+        if (warp >= W / 2) give(n, warp - W / 2);
+        if (n > 0) {
+          consumer_sync<32 * W>();
+        } else if (!cb.sync(lane, ctl)) {
+          gone = true;
+          break;
+        }
+        if (warp < W / 2) {
+          float f[2], fo[2];
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float top = -INFINITY, sum = 0.f;
+          for (int e = 0; e < 2; ++e) {
+            const int r = 8 * n + 2 * t + e;
+            float top = -INFINITY, sum = 0.f;
 #pragma unroll
-          for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * R + 8 * n + 2 * t + e].x);
+            for (int w = 0; w < W; ++w) top = fmaxf(top, ml[w * R + r].x);
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
-            const float2 x = ml[w * R + 8 * n + 2 * t + e];
-            sum += x.y * (x.x == -INFINITY ? 0.f : ex2_approx(x.x - top));  // a NaN stays
+            for (int w = 0; w < W; ++w) {
+              const float2 x = ml[w * R + r];
+              sum += x.y * (x.x == -INFINITY ? 0.f : ex2_approx(x.x - top));  // a NaN stays
+            }
+            const float mo = ml[(warp + W / 2) * R + r].x;
+            f[e] = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - top);
+            fo[e] = mo == -INFINITY ? 0.f : ex2_approx(mo - top);
+            m[n][e] = top;
+            l[n][e] = sum;
           }
-          const float f = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - top);
-          m[n][e] = top;
-          l[n][e] = sum;
 #pragma unroll
           for (int j = 0; j < D / 16; ++j) {
-            o[n][j][e] *= f;
-            o[n][j][e + 2] *= f;
+            o[n][j][0] *= f[0];
+            o[n][j][1] *= f[1];
+            o[n][j][2] *= f[0];
+            o[n][j][3] *= f[1];
           }
+          take(n, warp, fo[0], fo[1]);
         }
-      float4* join = reinterpret_cast<float4*>(smem + Cfg::kOffJoin);
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int half = W / 2; half >= 1; half /= 2) {
+        for (int half = W / 4; half >= 1; half /= 2) {
+          if (warp >= half && warp < 2 * half) give(n, warp);
           consumer_sync<32 * W>();
-          if (warp >= half && warp < 2 * half) {
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j)
-              join[((warp - half) * (D / 16) + j) * 32 + lane] =
-                  make_float4(o[n][j][0], o[n][j][1], o[n][j][2], o[n][j][3]);
-          }
-          consumer_sync<32 * W>();
-          if (warp < half) {
-#pragma unroll
-            for (int j = 0; j < D / 16; ++j) {
-              const float4 x = join[(warp * (D / 16) + j) * 32 + lane];
-              o[n][j][0] += x.x;
-              o[n][j][1] += x.y;
-              o[n][j][2] += x.z;
-              o[n][j][3] += x.w;
-            }
-          }
+          if (warp < half) take(n, warp + half, 1.f, 1.f);
         }
+      }
+      if (gone) break;
       // ---- warp 0 has the segment's sums: final rows, or a partial result of a cut unit
       const bool whole_unit = s.starts && s.ends;
       if (warp == 0) {
@@ -685,7 +715,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
             const int r = 8 * n + 2 * t + e;
             if (r >= s.nq * p.group) continue;
             if (whole_unit) {
-              const int qi = r / p.group, head = s.h * p.group + r - qi * p.group;
+              const int qi = group_div(r), head = s.h * p.group + r - qi * p.group;
               const int64_t row = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
               float top = m[n][e], z = l[n][e], f = 1.f;
               if (p.sinks != nullptr) {
@@ -718,15 +748,13 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
           }
         if (!whole_unit) {
           // The CTA that leaves a unit's last piece joins them (in their order, whoever it is).
-          __threadfence();
           __syncwarp();
           if (lane == 0) {
             int* count = parts.count + (blockIdx.x - s.before);
             const int pieces = s.before + 1 + s.more;
-            const bool join_now = atomicAdd(count, 1) == pieces - 1;
+            const bool join_now = atomic_add_acq_rel(count, 1) == pieces - 1;
             if (join_now) *count = 0;  // as the next call wants it
             err[2] = join_now;
-            __threadfence();
           }
         }
       }

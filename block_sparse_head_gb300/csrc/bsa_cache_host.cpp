@@ -214,6 +214,7 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   p.Hq = heads;
   p.Hkv = cache->kv_heads;
   p.group = heads / cache->kv_heads;
+  p.group_inv = (65536u + p.group - 1) / p.group;
   p.n_pages = cache->n_pages;
   p.max_pages = max_pages;
   p.window = x.window < 0 ? -1 : x.window;

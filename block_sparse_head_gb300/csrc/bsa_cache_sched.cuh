@@ -29,7 +29,7 @@ struct CacheSeg {
 
 struct CacheUnits {
   const CacheFwdParams& p;
-  int tq;        // queries of a tile (a power of two when there is a layout)
+  int tq_shift;  // log2 queries of a tile
   int sl;        // log2 keys of a piece, at most those of a page and of a layout block
   int overhead;  // places for a unit's fixed work
 
@@ -43,15 +43,17 @@ struct CacheUnits {
     r.n = c1 - c0;
     r.len = max(0, min(p.kv_len[b], p.max_pages << p.page_shift));
     r.p0 = r.len - r.n;
-    // With a layout, tiles begin at multiples of tq (negative positions included), so that
+    // With a layout, tiles begin at multiples of their size (negative positions included), so that
     // the queries of a tile share one layout row.
+    const int tq = 1 << tq_shift;
     r.o = p.row_ptr != nullptr ? (r.p0 & ~(tq - 1)) : r.p0;
-    r.tiles = r.n > 0 ? (r.len - r.o + tq - 1) / tq : 0;
+    r.tiles = r.n > 0 ? (r.len - r.o + tq - 1) >> tq_shift : 0;
     return r;
   }
   // Pieces of tile t; fills the tile's part of s.
   __device__ __forceinline__ int unit(const Request& r, int h, int t, CacheSeg& s) const {
-    const int a = max(r.p0, r.o + t * tq), e = min(r.len, r.o + (t + 1) * tq), last = e - 1;
+    const int a = max(r.p0, r.o + (t << tq_shift));
+    const int e = min(r.len, r.o + ((t + 1) << tq_shift)), last = e - 1;
     s.h = h;
     s.nq = e - a;
     s.q0 = r.q0 + (a - r.p0);
@@ -76,7 +78,15 @@ struct CacheUnits {
   }
 };
 
-// Walks a CTA's segments; one thread runs it.
+// ceil(a / b) for a >= 0, b > 0: 32-bit division where the numbers allow it (a 64-bit one is
+// several times as long, and these stand in the way of the first load).
+__device__ __forceinline__ long long div_up(long long a, long long b) {
+  if (a + b < (1ll << 31))
+    return (static_cast<uint32_t>(a) + static_cast<uint32_t>(b) - 1) / static_cast<uint32_t>(b);
+  return (a + b - 1) / b;
+}
+
+// Walks a CTA's segments.
 struct CacheWalk {
   int b, h, t;
   long long off;   // places of unit (b, h, t) that lie before this CTA
@@ -101,8 +111,8 @@ struct CacheWalk {
         s.s0 += static_cast<int>(max(0ll, off - u.overhead));
         s.starts = off == 0;
         s.ends = end == size;
-        s.before = static_cast<int>((off + chunk - 1) / chunk);
-        s.more = static_cast<int>((size - end + chunk - 1) / chunk);
+        s.before = off > 0 ? static_cast<int>(div_up(off, chunk)) : 0;
+        s.more = size > end ? static_cast<int>(div_up(size - end, chunk)) : 0;
         left -= take;
         off = 0;
         ++t;
@@ -125,12 +135,17 @@ __device__ __forceinline__ void cache_split(const CacheUnits& u, int min_chunk,
   const int per = (n + kThreads - 1) / kThreads;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int i0 = min(n, tid * per), i1 = min(n, i0 + per);
-  auto places = [&](int i) {
+  auto places = [&](int i, CacheUnits::Request& r) {
     const int b = lay ? i / p.Hkv : i;
-    return u.head_places(u.request(b), lay ? i - b * p.Hkv : 0);
+    r = u.request(b);
+    return u.head_places(r, lay ? i - b * p.Hkv : 0);
   };
-  long long mine = 0;
-  for (int i = i0; i < i1; ++i) mine += places(i) * mult;
+  CacheUnits::Request r{};
+  long long mine = 0, one = 0;
+  for (int i = i0; i < i1; ++i) {
+    one = places(i, r);
+    mine += one * mult;
+  }
   long long inc = mine;
 #pragma unroll
   for (int k = 1; k < 32; k *= 2) {
@@ -149,28 +164,30 @@ __device__ __forceinline__ void cache_split(const CacheUnits& u, int min_chunk,
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
-  const long long chunk =
-      max(static_cast<long long>(min_chunk), (total + gridDim.x - 1) / gridDim.x);
+  const long long chunk = max(static_cast<long long>(min_chunk), div_up(total, gridDim.x));
   const long long start = blockIdx.x * chunk;
   if (start >= before && start < before + mine) {
     // The thread whose items hold the start finds the item, the head and the tile.
     long long at = before;
     for (int i = i0; i < i1; ++i) {
-      const long long one = places(i);
+      if (per > 1) one = places(i, r);  // else still at hand
       if (start >= at + one * mult) {
         at += one * mult;
         continue;
       }
       CacheWalk w;
       w.b = lay ? i / p.Hkv : i;
-      w.h = lay ? i - w.b * p.Hkv : static_cast<int>((start - at) / one);
+      w.h = lay ? i - w.b * p.Hkv
+                : (start - at < (1ll << 31) && one < (1ll << 31)
+                       ? static_cast<uint32_t>(start - at) / static_cast<uint32_t>(one)
+                       : static_cast<int>((start - at) / one));
       w.off = start - at - (lay ? 0 : w.h * one);
       w.chunk = chunk;
       w.left = min(chunk, total - start);
-      w.r = u.request(w.b);
+      w.r = r;
       CacheSeg s;
-      for (w.t = 0; w.t < w.r.tiles - 1; ++w.t) {
-        const long long size = u.overhead + u.unit(w.r, w.h, w.t, s);
+      for (w.t = 0; w.t < r.tiles - 1; ++w.t) {
+        const long long size = u.overhead + u.unit(r, w.h, w.t, s);
         if (w.off < size) break;
         w.off -= size;
       }

@@ -238,6 +238,7 @@ struct CacheFwdParams {
   int32_t* status;           // [1]
   const float* sinks;        // [Hq] or null
   int B, T, Hq, Hkv, group;  // group = Hq / Hkv
+  uint32_t group_inv;        // r / group = r * group_inv >> 16 for r < 256, group <= 128
   int n_pages, max_pages, page_shift;
   int box_shift;             // log2 keys of a box (decode): of a page, a block, at most 64
   int nb, block_shift;       // layout rows per head, log2 of its block
