@@ -10,6 +10,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 import threading
 
 import numpy as np
@@ -46,19 +47,6 @@ class ExtArgs(ctypes.Structure):
                 ("softcap", ctypes.c_float), ("sinks", ctypes.c_void_p),
                 ("q_segment_ids", ctypes.c_void_p), ("kv_segment_ids", ctypes.c_void_p)]
 
-
-class Cache(ctypes.Structure):
-    """bsa_cache of include/bsa.h."""
-    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
-                ("v_scale", ctypes.c_void_p), ("n_pages", ctypes.c_int),
-                ("kv_heads", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
-                ("dtype", ctypes.c_int)]
-
-
-class CacheArgs(ctypes.Structure):
-    """bsa_cache_args of include/bsa.h."""
-    _fields_ = [("window", ctypes.c_int), ("softcap", ctypes.c_float), ("sinks", ctypes.c_void_p),
-                ("lut", ctypes.c_void_p), ("block", ctypes.c_int)]
 
 _lib = None
 _lock = threading.Lock()
@@ -104,10 +92,10 @@ def load_library():
                                          ctypes.c_float, vp]
         ci, i64 = ctypes.c_int, ctypes.c_int64
         lib.bsa_cache_resize.argtypes = [vp] * 10 + [ci] * 5 + [vp]
-        lib.bsa_cache_append.argtypes = [ctypes.POINTER(Cache), vp, vp, vp, ci, ci, i64, i64, i64,
+        lib.bsa_cache_append.argtypes = [vp, vp, vp, vp, ci, ci, i64, i64, i64,
                                          i64, vp]
-        lib.bsa_cache_forward.argtypes = [ctypes.POINTER(Cache)] + [vp] * 8 + [i64] + [ci] * 6 + \
-            [i64, i64, ctypes.c_float, ctypes.POINTER(CacheArgs), vp]
+        lib.bsa_cache_forward.argtypes = [vp] + [vp] * 8 + [i64] + [ci] * 6 + \
+            [i64, i64, ctypes.c_float, vp, vp]
         lib.bsa_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(i64)]
         lib.bsa_lut_export_csc.argtypes = [vp, vp, vp, vp]
         lib.bsa_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int,
@@ -383,29 +371,49 @@ def topk_forward(q: torch.Tensor, kv: torch.Tensor, sink: torch.Tensor, idx: tor
     return out, lse, status
 
 
-def _dev_ptr(t, name: str, dtype, shape) -> int:
-    """Pointer of a contiguous CUDA tensor of this type and shape on the current device.
-    The cache calls launch on the current device, so a tensor elsewhere is refused."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dtype or \
-            not t.is_contiguous() or tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
-    if t.device.index != torch.cuda.current_device():
+# Raw handle of the current stream of a device: torch.cuda.current_stream() builds an object
+# for it, which takes longer than all the other checks of a small call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+_CACHE = struct.Struct("@4P5i4x")        # bsa_cache
+_CACHE_ARGS = struct.Struct("@ifPPi4x")  # bsa_cache_args
+
+
+def _this_device(t, name: str) -> int:
+    """Index of the current device, which the cache calls launch on; t has to be there."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    dev = torch.cuda.current_device()
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
-    return t.data_ptr()
+    return dev
 
 
-def _rows_ptr(t, name: str, heads: int | None, d: int):
+def _dev_ptr(t, name: str, dtype, shape, dev: int) -> int:
+    """Pointer of a contiguous tensor of this type and shape on device dev."""
+    try:
+        if t.dtype is dtype and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:  # not a tensor
+        pass
+    if isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor of shape {tuple(shape)}")
+
+
+def _rows_ptr(t, name: str, heads: int | None, d: int, dev: int):
     """Pointer and (token, head) strides of a [T, heads, d] activation tensor whose numbers
     of one head are contiguous."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype not in _ACTIVATIONS or \
-            t.dim() != 3 or t.shape[2] != d or (heads is not None and t.shape[1] != heads):
+    if not isinstance(t, torch.Tensor) or t.dtype not in _ACTIVATIONS or t.dim() != 3 or \
+            t.shape[2] != d or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be a bf16 or fp16 CUDA tensor [T, heads, {d}]")
-    if t.stride(2) != 1 and t.numel() > 0:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current device")
+    token, head, one = t.stride()
+    if one != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
     # The stride of a dimension of one is never used, whatever the tensor says.
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else 0, t.stride(1) if t.shape[1] > 1 else 0
+    return t.data_ptr(), token if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
 
 
 def _on(stream):
@@ -419,16 +427,26 @@ def _on(stream):
     return torch.cuda.stream(stream)
 
 
-def _cache_view(k_cache, v_cache, k_scale, v_scale) -> Cache:
-    if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4 or \
-            k_cache.dtype not in _CACHE_TYPES:
+def _cache_view(k_cache, v_cache, k_scale, v_scale):
+    """(device, bsa_cache as bytes, kv_heads, d)."""
+    dev = _this_device(k_cache, "k_cache")
+    kind = _CACHE_TYPES.get(k_cache.dtype)
+    if kind is None or k_cache.dim() != 4:
         raise ValueError("k_cache must be float8_e4m3fn or int8 [pages, kv_heads, page, d]")
-    pages, heads, page, d = k_cache.shape
-    return Cache(_dev_ptr(k_cache, "k_cache", k_cache.dtype, k_cache.shape),
-                 _dev_ptr(v_cache, "v_cache", k_cache.dtype, k_cache.shape),
-                 _dev_ptr(k_scale, "k_scale", torch.float32, (pages, heads)),
-                 _dev_ptr(v_scale, "v_scale", torch.float32, (pages, heads)),
-                 pages, heads, page, d, _CACHE_TYPES[k_cache.dtype])
+    shape = k_cache.shape
+    pages, heads, page, d = shape
+    return dev, _CACHE.pack(
+        _dev_ptr(k_cache, "k_cache", k_cache.dtype, shape, dev),
+        _dev_ptr(v_cache, "v_cache", k_cache.dtype, shape, dev),
+        _dev_ptr(k_scale, "k_scale", torch.float32, (pages, heads), dev),
+        _dev_ptr(v_scale, "v_scale", torch.float32, (pages, heads), dev),
+        pages, heads, page, d, kind), heads, d
+
+
+def _cache_stream(stream, dev: int):
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(dev)
+    return _stream_handle(stream)
 
 
 def cache_resize(block_table: torch.Tensor, kv_len: torch.Tensor, new_len: torch.Tensor,
@@ -441,31 +459,34 @@ def cache_resize(block_table: torch.Tensor, kv_len: torch.Tensor, new_len: torch
     [1]; ``tokens`` is the capacity of the packed new tokens.  kv_len and free_count are
     updated in place unless other outputs are given.  Returns (cu_new [B + 1], slots
     [tokens], status [1]); a nonzero status means that nothing was changed."""
-    lib = load_library()
-    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+    lib = _lib or load_library()
+    dev = _this_device(block_table, "block_table")
+    if block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, max_pages]")
     B, max_pages = block_table.shape
     i32 = torch.int32
     tokens = int(tokens)
     if tokens < 0:
         raise ValueError("tokens must not be negative")
-    dev = block_table.device
-    kv_len_out = kv_len if kv_len_out is None else kv_len_out
-    free_count_out = free_count if free_count_out is None else free_count_out
-    with _on(stream):
-        cu_new = torch.empty(B + 1, dtype=i32, device=dev) if cu_new is None else cu_new
-        slots = torch.empty(tokens, dtype=i32, device=dev) if slots is None else slots
-        status = torch.empty(1, dtype=i32, device=dev) if status is None else status
+    if cu_new is None or slots is None or status is None:
+        with _on(stream):
+            where = block_table.device
+            cu_new = torch.empty(B + 1, dtype=i32, device=where) if cu_new is None else cu_new
+            slots = torch.empty(tokens, dtype=i32, device=where) if slots is None else slots
+            status = torch.empty(1, dtype=i32, device=where) if status is None else status
     n_pages = free_pages.numel()
+    len_ptr = _dev_ptr(kv_len, "kv_len", i32, (B,), dev)
+    count_ptr = _dev_ptr(free_count, "free_count", i32, (1,), dev)
     _check(lib.bsa_cache_resize(
-        _dev_ptr(block_table, "block_table", i32, (B, max_pages)),
-        _dev_ptr(kv_len, "kv_len", i32, (B,)), _dev_ptr(new_len, "new_len", i32, (B,)),
-        _dev_ptr(free_pages, "free_pages", i32, (n_pages,)),
-        _dev_ptr(free_count, "free_count", i32, (1,)), _dev_ptr(kv_len_out, "kv_len_out", i32, (B,)),
-        _dev_ptr(free_count_out, "free_count_out", i32, (1,)),
-        _dev_ptr(cu_new, "cu_new", i32, (B + 1,)), _dev_ptr(slots, "slots", i32, (tokens,)),
-        _dev_ptr(status, "status", i32, (1,)), B, max_pages, n_pages, int(page), tokens,
-        _stream_handle(stream)), "bsa_cache_resize")
+        _dev_ptr(block_table, "block_table", i32, (B, max_pages), dev), len_ptr,
+        _dev_ptr(new_len, "new_len", i32, (B,), dev),
+        _dev_ptr(free_pages, "free_pages", i32, (n_pages,), dev), count_ptr,
+        len_ptr if kv_len_out is None else _dev_ptr(kv_len_out, "kv_len_out", i32, (B,), dev),
+        count_ptr if free_count_out is None else
+        _dev_ptr(free_count_out, "free_count_out", i32, (1,), dev),
+        _dev_ptr(cu_new, "cu_new", i32, (B + 1,), dev), _dev_ptr(slots, "slots", i32, (tokens,), dev),
+        _dev_ptr(status, "status", i32, (1,), dev), B, max_pages, n_pages, int(page), tokens,
+        _cache_stream(stream, dev)), "bsa_cache_resize")
     return cu_new, slots, status
 
 
@@ -476,22 +497,22 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache:
     [T, kv_heads, d], any token and head stride; slots int32 [T] (cache_resize; -1: skip);
     caches float8_e4m3fn or int8 [pages, kv_heads, page, d], scales fp32 [pages, kv_heads],
     all on the current device and updated in place."""
-    lib = load_library()
-    c = _cache_view(k_cache, v_cache, k_scale, v_scale)
-    kp, kt, kh = _rows_ptr(k, "k", c.kv_heads, c.d)
-    vp, vt, vh = _rows_ptr(v, "v", c.kv_heads, c.d)
-    if v.dtype != k.dtype or v.shape != k.shape:
+    lib = _lib or load_library()
+    dev, cache, heads, d = _cache_view(k_cache, v_cache, k_scale, v_scale)
+    kp, kt, kh = _rows_ptr(k, "k", heads, d, dev)
+    vp, vt, vh = _rows_ptr(v, "v", heads, d, dev)
+    if v.dtype is not k.dtype or v.shape != k.shape:
         raise ValueError("k and v must have one type and shape")
     T = k.shape[0]
-    _check(lib.bsa_cache_append(ctypes.byref(c), kp, vp, _dev_ptr(slots, "slots", torch.int32, (T,)),
-                                T, _ACTIVATIONS[k.dtype], kt, kh, vt, vh, _stream_handle(stream)),
+    _check(lib.bsa_cache_append(cache, kp, vp, _dev_ptr(slots, "slots", torch.int32, (T,), dev), T,
+                                _ACTIVATIONS[k.dtype], kt, kh, vt, vh, _cache_stream(stream, dev)),
            "bsa_cache_append")
 
 
 def cache_workspace(heads: int, kv_heads: int, d: int, max_q: int) -> torch.Tensor:
     """A workspace for cache_forward on the current device, zeroed as its first call wants
     it; calls that may overlap on the GPU need one each."""
-    lib = load_library()
+    lib = _lib or load_library()
     n = ctypes.c_int64()
     _check(lib.bsa_cache_workspace(int(heads), int(kv_heads), int(d), int(max_q), ctypes.byref(n)),
            "bsa_cache_workspace")
@@ -511,40 +532,44 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     caches and scales as in cache_append; block_table int32 [B, max_pages], kv_len int32 [B]
     with the new tokens counted.  ``max_q``: the most queries of a request (T when None);
     ``window``: keys further back than that are masked (None or negative: no bound); ``lut``
-    with ``block``: only the layout's active blocks, one layout head per kv head.  Returns
-    (out [T, heads, d], lse fp32 [T, heads], status int32 [1]); a nonzero status (read after
-    the stream is synchronized) means a bounded wait gave up."""
-    lib = load_library()
-    c = _cache_view(k_cache, v_cache, k_scale, v_scale)
-    qp, qt, qh = _rows_ptr(q, "q", None, c.d)
-    T, heads, d = q.shape
+    with ``block``: only the layout's active blocks, one layout head per kv head;
+    ``workspace``: from cache_workspace (a zeroed one is made for the call when None).
+    Returns (out [T, heads, d], lse fp32 [T, heads], status int32 [1]); a nonzero status
+    (read after the stream is synchronized) means a bounded wait gave up."""
+    lib = _lib or load_library()
+    dev, cache, kv_heads, d = _cache_view(k_cache, v_cache, k_scale, v_scale)
+    qp, qt, qh = _rows_ptr(q, "q", None, d, dev)
+    T, heads, _ = q.shape
     if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
         raise ValueError("block_table must be int32 [B, max_pages]")
     B, max_pages = block_table.shape
     if lut is not None and block is None:
         raise ValueError("a lut needs its block")
     max_q = max(T, 1) if max_q is None else int(max_q)
-    with _on(stream):
-        if out is None:
-            out = torch.empty(T, heads, d, dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.empty(T, heads, dtype=torch.float32, device=q.device)
-        if status is None:
-            status = torch.empty(1, dtype=torch.int32, device=q.device)
-        if workspace is None:
-            workspace = cache_workspace(heads, c.kv_heads, d, max_q)
-    x = CacheArgs(-1 if window is None else int(window), float(softcap),
-                  None if sinks is None else _dev_ptr(sinks, "sinks", torch.float32, (heads,)),
-                  None if lut is None else lut.handle, 0 if block is None else int(block))
-    i32 = torch.int32
+    i32, f32 = torch.int32, torch.float32
+    if out is None or lse is None or status is None or workspace is None:
+        with _on(stream):
+            where = q.device
+            out = torch.empty(T, heads, d, dtype=q.dtype, device=where) if out is None else out
+            lse = torch.empty(T, heads, dtype=f32, device=where) if lse is None else lse
+            status = torch.empty(1, dtype=i32, device=where) if status is None else status
+            if workspace is None:
+                workspace = cache_workspace(heads, kv_heads, d, max_q)
+    args = None
+    if window is not None or softcap or sinks is not None or lut is not None:
+        args = _CACHE_ARGS.pack(-1 if window is None else max(-1, int(window)), float(softcap),
+                                0 if sinks is None else _dev_ptr(sinks, "sinks", f32, (heads,), dev),
+                                0 if lut is None else lut.handle.value,
+                                0 if block is None else int(block))
+    ws_bytes = workspace.numel()
     _check(lib.bsa_cache_forward(
-        ctypes.byref(c), qp, _dev_ptr(block_table, "block_table", i32, (B, max_pages)),
-        _dev_ptr(kv_len, "kv_len", i32, (B,)), _dev_ptr(cu_q, "cu_q", i32, (B + 1,)),
-        _dev_ptr(out, "out", q.dtype, (T, heads, d)), _dev_ptr(lse, "lse", torch.float32, (T, heads)),
-        _dev_ptr(status, "status", i32, (1,)),
-        _dev_ptr(workspace, "workspace", torch.uint8, (workspace.numel(),)), workspace.numel(),
-        B, max_pages, T, heads, max_q, _ACTIVATIONS[q.dtype], qt, qh, float(scale), ctypes.byref(x),
-        _stream_handle(stream)), "bsa_cache_forward")
+        cache, qp, _dev_ptr(block_table, "block_table", i32, (B, max_pages), dev),
+        _dev_ptr(kv_len, "kv_len", i32, (B,), dev), _dev_ptr(cu_q, "cu_q", i32, (B + 1,), dev),
+        _dev_ptr(out, "out", q.dtype, (T, heads, d), dev),
+        _dev_ptr(lse, "lse", f32, (T, heads), dev), _dev_ptr(status, "status", i32, (1,), dev),
+        _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, max_pages, T,
+        heads, max_q, _ACTIVATIONS[q.dtype], qt, qh, float(scale), args, _cache_stream(stream, dev)),
+        "bsa_cache_forward")
     return out, lse, status
 
 

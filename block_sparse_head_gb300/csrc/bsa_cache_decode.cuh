@@ -778,8 +778,8 @@ cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const Cach
                           void* workspace, int sms, cudaStream_t stream) {
   using Cfg = DecodeCfg<D, NT>;
   auto* kernel = bsa_cache_decode_kernel<A, C, D, NT>;
-  cudaError_t e =
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Cfg::kSmemB);
+  static int done[64];
+  const cudaError_t e = set_smem_once(kernel, Cfg::kSmemB, done);
   if (e != cudaSuccess) return e;
   kernel<<<sms, Cfg::kThreads, Cfg::kSmemB, stream>>>(k, v, p, workspace);
   return cudaGetLastError();

@@ -150,9 +150,9 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_resize_kernel(const CacheR
 
 cudaError_t launch_cache_resize(const CacheResizeParams& p, cudaStream_t stream) {
   const int smem = (4 * p.B + 3) * 4;
-  const cudaError_t e = cudaFuncSetAttribute(bsa_cache_resize_kernel,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (4 * kMaxResizeBatch + 3) * 4);
+  static int done[64];
+  const cudaError_t e =
+      set_smem_once(bsa_cache_resize_kernel, (4 * kMaxResizeBatch + 3) * 4, done);
   if (e != cudaSuccess) return e;
   bsa_cache_resize_kernel<<<1, kThreads, smem, stream>>>(p);
   return cudaGetLastError();

@@ -95,6 +95,20 @@ enum WaitSite : int {
 // Limit of every wait of the attention kernels over a cache.
 constexpr uint64_t kCacheWaitNs = 10000000000ull;
 
+// Raises a kernel's shared-memory limit once per device (done: one flag per device and
+// kernel; setting it twice in a race is harmless).  The call costs microseconds, as much as
+// a launch.
+template <class K>
+cudaError_t set_smem_once(K* kernel, int bytes, int (&done)[64]) {
+  int dev = -1;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 0 && dev < 64 && done[dev]) return cudaSuccess;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  if (e == cudaSuccess && dev >= 0 && dev < 64) done[dev] = 1;
+  return e;
+}
+
 // SMs of a device (0: the query failed).
 int sm_count(int dev);
 

@@ -19,7 +19,11 @@ def lib():
 
 
 def _cache(**kw):
-    return binding.Cache(kw.get("k", A), kw.get("v", A), kw.get("k_scale", A), kw.get("v_scale", A),
+    return binding._CACHE.pack(*(0 if x is None else x for x in _fields(kw)))
+
+
+def _fields(kw):
+    return (kw.get("k", A), kw.get("v", A), kw.get("k_scale", A), kw.get("v_scale", A),
                          kw.get("n_pages", 64), kw.get("kv_heads", 2), kw.get("page", 64),
                          kw.get("d", 128), kw.get("cache_dtype", 2))
 
@@ -51,7 +55,7 @@ def test_append(lib):
         c = _cache(**{n: kw[n] for n in kw if n in ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads",
                                                     "page", "d", "cache_dtype")})
         strides = [kw.get(n, 256) for n in ("kt", "kh", "vt", "vh")]
-        return lib.bsa_cache_append(ctypes.byref(c), kw.get("xk", A), kw.get("xv", A), kw.get("slots", A),
+        return lib.bsa_cache_append(c, kw.get("xk", A), kw.get("xv", A), kw.get("slots", A),
                                     kw.get("T", 5), kw.get("dtype", 0), *strides, None)
 
     for kw, status in CACHE_ERRORS:
@@ -75,13 +79,13 @@ def test_forward(lib):
     def f(**kw):
         c = _cache(**{n: kw[n] for n in kw if n in ("k", "v", "k_scale", "v_scale", "n_pages", "kv_heads",
                                                     "page", "d", "cache_dtype")})
-        x = binding.CacheArgs(kw.get("window", -1), kw.get("softcap", 0.0), kw.get("sinks"),
-                              kw.get("lut"), kw.get("block", 64))
+        x = binding._CACHE_ARGS.pack(kw.get("window", -1), kw.get("softcap", 0.0), kw.get("sinks", 0),
+                                     kw["lut"].value if "lut" in kw else 0, kw.get("block", 64))
         ptrs = [kw.get(n, A) for n in ("q", "table", "kv_len", "cu_q", "out", "lse", "status", "workspace")]
-        return lib.bsa_cache_forward(ctypes.byref(c), *ptrs, big, kw.get("B", 3), kw.get("max_pages", 8),
+        return lib.bsa_cache_forward(c, *ptrs, big, kw.get("B", 3), kw.get("max_pages", 8),
                                      kw.get("T", 9), kw.get("heads", 8), kw.get("max_q", 4), kw.get("dtype", 0),
                                      kw.get("qt", 1024), kw.get("qh", 128),
-                                     ctypes.c_float(kw.get("scale", 0.1)), ctypes.byref(x), None)
+                                     ctypes.c_float(kw.get("scale", 0.1)), x, None)
 
     for kw, status in CACHE_ERRORS:
         assert f(**kw) == status, kw
