@@ -27,13 +27,12 @@ SOURCES = [
     "bsa_cache_host.cpp",
     "bsa_cache_resize.cu",
     "bsa_cache_append.cu",
-    "bsa_cache_fwd.cu",
-] + [f"bsa_cache_decode_{c}_d{d}.cu" for c in ("e4m3", "int8") for d in (64, 128)
-] + [f"bsa_fwd_q{qb}_k{kb}_d{d}.cu" for qb, kb in ((64, 64), (128, 128), (64, 128), (128, 64))
+] + [f"bsa_cache_{k}_{c}_d{d}.cu" for k in ("decode", "tile") for c in ("e4m3", "int8")
+     for d in (64, 128)] + [f"bsa_fwd_q{qb}_k{kb}_d{d}.cu" for qb, kb in ((64, 64), (128, 128), (64, 128), (128, 64))
      for d in (64, 128)] + [f"bsa_bwd_b{b}_d{d}.cu" for b in (64, 128) for d in (64, 128)]
 HEADERS = ["bsa_internal.h", "bsa_ptx.cuh", "bsa_fwd_kernel.cuh", "bsa_bwd_kernel.cuh",
            "bsa_topk_kernel.cuh", "bsa_cache.cuh", "bsa_cache_sched.cuh",
-           "bsa_cache_decode.cuh"]
+           "bsa_cache_decode.cuh", "bsa_cache_tile.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

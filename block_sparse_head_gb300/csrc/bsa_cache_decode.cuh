@@ -151,16 +151,21 @@ template <int kThreads>
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
-struct ConsumerBarrier {
+template <bool kInline>
+struct BoundedBarrier {
   uint32_t bar, phase;
   __device__ __forceinline__ bool sync(int lane, const WaitCtl& ctl) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    const bool ok = mbar_wait(bar, phase, ctl, kSiteCacheJoin);
+    bool ok;
+    if constexpr (kInline) ok = mbar_wait_inl(bar, phase, ctl, kSiteCacheJoin);
+    else ok = mbar_wait(bar, phase, ctl, kSiteCacheJoin);
     phase ^= 1;
     return __all_sync(0xffffffffu, ok);
   }
 };
+using ConsumerBarrier = BoundedBarrier<false>;
+using ConsumerBarrierInl = BoundedBarrier<true>;  // where registers are split per warpgroup
 
 template <class C, int D, int NT>
 __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const CUtensorMap* tm_k,

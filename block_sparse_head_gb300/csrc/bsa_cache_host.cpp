@@ -143,7 +143,7 @@ int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* byte
   const int sms = bsa::sm_count(dev);
   if (sms <= 0) return BSA_ERR_CUDA;
   const int rows = decode_rows(heads / kv_heads, max_q);
-  *bytes = rows > 0 ? bsa::cache_parts_bytes(sms, rows, d) : 16;
+  *bytes = bsa::cache_parts_bytes(sms, rows > 0 ? rows : bsa::kTileRows, d);
   return BSA_OK;
 }
 
@@ -225,11 +225,11 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   }
   cudaError_t e;
   const int rows = decode_rows(p.group, max_q);
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+  const int sms = bsa::sm_count(dev);
+  const bool fp16 = dtype == BSA_FP16, int8 = cache->dtype == BSA_INT8;
   if (rows > 0) {
-    int dev = -1;
-    if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
-    const int sms = bsa::sm_count(dev);
-    const bool fp16 = dtype == BSA_FP16, int8 = cache->dtype == BSA_INT8;
     const int64_t tiles = static_cast<int64_t>(cache->n_pages) * cache->kv_heads;
     p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
     CUtensorMap k, v;
@@ -242,7 +242,10 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
             : (int8 ? bsa::launch_cache_decode_int8_d64(fp16, rows, k, v, p, workspace, sms, st)
                     : bsa::launch_cache_decode_e4m3_d64(fp16, rows, k, v, p, workspace, sms, st));
   } else {
-    e = bsa::launch_cache_fwd(cache->d, dtype, cache->dtype, p, st);
+    e = cache->d == 128 ? (int8 ? bsa::launch_cache_tile_int8_d128(fp16, p, workspace, sms, st)
+                                : bsa::launch_cache_tile_e4m3_d128(fp16, p, workspace, sms, st))
+                        : (int8 ? bsa::launch_cache_tile_int8_d64(fp16, p, workspace, sms, st)
+                                : bsa::launch_cache_tile_e4m3_d64(fp16, p, workspace, sms, st));
   }
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

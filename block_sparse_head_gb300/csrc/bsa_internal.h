@@ -90,6 +90,7 @@ enum WaitSite : int {
   kSiteSoftStatsFree = 14,
   kSiteSelftest = 15,
   kSiteCacheJoin = 16,
+  kSiteCacheInfo = 17,
 };
 
 // Limit of every wait of the attention kernels over a cache.
@@ -261,9 +262,6 @@ struct CacheFwdParams {
   float softcap_log2;        // cap * log2(e); 0: no soft-cap
   float softcap_inv;         // scale / cap
 };
-cudaError_t launch_cache_fwd(int d, int dtype, int cache_dtype, const CacheFwdParams& p,
-                             cudaStream_t stream);
-
 // Bytes of the partial results that `grid` CTAs of `rows` query rows may leave for the join
 // (bsa_cache_sched.cuh): a counter, and two pieces of rows * d numbers and rows pairs.
 inline int64_t cache_parts_bytes(int grid, int rows, int d) {
@@ -282,6 +280,17 @@ BSA_DECODE_LAUNCH(e4m3_d128);
 BSA_DECODE_LAUNCH(int8_d64);
 BSA_DECODE_LAUNCH(int8_d128);
 #undef BSA_DECODE_LAUNCH
+
+// Any number of query rows, in tiles of kTileRows.
+constexpr int kTileRows = 128;
+#define BSA_TILE_LAUNCH(name)                                                                \
+  cudaError_t launch_cache_tile_##name(bool fp16, const CacheFwdParams& p, void* workspace,  \
+                                       int sms, cudaStream_t stream)
+BSA_TILE_LAUNCH(e4m3_d64);
+BSA_TILE_LAUNCH(e4m3_d128);
+BSA_TILE_LAUNCH(int8_d64);
+BSA_TILE_LAUNCH(int8_d128);
+#undef BSA_TILE_LAUNCH
 
 // A cache side [tiles, page, d] of 8-bit numbers for boxes of `rows` rows of one tile,
 // swizzled over their whole row (128 or 64 bytes).  false: the encoder refused.
