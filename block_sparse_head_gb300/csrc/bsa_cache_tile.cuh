@@ -47,7 +47,7 @@ struct TileCfg {
   static constexpr int kOffV = kOffK + 2 * kTileB;
   static constexpr int kOffFactor = kOffV + 2 * kTileB;          // [kItems][128] fp32
   static constexpr int kOffInfo = kOffFactor + kItems * 128 * 4;
-  static constexpr int kInfoB = 192;
+  static constexpr int kInfoB = 224;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoB;
   // barriers
   static constexpr int kSF = 0;                 // [3] S(t) computed
@@ -82,8 +82,9 @@ struct TileStep {
   int tile[8];    // per 16 keys: page * heads + head, -1: not there
   float ks[8];    // scale of the scores (1 where the keys are not there)
   float lv[8];    // log2 of the value scale (-inf where the keys are not there)
+  float rv[8];    // its reciprocal (0 where the keys are not there)
 };
-static_assert(sizeof(TileStep) <= 192, "step slots");
+static_assert(sizeof(TileStep) <= 224, "step slots");
 
 // ---------------------------------------------------------------------- look-ups
 
@@ -132,6 +133,7 @@ __device__ __forceinline__ void tile_producer(const CacheFwdParams& p, uint8_t* 
           st.tile[j] = tile;
           st.ks[j] = ks;
           st.lv[j] = lv;
+          st.rv[j] = tile < 0 ? 0.f : ex2_approx(-lv);
           if ((j & 3) == 0) st.key0[j >> 2] = key;
         }
         if (lane == 0) {
@@ -229,6 +231,20 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, const 
 
 // --------------------------------------------------------------------- converter
 
+// 16 bytes, or zeros: a predicated load (as a branch, each of a thread's loads would wait
+// for the address of the one before).
+__device__ __forceinline__ uint4 load16_if(const void* ptr, bool on) {
+  uint4 x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
+      : "l"(ptr), "r"(static_cast<int>(on)));
+  return x;
+}
+
 template <class A, class C, int D>
 __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const WaitCtl& ctl) {
   using Cfg = TileCfg<D>;
@@ -253,16 +269,17 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   // A step's stored numbers of one side into registers; what no query of the tile sees is
   // zero (the cache may hold anything there).
   auto load = [&](const TileStep& st, const uint8_t* cache, uint4 (&x)[NP]) {
-    const int last = st.seg.pos0 + st.seg.nq - 1;
+    const int last = st.seg.pos0 + st.seg.nq - 1, lo = st.seg.lo_key;
+    const int k0 = st.key0[0], k1 = st.key0[1];
+    int tile[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) tile[i] = st.tile[(i * RPP + r0) >> 4];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int row = i * RPP + r0, tile = st.tile[row >> 4];
-      const int key = st.key0[row >> 6] + (row & 63);
-      x[i] = make_uint4(0, 0, 0, 0);
-      if (tile >= 0 && key <= last && key >= st.seg.lo_key)
-        x[i] = *reinterpret_cast<const uint4*>(
-            cache + ((static_cast<int64_t>(tile) << p.page_shift) + (key & ((1 << p.page_shift) - 1))) * D +
-            piece * 16);
+      const int row = i * RPP + r0, key = (i < NP / 2 ? k0 : k1) + (row & 63);
+      x[i] = load16_if(cache + ((static_cast<int64_t>(tile[i]) << p.page_shift) +
+                                (key & ((1 << p.page_shift) - 1))) * D + piece * 16,
+                       tile[i] >= 0 && key <= last && key >= lo);
     }
   };
   // 16 stored numbers to fp16, two 16-byte pieces of a swizzled row (the order of the two
@@ -284,96 +301,94 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
     }
   };
 
+  // Iteration t stores K(t), requests K(t + 1), stores V(t - 1) and requests V(t).
   int item = -1;
-  bool ok = wait_warp(Cfg::kIF, 0, kSiteCacheInfo);
-  bool end = !ok || (info(0).flags & kStageEnd);
-  if (ok && !end) load(info(0), p.k_cache, kr);
-  int t = 0;
-  for (; ok && !end; ++t) {
-    const int flags = info(t).flags;
-    // S(t - 2) read the K tile that this step overwrites, and the Q tile of the item before
-    // the last one (whose last step it is at the latest).
-    if (t >= 2 && !(ok = wait_warp(Cfg::kSF + (t - 2) % 3, ((t - 2) / 3) & 1, kSiteProdKEmpty))) break;
-    if (flags & kStageFirst) {
-      ++item;
-      // Row tid of the tile: query and head, scaled into fp16's range.
-      const CacheSeg& s = info(t).seg;
-      const int qi = static_cast<int>((tid * p.group_inv) >> 16);
-      const bool live = qi < s.nq;
-      const A* q = static_cast<const A*>(p.q) + (s.q0 + qi) * p.q_token_stride +
-                   (s.h * p.group + tid - qi * p.group) * p.q_head_stride;
-      float up = 1.f, back = 1.f;
-      if constexpr (!std::is_same<A, __half>::value) {
-        float top = 0.f;
-        if (live) {
+  for (int t = -1;; ++t) {
+    const int flags = t < 0 ? 0 : info(t).flags;
+    const bool end = flags & kStageEnd;
+    if (t >= 0 && !end) {
+      // S(t - 2) read the K tile that this step overwrites, and the Q tile of the item before
+      // the last one (whose last step it is at the latest).
+      if (t >= 2 && !wait_warp(Cfg::kSF + (t - 2) % 3, ((t - 2) / 3) & 1, kSiteProdKEmpty)) break;
+      if (flags & kStageFirst) {
+        ++item;
+        // Row tid of the tile: query and head, scaled into fp16's range.
+        const CacheSeg& s = info(t).seg;
+        const int qi = static_cast<int>((tid * p.group_inv) >> 16);
+        const bool live = qi < s.nq;
+        const A* q = static_cast<const A*>(p.q) + (s.q0 + qi) * p.q_token_stride +
+                     (s.h * p.group + tid - qi * p.group) * p.q_head_stride;
+        float up = 1.f, back = 1.f;
+        if constexpr (!std::is_same<A, __half>::value) {
+          float top = 0.f;
+          if (live) {
 #pragma unroll 4
-          for (int c = 0; c < D / 8; ++c) {
-            const uint4 x = *reinterpret_cast<const uint4*>(q + 8 * c);
-            const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+            for (int c = 0; c < D / 8; ++c) {
+              const uint4 x = *reinterpret_cast<const uint4*>(q + 8 * c);
+              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = act_to_float2<A>(w[i]);
-              top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = act_to_float2<A>(w[i]);
+                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
             }
           }
+          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
+          const int k = max(-113, min(120, 14 - e));
+          up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+          back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
         }
-        const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-        const int k = max(-113, min(120, 14 - e));
-        up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-        back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
-      }
-      uint8_t* row = smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB + tid * 128;
+        uint8_t* row = smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB + tid * 128;
 #pragma unroll 4
-      for (int c = 0; c < D / 8; ++c) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (live) {
-          x = *reinterpret_cast<const uint4*>(q + 8 * c);
-          if constexpr (!std::is_same<A, __half>::value) {
-            uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (live) {
+            x = *reinterpret_cast<const uint4*>(q + 8 * c);
+            if constexpr (!std::is_same<A, __half>::value) {
+              uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = act_to_float2<A>(w[i]);
-              w[i] = float2_to_act<__half>(f.x * up, f.y * up);
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = act_to_float2<A>(w[i]);
+                w[i] = float2_to_act<__half>(f.x * up, f.y * up);
+              }
+              x = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            x = make_uint4(w[0], w[1], w[2], w[3]);
           }
+          *reinterpret_cast<uint4*>(row + (c >> 3) * Cfg::kHalfB + (((c & 7) ^ (tid & 7)) << 4)) = x;
         }
-        *reinterpret_cast<uint4*>(row + (c >> 3) * Cfg::kHalfB + (((c & 7) ^ (tid & 7)) << 4)) = x;
+        reinterpret_cast<float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + tid] = back;
+        fence_proxy_async_smem();
+        arrive(Cfg::kQF + item % Cfg::kItems);
       }
-      reinterpret_cast<float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + tid] = back;
+      store(smem + Cfg::kOffK + (t & 1) * Cfg::kTileB, kr);
       fence_proxy_async_smem();
-      arrive(Cfg::kQF + item % Cfg::kItems);
+      arrive(Cfg::kKF + (t & 1));
     }
-    store(smem + Cfg::kOffK + (t & 1) * Cfg::kTileB, kr);
-    fence_proxy_async_smem();
-    arrive(Cfg::kKF + (t & 1));
-    // The next step's keys are requested before this step's predecessor's values are stored.
-    const int nx = t + 1;
-    if (!(ok = wait_warp(Cfg::kIF + nx % Cfg::kInfo, (nx / Cfg::kInfo) & 1, kSiteCacheInfo))) break;
-    end = info(nx).flags & kStageEnd;
-    if (!end) load(info(nx), p.k_cache, kr);
+    if (!end) {
+      const int nx = t + 1;
+      if (!wait_warp(Cfg::kIF + nx % Cfg::kInfo, (nx / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
+      if (!(info(nx).flags & kStageEnd)) load(info(nx), p.k_cache, kr);
+    }
     if (t > 0) {
       // PV(t - 3) read the V tile that V(t - 1) overwrites.
-      if (t >= 3 && !(ok = wait_warp(Cfg::kPVD + (t - 3) % 3, ((t - 3) / 3) & 1, kSiteProdVEmpty))) break;
+      if (t >= 3 && !wait_warp(Cfg::kPVD + (t - 3) % 3, ((t - 3) / 3) & 1, kSiteProdVEmpty)) break;
       store(smem + Cfg::kOffV + ((t - 1) & 1) * Cfg::kTileB, vr);
       fence_proxy_async_smem();
       arrive(Cfg::kVF + ((t - 1) & 1));
     }
-    load(info(t), p.v_cache, vr);
-    arrive(Cfg::kIE + t % Cfg::kInfo);
-  }
-  if (ok && t > 0) {  // the last step's values
-    if (t < 3 || wait_warp(Cfg::kPVD + (t - 3) % 3, ((t - 3) / 3) & 1, kSiteProdVEmpty)) {
-      store(smem + Cfg::kOffV + ((t - 1) & 1) * Cfg::kTileB, vr);
-      fence_proxy_async_smem();
-      arrive(Cfg::kVF + ((t - 1) & 1));
+    if (end) break;
+    if (t >= 0) {
+      load(info(t), p.v_cache, vr);
+      arrive(Cfg::kIE + t % Cfg::kInfo);
     }
   }
 }
 
 // ----------------------------------------------------------------------- softmax
 
-template <class A, int D>
+// FOLD: positive scale and no soft-cap, so that the scores' factor goes into the exponent's
+// multiplier; else they are transformed first.
+template <class A, int D, bool FOLD>
 __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* smem, uint32_t tmem,
                                              const CacheParts& parts, int* join_flag, const WaitCtl& ctl) {
   using Cfg = TileCfg<D>;
@@ -398,9 +413,6 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     if (lane == 0) mbar_arrive(bar(b));
   };
   ConsumerBarrierInl cb{bar(Cfg::kJoin), 0};
-  // Positive scale, no soft-cap: the scores' factor goes into the exponent.  Else they are
-  // transformed first.
-  const bool fold = p.softcap_log2 == 0.f && p.scale_log2 > 0.f;
 
   CacheSeg seg{};          // of the item whose O is pending
   float m = -INFINITY, l = 0.f, rf = 1.f;
@@ -475,16 +487,30 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     return cb.sync(lane, ctl);
   };
 
-  int t = 0;
-  bool ok = true, pending = false;
-  for (;; ++t) {
+  bool pending = false;
+  for (int t = 0;; ++t) {
     const int slot = t % Cfg::kInfo;
-    if (!(ok = wait_bar(Cfg::kIF + slot, (t / Cfg::kInfo) & 1, kSiteCacheInfo))) break;
+    if (!wait_bar(Cfg::kIF + slot, (t / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
     const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
     const int flags = st.flags;
-    if (flags & kStageEnd) break;
     const bool first = flags & kStageFirst;
-    if (!(ok = wait_bar(Cfg::kSF + t % 3, (t / 3) & 1, kSiteSoftSFull))) break;
+    if (flags & (kStageFirst | kStageEnd)) {
+      // The previous item's O goes out before this step's P is handed over (the product that
+      // reads it overwrites O).
+      if (pending && !(finish(t - 1) && join())) break;
+      if (flags & kStageEnd) break;
+      pending = true;
+      ++item;
+      if (!wait_bar(Cfg::kQF + item % Cfg::kItems, (item / Cfg::kItems) & 1, kSiteSoftSFull)) break;
+      seg = st.seg;
+      live = qi < seg.nq;
+      qpos = live ? seg.pos0 + qi : -1;
+      rf = reinterpret_cast<const float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + row] *
+           (FOLD || p.softcap_log2 == 0.f ? p.scale_log2 : p.softcap_inv);
+      m = -INFINITY;
+      l = 0.f;
+    }
+    if (!wait_bar(Cfg::kSF + t % 3, (t / 3) & 1, kSiteSoftSFull)) break;
     float x[NC];
     const uint32_t ts = tl + (t % 3) * 128;
     {
@@ -499,27 +525,6 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
         x[32 + i] = __uint_as_float(b[i]);
       }
     }
-    // An item's first step: the previous item's O goes out before this step's P is handed
-    // over (the product that reads it overwrites O).
-    bool joins = false;
-    if (first) {
-      if (pending) {
-        if (!(ok = finish(t - 1))) break;
-        joins = true;
-      }
-    }
-    const CacheSeg before = seg;
-    if (first) {
-      ++item;
-      if (!(ok = wait_bar(Cfg::kQF + item % Cfg::kItems, (item / Cfg::kItems) & 1, kSiteSoftSFull))) break;
-      seg = st.seg;
-      live = qi < seg.nq;
-      qpos = live ? seg.pos0 + qi : -1;
-      rf = reinterpret_cast<const float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + row] *
-           (p.softcap_log2 > 0.f ? p.softcap_inv : p.scale_log2);
-      m = -INFINITY;
-      l = 0.f;
-    }
     const int key0 = st.key0[half];
     float c[4], a[4];
 #pragma unroll
@@ -527,7 +532,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       c[i] = rf * st.ks[half * 4 + i];
       a[i] = st.lv[half * 4 + i];
     }
-    if (!fold) {
+    if constexpr (!FOLD) {
 #pragma unroll
       for (int i = 0; i < NC; ++i) {
         x[i] *= c[i >> 4];
@@ -544,8 +549,14 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       int lo = 0, hi = min(NC - 1, qpos - key0);
       if (p.window >= 0) lo = max(lo, qpos - p.window - key0);
       if (__any_sync(0xffffffffu, lo > 0 || hi < NC - 1)) {
+        // Bit i: score i is seen.
+        uint64_t seen = hi < lo ? 0ull : (~0ull >> (63 - (hi - lo))) << lo;
+        const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
 #pragma unroll
-        for (int i = 0; i < NC; ++i) x[i] = mask_outside(x[i], i, lo, hi);
+        for (int i = 0; i < 32; ++i) {
+          x[i] = (s0 >> i) & 1 ? x[i] : -INFINITY;
+          x[32 + i] = (s1 >> i) & 1 ? x[32 + i] : -INFINITY;
+        }
       }
     }
     float mx = -INFINITY;
@@ -586,9 +597,8 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
           pk[8 * g + i] = float2_to_act<__half>(f2_lo(e), f2_hi(e));
         }
         s2 = f2_add(s2, s3);
-        // w / vs; keys that are not there have no scale
-        const float rv = a[g] == -INFINITY ? 0.f : ex2_approx(-a[g]);
-        sum = fmaf(f2_lo(s2) + f2_hi(s2), rv, sum);
+        // w / vs
+        sum = fmaf(f2_lo(s2) + f2_hi(s2), st.rv[half * 4 + g], sum);
       }
       tmem_st_16x32bx2_x32<32>(ts, pk);
     }
@@ -596,7 +606,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     l = l * alpha + sum;
     if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
       // PV(t - 1) must be complete before O is rescaled.
-      if (!(ok = wait_bar(Cfg::kPVD + (t - 1) % 3, ((t - 1) / 3) & 1, kSiteSoftPvDone))) break;
+      if (!wait_bar(Cfg::kPVD + (t - 1) % 3, ((t - 1) / 3) & 1, kSiteSoftPvDone)) break;
 #pragma unroll
       for (int g = 0; g < D / 64; ++g) {
         uint32_t r[32];
@@ -611,21 +621,12 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     warp_arrive(Cfg::kPF + t % 3);
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(Cfg::kIE + slot));
-    pending = true;
-    if (joins) {
-      const CacheSeg now = seg;
-      seg = before;
-      ok = join();
-      seg = now;
-      if (!ok) break;
-    }
   }
-  if (ok && pending && finish(t - 1)) join();
 }
 
 // ------------------------------------------------------------------------ kernel
 
-template <class A, class C, int D>
+template <class A, class C, int D, bool FOLD>
 __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdParams p, void* workspace) {
   using Cfg = TileCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -682,7 +683,7 @@ __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdPa
     }
   } else if (warp < 12) {
     setmaxnreg_inc<Cfg::kRegSoft>();
-    tile_softmax<A, D>(p, smem, tmem, parts, err + 2, ctl);
+    tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 2, ctl);
   } else {
     setmaxnreg_dec<Cfg::kRegConv>();
     tile_convert<A, C, D>(p, smem, ctl);
@@ -698,10 +699,10 @@ __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdPa
   if (threadIdx.x == 0 && err[0] != 0) atomicMax(p.status, err[0]);
 }
 
-template <class A, class C, int D>
-cudaError_t launch_tile(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
+template <class A, class C, int D, bool FOLD>
+cudaError_t launch_tile_as(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
   using Cfg = TileCfg<D>;
-  auto* kernel = bsa_cache_tile_kernel<A, C, D>;
+  auto* kernel = bsa_cache_tile_kernel<A, C, D, FOLD>;
   static int done[64], regs = 0;
   cudaError_t e = set_smem_once(kernel, Cfg::kLaunchSmem, done);
   if (e != cudaSuccess) return e;
@@ -716,6 +717,13 @@ cudaError_t launch_tile(const CacheFwdParams& p, void* workspace, int sms, cudaS
   if (regs != Cfg::kLaunchRegs) return cudaErrorInvalidConfiguration;
   kernel<<<sms, Cfg::kThreads, Cfg::kLaunchSmem, stream>>>(p, workspace);
   return cudaGetLastError();
+}
+
+template <class A, class C, int D>
+cudaError_t launch_tile(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
+  return p.softcap_log2 == 0.f && p.scale_log2 > 0.f
+             ? launch_tile_as<A, C, D, true>(p, workspace, sms, stream)
+             : launch_tile_as<A, C, D, false>(p, workspace, sms, stream);
 }
 
 }  // namespace bsa
