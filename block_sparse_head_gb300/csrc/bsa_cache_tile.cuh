@@ -47,7 +47,7 @@ struct TileCfg {
   static constexpr int kOffV = kOffK + 2 * kTileB;
   static constexpr int kOffFactor = kOffV + 2 * kTileB;          // [kItems][128] fp32
   static constexpr int kOffInfo = kOffFactor + kItems * 128 * 4;
-  static constexpr int kInfoB = 224;
+  static constexpr int kInfoB = 240;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoB;
   // barriers
   static constexpr int kSF = 0;                 // [3] S(t) computed
@@ -76,15 +76,15 @@ struct TileCfg {
 
 // What the roles need to know of a step.
 struct TileStep {
-  CacheSeg seg;   // of every step
+  CacheSeg seg;   // of every step (13 words)
   int flags;      // DecodeFlags
   int key0[2];    // first key of each piece (kNoKeys: none)
-  int tile[8];    // per 16 keys: page * heads + head, -1: not there
+  int64_t off[8]; // per 16 keys: where they start in the cache (bytes), -1: not there
   float ks[8];    // scale of the scores (1 where the keys are not there)
   float lv[8];    // log2 of the value scale (-inf where the keys are not there)
   float rv[8];    // its reciprocal (0 where the keys are not there)
 };
-static_assert(sizeof(TileStep) <= 224, "step slots");
+static_assert(sizeof(TileStep) <= 240, "step slots");
 
 // ---------------------------------------------------------------------- look-ups
 
@@ -105,6 +105,7 @@ __device__ __forceinline__ void tile_producer(const CacheFwdParams& p, uint8_t* 
     for (int s = 0; s < steps; s += 4) {
       const int piece = seg.s0 + 2 * s + (lane >> 2);
       int key = kNoKeys, tile = -1;
+      int64_t off = -1;
       float ks = 1.f, lv = -INFINITY;
       if (seg.nq > 0 && piece < seg.s1) {
         key = piece << 6;
@@ -119,6 +120,7 @@ __device__ __forceinline__ void tile_producer(const CacheFwdParams& p, uint8_t* 
             tile = pid * p.Hkv + seg.h;
             ks = p.k_scale[tile];
             lv = log2_scale(p.v_scale[tile]);
+            off = ((static_cast<int64_t>(tile) << p.page_shift) + (k & ((1 << p.page_shift) - 1))) * D;
           }
         }
       }
@@ -130,7 +132,7 @@ __device__ __forceinline__ void tile_producer(const CacheFwdParams& p, uint8_t* 
         TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
         const int j = lane - 8 * i;
         if (j >= 0 && j < 8) {
-          st.tile[j] = tile;
+          st.off[j] = off;
           st.ks[j] = ks;
           st.lv[j] = lv;
           st.rv[j] = tile < 0 ? 0.f : ex2_approx(-lv);
@@ -248,13 +250,15 @@ __device__ __forceinline__ uint4 load16_if(const void* ptr, bool on) {
 template <class A, class C, int D>
 __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const WaitCtl& ctl) {
   using Cfg = TileCfg<D>;
-  constexpr int LPR = D / 16;         // lanes of a key row (16 stored numbers each)
-  constexpr int RPP = 128 / LPR;      // rows of a pass over the 128 threads
+  constexpr int RPP = 128 * 16 / D;   // rows of a pass of the 128 threads, 16 numbers each
   constexpr int NP = 128 / RPP;       // passes of a tile
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
-  const int tid = threadIdx.x & 127, lane = tid & 31;
-  const int r0 = tid / LPR, piece = tid % LPR;  // row of a pass, 16-number piece of the row
+  const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
+  // Row of a pass and 16-number piece of it.  Eight neighbouring lanes have four pieces each of
+  // an even and an odd row, which the swizzle puts on different banks.
+  const int piece = (lane & 3) | (D == 128 ? (lane >> 1) & 4 : 0);
+  const int r0 = warp * (RPP / 4) + (D == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2);
   auto info = [&](int t) -> const TileStep& {
     return *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + (t % Cfg::kInfo) * Cfg::kInfoB);
   };
@@ -268,40 +272,38 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   uint4 kr[NP], vr[NP];
   // A step's stored numbers of one side into registers; what no query of the tile sees is
   // zero (the cache may hold anything there).
+  const int64_t mine = (r0 & 15) * D + piece * 16;
   auto load = [&](const TileStep& st, const uint8_t* cache, uint4 (&x)[NP]) {
+    // Rows of the two pieces of the step that some query of the tile sees.
     const int last = st.seg.pos0 + st.seg.nq - 1, lo = st.seg.lo_key;
-    const int k0 = st.key0[0], k1 = st.key0[1];
-    int tile[NP];
+    const int lo0 = lo - st.key0[0], hi0 = last - st.key0[0], lo1 = lo - st.key0[1], hi1 = last - st.key0[1];
+    int64_t off[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) tile[i] = st.tile[(i * RPP + r0) >> 4];
+    for (int i = 0; i < NP; ++i) off[i] = st.off[(i * RPP + r0) >> 4];
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int row = i * RPP + r0, key = (i < NP / 2 ? k0 : k1) + (row & 63);
-      x[i] = load16_if(cache + ((static_cast<int64_t>(tile[i]) << p.page_shift) +
-                                (key & ((1 << p.page_shift) - 1))) * D + piece * 16,
-                       tile[i] >= 0 && key <= last && key >= lo);
+      const int r = (i * RPP + r0) & 63;
+      const bool seen = i < NP / 2 ? r >= lo0 && r <= hi0 : r >= lo1 && r <= hi1;
+      x[i] = load16_if(cache + mine + off[i], off[i] >= 0 && seen);
     }
   };
-  // 16 stored numbers to fp16, two 16-byte pieces of a swizzled row (the order of the two
-  // alternates over the lanes, which spreads them over the banks).
-  auto store = [&](uint8_t* tile, const uint4 (&x)[NP]) {
+  // 16 stored numbers to fp16, two 16-byte pieces of a swizzled row.
+  uint8_t* const dst0 = smem + (piece >> 2) * Cfg::kHalfB + r0 * 128 + (((2 * (piece & 3)) ^ (r0 & 7)) << 4);
+  uint8_t* const dst1 = smem + (piece >> 2) * Cfg::kHalfB + r0 * 128 + (((2 * (piece & 3) + 1) ^ (r0 & 7)) << 4);
+  auto store = [&](int tile, const uint4 (&x)[NP]) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int row = i * RPP + r0;
       uint32_t h[8];
       stored4_to_half2<C>(x[i].x, h[0], h[1]);
       stored4_to_half2<C>(x[i].y, h[2], h[3]);
       stored4_to_half2<C>(x[i].z, h[4], h[5]);
       stored4_to_half2<C>(x[i].w, h[6], h[7]);
-      uint8_t* dst = tile + (piece >> 2) * Cfg::kHalfB + row * 128;
-      const int c = 2 * (piece & 3), swap = (piece >> 2) & 1;
-      const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-      *reinterpret_cast<uint4*>(dst + (((c + swap) ^ (row & 7)) << 4)) = swap ? b : a;
-      *reinterpret_cast<uint4*>(dst + (((c + 1 - swap) ^ (row & 7)) << 4)) = swap ? a : b;
+      *reinterpret_cast<uint4*>(dst0 + tile + i * RPP * 128) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(dst1 + tile + i * RPP * 128) = make_uint4(h[4], h[5], h[6], h[7]);
     }
   };
 
-  // Iteration t stores K(t), requests K(t + 1), stores V(t - 1) and requests V(t).
+  // Iteration t stores K(t) and V(t - 1), then requests K(t + 1) and V(t).
   int item = -1;
   for (int t = -1;; ++t) {
     const int flags = t < 0 ? 0 : info(t).flags;
@@ -360,23 +362,23 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         fence_proxy_async_smem();
         arrive(Cfg::kQF + item % Cfg::kItems);
       }
-      store(smem + Cfg::kOffK + (t & 1) * Cfg::kTileB, kr);
-      fence_proxy_async_smem();
-      arrive(Cfg::kKF + (t & 1));
-    }
-    if (!end) {
-      const int nx = t + 1;
-      if (!wait_warp(Cfg::kIF + nx % Cfg::kInfo, (nx / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
-      if (!(info(nx).flags & kStageEnd)) load(info(nx), p.k_cache, kr);
+      store(Cfg::kOffK + (t & 1) * Cfg::kTileB, kr);
     }
     if (t > 0) {
       // PV(t - 3) read the V tile that V(t - 1) overwrites.
       if (t >= 3 && !wait_warp(Cfg::kPVD + (t - 3) % 3, ((t - 3) / 3) & 1, kSiteProdVEmpty)) break;
-      store(smem + Cfg::kOffV + ((t - 1) & 1) * Cfg::kTileB, vr);
-      fence_proxy_async_smem();
-      arrive(Cfg::kVF + ((t - 1) & 1));
+      store(Cfg::kOffV + ((t - 1) & 1) * Cfg::kTileB, vr);
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0 && t >= 0) {
+      if (!end) mbar_arrive(bar(Cfg::kKF + (t & 1)));
+      if (t > 0) mbar_arrive(bar(Cfg::kVF + ((t - 1) & 1)));
     }
     if (end) break;
+    const int nx = t + 1;
+    if (!wait_warp(Cfg::kIF + nx % Cfg::kInfo, (nx / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
+    if (!(info(nx).flags & kStageEnd)) load(info(nx), p.k_cache, kr);
     if (t >= 0) {
       load(info(t), p.v_cache, vr);
       arrive(Cfg::kIE + t % Cfg::kInfo);
