@@ -5,73 +5,209 @@
 // when the page keeps tokens before the run; kept numbers become rn(y * s_old / s), new
 // ones rn(x / s).  Both rounds are to 8 bits, once; scale_for explains the power of two.
 //
-// One CTA per (token, head); the CTA of a run's first token does the run, the others leave.
+// Bound: memory (a number is read as 16 bits and written as 8).  A CTA takes CT tokens of one
+// head and side and does the runs that begin there, however far they go: a run of up to two
+// tokens (a decode step) is a warp's, any other the CTA's, which holds its share of the page in
+// registers (at most eight 16-byte pieces a thread) between the maximum and the rounding, so
+// that the numbers are read once.  CT is 1 while that gives at most kSmallGrid CTAs (many
+// short runs at once, in little time), then 16 for pages of up to 32 tokens and 64 for larger
+// ones, which leaves few CTAs that only see that no run begins in their tokens.
 #include "bsa_cache.cuh"
 #include "bsa_internal.h"
+
+#include <type_traits>
 
 namespace bsa {
 
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kShortRun = 2;      // tokens of a run that a warp takes
+constexpr int kSmallGrid = 4096;
 
-template <class A, class C, int D>
+// Bits of the smallest magnitude that is not finite.
+template <class A>
+constexpr uint32_t kInfBits = std::is_same<A, __half>::value ? 0x7C00u : 0x7F80u;
+
+// Largest magnitudes (as bits, which order like the numbers) of the halves of w and m.
+__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t w) {
+  return __vmaxu2(m, w & 0x7FFF7FFFu);
+}
+// The same over the finite ones.
+template <class A>
+__device__ __forceinline__ uint32_t max_finite(uint32_t m, uint32_t w) {
+  w &= 0x7FFF7FFFu;
+  if ((w & 0xFFFFu) >= kInfBits<A>) w &= 0xFFFF0000u;
+  if ((w >> 16) >= kInfBits<A>) w &= 0xFFFFu;
+  return __vmaxu2(m, w);
+}
+template <class A>
+__device__ __forceinline__ bool has_nonfinite(uint32_t m) {
+  return (m & 0xFFFFu) >= kInfBits<A> || (m >> 16) >= kInfBits<A>;
+}
+__device__ __forceinline__ uint32_t warp_max(uint32_t m) {
+#pragma unroll
+  for (int s = 1; s < 32; s *= 2) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, s));
+  return m;
+}
+// The larger half of m as a number.
+template <class A>
+__device__ __forceinline__ float larger(uint32_t m) {
+  const float2 f = act_to_float2<A>(m);
+  return fmaxf(f.x, f.y);
+}
+
+template <class A, class C>
+__device__ __forceinline__ uint32_t quantise4(uint32_t a, uint32_t b, float inv) {
+  const float2 f = act_to_float2<A>(a), h = act_to_float2<A>(b);
+  return float2_to_stored<C>(f.x * inv, f.y * inv) | float2_to_stored<C>(h.x * inv, h.y * inv) << 16;
+}
+
+// Rounds `words` words of kept numbers to a grown scale; every `step`-th from `first` on.
+template <class C>
+__device__ __forceinline__ void rescale(uint32_t* cache, int words, float ratio, int first, int step) {
+  for (int i = first; i < words; i += step) {
+    const uint32_t w = cache[i];
+    const float2 lo = stored_to_float2<C>(w & 0xFFFFu), hi = stored_to_float2<C>(w >> 16);
+    cache[i] = float2_to_stored<C>(lo.x * ratio, lo.y * ratio) |
+               float2_to_stored<C>(hi.x * ratio, hi.y * ratio) << 16;
+  }
+}
+
+template <class A, class C, int D, int CT>
 __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheAppendParams p) {
-  const int t = blockIdx.x, h = blockIdx.y;
-  const int slot = p.slots[t], pid = slot >> p.page_shift;
-  if (pid < 0 || pid >= p.n_pages) return;
-  if (t > 0 && (p.slots[t - 1] >> p.page_shift) == pid) return;  // not the run's first
-  int t1 = t + 1;
-  while (t1 < p.T && (p.slots[t1] >> p.page_shift) == pid) ++t1;
-  const int page = 1 << p.page_shift, start = slot & (page - 1);
-  __shared__ float s_max[kThreads / 32];
-  constexpr int HD = D / 2;  // pairs of a token
-  for (int side = 0; side < 2; ++side) {
-    const A* x = static_cast<const A*>(p.x[side]) + h * p.head_stride[side];
-    const int64_t tile = static_cast<int64_t>(pid) * p.heads + h;
-    uint16_t* cache = static_cast<uint16_t*>(p.cache[side]) + tile * page * HD;
-    float amax = 0.f;
-    for (int i = threadIdx.x; i < (t1 - t) * HD; i += kThreads) {
-      const uint32_t w = *reinterpret_cast<const uint32_t*>(
-          x + (t + i / HD) * p.token_stride[side] + 2 * (i % HD));
-      const float2 f = act_to_float2<A>(w);
-      if (isfinite(f.x)) amax = fmaxf(amax, fabsf(f.x));
-      if (isfinite(f.y)) amax = fmaxf(amax, fabsf(f.y));
-    }
-    for (int n = 16; n >= 1; n /= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, n));
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) s_max[threadIdx.x >> 5] = amax;
-    __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) amax = fmaxf(amax, s_max[w]);
-    const float was = start > 0 ? p.scale[side][tile] : 0.f;
-    const float now = fmaxf(was, scale_for<C>(amax));
-    __syncthreads();
-    if (threadIdx.x == 0) p.scale[side][tile] = now;
-    if (start > 0 && now != was) {
-      const float ratio = was / now;
-      for (int i = threadIdx.x; i < start * HD; i += kThreads) {
-        const float2 y = stored_to_float2<C>(cache[i]);
-        cache[i] = static_cast<uint16_t>(float2_to_stored<C>(y.x * ratio, y.y * ratio));
+  constexpr int NS = (CT + 31) / 32;   // a warp looks at 32 tokens at a time
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y;
+  const bool v = blockIdx.z;
+  const int t0 = blockIdx.x * CT, page = 1 << p.page_shift;
+  const int64_t stride = v ? p.token_stride[1] : p.token_stride[0];
+  const A* const in = static_cast<const A*>(v ? p.x[1] : p.x[0]) + h * (v ? p.head_stride[1] : p.head_stride[0]);
+  uint8_t* const out = static_cast<uint8_t*>(v ? p.cache[1] : p.cache[0]);
+  float* const scales = v ? p.scale[1] : p.scale[0];
+  auto page_of = [&](int t) {  // -1: no such token or page
+    if (t < 0 || t >= p.T) return -1;
+    const int id = p.slots[t] >> p.page_shift;
+    return id < p.n_pages ? id : -1;
+  };
+  // Every warp looks at the chunk's tokens: which begin a run.
+  int pid[NS], before[NS];
+#pragma unroll
+  for (int u = 0; u < NS; ++u) {
+    const int i = 32 * u + lane;
+    pid[u] = i < CT ? page_of(t0 + i) : -1;
+    before[u] = i < CT ? page_of(t0 + i - 1) : -1;
+  }
+  __shared__ uint32_t s_max[kWarps];
+  int k = 0;  // runs of the chunk so far
+#pragma unroll
+  for (int u = 0; u < NS; ++u) {
+    for (uint32_t heads = __ballot_sync(0xffffffffu, pid[u] >= 0 && pid[u] != before[u]); heads != 0;
+         heads &= heads - 1, ++k) {
+      const int i = __ffs(heads) - 1, t = t0 + 32 * u + i;
+      const int id = __shfl_sync(0xffffffffu, pid[u], i), start = p.slots[t] & (page - 1);
+      const int64_t tile = static_cast<int64_t>(id) * p.heads + h;
+      const float was = start > 0 ? scales[tile] : 0.f;
+      // Tokens of the run; they fill the page from `start` on.
+      int n = 1;
+      for (int at = t + 1 + lane;; at += 32) {
+        const uint32_t same = __ballot_sync(0xffffffffu, page_of(at) == id);
+        n += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
+        if (same != 0xffffffffu || n >= page) break;
       }
-    }
-    const float inv = 1.f / now;  // exact: a power of two
-    for (int i = threadIdx.x; i < (t1 - t) * HD; i += kThreads) {
-      const int u = t + i / HD;
-      const uint32_t w =
-          *reinterpret_cast<const uint32_t*>(x + u * p.token_stride[side] + 2 * (i % HD));
-      const float2 f = act_to_float2<A>(w);
-      cache[(p.slots[u] & (page - 1)) * HD + i % HD] =
-          static_cast<uint16_t>(float2_to_stored<C>(f.x * inv, f.y * inv));
+      n = min(n, page - start);
+      uint8_t* const cache = out + tile * page * D;
+      if (n <= kShortRun) {
+        // ---- a warp
+        if (k % kWarps != warp) continue;
+        constexpr int E = D / 64;  // words of a token per lane
+        uint32_t x[kShortRun][E], m = 0;
+#pragma unroll
+        for (int w = 0; w < kShortRun; ++w)
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[w][e] = 0;
+            if (w < n)
+              x[w][e] = *reinterpret_cast<const uint32_t*>(in + (t + w) * stride + 2 * (lane * E + e));
+            m = max_finite<A>(m, x[w][e]);
+          }
+        const float now = fmaxf(was, scale_for<C>(larger<A>(warp_max(m))));
+        if (start > 0 && now != was)
+          rescale<C>(reinterpret_cast<uint32_t*>(cache), start * (D / 4), was / now, lane, 32);
+        const float inv = 1.f / now;  // exact: a power of two
+#pragma unroll
+        for (int w = 0; w < kShortRun; ++w) {
+          if (w >= n) break;
+          uint8_t* dst = cache + (start + w) * D + lane * 2 * E;
+          if constexpr (E == 2) {
+            *reinterpret_cast<uint32_t*>(dst) = quantise4<A, C>(x[w][0], x[w][1], inv);
+          } else {
+            const float2 f = act_to_float2<A>(x[w][0]);
+            *reinterpret_cast<uint16_t*>(dst) =
+                static_cast<uint16_t>(float2_to_stored<C>(f.x * inv, f.y * inv));
+          }
+        }
+        if (lane == 0) scales[tile] = now;
+        continue;
+      }
+      // ---- the CTA: 16-byte pieces, kThreads at a time
+      constexpr int PPT = D / 8;                  // pieces of a token
+      constexpr int RMAX = 128 * PPT / kThreads;  // of the longest run, per thread
+      const int pieces = n * PPT;
+      const A* const src = in + (t + tid / PPT) * stride + 8 * (tid % PPT);
+      uint4 x[RMAX];
+      uint32_t m = 0;
+#pragma unroll
+      for (int r = 0; r < RMAX; ++r) {
+        x[r] = make_uint4(0, 0, 0, 0);
+        if (r * kThreads + tid < pieces)
+          x[r] = *reinterpret_cast<const uint4*>(src + r * (kThreads / PPT) * stride);
+      }
+#pragma unroll
+      for (int r = 0; r < RMAX; ++r)
+        m = max_bits(max_bits(max_bits(max_bits(m, x[r].x), x[r].y), x[r].z), x[r].w);
+      if (has_nonfinite<A>(m)) {
+        m = 0;
+#pragma unroll
+        for (int r = 0; r < RMAX; ++r)
+          m = max_finite<A>(max_finite<A>(max_finite<A>(max_finite<A>(m, x[r].x), x[r].y), x[r].z), x[r].w);
+      }
+      m = warp_max(m);
+      __syncthreads();  // s_max of the run before has been read
+      if (lane == 0) s_max[warp] = m;
+      __syncthreads();  // and every thread has the old scale
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = __vmaxu2(m, s_max[w]);
+      const float now = fmaxf(was, scale_for<C>(larger<A>(m)));
+      if (start > 0 && now != was)
+        rescale<C>(reinterpret_cast<uint32_t*>(cache), start * (D / 4), was / now, tid, kThreads);
+      const float inv = 1.f / now;
+      uint8_t* const dst = cache + (start + tid / PPT) * D + 8 * (tid % PPT);
+#pragma unroll
+      for (int r = 0; r < RMAX; ++r)
+        if (r * kThreads + tid < pieces)
+          *reinterpret_cast<uint2*>(dst + r * (kThreads / PPT) * D) =
+              make_uint2(quantise4<A, C>(x[r].x, x[r].y, inv), quantise4<A, C>(x[r].z, x[r].w, inv));
+      if (tid == 0) scales[tile] = now;
     }
   }
 }
 
+template <class A, class C, int D>
+cudaError_t launch(const CacheAppendParams& p, cudaStream_t stream) {
+  auto grid = [&](int ct) { return dim3((p.T + ct - 1) / ct, p.heads, 2); };
+  if (static_cast<int64_t>(p.T) * p.heads * 2 <= kSmallGrid)
+    bsa_cache_append_kernel<A, C, D, 1><<<grid(1), kThreads, 0, stream>>>(p);
+  else if (p.page_shift <= 5)
+    bsa_cache_append_kernel<A, C, D, 16><<<grid(16), kThreads, 0, stream>>>(p);
+  else
+    bsa_cache_append_kernel<A, C, D, 64><<<grid(64), kThreads, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
 template <class A, class C>
 cudaError_t launch(int d, const CacheAppendParams& p, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(p.T), static_cast<unsigned>(p.heads));
-  if (d == 128) bsa_cache_append_kernel<A, C, 128><<<grid, kThreads, 0, stream>>>(p);
-  else bsa_cache_append_kernel<A, C, 64><<<grid, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  return d == 128 ? launch<A, C, 128>(p, stream) : launch<A, C, 64>(p, stream);
 }
 
 }  // namespace
