@@ -98,6 +98,10 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheA
     pid[u] = i < CT ? page_of(t0 + i) : -1;
     before[u] = i < CT ? page_of(t0 + i - 1) : -1;
   }
+  const int after = page_of(t0 + CT + lane);
+  uint32_t goes_on[NS];
+#pragma unroll
+  for (int u = 0; u < NS; ++u) goes_on[u] = __ballot_sync(0xffffffffu, pid[u] >= 0 && pid[u] == before[u]);
   __shared__ uint32_t s_max[kWarps];
   int k = 0;  // runs of the chunk so far
 #pragma unroll
@@ -110,10 +114,22 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheA
       const float was = start > 0 ? scales[tile] : 0.f;
       // Tokens of the run; they fill the page from `start` on.
       int n = 1;
-      for (int at = t + 1 + lane;; at += 32) {
-        const uint32_t same = __ballot_sync(0xffffffffu, page_of(at) == id);
+      bool open = true;  // the run may go on
+#pragma unroll
+      for (int w = u; w < NS; ++w) {
+        const int from = w == u ? i + 1 : 0, width = min(32, CT - 32 * w) - from;
+        if (open && width > 0) {
+          const uint32_t rest = ~(goes_on[w] >> from);
+          const int more = rest == 0 ? 32 : __ffs(rest) - 1;
+          n += min(more, width);
+          open = more >= width;
+        }
+      }
+      for (int at = t0 + CT + lane; open && n < page; at += 32) {
+        const uint32_t same =
+            __ballot_sync(0xffffffffu, (at == t0 + CT + lane ? after : page_of(at)) == id);
         n += same == 0xffffffffu ? 32 : __ffs(~same) - 1;
-        if (same != 0xffffffffu || n >= page) break;
+        open = same == 0xffffffffu;
       }
       n = min(n, page - start);
       uint8_t* const cache = out + tile * page * D;
