@@ -151,21 +151,16 @@ template <int kThreads>
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
-template <bool kInline>
-struct BoundedBarrier {
+struct ConsumerBarrier {
   uint32_t bar, phase;
   __device__ __forceinline__ bool sync(int lane, const WaitCtl& ctl) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    bool ok;
-    if constexpr (kInline) ok = mbar_wait_inl(bar, phase, ctl, kSiteCacheJoin);
-    else ok = mbar_wait(bar, phase, ctl, kSiteCacheJoin);
+    const bool ok = mbar_wait(bar, phase, ctl, kSiteCacheJoin);
     phase ^= 1;
     return __all_sync(0xffffffffu, ok);
   }
 };
-using ConsumerBarrier = BoundedBarrier<false>;
-using ConsumerBarrierInl = BoundedBarrier<true>;  // where registers are split per warpgroup
 
 template <class C, int D, int NT>
 __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const CUtensorMap* tm_k,
@@ -332,7 +327,7 @@ __device__ __forceinline__ void join_row(const CacheFwdParams& p, const CachePar
 #pragma unroll
   for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
   float z = sink == -INFINITY ? 0.f : ex2_approx(sink - top), o[E] = {};
-#pragma unroll 8
+#pragma unroll 4
   for (int i = 0; i <= more; ++i) {
     const int64_t at = slot(i);
     const float2 x = __ldcg(&parts.ml[at]);

@@ -8,22 +8,25 @@
 // cache; work is split on the device (bsa_cache_sched.cuh), one persistent CTA per SM:
 //   warp 0      S issuer (one thread): S(t) = Q K(t)^T into one of three TMEM buffers.
 //   warp 1      PV issuer: O += P(t) V(t), P read from the S buffer it was written over.
-//   warp 2      looks pages and scales up, two steps and more ahead (ring of 8 steps).
-//   softmax     warps 4-11.  Lanes t and t + 16 hold the two pieces of one row.  The K scale
+//   warp 2      looks pages and scales up, a batch of four steps ahead (ring of 8 steps).
+//   warp 3      brings the stored numbers in by TMA, 64 keys of one side a place.
+//   softmax     warps 4-11.  Lanes t and t + 16 hold the two halves of a row's piece.  The K scale
 //               of a page belongs to 16 keys at least, so it is folded into the exponent's
 //               multiplier per group of 16, and log2 of the V scale into its addend, as in
 //               the decode kernel: w = exp2(s + log2 vs - m), the sum takes w / vs, weights
 //               are rounded to fp16 relative to the largest (2^-11).  An item's O is read out
 //               at the next item's first step.
-//   converter   warps 12-15.  Stored numbers from global memory (16 bytes a lane, a step ahead
-//               in registers) to fp16 tiles in shared memory, in the 128-byte-swizzled layout
-//               that the products read; also the queries, bf16 ones scaled per row by a power
-//               of two into fp16's range.
-// Shared memory holds two tiles each of Q, K and V (192 KB); a step writes 64 KB into it and
-// the products read 96 KB of it, which bounds a step at about 1,280 cycles against the 1,024
-// of its products.
+//   converters  warps 12-15 for K (and the queries, bf16 ones scaled per row by a power of two
+//               into fp16's range), 16-19 for V: stored numbers to fp16 tiles in the
+//               128-byte-swizzled layout that the products read.  A lane's pieces are chosen so
+//               that neither its reads nor its writes meet another's banks.
+// Shared memory holds a tile of Q and two each of K and V in fp16 (160 KB), and seven places of
+// stored numbers (56 KB): a step writes 64 KB of fp16 into it and the products read 96 KB of
+// it, which bounds a step at about 1,280 cycles against the 1,024 of its products.  The loops
+// are rolled up where they can be: all roles' code has to fit the instruction cache, whose
+// misses were the first version's largest stall.
 //
-// Every wait is bounded (WaitCtl): one that runs out records a timeout, and all roles leave
+// Every wait is bounded: one that runs out records a timeout, and all roles leave
 // their loops, let the products in flight finish, free TMEM and return.
 #pragma once
 
@@ -33,36 +36,42 @@ namespace bsa {
 
 template <int D>
 struct TileCfg {
-  static constexpr int kThreads = 512;
+  static constexpr int kThreads = 640;
   static constexpr int kRows = 128;
-  static constexpr int kLaunchRegs = 128;
-  static constexpr int kRegCtl = 88, kRegSoft = 160, kRegConv = 104;
-  static_assert(kRegCtl + 2 * kRegSoft + kRegConv == 4 * kLaunchRegs, "register split");
   static constexpr int kTileB = 128 * D * 2;   // one fp16 tile of Q, K or V
   static constexpr int kHalfB = 128 * 128;     // its 64-column halves, [128][64] swizzled
+  static constexpr int kRawB = 64 * D;         // stored numbers of 64 keys of one side
+  static constexpr int kRawK = 4, kRawV = 3;   // places of them
   static constexpr int kInfo = 8;              // steps looked up ahead
   static constexpr int kItems = 8;             // items whose row factors are kept
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + 2 * kTileB;
+  static constexpr int kOffK = kOffQ + kTileB;
   static constexpr int kOffV = kOffK + 2 * kTileB;
-  static constexpr int kOffFactor = kOffV + 2 * kTileB;          // [kItems][128] fp32
-  static constexpr int kOffInfo = kOffFactor + kItems * 128 * 4;
-  static constexpr int kInfoB = 240;
+  static constexpr int kOffRawK = kOffV + 2 * kTileB;
+  static constexpr int kOffRawV = kOffRawK + kRawK * kRawB;
+  static constexpr int kOffFactor = kOffRawV + kRawV * kRawB;    // [kItems][128] fp32
+  static constexpr int kOffSegs = kOffFactor + kItems * 128 * 4; // the producer's segments
+  static constexpr int kOffInfo = kOffSegs + 4 * 64;
+  static constexpr int kInfoB = 208;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoB;
   // barriers
   static constexpr int kSF = 0;                 // [3] S(t) computed
   static constexpr int kPVD = 3;                // [3] PV(t) complete
   static constexpr int kPF = 6;                 // [3] P(t) written (softmax warps)
-  static constexpr int kKF = 9;                 // [2] K(t) converted (converter warps)
-  static constexpr int kVF = 11;                // [2] V(t) converted
+  static constexpr int kKF = 9;                 // [2] K(t) converted (4 warps)
+  static constexpr int kVF = 11;                // [2] V(t) converted (4 warps)
   static constexpr int kQF = 13;                // [kItems] Q of an item converted
   static constexpr int kIF = kQF + kItems;      // [kInfo] step looked up
   static constexpr int kIE = kIF + kInfo;       // [kInfo] step no longer needed
-  static constexpr int kDrain = kIE + kInfo;    // [2] S, PV issuers' last products
+  static constexpr int kRKF = kIE + kInfo;      // [kRawK] 64 keys landed
+  static constexpr int kRKE = kRKF + kRawK;     // [kRawK] and converted (4 warps)
+  static constexpr int kRVF = kRKE + kRawK;     // [kRawV]
+  static constexpr int kRVE = kRVF + kRawV;     // [kRawV]
+  static constexpr int kDrain = kRVE + kRawV;   // [2] S, PV issuers' last products
   static constexpr int kJoin = kDrain + 2;      // softmax warps
   static constexpr int kNumBars = kJoin + 1;
   static constexpr int kOffScan = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
-  static constexpr int kOffWalk = kOffScan + 16 * 8;
+  static constexpr int kOffWalk = kOffScan + 32 * 8;
   static constexpr int kOffCtl = kOffWalk + 96;  // TMEM address, status, abort flag, join
   static constexpr int kSmemB = kOffCtl + 16 + 1024;
   static_assert(kSmemB <= 232448, "shared memory");
@@ -79,76 +88,198 @@ struct TileStep {
   CacheSeg seg;   // of every step (13 words)
   int flags;      // DecodeFlags
   int key0[2];    // first key of each piece (kNoKeys: none)
-  int64_t off[8]; // per 16 keys: where they start in the cache (bytes), -1: not there
-  float ks[8];    // scale of the scores (1 where the keys are not there)
+  int there[2];   // per piece: bit i says that its keys 16 i .. are there
+  int tile[8];    // per 16 keys that are there: page * heads + head
+  float ks[8];    // per 16 keys: scale of the scores (1 where the keys are not there)
   float lv[8];    // log2 of the value scale (-inf where the keys are not there)
   float rv[8];    // its reciprocal (0 where the keys are not there)
 };
-static_assert(sizeof(TileStep) <= 240, "step slots");
+static_assert(sizeof(TileStep) <= 208, "step slots");
 
 // ---------------------------------------------------------------------- look-ups
 
 template <int D>
-__device__ __forceinline__ void tile_producer(const CacheFwdParams& p, uint8_t* smem,
-                                              const CacheUnits& units, const WaitCtl& ctl) {
+__device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* smem,
+                                            const CacheUnits& units, volatile int* ctl) {
   using Cfg = TileCfg<D>;
   const int lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   CacheWalk walk = *reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk);
-  CacheSeg seg;
-  int t = 0;
-  for (;;) {
-    walk.next(units, seg);
-    const int steps = seg.nq == 0 ? 1 : max(1, (seg.s1 - seg.s0 + 1) / 2);
-    // Four steps at a time: lane 8 i + j looks up group j of step i.
-    for (int s = 0; s < steps; s += 4) {
-      const int piece = seg.s0 + 2 * s + (lane >> 2);
-      int key = kNoKeys, tile = -1;
-      int64_t off = -1;
-      float ks = 1.f, lv = -INFINITY;
-      if (seg.nq > 0 && piece < seg.s1) {
-        key = piece << 6;
-        if (p.row_ptr != nullptr) {
-          const int sub = p.block_shift - 6;
-          key = (p.col_idx[seg.rp + (piece >> sub)] << p.block_shift) + ((piece & ((1 << sub) - 1)) << 6);
-        }
-        const int k = key + 16 * (lane & 3);
-        if (k < seg.pos0 + seg.nq && k + 16 > seg.lo_key) {
-          const int pid = p.table[static_cast<int64_t>(seg.b) * p.max_pages + (k >> p.page_shift)];
-          if (pid >= 0 && pid < p.n_pages) {
-            tile = pid * p.Hkv + seg.h;
-            ks = p.k_scale[tile];
-            lv = log2_scale(p.v_scale[tile]);
-            off = ((static_cast<int64_t>(tile) << p.page_shift) + (k & ((1 << p.page_shift) - 1))) * D;
-          }
-        }
-      }
-      for (int i = 0; i < 4 && s + i < steps; ++i, ++t) {
-        const int slot = t % Cfg::kInfo;
-        if (t >= Cfg::kInfo &&
-            !mbar_wait_inl(bar(Cfg::kIE + slot), (t / Cfg::kInfo - 1) & 1, ctl, kSiteProdKEmpty))
-          return;
-        TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
-        const int j = lane - 8 * i;
-        if (j >= 0 && j < 8) {
-          st.off[j] = off;
-          st.ks[j] = ks;
-          st.lv[j] = lv;
-          st.rv[j] = tile < 0 ? 0.f : ex2_approx(-lv);
-          if ((j & 3) == 0) st.key0[j >> 2] = key;
-        }
-        if (lane == 0) {
-          st.seg = seg;
-          st.flags = seg.nq == 0 ? kStageEnd
-                                 : (s + i == 0 ? kStageFirst : 0) | (s + i + 1 == steps ? kStageLast : 0);
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(Cfg::kIF + slot));
+  // Up to four steps of one segment: lane 8 i + j looks up group j (16 keys) of step i.  The
+  // look-ups depend on one another (layout block, page, scales), each a trip to memory; the
+  // next batch's are made one by one between the steps of this one.
+  struct Batch {
+    int seg, s, steps;  // place of its segment, first step, steps of the segment (0: the end)
+    int key, pid, tile;
+    float ks, vs;
+  };
+  auto seg_at = [&](int i) -> CacheSeg& {
+    return *reinterpret_cast<CacheSeg*>(smem + Cfg::kOffSegs + 64 * (i & 3));
+  };
+  auto place = [&](const Batch& before, Batch& x) {
+    if (before.s + 4 < before.steps) {
+      x.seg = before.seg;
+      x.s = before.s + 4;
+      x.steps = before.steps;
+    } else {
+      CacheSeg seg;
+      walk.next(units, seg);  // every lane walks the same way
+      x.seg = before.seg + 1;
+      x.s = 0;
+      x.steps = seg.nq == 0 ? 0 : max(1, (seg.s1 - seg.s0 + 1) / 2);
+      if (lane == 0) seg_at(x.seg) = seg;
+      __syncwarp();
+    }
+    const CacheSeg& seg = seg_at(x.seg);
+    const int piece = seg.s0 + 2 * x.s + (lane >> 2);
+    x.key = kNoKeys;
+    if (x.steps > 0 && piece < seg.s1)
+      x.key = p.row_ptr != nullptr ? p.col_idx[seg.rp + (piece >> (p.block_shift - 6))] : piece << 6;
+  };
+  auto find_page = [&](Batch& x) {
+    x.pid = -1;
+    if (x.key == kNoKeys) return;
+    const CacheSeg& seg = seg_at(x.seg);
+    if (p.row_ptr != nullptr) {
+      const int piece = seg.s0 + 2 * x.s + (lane >> 2), sub = p.block_shift - 6;
+      x.key = (x.key << p.block_shift) + ((piece & ((1 << sub) - 1)) << 6);
+    }
+    const int k = x.key + 16 * (lane & 3);
+    if (k < seg.pos0 + seg.nq && k + 16 > seg.lo_key)
+      x.pid = p.table[static_cast<int64_t>(seg.b) * p.max_pages + (k >> p.page_shift)];
+  };
+  auto find_scales = [&](Batch& x) {
+    x.tile = -1;
+    if (x.pid < 0 || x.pid >= p.n_pages) return;
+    x.tile = x.pid * p.Hkv + seg_at(x.seg).h;
+    x.ks = p.k_scale[x.tile];
+    x.vs = p.v_scale[x.tile];
+  };
+  Batch cur{}, next{};
+  cur.seg = -1;
+  next = cur;
+  place(next, cur);
+  find_page(cur);
+  find_scales(cur);
+  for (int t = 0, i = 0;; ++t, ++i) {
+    if (cur.steps > 0 && (i == 4 || cur.s + i >= cur.steps)) {
+      const int n = i;  // look-ups of next that the steps of cur left
+      if (n < 1) place(cur, next);
+      if (n < 2) find_page(next);
+      if (n < 3) find_scales(next);
+      cur = next;
+      i = 0;
+    }
+    const bool end = cur.steps == 0;
+    const int slot = t % Cfg::kInfo;
+    if (t >= Cfg::kInfo &&
+        !mbar_wait_tries(bar(Cfg::kIE + slot), (t / Cfg::kInfo - 1) & 1, ctl, kSiteProdKEmpty))
+      break;
+    TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    const int j = lane - 8 * i;
+    const bool on = cur.tile >= 0 && !end;
+    const uint32_t seen = __ballot_sync(0xffffffffu, on) >> (8 * i);
+    if (j >= 0 && j < 8) {
+      const float lv = log2_scale(cur.vs);
+      st.tile[j] = cur.tile;
+      st.ks[j] = on ? cur.ks : 1.f;
+      st.lv[j] = on ? lv : -INFINITY;
+      st.rv[j] = on ? ex2_approx(-lv) : 0.f;
+      if ((j & 3) == 0) {
+        st.key0[j >> 2] = cur.key;
+        st.there[j >> 2] = seen >> (j & 4) & 15;
       }
     }
-    if (seg.nq == 0) return;
+    if (lane < static_cast<int>(sizeof(CacheSeg) / 4))
+      reinterpret_cast<int*>(&st.seg)[lane] = reinterpret_cast<const int*>(&seg_at(cur.seg))[lane];
+    if (lane == 0)
+      st.flags = end ? kStageEnd
+                     : (cur.s + i == 0 ? kStageFirst : 0) | (cur.s + i + 1 == cur.steps ? kStageLast : 0);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(Cfg::kIF + slot));
+    if (end) break;
+    if (i == 0) place(cur, next);
+    else if (i == 1) find_page(next);
+    else if (i == 2) find_scales(next);
   }
+}
+
+// ------------------------------------------------------------------------ copies
+
+// One warp: stored numbers into the raw places, K of step t and then V of step t - 1 (whose
+// place is free later).  Lane j < 8 has group j of 16 keys.
+template <int D>
+__device__ __forceinline__ void tile_copy(const CacheFwdParams& p, const CUtensorMap* tm_k,
+                                          const CUtensorMap* tm_v, uint8_t* smem, volatile int* ctl) {
+  using Cfg = TileCfg<D>;
+  const int lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
+  // A box (2^box rows) is copied whole if any of its groups is there, by the lane of the first
+  // that is.
+  const int box = p.box_shift, groups = 1 << (box - 4);
+  const int base = lane & ~(groups - 1);
+  // Where this lane's copy goes in the piece, and its box's first row in the page.
+  struct Place {
+    bool load;
+    int tile, row;
+    uint32_t pieces;  // boxes of the first and (<< 8) of the second piece
+  };
+  auto place_of = [&](const TileStep& st) {
+    Place x;
+    const int there = st.there[0] | st.there[1] << 4;
+    const int mine = there >> base & ((1 << groups) - 1);
+    x.load = lane < 8 && mine != 0 && lane == base + __ffs(mine) - 1;
+    x.tile = st.tile[lane & 7];
+    x.row = (st.key0[lane >> 2 & 1] + 16 * (base & 3)) & ((1 << p.page_shift) - 1);
+    const uint32_t on = __ballot_sync(0xffffffffu, x.load);
+    x.pieces = __popc(on & 15u) | __popc(on & 0xF0u) << 8;
+    return x;
+  };
+  int pieces_k = 0, pieces_v = 0;  // announced so far
+  auto copy = [&](const CUtensorMap* tm, const Place& x, int full, int raw, int places, int site,
+                  int& n) -> bool {
+    const int s0 = n % places, s1 = (n + 1) % places;
+    const int empty = full + places;
+    if (n >= places && !mbar_wait_tries(bar(empty + s0), (n / places - 1) & 1, ctl, site)) return false;
+    if (n + 1 >= places && !mbar_wait_tries(bar(empty + s1), ((n + 1) / places - 1) & 1, ctl, site))
+      return false;
+    if (lane == 0) {
+      mbar_arrive_expect_tx(bar(full + s0), (x.pieces & 0xFF) * (D << box));
+      mbar_arrive_expect_tx(bar(full + s1), (x.pieces >> 8) * (D << box));
+    }
+    __syncwarp();
+    if (x.load) {
+      const int s = lane < 4 ? s0 : s1;
+      tma_load_3d(sbase + raw + s * Cfg::kRawB + 16 * (base & 3) * D, tm, bar(full + s), 0, x.row, x.tile);
+    }
+    n += 2;
+    return true;
+  };
+  static_assert(Cfg::kRKE == Cfg::kRKF + Cfg::kRawK && Cfg::kRVE == Cfg::kRVF + Cfg::kRawV, "order");
+  Place v{};
+  for (int t = 0;; ++t) {
+    const int slot = t % Cfg::kInfo;
+    if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
+    const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    const bool end = st.flags & kStageEnd;
+    Place k{};
+    if (!end) {
+      k = place_of(st);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(Cfg::kIE + slot));
+      if (!copy(tm_k, k, Cfg::kRKF, Cfg::kOffRawK, Cfg::kRawK, kSiteProdKEmpty, pieces_k)) break;
+    }
+    if (t > 0 && !copy(tm_v, v, Cfg::kRVF, Cfg::kOffRawV, Cfg::kRawV, kSiteProdVEmpty, pieces_v)) break;
+    if (end) break;
+    v = k;
+  }
+  // Every copy lands before the CTA leaves (also when the converters have given up).
+  for (int n = max(0, pieces_k - Cfg::kRawK); n < pieces_k; ++n)
+    mbar_drain_wait(bar(Cfg::kRKF + n % Cfg::kRawK), (n / Cfg::kRawK) & 1);
+  for (int n = max(0, pieces_v - Cfg::kRawV); n < pieces_v; ++n)
+    mbar_drain_wait(bar(Cfg::kRVF + n % Cfg::kRawV), (n / Cfg::kRawV) & 1);
 }
 
 // ------------------------------------------------------------------- MMA issuers
@@ -167,7 +298,7 @@ struct TileDescs {
 };
 
 template <int D>
-__device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, const WaitCtl& ctl) {
+__device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatile int* ctl) {
   using Cfg = TileCfg<D>;
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
@@ -175,21 +306,21 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, const W
   int item = -1;
   for (int t = 0;; ++t) {
     const int slot = t % Cfg::kInfo;
-    if (!mbar_wait_inl(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
+    if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
     const int flags = reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB)->flags;
     mbar_arrive(bar(Cfg::kIE + slot));
     if (flags & kStageEnd) break;
     if (flags & kStageFirst) {
       ++item;
-      if (!mbar_wait_inl(bar(Cfg::kQF + item % Cfg::kItems), (item / Cfg::kItems) & 1, ctl, kSiteMmaStage))
+      if (!mbar_wait_tries(bar(Cfg::kQF + item % Cfg::kItems), (item / Cfg::kItems) & 1, ctl, kSiteMmaStage))
         break;
     }
-    if (!mbar_wait_inl(bar(Cfg::kKF + (t & 1)), (t >> 1) & 1, ctl, kSiteMmaStage)) break;
+    if (!mbar_wait_tries(bar(Cfg::kKF + (t & 1)), (t >> 1) & 1, ctl, kSiteMmaStage)) break;
     // S[t % 3] was last read by PV(t - 3).
-    if (t >= 3 && !mbar_wait_inl(bar(Cfg::kPVD + t % 3), ((t - 3) / 3) & 1, ctl, kSiteMmaPvDone)) break;
+    if (t >= 3 && !mbar_wait_tries(bar(Cfg::kPVD + t % 3), ((t - 3) / 3) & 1, ctl, kSiteMmaPvDone)) break;
     tc_fence_after();
     const uint32_t s = tmem + (t % 3) * 128;
-    const uint32_t q = md.q0 + (item & 1) * (Cfg::kTileB >> 4);
+    const uint32_t q = md.q0;
     const uint32_t k = md.k0 + (t & 1) * (Cfg::kTileB >> 4);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
@@ -203,20 +334,20 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, const W
 }
 
 template <int D>
-__device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, const WaitCtl& ctl) {
+__device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volatile int* ctl) {
   using Cfg = TileCfg<D>;
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const TileDescs<D> md(sbase);
   for (int t = 0;; ++t) {
     const int slot = t % Cfg::kInfo;
-    if (!mbar_wait_inl(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
+    if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
     const int flags = reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB)->flags;
     mbar_arrive(bar(Cfg::kIE + slot));
     if (flags & kStageEnd) break;
     // P(t) written (at an item's first step: the previous item's O read out before that).
-    if (!mbar_wait_inl(bar(Cfg::kPF + t % 3), (t / 3) & 1, ctl, kSiteMmaPFull)) break;
-    if (!mbar_wait_inl(bar(Cfg::kVF + (t & 1)), (t >> 1) & 1, ctl, kSiteMmaStage)) break;
+    if (!mbar_wait_tries(bar(Cfg::kPF + t % 3), (t / 3) & 1, ctl, kSiteMmaPFull)) break;
+    if (!mbar_wait_tries(bar(Cfg::kVF + (t & 1)), (t >> 1) & 1, ctl, kSiteMmaStage)) break;
     tc_fence_after();
     const uint32_t ps = tmem + (t % 3) * 128;
     const uint32_t v = md.v0 + (t & 1) * (Cfg::kTileB >> 4);
@@ -231,91 +362,51 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, const 
   mbar_drain_wait(bar(Cfg::kDrain + 1), 0);
 }
 
-// --------------------------------------------------------------------- converter
+// -------------------------------------------------------------------- converters
 
-// 16 bytes, or zeros: a predicated load (as a branch, each of a thread's loads would wait
-// for the address of the one before).
-__device__ __forceinline__ uint4 load16_if(const void* ptr, bool on) {
-  uint4 x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
-      : "l"(ptr), "r"(static_cast<int>(on)));
-  return x;
-}
-
+// One side (V: values, else keys and the queries); 128 threads.  One piece of code for both.
 template <class A, class C, int D>
-__device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const WaitCtl& ctl) {
+__device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const bool V,
+                                             volatile int* ctl) {
   using Cfg = TileCfg<D>;
   constexpr int RPP = 128 * 16 / D;   // rows of a pass of the 128 threads, 16 numbers each
-  constexpr int NP = 128 / RPP;       // passes of a tile
+  constexpr int NP = 64 / RPP;        // passes of a piece of 64 keys
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
-  // Row of a pass and 16-number piece of it.  Eight neighbouring lanes have four pieces each of
-  // an even and an odd row, which the swizzle puts on different banks.
-  const int piece = (lane & 3) | (D == 128 ? (lane >> 1) & 4 : 0);
-  const int r0 = warp * (RPP / 4) + (D == 128 ? ((lane >> 2) & 1) | ((lane >> 3) & 2) : lane >> 2);
-  auto info = [&](int t) -> const TileStep& {
-    return *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + (t % Cfg::kInfo) * Cfg::kInfoB);
-  };
+  // Row of a pass and 16-number piece of it.  d = 128: eight neighbouring lanes read the left
+  // half of one row and the right half of the next, and write four 16-byte pieces of an even
+  // and four of an odd row, which the swizzle puts on different banks.
+  const int piece = D == 128 ? lane & 7 : lane & 3;
+  const int r0 = warp * (RPP / 4) +
+                 (D == 128 ? (((lane >> 2) ^ (lane >> 3)) & 1) | ((lane >> 3) & 2) : lane >> 2);
   auto wait_warp = [&](int b, int parity, int site) {
-    return __all_sync(0xffffffffu, mbar_wait_inl(bar(b), parity, ctl, site)) != 0;
+    return __all_sync(0xffffffffu, mbar_wait_tries(bar(b), parity, ctl, site)) != 0;
   };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
   };
-  uint4 kr[NP], vr[NP];
-  // A step's stored numbers of one side into registers; what no query of the tile sees is
-  // zero (the cache may hold anything there).
-  const int64_t mine = (r0 & 15) * D + piece * 16;
-  auto load = [&](const TileStep& st, const uint8_t* cache, uint4 (&x)[NP]) {
-    // Rows of the two pieces of the step that some query of the tile sees.
-    const int last = st.seg.pos0 + st.seg.nq - 1, lo = st.seg.lo_key;
-    const int lo0 = lo - st.key0[0], hi0 = last - st.key0[0], lo1 = lo - st.key0[1], hi1 = last - st.key0[1];
-    int64_t off[NP];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) off[i] = st.off[(i * RPP + r0) >> 4];
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int r = (i * RPP + r0) & 63;
-      const bool seen = i < NP / 2 ? r >= lo0 && r <= hi0 : r >= lo1 && r <= hi1;
-      x[i] = load16_if(cache + mine + off[i], off[i] >= 0 && seen);
-    }
-  };
-  // 16 stored numbers to fp16, two 16-byte pieces of a swizzled row.
-  uint8_t* const dst0 = smem + (piece >> 2) * Cfg::kHalfB + r0 * 128 + (((2 * (piece & 3)) ^ (r0 & 7)) << 4);
-  uint8_t* const dst1 = smem + (piece >> 2) * Cfg::kHalfB + r0 * 128 + (((2 * (piece & 3) + 1) ^ (r0 & 7)) << 4);
-  auto store = [&](int tile, const uint4 (&x)[NP]) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      uint32_t h[8];
-      stored4_to_half2<C>(x[i].x, h[0], h[1]);
-      stored4_to_half2<C>(x[i].y, h[2], h[3]);
-      stored4_to_half2<C>(x[i].z, h[4], h[5]);
-      stored4_to_half2<C>(x[i].w, h[6], h[7]);
-      *reinterpret_cast<uint4*>(dst0 + tile + i * RPP * 128) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(dst1 + tile + i * RPP * 128) = make_uint4(h[4], h[5], h[6], h[7]);
-    }
-  };
+  const int src0 = r0 * D + piece * 16;
+  const int row0 = (piece >> 2) * Cfg::kHalfB + r0 * 128;
+  const int dst0 = row0 + (((2 * (piece & 3)) ^ (r0 & 7)) << 4);
+  const int dst1 = row0 + (((2 * (piece & 3) + 1) ^ (r0 & 7)) << 4);
 
-  // Iteration t stores K(t) and V(t - 1), then requests K(t + 1) and V(t).
   int item = -1;
-  for (int t = -1;; ++t) {
-    const int flags = t < 0 ? 0 : info(t).flags;
-    const bool end = flags & kStageEnd;
-    if (t >= 0 && !end) {
-      // S(t - 2) read the K tile that this step overwrites, and the Q tile of the item before
-      // the last one (whose last step it is at the latest).
-      if (t >= 2 && !wait_warp(Cfg::kSF + (t - 2) % 3, ((t - 2) / 3) & 1, kSiteProdKEmpty)) break;
-      if (flags & kStageFirst) {
+  for (int t = 0;; ++t) {
+    const int slot = t % Cfg::kInfo;
+    if (!wait_warp(Cfg::kIF + slot, (t / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
+    const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    const int flags = st.flags;
+    if (flags & kStageEnd) break;
+    // S(t - 2) read the K tile that this step overwrites, PV(t - 2) the V tile; at an item's
+    // first step, S(t - 1) was the last to read the previous item's Q.
+    const int j = !V && (flags & kStageFirst) ? t - 1 : t - 2;
+    if (j >= 0 && !wait_warp((V ? Cfg::kPVD : Cfg::kSF) + j % 3, (j / 3) & 1, kSiteProdKEmpty)) break;
+    if (!V && (flags & kStageFirst)) {
         ++item;
         // Row tid of the tile: query and head, scaled into fp16's range.
-        const CacheSeg& s = info(t).seg;
+        const CacheSeg& s = st.seg;
         const int qi = static_cast<int>((tid * p.group_inv) >> 16);
         const bool live = qi < s.nq;
         const A* q = static_cast<const A*>(p.q) + (s.q0 + qi) * p.q_token_stride +
@@ -340,7 +431,7 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
           up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
           back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
         }
-        uint8_t* row = smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB + tid * 128;
+        uint8_t* row = smem + Cfg::kOffQ + tid * 128;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           uint4 x = make_uint4(0, 0, 0, 0);
@@ -362,26 +453,47 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         fence_proxy_async_smem();
         arrive(Cfg::kQF + item % Cfg::kItems);
       }
-      store(Cfg::kOffK + (t & 1) * Cfg::kTileB, kr);
+    const int tile = (V ? Cfg::kOffV : Cfg::kOffK) + (t & 1) * Cfg::kTileB;
+    const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
+    bool ok = true;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      const int n = 2 * t + half, places = V ? Cfg::kRawV : Cfg::kRawK, place = n % places;
+      uint8_t* raw = smem + (V ? Cfg::kOffRawV : Cfg::kOffRawK) + place * Cfg::kRawB + src0;
+      const int key0 = st.key0[half], there = st.there[half];
+      if (!(ok = wait_warp((V ? Cfg::kRVF : Cfg::kRKF) + place, (n / places) & 1, kSiteMmaStage))) break;
+      if (there != 15 || key0 < lo || key0 + 63 > last) {
+        // What no query of the tile sees is zero (the cache may hold anything there).
+#pragma unroll 1
+        for (int i = 0; i < NP; ++i) {
+          const int row = i * RPP + r0, key = key0 + row;
+          if (!(there >> (row >> 4) & 1) || key < lo || key > last)
+            *reinterpret_cast<uint4*>(raw + i * RPP * D) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();  // before a copy overwrites the zeros
+      }
+      uint4 x[NP];
+#pragma unroll
+      for (int i = 0; i < NP; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + i * RPP * D);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint32_t h[8];
+        stored4_to_half2<C>(x[i].x, h[0], h[1]);
+        stored4_to_half2<C>(x[i].y, h[2], h[3]);
+        stored4_to_half2<C>(x[i].z, h[4], h[5]);
+        stored4_to_half2<C>(x[i].w, h[6], h[7]);
+        const int at = tile + (half * 64 + i * RPP) * 128;
+        *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+      arrive((V ? Cfg::kRVE : Cfg::kRKE) + place);
     }
-    if (t > 0) {
-      // PV(t - 3) read the V tile that V(t - 1) overwrites.
-      if (t >= 3 && !wait_warp(Cfg::kPVD + (t - 3) % 3, ((t - 3) / 3) & 1, kSiteProdVEmpty)) break;
-      store(Cfg::kOffV + ((t - 1) & 1) * Cfg::kTileB, vr);
-    }
+    if (!ok) break;
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0 && t >= 0) {
-      if (!end) mbar_arrive(bar(Cfg::kKF + (t & 1)));
-      if (t > 0) mbar_arrive(bar(Cfg::kVF + ((t - 1) & 1)));
-    }
-    if (end) break;
-    const int nx = t + 1;
-    if (!wait_warp(Cfg::kIF + nx % Cfg::kInfo, (nx / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
-    if (!(info(nx).flags & kStageEnd)) load(info(nx), p.k_cache, kr);
-    if (t >= 0) {
-      load(info(t), p.v_cache, vr);
-      arrive(Cfg::kIE + t % Cfg::kInfo);
+    if (lane == 0) {
+      mbar_arrive(bar((V ? Cfg::kVF : Cfg::kKF) + (t & 1)));
+      mbar_arrive(bar(Cfg::kIE + slot));
     }
   }
 }
@@ -392,9 +504,8 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
 // multiplier; else they are transformed first.
 template <class A, int D, bool FOLD>
 __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* smem, uint32_t tmem,
-                                             const CacheParts& parts, int* join_flag, const WaitCtl& ctl) {
+                                             const CacheParts& parts, int* join_flag, volatile int* ctl) {
   using Cfg = TileCfg<D>;
-  constexpr int NC = 64;
   constexpr int R = Cfg::kRows;
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
@@ -405,7 +516,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   const uint32_t to = tl + Cfg::kOCol;
   const int qi = static_cast<int>((row * p.group_inv) >> 16);
   auto wait_bar = [&](int b, int parity, int site) -> bool {
-    const bool w = __all_sync(0xffffffffu, mbar_wait_inl(bar(b), parity, ctl, site));
+    const bool w = __all_sync(0xffffffffu, mbar_wait_tries(bar(b), parity, ctl, site));
     if (w) tc_fence_after();
     return w;
   };
@@ -414,7 +525,14 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
   };
-  ConsumerBarrierInl cb{bar(Cfg::kJoin), 0};
+  uint32_t join_phase = 0;
+  auto meet = [&]() -> bool {  // of the softmax warps
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(Cfg::kJoin));
+    const bool ok = mbar_wait_tries(bar(Cfg::kJoin), join_phase, ctl, kSiteCacheJoin);
+    join_phase ^= 1;
+    return __all_sync(0xffffffffu, ok);
+  };
 
   CacheSeg seg{};          // of the item whose O is pending
   float m = -INFINITY, l = 0.f, rf = 1.f;
@@ -440,7 +558,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       f = z == 0.f ? 0.f : f / z;
     }
     const int64_t slot = (2 * static_cast<int64_t>(blockIdx.x) + (seg.starts ? 1 : 0)) * R + row;
-#pragma unroll
+#pragma unroll 1
     for (int c = 0; c < D / 64; ++c) {
       uint32_t r[32];
       tmem_ld_16x32bx2_x32<32>(to + c * 64, r);
@@ -472,23 +590,28 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   // After a cut unit's piece is stored: the CTA that left the last one joins them.
   auto join = [&]() -> bool {
     if (seg.starts && seg.ends) return true;
-    if (!cb.sync(lane, ctl)) return false;
-    if (w8 == 0 && lane == 0) {
-      __threadfence();
-      int* count = parts.count + (blockIdx.x - seg.before);
-      const bool now = atomic_add_acq_rel(count, 1) == seg.before + seg.more;
-      if (now) *count = 0;
-      *join_flag = now;
-    }
-    if (!cb.sync(lane, ctl)) return false;
-    if (*reinterpret_cast<volatile int*>(join_flag)) {
+    // Once for the count, then for what it said, then for the word's next use.
 #pragma unroll 1
-      for (int r = w8; r < seg.nq * p.group; r += 8)
-        join_row<A, D, R>(p, parts, seg, blockIdx.x - seg.before, seg.before + seg.more, r, lane);
+    for (int i = 0; i < 3; ++i) {
+      if (!meet()) return false;
+      if (i == 0 && w8 == 0 && lane == 0) {
+        __threadfence();
+        int* count = parts.count + (blockIdx.x - seg.before);
+        const bool now = atomic_add_acq_rel(count, 1) == seg.before + seg.more;
+        if (now) *count = 0;
+        *join_flag = now;
+      }
+      if (i == 1 && *reinterpret_cast<volatile int*>(join_flag)) {
+#pragma unroll 1
+        for (int r = w8; r < seg.nq * p.group; r += 8)
+          join_row<A, D, R>(p, parts, seg, blockIdx.x - seg.before, seg.before + seg.more, r, lane);
+      }
     }
-    return cb.sync(lane, ctl);
+    return true;
   };
 
+  // A group's factor of the scores; a zero one would turn a masked score into a NaN.
+  auto factor = [&](float ks) { return FOLD ? fmaxf(rf * ks, 1.17549435e-38f) : rf * ks; };
   bool pending = false;
   for (int t = 0;; ++t) {
     const int slot = t % Cfg::kInfo;
@@ -513,65 +636,43 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       l = 0.f;
     }
     if (!wait_bar(Cfg::kSF + t % 3, (t / 3) & 1, kSiteSoftSFull)) break;
-    float x[NC];
+    // Piece by piece, 32 keys a thread (lane t the first of the piece, t + 16 the others), and
+    // twice: the maximum, then the weights.  Scores that have to be changed first (soft-cap,
+    // masks) are written back by the first pass, so that the second is the same for all.
     const uint32_t ts = tl + (t % 3) * 128;
-    {
-      uint32_t a[32], b[32];
-      tmem_ld_16x32bx2_x32<64>(ts, a);
-      tmem_ld_16x32bx2_x32<64>(ts + 32, b);
-      tmem_ld_wait(a);
-      tmem_ld_wait(b);
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        x[i] = __uint_as_float(a[i]);
-        x[32 + i] = __uint_as_float(b[i]);
-      }
-    }
-    const int key0 = st.key0[half];
-    float c[4], a[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      c[i] = rf * st.ks[half * 4 + i];
-      a[i] = st.lv[half * 4 + i];
-    }
-    if constexpr (!FOLD) {
-#pragma unroll
-      for (int i = 0; i < NC; ++i) {
-        x[i] *= c[i >> 4];
-        if (p.softcap_log2 > 0.f) x[i] = softcap(x[i], p.softcap_log2);
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = 1.f;
-    } else {
-      // A zero factor would turn a masked score into a NaN.
-#pragma unroll
-      for (int i = 0; i < 4; ++i) c[i] = fmaxf(c[i], 1.17549435e-38f);
-    }
-    {
-      int lo = 0, hi = min(NC - 1, qpos - key0);
-      if (p.window >= 0) lo = max(lo, qpos - p.window - key0);
-      if (__any_sync(0xffffffffu, lo > 0 || hi < NC - 1)) {
+    float mx = -INFINITY;
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t x[32];
+      tmem_ld_16x32bx2_x32<32>(ts + 64 * h, x);
+      const int g = 4 * h + 2 * half;
+      const float c0 = factor(st.ks[g]), c1 = factor(st.ks[g + 1]);
+      const int k = st.key0[h] + 32 * half;
+      int lo = 0, hi = min(31, qpos - k);
+      if (p.window >= 0) lo = max(lo, qpos - p.window - k);
+      const bool cut = __any_sync(0xffffffffu, lo > 0 || hi < 31);
+      tmem_ld_wait(x);
+      if (!FOLD || cut) {
         // Bit i: score i is seen.
-        uint64_t seen = hi < lo ? 0ull : (~0ull >> (63 - (hi - lo))) << lo;
-        const uint32_t s0 = static_cast<uint32_t>(seen), s1 = static_cast<uint32_t>(seen >> 32);
+        const uint32_t seen = hi < lo ? 0u : (0xffffffffu >> (31 - (hi - lo))) << lo;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          x[i] = (s0 >> i) & 1 ? x[i] : -INFINITY;
-          x[32 + i] = (s1 >> i) & 1 ? x[32 + i] : -INFINITY;
+          float y = __uint_as_float(x[i]);
+          if constexpr (!FOLD) {
+            y *= i < 16 ? c0 : c1;
+            if (p.softcap_log2 > 0.f) y = softcap(y, p.softcap_log2);
+          }
+          x[i] = __float_as_uint((seen >> i) & 1 ? y : -INFINITY);
         }
+        tmem_st_16x32bx2_x32<32>(ts + 64 * h, x);
       }
-    }
-    float mx = -INFINITY;
+      float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      float t0 = fmax3(x[16 * g], x[16 * g + 1], x[16 * g + 2]);
-      float t1 = fmax3(x[16 * g + 3], x[16 * g + 4], x[16 * g + 5]);
-      t0 = fmax3(t0, x[16 * g + 6], x[16 * g + 7]);
-      t1 = fmax3(t1, x[16 * g + 8], x[16 * g + 9]);
-      t0 = fmax3(t0, x[16 * g + 10], x[16 * g + 11]);
-      t1 = fmax3(t1, x[16 * g + 12], x[16 * g + 13]);
-      t0 = fmax3(t0, x[16 * g + 14], x[16 * g + 15]);
-      mx = fmaxf(mx, fmaf(fmaxf(t0, t1), c[g], a[g]));
+      for (int i = 0; i < 16; i += 2) {
+        t0 = fmax3(t0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        t1 = fmax3(t1, __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
+      }
+      mx = fmax3(mx, fmaf(t0, FOLD ? c0 : 1.f, st.lv[g]), fmaf(t1, FOLD ? c1 : 1.f, st.lv[g + 1]));
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     float alpha = 1.f;
@@ -584,32 +685,40 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     const float neg_m = m == -INFINITY ? 0.f : -m;
     float sum = 0.f;
-    {
-      uint32_t pk[32];
+    tmem_st_wait();  // scores written back
+#pragma unroll 1
+    for (int h = 0; h < 2; ++h) {
+      uint32_t x[32], pk[16];
+      tmem_ld_16x32bx2_x32<32>(ts + 64 * h, x);
+      const int g = 4 * h + 2 * half;
+      const float c0 = FOLD ? factor(st.ks[g]) : 1.f, c1 = FOLD ? factor(st.ks[g + 1]) : 1.f;
+      const float a0 = st.lv[g] + neg_m, a1 = st.lv[g + 1] + neg_m;
+      tmem_ld_wait(x);
+      uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const uint64_t c2 = f2_pack(c[g], c[g]), m2 = f2_pack(a[g] + neg_m, a[g] + neg_m);
-        uint64_t s2 = 0ull, s3 = 0ull;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint64_t y = f2_fma(f2_pack(x[16 * g + 2 * i], x[16 * g + 2 * i + 1]), c2, m2);
-          const uint64_t e = f2_pack(ex2_approx(f2_lo(y)), ex2_approx(f2_hi(y)));
-          if (i & 1) s3 = f2_add(s3, e);
-          else s2 = f2_add(s2, e);
-          pk[8 * g + i] = float2_to_act<__half>(f2_lo(e), f2_hi(e));
-        }
-        s2 = f2_add(s2, s3);
-        // w / vs
-        sum = fmaf(f2_lo(s2) + f2_hi(s2), st.rv[half * 4 + g], sum);
+      for (int i = 0; i < 8; ++i) {
+        const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+                                   f2_pack(c0, c0), f2_pack(a0, a0));
+        const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(x[16 + 2 * i]), __uint_as_float(x[17 + 2 * i])),
+                                   f2_pack(c1, c1), f2_pack(a1, a1));
+        const uint64_t e0 = f2_pack(ex2_approx(f2_lo(y0)), ex2_approx(f2_hi(y0)));
+        const uint64_t e1 = f2_pack(ex2_approx(f2_lo(y1)), ex2_approx(f2_hi(y1)));
+        s0 = f2_add(s0, e0);
+        s1 = f2_add(s1, e1);
+        pk[i] = float2_to_act<__half>(f2_lo(e0), f2_hi(e0));
+        pk[8 + i] = float2_to_act<__half>(f2_lo(e1), f2_hi(e1));
       }
-      tmem_st_16x32bx2_x32<32>(ts, pk);
+      // w / vs
+      sum = fmaf(f2_lo(s0) + f2_hi(s0), st.rv[g], fmaf(f2_lo(s1) + f2_hi(s1), st.rv[g + 1], sum));
+      // over scores that both lanes of the row have read
+      tmem_st_16x32bx2_x16<16>(ts + 32 * h, pk);
     }
     sum += __shfl_xor_sync(0xffffffffu, sum, 16);
     l = l * alpha + sum;
     if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
       // PV(t - 1) must be complete before O is rescaled.
       if (!wait_bar(Cfg::kPVD + (t - 1) % 3, ((t - 1) / 3) & 1, kSiteSoftPvDone)) break;
-#pragma unroll
+#pragma unroll 1
       for (int g = 0; g < D / 64; ++g) {
         uint32_t r[32];
         tmem_ld_16x32bx2_x32<32>(to + g * 64, r);
@@ -629,7 +738,10 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
 // ------------------------------------------------------------------------ kernel
 
 template <class A, class C, int D, bool FOLD>
-__global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdParams p, void* workspace) {
+__global__ void __launch_bounds__(640, 1)
+    bsa_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
+                          const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p,
+                          void* workspace) {
   using Cfg = TileCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -637,8 +749,8 @@ __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdPa
   const uint32_t sbase = smem_u32(smem);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + Cfg::kOffCtl);
-  int* err = reinterpret_cast<int*>(tmem_slot + 1);  // status, abort flag, join flag
-  const WaitCtl ctl{err + 1, err, kCacheWaitNs, 0};
+  int* err = reinterpret_cast<int*>(tmem_slot + 1);  // abort word, join flag
+  volatile int* const ctl = err;
   const CacheParts parts = cache_parts(workspace, gridDim.x, Cfg::kRows, D);
   const CacheUnits units{p, 31 - __clz(static_cast<int>((128u * p.group_inv) >> 16)), 6, 2};
   if (threadIdx.x == 0) {
@@ -656,10 +768,20 @@ __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdPa
     for (int i = 0; i < Cfg::kItems; ++i) mbar_init(bar(Cfg::kQF + i), 4);
     for (int i = 0; i < Cfg::kInfo; ++i) {
       mbar_init(bar(Cfg::kIF + i), 1);
-      mbar_init(bar(Cfg::kIE + i), 4 + 8 + 2);  // converter and softmax warps, two issuers
+      mbar_init(bar(Cfg::kIE + i), 8 + 8 + 2 + 1);  // converters, softmax, issuers, copies
+    }
+    for (int i = 0; i < Cfg::kRawK; ++i) {
+      mbar_init(bar(Cfg::kRKF + i), 1);
+      mbar_init(bar(Cfg::kRKE + i), 4);
+    }
+    for (int i = 0; i < Cfg::kRawV; ++i) {
+      mbar_init(bar(Cfg::kRVF + i), 1);
+      mbar_init(bar(Cfg::kRVE + i), 4);
     }
     mbar_init(bar(Cfg::kJoin), 8);
-    err[0] = err[1] = err[2] = 0;
+    tma_prefetch_desc(&tm_k);
+    tma_prefetch_desc(&tm_v);
+    err[0] = err[1] = 0;
     fence_mbar_init();
     if (blockIdx.x == 0) *p.status = 0;
   }
@@ -675,20 +797,19 @@ __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdPa
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
-    setmaxnreg_dec<Cfg::kRegCtl>();
     if (warp == 0) {
       if (lane == 0) tile_mma_s<D>(smem, tmem, ctl);
     } else if (warp == 1) {
       if (lane == 0) tile_mma_pv<D>(smem, tmem, ctl);
     } else if (warp == 2) {
-      tile_producer<D>(p, smem, units, ctl);
+      tile_lookup<D>(p, smem, units, ctl);
+    } else {
+      tile_copy<D>(p, &tm_k, &tm_v, smem, ctl);
     }
   } else if (warp < 12) {
-    setmaxnreg_inc<Cfg::kRegSoft>();
-    tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 2, ctl);
+    tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 1, ctl);
   } else {
-    setmaxnreg_dec<Cfg::kRegConv>();
-    tile_convert<A, C, D>(p, smem, ctl);
+    tile_convert<A, C, D>(p, smem, warp >= 16, ctl);
   }
   tc_fence_before();
   __syncthreads();
@@ -702,30 +823,23 @@ __global__ void __launch_bounds__(512, 1) bsa_cache_tile_kernel(const CacheFwdPa
 }
 
 template <class A, class C, int D, bool FOLD>
-cudaError_t launch_tile_as(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
+cudaError_t launch_tile_as(const CUtensorMap& k, const CUtensorMap& v, const CacheFwdParams& p, void* workspace, int sms,
+                           cudaStream_t stream) {
   using Cfg = TileCfg<D>;
   auto* kernel = bsa_cache_tile_kernel<A, C, D, FOLD>;
-  static int done[64], regs = 0;
-  cudaError_t e = set_smem_once(kernel, Cfg::kLaunchSmem, done);
+  static int done[64];
+  const cudaError_t e = set_smem_once(kernel, Cfg::kLaunchSmem, done);
   if (e != cudaSuccess) return e;
-  if (regs == 0) {
-    // setmaxnreg.inc waits for registers that the other warpgroups gave back: the shares
-    // only add up when the kernel is launched at exactly kLaunchRegs.
-    cudaFuncAttributes fa{};
-    e = cudaFuncGetAttributes(&fa, kernel);
-    if (e != cudaSuccess) return e;
-    regs = fa.numRegs;
-  }
-  if (regs != Cfg::kLaunchRegs) return cudaErrorInvalidConfiguration;
-  kernel<<<sms, Cfg::kThreads, Cfg::kLaunchSmem, stream>>>(p, workspace);
+  kernel<<<sms, Cfg::kThreads, Cfg::kLaunchSmem, stream>>>(k, v, p, workspace);
   return cudaGetLastError();
 }
 
 template <class A, class C, int D>
-cudaError_t launch_tile(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
+cudaError_t launch_tile(const CUtensorMap& k, const CUtensorMap& v, const CacheFwdParams& p,
+                        void* workspace, int sms, cudaStream_t stream) {
   return p.softcap_log2 == 0.f && p.scale_log2 > 0.f
-             ? launch_tile_as<A, C, D, true>(p, workspace, sms, stream)
-             : launch_tile_as<A, C, D, false>(p, workspace, sms, stream);
+             ? launch_tile_as<A, C, D, true>(k, v, p, workspace, sms, stream)
+             : launch_tile_as<A, C, D, false>(k, v, p, workspace, sms, stream);
 }
 
 }  // namespace bsa

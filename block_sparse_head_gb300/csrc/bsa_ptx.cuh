@@ -134,6 +134,30 @@ __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, con
   return mbar_wait_timed(bar, parity, ctl, site);
 }
 
+// A bounded wait in a dozen instructions, for kernels whose roles together have to fit the
+// instruction cache.  The bound is a count of tries: each suspends the thread for as long as
+// the hardware likes (up to the microsecond asked for), so 2^24 of them take between half a
+// second and about twenty.  A wait that runs out leaves kStatusTimeout | site in the CTA's
+// abort word; every other wait of the CTA then ends too.
+__device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity,
+                                                volatile int* abort_word, int site) {
+#pragma unroll 1
+  for (int i = 0; i < (1 << 24); ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, 1000;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (*abort_word != 0) return false;
+  }
+  *abort_word = kStatusTimeout | site;
+  return false;
+}
+
 // Bounded wait that ignores the abort flag and never records a status: used only
 // to drain work already in flight before the CTA releases its resources.  Its limit
 // is fixed and independent of the (possibly tiny) per-wait limit of the main loop.
@@ -325,6 +349,12 @@ template <int OFF>
 __device__ __forceinline__ void tmem_st_16x32bx2_x32(uint32_t taddr, const uint32_t (&r)[32]) {
   asm volatile("tcgen05.st.sync.aligned.16x32bx2.x32.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32,%33};"
                :: "r"(taddr), "n"(OFF), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31]) : "memory");
+}
+
+template <int OFF>
+__device__ __forceinline__ void tmem_st_16x32bx2_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile("tcgen05.st.sync.aligned.16x32bx2.x16.b32 [%0], %1, {%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17};"
+               :: "r"(taddr), "n"(OFF), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]) : "memory");
 }
 
 // Each thread reads 32 consecutive columns of its own TMEM lane (32x32b shape).
