@@ -63,6 +63,7 @@ struct TileCfg {
   static constexpr int kQF = 13;                // [kItems] Q of an item converted
   static constexpr int kIF = kQF + kItems;      // [kInfo] step looked up
   static constexpr int kIE = kIF + kInfo;       // [kInfo] step no longer needed
+  static_assert(kIE == kIF + kInfo, "RingBar users add 8 * kInfo");
   static constexpr int kRKF = kIE + kInfo;      // [kRawK] 64 keys landed
   static constexpr int kRKE = kRKF + kRawK;     // [kRawK] and converted (4 warps)
   static constexpr int kRVF = kRKE + kRawK;     // [kRawV]
@@ -95,6 +96,25 @@ struct TileStep {
   float rv[8];    // its reciprocal (0 where the keys are not there)
 };
 static_assert(sizeof(TileStep) <= 208, "step slots");
+
+// A barrier of a ring of N: its address and the parity of the phase to wait for (or to fill)
+// next.
+template <int N>
+struct RingBar {
+  uint32_t bar, first, parity;
+  __device__ __forceinline__ explicit RingBar(uint32_t b) : bar(b), first(b), parity(0) {}
+  __device__ __forceinline__ void advance() {
+    bar += 8;
+    if (bar == first + 8 * N) {
+      bar = first;
+      parity ^= 1;
+    }
+  }
+  __device__ __forceinline__ int index() const { return static_cast<int>(bar - first) >> 3; }
+  __device__ __forceinline__ bool wait(volatile int* ctl, int site) const {
+    return mbar_wait_tries(bar, parity, ctl, site);
+  }
+};
 
 // ---------------------------------------------------------------------- look-ups
 
@@ -303,31 +323,37 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const TileDescs<D> md(sbase);
-  int item = -1;
+  RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
+  RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
+  RingBar<2> keys(bar(Cfg::kKF));
+  RingBar<3> done(bar(Cfg::kPVD));
+  uint32_t s = 0, k = 0;  // columns of the S buffer, offset of the K tile
   for (int t = 0;; ++t) {
-    const int slot = t % Cfg::kInfo;
-    if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
-    const int flags = reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB)->flags;
-    mbar_arrive(bar(Cfg::kIE + slot));
+    if (!info.wait(ctl, kSiteCacheInfo)) break;
+    const int flags =
+        reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB)->flags;
+    mbar_arrive(info.bar + 8 * Cfg::kInfo);  // its kIE
+    info.advance();
     if (flags & kStageEnd) break;
     if (flags & kStageFirst) {
-      ++item;
-      if (!mbar_wait_tries(bar(Cfg::kQF + item % Cfg::kItems), (item / Cfg::kItems) & 1, ctl, kSiteMmaStage))
-        break;
+      if (!queries.wait(ctl, kSiteMmaStage)) break;
+      queries.advance();
     }
-    if (!mbar_wait_tries(bar(Cfg::kKF + (t & 1)), (t >> 1) & 1, ctl, kSiteMmaStage)) break;
-    // S[t % 3] was last read by PV(t - 3).
-    if (t >= 3 && !mbar_wait_tries(bar(Cfg::kPVD + t % 3), ((t - 3) / 3) & 1, ctl, kSiteMmaPvDone)) break;
+    if (!keys.wait(ctl, kSiteMmaStage)) break;
+    keys.advance();
+    if (t >= 3) {  // S[t % 3] was last read by PV(t - 3)
+      if (!done.wait(ctl, kSiteMmaPvDone)) break;
+      done.advance();
+    }
     tc_fence_after();
-    const uint32_t s = tmem + (t % 3) * 128;
-    const uint32_t q = md.q0;
-    const uint32_t k = md.k0 + (t & 1) * (Cfg::kTileB >> 4);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t off = ((kk >> 2) * Cfg::kHalfB + (kk & 3) * 32) >> 4;
-      tc_mma_ss_lh(s, q + off, md.hi, k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
+      tc_mma_ss_lh(tmem + s, md.q0 + off, md.hi, md.k0 + k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
     }
-    tc_commit(bar(Cfg::kSF + t % 3));
+    tc_commit(bar(Cfg::kSF) + s / 16);
+    s = s == 256 ? 0 : s + 128;
+    k ^= Cfg::kTileB >> 4;
   }
   tc_commit(bar(Cfg::kDrain));
   mbar_drain_wait(bar(Cfg::kDrain), 0);
@@ -339,24 +365,31 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const TileDescs<D> md(sbase);
-  for (int t = 0;; ++t) {
-    const int slot = t % Cfg::kInfo;
-    if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
-    const int flags = reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB)->flags;
-    mbar_arrive(bar(Cfg::kIE + slot));
+  RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
+  RingBar<3> weights(bar(Cfg::kPF));
+  RingBar<2> values(bar(Cfg::kVF));
+  uint32_t ps = 0, v = 0;  // columns of the S buffer, offset of the V tile
+  for (;;) {
+    if (!info.wait(ctl, kSiteCacheInfo)) break;
+    const int flags =
+        reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB)->flags;
+    mbar_arrive(info.bar + 8 * Cfg::kInfo);
+    info.advance();
     if (flags & kStageEnd) break;
-    // P(t) written (at an item's first step: the previous item's O read out before that).
-    if (!mbar_wait_tries(bar(Cfg::kPF + t % 3), (t / 3) & 1, ctl, kSiteMmaPFull)) break;
-    if (!mbar_wait_tries(bar(Cfg::kVF + (t & 1)), (t >> 1) & 1, ctl, kSiteMmaStage)) break;
+    // V(t) converted, P(t) written (at an item's first step: the previous item's O read out
+    // before that).
+    if (!values.wait(ctl, kSiteMmaStage) || !weights.wait(ctl, kSiteMmaPFull)) break;
+    values.advance();
+    weights.advance();
     tc_fence_after();
-    const uint32_t ps = tmem + (t % 3) * 128;
-    const uint32_t v = md.v0 + (t & 1) * (Cfg::kTileB >> 4);
     const bool first = flags & kStageFirst;
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)  // 16 keys each
-      tc_mma_ts_lh(tmem + Cfg::kOCol, ps + kk * 8, v + ((kk * 16 * 128) >> 4), md.hi, Cfg::kIdescPV,
-                   kk == 0 && first ? 0u : 1u);
-    tc_commit(bar(Cfg::kPVD + t % 3));
+      tc_mma_ts_lh(tmem + Cfg::kOCol, tmem + ps + kk * 8, md.v0 + v + ((kk * 16 * 128) >> 4), md.hi,
+                   Cfg::kIdescPV, kk == 0 && first ? 0u : 1u);
+    tc_commit(bar(Cfg::kPVD) + ps / 16);
+    ps = ps == 256 ? 0 : ps + 128;
+    v ^= Cfg::kTileB >> 4;
   }
   tc_commit(bar(Cfg::kDrain + 1));
   mbar_drain_wait(bar(Cfg::kDrain + 1), 0);
@@ -380,9 +413,6 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   const int piece = D == 128 ? lane & 7 : lane & 3;
   const int r0 = warp * (RPP / 4) +
                  (D == 128 ? (((lane >> 2) ^ (lane >> 3)) & 1) | ((lane >> 3) & 2) : lane >> 2);
-  auto wait_warp = [&](int b, int parity, int site) {
-    return __all_sync(0xffffffffu, mbar_wait_tries(bar(b), parity, ctl, site)) != 0;
-  };
   auto arrive = [&](int b) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar(b));
@@ -392,17 +422,33 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   const int dst0 = row0 + (((2 * (piece & 3)) ^ (r0 & 7)) << 4);
   const int dst1 = row0 + (((2 * (piece & 3) + 1) ^ (r0 & 7)) << 4);
 
+  // Rings: look-ups, places of stored numbers (counted up to this side's number of them), and
+  // what last read the tile that a step overwrites: S(t - 2) for K, PV(t - 2) for V, and S(t - 1)
+  // for an item's queries.
+  RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
+  RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF)), free1(bar(Cfg::kSF));
+  const uint32_t raw_first = bar(V ? Cfg::kRVF : Cfg::kRKF), places = V ? Cfg::kRawV : Cfg::kRawK;
+  const int raw_base = (V ? Cfg::kOffRawV : Cfg::kOffRawK) + src0;
+  uint32_t place = 0, raw_parity = 0;
+  int tile = V ? Cfg::kOffV : Cfg::kOffK;
+  auto wait_ring = [&](const auto& ring, int site) {
+    return __all_sync(0xffffffffu, ring.wait(ctl, site)) != 0;
+  };
   int item = -1;
   for (int t = 0;; ++t) {
-    const int slot = t % Cfg::kInfo;
-    if (!wait_warp(Cfg::kIF + slot, (t / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
-    const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    if (!wait_ring(info, kSiteCacheInfo)) break;
+    const TileStep& st =
+        *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
     const int flags = st.flags;
     if (flags & kStageEnd) break;
-    // S(t - 2) read the K tile that this step overwrites, PV(t - 2) the V tile; at an item's
-    // first step, S(t - 1) was the last to read the previous item's Q.
-    const int j = !V && (flags & kStageFirst) ? t - 1 : t - 2;
-    if (j >= 0 && !wait_warp((V ? Cfg::kPVD : Cfg::kSF) + j % 3, (j / 3) & 1, kSiteProdKEmpty)) break;
+    if (t >= 2) {
+      if (!wait_ring(free2, V ? kSiteProdVEmpty : kSiteProdKEmpty)) break;
+      free2.advance();
+    }
+    if (!V && t >= 1) {
+      if ((flags & kStageFirst) && !wait_ring(free1, kSiteProdKEmpty)) break;
+      free1.advance();
+    }
     if (!V && (flags & kStageFirst)) {
         ++item;
         // Row tid of the tile: query and head, scaled into fp16's range.
@@ -453,15 +499,14 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         fence_proxy_async_smem();
         arrive(Cfg::kQF + item % Cfg::kItems);
       }
-    const int tile = (V ? Cfg::kOffV : Cfg::kOffK) + (t & 1) * Cfg::kTileB;
     const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
     bool ok = true;
 #pragma unroll 1
     for (int half = 0; half < 2; ++half) {
-      const int n = 2 * t + half, places = V ? Cfg::kRawV : Cfg::kRawK, place = n % places;
-      uint8_t* raw = smem + (V ? Cfg::kOffRawV : Cfg::kOffRawK) + place * Cfg::kRawB + src0;
+      uint8_t* raw = smem + raw_base + place * Cfg::kRawB;
+      const uint32_t full = raw_first + 8 * place;
       const int key0 = st.key0[half], there = st.there[half];
-      if (!(ok = wait_warp((V ? Cfg::kRVF : Cfg::kRKF) + place, (n / places) & 1, kSiteMmaStage))) break;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait_tries(full, raw_parity, ctl, kSiteMmaStage)))) break;
       if (there != 15 || key0 < lo || key0 + 63 > last) {
         // What no query of the tile sees is zero (the cache may hold anything there).
 #pragma unroll 1
@@ -486,15 +531,22 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
       }
-      arrive((V ? Cfg::kRVE : Cfg::kRKE) + place);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(full + 8 * places);
+      if (++place == places) {
+        place = 0;
+        raw_parity ^= 1;
+      }
     }
     if (!ok) break;
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      mbar_arrive(bar((V ? Cfg::kVF : Cfg::kKF) + (t & 1)));
-      mbar_arrive(bar(Cfg::kIE + slot));
+      mbar_arrive(bar(V ? Cfg::kVF : Cfg::kKF) + 8 * (t & 1));
+      mbar_arrive(info.bar + 8 * Cfg::kInfo);
     }
+    info.advance();
+    tile += t & 1 ? -Cfg::kTileB : Cfg::kTileB;
   }
 }
 
@@ -515,15 +567,10 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32 + wg * 16) << 16);
   const uint32_t to = tl + Cfg::kOCol;
   const int qi = static_cast<int>((row * p.group_inv) >> 16);
-  auto wait_bar = [&](int b, int parity, int site) -> bool {
-    const bool w = __all_sync(0xffffffffu, mbar_wait_tries(bar(b), parity, ctl, site));
+  auto wait_ring = [&](const auto& ring, int site) -> bool {
+    const bool w = __all_sync(0xffffffffu, ring.wait(ctl, site));
     if (w) tc_fence_after();
     return w;
-  };
-  auto warp_arrive = [&](int b) {
-    tc_fence_before();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(b));
   };
   uint32_t join_phase = 0;
   auto meet = [&]() -> bool {  // of the softmax warps
@@ -536,13 +583,12 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
 
   CacheSeg seg{};          // of the item whose O is pending
   float m = -INFINITY, l = 0.f, rf = 1.f;
-  int qpos = -1, item = -1;
+  int qpos = -1;
   bool live = false;
 
   // The finished item's rows: its O (this thread's columns 64 c + 32 half + ..) scaled and
   // stored, or left as a piece of a cut unit.
-  auto finish = [&](int last_step) -> bool {
-    if (!wait_bar(Cfg::kPVD + last_step % 3, (last_step / 3) & 1, kSiteSoftItemDone)) return false;
+  auto finish = [&]() -> bool {
     const bool whole = seg.starts && seg.ends;
     const int head = seg.h * p.group + row - qi * p.group;
     const int64_t orow = static_cast<int64_t>(seg.q0 + qi) * p.Hq + head;
@@ -613,33 +659,37 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   // A group's factor of the scores; a zero one would turn a masked score into a NaN.
   auto factor = [&](float ks) { return FOLD ? fmaxf(rf * ks, 1.17549435e-38f) : rf * ks; };
   bool pending = false;
+  RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
+  RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
+  RingBar<3> scores(bar(Cfg::kSF)), before(bar(Cfg::kPVD));  // S(t), PV(t - 1)
+  uint32_t ts = tl;  // the step's S buffer
   for (int t = 0;; ++t) {
-    const int slot = t % Cfg::kInfo;
-    if (!wait_bar(Cfg::kIF + slot, (t / Cfg::kInfo) & 1, kSiteCacheInfo)) break;
-    const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    if (!wait_ring(info, kSiteCacheInfo)) break;
+    const TileStep& st =
+        *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
     const int flags = st.flags;
     const bool first = flags & kStageFirst;
     if (flags & (kStageFirst | kStageEnd)) {
       // The previous item's O goes out before this step's P is handed over (the product that
       // reads it overwrites O).
-      if (pending && !(finish(t - 1) && join())) break;
+      if (pending && !(wait_ring(before, kSiteSoftItemDone) && finish() && join())) break;
       if (flags & kStageEnd) break;
       pending = true;
-      ++item;
-      if (!wait_bar(Cfg::kQF + item % Cfg::kItems, (item / Cfg::kItems) & 1, kSiteSoftSFull)) break;
+      if (!wait_ring(queries, kSiteSoftSFull)) break;
       seg = st.seg;
       live = qi < seg.nq;
       qpos = live ? seg.pos0 + qi : -1;
-      rf = reinterpret_cast<const float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + row] *
+      rf = reinterpret_cast<const float*>(smem + Cfg::kOffFactor)[queries.index() * 128 + row] *
            (FOLD || p.softcap_log2 == 0.f ? p.scale_log2 : p.softcap_inv);
+      queries.advance();
       m = -INFINITY;
       l = 0.f;
     }
-    if (!wait_bar(Cfg::kSF + t % 3, (t / 3) & 1, kSiteSoftSFull)) break;
+    if (!wait_ring(scores, kSiteSoftSFull)) break;
+    scores.advance();
     // Piece by piece, 32 keys a thread (lane t the first of the piece, t + 16 the others), and
     // twice: the maximum, then the weights.  Scores that have to be changed first (soft-cap,
     // masks) are written back by the first pass, so that the second is the same for all.
-    const uint32_t ts = tl + (t % 3) * 128;
     float mx = -INFINITY;
 #pragma unroll 1
     for (int h = 0; h < 2; ++h) {
@@ -717,7 +767,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     l = l * alpha + sum;
     if (!first && __any_sync(0xffffffffu, alpha != 1.f)) {
       // PV(t - 1) must be complete before O is rescaled.
-      if (!wait_bar(Cfg::kPVD + (t - 1) % 3, ((t - 1) / 3) & 1, kSiteSoftPvDone)) break;
+      if (!wait_ring(before, kSiteSoftPvDone)) break;
 #pragma unroll 1
       for (int g = 0; g < D / 64; ++g) {
         uint32_t r[32];
@@ -729,9 +779,16 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       }
     }
     tmem_st_wait();
-    warp_arrive(Cfg::kPF + t % 3);
+    // P(t) handed over, the step's look-ups no longer needed.
+    tc_fence_before();
     __syncwarp();
-    if (lane == 0) mbar_arrive(bar(Cfg::kIE + slot));
+    if (lane == 0) {
+      mbar_arrive(bar(Cfg::kPF) + ((ts - tl) >> 4));
+      mbar_arrive(info.bar + 8 * Cfg::kInfo);
+    }
+    info.advance();
+    if (t > 0) before.advance();
+    ts = ts == tl + 256 ? tl : ts + 128;
   }
 }
 
