@@ -246,9 +246,9 @@ __device__ __forceinline__ void tile_copy(const CacheFwdParams& p, const CUtenso
     int tile, row;
     uint32_t pieces;  // boxes of the first and (<< 8) of the second piece
   };
-  auto place_of = [&](const TileStep& st) {
+  auto place_of = [&](const TileStep& st, bool end) {
     Place x;
-    const int there = st.there[0] | st.there[1] << 4;
+    const int there = end ? 0 : st.there[0] | st.there[1] << 4;
     const int mine = there >> base & ((1 << groups) - 1);
     x.load = lane < 8 && mine != 0 && lane == base + __ffs(mine) - 1;
     x.tile = st.tile[lane & 7];
@@ -284,16 +284,18 @@ __device__ __forceinline__ void tile_copy(const CacheFwdParams& p, const CUtenso
     if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
     const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
     const bool end = st.flags & kStageEnd;
-    Place k{};
-    if (!end) {
-      k = place_of(st);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(Cfg::kIE + slot));
-      if (!copy(tm_k, k, Cfg::kRKF, Cfg::kOffRawK, Cfg::kRawK, kSiteProdKEmpty, pieces_k)) break;
-    }
+    // (The end goes through the rings too, without bytes: the converters learn of a step by its
+    // pieces.)
+    const Place k = place_of(st, end);
+    __syncwarp();
+    if (lane == 0 && !end) mbar_arrive(bar(Cfg::kIE + slot));
+    if (!copy(tm_k, k, Cfg::kRKF, Cfg::kOffRawK, Cfg::kRawK, kSiteProdKEmpty, pieces_k)) break;
     if (t > 0 && !copy(tm_v, v, Cfg::kRVF, Cfg::kOffRawV, Cfg::kRawV, kSiteProdVEmpty, pieces_v)) break;
-    if (end) break;
     v = k;
+    if (end) {
+      copy(tm_v, v, Cfg::kRVF, Cfg::kOffRawV, Cfg::kRawV, kSiteProdVEmpty, pieces_v);
+      break;
+    }
   }
   // Every copy lands before the CTA leaves (also when the converters have given up).
   for (int n = max(0, pieces_k - Cfg::kRawK); n < pieces_k; ++n)
@@ -422,9 +424,9 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   const int dst0 = row0 + (((2 * (piece & 3)) ^ (r0 & 7)) << 4);
   const int dst1 = row0 + (((2 * (piece & 3) + 1) ^ (r0 & 7)) << 4);
 
-  // Rings: look-ups, places of stored numbers (counted up to this side's number of them), and
-  // what last read the tile that a step overwrites: S(t - 2) for K, PV(t - 2) for V, and S(t - 1)
-  // for an item's queries.
+  // Rings: places of stored numbers (counted up to this side's number of them; a step's pieces
+  // landed, its look-ups are there too), and what last read the tile that a step overwrites:
+  // S(t - 2) for K, PV(t - 2) for V, and S(t - 1) for an item's queries.
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF)), free1(bar(Cfg::kSF));
   const uint32_t raw_first = bar(V ? Cfg::kRVF : Cfg::kRKF), places = V ? Cfg::kRawV : Cfg::kRawK;
@@ -436,15 +438,17 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   };
   int item = -1;
   for (int t = 0;; ++t) {
-    if (!wait_ring(info, kSiteCacheInfo)) break;
+    const uint32_t place1 = place + 1 == places ? 0 : place + 1;
+    const uint32_t parity1 = place1 == 0 ? raw_parity ^ 1 : raw_parity;
+    bool ok = mbar_wait_tries(raw_first + 8 * place, raw_parity, ctl, kSiteMmaStage);
     const TileStep& st =
         *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
-    const int flags = st.flags;
-    if (flags & kStageEnd) break;
-    if (t >= 2) {
-      if (!wait_ring(free2, V ? kSiteProdVEmpty : kSiteProdKEmpty)) break;
-      free2.advance();
-    }
+    const int flags = ok ? st.flags : kStageEnd;
+    if (!(flags & kStageEnd))
+      ok = mbar_wait_tries(raw_first + 8 * place1, parity1, ctl, kSiteMmaStage) &&
+           (t < 2 || free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty));
+    if (!__all_sync(0xffffffffu, ok) || (flags & kStageEnd)) break;
+    if (t >= 2) free2.advance();
     if (!V && t >= 1) {
       if ((flags & kStageFirst) && !wait_ring(free1, kSiteProdKEmpty)) break;
       free1.advance();
@@ -500,52 +504,45 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         arrive(Cfg::kQF + item % Cfg::kItems);
       }
     const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
-    bool ok = true;
+    uint8_t* const raw0 = smem + raw_base + place * Cfg::kRawB;
+    uint8_t* const raw1 = smem + raw_base + place1 * Cfg::kRawB;
+    const int k0 = st.key0[0], k1 = st.key0[1], there = st.there[0] | st.there[1] << 4;
+    if (there != 255 || min(k0, k1) < lo || max(k0, k1) + 63 > last) {
+      // What no query of the tile sees is zero (the cache may hold anything there).
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half) {
-      uint8_t* raw = smem + raw_base + place * Cfg::kRawB;
-      const uint32_t full = raw_first + 8 * place;
-      const int key0 = st.key0[half], there = st.there[half];
-      if (!(ok = __all_sync(0xffffffffu, mbar_wait_tries(full, raw_parity, ctl, kSiteMmaStage)))) break;
-      if (there != 15 || key0 < lo || key0 + 63 > last) {
-        // What no query of the tile sees is zero (the cache may hold anything there).
-#pragma unroll 1
-        for (int i = 0; i < NP; ++i) {
-          const int row = i * RPP + r0, key = key0 + row;
-          if (!(there >> (row >> 4) & 1) || key < lo || key > last)
-            *reinterpret_cast<uint4*>(raw + i * RPP * D) = make_uint4(0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();  // before a copy overwrites the zeros
+      for (int i = 0; i < 2 * NP; ++i) {
+        const int row = i * RPP + r0, key = (i < NP ? k0 : k1) + (row & 63);
+        if (!(there >> (row >> 4) & 1) || key < lo || key > last)
+          *reinterpret_cast<uint4*>((i < NP ? raw0 : raw1) + (i % NP) * RPP * D) = make_uint4(0, 0, 0, 0);
       }
-      uint4 x[NP];
-#pragma unroll
-      for (int i = 0; i < NP; ++i) x[i] = *reinterpret_cast<const uint4*>(raw + i * RPP * D);
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        uint32_t h[8];
-        stored4_to_half2<C>(x[i].x, h[0], h[1]);
-        stored4_to_half2<C>(x[i].y, h[2], h[3]);
-        stored4_to_half2<C>(x[i].z, h[4], h[5]);
-        stored4_to_half2<C>(x[i].w, h[6], h[7]);
-        const int at = tile + (half * 64 + i * RPP) * 128;
-        *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
-        *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
-      }
-      __syncwarp();
-      if (lane == 0) mbar_arrive(full + 8 * places);
-      if (++place == places) {
-        place = 0;
-        raw_parity ^= 1;
-      }
+      fence_proxy_async_smem();  // before a copy overwrites the zeros
     }
-    if (!ok) break;
+    uint4 x[2 * NP];
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i)
+      x[i] = *reinterpret_cast<const uint4*>((i < NP ? raw0 : raw1) + (i % NP) * RPP * D);
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      uint32_t h[8];
+      stored4_to_half2<C>(x[i].x, h[0], h[1]);
+      stored4_to_half2<C>(x[i].y, h[2], h[3]);
+      stored4_to_half2<C>(x[i].z, h[4], h[5]);
+      stored4_to_half2<C>(x[i].w, h[6], h[7]);
+      const int at = tile + i * RPP * 128;
+      *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
+      *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
+    }
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(bar(V ? Cfg::kVF : Cfg::kKF) + 8 * (t & 1));
+      mbar_arrive(raw_first + 8 * (places + place));
+      mbar_arrive(raw_first + 8 * (places + place1));
       mbar_arrive(info.bar + 8 * Cfg::kInfo);
     }
     info.advance();
+    place = place1 + 1 == places ? 0 : place1 + 1;
+    raw_parity = place == 0 ? parity1 ^ 1 : parity1;
     tile += t & 1 ? -Cfg::kTileB : Cfg::kTileB;
   }
 }
