@@ -229,25 +229,23 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
   const int sms = bsa::sm_count(dev);
   const bool fp16 = dtype == BSA_FP16, int8 = cache->dtype == BSA_INT8;
-  const int64_t tiles = static_cast<int64_t>(cache->n_pages) * cache->kv_heads;
-  p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
-  // The decode kernels read the boxes as matrix fragments, the tile kernels row by row.
-  CUtensorMap k, v;
-  if (!bsa::encode_cache(&k, cache->k, tiles, cache->page, cache->d, 1 << p.box_shift, rows > 0) ||
-      !bsa::encode_cache(&v, cache->v, tiles, cache->page, cache->d, 1 << p.box_shift, rows > 0))
-    return BSA_ERR_CUDA;
   if (rows > 0) {
+    const int64_t tiles = static_cast<int64_t>(cache->n_pages) * cache->kv_heads;
+    p.box_shift = p.page_shift < 6 ? p.page_shift : 6;
+    CUtensorMap k, v;
+    if (!bsa::encode_cache(&k, cache->k, tiles, cache->page, cache->d, 1 << p.box_shift) ||
+        !bsa::encode_cache(&v, cache->v, tiles, cache->page, cache->d, 1 << p.box_shift))
+      return BSA_ERR_CUDA;
     e = cache->d == 128
             ? (int8 ? bsa::launch_cache_decode_int8_d128(fp16, rows, k, v, p, workspace, sms, st)
                     : bsa::launch_cache_decode_e4m3_d128(fp16, rows, k, v, p, workspace, sms, st))
             : (int8 ? bsa::launch_cache_decode_int8_d64(fp16, rows, k, v, p, workspace, sms, st)
                     : bsa::launch_cache_decode_e4m3_d64(fp16, rows, k, v, p, workspace, sms, st));
   } else {
-    e = cache->d == 128
-            ? (int8 ? bsa::launch_cache_tile_int8_d128(fp16, k, v, p, workspace, sms, st)
-                    : bsa::launch_cache_tile_e4m3_d128(fp16, k, v, p, workspace, sms, st))
-            : (int8 ? bsa::launch_cache_tile_int8_d64(fp16, k, v, p, workspace, sms, st)
-                    : bsa::launch_cache_tile_e4m3_d64(fp16, k, v, p, workspace, sms, st));
+    e = cache->d == 128 ? (int8 ? bsa::launch_cache_tile_int8_d128(fp16, p, workspace, sms, st)
+                                : bsa::launch_cache_tile_e4m3_d128(fp16, p, workspace, sms, st))
+                        : (int8 ? bsa::launch_cache_tile_int8_d64(fp16, p, workspace, sms, st)
+                                : bsa::launch_cache_tile_e4m3_d64(fp16, p, workspace, sms, st));
   }
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
 }

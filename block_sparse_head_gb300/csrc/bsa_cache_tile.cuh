@@ -38,37 +38,27 @@ template <int D>
 struct TileCfg {
   static constexpr int kThreads = 640;
   static constexpr int kRows = 128;
-  static constexpr int kTileB = 128 * D * 2;   // one fp16 tile of Q, K or V
+  static constexpr int kTileB = 128 * D * 2;   // one fp16 tile of K or V
   static constexpr int kHalfB = 128 * 128;     // its 64-column halves, [128][64] swizzled
-  static constexpr int kRawB = 64 * D;         // stored numbers of 64 keys of one side
-  static constexpr int kRawK = 4, kRawV = 3;   // places of them
   static constexpr int kInfo = 8;              // steps looked up ahead
   static constexpr int kItems = 8;             // items whose row factors are kept
-  static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kTileB;
+  static constexpr int kOffK = 0;
   static constexpr int kOffV = kOffK + 2 * kTileB;
-  static constexpr int kOffRawK = kOffV + 2 * kTileB;
-  static constexpr int kOffRawV = kOffRawK + kRawK * kRawB;
-  static constexpr int kOffFactor = kOffRawV + kRawV * kRawB;    // [kItems][128] fp32
+  static constexpr int kOffFactor = kOffV + 2 * kTileB;          // [kItems][128] fp32
   static constexpr int kOffSegs = kOffFactor + kItems * 128 * 4; // the producer's segments
   static constexpr int kOffInfo = kOffSegs + 4 * 64;
-  static constexpr int kInfoB = 208;
+  static constexpr int kInfoB = 240;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoB;
   // barriers
-  static constexpr int kSF = 0;                 // [3] S(t) computed
-  static constexpr int kPVD = 3;                // [3] PV(t) complete
-  static constexpr int kPF = 6;                 // [3] P(t) written (softmax warps)
-  static constexpr int kKF = 9;                 // [2] K(t) converted (4 warps)
-  static constexpr int kVF = 11;                // [2] V(t) converted (4 warps)
-  static constexpr int kQF = 13;                // [kItems] Q of an item converted
+  static constexpr int kSF = 0;                 // [2] S(t) computed
+  static constexpr int kPVD = 2;                // [2] PV(t) complete
+  static constexpr int kPF = 4;                 // [2] P(t) written (softmax warps)
+  static constexpr int kKF = 6;                 // [2] K(t) converted (4 warps)
+  static constexpr int kVF = 8;                 // [2] V(t) converted (4 warps)
+  static constexpr int kQF = 10;                // [kItems] Q of an item converted
   static constexpr int kIF = kQF + kItems;      // [kInfo] step looked up
   static constexpr int kIE = kIF + kInfo;       // [kInfo] step no longer needed
-  static_assert(kIE == kIF + kInfo, "RingBar users add 8 * kInfo");
-  static constexpr int kRKF = kIE + kInfo;      // [kRawK] 64 keys landed
-  static constexpr int kRKE = kRKF + kRawK;     // [kRawK] and converted (4 warps)
-  static constexpr int kRVF = kRKE + kRawK;     // [kRawV]
-  static constexpr int kRVE = kRVF + kRawV;     // [kRawV]
-  static constexpr int kDrain = kRVE + kRawV;   // [2] S, PV issuers' last products
+  static constexpr int kDrain = kIE + kInfo;    // [2] S, PV issuers' last products
   static constexpr int kJoin = kDrain + 2;      // softmax warps
   static constexpr int kNumBars = kJoin + 1;
   static constexpr int kOffScan = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
@@ -78,7 +68,8 @@ struct TileCfg {
   static_assert(kSmemB <= 232448, "shared memory");
   // Two CTAs never share an SM: each takes all 512 TMEM columns.
   static constexpr int kLaunchSmem = kSmemB > 120 * 1024 ? kSmemB : 120 * 1024;
-  static constexpr int kOCol = 384;
+  // TMEM columns: S buffers at 0 and 128 (P over them), O, two Q tiles in fp16
+  static constexpr int kOCol = 256, kQCol = 384;
   static constexpr uint32_t kIdesc = (1u << 4);  // fp16 inputs, fp32 sums
   static constexpr uint32_t kIdescS = kIdesc | (128u / 8) << 17 | (128u / 16) << 24;
   static constexpr uint32_t kIdescPV = kIdesc | 1u << 16 | (D / 8u) << 17 | (128u / 16) << 24;
@@ -89,13 +80,12 @@ struct TileStep {
   CacheSeg seg;   // of every step (13 words)
   int flags;      // DecodeFlags
   int key0[2];    // first key of each piece (kNoKeys: none)
-  int there[2];   // per piece: bit i says that its keys 16 i .. are there
-  int tile[8];    // per 16 keys that are there: page * heads + head
+  int64_t off[8]; // per 16 keys: where they start in the cache (bytes), -1: not there
   float ks[8];    // per 16 keys: scale of the scores (1 where the keys are not there)
   float lv[8];    // log2 of the value scale (-inf where the keys are not there)
   float rv[8];    // its reciprocal (0 where the keys are not there)
 };
-static_assert(sizeof(TileStep) <= 208, "step slots");
+static_assert(sizeof(TileStep) <= 240, "step slots");
 
 // A barrier of a ring of N: its address and the parity of the phase to wait for (or to fill)
 // next.
@@ -199,17 +189,14 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
     TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
     const int j = lane - 8 * i;
     const bool on = cur.tile >= 0 && !end;
-    const uint32_t seen = __ballot_sync(0xffffffffu, on) >> (8 * i);
     if (j >= 0 && j < 8) {
       const float lv = log2_scale(cur.vs);
-      st.tile[j] = cur.tile;
+      const int row = (cur.key + 16 * (j & 3)) & ((1 << p.page_shift) - 1);
+      st.off[j] = on ? ((static_cast<int64_t>(cur.tile) << p.page_shift) + row) * D : -1;
       st.ks[j] = on ? cur.ks : 1.f;
       st.lv[j] = on ? lv : -INFINITY;
       st.rv[j] = on ? ex2_approx(-lv) : 0.f;
-      if ((j & 3) == 0) {
-        st.key0[j >> 2] = cur.key;
-        st.there[j >> 2] = seen >> (j & 4) & 15;
-      }
+      if ((j & 3) == 0) st.key0[j >> 2] = cur.key;
     }
     if (lane < static_cast<int>(sizeof(CacheSeg) / 4))
       reinterpret_cast<int*>(&st.seg)[lane] = reinterpret_cast<const int*>(&seg_at(cur.seg))[lane];
@@ -225,96 +212,16 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
   }
 }
 
-// ------------------------------------------------------------------------ copies
-
-// One warp: stored numbers into the raw places, K of step t and then V of step t - 1 (whose
-// place is free later).  Lane j < 8 has group j of 16 keys.
-template <int D>
-__device__ __forceinline__ void tile_copy(const CacheFwdParams& p, const CUtensorMap* tm_k,
-                                          const CUtensorMap* tm_v, uint8_t* smem, volatile int* ctl) {
-  using Cfg = TileCfg<D>;
-  const int lane = threadIdx.x & 31;
-  const uint32_t sbase = smem_u32(smem);
-  auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
-  // A box (2^box rows) is copied whole if any of its groups is there, by the lane of the first
-  // that is.
-  const int box = p.box_shift, groups = 1 << (box - 4);
-  const int base = lane & ~(groups - 1);
-  // Where this lane's copy goes in the piece, and its box's first row in the page.
-  struct Place {
-    bool load;
-    int tile, row;
-    uint32_t pieces;  // boxes of the first and (<< 8) of the second piece
-  };
-  auto place_of = [&](const TileStep& st, bool end) {
-    Place x;
-    const int there = end ? 0 : st.there[0] | st.there[1] << 4;
-    const int mine = there >> base & ((1 << groups) - 1);
-    x.load = lane < 8 && mine != 0 && lane == base + __ffs(mine) - 1;
-    x.tile = st.tile[lane & 7];
-    x.row = (st.key0[lane >> 2 & 1] + 16 * (base & 3)) & ((1 << p.page_shift) - 1);
-    const uint32_t on = __ballot_sync(0xffffffffu, x.load);
-    x.pieces = __popc(on & 15u) | __popc(on & 0xF0u) << 8;
-    return x;
-  };
-  int pieces_k = 0, pieces_v = 0;  // announced so far
-  auto copy = [&](const CUtensorMap* tm, const Place& x, int full, int raw, int places, int site,
-                  int& n) -> bool {
-    const int s0 = n % places, s1 = (n + 1) % places;
-    const int empty = full + places;
-    if (n >= places && !mbar_wait_tries(bar(empty + s0), (n / places - 1) & 1, ctl, site)) return false;
-    if (n + 1 >= places && !mbar_wait_tries(bar(empty + s1), ((n + 1) / places - 1) & 1, ctl, site))
-      return false;
-    if (lane == 0) {
-      mbar_arrive_expect_tx(bar(full + s0), (x.pieces & 0xFF) * (D << box));
-      mbar_arrive_expect_tx(bar(full + s1), (x.pieces >> 8) * (D << box));
-    }
-    __syncwarp();
-    if (x.load) {
-      const int s = lane < 4 ? s0 : s1;
-      tma_load_3d(sbase + raw + s * Cfg::kRawB + 16 * (base & 3) * D, tm, bar(full + s), 0, x.row, x.tile);
-    }
-    n += 2;
-    return true;
-  };
-  static_assert(Cfg::kRKE == Cfg::kRKF + Cfg::kRawK && Cfg::kRVE == Cfg::kRVF + Cfg::kRawV, "order");
-  Place v{};
-  for (int t = 0;; ++t) {
-    const int slot = t % Cfg::kInfo;
-    if (!mbar_wait_tries(bar(Cfg::kIF + slot), (t / Cfg::kInfo) & 1, ctl, kSiteCacheInfo)) break;
-    const TileStep& st = *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
-    const bool end = st.flags & kStageEnd;
-    // (The end goes through the rings too, without bytes: the converters learn of a step by its
-    // pieces.)
-    const Place k = place_of(st, end);
-    __syncwarp();
-    if (lane == 0 && !end) mbar_arrive(bar(Cfg::kIE + slot));
-    if (!copy(tm_k, k, Cfg::kRKF, Cfg::kOffRawK, Cfg::kRawK, kSiteProdKEmpty, pieces_k)) break;
-    if (t > 0 && !copy(tm_v, v, Cfg::kRVF, Cfg::kOffRawV, Cfg::kRawV, kSiteProdVEmpty, pieces_v)) break;
-    v = k;
-    if (end) {
-      copy(tm_v, v, Cfg::kRVF, Cfg::kOffRawV, Cfg::kRawV, kSiteProdVEmpty, pieces_v);
-      break;
-    }
-  }
-  // Every copy lands before the CTA leaves (also when the converters have given up).
-  for (int n = max(0, pieces_k - Cfg::kRawK); n < pieces_k; ++n)
-    mbar_drain_wait(bar(Cfg::kRKF + n % Cfg::kRawK), (n / Cfg::kRawK) & 1);
-  for (int n = max(0, pieces_v - Cfg::kRawV); n < pieces_v; ++n)
-    mbar_drain_wait(bar(Cfg::kRVF + n % Cfg::kRawV), (n / Cfg::kRawV) & 1);
-}
-
 // ------------------------------------------------------------------- MMA issuers
 
 template <int D>
 struct TileDescs {
   using Cfg = TileCfg<D>;
-  uint32_t hi, q0, k0, v0;
+  uint32_t hi, k0, v0;
   __device__ __forceinline__ explicit TileDescs(uint32_t sbase) {
     const uint64_t k = sdesc_sw128(sbase + Cfg::kOffK, 16, 1024);
     hi = static_cast<uint32_t>(k >> 32);
     k0 = static_cast<uint32_t>(k);
-    q0 = static_cast<uint32_t>(sdesc_sw128(sbase + Cfg::kOffQ, 16, 1024));
     v0 = static_cast<uint32_t>(sdesc_sw128(sbase + Cfg::kOffV, Cfg::kHalfB, 1024));
   }
 };
@@ -328,8 +235,8 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
   RingBar<2> keys(bar(Cfg::kKF));
-  RingBar<3> done(bar(Cfg::kPVD));
-  uint32_t s = 0, k = 0;  // columns of the S buffer, offset of the K tile
+  RingBar<2> done(bar(Cfg::kPVD));
+  uint32_t s = 0, k = 0, q = tmem + Cfg::kQCol + 64;  // S buffer, K tile, the item's Q
   for (int t = 0;; ++t) {
     if (!info.wait(ctl, kSiteCacheInfo)) break;
     const int flags =
@@ -340,21 +247,21 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
     if (flags & kStageFirst) {
       if (!queries.wait(ctl, kSiteMmaStage)) break;
       queries.advance();
+      q = q == tmem + Cfg::kQCol ? q + 64 : tmem + Cfg::kQCol;
     }
     if (!keys.wait(ctl, kSiteMmaStage)) break;
     keys.advance();
-    if (t >= 3) {  // S[t % 3] was last read by PV(t - 3)
+    if (t >= 2) {  // S[t % 2] was last read by PV(t - 2)
       if (!done.wait(ctl, kSiteMmaPvDone)) break;
       done.advance();
     }
     tc_fence_after();
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const uint32_t off = ((kk >> 2) * Cfg::kHalfB + (kk & 3) * 32) >> 4;
-      tc_mma_ss_lh(tmem + s, md.q0 + off, md.hi, md.k0 + k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
-    }
+    for (int kk = 0; kk < D / 16; ++kk)
+      tc_mma_ts_lh(tmem + s, q + kk * 8, md.k0 + k + (((kk >> 2) * Cfg::kHalfB + (kk & 3) * 32) >> 4),
+                   md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
     tc_commit(bar(Cfg::kSF) + s / 16);
-    s = s == 256 ? 0 : s + 128;
+    s ^= 128;
     k ^= Cfg::kTileB >> 4;
   }
   tc_commit(bar(Cfg::kDrain));
@@ -368,7 +275,7 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const TileDescs<D> md(sbase);
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
-  RingBar<3> weights(bar(Cfg::kPF));
+  RingBar<2> weights(bar(Cfg::kPF));
   RingBar<2> values(bar(Cfg::kVF));
   uint32_t ps = 0, v = 0;  // columns of the S buffer, offset of the V tile
   for (;;) {
@@ -390,7 +297,7 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
       tc_mma_ts_lh(tmem + Cfg::kOCol, tmem + ps + kk * 8, md.v0 + v + ((kk * 16 * 128) >> 4), md.hi,
                    Cfg::kIdescPV, kk == 0 && first ? 0u : 1u);
     tc_commit(bar(Cfg::kPVD) + ps / 16);
-    ps = ps == 256 ? 0 : ps + 128;
+    ps ^= 128;
     v ^= Cfg::kTileB >> 4;
   }
   tc_commit(bar(Cfg::kDrain + 1));
@@ -399,13 +306,27 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
 
 // -------------------------------------------------------------------- converters
 
+// 16 bytes, or zeros: a predicated load (as a branch, each of a thread's loads would wait
+// for the address of the one before).
+__device__ __forceinline__ uint4 load16_if(const void* ptr, bool on) {
+  uint4 x;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
+      : "l"(ptr), "r"(static_cast<int>(on)));
+  return x;
+}
+
 // One side (V: values, else keys and the queries); 128 threads.  One piece of code for both.
 template <class A, class C, int D>
-__device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const bool V,
-                                             volatile int* ctl) {
+__device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, uint32_t tmem,
+                                             const bool V, volatile int* ctl) {
   using Cfg = TileCfg<D>;
   constexpr int RPP = 128 * 16 / D;   // rows of a pass of the 128 threads, 16 numbers each
-  constexpr int NP = 64 / RPP;        // passes of a piece of 64 keys
+  constexpr int NP = 128 / RPP;       // passes of a tile
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const int tid = threadIdx.x & 127, lane = tid & 31, warp = tid >> 5;
@@ -415,46 +336,45 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   const int piece = D == 128 ? lane & 7 : lane & 3;
   const int r0 = warp * (RPP / 4) +
                  (D == 128 ? (((lane >> 2) ^ (lane >> 3)) & 1) | ((lane >> 3) & 2) : lane >> 2);
-  auto arrive = [&](int b) {
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(b));
-  };
-  const int src0 = r0 * D + piece * 16;
+  const uint8_t* const cache = (V ? p.v_cache : p.k_cache) + (r0 & 15) * D + piece * 16;
   const int row0 = (piece >> 2) * Cfg::kHalfB + r0 * 128;
   const int dst0 = row0 + (((2 * (piece & 3)) ^ (r0 & 7)) << 4);
   const int dst1 = row0 + (((2 * (piece & 3) + 1) ^ (r0 & 7)) << 4);
-
-  // Rings: places of stored numbers (counted up to this side's number of them; a step's pieces
-  // landed, its look-ups are there too), and what last read the tile that a step overwrites:
-  // S(t - 2) for K, PV(t - 2) for V, and S(t - 1) for an item's queries.
-  RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
-  RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF)), free1(bar(Cfg::kSF));
-  const uint32_t raw_first = bar(V ? Cfg::kRVF : Cfg::kRKF), places = V ? Cfg::kRawV : Cfg::kRawK;
-  const int raw_base = (V ? Cfg::kOffRawV : Cfg::kOffRawK) + src0;
-  uint32_t place = 0, raw_parity = 0;
-  int tile = V ? Cfg::kOffV : Cfg::kOffK;
-  auto wait_ring = [&](const auto& ring, int site) {
-    return __all_sync(0xffffffffu, ring.wait(ctl, site)) != 0;
-  };
-  int item = -1;
-  for (int t = 0;; ++t) {
-    const uint32_t place1 = place + 1 == places ? 0 : place + 1;
-    const uint32_t parity1 = place1 == 0 ? raw_parity ^ 1 : raw_parity;
-    bool ok = mbar_wait_tries(raw_first + 8 * place, raw_parity, ctl, kSiteMmaStage);
-    const TileStep& st =
-        *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
-    const int flags = ok ? st.flags : kStageEnd;
-    if (!(flags & kStageEnd))
-      ok = mbar_wait_tries(raw_first + 8 * place1, parity1, ctl, kSiteMmaStage) &&
-           (t < 2 || free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty));
-    if (!__all_sync(0xffffffffu, ok) || (flags & kStageEnd)) break;
-    if (t >= 2) free2.advance();
-    if (!V && t >= 1) {
-      if ((flags & kStageFirst) && !wait_ring(free1, kSiteProdKEmpty)) break;
-      free1.advance();
+  uint4 x[NP];
+  // A step's stored numbers into registers; what no query of the tile sees is zero (the cache
+  // may hold anything there).
+  auto load = [&](const TileStep& st) {
+    const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
+    const int k0 = st.key0[0] + r0, k1 = st.key0[1] + r0;
+    int64_t off[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) off[i] = st.off[(i * RPP + r0) >> 4];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int key = (i < NP / 2 ? k0 : k1) + (i * RPP & 63);
+      x[i] = load16_if(cache + off[i], off[i] >= 0 && key >= lo && key <= last);
     }
-    if (!V && (flags & kStageFirst)) {
+  };
+  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K (and for
+  // the queries of the item before the last), PV(t - 2) for V.
+  RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
+  RingBar<2> free2(bar(V ? Cfg::kPVD : Cfg::kSF));
+  int tile = V ? Cfg::kOffV : Cfg::kOffK;
+  int item = -1, flags = 0;
+  auto step = [&]() -> const TileStep& {
+    return *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
+  };
+  // Iteration t stores step t and then requests step t + 1 (t = -1: requests the first).
+  for (int t = -1;; ++t) {
+    if (t >= 0) {
+      const TileStep& st = step();
+      if (t >= 2) {
+        if (!__all_sync(0xffffffffu, free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty))) break;
+        free2.advance();
+      }
+      if (!V && (flags & kStageFirst)) {
         ++item;
+        tc_fence_after();
         // Row tid of the tile: query and head, scaled into fp16's range.
         const CacheSeg& s = st.seg;
         const int qi = static_cast<int>((tid * p.group_inv) >> 16);
@@ -481,69 +401,59 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
           up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
           back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
         }
-        uint8_t* row = smem + Cfg::kOffQ + tid * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (live) {
-            x = *reinterpret_cast<const uint4*>(q + 8 * c);
-            if constexpr (!std::is_same<A, __half>::value) {
-              uint32_t w[4] = {x.x, x.y, x.z, x.w};
+        // Row = TMEM lane; two numbers a column, as the product takes its first operand.
+        const uint32_t dst = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Cfg::kQCol + 64 * (item & 1);
+#pragma unroll 1
+        for (int c = 0; c < D / 64; ++c) {
+          uint32_t w[32];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = act_to_float2<A>(w[i]);
-                w[i] = float2_to_act<__half>(f.x * up, f.y * up);
-              }
-              x = make_uint4(w[0], w[1], w[2], w[3]);
+          for (int i = 0; i < 8; ++i) {
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (live) y = *reinterpret_cast<const uint4*>(q + c * 64 + 8 * i);
+            w[4 * i] = y.x;
+            w[4 * i + 1] = y.y;
+            w[4 * i + 2] = y.z;
+            w[4 * i + 3] = y.w;
+          }
+          if constexpr (!std::is_same<A, __half>::value) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const float2 f = act_to_float2<A>(w[i]);
+              w[i] = float2_to_act<__half>(f.x * up, f.y * up);
             }
           }
-          *reinterpret_cast<uint4*>(row + (c >> 3) * Cfg::kHalfB + (((c & 7) ^ (tid & 7)) << 4)) = x;
+          tmem_st_32x32b_x32(dst + 32 * c, w);
         }
         reinterpret_cast<float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + tid] = back;
-        fence_proxy_async_smem();
-        arrive(Cfg::kQF + item % Cfg::kItems);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(Cfg::kQF + item % Cfg::kItems));
       }
-    const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
-    uint8_t* const raw0 = smem + raw_base + place * Cfg::kRawB;
-    uint8_t* const raw1 = smem + raw_base + place1 * Cfg::kRawB;
-    const int k0 = st.key0[0], k1 = st.key0[1], there = st.there[0] | st.there[1] << 4;
-    if (there != 255 || min(k0, k1) < lo || max(k0, k1) + 63 > last) {
-      // What no query of the tile sees is zero (the cache may hold anything there).
-#pragma unroll 1
-      for (int i = 0; i < 2 * NP; ++i) {
-        const int row = i * RPP + r0, key = (i < NP ? k0 : k1) + (row & 63);
-        if (!(there >> (row >> 4) & 1) || key < lo || key > last)
-          *reinterpret_cast<uint4*>((i < NP ? raw0 : raw1) + (i % NP) * RPP * D) = make_uint4(0, 0, 0, 0);
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint32_t h[8];
+        stored4_to_half2<C>(x[i].x, h[0], h[1]);
+        stored4_to_half2<C>(x[i].y, h[2], h[3]);
+        stored4_to_half2<C>(x[i].z, h[4], h[5]);
+        stored4_to_half2<C>(x[i].w, h[6], h[7]);
+        const int at = tile + i * RPP * 128;
+        *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
       }
-      fence_proxy_async_smem();  // before a copy overwrites the zeros
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) {
+        mbar_arrive(bar(V ? Cfg::kVF : Cfg::kKF) + 8 * (t & 1));
+        mbar_arrive(info.bar + 8 * Cfg::kInfo);
+      }
+      info.advance();
+      tile += t & 1 ? -Cfg::kTileB : Cfg::kTileB;
     }
-    uint4 x[2 * NP];
-#pragma unroll
-    for (int i = 0; i < 2 * NP; ++i)
-      x[i] = *reinterpret_cast<const uint4*>((i < NP ? raw0 : raw1) + (i % NP) * RPP * D);
-#pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) {
-      uint32_t h[8];
-      stored4_to_half2<C>(x[i].x, h[0], h[1]);
-      stored4_to_half2<C>(x[i].y, h[2], h[3]);
-      stored4_to_half2<C>(x[i].z, h[4], h[5]);
-      stored4_to_half2<C>(x[i].w, h[6], h[7]);
-      const int at = tile + i * RPP * 128;
-      *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
-    }
-    fence_proxy_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(bar(V ? Cfg::kVF : Cfg::kKF) + 8 * (t & 1));
-      mbar_arrive(raw_first + 8 * (places + place));
-      mbar_arrive(raw_first + 8 * (places + place1));
-      mbar_arrive(info.bar + 8 * Cfg::kInfo);
-    }
-    info.advance();
-    place = place1 + 1 == places ? 0 : place1 + 1;
-    raw_parity = place == 0 ? parity1 ^ 1 : parity1;
-    tile += t & 1 ? -Cfg::kTileB : Cfg::kTileB;
+    if (!__all_sync(0xffffffffu, info.wait(ctl, kSiteCacheInfo))) break;
+    flags = step().flags;
+    if (flags & kStageEnd) break;
+    load(step());
   }
 }
 
@@ -658,7 +568,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   bool pending = false;
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
-  RingBar<3> scores(bar(Cfg::kSF)), before(bar(Cfg::kPVD));  // S(t), PV(t - 1)
+  RingBar<2> scores(bar(Cfg::kSF)), before(bar(Cfg::kPVD));  // S(t), PV(t - 1)
   uint32_t ts = tl;  // the step's S buffer
   for (int t = 0;; ++t) {
     if (!wait_ring(info, kSiteCacheInfo)) break;
@@ -785,17 +695,14 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     info.advance();
     if (t > 0) before.advance();
-    ts = ts == tl + 256 ? tl : ts + 128;
+    ts = ts == tl ? tl + 128 : tl;
   }
 }
 
 // ------------------------------------------------------------------------ kernel
 
 template <class A, class C, int D, bool FOLD>
-__global__ void __launch_bounds__(640, 1)
-    bsa_cache_tile_kernel(const __grid_constant__ CUtensorMap tm_k,
-                          const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p,
-                          void* workspace) {
+__global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdParams p, void* workspace) {
   using Cfg = TileCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -809,12 +716,10 @@ __global__ void __launch_bounds__(640, 1)
   const CacheUnits units{p, 31 - __clz(static_cast<int>((128u * p.group_inv) >> 16)), 6, 2};
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
-    for (int i = 0; i < 3; ++i) {
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Cfg::kSF + i), 1);
       mbar_init(bar(Cfg::kPVD + i), 1);
       mbar_init(bar(Cfg::kPF + i), 8);
-    }
-    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Cfg::kKF + i), 4);
       mbar_init(bar(Cfg::kVF + i), 4);
       mbar_init(bar(Cfg::kDrain + i), 1);
@@ -822,19 +727,9 @@ __global__ void __launch_bounds__(640, 1)
     for (int i = 0; i < Cfg::kItems; ++i) mbar_init(bar(Cfg::kQF + i), 4);
     for (int i = 0; i < Cfg::kInfo; ++i) {
       mbar_init(bar(Cfg::kIF + i), 1);
-      mbar_init(bar(Cfg::kIE + i), 8 + 8 + 2 + 1);  // converters, softmax, issuers, copies
-    }
-    for (int i = 0; i < Cfg::kRawK; ++i) {
-      mbar_init(bar(Cfg::kRKF + i), 1);
-      mbar_init(bar(Cfg::kRKE + i), 4);
-    }
-    for (int i = 0; i < Cfg::kRawV; ++i) {
-      mbar_init(bar(Cfg::kRVF + i), 1);
-      mbar_init(bar(Cfg::kRVE + i), 4);
+      mbar_init(bar(Cfg::kIE + i), 8 + 8 + 2);  // converters, softmax, issuers
     }
     mbar_init(bar(Cfg::kJoin), 8);
-    tma_prefetch_desc(&tm_k);
-    tma_prefetch_desc(&tm_v);
     err[0] = err[1] = 0;
     fence_mbar_init();
     if (blockIdx.x == 0) *p.status = 0;
@@ -857,13 +752,11 @@ __global__ void __launch_bounds__(640, 1)
       if (lane == 0) tile_mma_pv<D>(smem, tmem, ctl);
     } else if (warp == 2) {
       tile_lookup<D>(p, smem, units, ctl);
-    } else {
-      tile_copy<D>(p, &tm_k, &tm_v, smem, ctl);
     }
   } else if (warp < 12) {
     tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 1, ctl);
   } else {
-    tile_convert<A, C, D>(p, smem, warp >= 16, ctl);
+    tile_convert<A, C, D>(p, smem, tmem, warp >= 16, ctl);
   }
   tc_fence_before();
   __syncthreads();
@@ -877,23 +770,22 @@ __global__ void __launch_bounds__(640, 1)
 }
 
 template <class A, class C, int D, bool FOLD>
-cudaError_t launch_tile_as(const CUtensorMap& k, const CUtensorMap& v, const CacheFwdParams& p, void* workspace, int sms,
+cudaError_t launch_tile_as(const CacheFwdParams& p, void* workspace, int sms,
                            cudaStream_t stream) {
   using Cfg = TileCfg<D>;
   auto* kernel = bsa_cache_tile_kernel<A, C, D, FOLD>;
   static int done[64];
   const cudaError_t e = set_smem_once(kernel, Cfg::kLaunchSmem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<sms, Cfg::kThreads, Cfg::kLaunchSmem, stream>>>(k, v, p, workspace);
+  kernel<<<sms, Cfg::kThreads, Cfg::kLaunchSmem, stream>>>(p, workspace);
   return cudaGetLastError();
 }
 
 template <class A, class C, int D>
-cudaError_t launch_tile(const CUtensorMap& k, const CUtensorMap& v, const CacheFwdParams& p,
-                        void* workspace, int sms, cudaStream_t stream) {
+cudaError_t launch_tile(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
   return p.softcap_log2 == 0.f && p.scale_log2 > 0.f
-             ? launch_tile_as<A, C, D, true>(k, v, p, workspace, sms, stream)
-             : launch_tile_as<A, C, D, false>(k, v, p, workspace, sms, stream);
+             ? launch_tile_as<A, C, D, true>(p, workspace, sms, stream)
+             : launch_tile_as<A, C, D, false>(p, workspace, sms, stream);
 }
 
 }  // namespace bsa

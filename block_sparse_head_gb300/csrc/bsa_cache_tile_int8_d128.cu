@@ -3,11 +3,10 @@
 
 namespace bsa {
 
-cudaError_t launch_cache_tile_int8_d128(bool fp16, const CUtensorMap& k, const CUtensorMap& v,
-                                       const CacheFwdParams& p, void* workspace, int sms,
-                                       cudaStream_t stream) {
-  return fp16 ? launch_tile<__half, Int8, 128>(k, v, p, workspace, sms, stream)
-              : launch_tile<__nv_bfloat16, Int8, 128>(k, v, p, workspace, sms, stream);
+cudaError_t launch_cache_tile_int8_d128(bool fp16, const CacheFwdParams& p, void* workspace,
+                                       int sms, cudaStream_t stream) {
+  return fp16 ? launch_tile<__half, Int8, 128>(p, workspace, sms, stream)
+              : launch_tile<__nv_bfloat16, Int8, 128>(p, workspace, sms, stream);
 }
 
 }  // namespace bsa

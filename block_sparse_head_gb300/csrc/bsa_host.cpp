@@ -66,7 +66,7 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int d, int bo
 }  // namespace
 
 bool bsa::encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int page, int d,
-                       int rows, bool swizzle) {
+                       int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
   if (fn == nullptr) return false;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(page),
@@ -76,8 +76,7 @@ bool bsa::encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int pa
   const cuuint32_t estr[3] = {1, 1, 1};
   return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box,
             estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-            !swizzle ? CU_TENSOR_MAP_SWIZZLE_NONE
-            : d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+            d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }

@@ -284,9 +284,8 @@ BSA_DECODE_LAUNCH(int8_d128);
 // Any number of query rows, in tiles of kTileRows.
 constexpr int kTileRows = 128;
 #define BSA_TILE_LAUNCH(name)                                                                \
-  cudaError_t launch_cache_tile_##name(bool fp16, const CUtensorMap& k, const CUtensorMap& v, \
-                                       const CacheFwdParams& p, void* workspace, int sms,     \
-                                       cudaStream_t stream)
+  cudaError_t launch_cache_tile_##name(bool fp16, const CacheFwdParams& p, void* workspace,  \
+                                       int sms, cudaStream_t stream)
 BSA_TILE_LAUNCH(e4m3_d64);
 BSA_TILE_LAUNCH(e4m3_d128);
 BSA_TILE_LAUNCH(int8_d64);
@@ -294,9 +293,8 @@ BSA_TILE_LAUNCH(int8_d128);
 #undef BSA_TILE_LAUNCH
 
 // A cache side [tiles, page, d] of 8-bit numbers for boxes of `rows` rows of one tile,
-// swizzled over their whole row (128 or 64 bytes) or plain.  false: the encoder refused.
-bool encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int page, int d, int rows,
-                  bool swizzle);
+// swizzled over their whole row (128 or 64 bytes).  false: the encoder refused.
+bool encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int page, int d, int rows);
 
 // One-CTA kernel whose only wait never completes; it must give up after limit_ns.
 cudaError_t launch_wait_selftest(int32_t* status, uint64_t limit_ns, cudaStream_t stream);
