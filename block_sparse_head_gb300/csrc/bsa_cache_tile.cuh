@@ -42,7 +42,8 @@ struct TileCfg {
   static constexpr int kHalfB = 128 * 128;     // its 64-column halves, [128][64] swizzled
   static constexpr int kInfo = 8;              // steps looked up ahead
   static constexpr int kItems = 8;             // items whose row factors are kept
-  static constexpr int kOffK = 0;
+  static constexpr int kOffQ = 0;
+  static constexpr int kOffK = kOffQ + kTileB;
   static constexpr int kOffV = kOffK + 2 * kTileB;
   static constexpr int kOffFactor = kOffV + 2 * kTileB;          // [kItems][128] fp32
   static constexpr int kOffSegs = kOffFactor + kItems * 128 * 4; // the producer's segments
@@ -50,12 +51,12 @@ struct TileCfg {
   static constexpr int kInfoB = 240;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoB;
   // barriers
-  static constexpr int kSF = 0;                 // [2] S(t) computed
-  static constexpr int kPVD = 2;                // [2] PV(t) complete
-  static constexpr int kPF = 4;                 // [2] P(t) written (softmax warps)
-  static constexpr int kKF = 6;                 // [2] K(t) converted (4 warps)
-  static constexpr int kVF = 8;                 // [2] V(t) converted (4 warps)
-  static constexpr int kQF = 10;                // [kItems] Q of an item converted
+  static constexpr int kSF = 0;                 // [3] S(t) computed
+  static constexpr int kPVD = 3;                // [3] PV(t) complete
+  static constexpr int kPF = 6;                 // [3] P(t) written (softmax warps)
+  static constexpr int kKF = 9;                 // [2] K(t) converted (4 warps)
+  static constexpr int kVF = 11;                // [2] V(t) converted (4 warps)
+  static constexpr int kQF = 13;                // [kItems] Q of an item converted
   static constexpr int kIF = kQF + kItems;      // [kInfo] step looked up
   static constexpr int kIE = kIF + kInfo;       // [kInfo] step no longer needed
   static constexpr int kDrain = kIE + kInfo;    // [2] S, PV issuers' last products
@@ -68,8 +69,7 @@ struct TileCfg {
   static_assert(kSmemB <= 232448, "shared memory");
   // Two CTAs never share an SM: each takes all 512 TMEM columns.
   static constexpr int kLaunchSmem = kSmemB > 120 * 1024 ? kSmemB : 120 * 1024;
-  // TMEM columns: S buffers at 0 and 128 (P over them), O, two Q tiles in fp16
-  static constexpr int kOCol = 256, kQCol = 384;
+  static constexpr int kOCol = 384;  // TMEM columns: three S buffers (P over them), O
   static constexpr uint32_t kIdesc = (1u << 4);  // fp16 inputs, fp32 sums
   static constexpr uint32_t kIdescS = kIdesc | (128u / 8) << 17 | (128u / 16) << 24;
   static constexpr uint32_t kIdescPV = kIdesc | 1u << 16 | (D / 8u) << 17 | (128u / 16) << 24;
@@ -116,9 +116,8 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   CacheWalk walk = *reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk);
-  // Up to four steps of one segment: lane 8 i + j looks up group j (16 keys) of step i.  The
-  // look-ups depend on one another (layout block, page, scales), each a trip to memory; the
-  // next batch's are made one by one between the steps of this one.
+  // Up to four steps of one segment at a time: lane 8 i + j looks up group j (16 keys) of step
+  // i.  A batch is looked up while the ring still holds the steps of the one before.
   struct Batch {
     int seg, s, steps;  // place of its segment, first step, steps of the segment (0: the end)
     int key, pid, tile;
@@ -167,48 +166,48 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
     x.vs = p.v_scale[x.tile];
   };
   Batch cur{}, next{};
-  cur.seg = -1;
-  next = cur;
-  place(next, cur);
-  find_page(cur);
-  find_scales(cur);
-  for (int t = 0, i = 0;; ++t, ++i) {
-    if (cur.steps > 0 && (i == 4 || cur.s + i >= cur.steps)) {
-      const int n = i;  // look-ups of next that the steps of cur left
-      if (n < 1) place(cur, next);
-      if (n < 2) find_page(next);
-      if (n < 3) find_scales(next);
-      cur = next;
-      i = 0;
+  next.seg = -1;
+  const int i = lane >> 3, j = lane & 7;
+  bool any = false;  // cur holds a batch
+  for (int t = 0;;) {
+    place(any ? cur : next, next);
+    if (any) {
+      // Publishes cur, whose look-ups have been made.
+      const bool end = cur.steps == 0;
+      const int n = end ? 1 : min(4, cur.steps - cur.s);
+      bool ok = true;
+#pragma unroll 1
+      for (int u = t; u < t + n; ++u)
+        ok = ok && (u < Cfg::kInfo || mbar_wait_tries(bar(Cfg::kIE + u % Cfg::kInfo),
+                                                      (u / Cfg::kInfo - 1) & 1, ctl, kSiteProdKEmpty));
+      if (!__all_sync(0xffffffffu, ok)) break;
+      const int slot = (t + i) % Cfg::kInfo;
+      TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+      if (i < n) {
+        const bool on = cur.tile >= 0 && !end;
+        const float lv = log2_scale(cur.vs);
+        const int row = (cur.key + 16 * (j & 3)) & ((1 << p.page_shift) - 1);
+        st.off[j] = on ? ((static_cast<int64_t>(cur.tile) << p.page_shift) + row) * D : -1;
+        st.ks[j] = on ? cur.ks : 1.f;
+        st.lv[j] = on ? lv : -INFINITY;
+        st.rv[j] = on ? ex2_approx(-lv) : 0.f;
+        if ((j & 3) == 0) st.key0[j >> 2] = cur.key;
+        if (j == 0)
+          st.flags = end ? kStageEnd
+                         : (cur.s + i == 0 ? kStageFirst : 0) | (cur.s + i + 1 == cur.steps ? kStageLast : 0);
+        const int* from = reinterpret_cast<const int*>(&seg_at(cur.seg));
+        for (int w = j; w < static_cast<int>(sizeof(CacheSeg) / 4); w += 8)
+          reinterpret_cast<int*>(&st.seg)[w] = from[w];
+      }
+      __syncwarp();
+      if (i < n && j == 0) mbar_arrive(bar(Cfg::kIF + slot));
+      if (end) break;
+      t += n;
     }
-    const bool end = cur.steps == 0;
-    const int slot = t % Cfg::kInfo;
-    if (t >= Cfg::kInfo &&
-        !mbar_wait_tries(bar(Cfg::kIE + slot), (t / Cfg::kInfo - 1) & 1, ctl, kSiteProdKEmpty))
-      break;
-    TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
-    const int j = lane - 8 * i;
-    const bool on = cur.tile >= 0 && !end;
-    if (j >= 0 && j < 8) {
-      const float lv = log2_scale(cur.vs);
-      const int row = (cur.key + 16 * (j & 3)) & ((1 << p.page_shift) - 1);
-      st.off[j] = on ? ((static_cast<int64_t>(cur.tile) << p.page_shift) + row) * D : -1;
-      st.ks[j] = on ? cur.ks : 1.f;
-      st.lv[j] = on ? lv : -INFINITY;
-      st.rv[j] = on ? ex2_approx(-lv) : 0.f;
-      if ((j & 3) == 0) st.key0[j >> 2] = cur.key;
-    }
-    if (lane < static_cast<int>(sizeof(CacheSeg) / 4))
-      reinterpret_cast<int*>(&st.seg)[lane] = reinterpret_cast<const int*>(&seg_at(cur.seg))[lane];
-    if (lane == 0)
-      st.flags = end ? kStageEnd
-                     : (cur.s + i == 0 ? kStageFirst : 0) | (cur.s + i + 1 == cur.steps ? kStageLast : 0);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar(Cfg::kIF + slot));
-    if (end) break;
-    if (i == 0) place(cur, next);
-    else if (i == 1) find_page(next);
-    else if (i == 2) find_scales(next);
+    find_page(next);
+    find_scales(next);
+    cur = next;
+    any = true;
   }
 }
 
@@ -217,11 +216,12 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
 template <int D>
 struct TileDescs {
   using Cfg = TileCfg<D>;
-  uint32_t hi, k0, v0;
+  uint32_t hi, q0, k0, v0;
   __device__ __forceinline__ explicit TileDescs(uint32_t sbase) {
     const uint64_t k = sdesc_sw128(sbase + Cfg::kOffK, 16, 1024);
     hi = static_cast<uint32_t>(k >> 32);
     k0 = static_cast<uint32_t>(k);
+    q0 = static_cast<uint32_t>(sdesc_sw128(sbase + Cfg::kOffQ, 16, 1024));
     v0 = static_cast<uint32_t>(sdesc_sw128(sbase + Cfg::kOffV, Cfg::kHalfB, 1024));
   }
 };
@@ -235,8 +235,8 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
   RingBar<2> keys(bar(Cfg::kKF));
-  RingBar<2> done(bar(Cfg::kPVD));
-  uint32_t s = 0, k = 0, q = tmem + Cfg::kQCol + 64;  // S buffer, K tile, the item's Q
+  RingBar<3> done(bar(Cfg::kPVD));
+  uint32_t s = 0, k = 0;  // columns of the S buffer, offset of the K tile
   for (int t = 0;; ++t) {
     if (!info.wait(ctl, kSiteCacheInfo)) break;
     const int flags =
@@ -247,21 +247,21 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
     if (flags & kStageFirst) {
       if (!queries.wait(ctl, kSiteMmaStage)) break;
       queries.advance();
-      q = q == tmem + Cfg::kQCol ? q + 64 : tmem + Cfg::kQCol;
     }
     if (!keys.wait(ctl, kSiteMmaStage)) break;
     keys.advance();
-    if (t >= 2) {  // S[t % 2] was last read by PV(t - 2)
+    if (t >= 3) {  // S[t % 3] was last read by PV(t - 3)
       if (!done.wait(ctl, kSiteMmaPvDone)) break;
       done.advance();
     }
     tc_fence_after();
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-      tc_mma_ts_lh(tmem + s, q + kk * 8, md.k0 + k + (((kk >> 2) * Cfg::kHalfB + (kk & 3) * 32) >> 4),
-                   md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t off = ((kk >> 2) * Cfg::kHalfB + (kk & 3) * 32) >> 4;
+      tc_mma_ss_lh(tmem + s, md.q0 + off, md.hi, md.k0 + k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
+    }
     tc_commit(bar(Cfg::kSF) + s / 16);
-    s ^= 128;
+    s = s == 256 ? 0 : s + 128;
     k ^= Cfg::kTileB >> 4;
   }
   tc_commit(bar(Cfg::kDrain));
@@ -275,7 +275,7 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const TileDescs<D> md(sbase);
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
-  RingBar<2> weights(bar(Cfg::kPF));
+  RingBar<3> weights(bar(Cfg::kPF));
   RingBar<2> values(bar(Cfg::kVF));
   uint32_t ps = 0, v = 0;  // columns of the S buffer, offset of the V tile
   for (;;) {
@@ -297,7 +297,7 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
       tc_mma_ts_lh(tmem + Cfg::kOCol, tmem + ps + kk * 8, md.v0 + v + ((kk * 16 * 128) >> 4), md.hi,
                    Cfg::kIdescPV, kk == 0 && first ? 0u : 1u);
     tc_commit(bar(Cfg::kPVD) + ps / 16);
-    ps ^= 128;
+    ps = ps == 256 ? 0 : ps + 128;
     v ^= Cfg::kTileB >> 4;
   }
   tc_commit(bar(Cfg::kDrain + 1));
@@ -322,8 +322,8 @@ __device__ __forceinline__ uint4 load16_if(const void* ptr, bool on) {
 
 // One side (V: values, else keys and the queries); 128 threads.  One piece of code for both.
 template <class A, class C, int D>
-__device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, uint32_t tmem,
-                                             const bool V, volatile int* ctl) {
+__device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const bool V,
+                                             volatile int* ctl) {
   using Cfg = TileCfg<D>;
   constexpr int RPP = 128 * 16 / D;   // rows of a pass of the 128 threads, 16 numbers each
   constexpr int NP = 128 / RPP;       // passes of a tile
@@ -355,10 +355,10 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
       x[i] = load16_if(cache + off[i], off[i] >= 0 && key >= lo && key <= last);
     }
   };
-  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K (and for
-  // the queries of the item before the last), PV(t - 2) for V.
+  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K, PV(t - 2)
+  // for V, and S(t - 1) for an item's queries.
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
-  RingBar<2> free2(bar(V ? Cfg::kPVD : Cfg::kSF));
+  RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF)), free1(bar(Cfg::kSF));
   int tile = V ? Cfg::kOffV : Cfg::kOffK;
   int item = -1, flags = 0;
   auto step = [&]() -> const TileStep& {
@@ -372,9 +372,12 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         if (!__all_sync(0xffffffffu, free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty))) break;
         free2.advance();
       }
+      if (!V && t >= 1) {
+        if ((flags & kStageFirst) && !__all_sync(0xffffffffu, free1.wait(ctl, kSiteProdKEmpty))) break;
+        free1.advance();
+      }
       if (!V && (flags & kStageFirst)) {
         ++item;
-        tc_fence_after();
         // Row tid of the tile: query and head, scaled into fp16's range.
         const CacheSeg& s = st.seg;
         const int qi = static_cast<int>((tid * p.group_inv) >> 16);
@@ -401,32 +404,26 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
           up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
           back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
         }
-        // Row = TMEM lane; two numbers a column, as the product takes its first operand.
-        const uint32_t dst = tmem + (static_cast<uint32_t>(warp * 32) << 16) + Cfg::kQCol + 64 * (item & 1);
-#pragma unroll 1
-        for (int c = 0; c < D / 64; ++c) {
-          uint32_t w[32];
+        uint8_t* row = smem + Cfg::kOffQ + tid * 128;
+#pragma unroll 4
+        for (int c = 0; c < D / 8; ++c) {
+          uint4 y = make_uint4(0, 0, 0, 0);
+          if (live) {
+            y = *reinterpret_cast<const uint4*>(q + 8 * c);
+            if constexpr (!std::is_same<A, __half>::value) {
+              uint32_t w[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (live) y = *reinterpret_cast<const uint4*>(q + c * 64 + 8 * i);
-            w[4 * i] = y.x;
-            w[4 * i + 1] = y.y;
-            w[4 * i + 2] = y.z;
-            w[4 * i + 3] = y.w;
-          }
-          if constexpr (!std::is_same<A, __half>::value) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float2 f = act_to_float2<A>(w[i]);
-              w[i] = float2_to_act<__half>(f.x * up, f.y * up);
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = act_to_float2<A>(w[i]);
+                w[i] = float2_to_act<__half>(f.x * up, f.y * up);
+              }
+              y = make_uint4(w[0], w[1], w[2], w[3]);
             }
           }
-          tmem_st_32x32b_x32(dst + 32 * c, w);
+          *reinterpret_cast<uint4*>(row + (c >> 3) * Cfg::kHalfB + (((c & 7) ^ (tid & 7)) << 4)) = y;
         }
         reinterpret_cast<float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + tid] = back;
-        tmem_st_wait();
-        tc_fence_before();
+        fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Cfg::kQF + item % Cfg::kItems));
       }
@@ -568,7 +565,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   bool pending = false;
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
-  RingBar<2> scores(bar(Cfg::kSF)), before(bar(Cfg::kPVD));  // S(t), PV(t - 1)
+  RingBar<3> scores(bar(Cfg::kSF)), before(bar(Cfg::kPVD));  // S(t), PV(t - 1)
   uint32_t ts = tl;  // the step's S buffer
   for (int t = 0;; ++t) {
     if (!wait_ring(info, kSiteCacheInfo)) break;
@@ -598,7 +595,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     // twice: the maximum, then the weights.  Scores that have to be changed first (soft-cap,
     // masks) are written back by the first pass, so that the second is the same for all.
     float mx = -INFINITY;
-#pragma unroll 1
+#pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t x[32];
       tmem_ld_16x32bx2_x32<32>(ts + 64 * h, x);
@@ -695,7 +692,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     info.advance();
     if (t > 0) before.advance();
-    ts = ts == tl ? tl + 128 : tl;
+    ts = ts == tl + 256 ? tl : ts + 128;
   }
 }
 
@@ -716,10 +713,12 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
   const CacheUnits units{p, 31 - __clz(static_cast<int>((128u * p.group_inv) >> 16)), 6, 2};
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < 3; ++i) {
       mbar_init(bar(Cfg::kSF + i), 1);
       mbar_init(bar(Cfg::kPVD + i), 1);
       mbar_init(bar(Cfg::kPF + i), 8);
+    }
+    for (int i = 0; i < 2; ++i) {
       mbar_init(bar(Cfg::kKF + i), 4);
       mbar_init(bar(Cfg::kVF + i), 4);
       mbar_init(bar(Cfg::kDrain + i), 1);
@@ -756,7 +755,7 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
   } else if (warp < 12) {
     tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 1, ctl);
   } else {
-    tile_convert<A, C, D>(p, smem, tmem, warp >= 16, ctl);
+    tile_convert<A, C, D>(p, smem, warp >= 16, ctl);
   }
   tc_fence_before();
   __syncthreads();

@@ -136,11 +136,11 @@ __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, con
 
 // A bounded wait in a dozen instructions, for kernels whose roles together have to fit the
 // instruction cache.  The bound is a count of tries: each suspends the thread for as long as
-// the hardware likes (up to the microsecond asked for), so 2^24 of them take between half a
-// second and about twenty.  A wait that runs out leaves kStatusTimeout | site in the CTA's
-// abort word; every other wait of the CTA then ends too.
+// the hardware likes (up to the microsecond asked for), so 2^24 of them take between a third of
+// a second and about twenty.  A wait that runs out leaves kStatusTimeout | site in the CTA's
+// word; the other waits of the CTA run out after it.
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity,
-                                                volatile int* abort_word, int site) {
+                                                volatile int* timeout_word, int site) {
   if (mbar_test_wait(bar, parity)) return true;  // half the latency, where it holds already
 #pragma unroll 1
   for (int i = 0; i < (1 << 24); ++i) {
@@ -153,9 +153,8 @@ __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity,
         : "r"(bar), "r"(parity)
         : "memory");
     if (ok) return true;
-    if (*abort_word != 0) return false;
   }
-  *abort_word = kStatusTimeout | site;
+  *timeout_word = kStatusTimeout | site;
   return false;
 }
 
