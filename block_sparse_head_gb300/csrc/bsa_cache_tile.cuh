@@ -38,17 +38,17 @@ template <int D>
 struct TileCfg {
   static constexpr int kThreads = 640;
   static constexpr int kRows = 128;
-  static constexpr int kTileB = 128 * D * 2;   // one fp16 tile of K or V
+  static constexpr int kTileB = 128 * D * 2;   // one fp16 tile of Q, K or V
   static constexpr int kHalfB = 128 * 128;     // its 64-column halves, [128][64] swizzled
   static constexpr int kInfo = 8;              // steps looked up ahead
   static constexpr int kItems = 8;             // items whose row factors are kept
   static constexpr int kOffQ = 0;
-  static constexpr int kOffK = kOffQ + kTileB;
+  static constexpr int kOffK = kOffQ + 2 * kTileB;
   static constexpr int kOffV = kOffK + 2 * kTileB;
   static constexpr int kOffFactor = kOffV + 2 * kTileB;          // [kItems][128] fp32
   static constexpr int kOffSegs = kOffFactor + kItems * 128 * 4; // the producer's segments
   static constexpr int kOffInfo = kOffSegs + 4 * 64;
-  static constexpr int kInfoB = 240;
+  static constexpr int kInfoB = 256;
   static constexpr int kOffBar = kOffInfo + kInfo * kInfoB;
   // barriers
   static constexpr int kSF = 0;                 // [3] S(t) computed
@@ -80,12 +80,13 @@ struct TileStep {
   CacheSeg seg;   // of every step (13 words)
   int flags;      // DecodeFlags
   int key0[2];    // first key of each piece (kNoKeys: none)
-  int64_t off[8]; // per 16 keys: where they start in the cache (bytes), -1: not there
+  int64_t off[8]; // per 16 keys: where they start in the cache (bytes; 0: not there)
+  int cut;        // bits 0-7: groups that are there; bit 8: some keys of those are not seen
   float ks[8];    // per 16 keys: scale of the scores (1 where the keys are not there)
   float lv[8];    // log2 of the value scale (-inf where the keys are not there)
   float rv[8];    // its reciprocal (0 where the keys are not there)
 };
-static_assert(sizeof(TileStep) <= 240, "step slots");
+static_assert(sizeof(TileStep) <= 256, "step slots");
 
 // A barrier of a ring of N: its address and the parity of the phase to wait for (or to fill)
 // next.
@@ -183,11 +184,12 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
       if (!__all_sync(0xffffffffu, ok)) break;
       const int slot = (t + i) % Cfg::kInfo;
       TileStep& st = *reinterpret_cast<TileStep*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+      const bool on = cur.tile >= 0 && !end;
+      const uint32_t there = __ballot_sync(0xffffffffu, on);
       if (i < n) {
-        const bool on = cur.tile >= 0 && !end;
         const float lv = log2_scale(cur.vs);
         const int row = (cur.key + 16 * (j & 3)) & ((1 << p.page_shift) - 1);
-        st.off[j] = on ? ((static_cast<int64_t>(cur.tile) << p.page_shift) + row) * D : -1;
+        st.off[j] = on ? ((static_cast<int64_t>(cur.tile) << p.page_shift) + row) * D : 0;
         st.ks[j] = on ? cur.ks : 1.f;
         st.lv[j] = on ? lv : -INFINITY;
         st.rv[j] = on ? ex2_approx(-lv) : 0.f;
@@ -195,7 +197,12 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
         if (j == 0)
           st.flags = end ? kStageEnd
                          : (cur.s + i == 0 ? kStageFirst : 0) | (cur.s + i + 1 == cur.steps ? kStageLast : 0);
-        const int* from = reinterpret_cast<const int*>(&seg_at(cur.seg));
+        const CacheSeg& seg = seg_at(cur.seg);
+        // Lanes 0 and 4 have the two pieces' first keys.
+        const int lo = cur.key - seg.lo_key, hi = seg.pos0 + seg.nq - 64 - cur.key;
+        const uint32_t part = __ballot_sync(0xffffffffu >> (32 - 8 * n), (j & 3) == 0 && (lo < 0 || hi < 0));
+        if (j == 0) st.cut = (there >> (8 * i) & 255) | (part >> (8 * i) & 255 ? 256 : 0);
+        const int* from = reinterpret_cast<const int*>(&seg);
         for (int w = j; w < static_cast<int>(sizeof(CacheSeg) / 4); w += 8)
           reinterpret_cast<int*>(&st.seg)[w] = from[w];
       }
@@ -236,7 +243,7 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
   RingBar<2> keys(bar(Cfg::kKF));
   RingBar<3> done(bar(Cfg::kPVD));
-  uint32_t s = 0, k = 0;  // columns of the S buffer, offset of the K tile
+  uint32_t s = 0, k = 0, q = Cfg::kTileB >> 4;  // S buffer's columns, offsets of the K, Q tile
   for (int t = 0;; ++t) {
     if (!info.wait(ctl, kSiteCacheInfo)) break;
     const int flags =
@@ -247,6 +254,7 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
     if (flags & kStageFirst) {
       if (!queries.wait(ctl, kSiteMmaStage)) break;
       queries.advance();
+      q ^= Cfg::kTileB >> 4;
     }
     if (!keys.wait(ctl, kSiteMmaStage)) break;
     keys.advance();
@@ -258,7 +266,7 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk) {
       const uint32_t off = ((kk >> 2) * Cfg::kHalfB + (kk & 3) * 32) >> 4;
-      tc_mma_ss_lh(tmem + s, md.q0 + off, md.hi, md.k0 + k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
+      tc_mma_ss_lh(tmem + s, md.q0 + q + off, md.hi, md.k0 + k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
     }
     tc_commit(bar(Cfg::kSF) + s / 16);
     s = s == 256 ? 0 : s + 128;
@@ -306,17 +314,12 @@ __device__ __forceinline__ void tile_mma_pv(uint8_t* smem, uint32_t tmem, volati
 
 // -------------------------------------------------------------------- converters
 
-// 16 bytes, or zeros: a predicated load (as a branch, each of a thread's loads would wait
-// for the address of the one before).
-__device__ __forceinline__ uint4 load16_if(const void* ptr, bool on) {
+// A load that stays where it is written: ahead of the waits that follow it.
+__device__ __forceinline__ uint4 load16(const void* ptr) {
   uint4 x;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %5, 0;\n\t"
-      "mov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
-      "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
-      : "=&r"(x.x), "=&r"(x.y), "=&r"(x.z), "=&r"(x.w)
-      : "l"(ptr), "r"(static_cast<int>(on)));
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+               : "l"(ptr));
   return x;
 }
 
@@ -344,21 +347,26 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   // A step's stored numbers into registers; what no query of the tile sees is zero (the cache
   // may hold anything there).
   auto load = [&](const TileStep& st) {
-    const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
-    const int k0 = st.key0[0] + r0, k1 = st.key0[1] + r0;
     int64_t off[NP];
 #pragma unroll
     for (int i = 0; i < NP; ++i) off[i] = st.off[(i * RPP + r0) >> 4];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const int key = (i < NP / 2 ? k0 : k1) + (i * RPP & 63);
-      x[i] = load16_if(cache + off[i], off[i] >= 0 && key >= lo && key <= last);
+    for (int i = 0; i < NP; ++i) x[i] = load16(cache + off[i]);
+    const int cut = st.cut;
+    if (cut != 255) {
+      const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
+      const int k0 = st.key0[0] + r0, k1 = st.key0[1] + r0;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int key = (i < NP / 2 ? k0 : k1) + (i * RPP & 63);
+        if (!(cut >> ((i * RPP + r0) >> 4) & 1) || key < lo || key > last) x[i] = make_uint4(0, 0, 0, 0);
+      }
     }
   };
-  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K, PV(t - 2)
-  // for V, and S(t - 1) for an item's queries.
+  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K (and for
+  // the queries of the item before the last), PV(t - 2) for V.
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
-  RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF)), free1(bar(Cfg::kSF));
+  RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF));
   int tile = V ? Cfg::kOffV : Cfg::kOffK;
   int item = -1, flags = 0;
   auto step = [&]() -> const TileStep& {
@@ -371,10 +379,6 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
       if (t >= 2) {
         if (!__all_sync(0xffffffffu, free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty))) break;
         free2.advance();
-      }
-      if (!V && t >= 1) {
-        if ((flags & kStageFirst) && !__all_sync(0xffffffffu, free1.wait(ctl, kSiteProdKEmpty))) break;
-        free1.advance();
       }
       if (!V && (flags & kStageFirst)) {
         ++item;
@@ -404,7 +408,7 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
           up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
           back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
         }
-        uint8_t* row = smem + Cfg::kOffQ + tid * 128;
+        uint8_t* row = smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB + tid * 128;
 #pragma unroll 4
         for (int c = 0; c < D / 8; ++c) {
           uint4 y = make_uint4(0, 0, 0, 0);
@@ -710,7 +714,10 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
   int* err = reinterpret_cast<int*>(tmem_slot + 1);  // abort word, join flag
   volatile int* const ctl = err;
   const CacheParts parts = cache_parts(workspace, gridDim.x, Cfg::kRows, D);
-  const CacheUnits units{p, 31 - __clz(static_cast<int>((128u * p.group_inv) >> 16)), 6, 2};
+  // Queries of a tile: as many as fill its rows, and of one layout row.
+  int tq_shift = 31 - __clz(static_cast<int>((128u * p.group_inv) >> 16));
+  if (p.row_ptr != nullptr) tq_shift = min(tq_shift, p.block_shift);
+  const CacheUnits units{p, tq_shift, 6, 2};
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
     for (int i = 0; i < 3; ++i) {

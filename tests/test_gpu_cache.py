@@ -322,6 +322,15 @@ def test_layout(news, page, block):
     c.check(layout=layout, block=block, window=150, softcap=10.0, sinks=torch.randn(6, device="cuda"))
 
 
+@pytest.mark.parametrize("block", [64, 128])
+def test_layout_rows_inside_a_tile(block):
+    """One query head a kv head: 128 rows would reach over two layout rows of 64 queries."""
+    c = Case([500, 333], [300, 130], 1, 2, page=64, seed=block)
+    nb = -(-c.table.shape[1] * 64 // block)
+    layout = (np.random.default_rng(2).random((2, nb, nb)) < 0.5).astype(np.int32)
+    c.check(layout=layout, block=block)
+
+
 def test_layout_above_the_diagonal_is_not_seen():
     """A full layout is the dense call: keys after the query are not attended."""
     c = Case([333, 70], [40, 1], 2, 2, seed=3)
