@@ -416,12 +416,15 @@ def _rows_ptr(t, name: str, heads: int | None, d: int, dev: int):
     return t.data_ptr(), token if t.shape[0] > 1 else 0, head if t.shape[1] > 1 else 0
 
 
+_HERE_AND_NOW = contextlib.nullcontext()
+
+
 def _on(stream):
     """Context in which a call allocates what the caller did not give it: memory of the
     stream that the call runs on, so that neither earlier nor later work of the current
     stream touches it meanwhile."""
     if stream is None:
-        return contextlib.nullcontext()
+        return _HERE_AND_NOW
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream))
     return torch.cuda.stream(stream)
@@ -556,7 +559,7 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
             if workspace is None:
                 workspace = cache_workspace(heads, kv_heads, d, max_q)
     args = None
-    if window is not None or softcap or sinks is not None or lut is not None:
+    if (window is not None and window >= 0) or softcap or sinks is not None or lut is not None:
         args = _CACHE_ARGS.pack(-1 if window is None else max(-1, int(window)), float(softcap),
                                 0 if sinks is None else _dev_ptr(sinks, "sinks", f32, (heads,), dev),
                                 0 if lut is None else lut.handle.value,
