@@ -560,7 +560,7 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                 workspace = cache_workspace(heads, kv_heads, d, max_q)
     args = None
     if (window is not None and window >= 0) or softcap or sinks is not None or lut is not None:
-        args = _CACHE_ARGS.pack(-1 if window is None else max(-1, int(window)), float(softcap),
+        args = _CACHE_ARGS.pack(-1 if window is None else min(max(-1, int(window)), 2 ** 31 - 1), float(softcap),
                                 0 if sinks is None else _dev_ptr(sinks, "sinks", f32, (heads,), dev),
                                 0 if lut is None else lut.handle.value,
                                 0 if block is None else int(block))

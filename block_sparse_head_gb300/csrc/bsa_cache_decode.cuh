@@ -143,7 +143,7 @@ struct DecodeBox {
   float ks, lv;
   int pad;
 };
-constexpr int kNoKeys = 1 << 30;  // past every position, so that the masks cover it
+constexpr int kNoKeys = kMaxPositions;  // past every position, so that the masks cover it
 
 enum DecodeFlags { kStageFirst = 1, kStageLast = 2, kStageEnd = 4 };
 

@@ -2,6 +2,7 @@
 // See include/bsa.h for the contract of every exported function.
 #include "../../include/bsa.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdint>
 #include <limits>
@@ -161,9 +162,10 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
       workspace == nullptr || (T > 0 && (q == nullptr || out == nullptr || lse == nullptr)))
     return BSA_ERR_NULL;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_DTYPE;
-  if (B < 1 || T < 0 || max_pages < 1 || max_q < 1 ||
+  if (B < 1 || T < 0 || T > bsa::kMaxPositions || max_pages < 1 || max_q < 1 ||
       check_heads(heads, cache->kv_heads) != BSA_OK ||
-      static_cast<int64_t>(max_pages) * cache->page > kInt32Max)
+      static_cast<int64_t>(max_pages) * cache->page > bsa::kMaxPositions ||
+      static_cast<int64_t>(B) * cache->kv_heads > kInt32Max)
     return BSA_ERR_SHAPE;
   if (!std::isfinite(scale) || !std::isfinite(x.softcap) || x.softcap < 0.f)
     return BSA_ERR_UNSUPPORTED;
@@ -217,7 +219,7 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   p.group_inv = (65536u + p.group - 1) / p.group;
   p.n_pages = cache->n_pages;
   p.max_pages = max_pages;
-  p.window = x.window < 0 ? -1 : x.window;
+  p.window = x.window < 0 ? -1 : std::min(x.window, bsa::kMaxPositions);
   p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   if (x.softcap > 0.f) {
     p.softcap_log2 = static_cast<float>(static_cast<double>(x.softcap) * 1.4426950408889634);

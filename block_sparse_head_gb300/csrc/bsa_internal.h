@@ -269,6 +269,10 @@ inline int64_t cache_parts_bytes(int grid, int rows, int d) {
          static_cast<int64_t>(grid) * 2 * (static_cast<int64_t>(rows) * d * 4 + rows * 8);
 }
 
+// Positions, queries and windows of the attention over a cache stay below this, so that sums
+// and differences of three of them fit 32 bits.
+constexpr int kMaxPositions = 1 << 29;
+
 // Few query rows (group * max_q <= kDecodeRows): the decode kernels, split over the keys.
 constexpr int kDecodeRows = 16;
 #define BSA_DECODE_LAUNCH(name)                                                              \

@@ -458,8 +458,11 @@ typedef struct bsa_cache_args {
  *   out    = sum_{c in A(r)} exp(s_c - lse) * v_scale[page(c)][g] * v8_c    (0 when empty)
  *
  * A query whose position is negative (more queries than tokens) sees no key.  kv_len is
- * taken as at most max_pages * page.  V scales count as lying in [2^-60, 2^60], which those
- * of bsa_cache_append do.  What the cache holds behind a request's length is not used.
+ * taken as at most max_pages * page, which, like T, is at most 2^29; B * kv_heads is below
+ * 2^31.  V scales count as lying in [2^-60, 2^60], which those of bsa_cache_append do; K
+ * scales are positive.  What the cache holds behind a request's length is not used.  A NaN
+ * stored among a request's values may reach the outputs of all queries that the call has for
+ * it, also of those that do not see it; one among its keys reaches only those that do.
  *
  *   q         device, dtype BSA_BF16 or BSA_FP16, [T, heads, d] with strides as in
  *             bsa_cache_append, 16-byte aligned.

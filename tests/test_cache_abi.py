@@ -98,6 +98,8 @@ def test_forward(lib):
     assert f(qt=1020) == -5 and f(qh=4) == -5
     assert f(dtype=3) == -4
     assert f(B=0) == -2 and f(T=-1) == -2 and f(max_pages=0) == -2 and f(max_q=0) == -2
+    assert f(max_pages=(1 << 23) + 1) == -2 and f(T=(1 << 29) + 1) == -2    # positions past 2^29
+    assert f(B=1 << 30, kv_heads=4) == -2
     assert f(heads=7) == -2 and f(heads=0) == -2 and f(heads=258) == -2 and f(max_pages=1 << 25) == -2
     assert f(scale=float("nan")) == -6 and f(softcap=-1.0) == -6 and f(softcap=float("inf")) == -6
     assert f(lut=lut.handle, block=32) == -6

@@ -358,6 +358,79 @@ def test_more_queries_than_tokens(news):
     c.check(sinks=torch.randn(8, device="cuda"))
 
 
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 40])
+@pytest.mark.parametrize("news", [[3, 1, 2], [70, 1, 20]])
+def test_window_wider_than_anything(news, window):
+    """The widest window masks nothing, negative positions included."""
+    c = Case([2, 500, 0], news, 4, 2, seed=26)
+    a, b = c.run(), c.run(window=window)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    c.check(window=window)
+
+
+@pytest.mark.parametrize("news", [[1, 1], [1, 60]])
+def test_nan_in_places_that_are_masked(news):
+    """NaN keys and values before the window, of one request's single query; NaN keys that a
+    query does not see yet."""
+    c = Case([300, 200], news, 4, 2, page=16, seed=27)
+    nan = torch.full((128,), 0x7F, dtype=torch.uint8, device="cuda")
+    for pos in (0, 17, 200):
+        for x in (c.kc, c.vc):
+            x.view(torch.uint8)[c.table[0, pos // 16], :, pos % 16] = nan
+    if news[1] > 1:  # keys of the newest token: seen by the last query alone
+        c.kc.view(torch.uint8)[c.table[1, 199 // 16], :, 199 % 16] = nan
+        out, lse = c.run(window=50)
+        n = int(c.cu[-1])
+        assert torch.all(torch.isnan(lse[n - 1])) and torch.all(torch.isfinite(lse[: n - 1]))
+        assert torch.all(torch.isfinite(out[: n - 1]))
+    else:
+        c.check(window=50)
+
+
+def test_zero_requests_queries_and_tokens():
+    """No packed tokens at all, and requests none of which has a query."""
+    c = Case([50, 20], [1, 0], 4, 2, seed=28)
+    for T, cu in ((0, [0, 0, 0]), (3, [0, 0, 0]), (3, [1, 1, 1])):
+        q = c.q[:1].repeat(max(T, 1), 1, 1)[:T]
+        out, lse = torch.full_like(q, 5.0), torch.full((T, 8), 5.0, device="cuda")
+        for max_q in (1, 40):
+            _, _, status = bsa.cache_forward(q, c.kc, c.vc, c.ks, c.vs, ints(c.table), ints(c.lens), ints(cu), 0.1,
+                                             max_q=max_q, out=out, lse=lse)
+            assert int(status[0]) == 0 and torch.all(out == 5) and torch.all(lse == 5)
+        bsa.cache_append(q[:, :2], q[:, :2], ints([-1] * T), c.kc.view(torch.float8_e4m3fn), c.vc, c.ks, c.vs)
+
+
+def test_calls_side_by_side():
+    """Calls of both kinds on two streams at once, each with a workspace of its own."""
+    cs = [Case([9000, 300], [1, 1], 4, 2, seed=29), Case([2000, 900], [300, 50], 4, 2, seed=30)]
+    refs = [c.run() for c in cs]
+    args = [[ints(c.table), ints(c.lens), ints(c.cu)] for c in cs]
+    ws = [bsa.cache_workspace(8, 2, 128, max(c.news)) for c in cs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[], []]
+    for _ in range(10):
+        for i, c in enumerate(cs):
+            with torch.cuda.stream(streams[i]):
+                outs[i].append(bsa.cache_forward(c.q, c.kc, c.vc, c.ks, c.vs, *args[i], 1 / math.sqrt(c.d),
+                                                 max_q=max(c.news), workspace=ws[i]))
+    torch.cuda.synchronize()
+    for i, c in enumerate(cs):
+        n = int(c.cu[-1])
+        for out, lse, status in outs[i]:
+            assert int(status[0]) == 0
+            assert torch.equal(out[:n], refs[i][0][:n]) and torch.equal(lse[:n], refs[i][1][:n])
+
+
+def test_one_workspace_for_all_shapes():
+    """A workspace made for the largest call serves smaller ones of other head counts."""
+    ws = bsa.cache_workspace(32, 1, 128, 1000)
+    for G, H, d, news in ((4, 2, 128, [1, 1]), (8, 1, 64, [2, 1]), (1, 3, 128, [1, 200]), (32, 1, 64, [1, 1])):
+        c = Case([6000, 5000], news, G, H, d, 64, seed=G)
+        ref, got = c.run(), c.run(workspace=ws)
+        assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
 def test_length_past_the_table():
     """kv_len counts as at most max_pages * page."""
     c = Case([128, 64], [1, 5], 2, 1, seed=8)
