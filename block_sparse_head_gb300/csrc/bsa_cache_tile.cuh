@@ -6,25 +6,38 @@
 // exact; e4m3 operands (kind::f8f6f4) would need the queries and the weights rounded to 8
 // bits, and int8 has no such kind.  A step is 128 keys, two pieces of 64 from anywhere in the
 // cache; work is split on the device (bsa_cache_sched.cuh), one persistent CTA per SM:
-//   warp 0      S issuer (one thread): S(t) = Q K(t)^T into one of three TMEM buffers.
+//   warp 0      S issuer (one thread): S(t) = Q K(t)^T into one of three TMEM buffers, which
+//               lets it run ahead of the softmax.
 //   warp 1      PV issuer: O += P(t) V(t), P read from the S buffer it was written over.
-//   warp 2      looks pages and scales up, a batch of four steps ahead (ring of 8 steps).
-//   warp 3      brings the stored numbers in by TMA, 64 keys of one side a place.
-//   softmax     warps 4-11.  Lanes t and t + 16 hold the two halves of a row's piece.  The K scale
-//               of a page belongs to 16 keys at least, so it is folded into the exponent's
-//               multiplier per group of 16, and log2 of the V scale into its addend, as in
-//               the decode kernel: w = exp2(s + log2 vs - m), the sum takes w / vs, weights
-//               are rounded to fp16 relative to the largest (2^-11).  An item's O is read out
-//               at the next item's first step.
+//   warp 2      looks pages and scales up, a batch of four steps at a time, up to eight steps
+//               ahead, while the numbers of the steps before are on their way.
+//   warp 3      idle: the roles after it have to begin at a warpgroup.
+//   softmax     warps 4-11, 64 scores a thread: lanes t and t + 16 hold the two halves of each
+//               piece of a row.  The K scale of a page belongs to 16 keys at least, so it is
+//               folded into the exponent's multiplier per group of 16, and log2 of the V scale
+//               into its addend, as in the decode kernel: w = exp2(s + log2 vs - m), the sum
+//               takes w / vs, weights are rounded to fp16 relative to the largest (2^-11).  An
+//               item's O is read out at the next item's first step.
 //   converters  warps 12-15 for K (and the queries, bf16 ones scaled per row by a power of two
-//               into fp16's range), 16-19 for V: stored numbers to fp16 tiles in the
-//               128-byte-swizzled layout that the products read.  A lane's pieces are chosen so
-//               that neither its reads nor its writes meet another's banks.
-// Shared memory holds a tile of Q and two each of K and V in fp16 (160 KB), and seven places of
-// stored numbers (56 KB): a step writes 64 KB of fp16 into it and the products read 96 KB of
-// it, which bounds a step at about 1,280 cycles against the 1,024 of its products.  The loops
-// are rolled up where they can be: all roles' code has to fit the instruction cache, whose
-// misses were the first version's largest stall.
+//               into fp16's range), 16-19 for V: stored numbers, loaded into registers a step
+//               ahead, to fp16 tiles in the 128-byte-swizzled layout that the products read.  A
+//               lane's pieces are chosen so that its writes meet no other's banks.
+// Shared memory holds two tiles each of Q, K and V in fp16 (192 KB): a step writes 64 KB of
+// fp16 into it and the products read 96 KB of it, which bounds a step at about 1,280 cycles
+// against the 1,024 of its products.
+//
+// Measured, 2,048 queries on 16,384 tokens, 32 query and 8 kv heads, d = 128, e4m3: 539 us,
+// 955 TFLOP/s, 0.50 of a cuBLAS bf16 product.  A step takes about 2,500 cycles: the softmax
+// warps' chain of waits, TMEM loads, maxima, exponentials and conversions is the limit (without
+// the conversion of the cache it is 12 % less, without the exponentials 5 %, with an eighth of
+// the products 3 %).  What counted on the way there, at these sizes: the raw bytes by TMA into
+// shared memory and the conversion from there (664 us) against loads into registers; two S
+// buffers instead of three (606); scores read from TMEM twice with 32 at a time in registers,
+// where all threads have 96 registers (592), against once with the register split below (577);
+// causal and window masks decided by the look-ups, once a step, instead of by votes (554);
+// requesting the next step's numbers before the fence that publishes this one's (531).  A few
+// registers spilled in these loops cost a quarter of the speed, and unrolling more of them
+// costs as much in instruction fetches: the roles' loops together just fit that cache.
 //
 // Every wait is bounded: one that runs out records a timeout, and all roles leave
 // their loops, let the products in flight finish, free TMEM and return.
@@ -38,6 +51,9 @@ template <int D>
 struct TileCfg {
   static constexpr int kThreads = 640;
   static constexpr int kRows = 128;
+  // Registers a thread: of the launch, then of warps 0-3, the softmax and the converter warps.
+  static constexpr int kRegs = 96, kRegCtl = 64, kRegSoft = 120, kRegConv = 88;
+  static_assert(128 * kRegCtl + 256 * (kRegSoft + kRegConv) <= kThreads * kRegs, "register split");
   static constexpr int kTileB = 128 * D * 2;   // one fp16 tile of Q, K or V
   static constexpr int kHalfB = 128 * 128;     // its 64-column halves, [128][64] swizzled
   static constexpr int kInfo = 8;              // steps looked up ahead
@@ -75,16 +91,20 @@ struct TileCfg {
   static constexpr uint32_t kIdescPV = kIdesc | 1u << 16 | (D / 8u) << 17 | (128u / 16) << 24;
 };
 
+constexpr int kStepMask = 8;  // beside DecodeFlags: some query of the tile does not see all keys
+
 // What the roles need to know of a step.
-struct TileStep {
-  CacheSeg seg;   // of every step (13 words)
-  int flags;      // DecodeFlags
-  int key0[2];    // first key of each piece (kNoKeys: none)
-  int64_t off[8]; // per 16 keys: where they start in the cache (bytes; 0: not there)
-  int cut;        // bits 0-7: groups that are there; bit 8: some keys of those are not seen
-  float ks[8];    // per 16 keys: scale of the scores (1 where the keys are not there)
-  float lv[8];    // log2 of the value scale (-inf where the keys are not there)
-  float rv[8];    // its reciprocal (0 where the keys are not there)
+struct alignas(16) TileStep {
+  int flags;        // DecodeFlags, kStepMask
+  int cut;          // bits 0-7: groups of 16 keys that are there; bit 8: of those, some keys unseen
+  int key0[2];      // first key of each piece (kNoKeys: none)
+  uint32_t off[8];  // per group: where it starts in the cache (in 16 rows; 0 where it is not there)
+  struct {
+    float ks[2];    // scales of the scores (1 where the keys are not there)
+    float lv[2];    // log2 of the value scales (-inf where the keys are not there)
+  } f[4];           // of two groups each
+  float rv[8];      // reciprocals of the value scales (0 where the keys are not there)
+  CacheSeg seg;     // of every step (13 words)
 };
 static_assert(sizeof(TileStep) <= 256, "step slots");
 
@@ -189,19 +209,26 @@ __device__ __forceinline__ void tile_lookup(const CacheFwdParams& p, uint8_t* sm
       if (i < n) {
         const float lv = log2_scale(cur.vs);
         const int row = (cur.key + 16 * (j & 3)) & ((1 << p.page_shift) - 1);
-        st.off[j] = on ? ((static_cast<int64_t>(cur.tile) << p.page_shift) + row) * D : 0;
-        st.ks[j] = on ? cur.ks : 1.f;
-        st.lv[j] = on ? lv : -INFINITY;
+        st.off[j] = on ? (static_cast<uint32_t>(cur.tile) << (p.page_shift - 4)) + (row >> 4) : 0;
+        st.f[j >> 1].ks[j & 1] = on ? cur.ks : 1.f;
+        st.f[j >> 1].lv[j & 1] = on ? lv : -INFINITY;
         st.rv[j] = on ? ex2_approx(-lv) : 0.f;
         if ((j & 3) == 0) st.key0[j >> 2] = cur.key;
-        if (j == 0)
-          st.flags = end ? kStageEnd
-                         : (cur.s + i == 0 ? kStageFirst : 0) | (cur.s + i + 1 == cur.steps ? kStageLast : 0);
         const CacheSeg& seg = seg_at(cur.seg);
-        // Lanes 0 and 4 have the two pieces' first keys.
+        // Lanes 0 and 4 have the two pieces' first keys.  Of some keys: the tile's last query
+        // (or its window's first key) cuts; of some query: the first one (the last's window).
         const int lo = cur.key - seg.lo_key, hi = seg.pos0 + seg.nq - 64 - cur.key;
-        const uint32_t part = __ballot_sync(0xffffffffu >> (32 - 8 * n), (j & 3) == 0 && (lo < 0 || hi < 0));
-        if (j == 0) st.cut = (there >> (8 * i) & 255) | (part >> (8 * i) & 255 ? 256 : 0);
+        const uint32_t mine = 255u << (8 * i), active = 0xffffffffu >> (32 - 8 * n);
+        const uint32_t part = __ballot_sync(active, (j & 3) == 0 && (lo < 0 || hi < 0));
+        const bool inner = (p.window >= 0 && cur.key < seg.pos0 + seg.nq - 1 - p.window) ||
+                           cur.key > seg.pos0 - 63 || !on;
+        const uint32_t mask = __ballot_sync(active, inner);
+        if (j == 0) {
+          st.cut = (there & mine) >> (8 * i) | (part & mine ? 256 : 0);
+          st.flags = end ? kStageEnd
+                         : (cur.s + i == 0 ? kStageFirst : 0) |
+                               (cur.s + i + 1 == cur.steps ? kStageLast : 0) | (mask & mine ? kStepMask : 0);
+        }
         const int* from = reinterpret_cast<const int*>(&seg);
         for (int w = j; w < static_cast<int>(sizeof(CacheSeg) / 4); w += 8)
           reinterpret_cast<int*>(&st.seg)[w] = from[w];
@@ -347,11 +374,11 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   // A step's stored numbers into registers; what no query of the tile sees is zero (the cache
   // may hold anything there).
   auto load = [&](const TileStep& st) {
-    int64_t off[NP];
+    uint32_t off[NP];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) off[i] = st.off[(i * RPP + r0) >> 4];
+    for (int i = 0; i < NP; ++i) off[i] = st.off[RPP == 16 ? i : (i * RPP + r0) >> 4];
 #pragma unroll
-    for (int i = 0; i < NP; ++i) x[i] = load16(cache + off[i]);
+    for (int i = 0; i < NP; ++i) x[i] = load16(cache + static_cast<int64_t>(off[i]) * (16 * D));
     const int cut = st.cut;
     if (cut != 255) {
       const int lo = st.seg.lo_key, last = st.seg.pos0 + st.seg.nq - 1;
@@ -369,6 +396,7 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF));
   int tile = V ? Cfg::kOffV : Cfg::kOffK;
   int item = -1, flags = 0;
+  bool ok = true;
   auto step = [&]() -> const TileStep& {
     return *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
   };
@@ -442,19 +470,24 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
         *reinterpret_cast<uint4*>(smem + dst0 + at) = make_uint4(h[0], h[1], h[2], h[3]);
         *reinterpret_cast<uint4*>(smem + dst1 + at) = make_uint4(h[4], h[5], h[6], h[7]);
       }
+      const uint32_t release = info.bar + 8 * Cfg::kInfo;
+      info.advance();
+      ok = __all_sync(0xffffffffu, info.wait(ctl, kSiteCacheInfo));
+      flags = step().flags;
+      if (ok && !(flags & kStageEnd)) load(step());
       fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) {
         mbar_arrive(bar(V ? Cfg::kVF : Cfg::kKF) + 8 * (t & 1));
-        mbar_arrive(info.bar + 8 * Cfg::kInfo);
+        mbar_arrive(release);
       }
-      info.advance();
       tile += t & 1 ? -Cfg::kTileB : Cfg::kTileB;
+    } else {
+      ok = __all_sync(0xffffffffu, info.wait(ctl, kSiteCacheInfo));
+      flags = step().flags;
+      if (ok && !(flags & kStageEnd)) load(step());
     }
-    if (!__all_sync(0xffffffffu, info.wait(ctl, kSiteCacheInfo))) break;
-    flags = step().flags;
-    if (flags & kStageEnd) break;
-    load(step());
+    if (!ok || (flags & kStageEnd)) break;
   }
 }
 
@@ -571,11 +604,12 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
   RingBar<3> scores(bar(Cfg::kSF)), before(bar(Cfg::kPVD));  // S(t), PV(t - 1)
   uint32_t ts = tl;  // the step's S buffer
+  if (!wait_ring(info, kSiteCacheInfo)) return;
   for (int t = 0;; ++t) {
-    if (!wait_ring(info, kSiteCacheInfo)) break;
     const TileStep& st =
         *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
-    const int flags = st.flags;
+    const int4 head = *reinterpret_cast<const int4*>(&st);
+    const int flags = head.x;
     const bool first = flags & kStageFirst;
     if (flags & (kStageFirst | kStageEnd)) {
       // The previous item's O goes out before this step's P is handed over (the product that
@@ -595,42 +629,48 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     if (!wait_ring(scores, kSiteSoftSFull)) break;
     scores.advance();
-    // Piece by piece, 32 keys a thread (lane t the first of the piece, t + 16 the others), and
-    // twice: the maximum, then the weights.  Scores that have to be changed first (soft-cap,
-    // masks) are written back by the first pass, so that the second is the same for all.
+    // 32 keys of each piece a thread (lane t the first of a piece, t + 16 the others).
+    uint32_t x[2][32];
+    tmem_ld_16x32bx2_x32<32>(ts, x[0]);
+    tmem_ld_16x32bx2_x32<32>(ts + 64, x[1]);
+    float cf[4], la[4];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float4 f = *reinterpret_cast<const float4*>(&st.f[2 * h + half]);
+      cf[2 * h] = factor(f.x);
+      cf[2 * h + 1] = factor(f.y);
+      la[2 * h] = f.z;
+      la[2 * h + 1] = f.w;
+    }
+    tmem_ld_wait(x[0]);
+    tmem_ld_wait(x[1]);
     float mx = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t x[32];
-      tmem_ld_16x32bx2_x32<32>(ts + 64 * h, x);
-      const int g = 4 * h + 2 * half;
-      const float c0 = factor(st.ks[g]), c1 = factor(st.ks[g + 1]);
-      const int k = st.key0[h] + 32 * half;
-      int lo = 0, hi = min(31, qpos - k);
-      if (p.window >= 0) lo = max(lo, qpos - p.window - k);
-      const bool cut = __any_sync(0xffffffffu, lo > 0 || hi < 31);
-      tmem_ld_wait(x);
-      if (!FOLD || cut) {
+      if (!FOLD || (flags & kStepMask)) {
         // Bit i: score i is seen.
+        const int k = (h ? head.w : head.z) + 32 * half;
+        int lo = 0, hi = min(31, qpos - k);
+        if (p.window >= 0) lo = max(lo, qpos - p.window - k);
         const uint32_t seen = hi < lo ? 0u : (0xffffffffu >> (31 - (hi - lo))) << lo;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-          float y = __uint_as_float(x[i]);
+          float y = __uint_as_float(x[h][i]);
           if constexpr (!FOLD) {
-            y *= i < 16 ? c0 : c1;
+            y *= cf[2 * h + (i >> 4)];
             if (p.softcap_log2 > 0.f) y = softcap(y, p.softcap_log2);
           }
-          x[i] = __float_as_uint((seen >> i) & 1 ? y : -INFINITY);
+          x[h][i] = __float_as_uint((seen >> i) & 1 ? y : -INFINITY);
         }
-        tmem_st_16x32bx2_x32<32>(ts + 64 * h, x);
       }
       float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
       for (int i = 0; i < 16; i += 2) {
-        t0 = fmax3(t0, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-        t1 = fmax3(t1, __uint_as_float(x[16 + i]), __uint_as_float(x[17 + i]));
+        t0 = fmax3(t0, __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
+        t1 = fmax3(t1, __uint_as_float(x[h][16 + i]), __uint_as_float(x[h][17 + i]));
       }
-      mx = fmax3(mx, fmaf(t0, FOLD ? c0 : 1.f, st.lv[g]), fmaf(t1, FOLD ? c1 : 1.f, st.lv[g + 1]));
+      mx = fmax3(mx, fmaf(t0, FOLD ? cf[2 * h] : 1.f, la[2 * h]),
+                 fmaf(t1, FOLD ? cf[2 * h + 1] : 1.f, la[2 * h + 1]));
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     float alpha = 1.f;
@@ -643,22 +683,19 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     const float neg_m = m == -INFINITY ? 0.f : -m;
     float sum = 0.f;
-    tmem_st_wait();  // scores written back
-#pragma unroll 1
+#pragma unroll
     for (int h = 0; h < 2; ++h) {
-      uint32_t x[32], pk[16];
-      tmem_ld_16x32bx2_x32<32>(ts + 64 * h, x);
-      const int g = 4 * h + 2 * half;
-      const float c0 = FOLD ? factor(st.ks[g]) : 1.f, c1 = FOLD ? factor(st.ks[g + 1]) : 1.f;
-      const float a0 = st.lv[g] + neg_m, a1 = st.lv[g + 1] + neg_m;
-      tmem_ld_wait(x);
+      uint32_t pk[16];
+      const float c0 = FOLD ? cf[2 * h] : 1.f, c1 = FOLD ? cf[2 * h + 1] : 1.f;
+      const float a0 = la[2 * h] + neg_m, a1 = la[2 * h + 1] + neg_m;
       uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])),
+        const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(x[h][2 * i]), __uint_as_float(x[h][2 * i + 1])),
                                    f2_pack(c0, c0), f2_pack(a0, a0));
-        const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(x[16 + 2 * i]), __uint_as_float(x[17 + 2 * i])),
-                                   f2_pack(c1, c1), f2_pack(a1, a1));
+        const uint64_t y1 =
+            f2_fma(f2_pack(__uint_as_float(x[h][16 + 2 * i]), __uint_as_float(x[h][17 + 2 * i])),
+                   f2_pack(c1, c1), f2_pack(a1, a1));
         const uint64_t e0 = f2_pack(ex2_approx(f2_lo(y0)), ex2_approx(f2_hi(y0)));
         const uint64_t e1 = f2_pack(ex2_approx(f2_lo(y1)), ex2_approx(f2_hi(y1)));
         s0 = f2_add(s0, e0);
@@ -667,7 +704,8 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
         pk[8 + i] = float2_to_act<__half>(f2_lo(e1), f2_hi(e1));
       }
       // w / vs
-      sum = fmaf(f2_lo(s0) + f2_hi(s0), st.rv[g], fmaf(f2_lo(s1) + f2_hi(s1), st.rv[g + 1], sum));
+      const float2 rv = *reinterpret_cast<const float2*>(st.rv + 4 * h + 2 * half);
+      sum = fmaf(f2_lo(s0) + f2_hi(s0), rv.x, fmaf(f2_lo(s1) + f2_hi(s1), rv.y, sum));
       // over scores that both lanes of the row have read
       tmem_st_16x32bx2_x16<16>(ts + 32 * h, pk);
     }
@@ -686,15 +724,18 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
         tmem_st_16x32bx2_x32<32>(to + g * 64, r);
       }
     }
+    // The next step's look-ups, long there, while the weights' stores are under way.
+    const uint32_t release = info.bar + 8 * Cfg::kInfo;
+    info.advance();
+    if (!wait_ring(info, kSiteCacheInfo)) break;
     tmem_st_wait();
     // P(t) handed over, the step's look-ups no longer needed.
     tc_fence_before();
     __syncwarp();
     if (lane == 0) {
       mbar_arrive(bar(Cfg::kPF) + ((ts - tl) >> 4));
-      mbar_arrive(info.bar + 8 * Cfg::kInfo);
+      mbar_arrive(release);
     }
-    info.advance();
     if (t > 0) before.advance();
     ts = ts == tl + 256 ? tl : ts + 128;
   }
@@ -752,6 +793,7 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
   const uint32_t tmem = *tmem_slot;
 
   if (warp < 4) {
+    setmaxnreg_dec<Cfg::kRegCtl>();
     if (warp == 0) {
       if (lane == 0) tile_mma_s<D>(smem, tmem, ctl);
     } else if (warp == 1) {
@@ -760,8 +802,10 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
       tile_lookup<D>(p, smem, units, ctl);
     }
   } else if (warp < 12) {
+    setmaxnreg_inc<Cfg::kRegSoft>();
     tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 1, ctl);
   } else {
+    setmaxnreg_dec<Cfg::kRegConv>();
     tile_convert<A, C, D>(p, smem, warp >= 16, ctl);
   }
   tc_fence_before();
