@@ -75,7 +75,8 @@ struct TileCfg {
   static constexpr int kQF = 13;                // [kItems] Q of an item converted
   static constexpr int kIF = kQF + kItems;      // [kInfo] step looked up
   static constexpr int kIE = kIF + kInfo;       // [kInfo] step no longer needed
-  static constexpr int kDrain = kIE + kInfo;    // [2] S, PV issuers' last products
+  static constexpr int kQE = kIE + kInfo;       // [2] Q tile read by its item's last product
+  static constexpr int kDrain = kQE + 2;        // [2] S, PV issuers' last products
   static constexpr int kJoin = kDrain + 2;      // softmax warps
   static constexpr int kNumBars = kJoin + 1;
   static constexpr int kOffScan = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
@@ -296,6 +297,7 @@ __device__ __forceinline__ void tile_mma_s(uint8_t* smem, uint32_t tmem, volatil
       tc_mma_ss_lh(tmem + s, md.q0 + q + off, md.hi, md.k0 + k + off, md.hi, Cfg::kIdescS, kk > 0 ? 1u : 0u);
     }
     tc_commit(bar(Cfg::kSF) + s / 16);
+    if (flags & kStageLast) tc_commit(bar(Cfg::kQE) + (q ? 8 : 0));
     s = s == 256 ? 0 : s + 128;
     k ^= Cfg::kTileB >> 4;
   }
@@ -350,7 +352,57 @@ __device__ __forceinline__ uint4 load16(const void* ptr) {
   return x;
 }
 
-// One side (V: values, else keys and the queries); 128 threads.  One piece of code for both.
+// Queries of a tile into fp16, a share of the rows for each of eight warps: 16 bytes a lane, as
+// many rows at once as a warp holds, a few loads in flight.
+template <class A, int D>
+__device__ __forceinline__ void tile_queries(const CacheFwdParams& p, const CacheSeg& s, uint8_t* tile,
+                                             float* factor, int warp, int lane) {
+  constexpr int L = D / 8, RPI = 32 / L;  // lanes of a row, rows at once
+  constexpr int N = 4;
+  const int c = lane % L, rows = s.nq * p.group;
+  const A* const q = static_cast<const A*>(p.q) + static_cast<int64_t>(s.q0) * p.q_token_stride +
+                     static_cast<int64_t>(s.h) * p.group * p.q_head_stride + 8 * c;
+  tile += (c >> 3) * TileCfg<D>::kHalfB;
+#pragma unroll 1
+  for (int i = 0; i < 16; i += N * RPI) {
+    const int first = warp * 16 + i + lane / L;
+    uint4 x[N];
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int r = first + u * RPI, qi = static_cast<int>((r * p.group_inv) >> 16);
+      x[u] = make_uint4(0, 0, 0, 0);
+      if (r < rows)
+        x[u] = *reinterpret_cast<const uint4*>(q + qi * p.q_token_stride + (r - qi * p.group) * p.q_head_stride);
+    }
+#pragma unroll
+    for (int u = 0; u < N; ++u) {
+      const int r = first + u * RPI;
+      float back = 1.f;
+      if constexpr (!std::is_same<A, __half>::value) {
+        // The row's largest number to [2^14, 2^15), as far as the factors' exponents go.
+        uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+        uint32_t top = __vmaxu2(__vmaxu2(w[0] & 0x7FFF7FFFu, w[1] & 0x7FFF7FFFu),
+                                __vmaxu2(w[2] & 0x7FFF7FFFu, w[3] & 0x7FFF7FFFu));
+#pragma unroll
+        for (int k = 1; k < L; k *= 2) top = __vmaxu2(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const int e = static_cast<int>(max(top & 0xFFFFu, top >> 16) >> 7) - 127;
+        const int k = max(-113, min(120, 14 - e));
+        const float up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+        back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          const float2 f = act_to_float2<A>(w[v]);
+          w[v] = float2_to_act<__half>(f.x * up, f.y * up);
+        }
+        x[u] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
+      if (c == 0) factor[r] = back;
+      *reinterpret_cast<uint4*>(tile + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = x[u];
+    }
+  }
+}
+
+// One side (V: values, else keys) and half the queries; 128 threads.  One piece of code for both.
 template <class A, class C, int D>
 __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const bool V,
                                              volatile int* ctl) {
@@ -390,12 +442,13 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
       }
     }
   };
-  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K (and for
-  // the queries of the item before the last), PV(t - 2) for V.
+  // Rings: look-ups, and what last read the tile that a step overwrites: S(t - 2) for K,
+  // PV(t - 2) for V.
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<3> free2(bar(V ? Cfg::kPVD : Cfg::kSF));
   int tile = V ? Cfg::kOffV : Cfg::kOffK;
-  int item = -1, flags = 0;
+  RingBar<2> free_q(bar(Cfg::kQE));
+  int item = 0, flags = 0;
   bool ok = true;
   auto step = [&]() -> const TileStep& {
     return *reinterpret_cast<const TileStep*>(smem + Cfg::kOffInfo + info.index() * Cfg::kInfoB);
@@ -403,61 +456,22 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
   // Iteration t stores step t and then requests step t + 1 (t = -1: requests the first).
   for (int t = -1;; ++t) {
     if (t >= 0) {
-      const TileStep& st = step();
-      if (t >= 2) {
-        if (!__all_sync(0xffffffffu, free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty))) break;
-        free2.advance();
-      }
-      if (!V && (flags & kStageFirst)) {
-        ++item;
-        // Row tid of the tile: query and head, scaled into fp16's range.
-        const CacheSeg& s = st.seg;
-        const int qi = static_cast<int>((tid * p.group_inv) >> 16);
-        const bool live = qi < s.nq;
-        const A* q = static_cast<const A*>(p.q) + (s.q0 + qi) * p.q_token_stride +
-                     (s.h * p.group + tid - qi * p.group) * p.q_head_stride;
-        float up = 1.f, back = 1.f;
-        if constexpr (!std::is_same<A, __half>::value) {
-          float top = 0.f;
-          if (live) {
-#pragma unroll 4
-            for (int c = 0; c < D / 8; ++c) {
-              const uint4 x = *reinterpret_cast<const uint4*>(q + 8 * c);
-              const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = act_to_float2<A>(w[i]);
-                top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
-              }
-            }
-          }
-          const int e = static_cast<int>(__float_as_uint(top) >> 23) - 127;
-          const int k = max(-113, min(120, 14 - e));
-          up = __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
-          back = __uint_as_float(static_cast<uint32_t>(127 - k) << 23);
+      if (flags & kStageFirst) {
+        if (item >= 2) {  // the products of the item before the last
+          if (!__all_sync(0xffffffffu, free_q.wait(ctl, kSiteProdKEmpty))) break;
+          free_q.advance();
         }
-        uint8_t* row = smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB + tid * 128;
-#pragma unroll 4
-        for (int c = 0; c < D / 8; ++c) {
-          uint4 y = make_uint4(0, 0, 0, 0);
-          if (live) {
-            y = *reinterpret_cast<const uint4*>(q + 8 * c);
-            if constexpr (!std::is_same<A, __half>::value) {
-              uint32_t w[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const float2 f = act_to_float2<A>(w[i]);
-                w[i] = float2_to_act<__half>(f.x * up, f.y * up);
-              }
-              y = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          }
-          *reinterpret_cast<uint4*>(row + (c >> 3) * Cfg::kHalfB + (((c & 7) ^ (tid & 7)) << 4)) = y;
-        }
-        reinterpret_cast<float*>(smem + Cfg::kOffFactor)[(item % Cfg::kItems) * 128 + tid] = back;
+        tile_queries<A, D>(p, step().seg, smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB,
+                           reinterpret_cast<float*>(smem + Cfg::kOffFactor) + (item % Cfg::kItems) * 128,
+                           warp + (V ? 4 : 0), lane);
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(bar(Cfg::kQF + item % Cfg::kItems));
+        ++item;
+      }
+      if (t >= 2) {
+        if (!__all_sync(0xffffffffu, free2.wait(ctl, V ? kSiteProdVEmpty : kSiteProdKEmpty))) break;
+        free2.advance();
       }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
@@ -770,8 +784,9 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
       mbar_init(bar(Cfg::kKF + i), 4);
       mbar_init(bar(Cfg::kVF + i), 4);
       mbar_init(bar(Cfg::kDrain + i), 1);
+      mbar_init(bar(Cfg::kQE + i), 1);
     }
-    for (int i = 0; i < Cfg::kItems; ++i) mbar_init(bar(Cfg::kQF + i), 4);
+    for (int i = 0; i < Cfg::kItems; ++i) mbar_init(bar(Cfg::kQF + i), 8);
     for (int i = 0; i < Cfg::kInfo; ++i) {
       mbar_init(bar(Cfg::kIF + i), 1);
       mbar_init(bar(Cfg::kIE + i), 8 + 8 + 2);  // converters, softmax, issuers
