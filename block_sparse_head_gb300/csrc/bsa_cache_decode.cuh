@@ -322,47 +322,71 @@ __device__ __forceinline__ int atomic_add_acq_rel(int* p, int x) {
   return r;
 }
 
-// Row r of a cut unit: pieces 0 .. more, the first at the end of CTA root's share, piece i at
-// the start of CTA root + i's.  One warp.
-template <class A, int D, int R>
-__device__ __forceinline__ void join_row(const CacheFwdParams& p, const CacheParts& parts,
-                                         const CacheSeg& s, int root, int more, int r, int lane) {
-  constexpr int E = D / 32;
-  auto slot = [&](int i) {
-    return static_cast<int64_t>(i == 0 ? 2 * root + 1 : 2 * (root + i)) * R + r;
+// Rows r0, r0 + step, .. (N of them, fewer at the unit's end) of a cut unit: pieces 0 .. more,
+// the first at the end of CTA root's share, piece i at the start of CTA root + i's.  One warp;
+// the rows' loads overlap.
+template <class A, int D, int R, int N>
+__device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CacheParts& parts,
+                                          const CacheSeg& s, int root, int more, int r0, int step,
+                                          int lane) {
+  constexpr int E = D / 32, U = N > 1 ? 2 : 4;
+  const int rows = s.nq * p.group;
+  int64_t row[N];  // of the output
+  float top[N], z[N], o[N][E] = {};
+  auto row_of = [&](int j) { return min(r0 + j * step, rows - 1); };
+  auto slot = [&](int i, int j) {
+    return static_cast<int64_t>(i == 0 ? 2 * root + 1 : 2 * (root + i)) * R + row_of(j);
   };
-  const int qi = r / p.group, head = s.h * p.group + r - qi * p.group;
-  const float sink = p.sinks != nullptr ? p.sinks[head] * kLog2e : -INFINITY;
-  float top = sink;
-  for (int i = lane; i <= more; i += 32) top = fmaxf(top, __ldcg(&parts.ml[slot(i)]).x);
 #pragma unroll
-  for (int k = 1; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-  float z = sink == -INFINITY ? 0.f : ex2_approx(sink - top), o[E] = {};
-#pragma unroll 4
-  for (int i = 0; i <= more; ++i) {
-    const int64_t at = slot(i);
-    const float2 x = __ldcg(&parts.ml[at]);
-    const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top);
-    const float* src = parts.o + at * D + lane * E;
-    if constexpr (E == 4) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
-      o[0] += f * v.x;
-      o[1] += f * v.y;
-      o[2] += f * v.z;
-      o[3] += f * v.w;
-    } else {
-      const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
-      o[0] += f * v.x;
-      o[1] += f * v.y;
-    }
-    z += f * x.y;
+  for (int j = 0; j < N; ++j) {
+    const int qi = static_cast<int>((row_of(j) * p.group_inv) >> 16);
+    const int head = s.h * p.group + row_of(j) - qi * p.group;
+    row[j] = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
+    z[j] = p.sinks != nullptr ? p.sinks[head] * kLog2e : -INFINITY;
+    top[j] = z[j];
   }
-  const float inv = z == 0.f ? 0.f : 1.f / z;
-  const int64_t row = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
-  uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row * D + lane * E);
+#pragma unroll 1
+  for (int i = lane; i <= more; i += 32)
 #pragma unroll
-  for (int i = 0; i < E / 2; ++i) dst[i] = float2_to_act<A>(o[2 * i] * inv, o[2 * i + 1] * inv);
-  if (lane == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * kLn2;
+    for (int j = 0; j < N; ++j) top[j] = fmaxf(top[j], __ldcg(&parts.ml[slot(i, j)]).x);
+#pragma unroll
+  for (int k = 1; k < 32; k *= 2)
+#pragma unroll
+    for (int j = 0; j < N; ++j) top[j] = fmaxf(top[j], __shfl_xor_sync(0xffffffffu, top[j], k));
+#pragma unroll
+  for (int j = 0; j < N; ++j) z[j] = z[j] == -INFINITY ? 0.f : ex2_approx(z[j] - top[j]);
+#pragma unroll U
+  for (int i = 0; i <= more; ++i) {
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+      const int64_t at = slot(i, j);
+      const float2 x = __ldcg(&parts.ml[at]);
+      const float f = x.x == -INFINITY ? 0.f : ex2_approx(x.x - top[j]);
+      const float* src = parts.o + at * D + lane * E;
+      if constexpr (E == 4) {
+        const float4 v = __ldcg(reinterpret_cast<const float4*>(src));
+        o[j][0] += f * v.x;
+        o[j][1] += f * v.y;
+        o[j][2] += f * v.z;
+        o[j][3] += f * v.w;
+      } else {
+        const float2 v = __ldcg(reinterpret_cast<const float2*>(src));
+        o[j][0] += f * v.x;
+        o[j][1] += f * v.y;
+      }
+      z[j] += f * x.y;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    if (r0 + j * step >= rows) continue;
+    const float inv = z[j] == 0.f ? 0.f : 1.f / z[j];
+    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row[j] * D + lane * E);
+#pragma unroll
+    for (int i = 0; i < E / 2; ++i)
+      dst[i] = float2_to_act<A>(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+    if (lane == 0) p.lse[row[j]] = z[j] == 0.f ? -INFINITY : (top[j] + log2f(z[j])) * kLn2;
+  }
 }
 
 template <class A, class C, int D, int NT>
@@ -387,7 +411,10 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
   const CacheParts parts = cache_parts(workspace, gridDim.x, R, D);
   auto group_div = [&](int r) { return static_cast<int>((r * p.group_inv) >> 16); };
 
-  const CacheUnits units{p, 31 - __clz(group_div(R)), p.box_shift, p.box_shift == 4 ? 2 : 1};
+  // A unit's fixed work (joining its warps, its rows, the next unit's queries) counts like 512
+  // keys: 64 requests of 128 to 8,192 tokens 117.4 us with 64 keys, 116 with 256, 111 with 512.
+  const CacheUnits units{p, 31 - __clz(group_div(R)), p.box_shift, 512 >> p.box_shift,
+                         128 >> p.box_shift};
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
       mbar_init(full(i), 2);  // copies announced, boxes described
@@ -400,9 +427,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
-  cache_split<Cfg::kThreads>(units, 128 >> p.box_shift,
-                            reinterpret_cast<long long*>(smem + Cfg::kOffScan),
-                                       reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk));
+  cache_split<Cfg::kThreads>(units, reinterpret_cast<long long*>(smem + Cfg::kOffScan),
+                             reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk));
 
   if (warp == W) {
     decode_producer<C, D, NT>(p, &tm_k, &tm_v, smem, units, ctl);
@@ -772,8 +798,9 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
       consumer_sync<32 * W>();  // the join buffer is free again
       if (!whole_unit) {
         if (err[2]) {
-          for (int r = warp; r < s.nq * p.group; r += W)
-            join_row<A, D, R>(p, parts, s, blockIdx.x - s.before, s.before + s.more, r, lane);
+          // At most two rows a warp.
+          if (warp < s.nq * p.group)
+            join_rows<A, D, R, R / W>(p, parts, s, blockIdx.x - s.before, s.before + s.more, warp, W, lane);
         }
         consumer_sync<32 * W>();  // err[2] has been read
       }

@@ -4,11 +4,12 @@
 // all G query heads of h packed together, against the keys those queries can see.  Its keys
 // are taken in slices of 2^SL keys (of the dense range, or of the layout row's blocks).
 // Every length sits on the device, so the split is made there: all units are laid end to
-// end on one axis, a unit taking kOverhead + slices places, and CTA c takes the c-th piece
-// of equal length.  A CTA thus runs whole units and at most two cut ones; cut units leave
-// partial results (running maximum, sum, accumulator) in the workspace, and the CTA that
-// leaves the last one joins them.  Any mix of lengths splits evenly, one long request over all CTAs as
-// well as a thousand short ones, and the result does not depend on which CTA is first.
+// end on one axis, a unit taking a few places for its fixed work and one a slice, and CTA c
+// takes the c-th piece of equal length.  A CTA thus runs whole units and at most two cut ones;
+// cut units leave partial results (running maximum, sum, accumulator) in the workspace, and the
+// CTA that leaves the last one joins them.  Any mix of lengths splits evenly, one long request
+// over all CTAs as well as a thousand short ones, and the result does not depend on which CTA
+// is first.
 #pragma once
 
 #include "bsa_internal.h"
@@ -32,6 +33,7 @@ struct CacheUnits {
   int tq_shift;  // log2 queries of a tile
   int sl;        // log2 keys of a piece, at most those of a page and of a layout block
   int overhead;  // places for a unit's fixed work
+  int least;     // places of a CTA's share at least (a power of two)
 
   struct Request {
     int q0, n, len, p0, o, tiles;
@@ -70,10 +72,17 @@ struct CacheUnits {
     s.s0 = s.lo_key >> sl;
     return (last >> sl) + 1 - s.s0;
   }
+  // Places of a unit before its pieces: those of the fixed work, and as many as make the unit a
+  // multiple of the least share, so that in the smallest calls no CTA has parts of two units.
+  __device__ __forceinline__ int fixed(int pieces) const { return overhead + (-pieces & (least - 1)); }
+  __device__ __forceinline__ int places(const Request& r, int h, int t, CacheSeg& s) const {
+    const int pieces = unit(r, h, t, s);
+    return fixed(pieces) + pieces;
+  }
   __device__ __forceinline__ long long head_places(const Request& r, int h) const {
     long long n = 0;
     CacheSeg s;
-    for (int t = 0; t < r.tiles; ++t) n += overhead + unit(r, h, t, s);
+    for (int t = 0; t < r.tiles; ++t) n += places(r, h, t, s);
     return n;
   }
 };
@@ -104,11 +113,12 @@ struct CacheWalk {
         if (t >= r.tiles) continue;
         s.b = b;
         const int pieces = u.unit(r, h, t, s);
-        const long long size = u.overhead + pieces;
+        const int fixed = u.fixed(pieces);
+        const long long size = fixed + pieces;
         const long long take = min(left, size - off), end = off + take;
         // the unit's fixed places come first
-        s.s1 = s.s0 + static_cast<int>(max(0ll, end - u.overhead));
-        s.s0 += static_cast<int>(max(0ll, off - u.overhead));
+        s.s1 = s.s0 + static_cast<int>(max(0ll, end - fixed));
+        s.s0 += static_cast<int>(max(0ll, off - fixed));
         s.starts = off == 0;
         s.ends = end == size;
         s.before = off > 0 ? static_cast<int>(div_up(off, chunk)) : 0;
@@ -125,8 +135,8 @@ struct CacheWalk {
 // Splits the axis: every thread of the CTA calls it, thread 0 of the caller gets the walk
 // through `out` (shared memory).  scratch: kThreads / 32 + 1 long longs.
 template <int kThreads>
-__device__ __forceinline__ void cache_split(const CacheUnits& u, int min_chunk,
-                                            long long* scratch, CacheWalk* out) {
+__device__ __forceinline__ void cache_split(const CacheUnits& u, long long* scratch,
+                                            CacheWalk* out) {
   const CacheFwdParams& p = u.p;
   // Without a layout the heads of a request have the same places, so the requests are
   // scanned; with one, the (request, head) pairs are.
@@ -164,7 +174,7 @@ __device__ __forceinline__ void cache_split(const CacheUnits& u, int min_chunk,
     if (w < warp) before += scratch[w];
     total += scratch[w];
   }
-  const long long chunk = max(static_cast<long long>(min_chunk), div_up(total, gridDim.x));
+  const long long chunk = max(static_cast<long long>(u.least), div_up(total, gridDim.x));
   const long long start = blockIdx.x * chunk;
   if (start >= before && start < before + mine) {
     // The thread whose items hold the start finds the item, the head and the tile.
@@ -187,7 +197,7 @@ __device__ __forceinline__ void cache_split(const CacheUnits& u, int min_chunk,
       w.r = r;
       CacheSeg s;
       for (w.t = 0; w.t < r.tiles - 1; ++w.t) {
-        const long long size = u.overhead + u.unit(r, w.h, w.t, s);
+        const long long size = u.places(r, w.h, w.t, s);
         if (w.off < size) break;
         w.off -= size;
       }

@@ -513,7 +513,7 @@ template <class A, int D, bool FOLD>
 __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* smem, uint32_t tmem,
                                              const CacheParts& parts, int* join_flag, volatile int* ctl) {
   using Cfg = TileCfg<D>;
-  constexpr int R = Cfg::kRows;
+  constexpr int R = Cfg::kRows, kJoinRows = 4;
   const uint32_t sbase = smem_u32(smem);
   auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   const int w8 = (threadIdx.x >> 5) - 4, wg = w8 >> 2, wq = w8 & 3;
@@ -604,8 +604,9 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       }
       if (i == 1 && *reinterpret_cast<volatile int*>(join_flag)) {
 #pragma unroll 1
-        for (int r = w8; r < seg.nq * p.group; r += 8)
-          join_row<A, D, R>(p, parts, seg, blockIdx.x - seg.before, seg.before + seg.more, r, lane);
+        for (int r = w8; r < seg.nq * p.group; r += 8 * kJoinRows)
+          join_rows<A, D, R, kJoinRows>(p, parts, seg, blockIdx.x - seg.before, seg.before + seg.more, r, 8,
+                                        lane);
       }
     }
     return true;
@@ -772,7 +773,8 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
   // Queries of a tile: as many as fill its rows, and of one layout row.
   int tq_shift = 31 - __clz(static_cast<int>((128u * p.group_inv) >> 16));
   if (p.row_ptr != nullptr) tq_shift = min(tq_shift, p.block_shift);
-  const CacheUnits units{p, tq_shift, 6, 2};
+  // A unit's fixed work (its queries, O, sums) takes about as long as 256 keys.
+  const CacheUnits units{p, tq_shift, 6, 4, 4};
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
     for (int i = 0; i < 3; ++i) {
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
-  cache_split<Cfg::kThreads>(units, 4, reinterpret_cast<long long*>(smem + Cfg::kOffScan),
+  cache_split<Cfg::kThreads>(units, reinterpret_cast<long long*>(smem + Cfg::kOffScan),
                              reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk));
   tc_fence_before();
   __syncthreads();
