@@ -12,6 +12,11 @@
 // that the numbers are read once.  CT is 1 while that gives at most kSmallGrid CTAs (many
 // short runs at once, in little time), then 16 for pages of up to 32 tokens and 64 for larger
 // ones, which leaves few CTAs that only see that no run begins in their tokens.
+//
+// Measured: 16,384 tokens of 8 heads, d = 128, one prompt: 21.3 us, 4.7 TB/s (0.70 of a copy;
+// 23.3 without the prefetch); 1,000 tokens of 16 heads of 64 in five chunks, pages of 16: 11.2
+// us; 64 requests a token each: 3.7 us.  The launch and three trips to memory one after the
+// other (slots, old scales, numbers) are about 4 us of each.
 #include "bsa_cache.cuh"
 #include "bsa_internal.h"
 
@@ -90,6 +95,13 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheA
     const int id = p.slots[t] >> p.page_shift;
     return id < p.n_pages ? id : -1;
   };
+  if constexpr (CT > 1) {
+    // The chunk's numbers on their way to L2 while the slots are looked at.
+    constexpr int LINES = D / 64;  // 128 bytes each, of a token
+    for (int i = tid; i < CT * LINES; i += kThreads)
+      if (t0 + i / LINES < p.T)
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(in + (t0 + i / LINES) * stride + i % LINES * 64));
+  }
   // Every warp looks at the chunk's tokens: which begin a run.
   int pid[NS], before[NS];
 #pragma unroll

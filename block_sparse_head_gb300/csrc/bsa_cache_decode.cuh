@@ -412,7 +412,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
   auto group_div = [&](int r) { return static_cast<int>((r * p.group_inv) >> 16); };
 
   // A unit's fixed work (joining its warps, its rows, the next unit's queries) counts like 512
-  // keys: 64 requests of 128 to 8,192 tokens 117.4 us with 64 keys, 116 with 256, 111 with 512.
+  // keys: 64 requests of up to 8,192 tokens 117.4 us with 64 keys, 116 with 256, 111 with 512.
   const CacheUnits units{p, 31 - __clz(group_div(R)), p.box_shift, 512 >> p.box_shift,
                          128 >> p.box_shift};
   if (tid == 0) {
