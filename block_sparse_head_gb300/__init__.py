@@ -14,6 +14,7 @@ from .binding import (  # noqa: F401
     cache_append,
     cache_forward,
     cache_resize,
+    cache_status,
     cache_workspace,
     forward,
     forward_ext,

@@ -522,6 +522,14 @@ def cache_workspace(heads: int, kv_heads: int, d: int, max_q: int) -> torch.Tens
     return torch.zeros(n.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
 
 
+def cache_status(workspace: torch.Tensor) -> int:
+    """Waits for the device and returns the status that calls with this workspace and no
+    ``status`` of their own have left: 0, or nonzero when a bounded wait gave up in one of them
+    (its outputs are undefined and the workspace has to be zeroed)."""
+    torch.cuda.synchronize(workspace.device)
+    return int(workspace[:4].view(torch.int32).item())
+
+
 def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
                   kv_len: torch.Tensor, cu_q: torch.Tensor, scale: float, max_q: int | None = None,
@@ -537,8 +545,9 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
     ``window``: keys further back than that are masked (None or negative: no bound); ``lut``
     with ``block``: only the layout's active blocks, one layout head per kv head;
     ``workspace``: from cache_workspace (a zeroed one is made for the call when None).
-    Returns (out [T, heads, d], lse fp32 [T, heads], status int32 [1]); a nonzero status
-    (read after the stream is synchronized) means a bounded wait gave up."""
+    Returns (out [T, heads, d], lse fp32 [T, heads], status); a nonzero status int32 [1] (read
+    after the stream is synchronized) means a bounded wait gave up.  With a workspace and no
+    ``status`` the workspace keeps it (cache_status) and None is returned."""
     lib = _lib or load_library()
     dev, cache, kv_heads, d = _cache_view(k_cache, v_cache, k_scale, v_scale)
     qp, qt, qh = _rows_ptr(q, "q", None, d, dev)
@@ -550,14 +559,15 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         raise ValueError("a lut needs its block")
     max_q = max(T, 1) if max_q is None else int(max_q)
     i32, f32 = torch.int32, torch.float32
-    if out is None or lse is None or status is None or workspace is None:
+    if out is None or lse is None or workspace is None:
         with _on(stream):
             where = q.device
             out = torch.empty(T, heads, d, dtype=q.dtype, device=where) if out is None else out
             lse = torch.empty(T, heads, dtype=f32, device=where) if lse is None else lse
-            status = torch.empty(1, dtype=i32, device=where) if status is None else status
             if workspace is None:
                 workspace = cache_workspace(heads, kv_heads, d, max_q)
+                if status is None:
+                    status = torch.empty(1, dtype=i32, device=where)
     args = None
     if (window is not None and window >= 0) or softcap or sinks is not None or lut is not None:
         args = _CACHE_ARGS.pack(-1 if window is None else min(max(-1, int(window)), 2 ** 31 - 1), float(softcap),
@@ -569,7 +579,8 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         cache, qp, _dev_ptr(block_table, "block_table", i32, (B, max_pages), dev),
         _dev_ptr(kv_len, "kv_len", i32, (B,), dev), _dev_ptr(cu_q, "cu_q", i32, (B + 1,), dev),
         _dev_ptr(out, "out", q.dtype, (T, heads, d), dev),
-        _dev_ptr(lse, "lse", f32, (T, heads), dev), _dev_ptr(status, "status", i32, (1,), dev),
+        _dev_ptr(lse, "lse", f32, (T, heads), dev),
+        None if status is None else _dev_ptr(status, "status", i32, (1,), dev),
         _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, max_pages, T,
         heads, max_q, _ACTIVATIONS[q.dtype], qt, qh, float(scale), args, _cache_stream(stream, dev)),
         "bsa_cache_forward")

@@ -158,8 +158,8 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   if (bad != BSA_OK) return bad;
   bsa_cache_args x{-1, 0.f, nullptr, nullptr, 0};
   if (args != nullptr) x = *args;
-  if (block_table == nullptr || kv_len == nullptr || cu_q == nullptr || status == nullptr ||
-      workspace == nullptr || (T > 0 && (q == nullptr || out == nullptr || lse == nullptr)))
+  if (block_table == nullptr || kv_len == nullptr || cu_q == nullptr || workspace == nullptr ||
+      (T > 0 && (q == nullptr || out == nullptr || lse == nullptr)))
     return BSA_ERR_NULL;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_DTYPE;
   if (B < 1 || T < 0 || T > bsa::kMaxPositions || max_pages < 1 || max_q < 1 ||
@@ -196,7 +196,9 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   if (rc != BSA_OK) return rc;
   if (workspace_bytes < need) return BSA_ERR_TOO_LARGE;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T == 0) return cudaMemsetAsync(status, 0, 4, st) == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+  if (T == 0)
+    return status == nullptr || cudaMemsetAsync(status, 0, 4, st) == cudaSuccess ? BSA_OK
+                                                                                : BSA_ERR_CUDA;
   p.q = q;
   p.q_token_stride = q_token_stride;
   p.q_head_stride = q_head_stride;

@@ -214,6 +214,7 @@ __device__ __forceinline__ void cache_split(const CacheUnits& u, long long* scra
 // count[c]: pieces so far of the unit that was cut at the end of CTA c's share; zero before
 // and after every call.
 struct CacheParts {
+  int* status;
   int* count;
   float* o;
   float2* ml;
@@ -221,7 +222,8 @@ struct CacheParts {
 
 __device__ __forceinline__ CacheParts cache_parts(void* ws, int grid, int rows, int d) {
   CacheParts c;
-  c.count = static_cast<int*>(ws);
+  c.status = static_cast<int*>(ws);
+  c.count = c.status + 4;
   c.o = reinterpret_cast<float*>(c.count + (grid + 3) / 4 * 4);
   c.ml = reinterpret_cast<float2*>(c.o + static_cast<int64_t>(grid) * 2 * rows * d);
   return c;

@@ -796,7 +796,7 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
     mbar_init(bar(Cfg::kJoin), 8);
     err[0] = err[1] = 0;
     fence_mbar_init();
-    if (blockIdx.x == 0) *p.status = 0;
+    if (blockIdx.x == 0 && p.status != nullptr) *p.status = 0;
   }
   if (warp == 0) {
     tmem_alloc(smem_u32(tmem_slot), 512);
@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
     tmem_dealloc(tmem, 512);
   }
   // A wait gives up long after CTA 0 has cleared the word.
-  if (threadIdx.x == 0 && err[0] != 0) atomicMax(p.status, err[0]);
+  if (threadIdx.x == 0 && err[0] != 0) atomicMax(p.status != nullptr ? p.status : parts.status, err[0]);
 }
 
 template <class A, class C, int D, bool FOLD>

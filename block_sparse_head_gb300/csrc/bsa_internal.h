@@ -263,9 +263,10 @@ struct CacheFwdParams {
   float softcap_inv;         // scale / cap
 };
 // Bytes of the partial results that `grid` CTAs of `rows` query rows may leave for the join
-// (bsa_cache_sched.cuh): a counter, and two pieces of rows * d numbers and rows pairs.
+// (bsa_cache_sched.cuh): a counter, and two pieces of rows * d numbers and rows pairs; before
+// them the status word of calls that have no other.
 inline int64_t cache_parts_bytes(int grid, int rows, int d) {
-  return (grid + 3) / 4 * 16 +
+  return 16 + (grid + 3) / 4 * 16 +
          static_cast<int64_t>(grid) * 2 * (static_cast<int64_t>(rows) * d * 4 + rows * 8);
 }
 

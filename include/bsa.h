@@ -470,7 +470,9 @@ typedef struct bsa_cache_args {
  *   cu_q      device int32 [B + 1], ascending, cu_q[B] <= T (bsa_cache_resize's cu_new).
  *   out       device [T, heads, d] of dtype, 16-byte aligned;  lse  device fp32 [T, heads].
  *   status    device int32 [1], written: 0, or 0x10000 | site when a bounded wait in the
- *             kernel gave up (the outputs are then undefined).
+ *             kernel gave up (the outputs are then undefined).  NULL: the workspace's first
+ *             word takes the latter, and is else left as it is, so that one look at it after
+ *             many calls tells whether all went well.
  *   workspace device, 16-byte aligned, of the size that bsa_cache_workspace gives for the
  *             same heads, kv_heads, d and max_q, all zero before its first use; a call that
  *             ends with status 0 leaves it fit for any later call.  Calls that may overlap on

@@ -89,8 +89,9 @@ def test_forward(lib):
 
     for kw, status in CACHE_ERRORS:
         assert f(**kw) == status, kw
-    for n in ("q", "table", "kv_len", "cu_q", "out", "lse", "status", "workspace"):
+    for n in ("q", "table", "kv_len", "cu_q", "out", "lse", "workspace"):
         assert f(**{n: None}) == -1, n
+    assert f(status=None, T=-1) == -2       # may be left out
     for n in ("q", "out", "workspace"):
         assert f(**{n: A + 8}) == -5, n
     for n in ("table", "kv_len", "cu_q", "lse", "status", "sinks"):

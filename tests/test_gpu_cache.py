@@ -237,6 +237,7 @@ class Case:
         out = torch.full((T, Hq, self.d), 77.0, dtype=self.q.dtype, device="cuda")
         lse = torch.full((T, Hq), 77.0, device="cuda")
         kw.setdefault("max_q", max(max(self.news), 1))
+        kw.setdefault("status", torch.full((1,), -1, **I32))
         _, _, status = bsa.cache_forward(self.q, self.kc, self.vc, self.ks, self.vs, ints(self.table),
                                          ints(self.lens), ints(self.cu), scale, out=out, lse=lse, **kw)
         assert int(status[0]) == 0, hex(int(status[0]))
@@ -417,8 +418,9 @@ def test_calls_side_by_side():
     torch.cuda.synchronize()
     for i, c in enumerate(cs):
         n = int(c.cu[-1])
+        assert bsa.cache_status(ws[i]) == 0
         for out, lse, status in outs[i]:
-            assert int(status[0]) == 0
+            assert status is None
             assert torch.equal(out[:n], refs[i][0][:n]) and torch.equal(lse[:n], refs[i][1][:n])
 
 
@@ -429,6 +431,22 @@ def test_one_workspace_for_all_shapes():
         c = Case([6000, 5000], news, G, H, d, 64, seed=G)
         ref, got = c.run(), c.run(workspace=ws)
         assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+def test_status_in_the_workspace(max_q):
+    """Without a status word of its own a call leaves the workspace's as it is, or notes a wait
+    that gave up; with one it does not touch the workspace's."""
+    c = Case([500, 300], [1, 1], 4, 2, seed=31)
+    ws = bsa.cache_workspace(8, 2, 128, max_q)
+    for word in (0, 0x10010):
+        ws[:4].view(torch.int32).fill_(word)
+        ref = c.run(max_q=max_q, workspace=ws)
+        assert bsa.cache_status(ws) == word
+        out, lse, status = bsa.cache_forward(c.q, c.kc, c.vc, c.ks, c.vs, ints(c.table), ints(c.lens), ints(c.cu),
+                                             1 / math.sqrt(c.d), max_q=max_q, workspace=ws)
+        assert status is None and bsa.cache_status(ws) == word
+        assert torch.equal(out[:2], ref[0][:2]) and torch.equal(lse[:2], ref[1][:2])
 
 
 def test_length_past_the_table():
