@@ -8,15 +8,18 @@
 // Bound: memory (a number is read as 16 bits and written as 8).  A CTA takes CT tokens of one
 // head and side and does the runs that begin there, however far they go: a run of up to two
 // tokens (a decode step) is a warp's, any other the CTA's, which holds its share of the page in
-// registers (at most eight 16-byte pieces a thread) between the maximum and the rounding, so
-// that the numbers are read once.  CT is 1 while that gives at most kSmallGrid CTAs (many
-// short runs at once, in little time), then 16 for pages of up to 32 tokens and 64 for larger
-// ones, which leaves few CTAs that only see that no run begins in their tokens.
+// registers (at most sixteen 16-byte pieces a thread) between the maximum and the rounding, so
+// that the numbers are read once.  CT is 1 for up to kSmallRows rows, where the call is as long
+// as one CTA's way (256 tokens of 8 heads one by one: 9.4 us, 7.8 with 16 a CTA; 128: 5.6
+// against 7.6), then 16 for up to kMediumRows and for pages of up to 32 tokens (512 one by one:
+// 8.0 us, 21 with 64 a CTA), and 64 for long prompts (6,400 tokens in pages of 64: 13 us, 19
+// with 16 a CTA), which leaves few CTAs that only see that no run begins in their tokens.
 //
-// Measured: 16,384 tokens of 8 heads, d = 128, one prompt: 21.3 us, 4.7 TB/s (0.70 of a copy;
-// 23.3 without the prefetch); 1,000 tokens of 16 heads of 64 in five chunks, pages of 16: 11.2
-// us; 64 requests a token each: 3.7 us.  The launch and three trips to memory one after the
-// other (slots, old scales, numbers) are about 4 us of each.
+// Measured: 16,384 tokens of 8 heads, d = 128, one prompt: 19.8 us, 5.1 TB/s (0.75 of a copy;
+// 23.3 before the prefetch, the maxima two numbers at once and CTAs of 128 threads instead of
+// 256); 1,000 tokens of 16 heads of 64 in five chunks, pages of 16: 7.8 us (10.6 with 256
+// threads); 64 requests a token each: 3.4 us.  The launch and three trips to memory one after
+// the other (slots, old scales, numbers) are about 3 us of each.
 #include "bsa_cache.cuh"
 #include "bsa_internal.h"
 
@@ -26,20 +29,27 @@ namespace bsa {
 
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
 constexpr int kShortRun = 2;      // tokens of a run that a warp takes
-constexpr int kSmallGrid = 4096;
+// Token rows (tokens x heads x 2) up to which a CTA takes one token, and 16.
+constexpr int kSmallRows = 2048, kMediumRows = 32768;
 
 // Bits of the smallest magnitude that is not finite.
 template <class A>
 constexpr uint32_t kInfBits = std::is_same<A, __half>::value ? 0x7C00u : 0x7F80u;
 
-// Largest magnitudes (as bits, which order like the numbers) of the halves of w and m.
-__device__ __forceinline__ uint32_t max_bits(uint32_t m, uint32_t w) {
-  return __vmaxu2(m, w & 0x7FFF7FFFu);
+// Largest magnitudes of the halves of w and m; NaN where there is one.
+template <class A>
+__device__ __forceinline__ uint32_t max_abs(uint32_t m, uint32_t w) {
+  uint32_t r;
+  if constexpr (std::is_same<A, __half>::value)
+    asm("{\n\t.reg .b32 a;\n\tabs.f16x2 a, %2;\n\tmax.NaN.f16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  else
+    asm("{\n\t.reg .b32 a;\n\tabs.bf16x2 a, %2;\n\tmax.NaN.bf16x2 %0, %1, a;\n\t}" : "=r"(r) : "r"(m), "r"(w));
+  return r;
 }
-// The same over the finite ones.
+// The same over the finite ones (as bits, which order like the numbers).
 template <class A>
 __device__ __forceinline__ uint32_t max_finite(uint32_t m, uint32_t w) {
   w &= 0x7FFF7FFFu;
@@ -193,7 +203,8 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheA
       }
 #pragma unroll
       for (int r = 0; r < RMAX; ++r)
-        m = max_bits(max_bits(max_bits(max_bits(m, x[r].x), x[r].y), x[r].z), x[r].w);
+        if (r * kThreads < pieces)
+          m = max_abs<A>(max_abs<A>(max_abs<A>(max_abs<A>(m, x[r].x), x[r].y), x[r].z), x[r].w);
       if (has_nonfinite<A>(m)) {
         m = 0;
 #pragma unroll
@@ -212,10 +223,12 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheA
       const float inv = 1.f / now;
       uint8_t* const dst = cache + (start + tid / PPT) * D + 8 * (tid % PPT);
 #pragma unroll
-      for (int r = 0; r < RMAX; ++r)
+      for (int r = 0; r < RMAX; ++r) {
+        if (r * kThreads >= pieces) break;
         if (r * kThreads + tid < pieces)
           *reinterpret_cast<uint2*>(dst + r * (kThreads / PPT) * D) =
               make_uint2(quantise4<A, C>(x[r].x, x[r].y, inv), quantise4<A, C>(x[r].z, x[r].w, inv));
+      }
       if (tid == 0) scales[tile] = now;
     }
   }
@@ -224,9 +237,10 @@ __global__ void __launch_bounds__(kThreads) bsa_cache_append_kernel(const CacheA
 template <class A, class C, int D>
 cudaError_t launch(const CacheAppendParams& p, cudaStream_t stream) {
   auto grid = [&](int ct) { return dim3((p.T + ct - 1) / ct, p.heads, 2); };
-  if (static_cast<int64_t>(p.T) * p.heads * 2 <= kSmallGrid)
+  const int64_t rows = static_cast<int64_t>(p.T) * p.heads * 2;
+  if (rows <= kSmallRows)
     bsa_cache_append_kernel<A, C, D, 1><<<grid(1), kThreads, 0, stream>>>(p);
-  else if (p.page_shift <= 5)
+  else if (rows <= kMediumRows || p.page_shift <= 5)
     bsa_cache_append_kernel<A, C, D, 16><<<grid(16), kThreads, 0, stream>>>(p);
   else
     bsa_cache_append_kernel<A, C, D, 64><<<grid(64), kThreads, 0, stream>>>(p);
