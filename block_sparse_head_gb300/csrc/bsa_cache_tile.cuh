@@ -18,26 +18,32 @@
 //               into its addend, as in the decode kernel: w = exp2(s + log2 vs - m), the sum
 //               takes w / vs, weights are rounded to fp16 relative to the largest (2^-11).  An
 //               item's O is read out at the next item's first step.
-//   converters  warps 12-15 for K (and the queries, bf16 ones scaled per row by a power of two
-//               into fp16's range), 16-19 for V: stored numbers, loaded into registers a step
+//   converters  warps 12-15 for K, 16-19 for V: stored numbers, loaded into registers a step
 //               ahead, to fp16 tiles in the 128-byte-swizzled layout that the products read.  A
-//               lane's pieces are chosen so that its writes meet no other's banks.
+//               lane's pieces are chosen so that its writes meet no other's banks.  At an item's
+//               first step all eight turn its queries into an fp16 tile, bf16 ones scaled per
+//               row by a power of two into fp16's range.
 // Shared memory holds two tiles each of Q, K and V in fp16 (192 KB): a step writes 64 KB of
 // fp16 into it and the products read 96 KB of it, which bounds a step at about 1,280 cycles
 // against the 1,024 of its products.
 //
-// Measured, 2,048 queries on 16,384 tokens, 32 query and 8 kv heads, d = 128, e4m3: 539 us,
-// 955 TFLOP/s, 0.50 of a cuBLAS bf16 product.  A step takes about 2,500 cycles: the softmax
+// Measured, 2,048 queries on 16,384 tokens, 32 query and 8 kv heads, d = 128, e4m3: 525 us,
+// 980 TFLOP/s, 0.51 of a cuBLAS bf16 product.  A step takes about 2,450 cycles: the softmax
 // warps' chain of waits, TMEM loads, maxima, exponentials and conversions is the limit (without
-// the conversion of the cache it is 12 % less, without the exponentials 5 %, with an eighth of
-// the products 3 %).  What counted on the way there, at these sizes: the raw bytes by TMA into
-// shared memory and the conversion from there (664 us) against loads into registers; two S
-// buffers instead of three (606); scores read from TMEM twice with 32 at a time in registers,
-// where all threads have 96 registers (592), against once with the register split below (577);
-// causal and window masks decided by the look-ups, once a step, instead of by votes (554);
-// requesting the next step's numbers before the fence that publishes this one's (531).  A few
-// registers spilled in these loops cost a quarter of the speed, and unrolling more of them
-// costs as much in instruction fetches: the roles' loops together just fit that cache.
+// the conversion of the cache the time is 12 % less, without the exponentials 5 %, with an
+// eighth of the products 3 %).  What counted on the way there, at these sizes: the raw bytes by
+// TMA into shared memory and the conversion from there (664 us) against loads into registers;
+// two S buffers instead of three (606); scores read from TMEM twice with 32 at a time in
+// registers, where all threads have 96 registers (592), against once with the register split
+// below (577); causal and window masks decided by the look-ups, once a step, instead of by
+// votes (554); requesting the next step's numbers before the fence that publishes this one's
+// (531).  A few registers spilled in these loops cost a quarter of the speed, and unrolling more
+// of them costs as much in instruction fetches: the roles' loops together just fit that cache.
+//
+// Three chunks of up to 1,000 queries under a block layout that leaves them five blocks of 64
+// each (16 heads, 64 of a tile's 128 rows in use): 58 us.  Of the 6 us that an item takes there
+// about 2 are its change: the queries (2 us; 5 with one thread a row of them) and the read-out
+// of O before it (1.6 us), partly beside the last steps.
 //
 // Every wait is bounded: one that runs out records a timeout, and all roles leave
 // their loops, let the products in flight finish, free TMEM and return.
