@@ -175,6 +175,14 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
       q_head_stride % 8 != 0)
     return BSA_ERR_ALIGN;
   bsa::CacheFwdParams p{};
+  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  if (x.softcap > 0.f) {
+    p.softcap_log2 = static_cast<float>(static_cast<double>(x.softcap) * 1.4426950408889634);
+    p.softcap_inv = static_cast<float>(static_cast<double>(scale) / x.softcap);
+  }
+  if (!std::isfinite(p.scale_log2) || !std::isfinite(p.softcap_log2) ||
+      !std::isfinite(p.softcap_inv))
+    return BSA_ERR_UNSUPPORTED;
   p.page_shift = shift_of(cache->page, 16);
   if (x.lut != nullptr) {
     p.block_shift = shift_of(x.block, 64);
@@ -195,10 +203,6 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   const int rc = bsa_cache_workspace(heads, cache->kv_heads, cache->d, max_q, &need);
   if (rc != BSA_OK) return rc;
   if (workspace_bytes < need) return BSA_ERR_TOO_LARGE;
-  cudaStream_t st = static_cast<cudaStream_t>(stream);
-  if (T == 0)
-    return status == nullptr || cudaMemsetAsync(status, 0, 4, st) == cudaSuccess ? BSA_OK
-                                                                                : BSA_ERR_CUDA;
   p.q = q;
   p.q_token_stride = q_token_stride;
   p.q_head_stride = q_head_stride;
@@ -222,11 +226,10 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   p.n_pages = cache->n_pages;
   p.max_pages = max_pages;
   p.window = x.window < 0 ? -1 : std::min(x.window, bsa::kMaxPositions);
-  p.scale_log2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  if (x.softcap > 0.f) {
-    p.softcap_log2 = static_cast<float>(static_cast<double>(x.softcap) * 1.4426950408889634);
-    p.softcap_inv = static_cast<float>(static_cast<double>(scale) / x.softcap);
-  }
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (T == 0)
+    return status == nullptr || cudaMemsetAsync(status, 0, 4, st) == cudaSuccess ? BSA_OK
+                                                                                : BSA_ERR_CUDA;
   cudaError_t e;
   const int rows = decode_rows(p.group, max_q);
   int dev = -1;

@@ -480,10 +480,13 @@ typedef struct bsa_cache_args {
  *   max_q     at least the queries of any request, as far as the caller knows: chooses the
  *             kernel, results are right for any value >= 1.
  *   heads     a multiple of kv_heads, at most 128 times it.
- *   scale     any finite value.
+ *   scale     such that scale * log2(e) and, with a soft-cap, softcap * log2(e) and scale /
+ *             softcap are finite in fp32.
+ *
+ * No output overlaps another tensor of the call.
  *
  * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN, BSA_ERR_UNSUPPORTED
- * (page, d, block, window or soft-cap out of range, non-finite scale), BSA_ERR_STATE (LUT
+ * (page, d, block, scale or soft-cap out of range), BSA_ERR_STATE (LUT
  * not uploaded to the current device), BSA_ERR_TOO_LARGE (workspace too small),
  * BSA_ERR_CUDA.  The LUT has kv_heads heads (its batch does not matter) and covers the
  * block table: max_pages * page <= nb * block, and the same for its key blocks.

@@ -102,6 +102,7 @@ def test_forward(lib):
     assert f(max_pages=(1 << 23) + 1) == -2 and f(T=(1 << 29) + 1) == -2    # positions past 2^29
     assert f(B=1 << 30, kv_heads=4) == -2
     assert f(heads=7) == -2 and f(heads=0) == -2 and f(heads=258) == -2 and f(max_pages=1 << 25) == -2
+    assert f(scale=3e38) == -6 and f(softcap=3e38) == -6 and f(scale=1e20, softcap=1e-30) == -6
     assert f(scale=float("nan")) == -6 and f(softcap=-1.0) == -6 and f(softcap=float("inf")) == -6
     assert f(lut=lut.handle, block=32) == -6
     assert f(lut=lut.handle, max_pages=9) == -2          # the block table outgrows the layout
