@@ -115,8 +115,9 @@ def _empty_cache(P, H, page, d, kind, seed):
     return x.cuda(), s.cuda()
 
 
-def _check_append(kind, page, d, H, dtype, runs, seed, spread=1.0, pad=2, mutate=None):
-    """runs: (page id, first offset, tokens) of each run, in packed order."""
+def _check_append(kind, page, d, H, dtype, runs, seed, spread=1.0, pad=2, mutate=None, copies=1):
+    """runs: (page id, first offset, tokens) of each run, in packed order; copies: times that
+    the call has every head, for a large call that the oracle does one copy of."""
     P = max(r[0] for r in runs) + 3
     kc, ks = _empty_cache(P, H, page, d, kind, seed)
     vc, vs = _empty_cache(P, H, page, d, kind, seed + 1)
@@ -131,10 +132,13 @@ def _check_append(kind, page, d, H, dtype, runs, seed, spread=1.0, pad=2, mutate
     k, v = dev[:, H: 2 * H], dev[:, 2 * H:]  # strided, as a projection's output is split
     ref = [oc.append(x.double().cpu().numpy(), slots, _stored(c), s.double().cpu().numpy(), kind)
            for x, c, s in ((k, kc, ks), (v, vc, vs))]
+    if copies > 1:
+        k, v, kc, vc, ks, vs = (x.repeat(*[copies if i == 1 else 1 for i in range(x.dim())])
+                                for x in (k, v, kc, vc, ks, vs))
     bsa.cache_append(k, v, ints(slots), kc, vc, ks, vs)
     for (rc, rs), c, s, name in zip(ref, (kc, vc), (ks, vs), "kv"):
-        assert np.array_equal(s.double().cpu().numpy(), rs), name
-        assert np.array_equal(_stored(c), rc, equal_nan=True), name
+        assert np.array_equal(s.double().cpu().numpy(), np.tile(rs, (1, copies))), name
+        assert np.array_equal(_stored(c), np.tile(rc, (1, copies, 1, 1)), equal_nan=True), name
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
@@ -146,6 +150,26 @@ def test_append_runs(kind, dtype, page, d, H):
     runs = [(5, 0, page), (0, 0, 1), (2, page - 1, 1), (7, 3, page - 7), (1, page // 2, page // 2),
             (9, 0, page), (3, 0, 5), (11, 1, 1)]
     _check_append(kind, page, d, H, dtype, runs, seed=page + d + H)
+
+
+@pytest.mark.parametrize("page,d,heads,kind,dtype", [
+    (16, 64, 8, "e4m3", "bf16"), (32, 128, 8, "int8", "fp16"), (64, 64, 8, "e4m3", "fp16"),
+    (128, 64, 8, "int8", "bf16"), (64, 64, 40, "int8", "fp16"), (64, 128, 40, "e4m3", "bf16"),
+    (128, 64, 40, "e4m3", "fp16"), (128, 128, 40, "int8", "bf16")])
+def test_append_many_rows(page, d, heads, kind, dtype):
+    """Calls of thousands of token rows, where a CTA takes 16 or 64 tokens: runs of one and two
+    tokens one after the other, long ones across the CTAs' borders, numbers that are not finite."""
+    runs = [(i, int(o), 1 + i % 2) for i, o in enumerate(np.random.default_rng(page).integers(0, page - 1, 70))]
+    runs += [(70, 0, page), (73, 0, page), (71, 5, page - 5), (72, 0, 3), (74, page // 2, page // 2)]
+    runs += [(75 + i, 0, page) for i in range(max(1, 256 // page))] + [(100, 0, 7), (101, page - 2, 2)]
+
+    def mutate(rows, slots):
+        rows[3, :, 1] = float("inf")
+        rows[150, :, 2] = float("-inf")
+        rows[180, :, 3] = float("nan")
+        slots[50] = -1
+        return slots
+    _check_append(kind, page, d, 1, dtype, runs, seed=page + d, pad=5, mutate=mutate, copies=heads)
 
 
 @pytest.mark.parametrize("kind", ["e4m3", "int8"])
@@ -291,6 +315,16 @@ def test_decode_lengths(G, H, d, page, kind, dtype):
 def test_several_queries(G, H, d, page, kind, dtype):
     """Requests without queries, drafts, chunks longer than a tile, a whole prompt at once."""
     Case([40, 9, 300, 200, 131, 257, 64], [0, 1, 4, 70, 131, 129, 17], G, H, d, page, kind, dtype, seed=d).check()
+
+
+@pytest.mark.parametrize("max_q", [1, 40])
+@pytest.mark.parametrize("d,kind", [(128, "e4m3"), (64, "int8")])
+def test_many_short_units(max_q, d, kind):
+    """A dozen units and more for every CTA, most of them a step long, some without a key."""
+    rng = np.random.default_rng(d)
+    lens = rng.integers(0, 150, 130)
+    news = [int(rng.integers(0, min(n, 12) + 2)) for n in lens]
+    Case(lens, news, 4, 16, d, 32, kind, "bf16", seed=d).check(max_q=max_q, sinks=torch.randn(64, device="cuda"))
 
 
 @pytest.mark.parametrize("max_q", [1, 2, 16, 1000])
