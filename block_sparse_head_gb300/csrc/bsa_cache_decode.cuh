@@ -31,7 +31,7 @@
 // us, 5.9 TB/s; one of 1,000 tokens 9.8 us, almost all of it the way of one CTA: the split (1.6
 // us), the first look-ups (0.8), a stage (1.2), the join of its warps (1) and of the unit's
 // pieces (1).  Four queries of 16 requests with a window of 1,000 (d = 64, int8, pages of 16,
-// soft-cap, sinks) 22 us.  Smaller stages wait for a look-up each (128 keys: 157 us where 256
+// soft-cap, sinks) 21 us.  Smaller stages wait for a look-up each (128 keys: 157 us where 256
 // took 125, before the split weighed its units); per-lane loads instead of TMA 170.
 #pragma once
 
@@ -90,17 +90,28 @@ __device__ __forceinline__ float lg2_approx(float x) {
   return y;
 }
 
-// cap * log2(e) * tanh(z).  From e^(2z) (exact limits for large |z|), which near zero would
-// leave half an ulp of 1 instead of one of z: there the series of tanh up to z^9, 2e-8 off at
-// 0.3.
-__device__ __forceinline__ float softcap(float z, float cap_log2) {
-  const float w = z * z;
-  float y = fmaf(w, 62.f / 2835.f, -17.f / 315.f);
-  y = fmaf(w, y, 2.f / 15.f);
-  y = fmaf(w, y, -1.f / 3.f);
-  y = fmaf(w * z, y, z);
-  if (w > 0.09f) y = 1.f - __fdividef(2.f, 1.f + ex2_approx(z * (2.f * kLog2e)));
-  return cap_log2 * y;
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// cap * log2(e) * tanh(z) of two scores.  From e^(2z) (exact limits for large |z|), which near
+// zero would leave half an ulp of 1 instead of one of z: there the series of tanh up to z^9,
+// 2e-8 off at 0.3.  Both are taken and one is chosen: neighbours differ.
+__device__ __forceinline__ void softcap2(float& a, float& b, float cap_log2) {
+  auto both = [](float x) { return f2_pack(x, x); };
+  const uint64_t zero = 0x8000000080000000ull;  // -0: a sum with it changes nothing
+  const uint64_t z = f2_pack(a, b), w = f2_fma(z, z, zero);
+  uint64_t y = f2_fma(w, both(62.f / 2835.f), both(-17.f / 315.f));
+  y = f2_fma(w, y, both(2.f / 15.f));
+  y = f2_fma(w, y, both(-1.f / 3.f));
+  y = f2_fma(f2_fma(w, z, zero), y, z);
+  const uint64_t t = f2_fma(z, both(2.f * kLog2e), zero);
+  const uint64_t d = f2_add(f2_pack(ex2_approx(f2_lo(t)), ex2_approx(f2_hi(t))), both(1.f));
+  const uint64_t far = f2_fma(f2_pack(rcp_approx(f2_lo(d)), rcp_approx(f2_hi(d))), both(-2.f), both(1.f));
+  a = cap_log2 * (fabsf(a) > 0.3f ? f2_lo(far) : f2_lo(y));
+  b = cap_log2 * (fabsf(b) > 0.3f ? f2_hi(far) : f2_hi(y));
 }
 
 // log2 of a V scale inside the range that the exponents take (NaN and zero count as its
@@ -573,15 +584,26 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
         }
         bool grow = false, whole[SUB];
 #pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[u][n][e] *= rf[n][e & 1] * sl[u].ks;
+        if (p.softcap_log2 > 0.f)
+#pragma unroll
+          for (int u = 0; u < SUB; ++u)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; e += 2) softcap2(x[u][n][e], x[u][n][e + 1], p.softcap_log2);
+#pragma unroll
         for (int u = 0; u < SUB; ++u) {
           whole[u] = sl[u].key0 + 15 <= s.pos0 && (p.window < 0 || sl[u].key0 >= last - p.window);
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float y = x[u][n][e] * (rf[n][e & 1] * sl[u].ks);
-              if (p.softcap_log2 > 0.f) y = softcap(y, p.softcap_log2);
-              y += sl[u].lv;
+              float y = x[u][n][e] + sl[u].lv;
               if (!whole[u]) {
                 const int key = sl[u].key0 + g + (e >> 1) * 8, top = hi[n][e & 1];
                 if (key > top || (p.window >= 0 && key < top - p.window)) y = -INFINITY;

@@ -618,8 +618,9 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     return true;
   };
 
-  // A group's factor of the scores; a zero one would turn a masked score into a NaN.
-  auto factor = [&](float ks) { return FOLD ? fmaxf(rf * ks, 1.17549435e-38f) : rf * ks; };
+  // A group's factor of the scores (one, where they have been changed already); a zero one would
+  // turn a masked score into a NaN.
+  auto factor = [&](float ks) { return FOLD ? fmaxf(rf * ks, 1.17549435e-38f) : 1.f; };
   bool pending = false;
   RingBar<Cfg::kInfo> info(bar(Cfg::kIF));
   RingBar<Cfg::kItems> queries(bar(Cfg::kQF));
@@ -650,6 +651,28 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     if (!wait_ring(scores, kSiteSoftSFull)) break;
     scores.advance();
+    if constexpr (!FOLD) {
+      // Scores changed in place, in a loop: unrolled it would not fit the instruction cache (with
+      // a soft-cap 1.17 ms for the case of the file's head, 1.03 so).
+#pragma unroll 1
+      for (int h = 0; h < 2; ++h) {
+        uint32_t x[32];
+        tmem_ld_16x32bx2_x32<32>(ts + 64 * h, x);
+        const float2 ks = *reinterpret_cast<const float2*>(st.f[2 * h + half].ks);
+        const float c0 = rf * ks.x, c1 = rf * ks.y;
+        tmem_ld_wait(x);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float y0 = __uint_as_float(x[i]) * (i < 16 ? c0 : c1);
+          float y1 = __uint_as_float(x[i + 1]) * (i < 16 ? c0 : c1);
+          if (p.softcap_log2 > 0.f) softcap2(y0, y1, p.softcap_log2);
+          x[i] = __float_as_uint(y0);
+          x[i + 1] = __float_as_uint(y1);
+        }
+        tmem_st_16x32bx2_x32<32>(ts + 64 * h, x);
+      }
+      tmem_st_wait();
+    }
     // 32 keys of each piece a thread (lane t the first of a piece, t + 16 the others).
     uint32_t x[2][32];
     tmem_ld_16x32bx2_x32<32>(ts, x[0]);
@@ -668,21 +691,15 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     float mx = -INFINITY;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      if (!FOLD || (flags & kStepMask)) {
+      if (flags & kStepMask) {
         // Bit i: score i is seen.
         const int k = (h ? head.w : head.z) + 32 * half;
         int lo = 0, hi = min(31, qpos - k);
         if (p.window >= 0) lo = max(lo, qpos - p.window - k);
         const uint32_t seen = hi < lo ? 0u : (0xffffffffu >> (31 - (hi - lo))) << lo;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          float y = __uint_as_float(x[h][i]);
-          if constexpr (!FOLD) {
-            y *= cf[2 * h + (i >> 4)];
-            if (p.softcap_log2 > 0.f) y = softcap(y, p.softcap_log2);
-          }
-          x[h][i] = __float_as_uint((seen >> i) & 1 ? y : -INFINITY);
-        }
+        for (int i = 0; i < 32; ++i)
+          if (!((seen >> i) & 1)) x[h][i] = __float_as_uint(-INFINITY);
       }
       float t0 = -INFINITY, t1 = -INFINITY;
 #pragma unroll
@@ -690,8 +707,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
         t0 = fmax3(t0, __uint_as_float(x[h][i]), __uint_as_float(x[h][i + 1]));
         t1 = fmax3(t1, __uint_as_float(x[h][16 + i]), __uint_as_float(x[h][17 + i]));
       }
-      mx = fmax3(mx, fmaf(t0, FOLD ? cf[2 * h] : 1.f, la[2 * h]),
-                 fmaf(t1, FOLD ? cf[2 * h + 1] : 1.f, la[2 * h + 1]));
+      mx = fmax3(mx, fmaf(t0, cf[2 * h], la[2 * h]), fmaf(t1, cf[2 * h + 1], la[2 * h + 1]));
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     float alpha = 1.f;
@@ -707,7 +723,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       uint32_t pk[16];
-      const float c0 = FOLD ? cf[2 * h] : 1.f, c1 = FOLD ? cf[2 * h + 1] : 1.f;
+      const float c0 = cf[2 * h], c1 = cf[2 * h + 1];
       const float a0 = la[2 * h] + neg_m, a1 = la[2 * h + 1] + neg_m;
       uint64_t s0 = 0ull, s1 = 0ull;
 #pragma unroll
