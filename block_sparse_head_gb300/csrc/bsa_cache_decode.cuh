@@ -697,8 +697,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
       if (!(flags & kStageLast)) continue;
 
       // ---- join the warps: halves onto halves, each warp's accumulator scaled to the common
-      // maximum by its reader (round 1: the row statistics come with it).  Slot i of the
-      // buffer is read by warp i in round 1, so warp i may write it again after that.
+      // maximum by its reader (pass 1: the row statistics come with it).  Slot i of the
+      // buffer is read by warp i in pass 1, so warp i may write it again after that.
       float2* ml = reinterpret_cast<float2*>(smem + Cfg::kOffStats);
       float4* join = reinterpret_cast<float4*>(smem + Cfg::kOffJoin);
       auto give = [&](int n, int slot) {
