@@ -127,10 +127,15 @@ __device__ __forceinline__ float log2_scale(float s) {
 template <int D, int NT>
 struct DecodeCfg {
   static constexpr int kWarps = 8;                    // consumers; the producer comes after
-  static constexpr int kThreads = 32 * (kWarps + 1);
+  // 16 rows of d = 128 take more registers than nine warps leave each (168): the producer gets a
+  // warpgroup of its own, whose registers go to the consumers.  64 requests of 8,192 tokens, 4
+  // queries each: 222 us; 297 with nine warps and one slice a warp at a time, 260 with one.
+  static constexpr bool kSplitRegs = NT * D == 256;
+  static constexpr int kThreads = kSplitRegs ? 384 : 32 * (kWarps + 1);
+  static constexpr int kRegs = 168, kRegProd = 72, kRegCons = 216;
+  static_assert(128 * kRegProd + 256 * kRegCons <= 384 * kRegs, "register split");
   static constexpr int kRows = 8 * NT;
-  // Slices of a stage per warp: two, or one where two would not fit the registers.
-  static constexpr int kSub = NT * D == 256 ? 1 : 2;
+  static constexpr int kSub = 2;                      // slices of a stage per warp
   static constexpr int kSlices = kWarps * kSub;       // slices of a stage
   static constexpr int kStages = 192 * 1024 / (2 * kSlices * 16 * D);
   static constexpr int kVB = D / 8;                   // bytes of a value row per lane
@@ -181,12 +186,20 @@ template <int kThreads>
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
+// A bounded wait; INLINE: nothing out of line, where registers are split.
+template <bool INLINE>
+__device__ __forceinline__ bool decode_wait(uint32_t bar, uint32_t parity, const WaitCtl& ctl, int site) {
+  if constexpr (INLINE) return mbar_wait_inl(bar, parity, ctl, site);
+  else return mbar_wait(bar, parity, ctl, site);
+}
+
+template <bool INLINE>
 struct ConsumerBarrier {
   uint32_t bar, phase;
   __device__ __forceinline__ bool sync(int lane, const WaitCtl& ctl) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    const bool ok = mbar_wait(bar, phase, ctl, kSiteCacheJoin);
+    const bool ok = decode_wait<INLINE>(bar, phase, ctl, kSiteCacheJoin);
     phase ^= 1;
     return __all_sync(0xffffffffu, ok);
   }
@@ -297,7 +310,7 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
     const int flags = end ? kStageEnd
                           : (__any_sync(0xffffffffu, mine && cur.first) ? kStageFirst : 0) |
                                 (__any_sync(0xffffffffu, mine && cur.last) ? kStageLast : 0);
-    if (g >= S && !mbar_wait(empty(slot), (g / S - 1) & 1, ctl, kSiteProdKEmpty)) break;
+    if (g >= S && !decode_wait<Cfg::kSplitRegs>(empty(slot), (g / S - 1) & 1, ctl, kSiteProdKEmpty)) break;
     DecodeStage& st = *reinterpret_cast<DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
     const bool load = mine && cur.key != kNoKeys;
     const int loads = __popc(__ballot_sync(0xffffffffu, load));
@@ -449,9 +462,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
   cache_split<Cfg::kThreads>(units, reinterpret_cast<long long*>(smem + Cfg::kOffScan),
                              reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk));
 
-  if (warp == W) {
-    decode_producer<C, D, NT>(p, &tm_k, &tm_v, smem, units, ctl);
+  if (warp >= W) {
+    if constexpr (Cfg::kSplitRegs) setmaxnreg_dec<Cfg::kRegProd>();
+    if (warp == W) decode_producer<C, D, NT>(p, &tm_k, &tm_v, smem, units, ctl);
   } else {
+    if constexpr (Cfg::kSplitRegs) setmaxnreg_inc<Cfg::kRegCons>();
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
     uint32_t qf[NT][KT][8];  // Q fragments: row 8n + g, the columns of this lane's pieces
     float rf[NT][2];         // factor of the scores of rows 8n + 2t, 8n + 2t + 1
@@ -484,12 +499,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     walk.next(units, s);
     load_q(s);
     int last = 0;  // last position of the tile
-    ConsumerBarrier cb{sbase + Cfg::kOffBar + 8 * (2 * S), 0};
+    ConsumerBarrier<Cfg::kSplitRegs> cb{sbase + Cfg::kOffBar + 8 * (2 * S), 0};
     bool gone = false;
     for (int gs = 0;; ++gs) {
       const int slot = gs % S;
       // A warp whose wait gave up leaves; the abort flag ends the others' waits too.
-      if (!__all_sync(0xffffffffu, mbar_wait(full(slot), (gs / S) & 1, ctl, kSiteMmaStage)))
+      if (!__all_sync(0xffffffffu, decode_wait<Cfg::kSplitRegs>(full(slot), (gs / S) & 1, ctl, kSiteMmaStage)))
         break;
       const DecodeStage& st =
           *reinterpret_cast<const DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
