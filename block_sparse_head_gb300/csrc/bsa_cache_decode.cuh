@@ -4,9 +4,9 @@
 // Bound: memory.  A key costs 2 D bytes and 4 D R flops, R <= 16, so the kernel has to keep
 // the loads in flight and spend few instructions a byte.
 //   * Work is split evenly on the device (bsa_cache_sched.cuh).  One CTA per SM: a producer
-//     warp walks its segments, looks pages and scales up and brings the keys and values in
-//     by TMA, 256 keys a stage, about 190 KB ahead of the eight consumer warps; joining a
-//     segment's warps thus stalls no load.
+//     warp walks its segments, looks pages and scales up and brings the keys in by TMA, a
+//     second one the values, 256 keys a stage, about 190 KB ahead of the eight consumer warps;
+//     joining a segment's warps thus stalls no load.
 //   * A consumer warp takes two 16-key slices of a stage (two chains that overlap), with a
 //     running maximum and sum of its own; the warps are joined when the segment ends.
 //   * Products on mma.m16n8k16 (fp16 inputs, fp32 sums), transposed so that the keys (then
@@ -126,12 +126,12 @@ __device__ __forceinline__ float log2_scale(float s) {
 
 template <int D, int NT>
 struct DecodeCfg {
-  static constexpr int kWarps = 8;                    // consumers; the producer comes after
-  // 16 rows of d = 128 take more registers than nine warps leave each (168): the producer gets a
+  static constexpr int kWarps = 8;  // consumers; the producer and the values' copier come after
+  // 16 rows of d = 128 take more registers than ten warps leave each (168): the producer gets a
   // warpgroup of its own, whose registers go to the consumers.  64 requests of 8,192 tokens, 4
   // queries each: 222 us; 297 with nine warps and one slice a warp at a time, 260 with one.
   static constexpr bool kSplitRegs = NT * D == 256;
-  static constexpr int kThreads = kSplitRegs ? 384 : 32 * (kWarps + 1);
+  static constexpr int kThreads = kSplitRegs ? 384 : 32 * (kWarps + 2);
   static constexpr int kRegs = 168, kRegProd = 72, kRegCons = 216;
   static_assert(128 * kRegProd + 256 * kRegCons <= 384 * kRegs, "register split");
   static constexpr int kRows = 8 * NT;
@@ -143,14 +143,14 @@ struct DecodeCfg {
   static constexpr int kSideB = kSlices * kSliceB;
   static constexpr int kStageB = 2 * kSideB;          // K boxes, then V boxes
   static constexpr int kJoinB = (kWarps / 2) * 32 * (D / 4) * 4;  // half the warps' O, one NT
-  static constexpr int kInfoB = 64 + 16 + 16 * 16;  // DecodeStage
+  static constexpr int kInfoB = 64 + 16 + 16 * 16 + 16 * 8;  // DecodeStage
   static_assert(kSlices <= 16, "boxes of a DecodeStage");
   static constexpr int kOffJoin = kStages * kStageB;
   static constexpr int kOffStats = kOffJoin + kJoinB;  // (max, sum) of each warp's rows
   static constexpr int kOffSegs = kOffStats + kWarps * kRows * 8;
   static constexpr int kOffInfo = kOffSegs + 64 * static_cast<int>(sizeof(CacheSeg));
-  static constexpr int kOffBar = kOffInfo + kStages * kInfoB;  // full, empty
-  static constexpr int kOffScan = kOffBar + (2 * kStages + 1) * 8;  // and the consumers' barrier
+  static constexpr int kOffBar = kOffInfo + kStages * kInfoB;  // full, empty, values to copy
+  static constexpr int kOffScan = kOffBar + (3 * kStages + 1) * 8;  // and the consumers' barrier
   static constexpr int kOffWalk = kOffScan + 16 * 8;
   static constexpr int kOffCtl = kOffWalk + 96;       // status, abort flag
   static constexpr int kSmemB = kOffCtl + 16 + 1024;  // + align slack
@@ -177,6 +177,7 @@ struct DecodeStage {
   int seg_pad[(64 - sizeof(CacheSeg)) / 4];
   int flags, pad[3];
   DecodeBox boxes[16];
+  int2 copies[16];  // page and head, first row of each box (-1: none; -2 in the first: the end)
 };
 
 // Barriers of the consumer warps.  A warp whose wait on a copy gave up leaves the loop, so
@@ -207,14 +208,15 @@ struct ConsumerBarrier {
 
 template <class C, int D, int NT>
 __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const CUtensorMap* tm_k,
-                                                const CUtensorMap* tm_v, uint8_t* smem,
-                                                const CacheUnits& units, const WaitCtl& ctl) {
+                                                uint8_t* smem, const CacheUnits& units,
+                                                const WaitCtl& ctl) {
   using Cfg = DecodeCfg<D, NT>;
   constexpr int S = Cfg::kStages;
   const int lane = threadIdx.x & 31;
   const uint32_t sbase = smem_u32(smem);
   auto full = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   auto empty = [&](int i) { return sbase + Cfg::kOffBar + 8 * (S + i); };
+  auto go = [&](int i) { return sbase + Cfg::kOffBar + 8 * (2 * S + i); };
   CacheWalk walk = *reinterpret_cast<CacheWalk*>(smem + Cfg::kOffWalk);
   const int sl = units.sl, per_stage = (16 * Cfg::kSlices) >> sl;
   const int box_b = D << sl;
@@ -314,14 +316,17 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
     DecodeStage& st = *reinterpret_cast<DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
     const bool load = mine && cur.key != kNoKeys;
     const int loads = __popc(__ballot_sync(0xffffffffu, load));
-    if (lane == 0) mbar_arrive_expect_tx(full(slot), loads * 2 * box_b);
+    const int row = cur.key & ((1 << p.page_shift) - 1);
+    if (lane < Cfg::kSlices) st.copies[lane] = make_int2(end ? -2 : -1, 0);
     __syncwarp();
-    if (load) {
-      const uint32_t dst = sbase + slot * Cfg::kStageB + (lane - at) * box_b;
-      const int row = cur.key & ((1 << p.page_shift) - 1);
-      tma_load_3d(dst, tm_k, full(slot), 0, row, cur.tile);
-      tma_load_3d(dst + Cfg::kSideB, tm_v, full(slot), 0, row, cur.tile);
+    if (load) st.copies[lane - at] = make_int2(cur.tile, row);
+    __syncwarp();
+    if (lane == 0) {
+      mbar_arrive_expect_tx(full(slot), loads * 2 * box_b);
+      mbar_arrive(go(slot));
     }
+    __syncwarp();
+    if (load) tma_load_3d(sbase + slot * Cfg::kStageB + (lane - at) * box_b, tm_k, full(slot), 0, row, cur.tile);
     // The scales may still be on their way: described after the copies have begun.
     if (lane < Cfg::kSlices) st.boxes[lane] = DecodeBox{kNoKeys, 0.f, 0.f, 0};
     __syncwarp();
@@ -341,6 +346,32 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
   }
   // Every copy lands before the CTA leaves (also when the consumers have given up).
   for (int j = max(0, issued - S); j < issued; ++j) mbar_drain_wait(full(j % S), (j / S) & 1);
+}
+
+// The values' copies, beside the producer, which the issue of small boxes' copies keeps busy
+// (64 requests of 2,048 to 8,192 tokens in pages of 16: 141 us, 170 with all in the producer; in
+// pages of 64 no difference).  One warp.
+template <int D, int NT>
+__device__ __forceinline__ void decode_values(const CUtensorMap* tm_v, uint8_t* smem, int box_b,
+                                              const WaitCtl& ctl) {
+  using Cfg = DecodeCfg<D, NT>;
+  constexpr int S = Cfg::kStages;
+  const int lane = threadIdx.x & 31;
+  const uint32_t sbase = smem_u32(smem);
+  for (int g = 0;; ++g) {
+    const int slot = g % S;
+    const uint32_t full = sbase + Cfg::kOffBar + 8 * slot;
+    if (!__all_sync(0xffffffffu, decode_wait<Cfg::kSplitRegs>(full + 16 * S, (g / S) & 1, ctl, kSiteProdVEmpty)))
+      break;
+    const DecodeStage& st =
+        *reinterpret_cast<const DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
+    const int2 c = lane < Cfg::kSlices ? st.copies[lane] : make_int2(-1, 0);
+    if (c.x >= 0)
+      tma_load_3d(sbase + slot * Cfg::kStageB + Cfg::kSideB + lane * box_b, tm_v, full, 0, c.y, c.x);
+    const bool end = __any_sync(0xffffffffu, c.x == -2);
+    if (lane == 0) mbar_arrive(full);
+    if (end) break;
+  }
 }
 
 // Adds and returns what was there; the warp's earlier writes (after a __syncwarp) are seen by
@@ -449,10 +480,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
                          128 >> p.box_shift};
   if (tid == 0) {
     for (int i = 0; i < S; ++i) {
-      mbar_init(full(i), 2);  // copies announced, boxes described
+      mbar_init(full(i), 3);  // copies announced, boxes described, values' copies begun
       mbar_init(empty(i), W);
+      mbar_init(sbase + Cfg::kOffBar + 8 * (2 * S + i), 1);
     }
-    mbar_init(sbase + Cfg::kOffBar + 8 * (2 * S), W);
+    mbar_init(sbase + Cfg::kOffBar + 8 * (3 * S), W);
     err[0] = err[1] = 0;
     fence_mbar_init();
     if (blockIdx.x == 0 && p.status != nullptr) *p.status = 0;
@@ -464,7 +496,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
 
   if (warp >= W) {
     if constexpr (Cfg::kSplitRegs) setmaxnreg_dec<Cfg::kRegProd>();
-    if (warp == W) decode_producer<C, D, NT>(p, &tm_k, &tm_v, smem, units, ctl);
+    if (warp == W) decode_producer<C, D, NT>(p, &tm_k, smem, units, ctl);
+    else if (warp == W + 1) decode_values<D, NT>(&tm_v, smem, D << p.box_shift, ctl);
   } else {
     if constexpr (Cfg::kSplitRegs) setmaxnreg_inc<Cfg::kRegCons>();
     float o[NT][D / 16][4], m[NT][2], l[NT][2];
@@ -499,7 +532,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     walk.next(units, s);
     load_q(s);
     int last = 0;  // last position of the tile
-    ConsumerBarrier<Cfg::kSplitRegs> cb{sbase + Cfg::kOffBar + 8 * (2 * S), 0};
+    ConsumerBarrier<Cfg::kSplitRegs> cb{sbase + Cfg::kOffBar + 8 * (3 * S), 0};
     bool gone = false;
     for (int gs = 0;; ++gs) {
       const int slot = gs % S;
