@@ -26,8 +26,8 @@
 //   * The running maximum moves only when a score passes it by 2^8 (one vote a stage; the
 //     weights stay below 256), so the usual stage needs no shuffles.
 //
-// Measured, 32 query and 8 kv heads, d = 128, e4m3: 64 requests of 2,048 to 8,192 tokens 111 us,
-// 5.9 TB/s (0.88 of a copy; the loads alone, without the products, 0.93); 4 of 65,536 tokens 91
+// Measured, 32 query and 8 kv heads, d = 128, e4m3: 64 requests of 2,048 to 8,192 tokens 110 us,
+// 6.0 TB/s (0.89 of a copy; the loads alone, without the products, 0.93); 4 of 65,536 tokens 91
 // us, 5.9 TB/s; one of 1,000 tokens 9.8 us, almost all of it the way of one CTA: the split (1.6
 // us), the first look-ups (0.8), a stage (1.2), the join of its warps (1) and of the unit's
 // pieces (1).  Four queries of 16 requests with a window of 1,000 (d = 64, int8, pages of 16,
