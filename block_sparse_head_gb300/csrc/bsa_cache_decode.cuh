@@ -22,9 +22,12 @@
 //     into fp16's range (exact but for numbers 2^-28 of the row's largest).  The V scale
 //     is folded into the exponent, w = exp2(s + log2 vs - m), so that weights are rounded
 //     to fp16 relative to the largest weight times scale, and the sum takes w / vs: both
-//     sums are held in fp32, with m the running maximum of s + log2 vs.
-//   * The running maximum moves only when a score passes it by 2^8 (one vote a stage; the
-//     weights stay below 256), so the usual stage needs no shuffles.
+//     sums are held in fp32, with m following the running maximum of s + log2 vs.
+//   * Weights are taken relative to a reference m, set 2^7 below the running maximum and moved
+//     only when a score passes that maximum by 2^8 (one vote a stage), so the usual stage needs
+//     no shuffles.  They stay below 2^15, and one in 2^21 of the largest is still a normal fp16
+//     number (with m at the maximum one in 2^14: behind a key that leads by 2^24 with values
+//     near zero, or beside a page of 2^24 times the V scale, nothing was left of the others).
 //
 // Measured, 32 query and 8 kv heads, d = 128, e4m3: 64 requests of 2,048 to 8,192 tokens 110 us,
 // 6.0 TB/s (0.89 of a copy; the loads alone, without the products, 0.93); 4 of 65,536 tokens 91
@@ -45,6 +48,10 @@ namespace bsa {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+
+// log2 of the largest weight when a row's reference is set, and how far (in log2) scores may
+// pass that maximum before it is set again: weights reach 2^(kLift + kSlack), below fp16's 65504.
+constexpr float kLift = 7.f, kSlack = 8.f;
 
 // Four stored numbers (one word) as two fp16 pairs: (0, 1) and (2, 3).
 template <class C>
@@ -146,7 +153,7 @@ struct DecodeCfg {
   static constexpr int kInfoB = 64 + 16 + 16 * 16 + 16 * 8;  // DecodeStage
   static_assert(kSlices <= 16, "boxes of a DecodeStage");
   static constexpr int kOffJoin = kStages * kStageB;
-  static constexpr int kOffStats = kOffJoin + kJoinB;  // (max, sum) of each warp's rows
+  static constexpr int kOffStats = kOffJoin + kJoinB;  // (reference, sum) of each warp's rows
   static constexpr int kOffSegs = kOffStats + kWarps * kRows * 8;
   static constexpr int kOffInfo = kOffSegs + 64 * static_cast<int>(sizeof(CacheSeg));
   static constexpr int kOffBar = kOffInfo + kStages * kInfoB;  // full, empty, values to copy
@@ -657,7 +664,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
                 if (key > top || (p.window >= 0 && key < top - p.window)) y = -INFINITY;
               }
               x[u][n][e] = y;
-              grow |= y > m[n][e & 1] + 8.f;
+              grow |= y > m[n][e & 1] + (kLift + kSlack);
             }
           }
         }
@@ -671,7 +678,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
               for (int u = 1; u < SUB; ++u) top = fmaxf(top, fmaxf(x[u][n][e], x[u][n][e + 2]));
 #pragma unroll
               for (int k = 4; k < 32; k *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
-              top = fmaxf(top, m[n][e]);
+              top = fmaxf(top - kLift, m[n][e]);
               const float f = m[n][e] == -INFINITY ? 0.f : ex2_approx(m[n][e] - top);
               m[n][e] = top;
               l[n][e] *= f;

@@ -6,7 +6,7 @@
 // Every length sits on the device, so the split is made there: all units are laid end to
 // end on one axis, a unit taking a few places for its fixed work and one a slice, and CTA c
 // takes the c-th piece of equal length.  A CTA thus runs whole units and at most two cut ones;
-// cut units leave partial results (running maximum, sum, accumulator) in the workspace, and the
+// cut units leave partial results (reference, sum, accumulator) in the workspace, and the
 // CTA that leaves the last one joins them.  Any mix of lengths splits evenly, one long request
 // over all CTAs as well as a thousand short ones, and the result does not depend on which CTA
 // is first.
@@ -210,7 +210,7 @@ __device__ __forceinline__ void cache_split(const CacheUnits& u, long long* scra
 
 // Partial results of a cut unit: slot 2c holds the piece at the start of CTA c's share (a
 // unit begun earlier), slot 2c + 1 the piece at its end.  Slot s: R rows of D fp32 at
-// o + s * R * D, and R (max, sum) pairs at ml + s * R.
+// o + s * R * D, and R (reference, sum) pairs at ml + s * R.
 // count[c]: pieces so far of the unit that was cut at the end of CTA c's share; zero before
 // and after every call.
 struct CacheParts {

@@ -16,8 +16,9 @@
 //               piece of a row.  The K scale of a page belongs to 16 keys at least, so it is
 //               folded into the exponent's multiplier per group of 16, and log2 of the V scale
 //               into its addend, as in the decode kernel: w = exp2(s + log2 vs - m), the sum
-//               takes w / vs, weights are rounded to fp16 relative to the largest (2^-11).  An
-//               item's O is read out at the next item's first step.
+//               takes w / vs, weights are rounded to fp16 (2^-11) relative to a reference m that
+//               makes the largest 2^7 to 2^15, as there.  An item's O is read out at the next
+//               item's first step.
 //   converters  warps 12-15 for K, 16-19 for V: stored numbers, loaded into registers a step
 //               ahead, to fp16 tiles in the 128-byte-swizzled layout that the products read.  A
 //               lane's pieces are chosen so that its writes meet no other's banks.  At an item's
@@ -711,12 +712,11 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     }
     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
     float alpha = 1.f;
-    const float m_new = fmaxf(m, mx);
     if (first) {
-      m = m_new;
-    } else if (m_new > m + 8.f) {
-      alpha = ex2_approx(m - m_new);
-      m = m_new;
+      m = mx - kLift;
+    } else if (mx > m + (kLift + kSlack)) {
+      alpha = ex2_approx(m - (mx - kLift));
+      m = mx - kLift;
     }
     const float neg_m = m == -INFINITY ? 0.f : -m;
     float sum = 0.f;

@@ -463,6 +463,8 @@ typedef struct bsa_cache_args {
  * scales are positive.  What the cache holds behind a request's length is not used.  A NaN
  * stored among a request's values may reach the outputs of all queries that the call has for
  * it, also of those that do not see it; one among its keys reaches only those that do.
+ * exp(s_c) * v_scale is rounded to fp16, in units in which a row's largest is 2^7 to 2^15: keys
+ * below 2^-21 of it lose bits, those below 2^-32 add nothing to out (lse counts them in fp32).
  *
  *   q         device, dtype BSA_BF16 or BSA_FP16, [T, heads, d] with strides as in
  *             bsa_cache_append, 16-byte aligned.
