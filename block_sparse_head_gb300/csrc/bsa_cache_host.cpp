@@ -69,6 +69,7 @@ int bsa_cache_resize(int32_t* block_table, const int32_t* kv_len, const int32_t*
   const int shift = shift_of(page, 16);
   if (shift < 0) return BSA_ERR_UNSUPPORTED;
   if (B < 1 || B > bsa::kMaxResizeBatch || max_pages < 1 || n_pages < 1 || tokens < 0 ||
+      tokens > bsa::kMaxPositions ||
       static_cast<int64_t>(max_pages) * page > kInt32Max ||
       static_cast<int64_t>(n_pages) * page > kInt32Max)
     return BSA_ERR_SHAPE;

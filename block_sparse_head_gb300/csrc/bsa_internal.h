@@ -208,6 +208,11 @@ cudaError_t launch_bwd_delta(const void* out, const void* dout, float* delta, in
 // shared memory).
 constexpr int kMaxResizeBatch = 8192;
 
+// Positions, queries and windows of the attention over a cache, and the packed tokens of the
+// other cache calls, are at most this, so that sums and differences of three of them fit 32 bits
+// (and an index that goes on by a whole grid of the kernels' steps).
+constexpr int kMaxPositions = 1 << 29;
+
 struct CacheResizeParams {
   int32_t* table;            // [B, max_pages]
   const int32_t* kv_len;     // [B]
@@ -269,10 +274,6 @@ inline int64_t cache_parts_bytes(int grid, int rows, int d) {
   return 16 + (grid + 3) / 4 * 16 +
          static_cast<int64_t>(grid) * 2 * (static_cast<int64_t>(rows) * d * 4 + rows * 8);
 }
-
-// Positions, queries and windows of the attention over a cache stay below this, so that sums
-// and differences of three of them fit 32 bits.
-constexpr int kMaxPositions = 1 << 29;
 
 // Few query rows (group * max_q <= kDecodeRows): the decode kernels, split over the keys.
 constexpr int kDecodeRows = 16;

@@ -397,7 +397,7 @@ typedef struct bsa_cache {
  *                     INT32_MIN    there are more than `tokens` new tokens
  *                     INT32_MIN+1  free_count is not in [0, n_pages], or the freed pages
  *                                  do not fit the stack
- *   B               1 to 8192.
+ *   B               1 to 8192;  tokens 0 to 2^29.
  *
  * One kernel launch.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_UNSUPPORTED (page),
  * BSA_ERR_ALIGN (4-byte), BSA_ERR_CUDA.
