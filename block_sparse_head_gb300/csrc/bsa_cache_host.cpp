@@ -106,7 +106,7 @@ int bsa_cache_append(const bsa_cache* cache, const void* k, const void* v, const
                      int64_t v_token_stride, int64_t v_head_stride, void* stream) {
   const int bad = check_cache(cache);
   if (bad != BSA_OK) return bad;
-  if (T < 0) return BSA_ERR_SHAPE;
+  if (T < 0 || T > bsa::kMaxPositions) return BSA_ERR_SHAPE;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_DTYPE;
   if (T == 0) return BSA_OK;
   if (k == nullptr || v == nullptr || slots == nullptr) return BSA_ERR_NULL;

@@ -425,9 +425,9 @@ int bsa_cache_resize(int32_t* block_table, const int32_t* kv_len, const int32_t*
  *   k, v    device, dtype BSA_BF16 or BSA_FP16, [T, kv_heads, d]: element (t, h, x) at
  *           t * token_stride + h * head_stride + x (strides in elements, multiples of 8;
  *           rows of a fused projection are passed as they are), 16-byte aligned.
- *   slots   device int32 [T]; a slot outside [0, n_pages * page) skips its token.  No slot
- *           may be listed twice in a call, and no page in two runs (the page's contents
- *           are then undefined).
+ *   slots   device int32 [T], T at most 2^29; a slot outside [0, n_pages * page) skips its
+ *           token.  No slot may be listed twice in a call, and no page in two runs (the
+ *           page's contents are then undefined).
  *
  * One kernel launch.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_DTYPE, BSA_ERR_ALIGN,
  * BSA_ERR_UNSUPPORTED (page, d), BSA_ERR_CUDA.
