@@ -319,7 +319,11 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
     const int flags = end ? kStageEnd
                           : (__any_sync(0xffffffffu, mine && cur.first) ? kStageFirst : 0) |
                                 (__any_sync(0xffffffffu, mine && cur.last) ? kStageLast : 0);
-    if (g >= S && !decode_wait<Cfg::kSplitRegs>(empty(slot), (g / S - 1) & 1, ctl, kSiteProdKEmpty)) break;
+    // One answer for the warp: lanes that saw the slot freed must not go on without lanes that
+    // saw the abort flag first.
+    if (g >= S && !__all_sync(0xffffffffu, decode_wait<Cfg::kSplitRegs>(empty(slot), (g / S - 1) & 1, ctl,
+                                                                        kSiteProdKEmpty)))
+      break;
     DecodeStage& st = *reinterpret_cast<DecodeStage*>(smem + Cfg::kOffInfo + slot * Cfg::kInfoB);
     const bool load = mine && cur.key != kNoKeys;
     const int loads = __popc(__ballot_sync(0xffffffffu, load));
@@ -477,7 +481,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
   auto full = [&](int i) { return sbase + Cfg::kOffBar + 8 * i; };
   auto empty = [&](int i) { return sbase + Cfg::kOffBar + 8 * (S + i); };
   int* err = reinterpret_cast<int*>(smem + Cfg::kOffCtl);
-  const WaitCtl ctl{err + 1, err, kCacheWaitNs, 0};
+  const WaitCtl ctl{err + 1, err, kCacheWaitNs, p.expire_site};
   const CacheParts parts = cache_parts(workspace, gridDim.x, R, D);
   auto group_div = [&](int r) { return static_cast<int>((r * p.group_inv) >> 16); };
 

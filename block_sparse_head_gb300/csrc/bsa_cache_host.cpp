@@ -199,6 +199,7 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
     p.row_ptr = x.lut->d_row_ptr;
     p.col_idx = x.lut->d_col_idx;
     p.nb = x.lut->nb;
+    p.expire_site = x.lut->expire_site;
   }
   int64_t need = 0;
   const int rc = bsa_cache_workspace(heads, cache->kv_heads, cache->d, max_q, &need);

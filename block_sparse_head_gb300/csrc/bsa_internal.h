@@ -266,6 +266,7 @@ struct CacheFwdParams {
   float scale_log2;          // scale * log2(e)
   float softcap_log2;        // cap * log2(e); 0: no soft-cap
   float softcap_inv;         // scale / cap
+  int expire_site;           // decode: waits at this site give up at once (0: none; a test knob)
 };
 // Bytes of the partial results that `grid` CTAs of `rows` query rows may leave for the join
 // (bsa_cache_sched.cuh): a counter, and two pieces of rows * d numbers and rows pairs; before

@@ -556,7 +556,10 @@ int bsa_set_wait_limit(bsa_lut* lut, uint64_t ns);
  * their counterparts: 1 and 2 the producer's item and step slots free, 6 tiles landed,
  * 7 the elementwise warps' operands written (or the accumulators read out), 8 a TMEM
  * region free, 9 the elementwise warps waiting for a product, 12 an item's last
- * products done.  Errors: BSA_ERR_NULL, BSA_ERR_UNSUPPORTED (site outside [0, 65535]).
+ * products done.  bsa_cache_forward with this LUT for few query rows (heads / kv_heads *
+ * max_q <= 16) takes the knob as well and reports in its own status word: 1 producer, stage
+ * free; 2 values' copier, stage announced; 6 consumers, stage landed; 16 consumers, joining a
+ * segment.  Errors: BSA_ERR_NULL, BSA_ERR_UNSUPPORTED (site outside [0, 65535]).
  */
 int bsa_debug_expire_wait(bsa_lut* lut, int site);
 
