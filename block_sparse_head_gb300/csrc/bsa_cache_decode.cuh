@@ -159,7 +159,7 @@ struct DecodeCfg {
   static constexpr int kOffBar = kOffInfo + kStages * kInfoB;  // full, empty, values to copy
   static constexpr int kOffScan = kOffBar + (3 * kStages + 1) * 8;  // and the consumers' barrier
   static constexpr int kOffWalk = kOffScan + 16 * 8;
-  static constexpr int kOffCtl = kOffWalk + 96;       // status, abort flag
+  static constexpr int kOffCtl = kOffWalk + 96;       // status, abort flag, last piece, join's word
   static constexpr int kSmemB = kOffCtl + 16 + 1024;  // + align slack
   static_assert(sizeof(CacheSeg) <= 64 && sizeof(CacheWalk) <= 96, "slots");
   static_assert(kThreads / 32 <= 16, "scan scratch");
@@ -188,8 +188,8 @@ struct DecodeStage {
 };
 
 // Barriers of the consumer warps.  A warp whose wait on a copy gave up leaves the loop, so
-// the warps first meet with a bounded wait; once all are there none leaves before the end of
-// the join, and the hardware barrier does.
+// the warps first meet with a bounded wait and settle whether the join takes place
+// (ConsumerBarrier); if it does, none leaves before its end, and the hardware barrier does.
 template <int kThreads>
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
@@ -201,15 +201,31 @@ __device__ __forceinline__ bool decode_wait(uint32_t bar, uint32_t parity, const
   else return mbar_wait(bar, parity, ctl, site);
 }
 
-template <bool INLINE>
+// A warp's arrival stays counted when its wait gives up, so a slower one may find everybody
+// there after that: the wait alone does not say who goes on.  A word in shared memory, WORD bytes
+// behind the barrier, does: it holds the parity of the joins so far, the first warp behind its
+// wait flips it (the wait held, so all have arrived and all come here) or leaves -1, and every
+// warp, whatever its own wait said, goes by the word.  None can meet a later join's flip: that
+// join needs its arrival.
+template <bool INLINE, int WORD>
 struct ConsumerBarrier {
   uint32_t bar, phase;
   __device__ __forceinline__ bool sync(int lane, const WaitCtl& ctl) {
     __syncwarp();
     if (lane == 0) mbar_arrive(bar);
-    const bool ok = decode_wait<INLINE>(bar, phase, ctl, kSiteCacheJoin);
+    const bool ok = __all_sync(0xffffffffu, decode_wait<INLINE>(bar, phase, ctl, kSiteCacheJoin));
+    const uint32_t was = phase;
     phase ^= 1;
-    return __all_sync(0xffffffffu, ok);
+    uint32_t says = 0;
+    if (lane == 0) {
+      const uint32_t mine = ok ? phase : 0xffffffffu;
+      asm volatile("atom.relaxed.cta.shared::cta.cas.b32 %0, [%1], %2, %3;"
+                   : "=r"(says)
+                   : "r"(bar + WORD), "r"(was), "r"(mine)
+                   : "memory");
+      if (says == was) says = mine;
+    }
+    return __shfl_sync(0xffffffffu, says, 0) == phase;
   }
 };
 
@@ -496,7 +512,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
       mbar_init(sbase + Cfg::kOffBar + 8 * (2 * S + i), 1);
     }
     mbar_init(sbase + Cfg::kOffBar + 8 * (3 * S), W);
-    err[0] = err[1] = 0;
+    err[0] = err[1] = err[3] = 0;
     fence_mbar_init();
     if (blockIdx.x == 0 && p.status != nullptr) *p.status = 0;
     tma_prefetch_desc(&tm_k);
@@ -543,7 +559,8 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     walk.next(units, s);
     load_q(s);
     int last = 0;  // last position of the tile
-    ConsumerBarrier<Cfg::kSplitRegs> cb{sbase + Cfg::kOffBar + 8 * (3 * S), 0};
+    constexpr int kJoinBar = Cfg::kOffBar + 8 * (3 * S);
+    ConsumerBarrier<Cfg::kSplitRegs, Cfg::kOffCtl + 12 - kJoinBar> cb{sbase + kJoinBar, 0};
     bool gone = false;
     for (int gs = 0;; ++gs) {
       const int slot = gs % S;

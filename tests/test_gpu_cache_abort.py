@@ -79,3 +79,11 @@ def test_decode_producer_gives_up(G, d):
     """One request and kv head over all CTAs, each with more stages of 256 keys than its ring
     holds (3 of d = 128, 6 of 64): none comes to the end of a segment before the wait."""
     Call([1 << 19], 1, G, 1, d).check_site(1)
+
+
+@pytest.mark.parametrize("site", [6, 16])
+@pytest.mark.parametrize("G,n,d", [(4, 1, 128), (4, 4, 128), (9, 1, 64)])
+def test_decode_wait_gives_up(G, n, d, site):
+    """Whole and cut units, several segments a CTA: consumers that wait for a stage, and that meet
+    in a join."""
+    Call([3000, 130, 9000, 257] * 8, n, G, 4, d).check_site(site)
