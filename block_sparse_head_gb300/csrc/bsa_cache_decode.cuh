@@ -371,8 +371,13 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
     else if (step == 2) find_scales(next);
     step = min(step + 1, 3);
   }
-  // Every copy lands before the CTA leaves (also when the consumers have given up).
-  for (int j = max(0, issued - S); j < issued; ++j) mbar_drain_wait(full(j % S), (j / S) & 1);
+  // Every copy lands before the CTA leaves (also when the consumers have given up).  One limit for
+  // all: where the values' copier has given up, no stage fills any more.
+  const uint64_t t0 = globaltimer_ns();
+  for (int j = max(0, issued - S); j < issued; ++j) {
+    const uint64_t gone = globaltimer_ns() - t0;
+    mbar_drain_wait(full(j % S), (j / S) & 1, gone < kDrainLimitNs ? kDrainLimitNs - gone : 0);
+  }
 }
 
 // The values' copies, beside the producer, which the issue of small boxes' copies keeps busy

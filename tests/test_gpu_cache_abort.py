@@ -4,6 +4,7 @@ and every role of every CTA returns; the next call, with a zeroed workspace and 
 the same bits as before."""
 
 import math
+import time
 
 import numpy as np
 import pytest
@@ -87,3 +88,12 @@ def test_decode_wait_gives_up(G, n, d, site):
     """Whole and cut units, several segments a CTA: consumers that wait for a stage, and that meet
     in a join."""
     Call([3000, 130, 9000, 257] * 8, n, G, 4, d).check_site(site)
+
+
+@pytest.mark.parametrize("d", [128, 64])
+def test_decode_copier_gives_up(d):
+    """The values' copier leaves; the producer's wait for its own copies has one limit for all stages
+    (4 s), the call returns after it."""
+    begin = time.monotonic()
+    Call([3000, 130, 9000, 257], 1, 4, 4, d).check_site(2)
+    assert time.monotonic() - begin < 14  # two calls that give up
