@@ -776,6 +776,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     if (t > 0) before.advance();
     ts = ts == tl + 256 ? tl : ts + 128;
   }
+  tmem_st_wait();  // TMEM is freed after this: no store of a loop that was left early is under way
 }
 
 // ------------------------------------------------------------------------ kernel
