@@ -46,8 +46,8 @@
 // about 2 are its change: the queries (2 us; 5 with one thread a row of them) and the read-out
 // of O before it (1.6 us), partly beside the last steps.
 //
-// Every wait is bounded: one that runs out records a timeout, and all roles leave
-// their loops, let the products in flight finish, free TMEM and return.
+// Every wait is bounded, by a count of tries: one that runs out records a timeout, and all roles
+// leave their loops, let the products in flight finish, free TMEM and return.
 #pragma once
 
 #include "bsa_cache_decode.cuh"
@@ -834,12 +834,13 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
 
   if (warp < 4) {
     setmaxnreg_dec<Cfg::kRegCtl>();
+    // The test knob ends one of these roles before it begins; the others' waits run out.
     if (warp == 0) {
-      if (lane == 0) tile_mma_s<D>(smem, tmem, ctl);
+      if (lane == 0 && p.expire_site != kSiteMmaStage) tile_mma_s<D>(smem, tmem, ctl);
     } else if (warp == 1) {
-      if (lane == 0) tile_mma_pv<D>(smem, tmem, ctl);
+      if (lane == 0 && p.expire_site != kSiteMmaPFull) tile_mma_pv<D>(smem, tmem, ctl);
     } else if (warp == 2) {
-      tile_lookup<D>(p, smem, units, ctl);
+      if (p.expire_site != kSiteCacheInfo) tile_lookup<D>(p, smem, units, ctl);
     }
   } else if (warp < 12) {
     setmaxnreg_inc<Cfg::kRegSoft>();

@@ -93,7 +93,7 @@ enum WaitSite : int {
   kSiteCacheInfo = 17,
 };
 
-// Limit of every wait of the attention kernels over a cache.
+// Limit of every wait of the decode kernels over a cache (those for many rows count tries).
 constexpr uint64_t kCacheWaitNs = 10000000000ull;
 
 // Raises a kernel's shared-memory limit once per device (done: one flag per device and
@@ -266,7 +266,8 @@ struct CacheFwdParams {
   float scale_log2;          // scale * log2(e)
   float softcap_log2;        // cap * log2(e); 0: no soft-cap
   float softcap_inv;         // scale / cap
-  int expire_site;           // decode: waits at this site give up at once (0: none; a test knob)
+  int expire_site;           // decode: waits at this site give up at once, tiles: its role does
+                             // (0: none; a test knob)
 };
 // Bytes of the partial results that `grid` CTAs of `rows` query rows may leave for the join
 // (bsa_cache_sched.cuh): a counter, and two pieces of rows * d numbers and rows pairs; before

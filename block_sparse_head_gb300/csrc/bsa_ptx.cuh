@@ -136,14 +136,15 @@ __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, con
 
 // A bounded wait in a dozen instructions, for kernels whose roles together have to fit the
 // instruction cache.  The bound is a count of tries: each suspends the thread for as long as
-// the hardware likes (up to the microsecond asked for), so 2^24 of them take between a third of
-// a second and about twenty.  A wait that runs out leaves kStatusTimeout | site in the CTA's
-// word; the other waits of the CTA run out after it.
+// the hardware likes; 2^20 of them take four seconds (3.7 us a try, measured), and not below 20
+// ms if they did not suspend it at all.  A wait that runs out leaves kStatusTimeout | site in the
+// CTA's word; the other waits of the CTA run out by themselves (a look at the word in this loop
+// costs the tile kernel 5 to 8 % of its speed: registers).
 __device__ __forceinline__ bool mbar_wait_tries(uint32_t bar, uint32_t parity,
                                                 volatile int* timeout_word, int site) {
   if (mbar_test_wait(bar, parity)) return true;  // half the latency, where it holds already
 #pragma unroll 1
-  for (int i = 0; i < (1 << 24); ++i) {
+  for (int i = 0; i < (1 << 20); ++i) {
     uint32_t ok;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"

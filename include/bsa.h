@@ -556,10 +556,15 @@ int bsa_set_wait_limit(bsa_lut* lut, uint64_t ns);
  * their counterparts: 1 and 2 the producer's item and step slots free, 6 tiles landed,
  * 7 the elementwise warps' operands written (or the accumulators read out), 8 a TMEM
  * region free, 9 the elementwise warps waiting for a product, 12 an item's last
- * products done.  bsa_cache_forward with this LUT for few query rows (heads / kv_heads *
- * max_q <= 16) takes the knob as well and reports in its own status word: 1 producer, stage
- * free; 2 values' copier, stage announced; 6 consumers, stage landed; 16 consumers, joining a
- * segment.  Errors: BSA_ERR_NULL, BSA_ERR_UNSUPPORTED (site outside [0, 65535]).
+ * products done.  bsa_cache_forward with this LUT takes the knob as well and reports
+ * in its own status word.  For few query rows (heads / kv_heads * max_q <= 16): 1 producer,
+ * stage free; 2 values' copier, stage announced; 6 consumers, stage landed; 16 consumers,
+ * joining a segment.  For more rows the knob ends one role at once (6 the issuer of the S
+ * products, 7 of the PV products, 17 the look-ups; others have no effect), and the other roles'
+ * waits for it run out, which takes seconds and records their sites: 1 look-ups and key
+ * converters, 2 value converters, place free; 6 issuers, operands converted; 7 PV issuer, P
+ * written; 8 S issuer, S buffer free; 9 softmax, S computed; 11 O free for a rescale; 12 an
+ * item's last PV done; 16 joining a unit; 17 step looked up.  Errors: BSA_ERR_NULL, BSA_ERR_UNSUPPORTED (site outside [0, 65535]).
  */
 int bsa_debug_expire_wait(bsa_lut* lut, int site);
 
