@@ -208,12 +208,6 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
                "l"(reinterpret_cast<uint64_t>(src))
                : "memory");
 }
-// The same for 8 bytes (through L1).
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst),
-               "l"(reinterpret_cast<uint64_t>(src))
-               : "memory");
-}
 __device__ __forceinline__ void cp_async_commit() {
   asm volatile("cp.async.commit_group;" ::: "memory");
 }
