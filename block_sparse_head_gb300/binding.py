@@ -215,7 +215,8 @@ class Lut:
         _check(self._lib.bsa_set_wait_limit(self.handle, int(ns)), "bsa_set_wait_limit")
 
     def debug_expire_wait(self, site: int):
-        """Test knob: later forwards treat every wait at ``site`` as run out (0: off)."""
+        """Test knob: later forwards (cache_forward with this layout too) treat every wait at
+        ``site`` as run out (0: off)."""
         _check(self._lib.bsa_debug_expire_wait(self.handle, int(site)), "bsa_debug_expire_wait")
 
     def device_status(self, stream=None) -> tuple[int, int]:
@@ -497,9 +498,9 @@ def cache_append(k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor, k_cache:
                  v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
                  stream=None) -> None:
     """Quantise new keys and values into the cache (bsa_cache_append).  k, v: bf16 or fp16
-    [T, kv_heads, d], any token and head stride; slots int32 [T] (cache_resize; -1: skip);
-    caches float8_e4m3fn or int8 [pages, kv_heads, page, d], scales fp32 [pages, kv_heads],
-    all on the current device and updated in place."""
+    [T, kv_heads, d], 16-byte aligned, token and head strides any multiples of 8 elements; slots
+    int32 [T] (cache_resize; -1: skip); caches float8_e4m3fn or int8 [pages, kv_heads, page, d],
+    scales fp32 [pages, kv_heads], all on the current device and updated in place."""
     lib = _lib or load_library()
     dev, cache, heads, d = _cache_view(k_cache, v_cache, k_scale, v_scale)
     kp, kt, kh = _rows_ptr(k, "k", heads, d, dev)
@@ -539,9 +540,10 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
                   workspace: torch.Tensor | None = None, stream=None):
     """Attention of the newest tokens of every request over its cache (bsa_cache_forward).
-    q: bf16 or fp16 [T, heads, d], any token and head stride, packed by cu_q int32 [B + 1];
+    q: bf16 or fp16 [T, heads, d], strides as in cache_append, packed by cu_q int32 [B + 1];
     caches and scales as in cache_append; block_table int32 [B, max_pages], kv_len int32 [B]
-    with the new tokens counted.  ``max_q``: the most queries of a request (T when None);
+    with the new tokens counted.  ``max_q``: the most queries of a request (T when None, which is
+    right but takes a batch of decoding requests through the kernel for many rows: give 1 there);
     ``window``: keys further back than that are masked (None or negative: no bound); ``lut``
     with ``block``: only the layout's active blocks, one layout head per kv head;
     ``workspace``: from cache_workspace (a zeroed one is made for the call when None).

@@ -15,9 +15,9 @@
 // 8.0 us, 21 with 64 a CTA), and 64 for long prompts (6,400 tokens in pages of 64: 13 us, 19
 // with 16 a CTA), which leaves few CTAs that only see that no run begins in their tokens.
 //
-// Measured: 16,384 tokens of 8 heads, d = 128, one prompt: 19.8 us, 5.1 TB/s (0.75 of a copy;
+// Measured: 16,384 tokens of 8 heads, d = 128, one prompt: 20.1 us, 5.0 TB/s (0.74 of a copy;
 // 23.3 before the prefetch, the maxima two numbers at once and CTAs of 128 threads instead of
-// 256); 1,000 tokens of 16 heads of 64 in five chunks, pages of 16: 7.8 us (10.6 with 256
+// 256); 1,000 tokens of 16 heads of 64 in five chunks, pages of 16: 8.0 us (10.6 with 256
 // threads); 64 requests a token each: 3.4 us.  The launch and three trips to memory one after
 // the other (slots, old scales, numbers) are about 3 us of each.
 #include "bsa_cache.cuh"

@@ -29,12 +29,12 @@
 //     number (with m at the maximum one in 2^14: behind a key that leads by 2^24 with values
 //     near zero, or beside a page of 2^24 times the V scale, nothing was left of the others).
 //
-// Measured, 32 query and 8 kv heads, d = 128, e4m3: 64 requests of 2,048 to 8,192 tokens 110 us,
-// 6.0 TB/s (0.89 of a copy; the loads alone, without the products, 0.93); 4 of 65,536 tokens 91
-// us, 5.9 TB/s; one of 1,000 tokens 9.8 us, almost all of it the way of one CTA: the split (1.6
-// us), the first look-ups (0.8), a stage (1.2), the join of its warps (1) and of the unit's
-// pieces (1).  Four queries of 16 requests with a window of 1,000 (d = 64, int8, pages of 16,
-// soft-cap, sinks) 21 us.  Smaller stages wait for a look-up each (128 keys: 157 us where 256
+// Measured, 32 query and 8 kv heads, d = 128, e4m3: 64 requests of 2,048 to 8,192 tokens 111 us,
+// 6.0 TB/s (0.88 of a copy; the loads alone, without the products, 0.93); 4 of 65,536 tokens 91
+// us, 5.9 TB/s; one of 1,000 tokens 10.8 us, almost all of it the way of one CTA: the launch, the
+// split (1.6 us), the first look-ups (0.8), a stage (1.2), the join of its warps (1) and of the
+// unit's pieces (1).  Four queries of 16 requests with a window of 1,000 (d = 64, int8, pages of
+// 16, soft-cap, sinks) 21 us.  Smaller stages wait for a look-up each (128 keys: 157 us where 256
 // took 125, before the split weighed its units); per-lane loads instead of TMA 170.
 #pragma once
 
@@ -136,7 +136,7 @@ struct DecodeCfg {
   static constexpr int kWarps = 8;  // consumers; the producer and the values' copier come after
   // 16 rows of d = 128 take more registers than ten warps leave each (168): the producer gets a
   // warpgroup of its own, whose registers go to the consumers.  64 requests of 8,192 tokens, 4
-  // queries each: 222 us; 297 with nine warps and one slice a warp at a time, 260 with one.
+  // queries each: 219 us; 297 with 168 registers for each of nine warps.
   static constexpr bool kSplitRegs = NT * D == 256;
   static constexpr int kThreads = kSplitRegs ? 384 : 32 * (kWarps + 2);
   static constexpr int kRegs = 168, kRegProd = 72, kRegCons = 216;
@@ -381,7 +381,7 @@ __device__ __forceinline__ void decode_producer(const CacheFwdParams& p, const C
 }
 
 // The values' copies, beside the producer, which the issue of small boxes' copies keeps busy
-// (64 requests of 2,048 to 8,192 tokens in pages of 16: 141 us, 170 with all in the producer; in
+// (64 requests of 2,048 to 8,192 tokens in pages of 16: 140 us, 170 with all in the producer; in
 // pages of 64 no difference).  One warp.
 template <int D, int NT>
 __device__ __forceinline__ void decode_values(const CUtensorMap* tm_v, uint8_t* smem, int box_b,

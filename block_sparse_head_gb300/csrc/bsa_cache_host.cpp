@@ -47,8 +47,9 @@ int check_heads(int heads, int kv_heads) {
              : BSA_OK;
 }
 
-// Rows of the decode kernel that a call takes, 0: too many for it.  All queries of a
-// request in one tile, else the cache would be read once for each tile.
+// Rows of the decode kernel that a call takes, 0: too many for it.  A request's queries are then
+// one tile, which reads the cache once, where they fill it to a power of two (bsa_cache_sched.cuh),
+// and two else; with more rows each 8 or 16 of them would read it again.
 int decode_rows(int group, int max_q) {
   const int64_t rows = static_cast<int64_t>(group) * max_q;
   return rows <= 8 ? 8 : rows <= bsa::kDecodeRows ? 16 : 0;

@@ -1,7 +1,9 @@
 // bsa_cache_sched.cuh -- how the attention kernels over a cache share their work out.
 //
 // A unit is (request b, kv head h, query tile t): TQ consecutive queries of b, the rows of
-// all G query heads of h packed together, against the keys those queries can see.  Its keys
+// all G query heads of h packed together, against the keys those queries can see.  (TQ is a power
+// of two, and with a layout tiles begin at multiples of it: 5 queries of 3 heads are two decode
+// tiles of 4 queries, 12 of 16 rows, and read the cache twice.)  Its keys
 // are taken in slices of 2^SL keys (of the dense range, or of the layout row's blocks).
 // Every length sits on the device, so the split is made there: all units are laid end to
 // end on one axis, a unit taking a few places for its fixed work and one a slice, and CTA c
@@ -31,7 +33,7 @@ struct CacheSeg {
 struct CacheUnits {
   const CacheFwdParams& p;
   int tq_shift;  // log2 queries of a tile
-  int sl;        // log2 keys of a piece, at most those of a page and of a layout block
+  int sl;        // log2 keys of a piece, at most those of a layout block (decode: and of a page)
   int overhead;  // places for a unit's fixed work
   int least;     // places of a CTA's share at least (a power of two)
 

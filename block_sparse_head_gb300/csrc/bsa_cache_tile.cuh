@@ -28,7 +28,7 @@
 // fp16 into it and the products read 96 KB of it, which bounds a step at about 1,280 cycles
 // against the 1,024 of its products.
 //
-// Measured, 2,048 queries on 16,384 tokens, 32 query and 8 kv heads, d = 128, e4m3: 525 us,
+// Measured, 2,048 queries on 16,384 tokens, 32 query and 8 kv heads, d = 128, e4m3: 526 us,
 // 980 TFLOP/s, 0.51 of a cuBLAS bf16 product.  A step takes about 2,450 cycles: the softmax
 // warps' chain of waits, TMEM loads, maxima, exponentials and conversions is the limit (without
 // the conversion of the cache the time is 12 % less, without the exponentials 5 %, with an
@@ -654,7 +654,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
     scores.advance();
     if constexpr (!FOLD) {
       // Scores changed in place, in a loop: unrolled it would not fit the instruction cache (with
-      // a soft-cap 1.17 ms for the case of the file's head, 1.03 so).
+      // a soft-cap 1.17 ms for the case of the file's head, 1.04 so).
 #pragma unroll 1
       for (int h = 0; h < 2; ++h) {
         uint32_t x[32];
