@@ -16,6 +16,9 @@ from .binding import (  # noqa: F401
     cache_resize,
     cache_status,
     cache_workspace,
+    diff_backward,
+    diff_forward,
+    diff_workspace,
     forward,
     forward_ext,
     library_path,

@@ -34,7 +34,8 @@ EXPORTED = (
     "bsa_status_string", "bsa_version", "bsa_forward_noalloc", "bsa_debug_expire_wait",
     "bsa_build_lut_rect", "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
     "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
-    "bsa_cache_forward", "bsa_cache_workspace",
+    "bsa_cache_forward", "bsa_cache_workspace", "bsa_diff_forward", "bsa_diff_backward",
+    "bsa_diff_workspace",
 )
 
 _ACTIVATIONS = {torch.bfloat16: 0, torch.float16: 1}          # BSA_BF16, BSA_FP16
@@ -97,6 +98,9 @@ def load_library():
         lib.bsa_cache_forward.argtypes = [vp] + [vp] * 8 + [i64] + [ci] * 6 + \
             [i64, i64, ctypes.c_float, vp, vp]
         lib.bsa_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(i64)]
+        lib.bsa_diff_forward.argtypes = [vp] * 8 + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
+        lib.bsa_diff_backward.argtypes = [vp] * 14 + [i64] + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
+        lib.bsa_diff_workspace.argtypes = [ci, ci, ci, ctypes.POINTER(i64)]
         lib.bsa_lut_export_csc.argtypes = [vp, vp, vp, vp]
         lib.bsa_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
@@ -129,7 +133,8 @@ def load_library():
                      "bsa_wait_selftest", "bsa_debug_expire_wait", "bsa_build_lut_rect",
                      "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
                      "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
-                     "bsa_cache_forward", "bsa_cache_workspace"):
+                     "bsa_cache_forward", "bsa_cache_workspace", "bsa_diff_forward",
+                     "bsa_diff_backward", "bsa_diff_workspace"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -587,6 +592,95 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         heads, max_q, _ACTIVATIONS[q.dtype], qt, qh, float(scale), args, _cache_stream(stream, dev)),
         "bsa_cache_forward")
     return out, lse, status
+
+
+def _diff_shapes(q, k, lam):
+    """(device, B, H, kv_heads, L, d, dq, shape of lam) of a differential attention call."""
+    dev = _this_device(q, "q")
+    if q.dim() != 4 or q.shape[1] % 2:
+        raise ValueError("q must be bf16 [B, 2H, L, dq]")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be bf16 [B, kv_heads, L, d]")
+    B, H2, L, dq = q.shape
+    H = H2 // 2
+    if not isinstance(lam, torch.Tensor) or lam.dim() not in (1, 3):
+        raise ValueError("lam must be fp32 [H] or [B, H, L]")
+    return dev, B, H, k.shape[1], L, k.shape[3], dq, (H,) if lam.dim() == 1 else (B, H, L)
+
+
+def diff_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, lut: Lut,
+                 scale: float, block: int, causal_diag: bool, training: bool = False,
+                 out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                 out2: torch.Tensor | None = None, stream=None):
+    """Block-sparse differential attention (bsa_diff_forward): out = (P_0 - lam P_1) V with two
+    softmax maps a head.  q: bf16 [B, 2H, L, dq], head h's maps at 2h and 2h + 1; k, v: bf16
+    [B, kv_heads, L, d], contiguous, on the current device; dq = d (both maps score the whole
+    key) or d / 2 = 64 (the key's first half for map 0, its second for map 1).  lam: fp32 [H] or
+    [B, H, L].  lut: of a layout [kv_heads, nb, nb], nb = ceil(L / block), for batch B.
+    Returns (out bf16 [B, H, L, d], lse fp32 [B, 2H, L], out2); out2, the second map's output
+    that diff_backward takes, is made where ``training`` is set (None else)."""
+    lib = _lib or load_library()
+    dev, B, H, kv, L, d, dq, lam_shape = _diff_shapes(q, k, lam)
+    bf16, f32 = torch.bfloat16, torch.float32
+    shape = (B, H, L, d)
+    if out is None or lse is None or (training and out2 is None):
+        with _on(stream):
+            out = torch.empty(shape, dtype=bf16, device=q.device) if out is None else out
+            lse = torch.empty(B, 2 * H, L, dtype=f32, device=q.device) if lse is None else lse
+            if training and out2 is None:
+                out2 = torch.empty(shape, dtype=bf16, device=q.device)
+    _check(lib.bsa_diff_forward(
+        _dev_ptr(q, "q", bf16, (B, 2 * H, L, dq), dev), _dev_ptr(k, "k", bf16, (B, kv, L, d), dev),
+        _dev_ptr(v, "v", bf16, (B, kv, L, d), dev), _dev_ptr(lam, "lam", f32, lam_shape, dev), lut.handle,
+        _dev_ptr(out, "out", bf16, shape, dev), _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev),
+        None if out2 is None else _dev_ptr(out2, "out2", bf16, shape, dev), B, H, kv, L, d, dq,
+        int(len(lam_shape) == 3), float(scale), int(block), int(bool(causal_diag)),
+        _cache_stream(stream, dev)), "bsa_diff_forward")
+    return out, lse, out2
+
+
+def diff_workspace(B: int, H: int, L: int) -> torch.Tensor:
+    """A workspace for diff_backward on the current device; calls that may overlap on the GPU
+    need one each."""
+    lib = _lib or load_library()
+    n = ctypes.c_int64()
+    _check(lib.bsa_diff_workspace(int(B), int(H), int(L), ctypes.byref(n)), "bsa_diff_workspace")
+    return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
+
+
+def diff_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor,
+                  out: torch.Tensor, out2: torch.Tensor, lse: torch.Tensor, dout: torch.Tensor,
+                  lut: Lut, scale: float, block: int, causal_diag: bool, dq: torch.Tensor | None = None,
+                  dk: torch.Tensor | None = None, dv: torch.Tensor | None = None,
+                  dlam: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients (dq, dk, dv, dlam) of diff_forward (bsa_diff_backward).  out, out2 (of a call
+    with ``training``) and lse as it returned them; dout bf16 [B, H, L, d].  dlam is fp32 in
+    lam's shape, the others bf16 in those of q, k, v.  ``workspace``: from diff_workspace (one is
+    made for the call when None)."""
+    lib = _lib or load_library()
+    dev, B, H, kv, L, d, n, lam_shape = _diff_shapes(q, k, lam)
+    bf16, f32 = torch.bfloat16, torch.float32
+    if dq is None or dk is None or dv is None or dlam is None or workspace is None:
+        with _on(stream):
+            where = q.device
+            dq = torch.empty(q.shape, dtype=bf16, device=where) if dq is None else dq
+            dk = torch.empty(k.shape, dtype=bf16, device=where) if dk is None else dk
+            dv = torch.empty(k.shape, dtype=bf16, device=where) if dv is None else dv
+            dlam = torch.empty(lam_shape, dtype=f32, device=where) if dlam is None else dlam
+            workspace = diff_workspace(B, H, L) if workspace is None else workspace
+    rows, keys = (B, H, L, d), (B, kv, L, d)
+    ws_bytes = workspace.numel()
+    _check(lib.bsa_diff_backward(
+        _dev_ptr(q, "q", bf16, (B, 2 * H, L, n), dev), _dev_ptr(k, "k", bf16, keys, dev),
+        _dev_ptr(v, "v", bf16, keys, dev), _dev_ptr(lam, "lam", f32, lam_shape, dev),
+        _dev_ptr(out, "out", bf16, rows, dev), _dev_ptr(out2, "out2", bf16, rows, dev),
+        _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev), _dev_ptr(dout, "dout", bf16, rows, dev),
+        lut.handle, _dev_ptr(dq, "dq", bf16, (B, 2 * H, L, n), dev), _dev_ptr(dk, "dk", bf16, keys, dev),
+        _dev_ptr(dv, "dv", bf16, keys, dev), _dev_ptr(dlam, "dlam", f32, lam_shape, dev),
+        _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, H, kv, L, d, n,
+        int(len(lam_shape) == 3), float(scale), int(block), int(bool(causal_diag)),
+        _cache_stream(stream, dev)), "bsa_diff_backward")
+    return dq, dk, dv, dlam
 
 
 def forward_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lut: Lut, scale: float,

@@ -27,11 +27,14 @@ SOURCES = [
     "bsa_cache_host.cpp",
     "bsa_cache_resize.cu",
     "bsa_cache_append.cu",
-] + [f"bsa_cache_{k}_{c}_d{d}.cu" for k in ("decode", "tile") for c in ("e4m3", "int8")
+    "bsa_diff_host.cpp",
+    "bsa_diff_rows.cu",
+] + [f"bsa_diff_{k}_b{b}_d{d}.cu" for k in ("fwd", "bwd") for b in (64, 128) for d in (64, 128)] + [f"bsa_cache_{k}_{c}_d{d}.cu" for k in ("decode", "tile") for c in ("e4m3", "int8")
      for d in (64, 128)] + [f"bsa_fwd_q{qb}_k{kb}_d{d}.cu" for qb, kb in ((64, 64), (128, 128), (64, 128), (128, 64))
      for d in (64, 128)] + [f"bsa_bwd_b{b}_d{d}.cu" for b in (64, 128) for d in (64, 128)]
 HEADERS = ["bsa_internal.h", "bsa_ptx.cuh", "bsa_fwd_kernel.cuh", "bsa_bwd_kernel.cuh",
-           "bsa_topk_kernel.cuh", "bsa_cache.cuh", "bsa_cache_sched.cuh",
+           "bsa_topk_kernel.cuh", "bsa_diff.cuh", "bsa_diff_fwd_kernel.cuh",
+           "bsa_diff_bwd_kernel.cuh", "bsa_cache.cuh", "bsa_cache_sched.cuh",
            "bsa_cache_decode.cuh", "bsa_cache_tile.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

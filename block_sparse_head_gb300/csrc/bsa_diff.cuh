@@ -1,0 +1,40 @@
+// bsa_diff.cuh -- what the kernels of differential attention share: their work list and the
+// weight of the second map.
+//
+// A tile holds 64 queries of both maps of one head as 128 rows, so that one pass over the key
+// blocks serves both softmaxes: K and V are loaded once, every product has 128 rows, and the
+// pipelines are those of the plain kernels.  Queries of d / 2 numbers (a key half for each map)
+// are laid out over d columns, zero in the half that the other map's keys take, so that one
+// product over d columns gives each row its own map's scores.
+#pragma once
+
+#include "bsa_fwd_kernel.cuh"
+
+namespace bsa {
+
+// CTA c's u-th sub-item of the work list (descending cost): c, 2G - 1 - c, 2G + c, ... of the
+// list of items times pairs times halves, forwards and backwards in turn.
+__device__ __forceinline__ int2 stream_range(const DiffList& p) {
+  const int grid = gridDim.x, c = blockIdx.x;
+  const int full = p.n / grid, rest = p.n - full * grid;
+  return make_int2(0, full + (((full & 1) ? grid - 1 - c : c) < rest ? 1 : 0));
+}
+
+// Sub-item u of this CTA as a device record {b * H + h, first query / 64, first col_idx entry,
+// nnz | (dpos + 1) << 16}.
+__device__ __forceinline__ int4 stream_item(const DiffList& p, int u) {
+  const int grid = gridDim.x, c = blockIdx.x;
+  const unsigned k = u * grid + ((u & 1) ? grid - 1 - c : c);
+  const unsigned per = p.pairs * p.halves, item = k / per, rest = k - item * per;
+  const unsigned half = rest / p.pairs, pair = rest - half * p.pairs;
+  const int4 r = p.list[item];
+  return make_int4(r.x * p.pairs + pair, r.y * p.halves + half, r.z, r.w);
+}
+__device__ __forceinline__ int2 stream_range(const DiffFwdParams& p) {
+  return stream_range(static_cast<const DiffList&>(p));
+}
+__device__ __forceinline__ int4 stream_item(const DiffFwdParams& p, int u) {
+  return stream_item(static_cast<const DiffList&>(p), u);
+}
+
+}  // namespace bsa

@@ -1,0 +1,821 @@
+// bsa_diff_bwd_kernel.cuh -- backward of block-sparse differential attention for sm_103a.
+//
+// With P_m = exp(scale q_m . k - lse_m) on the active entries, w = (1, -lam), dP = dO V^T and
+// D_m = rowsum(dO * O_m):
+//     dS_m = w_m P_m (dP - D_m),   dQ_m = scale dS_m K_m,   dK_m = scale dS_m^T Q_m,
+//     dV = (P_0 - lam P_1)^T dO,   dlam = -D_1.
+// K, V and their gradients are shared by both maps and by the heads of a kv head.
+//
+// Three kernels: the row terms (below), dQ over the layout's rows, dK and dV over its columns.
+// The two walks are the plain backward's pipelines (bsa_bwd_kernel.cuh: roles, barriers, TMEM
+// regions) on tiles of 64 queries with both maps as 128 rows, row 64 a + 32 m + r being query
+// 32 a + r under map m:
+//   dQ walk    item: such a tile, A = its Q, B = its dO (each row twice).  Step: 128 keys,
+//              X = K, Y = V.  T1 = A X^T, T2 = B Y^T, E = dS, acc += E X.  The row sums of
+//              P_1 dP, in fp32 throughout, give dlam (D_1 from the bf16 O_1 would carry its
+//              rounding).
+//   dK/dV walk item: a key block, A = K, B = V (rows: keys).  Step: 64 queries of one head of
+//              the kv head, X = Q of both maps (128 rows), Y = dO (64 rows).  T1 = A X^T (128
+//              columns), T2 = B Y^T (64 columns, for both maps).  A thread's 64 columns of T1
+//              are 32 queries under both maps, so that E1 = P_0^T - lam P_1^T, combined in fp32
+//              and rounded once, takes 64 columns (half the product of two maps apart), and
+//              E2 = dS^T 128.  acc1 += E1 Y = dV,  acc2 += E2 X = dK / scale: the sum over maps
+//              and heads stays in TMEM.
+// Queries of d / 2 numbers are laid out over d columns, zero in the other map's half
+// (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
+// Rows past the end of the sequence read as zero and carry lse = +inf, so that their P is 0;
+// keys past it have K = V = 0 and are not stored.
+// Every wait is bounded (WaitCtl), as in the plain kernels.
+#pragma once
+
+#include "bsa_bwd_kernel.cuh"
+#include "bsa_diff.cuh"
+
+namespace bsa {
+
+__device__ __forceinline__ int2 stream_range(const DiffBwdParams& p) {
+  if (p.items != nullptr) return make_int2(p.cta_start[blockIdx.x], p.cta_start[blockIdx.x + 1]);
+  return stream_range(static_cast<const DiffList&>(p));
+}
+__device__ __forceinline__ int4 stream_item(const DiffBwdParams& p, int u) {
+  return p.items != nullptr ? p.items[u] : stream_item(static_cast<const DiffList&>(p), u);
+}
+
+// Row terms of 64 queries: two groups of 32, each [lse_0, lse_1 (log2 units), D_0, D_1, lam]
+// of 32 fp32 and 16 bytes of room, so that the two half-warps, which read the same places of
+// different groups, hit different banks.
+constexpr int kDiffVecHalf = 5 * 32 + 4;
+constexpr int kDiffVec = 2 * kDiffVecHalf;
+static_assert(kDiffVec == kDiffVecFloats, "workspace");
+
+template <int BLK, int D, bool KV>
+struct DiffBwdCfg {
+  static constexpr int kRows = KV ? BLK : 128;         // rows of an item tile
+  static constexpr int kNumWG = kRows / 64;            // elementwise warpgroups
+  static constexpr int kEwWarps = 4 * kNumWG;
+  static constexpr int kMma2Warp = 2 + kEwWarps;
+  static constexpr int kThreads = 32 * (3 + kEwWarps);
+  static constexpr int kG = KV ? 1 : 128 / BLK;        // key blocks of a step (dQ walk)
+  static constexpr int kHalves = BLK / 64;             // query tiles of a block
+  static constexpr int kItemTile = kRows * D * 2;
+  static constexpr int kItemPlane = kRows * 128;       // 64 columns of an item tile
+  static constexpr int kXTile = 128 * D * 2;           // dQ: K of a step; dK/dV: Q of both maps
+  static constexpr int kXBlk = KV ? 128 : BLK;         // rows that one plane of X holds
+  static constexpr int kXPlane = kXBlk * 128;
+  static constexpr int kXBlkB = kXBlk * D * 2;
+  static constexpr int kYTile = (KV ? 64 : 128) * D * 2;
+  static constexpr int kYPlane = (KV ? 64 : BLK) * 128;
+  static constexpr int kNX = KV ? 2 : 3;
+  static constexpr int kOffA = 0;
+  static constexpr int kOffB = kItemTile;
+  static constexpr int kOffX = 2 * kItemTile;
+  static constexpr int kOffY = kOffX + kNX * kXTile;
+  static constexpr int kVecB = kDiffVec * 4;
+  static constexpr int kOffVec = kOffY + 2 * kYTile;
+  static constexpr int kOffBar = kOffVec + (KV ? 2 * kVecB : 0);
+  // barriers: as in the plain backward
+  static constexpr int kBarIF = 0, kBarIE = 1, kBarXF = 2, kBarXE = 5, kBarYF = 8, kBarYE = 10;
+  static constexpr int kBarTF = 12, kBarEF = 13, kBarAD = 14, kBarAR = 16, kBarDrain = 17;
+  static constexpr int kBarEF1 = 18, kBarDF = 19, kBarDL = 20, kBarIFV = 21, kBarIEV = 22;
+  static constexpr int kBarVI = 23, kBarDrain2 = 24, kBarQI = 25, kNumBars = 26;
+  static constexpr int kBarBytes = 256;
+  static_assert(kNumBars * 8 + 8 <= kBarBytes && kOffBar % 8 == 0 && kOffVec % 16 == 0, "barrier area");
+  static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static constexpr int kLaunchSmem = kSmemBytes > 120 * 1024 ? kSmemBytes : 120 * 1024;
+  // TMEM columns, as in the plain backward.  dQ: T1 at 0 or 256, T2 at 128, acc at 384.  dK/dV:
+  // T1 and T2 (its first 64 columns) swap between 0 and 128; E1 and E2 over T1.
+  static constexpr int kT1 = 0, kT2 = 128, kT1b = 256;
+  static constexpr int kAcc1 = KV ? 256 : 384, kAcc2 = 256 + D;
+  static constexpr uint32_t kIdescT1 = idesc_bf16_f32(kRows, KV ? 128 : BLK, false, false);
+  static constexpr uint32_t kIdescT2 = idesc_bf16_f32(kRows, KV ? 64 : BLK, false, false);
+  static constexpr uint32_t kIdescAcc = idesc_bf16_f32(kRows, D, false, true);  // B MN-major
+};
+
+// Steps of the dK/dV walk: of each item (b, kv head, key block) the heads of the kv head, the
+// query blocks of its column and the halves of a block.
+template <int HALVES>
+struct DiffKvCursor {
+  ItemStream is;
+  int pair, e, half;
+  __device__ __forceinline__ void init(const DiffBwdParams& p) {
+    is.init<true>(p);
+    pair = e = half = 0;
+  }
+  __device__ __forceinline__ void advance(const DiffBwdParams& p) {
+    if (++half < HALVES) return;
+    half = 0;
+    if (++e < is.nnz()) return;
+    e = 0;
+    if (++pair < p.pairs) return;
+    pair = 0;
+    is.next<true>(p);
+  }
+  __device__ __forceinline__ bool valid() const { return !is.done(); }
+  __device__ __forceinline__ bool first() const { return (pair | e | half) == 0; }
+  __device__ __forceinline__ bool last(const DiffBwdParams& p) const {
+    return half == HALVES - 1 && e == is.nnz() - 1 && pair == p.pairs - 1;
+  }
+};
+
+// Both maps' rows of 64 queries of head `pair`, 32 at a time, into a tile of 128 rows.
+// `tile` planes are 128 rows apart.  SPLIT: one plane a map.
+template <int D, bool SPLIT>
+__device__ __forceinline__ void diff_load_q(uint32_t tile, const CUtensorMap* tm, uint32_t bar,
+                                            int q0, int pair) {
+#pragma unroll
+  for (int a = 0; a < 2; ++a)
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int z = 0; z < (SPLIT ? 1 : D / 64); ++z)
+        tma_load_4d(tile + (SPLIT ? m : z) * (128 * 128) + (64 * a + 32 * m) * 128, tm, bar, 0,
+                    q0 + 32 * a, z, 2 * pair + m);
+}
+
+// ----------------------------------------------------------------- producers
+
+template <int BLK, int D, bool SPLIT>
+__device__ __forceinline__ void diff_dq_producer(const DiffBwdParams& p, const CUtensorMap* tm_q,
+                                                 const CUtensorMap* tm_do, const CUtensorMap* tm_k,
+                                                 const CUtensorMap* tm_v, uint32_t sbase,
+                                                 const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, false>;
+  constexpr int G = C::kG;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  StepCursor<G> c;
+  c.init(p);
+  int n = -1;          // items whose tiles were armed
+  int nx = 0, ny = 0;  // steps whose X (Y) copies were armed
+  for (int t = 0; c.valid(); ++t) {
+    const int nblk = c.nblk();
+    const int pair = c.is.cur.x, q0 = c.is.cur.y * 64, head = pair / p.pairs;
+    int cols[G];
+#pragma unroll
+    for (int g = 0; g < G; ++g) cols[g] = (g < nblk) ? p.col_idx[c.is.cur.z + c.s * G + g] : 0;
+    if (c.s == 0) {
+      // Free once the previous item's last T1 and T2 are complete.
+      if (n >= 0 && !mbar_wait(bar(C::kBarIE), n & 1, ctl, kSiteProdKEmpty)) break;
+      const uint32_t fb = bar(C::kBarIF);
+      mbar_arrive_expect_tx(fb, (SPLIT ? C::kItemTile / 2 : C::kItemTile) + C::kItemTile);
+      ++n;
+      diff_load_q<D, SPLIT>(sbase + C::kOffA, tm_q, fb, q0, pair);
+#pragma unroll
+      for (int a = 0; a < 2; ++a)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int z = 0; z < D / 64; ++z)
+            tma_load_4d(sbase + C::kOffB + z * C::kItemPlane + (64 * a + 32 * m) * 128, tm_do, fb, 0,
+                        q0 + 32 * a, z, pair);
+    }
+    c.advance(p);
+    // X slot t % 3 held K(t-3), read by the dQ product of t-3; Y slot t % 2 held V(t-2), read
+    // by T2(t-2).
+    if (t >= 3 && !mbar_wait(bar(C::kBarXE + t % 3), ((t - 3) / 3) & 1, ctl, kSiteProdKEmpty)) break;
+    const uint32_t fx = bar(C::kBarXF + t % 3);
+    mbar_arrive_expect_tx(fx, nblk * C::kXBlkB);
+    const uint32_t xd = sbase + C::kOffX + (t % 3) * C::kXTile;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      if (g < nblk) tma_load_4d(xd + g * C::kXBlkB, tm_k, fx, 0, cols[g] * BLK, 0, head);
+    ++nx;
+    if (t >= 2 && !mbar_wait(bar(C::kBarYE + t % 2), ((t - 2) / 2) & 1, ctl, kSiteProdVEmpty)) break;
+    const uint32_t fy = bar(C::kBarYF + t % 2);
+    mbar_arrive_expect_tx(fy, nblk * C::kXBlkB);
+    const uint32_t yd = sbase + C::kOffY + (t % 2) * C::kYTile;
+#pragma unroll
+    for (int g = 0; g < G; ++g)
+      if (g < nblk) tma_load_4d(yd + g * C::kXBlkB, tm_v, fy, 0, cols[g] * BLK, 0, head);
+    ++ny;
+  }
+  // Wait for every copy this thread issued (immediate on the normal path).
+  for (int j = (nx > 3 ? nx - 3 : 0); j < nx; ++j) mbar_drain_wait(bar(C::kBarXF + j % 3), (j / 3) & 1);
+  for (int j = (ny > 2 ? ny - 2 : 0); j < ny; ++j) mbar_drain_wait(bar(C::kBarYF + j % 2), (j / 2) & 1);
+  if (n >= 0) mbar_drain_wait(bar(C::kBarIF), n & 1);
+}
+
+template <int BLK, int D, bool SPLIT>
+__device__ __forceinline__ void diff_kv_producer(const DiffBwdParams& p, const CUtensorMap* tm_k,
+                                                 const CUtensorMap* tm_v, const CUtensorMap* tm_q,
+                                                 const CUtensorMap* tm_do, uint32_t sbase,
+                                                 const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, true>;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  DiffKvCursor<C::kHalves> c;
+  c.init(p);
+  const int tiles = (p.L + 63) / 64;
+  int n = -1, t = 0;  // items whose A was armed; steps armed
+  int nv = 0;         // items whose B was armed
+  for (; c.valid(); ++t) {
+    const int head = c.is.cur.x, key0 = c.is.cur.y * BLK;
+    const int pair = head * p.pairs + c.pair;
+    const int q64 = p.col_idx[c.is.cur.z + c.e] * C::kHalves + c.half;
+    const bool item_first = c.first();
+    if (item_first) {
+      // A is free once the previous item's last T1 is complete.
+      if (n >= 0 && !mbar_wait(bar(C::kBarIE), n & 1, ctl, kSiteProdKEmpty)) break;
+      const uint32_t fb = bar(C::kBarIF);
+      mbar_arrive_expect_tx(fb, C::kItemTile);
+      ++n;
+      tma_load_4d(sbase + C::kOffA, tm_k, fb, 0, key0, 0, head);
+    }
+    c.advance(p);
+    // Stage t % 2 held step t-2, read by its dV and dK products.
+    if (t >= 2 && !mbar_wait(bar(C::kBarXE + t % 2), ((t - 2) / 2) & 1, ctl, kSiteProdVEmpty)) break;
+    const uint32_t fb = bar(C::kBarXF + t % 2);
+    mbar_arrive_expect_tx(fb, (SPLIT ? C::kXTile / 2 : C::kXTile) + C::kYTile + C::kVecB);
+    diff_load_q<D, SPLIT>(sbase + C::kOffX + (t % 2) * C::kXTile, tm_q, fb, q64 * 64, pair);
+    tma_load_4d(sbase + C::kOffY + (t % 2) * C::kYTile, tm_do, fb, 0, q64 * 64, 0, pair);
+    // A block's second half may lie past the sequence; the row terms have room for it.
+    bulk_load(sbase + C::kOffVec + (t % 2) * C::kVecB,
+              p.vec + (static_cast<int64_t>(pair) * diff_vec_tiles(tiles) + q64) * kDiffVec, C::kVecB, fb);
+    if (item_first) {
+      // B (V) after the step's tiles: the previous item's last T2 completes later.
+      if (nv > 0 && !mbar_wait(bar(C::kBarIEV), (nv - 1) & 1, ctl, kSiteProdKEmpty)) {
+        ++t;
+        break;
+      }
+      const uint32_t fv = bar(C::kBarIFV);
+      mbar_arrive_expect_tx(fv, C::kItemTile);
+      tma_load_4d(sbase + C::kOffB, tm_v, fv, 0, key0, 0, head);
+      ++nv;
+    }
+  }
+  for (int j = (t > 2 ? t - 2 : 0); j < t; ++j) mbar_drain_wait(bar(C::kBarXF + j % 2), (j / 2) & 1);
+  if (n >= 0) mbar_drain_wait(bar(C::kBarIF), n & 1);
+  if (nv > 0) mbar_drain_wait(bar(C::kBarIFV), (nv - 1) & 1);
+}
+
+// ---------------------------------------------------------------- MMA issuers
+
+// td = item tile x step tile^T over d; rows of the step in blocks of N (idesc), nb of them.
+template <int D, int PLANE_I, int PLANE_S, int BLOCK_B, int NCOL>
+__device__ __forceinline__ void diff_issue_first(uint32_t td, uint32_t it, uint32_t st, uint32_t hi,
+                                                 uint32_t idesc, int nb) {
+  auto mmas = [&](int n) {
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk) {
+      const uint32_t ia = ((kk >> 2) * PLANE_I + (kk & 3) * 32) >> 4;
+      const uint32_t is = ((kk >> 2) * PLANE_S + (kk & 3) * 32) >> 4;
+#pragma unroll
+      for (int g = 0; g < n; ++g)
+        tc_mma_ss_lh(td + g * NCOL, it + ia, hi, st + is + ((g * BLOCK_B) >> 4), hi, idesc,
+                     kk > 0 ? 1u : 0u);
+    }
+  };
+  // A branch between two MMAs slows their issue.
+  if (nb > 1)
+    mmas(2);
+  else
+    mmas(1);
+}
+
+template <int BLK, int D>
+__device__ __forceinline__ void diff_dq_mma(const DiffBwdParams& p, uint32_t sbase, uint32_t tmem,
+                                            const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, false>;
+  constexpr int G = C::kG;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const uint64_t a_desc = sdesc_sw128(sbase + C::kOffA, 16, 1024);
+  const uint32_t hi = static_cast<uint32_t>(a_desc >> 32);
+  const uint32_t a0 = static_cast<uint32_t>(a_desc);
+  const uint32_t b0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffB, 16, 1024));
+  const uint32_t x0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffX, 16, 1024));
+  const uint32_t y0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffY, 16, 1024));
+  StepCursor<G> c;
+  c.init(p);
+  int n = -1;
+  for (int t = 0; c.valid(); ++t) {
+    const int nblk = G == 1 ? 1 : c.nblk();
+    const bool first = c.s == 0, last = c.s == c.nsteps - 1;
+    c.advance(p);
+    if (first) {
+      ++n;
+      if (!mbar_wait(bar(C::kBarIF), n & 1, ctl, kSiteMmaStage)) break;
+    }
+    if (!mbar_wait(bar(C::kBarXF + t % 3), (t / 3) & 1, ctl, kSiteMmaStage)) break;
+    // This T1 region held step t-2, whose dQ product read E from it.
+    if (t >= 2 && !mbar_wait(bar(C::kBarAD + (t & 1)), ((t - 2) / 2) & 1, ctl, kSiteMmaPvDone)) break;
+    tc_fence_after();
+    diff_issue_first<D, C::kItemPlane, C::kXPlane, C::kXBlkB, BLK>(
+        tmem + ((t & 1) ? C::kT1b : C::kT1), a0, x0 + (t % 3) * (C::kXTile >> 4), hi, C::kIdescT1, nblk);
+    // T2 is free once the elementwise warps finished step t-1.
+    if (t >= 1 && !mbar_wait(bar(C::kBarEF), (t - 1) & 1, ctl, kSiteMmaPFull)) break;
+    if (!mbar_wait(bar(C::kBarYF + t % 2), (t / 2) & 1, ctl, kSiteMmaStage)) break;
+    tc_fence_after();
+    diff_issue_first<D, C::kItemPlane, C::kYPlane, C::kXBlkB, BLK>(
+        tmem + C::kT2, b0, y0 + (t % 2) * (C::kYTile >> 4), hi, C::kIdescT2, nblk);
+    tc_commit(bar(C::kBarTF));
+    tc_commit(bar(C::kBarYE + t % 2));
+    if (last) tc_commit(bar(C::kBarIE));
+  }
+  tc_commit(bar(C::kBarDrain));
+  mbar_drain_wait(bar(C::kBarDrain), 0);
+}
+
+// dQ walk, second issuing thread: acc += dS K of step u once the warps have written dS.
+template <int BLK, int D>
+__device__ __forceinline__ void diff_dq_mma2(const DiffBwdParams& p, uint32_t sbase, uint32_t tmem,
+                                             const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, false>;
+  constexpr int G = C::kG;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const uint64_t x_desc = sdesc_sw128(sbase + C::kOffX, C::kXPlane, 1024);
+  const uint32_t hi = static_cast<uint32_t>(x_desc >> 32);
+  const uint32_t x0 = static_cast<uint32_t>(x_desc);
+  StepCursor<G> c;
+  c.init(p);
+  int n = -1;
+  for (int u = 0; c.valid(); ++u) {
+    const int nblk = c.nblk();
+    const bool first = c.s == 0;
+    c.advance(p);
+    if (first) ++n;
+    if (!mbar_wait(bar(C::kBarEF), u & 1, ctl, kSiteMmaPFull)) break;
+    if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
+    tc_fence_after();
+    const uint32_t te = tmem + ((u & 1) ? C::kT1b : C::kT1), xs = x0 + (u % 3) * (C::kXTile >> 4);
+    auto one = [&](int kk) {
+      const uint32_t bo = ((((kk * 16) / BLK) * C::kXBlkB + ((kk * 16) % BLK) * 128) >> 4);
+      tc_mma_ts_lh(tmem + C::kAcc1, te + kk * 8, xs + bo, hi, C::kIdescAcc, (first && kk == 0) ? 0u : 1u);
+    };
+#pragma unroll
+    for (int kk = 0; kk < (G == 1 ? 8 : 4); ++kk) one(kk);
+    if (G == 2 && nblk > 1) {
+#pragma unroll
+      for (int kk = 4; kk < 8; ++kk) one(kk);
+    }
+    tc_commit(bar(C::kBarAD + (u & 1)));
+    tc_commit(bar(C::kBarXE + u % 3));
+    mbar_arrive(bar(C::kBarQI));
+  }
+  tc_commit(bar(C::kBarDrain2));
+  mbar_drain_wait(bar(C::kBarDrain2), 0);
+}
+
+// dK/dV walk: T1 and T2.  T1(t) is the region at 0 on even steps and at 128 on odd ones, T2(t)
+// the other's first columns.  Per step: T2(t) over T1(t-1) once the products of t-1 have read
+// E1 and E2 there; T1(t+1) over T2(t) once every elementwise warp has loaded it and the dV
+// product of t has been issued (so that E1 of t+1 cannot complete before the other thread has
+// waited for E1 of t).
+template <int BLK, int D>
+__device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sbase, uint32_t tmem,
+                                            const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, true>;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const uint64_t a_desc = sdesc_sw128(sbase + C::kOffA, 16, 1024);
+  const uint32_t hi = static_cast<uint32_t>(a_desc >> 32);
+  const uint32_t a0 = static_cast<uint32_t>(a_desc);
+  const uint32_t b0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffB, 16, 1024));
+  const uint32_t x0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffX, 16, 1024));
+  const uint32_t y0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffY, 16, 1024));
+  auto issue1 = [&](int t) {
+    diff_issue_first<D, C::kItemPlane, C::kXPlane, 0, 128>(tmem + ((t & 1) ? C::kT2 : C::kT1), a0,
+                                                           x0 + (t % 2) * (C::kXTile >> 4), hi,
+                                                           C::kIdescT1, 1);
+  };
+  DiffKvCursor<C::kHalves> c;
+  c.init(p);
+  if (c.valid()) {
+    int n = 0;
+    bool first = true, last = c.last(p);
+    c.advance(p);
+    bool ok = mbar_wait(bar(C::kBarIF), 0, ctl, kSiteMmaStage) &&
+              mbar_wait(bar(C::kBarXF), 0, ctl, kSiteMmaStage);
+    if (ok) {
+      tc_fence_after();
+      issue1(0);  // S^T = K Q^T
+      tc_commit(bar(C::kBarTF));
+      if (last) tc_commit(bar(C::kBarIE));
+    }
+    for (int t = 0; ok; ++t) {
+      if (t > 0 && !mbar_wait(bar(C::kBarAD), (t - 1) & 1, ctl, kSiteMmaPvDone)) break;
+      if (first && !mbar_wait(bar(C::kBarIFV), n & 1, ctl, kSiteMmaStage)) break;
+      tc_fence_after();
+      diff_issue_first<D, C::kItemPlane, C::kYPlane, 0, 64>(
+          tmem + ((t & 1) ? C::kT1 : C::kT2), b0, y0 + (t % 2) * (C::kYTile >> 4), hi, C::kIdescT2,
+          1);  // dP^T = V dO^T
+      tc_commit(bar(C::kBarDF));
+      if (last) tc_commit(bar(C::kBarIEV));
+      if (!c.valid()) break;
+      first = c.first();
+      last = c.last(p);
+      c.advance(p);
+      if (!mbar_wait(bar(C::kBarDL), t & 1, ctl, kSiteMmaPFull)) break;
+      if (!mbar_wait(bar(C::kBarVI), t & 1, ctl, kSiteMmaPFull)) break;
+      if (first && !mbar_wait(bar(C::kBarIF), (n + 1) & 1, ctl, kSiteMmaStage)) break;
+      if (!mbar_wait(bar(C::kBarXF + (t + 1) % 2), ((t + 1) / 2) & 1, ctl, kSiteMmaStage)) break;
+      tc_fence_after();
+      issue1(t + 1);
+      tc_commit(bar(C::kBarTF));
+      if (last) tc_commit(bar(C::kBarIE));
+      if (first) ++n;
+    }
+  }
+  tc_commit(bar(C::kBarDrain));
+  mbar_drain_wait(bar(C::kBarDrain), 0);
+}
+
+// dK/dV walk, second issuing thread: dV += E1 dO once E1 is written, dK += E2 Q once E2 is.
+template <int BLK, int D>
+__device__ __forceinline__ void diff_kv_mma2(const DiffBwdParams& p, uint32_t sbase, uint32_t tmem,
+                                             const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, true>;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const uint64_t x_desc = sdesc_sw128(sbase + C::kOffX, C::kXPlane, 1024);
+  const uint64_t y_desc = sdesc_sw128(sbase + C::kOffY, C::kYPlane, 1024);
+  const uint32_t hi = static_cast<uint32_t>(x_desc >> 32);
+  const uint32_t x0 = static_cast<uint32_t>(x_desc), y0 = static_cast<uint32_t>(y_desc);
+  DiffKvCursor<C::kHalves> c;
+  c.init(p);
+  int n = -1;
+  for (int t = 0; c.valid(); ++t) {
+    const bool first = c.first();
+    c.advance(p);
+    if (first) ++n;
+    const uint32_t t1 = tmem + ((t & 1) ? C::kT2 : C::kT1);
+    if (!mbar_wait(bar(C::kBarEF1), t & 1, ctl, kSiteMmaPFull)) break;
+    if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < 4; ++kk)
+      tc_mma_ts_lh(tmem + C::kAcc1, t1 + kk * 8, y0 + (t % 2) * (C::kYTile >> 4) + ((kk * 16 * 128) >> 4),
+                   hi, C::kIdescAcc, (first && kk == 0) ? 0u : 1u);
+    mbar_arrive(bar(C::kBarVI));
+    if (!mbar_wait(bar(C::kBarEF), t & 1, ctl, kSiteMmaPFull)) break;
+    tc_fence_after();
+#pragma unroll
+    for (int kk = 0; kk < 8; ++kk)
+      tc_mma_ts_lh(tmem + C::kAcc2, t1 + 64 + kk * 8,
+                   x0 + (t % 2) * (C::kXTile >> 4) + ((kk * 16 * 128) >> 4), hi, C::kIdescAcc,
+                   (first && kk == 0) ? 0u : 1u);
+    tc_commit(bar(C::kBarAD));
+    tc_commit(bar(C::kBarXE + t % 2));
+  }
+  tc_commit(bar(C::kBarDrain2));
+  mbar_drain_wait(bar(C::kBarDrain2), 0);
+}
+
+// ----------------------------------------------------------- elementwise warps
+
+template <int BLK, int D, bool SPLIT>
+__device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint32_t sbase,
+                                                    uint32_t tmem, const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, false>;
+  constexpr int G = C::kG, DQ = SPLIT ? D / 2 : D;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const int wg = ((threadIdx.x >> 5) - 2) >> 2;
+  const int wq = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31;
+  const int half = lane >> 4;
+  // Row 64 a + 32 m + r of the tile is query 32 a + r under map m.
+  const int map = wq & 1;
+  const int qin = 32 * (wq >> 1) + wg * 16 + (lane & 15);
+  const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32 + wg * 16) << 16);
+  const int kbase = (BLK == 128) ? 64 * half : 0;
+  const int tiles = diff_vec_tiles((p.L + 63) / 64);
+  auto warp_arrive = [&](int b) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+  auto wait_bar = [&](int b, int parity, int site) -> bool {
+    bool w = mbar_wait(bar(b), parity, ctl, site);
+    w = __all_sync(0xffffffffu, w);
+    if (w) tc_fence_after();
+    return w;
+  };
+  // This thread's 32-column groups of an accumulator row (read_o's) that are the row's dQ: all
+  // of them, or (SPLIT) its map's half.
+  auto store_dq = [&](int64_t pair, int q, const uint32_t (&pk)[D / 4]) {
+    if (q >= p.L) return;
+    __nv_bfloat16* r = static_cast<__nv_bfloat16*>(p.dq) + ((2 * pair + map) * p.L + q) * DQ + half * 32;
+#pragma unroll
+    for (int c = 0; c < D / 64; ++c) {
+      if (SPLIT && c != map) continue;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *reinterpret_cast<uint4*>(r + (SPLIT ? 0 : c * 64) + i * 8) =
+            make_uint4(pk[16 * c + 4 * i], pk[16 * c + 4 * i + 1], pk[16 * c + 4 * i + 2],
+                       pk[16 * c + 4 * i + 3]);
+    }
+  };
+  // The previous item's accumulator goes out at the next item's first step, once that step's E
+  // is handed over.
+  bool pending = false;
+  int64_t ppair = 0;
+  int pq = 0, pg = 0;  // its query and last step
+  auto read_pending = [&]() -> bool {
+    if (!wait_bar(C::kBarAD + (pg & 1), (pg / 2) & 1, kSiteSoftItemDone)) return false;
+    uint32_t pk[D / 4];
+    read_o<D>(tl + C::kAcc1, p.scale, pk);
+    warp_arrive(C::kBarAR);
+    store_dq(ppair, pq, pk);
+    pending = false;
+    return true;
+  };
+
+  int g = 0;
+  bool ok = true;
+  ItemStream is;
+  for (is.init<false>(p); ok && !is.done(); is.next<false>(p)) {
+    const int cnt = is.nnz();
+    const int64_t pair = is.cur.x;
+    const int q = is.cur.y * 64 + qin;
+    if (cnt == 0) {
+      const uint32_t zero[D / 4] = {};
+      store_dq(pair, q, zero);
+      if (map == 1 && half == 0 && q < p.L) p.dlam[pair * p.L + q] = 0.f;
+      continue;
+    }
+    const float* v = p.vec + (pair * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + (qin & 31);
+    const float lr = v[32 * map], dr = v[64 + 32 * map];
+    const float w = map ? -v[128] : 1.f;
+    const int dpos = p.causal_diag ? is.dpos() : -1;
+    const int qblk = qin + (BLK == 128 ? (is.cur.y & 1) * 64 : 0);
+    const int nsteps = (cnt + G - 1) / G;
+    float rsum = 0.f;  // of P dP
+    for (int s = 0; s < nsteps; ++s, ++g) {
+      const int nblk = step_blocks<G>(cnt, s);
+      const bool valid = (BLK == 128) || (half < nblk);
+      const bool diag = valid && (((BLK == 128) ? s : s * 2 + half) == dpos);
+      if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) {
+        ok = false;
+        break;
+      }
+      const uint32_t t1 = tl + ((g & 1) ? C::kT1b : C::kT1);
+      uint32_t rs[64], rp[64];
+      tmem_ld_16x32bx2_x32<64>(t1, *reinterpret_cast<uint32_t(*)[32]>(rs));
+      tmem_ld_16x32bx2_x32<64>(t1 + 32, *reinterpret_cast<uint32_t(*)[32]>(rs + 32));
+      tmem_ld_16x32bx2_x32<64>(tl + C::kT2, *reinterpret_cast<uint32_t(*)[32]>(rp));
+      tmem_ld_16x32bx2_x32<64>(tl + C::kT2 + 32, *reinterpret_cast<uint32_t(*)[32]>(rp + 32));
+      tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rs));
+      tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rs + 32));
+      tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp));
+      tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp + 32));
+      const int hi = diag ? qblk - kbase : (1 << 30);  // keys after the query: masked
+      uint32_t pk1[32];
+      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        float ds[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const int cc = 2 * i + u;
+          // masked after scaling, so that a negative scale cannot turn -inf into +inf
+          const float y = mask_outside(__uint_as_float(rs[cc]) * p.scale_log2 - lr, cc, -(1 << 30), hi);
+          const float pe = valid ? ex2_approx(y) : 0.f;
+          const float dp = valid ? __uint_as_float(rp[cc]) : 0.f;
+          sums[cc & 3] = fmaf(pe, dp, sums[cc & 3]);
+          ds[u] = pe * w * (dp - dr);
+        }
+        pk1[i] = pack_bf16x2(ds[0], ds[1]);
+      }
+      rsum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      tmem_st_16x32bx2_x32<32>(t1, pk1);
+      tmem_st_wait();
+      // The previous step's dQ product issued (its issuer cannot fall two phases behind).
+      if (g >= 1 && !wait_bar(C::kBarQI, (g - 1) & 1, kSiteSoftSFull)) {
+        ok = false;
+        break;
+      }
+      warp_arrive(C::kBarEF);
+      if (s == 0 && pending && !read_pending()) {
+        ok = false;
+        break;
+      }
+    }
+    if (!ok) break;
+    rsum += __shfl_xor_sync(0xffffffffu, rsum, 16);
+    if (map == 1 && half == 0 && q < p.L) p.dlam[pair * p.L + q] = -rsum;
+    pending = true;
+    ppair = pair;
+    pq = q;
+    pg = g - 1;
+  }
+  if (ok && pending) read_pending();
+  tmem_st_wait();
+}
+
+template <int BLK, int D>
+__device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint32_t sbase,
+                                                    const uint8_t* smem, uint32_t tmem,
+                                                    const WaitCtl& ctl) {
+  using C = DiffBwdCfg<BLK, D, true>;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const int wg = ((threadIdx.x >> 5) - 2) >> 2;
+  const int wq = (threadIdx.x >> 5) & 3;
+  const int lane = threadIdx.x & 31;
+  const int half = lane >> 4;
+  const int row = (BLK == 128) ? (wq * 32 + wg * 16 + (lane & 15)) : (wq * 16 + (lane & 15));
+  const uint32_t tl = tmem + (static_cast<uint32_t>(wq * 32 + (BLK == 128 ? wg * 16 : 0)) << 16);
+  auto warp_arrive = [&](int b) {
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar(b));
+  };
+  auto wait_bar = [&](int b, int parity, int site) -> bool {
+    bool w = mbar_wait(bar(b), parity, ctl, site);
+    w = __all_sync(0xffffffffu, w);
+    if (w) tc_fence_after();
+    return w;
+  };
+
+  int g = 0;
+  bool ok = true;
+  ItemStream is;
+  for (is.init<false>(p); ok && !is.done(); is.next<false>(p)) {
+    const int cnt = is.nnz();
+    const int key = is.cur.y * BLK + row;
+    const int64_t orow = static_cast<int64_t>(is.cur.x) * p.L + key;
+    if (cnt == 0) {
+      if (key < p.L) {
+        uint4* k = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + orow * D + half * (D / 2));
+        uint4* v = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + orow * D + half * (D / 2));
+#pragma unroll
+        for (int c = 0; c < D / 16; ++c) k[c] = v[c] = make_uint4(0, 0, 0, 0);
+      }
+      continue;
+    }
+    const int dpos = p.causal_diag ? is.dpos() : -1;
+    const int nsteps = p.pairs * cnt * C::kHalves;
+    int e = 0, hs = 0;  // place in the column, half of the block
+    for (int s = 0; s < nsteps; ++s, ++g) {
+      const uint32_t t1 = tl + ((g & 1) ? C::kT2 : C::kT1);
+      const uint32_t t2 = tl + ((g & 1) ? C::kT1 : C::kT2);
+      // Of this half's 32 queries those before the key are masked in the diagonal block.
+      const int lo = (e == dpos) ? row - 64 * hs - 32 * half : -(1 << 30);
+      if (++hs == C::kHalves) {
+        hs = 0;
+        if (++e == cnt) e = 0;
+      }
+      const float4* vec = reinterpret_cast<const float4*>(smem + C::kOffVec + (g % 2) * C::kVecB +
+                                                          half * (kDiffVecHalf * 4));
+      if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) {
+        ok = false;
+        break;
+      }
+      uint32_t rs[2][32];  // S^T, then P^T, of each map
+      tmem_ld_16x32bx2_x32<64>(t1, rs[0]);
+      tmem_ld_16x32bx2_x32<64>(t1 + 32, rs[1]);
+      tmem_ld_wait(rs[0]);
+      tmem_ld_wait(rs[1]);
+      // E1 = P_0^T - lam P_1^T, handed over on its own so that dV's product runs while dS^T is
+      // formed.  The second map's P is kept with its weight -lam.
+      {
+        uint32_t pk[16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const float4 l0 = vec[i], l1 = vec[8 + i], lm = vec[32 + i];
+          const float a0[4] = {l0.x, l0.y, l0.z, l0.w}, a1[4] = {l1.x, l1.y, l1.z, l1.w};
+          const float am[4] = {lm.x, lm.y, lm.z, lm.w};
+          float c[4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) {
+            const int cc = 4 * i + u;
+            const float y0 = mask_outside(fmaf(__uint_as_float(rs[0][cc]), p.scale_log2, -a0[u]), cc, lo, 1 << 30);
+            const float y1 = mask_outside(fmaf(__uint_as_float(rs[1][cc]), p.scale_log2, -a1[u]), cc, lo, 1 << 30);
+            const float p0 = ex2_approx(y0), p1 = -am[u] * ex2_approx(y1);
+            rs[0][cc] = __float_as_uint(p0);
+            rs[1][cc] = __float_as_uint(p1);
+            c[u] = p0 + p1;
+          }
+          pk[2 * i] = pack_bf16x2(c[0], c[1]);
+          pk[2 * i + 1] = pack_bf16x2(c[2], c[3]);
+        }
+        tmem_st_16x32bx2_x16<16>(t1, pk);
+      }
+      tmem_st_wait();
+      warp_arrive(C::kBarEF1);
+      if (!wait_bar(C::kBarDF, g & 1, kSiteSoftSFull)) {
+        ok = false;
+        break;
+      }
+      uint32_t rp[32];  // dP^T
+      tmem_ld_16x32bx2_x32<32>(t2, rp);
+      tmem_ld_wait(rp);
+      warp_arrive(C::kBarDL);  // T2 may now take the next step's S^T
+      {
+        uint32_t pk[32];
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float4 dd = vec[16 + 8 * m + i];
+            const float a[4] = {dd.x, dd.y, dd.z, dd.w};
+            float c[4];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+              c[u] = __uint_as_float(rs[m][4 * i + u]) * (__uint_as_float(rp[4 * i + u]) - a[u]);
+            pk[16 * m + 2 * i] = pack_bf16x2(c[0], c[1]);
+            pk[16 * m + 2 * i + 1] = pack_bf16x2(c[2], c[3]);
+          }
+        tmem_st_16x32bx2_x32<32>(t1 + 64, pk);
+      }
+      tmem_st_wait();
+      warp_arrive(C::kBarEF);
+    }
+    if (!ok) break;
+    // Complete once the last step's products are.
+    if (!wait_bar(C::kBarAD, (g - 1) & 1, kSiteSoftItemDone)) break;
+    uint32_t pk[D / 4], pk2[D / 4];
+    read_o<D>(tl + C::kAcc1, 1.f, pk);
+    read_o<D>(tl + C::kAcc2, p.scale, pk2);
+    warp_arrive(C::kBarAR);
+    if (key < p.L) {
+      store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dv) + orow * D, 0, half, pk);
+      store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dk) + orow * D, 0, half, pk2);
+    }
+  }
+  tmem_st_wait();
+}
+
+// ------------------------------------------------------------------- kernel
+
+// a, b: the item tiles' tensors (dQ: q, dO; dK/dV: k, v), x, y the step tiles' (dQ: k, v;
+// dK/dV: q, dO).
+template <int BLK, int D, bool SPLIT, bool KV>
+__global__ void __launch_bounds__(DiffBwdCfg<BLK, D, KV>::kThreads, 1)
+    bsa_diff_bwd_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                        const __grid_constant__ CUtensorMap tm_x, const __grid_constant__ CUtensorMap tm_y,
+                        const DiffBwdParams p) {
+  using C = DiffBwdCfg<BLK, D, KV>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  const uint32_t sbase = smem_u32(smem);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + C::kOffBar + C::kNumBars * 8);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5;
+  const int lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+    for (int i = 0; i < C::kNumBars; ++i)
+      mbar_init(bar(i), (i == C::kBarEF || i == C::kBarAR || i == C::kBarEF1 || i == C::kBarDL)
+                           ? C::kEwWarps
+                           : 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    tma_prefetch_desc(&tm_a);
+    tma_prefetch_desc(&tm_b);
+    tma_prefetch_desc(&tm_x);
+    tma_prefetch_desc(&tm_y);
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  if constexpr (SPLIT) {  // the column halves of Q that no copy writes
+    const int bytes = KV ? C::kNX * C::kXTile : C::kItemTile;
+    for (int i = threadIdx.x; i < bytes / 16; i += C::kThreads)
+      reinterpret_cast<uint4*>(smem + (KV ? C::kOffX : C::kOffA))[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, p.expire_site};
+  if (warp == 0) {
+    if (lane == 0) {
+      if constexpr (KV) diff_kv_producer<BLK, D, SPLIT>(p, &tm_a, &tm_b, &tm_x, &tm_y, sbase, ctl);
+      else diff_dq_producer<BLK, D, SPLIT>(p, &tm_a, &tm_b, &tm_x, &tm_y, sbase, ctl);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      if constexpr (KV) diff_kv_mma<BLK, D>(p, sbase, tmem, ctl);
+      else diff_dq_mma<BLK, D>(p, sbase, tmem, ctl);
+    }
+  } else if (warp == C::kMma2Warp) {
+    if (lane == 0) {
+      if constexpr (KV) diff_kv_mma2<BLK, D>(p, sbase, tmem, ctl);
+      else diff_dq_mma2<BLK, D>(p, sbase, tmem, ctl);
+    }
+  } else {
+    if constexpr (KV) diff_kv_elementwise<BLK, D>(p, sbase, smem, tmem, ctl);
+    else diff_dq_elementwise<BLK, D, SPLIT>(p, sbase, tmem, ctl);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int BLK, int D, bool SPLIT, bool KV>
+cudaError_t launch_diff_bwd(const DiffBwdParams& p, const CUtensorMap& a, const CUtensorMap& b,
+                            const CUtensorMap& x, const CUtensorMap& y, int grid, cudaStream_t stream) {
+  using C = DiffBwdCfg<BLK, D, KV>;
+  auto* kernel = bsa_diff_bwd_kernel<BLK, D, SPLIT, KV>;
+  static int done[64] = {0};
+  const cudaError_t e = set_smem_once(kernel, C::kLaunchSmem, done);
+  if (e != cudaSuccess) return e;
+  kernel<<<grid, C::kThreads, C::kLaunchSmem, stream>>>(a, b, x, y, p);
+  return cudaGetLastError();
+}
+
+}  // namespace bsa

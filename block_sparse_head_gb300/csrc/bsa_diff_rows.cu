@@ -1,0 +1,100 @@
+// bsa_diff_rows.cu -- row terms of the backward of differential attention, and the sum of the
+// weight's gradient.
+#include <cuda_bf16.h>
+
+#include "bsa_internal.h"
+
+namespace bsa {
+namespace {
+
+// Per query: D_1 = sum dO O_1, D_0 = sum dO out + lam D_1 (out = O_0 - lam O_1), the two lse in
+// log2 units and lam, laid out as the kernels read them.  Bound: memory, 6 d bytes a query.
+// D / 8 lanes a row, 16-byte loads.
+template <int D>
+__global__ void __launch_bounds__(256) bsa_diff_rows_kernel(const DiffRowsParams p) {
+  constexpr int R = D / 8;
+  constexpr float kLog2e = 1.4426950408889634f;
+  const int lane = threadIdx.x & 31;
+  const int tiles = diff_vec_tiles((p.L + 63) / 64);
+  const int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / R) + threadIdx.x / R;
+  const int64_t pair = r / (64 * tiles);
+  const int q = static_cast<int>(r - pair * (64 * tiles));
+  const bool in = pair < p.pairs, live = in && q < p.L;
+  float a0 = 0.f, a1 = 0.f;
+  if (live) {
+    const int64_t at = (pair * p.L + q) * D + (lane % R) * 8;
+    const uint4 o = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.out) + at);
+    const uint4 o2 = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.out2) + at);
+    const uint4 g = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.dout) + at);
+    const __nv_bfloat162* vo = reinterpret_cast<const __nv_bfloat162*>(&o);
+    const __nv_bfloat162* vo2 = reinterpret_cast<const __nv_bfloat162*>(&o2);
+    const __nv_bfloat162* vg = reinterpret_cast<const __nv_bfloat162*>(&g);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = __bfloat1622float2(vo[i]), y = __bfloat1622float2(vo2[i]);
+      const float2 z = __bfloat1622float2(vg[i]);
+      a0 = fmaf(z.x, x.x, fmaf(z.y, x.y, a0));
+      a1 = fmaf(z.x, y.x, fmaf(z.y, y.y, a1));
+    }
+  }
+#pragma unroll
+  for (int w = R / 2; w >= 1; w /= 2) {
+    a0 += __shfl_xor_sync(0xffffffffu, a0, w);
+    a1 += __shfl_xor_sync(0xffffffffu, a1, w);
+  }
+  if (!in || lane % R >= 5) return;
+  // Lane i of a row writes term i.  Rows past the end, and rows without an active key, get
+  // lse = +inf: their P is 0.
+  const int i = lane % R;
+  const float lam = live ? (p.lam_rows ? p.lam[pair * p.L + q] : p.lam[pair % p.H]) : 0.f;
+  float x;
+  if (i < 2) {
+    x = live ? p.lse[(2 * pair + i) * p.L + q] * kLog2e : INFINITY;
+    if (x == -INFINITY) x = INFINITY;
+  } else {
+    x = i == 2 ? fmaf(lam, a1, a0) : i == 3 ? a1 : lam;
+  }
+  p.vec[(pair * tiles + (q >> 6)) * kDiffVecFloats + ((q >> 5) & 1) * (kDiffVecFloats / 2) + 32 * i +
+        (q & 31)] = x;
+}
+
+// One CTA a head; fp64 sums in a fixed order.
+__global__ void __launch_bounds__(256) bsa_diff_lam_kernel(const float* __restrict__ rows,
+                                                           float* __restrict__ dlam, int B, int H,
+                                                           int L) {
+  __shared__ double part[8];
+  double s = 0.0;
+  for (int b = 0; b < B; ++b) {
+    const float* r = rows + (static_cast<int64_t>(b) * H + blockIdx.x) * L;
+    for (int i = threadIdx.x; i < L; i += 256) s += static_cast<double>(r[i]);
+  }
+#pragma unroll
+  for (int w = 16; w >= 1; w /= 2) s += __shfl_xor_sync(0xffffffffu, s, w);
+  if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < 8; ++w) s += part[w];
+    dlam[blockIdx.x] = static_cast<float>(s);
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream) {
+  const int64_t rows = p.pairs * 64 * diff_vec_tiles((p.L + 63) / 64);
+  const int per = 256 / (p.d / 8);
+  const int64_t grid = (rows + per - 1) / per;
+  if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
+  if (p.d == 128)
+    bsa_diff_rows_kernel<128><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+  else
+    bsa_diff_rows_kernel<64><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_diff_lam(const float* rows, float* dlam, int B, int H, int L, cudaStream_t stream) {
+  bsa_diff_lam_kernel<<<H, 256, 0, stream>>>(rows, dlam, B, H, L);
+  return cudaGetLastError();
+}
+
+}  // namespace bsa

@@ -166,6 +166,16 @@ __device__ __forceinline__ int step_blocks(int nnz, int s) {
   return rem < G ? rem : G;
 }
 
+// This CTA's share [x, y) of a work list, and its item u.
+template <class P>
+__device__ __forceinline__ int2 stream_range(const P& p) {
+  return make_int2(p.cta_start[blockIdx.x], p.cta_start[blockIdx.x + 1]);
+}
+template <class P>
+__device__ __forceinline__ int4 stream_item(const P& p, int u) {
+  return p.items[u];
+}
+
 // The CTA's share of the work list: items[cta_start[c] .. cta_start[c+1]) for CTA c, as
 // device records {bh, i, rs, nnz | (dpos + 1) << 16}: the item's (batch, head) pair
 // bh = b * H + h and query block i (its rows start at row bh * Lq + i * QB of Q and O;
@@ -180,10 +190,11 @@ struct ItemStream {
   int4 nx1;
   int4 nx2;
 
-  // P: any kernel-argument struct with `items` and `cta_start` (forward or backward).
+  // P: any kernel-argument struct with `items` and `cta_start` (forward or backward), or one
+  // with overloads of stream_range and stream_item of its own.
   template <class P>
   __device__ __forceinline__ int4 fetch(const P& p, int u) const {
-    return u < end ? p.items[u] : make_int4(0, 0, 0, -1);
+    return u < end ? stream_item(p, u) : make_int4(0, 0, 0, -1);
   }
   // Moves to the next item (kSkipEmpty: the next one with active blocks).
   template <bool kSkipEmpty, class P>
@@ -199,8 +210,9 @@ struct ItemStream {
   }
   template <bool kSkipEmpty, class P>
   __device__ __forceinline__ void init(const P& p) {
-    t = p.cta_start[blockIdx.x] - 1;
-    end = p.cta_start[blockIdx.x + 1];
+    const int2 range = stream_range(p);
+    t = range.x - 1;
+    end = range.y;
     n = -1;
     nx1 = fetch(p, t + 1);
     nx2 = fetch(p, t + 2);
@@ -354,8 +366,8 @@ struct MmaDescs {
 };
 
 // S(t) = Q K(t)^T into S[t % 3].
-template <int QB, int KB, int D>
-__device__ __forceinline__ void fwd_mma_s(const FwdParams& p, uint32_t sbase, uint32_t tmem,
+template <int QB, int KB, int D, class P>
+__device__ __forceinline__ void fwd_mma_s(const P& p, uint32_t sbase, uint32_t tmem,
                                           const WaitCtl& ctl) {
   using C = FwdCfg<QB, KB, D>;
   constexpr int G = C::kG;
@@ -406,8 +418,8 @@ __device__ __forceinline__ void fwd_mma_s(const FwdParams& p, uint32_t sbase, ui
 }
 
 // O += P(g) V(g), P read from S[g % 3].
-template <int QB, int KB, int D>
-__device__ __forceinline__ void fwd_mma_pv(const FwdParams& p, uint32_t sbase, uint32_t tmem,
+template <int QB, int KB, int D, class P>
+__device__ __forceinline__ void fwd_mma_pv(const P& p, uint32_t sbase, uint32_t tmem,
                                            const WaitCtl& ctl) {
   using C = FwdCfg<QB, KB, D>;
   constexpr int G = C::kG;

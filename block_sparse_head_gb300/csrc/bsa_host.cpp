@@ -65,6 +65,23 @@ bool encode_rows(CUtensorMap* map, const void* base, int64_t rows, int d, int bo
 
 }  // namespace
 
+bool bsa::encode_heads(CUtensorMap* map, const void* base, int64_t heads, int64_t L, int d,
+                       int box_rows, int box_halves) {
+  auto fn = encode_fn();
+  if (fn == nullptr) return false;
+  const cuuint64_t dims[4] = {64, static_cast<cuuint64_t>(L), static_cast<cuuint64_t>(d / 64),
+                              static_cast<cuuint64_t>(heads)};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(d) * 2, 128,
+                                 static_cast<cuuint64_t>(L) * d * 2};
+  const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(box_halves), 1};
+  const cuuint32_t estr[4] = {1, 1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void*>(base), dims, strides, box,
+            estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 bool bsa::encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int page, int d,
                        int rows) {
   PFN_cuTensorMapEncodeTiled_v12000 fn = encode_fn();
@@ -232,6 +249,8 @@ namespace {
 void free_device(bsa_lut* lut) {
   if (lut->d_row_ptr) cudaFree(lut->d_row_ptr);
   if (lut->d_row_idx) cudaFree(lut->d_row_idx);
+  if (lut->d_list) cudaFree(lut->d_list);
+  lut->d_list = nullptr;
   lut->d_row_ptr = lut->d_row_idx = nullptr;
   for (int o = 0; o < 2; ++o) {
     if (lut->d_items_t[o]) cudaFree(lut->d_items_t[o]);
@@ -419,7 +438,9 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
   if (sms <= 0) return BSA_ERR_CUDA;
   lut->sched_grid = std::max(1, std::min(lut->n_items, sms));
   std::vector<int32_t>* rec = lut->sched_records;  // device records of both schedules
+  std::vector<int32_t> list;                       // and of the work list itself
   try {
+    bsa::device_records(*lut, lut->items, list);
     for (int o = 0; o < 2; ++o) {
       bsa::build_schedule(*lut, lut->sched_grid, o == 1, lut->sched_items[o], lut->sched_start[o]);
       bsa::device_records(*lut, lut->sched_items[o], rec[o]);
@@ -437,7 +458,8 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
       cudaMalloc(&lut->d_status, 16) != cudaSuccess ||
       cudaMalloc(&lut->d_sched_start, ns) != cudaSuccess ||
       cudaMalloc(&lut->d_items_g, ni) != cudaSuccess ||
-      cudaMalloc(&lut->d_sched_start_g, ns) != cudaSuccess) {
+      cudaMalloc(&lut->d_sched_start_g, ns) != cudaSuccess ||
+      cudaMalloc(&lut->d_list, ni) != cudaSuccess) {
     free_device(lut);
     cudaGetLastError();
     return BSA_ERR_ALLOC;
@@ -451,7 +473,9 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
              (cudaMemcpyAsync(lut->d_items, rec[0].data(), rec[0].size() * 4,
                               cudaMemcpyHostToDevice, st) == cudaSuccess &&
               cudaMemcpyAsync(lut->d_items_g, rec[1].data(), rec[1].size() * 4,
-                              cudaMemcpyHostToDevice, st) == cudaSuccess)) &&
+                              cudaMemcpyHostToDevice, st) == cudaSuccess &&
+              cudaMemcpyAsync(lut->d_list, list.data(), list.size() * 4, cudaMemcpyHostToDevice,
+                              st) == cudaSuccess)) &&
             cudaMemcpyAsync(lut->d_sched_start, lut->sched_start[0].data(), ns,
                             cudaMemcpyHostToDevice, st) == cudaSuccess &&
             cudaMemcpyAsync(lut->d_sched_start_g, lut->sched_start[1].data(), ns,

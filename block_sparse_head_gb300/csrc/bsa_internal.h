@@ -46,6 +46,7 @@ struct bsa_lut {
   int32_t* d_row_idx = nullptr;        // column view: row_idx
   int32_t* d_items_t[2] = {nullptr, nullptr};        // records of both column schedules
   int32_t* d_sched_start_t[2] = {nullptr, nullptr};
+  int32_t* d_list = nullptr;           // records of items, in work-list order
   uint64_t wait_limit_ns = 10000000000ull;
   int expire_site = 0;  // bsa_debug_expire_wait
 };
@@ -163,6 +164,92 @@ cudaError_t launch_fwd_q128_k64_d64(bool ext, const FwdParams& p, const CUtensor
 cudaError_t launch_fwd_q128_k64_d128(bool ext, const FwdParams& p, const CUtensorMap& q,
                                     const CUtensorMap& k, const CUtensorMap& v, int grid,
                                     cudaStream_t stream);
+
+// Differential attention.  Its tiles hold 64 queries of both maps of a head (128 rows); the
+// work list of its forward and of its dQ walk is the LUT's, every item taken once for each
+// head of its kv head and, at block 128, for each half of its query block.
+struct DiffList {
+  const int4* list;    // records of the LUT's items in work-list order
+  int n;               // sub-items: n_items * pairs * halves
+  int pairs;           // heads of a kv head
+  int halves;          // block / 64
+};
+
+struct DiffFwdParams : DiffList {
+  const int32_t* col_idx;
+  void* out;           // bf16 [B,H,L,d]
+  void* out2;          // bf16 [B,H,L,d]: the second map's output, or null
+  float* lse;          // fp32 [B,2H,L]
+  const float* lam;    // [H], or [B,H,L] (lam_rows)
+  int32_t* status;
+  float scale_log2;    // scale * log2(e)
+  int causal_diag, lam_rows;
+  int H, L;
+  unsigned long long wait_limit_ns;
+  int expire_site;
+};
+
+// (block, d) instances; split: the queries have d / 2 numbers, a key half for each map.
+#define BSA_DIFF_FWD(name)                                                                     \
+  cudaError_t launch_diff_fwd_##name(bool split, const DiffFwdParams& p, const CUtensorMap& q, \
+                                     const CUtensorMap& k, const CUtensorMap& v, int grid,     \
+                                     cudaStream_t stream)
+BSA_DIFF_FWD(b64_d64);
+BSA_DIFF_FWD(b64_d128);
+BSA_DIFF_FWD(b128_d64);
+BSA_DIFF_FWD(b128_d128);
+#undef BSA_DIFF_FWD
+
+// Row terms of the backward, fp32 [B * H][diff_vec_tiles][kDiffVecFloats]: 64 queries a tile,
+// a whole block of 128 in any case.
+constexpr int kDiffVecFloats = 328;
+__host__ __device__ inline int diff_vec_tiles(int tiles) { return (tiles + 1) & ~1; }
+
+struct DiffBwdParams : DiffList {
+  const int4* items;         // dK/dV walk: the plain backward's column work list (else null)
+  const int32_t* cta_start;
+  const int32_t* col_idx;    // dQ: key blocks of each row; dK/dV: query blocks of each column
+  const float* vec;          // row terms
+  void* dq;                  // dQ walk: bf16 [B,2H,L,dq]
+  float* dlam;               // and fp32 [B,H,L]
+  void* dk;                  // dK/dV walk: bf16 [B,Hkv,L,d]
+  void* dv;
+  int32_t* status;
+  float scale_log2, scale;
+  int causal_diag, L;
+  unsigned long long wait_limit_ns;
+  int expire_site;
+};
+// a, b, x, y: q, dO, k, v (dQ walk) or k, v, q, dO (kv).
+#define BSA_DIFF_BWD(name)                                                                      \
+  cudaError_t launch_diff_bwd_##name(bool split, bool kv, const DiffBwdParams& p,               \
+                                     const CUtensorMap& a, const CUtensorMap& b,                \
+                                     const CUtensorMap& x, const CUtensorMap& y, int grid,      \
+                                     cudaStream_t stream)
+BSA_DIFF_BWD(b64_d64);
+BSA_DIFF_BWD(b64_d128);
+BSA_DIFF_BWD(b128_d64);
+BSA_DIFF_BWD(b128_d128);
+#undef BSA_DIFF_BWD
+
+struct DiffRowsParams {
+  const void* out;   // bf16 [B,H,L,d]
+  const void* out2;
+  const void* dout;
+  const float* lse;  // [B,2H,L]
+  const float* lam;  // [H] or [B,H,L]
+  float* vec;
+  int64_t pairs;     // B * H
+  int H, L, d, lam_rows;
+};
+cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream);
+// dlam[h] = sum over b and rows of rows[b, h, :], in a fixed order.
+cudaError_t launch_diff_lam(const float* rows, float* dlam, int B, int H, int L, cudaStream_t stream);
+
+// [heads, L, d] bf16 as four dimensions: 64 columns, rows, d/64 column halves, heads.  The box
+// is 64 columns x rows x halves of one head, 128-byte swizzled; rows past L read as zero.
+bool encode_heads(CUtensorMap* map, const void* base, int64_t heads, int64_t L, int d, int box_rows,
+                  int box_halves);
 
 // Backward kernel arguments besides the four tensor maps (item tiles A, B; step tiles X, Y).
 struct BwdParams {

@@ -264,6 +264,73 @@ int bsa_backward(const void* q, const void* k, const void* v, const void* out, c
                  void* stream);
 
 /*
+ * bsa_diff_forward -- block-sparse differential attention: the difference of two softmax maps
+ * over one value matrix, with a weight lam that the model learns.  Head h of H has two query
+ * maps, heads 2h and 2h+1 of q, and uses kv head g = h / (H / kv_heads).  With A(r) the active
+ * keys of row r under the layout of kv head g (bsa_forward's, with L any length: keys past the
+ * end are no keys) and map m in {0, 1}:
+ *
+ *   s_m[c]  = scale * <q[b,2h+m,r,:], key m of c>
+ *   lse_m   = ln sum_{c in A(r)} exp(s_m[c])                           (-inf when A(r) is empty)
+ *   O_m     = sum_{c in A(r)} exp(s_m[c] - lse_m) v[b,g,c,:]           (0 when A(r) is empty)
+ *   out[r]  = O_0 - lam O_1
+ *
+ *   q        device bf16 [B, 2H, L, dq].  dq = d: both maps score the whole key k[b,g,c,:].
+ *            dq = d/2 (d = 128): a key of its own for each map, key m being
+ *            k[b,g,c, m*dq : (m+1)*dq].
+ *   k, v     device bf16 [B, kv_heads, L, d].
+ *   lam      device fp32 [H], or with lam_rows nonzero [B, H, L] (a weight for each query).
+ *   lut      uploaded LUT of a square layout [kv_heads, nb, nb], nb = ceil(L / block), batch B.
+ *   out      device bf16 [B, H, L, d];  lse  device fp32 [B, 2H, L].
+ *   out2     device bf16 [B, H, L, d], receives O_1 for bsa_diff_backward; NULL: not kept.
+ *   B .. causal_diag  as bsa_forward; H a multiple of kv_heads, 2*B*H*L < 2^31.
+ *
+ * q, k, v, out, out2 16-byte aligned (lam, lse 4-byte); no output overlaps another tensor.  A
+ * NaN or an infinity among the keys or values of a block may reach every row that the block is
+ * active for, also rows that its diagonal masks.  P is rounded to bf16 before it meets V, as in
+ * bsa_forward, so an output that is far smaller than O_0 and lam O_1, its parts, keeps their
+ * absolute error.
+ * Asynchronous, one kernel launch, allocates nothing; the LUT's status word as in bsa_forward.
+ * Errors: as bsa_forward (BSA_ERR_UNSUPPORTED also for a scale whose product with log2 e is not
+ * finite in fp32, and for other dq).
+ */
+int bsa_diff_forward(const void* q, const void* k, const void* v, const float* lam,
+                     const bsa_lut* lut, void* out, float* lse, void* out2, int B, int H,
+                     int kv_heads, int L, int d, int dq, int lam_rows, float scale, int block,
+                     int causal_diag, void* stream);
+
+/*
+ * bsa_diff_backward -- gradients of bsa_diff_forward with respect to q, k, v and lam, given its
+ * out, out2 and lse and the upstream gradient dout.  With P_m the masked softmax of map m,
+ * recomputed from lse, w_0 = 1, w_1 = -lam:
+ *
+ *   D_1 = rowsum(dout * out2),  D_0 = rowsum(dout * out) + lam D_1,  dP = dout V^T
+ *   dS_m = w_m P_m (dP - D_m),  dq_m = scale dS_m K_m,
+ *   dk = scale sum of dS_m^T Q_m (dq = d: over both maps; dq = d/2: map m's in its half) and
+ *   dv = sum of (P_0 - lam P_1)^T dout, both over the heads of the kv head,
+ *   dlam = -rowsum(P_1 * dP), and without lam_rows its sum over batch and rows.
+ *
+ *   dq_out  device bf16 [B, 2H, L, dq];  dk, dv  bf16 [B, kv_heads, L, d];  dlam  fp32 [H] or
+ *           [B, H, L].  Every element is written; no order of summation depends on timing.
+ *   workspace  device, 16-byte aligned, of the size bsa_diff_workspace gives; any contents.
+ *           Calls that may overlap on the GPU need one each.
+ *   the others as in bsa_diff_forward.
+ *
+ * Asynchronous; three kernels, a fourth without lam_rows; allocates nothing.  Errors: as
+ * bsa_diff_forward, BSA_ERR_TOO_LARGE (workspace too small).
+ */
+int bsa_diff_backward(const void* q, const void* k, const void* v, const float* lam,
+                      const void* out, const void* out2, const float* lse, const void* dout,
+                      const bsa_lut* lut, void* dq_out, void* dk, void* dv, float* dlam,
+                      void* workspace, int64_t workspace_bytes, int B, int H, int kv_heads, int L,
+                      int d, int dq, int lam_rows, float scale, int block, int causal_diag,
+                      void* stream);
+
+/* bsa_diff_workspace -- bytes of workspace that bsa_diff_backward needs.  Errors: BSA_ERR_NULL,
+ * BSA_ERR_SHAPE. */
+int bsa_diff_workspace(int B, int H, int L, int64_t* bytes);
+
+/*
  * bsa_topk_forward -- top-k token-gather attention with an attention sink, the second
  * sparsity granularity of the pages: the sparse_attn kernel of the DeepSeek-V4.1
  * "Sparse attention / Weighted row sum" page.  Every query position lists K rows of its

@@ -20,3 +20,4 @@ from .bsa_oracle import (  # noqa: F401
 from .bsa_oracle_ext import element_mask, forward_ext, n_blocks  # noqa: F401,E402
 from .bsa_oracle_topk import topk_attention, topk_flops  # noqa: F401,E402
 from . import bsa_oracle_cache as cache  # noqa: F401,E402
+from . import bsa_oracle_diff as diff  # noqa: F401,E402
