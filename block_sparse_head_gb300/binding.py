@@ -100,7 +100,7 @@ def load_library():
         lib.bsa_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(i64)]
         lib.bsa_diff_forward.argtypes = [vp] * 8 + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
         lib.bsa_diff_backward.argtypes = [vp] * 14 + [i64] + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
-        lib.bsa_diff_workspace.argtypes = [ci, ci, ci, ctypes.POINTER(i64)]
+        lib.bsa_diff_workspace.argtypes = [ci] * 5 + [ctypes.POINTER(i64)]
         lib.bsa_lut_export_csc.argtypes = [vp, vp, vp, vp]
         lib.bsa_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
@@ -639,12 +639,13 @@ def diff_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.T
     return out, lse, out2
 
 
-def diff_workspace(B: int, H: int, L: int) -> torch.Tensor:
+def diff_workspace(B: int, H: int, L: int, d: int, block: int) -> torch.Tensor:
     """A workspace for diff_backward on the current device; calls that may overlap on the GPU
     need one each."""
     lib = _lib or load_library()
     n = ctypes.c_int64()
-    _check(lib.bsa_diff_workspace(int(B), int(H), int(L), ctypes.byref(n)), "bsa_diff_workspace")
+    _check(lib.bsa_diff_workspace(int(B), int(H), int(L), int(d), int(block), ctypes.byref(n)),
+           "bsa_diff_workspace")
     return torch.empty(n.value, dtype=torch.uint8, device=torch.device("cuda", torch.cuda.current_device()))
 
 
@@ -667,7 +668,7 @@ def diff_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
             dk = torch.empty(k.shape, dtype=bf16, device=where) if dk is None else dk
             dv = torch.empty(k.shape, dtype=bf16, device=where) if dv is None else dv
             dlam = torch.empty(lam_shape, dtype=f32, device=where) if dlam is None else dlam
-            workspace = diff_workspace(B, H, L) if workspace is None else workspace
+            workspace = diff_workspace(B, H, L, d, block) if workspace is None else workspace
     rows, keys = (B, H, L, d), (B, kv, L, d)
     ws_bytes = workspace.numel()
     _check(lib.bsa_diff_backward(

@@ -6,9 +6,9 @@
 //     dV = (P_0 - lam P_1)^T dO,   dlam = -D_1.
 // K, V and their gradients are shared by both maps and by the heads of a kv head.
 //
-// Three kernels: the row terms (below), dQ over the layout's rows, dK and dV over its columns.
-// The two walks are the plain backward's pipelines (bsa_bwd_kernel.cuh: roles, barriers, TMEM
-// regions) on tiles of 64 queries with both maps as 128 rows, row 64 a + 32 m + r being query
+// The row terms and the sums at the end are bsa_diff_rows.cu's; the two walks here are dQ over the
+// layout's rows and dK and dV over its columns.
+// Both are the plain backward's pipelines (bsa_bwd_kernel.cuh: roles, barriers, TMEM regions) on tiles of 64 queries with both maps as 128 rows, row 64 a + 32 m + r being query
 // 32 a + r under map m:
 //   dQ walk    item: such a tile, A = its Q, B = its dO (each row twice).  Step: 128 keys,
 //              X = K, Y = V.  T1 = A X^T, T2 = B Y^T, E = dS, acc += E X.  The row sums of
@@ -20,7 +20,10 @@
 //              are 32 queries under both maps, so that E1 = P_0^T - lam P_1^T, combined in fp32
 //              and rounded once, takes 64 columns (half the product of two maps apart), and
 //              E2 = dS^T 128.  acc1 += E1 Y = dV,  acc2 += E2 X = dK / scale: the sum over maps
-//              and heads stays in TMEM.
+//              and heads stays in TMEM.  A column's steps are its entries times heads times
+//              halves, and columns differ widely (a global one is seen by every row), so that
+//              the CTAs share the steps, not the columns out (diff_share): a share's cut columns
+//              leave fp32 pieces that bsa_diff_rows.cu joins in order.
 // Queries of d / 2 numbers are laid out over d columns, zero in the other map's half
 // (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
 // Rows past the end of the sequence read as zero and carry lse = +inf, so that their P is 0;
@@ -34,11 +37,10 @@
 namespace bsa {
 
 __device__ __forceinline__ int2 stream_range(const DiffBwdParams& p) {
-  if (p.items != nullptr) return make_int2(p.cta_start[blockIdx.x], p.cta_start[blockIdx.x + 1]);
   return stream_range(static_cast<const DiffList&>(p));
 }
 __device__ __forceinline__ int4 stream_item(const DiffBwdParams& p, int u) {
-  return p.items != nullptr ? p.items[u] : stream_item(static_cast<const DiffList&>(p), u);
+  return stream_item(static_cast<const DiffList&>(p), u);
 }
 
 // Row terms of 64 queries: two groups of 32, each [lse_0, lse_1 (log2 units), D_0, D_1, lam]
@@ -92,29 +94,63 @@ struct DiffBwdCfg {
   static constexpr uint32_t kIdescAcc = idesc_bf16_f32(kRows, D, false, true);  // B MN-major
 };
 
-// Steps of the dK/dV walk: of each item (b, kv head, key block) the heads of the kv head, the
-// query blocks of its column and the halves of a block.
-template <int HALVES>
-struct DiffKvCursor {
-  ItemStream is;
-  int pair, e, half;
+// This CTA's steps of the dK/dV walk (see diff_share), a column's end loaded one column ahead.
+struct DiffKvWalk {
+  long long left;    // steps still to go, this one among them
+  int per;           // steps of a column's entry: heads of the kv head times halves
+  int b, x, rest;    // batch, entry of row_idx, head * halves + half
+  int col, begin, end, next_end;  // column and its entries; the next column's end
+  bool first, head;  // first step of the piece; the piece begins the column
+  __device__ __forceinline__ int end_of(const DiffBwdParams& p, int c) const {
+    return c < p.cols ? p.col_ptr[c + 1] : 0;
+  }
   __device__ __forceinline__ void init(const DiffBwdParams& p) {
-    is.init<true>(p);
-    pair = e = half = 0;
+    const long long total = diff_steps(p), share = diff_share(p, gridDim.x);
+    const long long at = blockIdx.x * share;
+    left = total - at < share ? total - at : share;
+    if (left <= 0) return;
+    per = p.pairs * p.halves;
+    const long long entry = at / per;
+    rest = static_cast<int>(at - entry * per);
+    b = static_cast<int>(entry / p.nnz);
+    x = static_cast<int>(entry - static_cast<long long>(b) * p.nnz);
+    // the column with col_ptr[col] <= x < col_ptr[col + 1]
+    int lo = 0, hi = p.cols - 1;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (p.col_ptr[mid + 1] > x) hi = mid;
+      else lo = mid + 1;
+    }
+    col = lo;
+    begin = p.col_ptr[col];
+    end = p.col_ptr[col + 1];
+    next_end = end_of(p, col + 1);
+    first = true;
+    head = x == begin && rest == 0;
   }
+  __device__ __forceinline__ bool valid() const { return left > 0; }
+  __device__ __forceinline__ bool tail() const { return x + 1 == end && rest + 1 == per; }
+  __device__ __forceinline__ bool last() const { return left == 1 || tail(); }
   __device__ __forceinline__ void advance(const DiffBwdParams& p) {
-    if (++half < HALVES) return;
-    half = 0;
-    if (++e < is.nnz()) return;
-    e = 0;
-    if (++pair < p.pairs) return;
-    pair = 0;
-    is.next<true>(p);
-  }
-  __device__ __forceinline__ bool valid() const { return !is.done(); }
-  __device__ __forceinline__ bool first() const { return (pair | e | half) == 0; }
-  __device__ __forceinline__ bool last(const DiffBwdParams& p) const {
-    return half == HALVES - 1 && e == is.nnz() - 1 && pair == p.pairs - 1;
+    --left;
+    first = false;
+    if (++rest < per) return;
+    rest = 0;
+    if (++x < end || left <= 0) return;
+    first = head = true;
+    do {  // the next column with entries
+      if (++col == p.cols) {
+        col = 0;
+        ++b;
+        x = 0;
+        begin = 0;
+        end = p.col_ptr[1];
+      } else {
+        begin = end;
+        end = next_end;
+      }
+      next_end = end_of(p, col + 1);
+    } while (begin == end);
   }
 };
 
@@ -202,18 +238,19 @@ __device__ __forceinline__ void diff_kv_producer(const DiffBwdParams& p, const C
                                                  const WaitCtl& ctl) {
   using C = DiffBwdCfg<BLK, D, true>;
   auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
-  DiffKvCursor<C::kHalves> c;
+  DiffKvWalk c;
   c.init(p);
   const int tiles = (p.L + 63) / 64;
-  int n = -1, t = 0;  // items whose A was armed; steps armed
-  int nv = 0;         // items whose B was armed
+  int n = -1, t = 0;  // pieces whose A was armed; steps armed
+  int nv = 0;         // pieces whose B was armed
   for (; c.valid(); ++t) {
-    const int head = c.is.cur.x, key0 = c.is.cur.y * BLK;
-    const int pair = head * p.pairs + c.pair;
-    const int q64 = p.col_idx[c.is.cur.z + c.e] * C::kHalves + c.half;
-    const bool item_first = c.first();
+    const int kv = c.col / p.nb, head = c.b * (p.cols / p.nb) + kv;
+    const int key0 = (c.col - kv * p.nb) * BLK;
+    const int pair = head * p.pairs + c.rest / C::kHalves;
+    const int q64 = p.row_idx[c.x] * C::kHalves + c.rest % C::kHalves;
+    const bool item_first = c.first;
     if (item_first) {
-      // A is free once the previous item's last T1 is complete.
+      // A is free once the previous piece's last T1 is complete.
       if (n >= 0 && !mbar_wait(bar(C::kBarIE), n & 1, ctl, kSiteProdKEmpty)) break;
       const uint32_t fb = bar(C::kBarIF);
       mbar_arrive_expect_tx(fb, C::kItemTile);
@@ -375,11 +412,11 @@ __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sba
                                                            x0 + (t % 2) * (C::kXTile >> 4), hi,
                                                            C::kIdescT1, 1);
   };
-  DiffKvCursor<C::kHalves> c;
+  DiffKvWalk c;
   c.init(p);
   if (c.valid()) {
     int n = 0;
-    bool first = true, last = c.last(p);
+    bool first = true, last = c.last();
     c.advance(p);
     bool ok = mbar_wait(bar(C::kBarIF), 0, ctl, kSiteMmaStage) &&
               mbar_wait(bar(C::kBarXF), 0, ctl, kSiteMmaStage);
@@ -399,8 +436,8 @@ __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sba
       tc_commit(bar(C::kBarDF));
       if (last) tc_commit(bar(C::kBarIEV));
       if (!c.valid()) break;
-      first = c.first();
-      last = c.last(p);
+      first = c.first;
+      last = c.last();
       c.advance(p);
       if (!mbar_wait(bar(C::kBarDL), t & 1, ctl, kSiteMmaPFull)) break;
       if (!mbar_wait(bar(C::kBarVI), t & 1, ctl, kSiteMmaPFull)) break;
@@ -427,11 +464,11 @@ __device__ __forceinline__ void diff_kv_mma2(const DiffBwdParams& p, uint32_t sb
   const uint64_t y_desc = sdesc_sw128(sbase + C::kOffY, C::kYPlane, 1024);
   const uint32_t hi = static_cast<uint32_t>(x_desc >> 32);
   const uint32_t x0 = static_cast<uint32_t>(x_desc), y0 = static_cast<uint32_t>(y_desc);
-  DiffKvCursor<C::kHalves> c;
+  DiffKvWalk c;
   c.init(p);
   int n = -1;
   for (int t = 0; c.valid(); ++t) {
-    const bool first = c.first();
+    const bool first = c.first;
     c.advance(p);
     if (first) ++n;
     const uint32_t t1 = tmem + ((t & 1) ? C::kT2 : C::kT1);
@@ -622,111 +659,107 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     return w;
   };
 
-  int g = 0;
-  bool ok = true;
-  ItemStream is;
-  for (is.init<false>(p); ok && !is.done(); is.next<false>(p)) {
-    const int cnt = is.nnz();
-    const int key = is.cur.y * BLK + row;
-    const int64_t orow = static_cast<int64_t>(is.cur.x) * p.L + key;
-    if (cnt == 0) {
-      if (key < p.L) {
-        uint4* k = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dk) + orow * D + half * (D / 2));
-        uint4* v = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.dv) + orow * D + half * (D / 2));
+  DiffKvWalk c;
+  c.init(p);
+  int dpos = -1;
+  for (int g = 0; c.valid(); ++g) {
+    const uint32_t t1 = tl + ((g & 1) ? C::kT2 : C::kT1);
+    const uint32_t t2 = tl + ((g & 1) ? C::kT1 : C::kT2);
+    if (c.first && p.causal_diag) dpos = p.diag_pos[c.col];
+    // Of this half's 32 queries those before the key are masked in the diagonal block.
+    const int lo = (c.x - c.begin == dpos) ? row - 64 * (c.rest % C::kHalves) - 32 * half : -(1 << 30);
+    const float4* vec = reinterpret_cast<const float4*>(smem + C::kOffVec + (g % 2) * C::kVecB +
+                                                        half * (kDiffVecHalf * 4));
+    if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) break;
+    uint32_t rs[2][32];  // S^T, then P^T, of each map
+    tmem_ld_16x32bx2_x32<64>(t1, rs[0]);
+    tmem_ld_16x32bx2_x32<64>(t1 + 32, rs[1]);
+    tmem_ld_wait(rs[0]);
+    tmem_ld_wait(rs[1]);
+    // E1 = P_0^T - lam P_1^T, handed over on its own so that dV's product runs while dS^T is
+    // formed.  The second map's P is kept with its weight -lam.
+    {
+      uint32_t pk[16];
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) k[c] = v[c] = make_uint4(0, 0, 0, 0);
+      for (int i = 0; i < 8; ++i) {
+        const float4 l0 = vec[i], l1 = vec[8 + i], lm = vec[32 + i];
+        const float a0[4] = {l0.x, l0.y, l0.z, l0.w}, a1[4] = {l1.x, l1.y, l1.z, l1.w};
+        const float am[4] = {lm.x, lm.y, lm.z, lm.w};
+        float w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int cc = 4 * i + u;
+          const float y0 = mask_outside(fmaf(__uint_as_float(rs[0][cc]), p.scale_log2, -a0[u]), cc, lo, 1 << 30);
+          const float y1 = mask_outside(fmaf(__uint_as_float(rs[1][cc]), p.scale_log2, -a1[u]), cc, lo, 1 << 30);
+          const float p0 = ex2_approx(y0), p1 = -am[u] * ex2_approx(y1);
+          rs[0][cc] = __float_as_uint(p0);
+          rs[1][cc] = __float_as_uint(p1);
+          w[u] = p0 + p1;
+        }
+        pk[2 * i] = pack_bf16x2(w[0], w[1]);
+        pk[2 * i + 1] = pack_bf16x2(w[2], w[3]);
       }
-      continue;
+      tmem_st_16x32bx2_x16<16>(t1, pk);
     }
-    const int dpos = p.causal_diag ? is.dpos() : -1;
-    const int nsteps = p.pairs * cnt * C::kHalves;
-    int e = 0, hs = 0;  // place in the column, half of the block
-    for (int s = 0; s < nsteps; ++s, ++g) {
-      const uint32_t t1 = tl + ((g & 1) ? C::kT2 : C::kT1);
-      const uint32_t t2 = tl + ((g & 1) ? C::kT1 : C::kT2);
-      // Of this half's 32 queries those before the key are masked in the diagonal block.
-      const int lo = (e == dpos) ? row - 64 * hs - 32 * half : -(1 << 30);
-      if (++hs == C::kHalves) {
-        hs = 0;
-        if (++e == cnt) e = 0;
-      }
-      const float4* vec = reinterpret_cast<const float4*>(smem + C::kOffVec + (g % 2) * C::kVecB +
-                                                          half * (kDiffVecHalf * 4));
-      if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) {
-        ok = false;
-        break;
-      }
-      uint32_t rs[2][32];  // S^T, then P^T, of each map
-      tmem_ld_16x32bx2_x32<64>(t1, rs[0]);
-      tmem_ld_16x32bx2_x32<64>(t1 + 32, rs[1]);
-      tmem_ld_wait(rs[0]);
-      tmem_ld_wait(rs[1]);
-      // E1 = P_0^T - lam P_1^T, handed over on its own so that dV's product runs while dS^T is
-      // formed.  The second map's P is kept with its weight -lam.
-      {
-        uint32_t pk[16];
+    tmem_st_wait();
+    warp_arrive(C::kBarEF1);
+    if (!wait_bar(C::kBarDF, g & 1, kSiteSoftSFull)) break;
+    uint32_t rp[32];  // dP^T
+    tmem_ld_16x32bx2_x32<32>(t2, rp);
+    tmem_ld_wait(rp);
+    warp_arrive(C::kBarDL);  // T2 may now take the next step's S^T
+    {
+      uint32_t pk[32];
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          const float4 l0 = vec[i], l1 = vec[8 + i], lm = vec[32 + i];
-          const float a0[4] = {l0.x, l0.y, l0.z, l0.w}, a1[4] = {l1.x, l1.y, l1.z, l1.w};
-          const float am[4] = {lm.x, lm.y, lm.z, lm.w};
-          float c[4];
+          const float4 dd = vec[16 + 8 * m + i];
+          const float a[4] = {dd.x, dd.y, dd.z, dd.w};
+          float w[4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) {
-            const int cc = 4 * i + u;
-            const float y0 = mask_outside(fmaf(__uint_as_float(rs[0][cc]), p.scale_log2, -a0[u]), cc, lo, 1 << 30);
-            const float y1 = mask_outside(fmaf(__uint_as_float(rs[1][cc]), p.scale_log2, -a1[u]), cc, lo, 1 << 30);
-            const float p0 = ex2_approx(y0), p1 = -am[u] * ex2_approx(y1);
-            rs[0][cc] = __float_as_uint(p0);
-            rs[1][cc] = __float_as_uint(p1);
-            c[u] = p0 + p1;
-          }
-          pk[2 * i] = pack_bf16x2(c[0], c[1]);
-          pk[2 * i + 1] = pack_bf16x2(c[2], c[3]);
+          for (int u = 0; u < 4; ++u)
+            w[u] = __uint_as_float(rs[m][4 * i + u]) * (__uint_as_float(rp[4 * i + u]) - a[u]);
+          pk[16 * m + 2 * i] = pack_bf16x2(w[0], w[1]);
+          pk[16 * m + 2 * i + 1] = pack_bf16x2(w[2], w[3]);
         }
-        tmem_st_16x32bx2_x16<16>(t1, pk);
-      }
-      tmem_st_wait();
-      warp_arrive(C::kBarEF1);
-      if (!wait_bar(C::kBarDF, g & 1, kSiteSoftSFull)) {
-        ok = false;
-        break;
-      }
-      uint32_t rp[32];  // dP^T
-      tmem_ld_16x32bx2_x32<32>(t2, rp);
-      tmem_ld_wait(rp);
-      warp_arrive(C::kBarDL);  // T2 may now take the next step's S^T
-      {
-        uint32_t pk[32];
-#pragma unroll
-        for (int m = 0; m < 2; ++m)
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 dd = vec[16 + 8 * m + i];
-            const float a[4] = {dd.x, dd.y, dd.z, dd.w};
-            float c[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              c[u] = __uint_as_float(rs[m][4 * i + u]) * (__uint_as_float(rp[4 * i + u]) - a[u]);
-            pk[16 * m + 2 * i] = pack_bf16x2(c[0], c[1]);
-            pk[16 * m + 2 * i + 1] = pack_bf16x2(c[2], c[3]);
-          }
-        tmem_st_16x32bx2_x32<32>(t1 + 64, pk);
-      }
-      tmem_st_wait();
-      warp_arrive(C::kBarEF);
+      tmem_st_16x32bx2_x32<32>(t1 + 64, pk);
     }
-    if (!ok) break;
-    // Complete once the last step's products are.
-    if (!wait_bar(C::kBarAD, (g - 1) & 1, kSiteSoftItemDone)) break;
-    uint32_t pk[D / 4], pk2[D / 4];
-    read_o<D>(tl + C::kAcc1, 1.f, pk);
-    read_o<D>(tl + C::kAcc2, p.scale, pk2);
-    warp_arrive(C::kBarAR);
-    if (key < p.L) {
-      store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dv) + orow * D, 0, half, pk);
-      store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dk) + orow * D, 0, half, pk2);
+    tmem_st_wait();
+    warp_arrive(C::kBarEF);
+    const bool whole = c.head && c.tail();
+    if (c.last()) {
+      // The piece is complete once its last step's products are.
+      if (!wait_bar(C::kBarAD, g & 1, kSiteSoftItemDone)) break;
+      const int kv = c.col / p.nb, key = (c.col - kv * p.nb) * BLK + row;
+      if (whole) {
+        uint32_t pk[D / 4], pk2[D / 4];
+        read_o<D>(tl + C::kAcc1, 1.f, pk);
+        read_o<D>(tl + C::kAcc2, p.scale, pk2);
+        warp_arrive(C::kBarAR);
+        if (key < p.L) {
+          const int64_t orow = static_cast<int64_t>(c.b * (p.cols / p.nb) + kv) * p.L + key;
+          store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dv) + orow * D, 0, half, pk);
+          store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dk) + orow * D, 0, half, pk2);
+        }
+      } else {
+        // dV and dK as they are: this thread's 32-column groups, one after another.
+        float* slot = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (c.head ? 1 : 0)) * (BLK * 2 * D) +
+                      row * (2 * D) + half * 32;
+#pragma unroll 1
+        for (int i = 0; i < D / 32; ++i) {
+          uint32_t r[32];
+          load_o32(tl + C::kAcc1, i, r);
+          tmem_ld_wait(r);
+          if (i == D / 32 - 1) warp_arrive(C::kBarAR);
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            *reinterpret_cast<uint4*>(slot + 64 * i + 4 * u) =
+                make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+        }
+      }
     }
+    c.advance(p);
   }
   tmem_st_wait();
 }

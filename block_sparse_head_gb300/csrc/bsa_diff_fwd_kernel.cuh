@@ -318,9 +318,11 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
   auto store32 = [&](__nv_bfloat16* dst, const uint32_t (&w)[16]) {
     if (v8) {
 #pragma unroll
-      for (int q = 0; q < 2; ++q)
+      for (int q = 0; q < 2; ++q) {
+        __nanosleep(C::kStoreGapNs);  // a burst of stores stalls the softmax warps
         st_global_v8(dst + 16 * q, w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3], w[8 * q + 4],
                      w[8 * q + 5], w[8 * q + 6], w[8 * q + 7]);
+      }
     } else {
 #pragma unroll
       for (int q = 0; q < 4; ++q)
@@ -358,6 +360,7 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
     warp_arrive(C::kBarStFree);
     if (!wait_bar(C::kBarPVD + gl % 3, (gl / 3) & 1, kSiteSoftItemDone)) break;
     const float inv = (ml.y > 0.f) ? 1.f / ml.y : 0.f;
+    uint32_t w[HC / 32][16], w2[HC / 32][16];
 #pragma unroll
     for (int c = 0; c < HC / 32; ++c) {
       uint32_t r0[32], r1[32];  // of this lane's row: the columns that lanes 0-15 and 16-31 store
@@ -366,7 +369,6 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
       tmem_ld_wait(r0);
       tmem_ld_wait(r1);
       if (c == HC / 32 - 1) warp_arrive(C::kBarOFree);  // O may be overwritten now
-      uint32_t w[16], w2[16];
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         float o[2], o2[2];
@@ -378,12 +380,15 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
           o[u] = fmaf(-lam, second, first);
           o2[u] = second;
         }
-        w[i] = pack_bf16x2(o[0], o[1]);
-        w2[i] = pack_bf16x2(o2[0], o2[1]);
+        w[c][i] = pack_bf16x2(o[0], o[1]);
+        w2[c][i] = pack_bf16x2(o2[0], o2[1]);
       }
-      if (live) {
-        store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, w);
-        if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, w2);
+    }
+    if (live) {
+#pragma unroll
+      for (int c = 0; c < HC / 32; ++c) {
+        store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, w[c]);
+        if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, w2[c]);
       }
     }
     if (live) *lse = (ml.y > 0.f) ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;

@@ -53,10 +53,15 @@ auto pick(int block, int d, F64_64 a, F64_128 b, F128_64 c, F128_128 e) {
   return block == 64 ? (d == 64 ? a : b) : (d == 64 ? c : e);
 }
 
-// Bytes of the row terms; the rows of dlam come after them.
-int64_t vec_bytes(int B, int H, int L) {
-  return static_cast<int64_t>(B) * H * bsa::diff_vec_tiles((L + 63) / 64) * bsa::kDiffVecFloats * 4;
-}
+// The workspace: row terms, the pieces of cut columns (two a CTA), rows of dlam.
+struct Parts {
+  int64_t parts, rows, bytes;  // offsets
+  Parts(int B, int H, int L, int d, int block, int sms) {
+    parts = static_cast<int64_t>(B) * H * bsa::diff_vec_tiles((L + 63) / 64) * bsa::kDiffVecFloats * 4;
+    rows = parts + static_cast<int64_t>(sms) * 2 * block * 2 * d * 4;
+    bytes = rows + static_cast<int64_t>(B) * H * L * 4;
+  }
+};
 
 }  // namespace
 
@@ -104,13 +109,18 @@ int bsa_diff_forward(const void* q, const void* k, const void* v, const float* l
              : BSA_ERR_CUDA;
 }
 
-int bsa_diff_workspace(int B, int H, int L, int64_t* bytes) {
+int bsa_diff_workspace(int B, int H, int L, int d, int block, int64_t* bytes) {
   if (bytes == nullptr) return BSA_ERR_NULL;
   *bytes = 0;
+  if ((block != 64 && block != 128) || (d != 64 && d != 128)) return BSA_ERR_UNSUPPORTED;
   if (B < 1 || H < 1 || L < 1 || L > bsa::kMaxPositions || 2ll * B * H > kInt32Max ||
       2ll * B * H * L > kInt32Max - 128)
     return BSA_ERR_SHAPE;
-  *bytes = vec_bytes(B, H, L) + static_cast<int64_t>(B) * H * L * 4;
+  int dev = -1;
+  if (cudaGetDevice(&dev) != cudaSuccess) return BSA_ERR_CUDA;
+  const int sms = bsa::sm_count(dev);
+  if (sms <= 0) return BSA_ERR_CUDA;
+  *bytes = Parts(B, H, L, d, block, sms).bytes;
   return BSA_OK;
 }
 
@@ -132,9 +142,8 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   int sms = 0;
   const int bad = check(lut, B, H, kv_heads, L, d, dq, scale, block, &sms);
   if (bad != BSA_OK) return bad;
-  int64_t need = 0;
-  if (bsa_diff_workspace(B, H, L, &need) != BSA_OK) return BSA_ERR_SHAPE;
-  if (workspace_bytes < need) return BSA_ERR_TOO_LARGE;
+  const Parts parts(B, H, L, d, block, sms);
+  if (workspace_bytes < parts.bytes) return BSA_ERR_TOO_LARGE;
   CUtensorMap tq, tk, tv, tdo32, tdo64;
   const int64_t heads = static_cast<int64_t>(B) * H, kv = static_cast<int64_t>(B) * kv_heads;
   if (!bsa::encode_heads(&tq, q, 2 * heads, L, dq, 32, 1) ||
@@ -157,11 +166,20 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   r.d = d;
   r.lam_rows = lam_rows != 0;
   if (bsa::launch_diff_rows(r, st) != cudaSuccess) return BSA_ERR_CUDA;
-  float* rows = lam_rows ? dlam : reinterpret_cast<float*>(static_cast<char*>(workspace) + vec_bytes(B, H, L));
+  char* ws = static_cast<char*>(workspace);
+  float* rows = lam_rows ? dlam : reinterpret_cast<float*>(ws + parts.rows);
   bsa::DiffBwdParams p{};
   fill_list(p, lut, H / kv_heads, block);
   p.col_idx = lut->d_col_idx;
+  p.col_ptr = lut->d_col_ptr;
+  p.row_idx = lut->d_row_idx;
+  p.diag_pos = lut->d_diag_t;
+  p.B = B;
+  p.nb = lut->nb;
+  p.nnz = lut->nnz_total;
+  p.cols = lut->H * lut->nb;
   p.vec = r.vec;
+  p.parts = reinterpret_cast<float*>(ws + parts.parts);
   p.dq = dq_out;
   p.dlam = rows;
   p.dk = dk;
@@ -171,16 +189,16 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   p.scale = scale;
   p.causal_diag = causal_diag != 0;
   p.L = L;
+  p.block = block;
+  p.d = d;
   p.wait_limit_ns = lut->wait_limit_ns;
   p.expire_site = lut->expire_site;
   auto* launch = pick(block, d, bsa::launch_diff_bwd_b64_d64, bsa::launch_diff_bwd_b64_d128,
                       bsa::launch_diff_bwd_b128_d64, bsa::launch_diff_bwd_b128_d128);
   if (launch(dq != d, false, p, tq, tdo32, tk, tv, std::min(p.n, sms), st) != cudaSuccess)
     return BSA_ERR_CUDA;
-  p.items = reinterpret_cast<const int4*>(lut->d_items_t[0]);
-  p.cta_start = lut->d_sched_start_t[0];
-  p.col_idx = lut->d_row_idx;
-  if (launch(dq != d, true, p, tk, tv, tq, tdo64, lut->sched_grid, st) != cudaSuccess)
+  if (launch(dq != d, true, p, tk, tv, tq, tdo64, sms, st) != cudaSuccess ||
+      bsa::launch_diff_join(p, sms, st) != cudaSuccess)
     return BSA_ERR_CUDA;
   if (!lam_rows && bsa::launch_diff_lam(rows, dlam, B, H, L, st) != cudaSuccess) return BSA_ERR_CUDA;
   return BSA_OK;

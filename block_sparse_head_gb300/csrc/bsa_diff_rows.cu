@@ -1,5 +1,7 @@
-// bsa_diff_rows.cu -- row terms of the backward of differential attention, and the sum of the
-// weight's gradient.
+// bsa_diff_rows.cu -- the small kernels of differential attention's backward: the row terms
+// before its walks, the joining of cut columns and the sum of the weight's gradient after them.
+#include <algorithm>
+
 #include <cuda_bf16.h>
 
 #include "bsa_internal.h"
@@ -78,7 +80,71 @@ __global__ void __launch_bounds__(256) bsa_diff_lam_kernel(const float* __restri
   }
 }
 
+// Block x < grid of the dK/dV walk: the column cut at the start of CTA x's share, if CTA x - 1 has
+// its first piece, is the sum of its pieces in the CTAs' order.  Blocks behind: the zeros of
+// columns without an active block.  y: a share of the column's rows.
+__global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams p, int grid) {
+  const int d = p.d, lanes = d / 2;  // threads of a row, four numbers of dV | dK each
+  const int r0 = threadIdx.x / lanes, at = threadIdx.x % lanes * 4;
+  const int rows = p.block / gridDim.y, step = 256 / lanes;
+  auto store = [&](int b, int col, int row, float4 x) {
+    const int kv = col / p.nb, key = (col - kv * p.nb) * p.block + row;
+    if (key >= p.L) return;
+    const int64_t to = (static_cast<int64_t>(b * (p.cols / p.nb) + kv) * p.L + key) * d;
+    const float f = at < d ? 1.f : p.scale;
+    __nv_bfloat162 y[2] = {__floats2bfloat162_rn(x.x * f, x.y * f), __floats2bfloat162_rn(x.z * f, x.w * f)};
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(at < d ? p.dv : p.dk) + to + (at < d ? at : at - d);
+    *reinterpret_cast<uint2*>(out) = *reinterpret_cast<const uint2*>(y);
+  };
+  const int row0 = blockIdx.y * rows;
+  if (static_cast<int>(blockIdx.x) >= grid) {
+    const long long n = static_cast<long long>(p.B) * p.cols;
+    for (long long i = blockIdx.x - grid; i < n; i += gridDim.x - grid) {
+      const int b = static_cast<int>(i / p.cols), col = static_cast<int>(i - static_cast<long long>(b) * p.cols);
+      if (p.col_ptr[col] != p.col_ptr[col + 1]) continue;
+      for (int r = r0; r < rows; r += step) store(b, col, row0 + r, make_float4(0.f, 0.f, 0.f, 0.f));
+    }
+    return;
+  }
+  const long long total = diff_steps(p), share = diff_share(p, grid), start = blockIdx.x * share;
+  if (blockIdx.x == 0 || start >= total) return;
+  const int per = p.pairs * p.halves;
+  const long long entry = start / per;
+  const int b = static_cast<int>(entry / p.nnz);
+  const long long base = static_cast<long long>(b) * p.nnz;
+  const int x = static_cast<int>(entry - base);
+  int lo = 0, hi = p.cols - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    if (p.col_ptr[mid + 1] > x) hi = mid;
+    else lo = mid + 1;
+  }
+  const long long first = (base + p.col_ptr[lo]) * per, end = (base + p.col_ptr[lo + 1]) * per;
+  const int root = static_cast<int>(first / share), last = static_cast<int>((end - 1) / share);
+  if (first == start || root != static_cast<int>(blockIdx.x) - 1) return;
+  const int64_t slot = static_cast<int64_t>(p.block) * 2 * d;
+  for (int r = r0; r < rows; r += step) {
+    const float* src = p.parts + (row0 + r) * (2 * d) + at;
+    float4 sum = *reinterpret_cast<const float4*>(src + (2 * static_cast<int64_t>(root) + 1) * slot);
+#pragma unroll 4
+    for (int i = root + 1; i <= last; ++i) {
+      const float4 y = *reinterpret_cast<const float4*>(src + 2 * static_cast<int64_t>(i) * slot);
+      sum.x += y.x;
+      sum.y += y.y;
+      sum.z += y.z;
+      sum.w += y.w;
+    }
+    store(b, lo, row0 + r, sum);
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, cudaStream_t stream) {
+  const int more = static_cast<int>(std::min<long long>(64, static_cast<long long>(p.B) * p.cols));
+  bsa_diff_join_kernel<<<dim3(grid + more, 8), 256, 0, stream>>>(p, grid);
+  return cudaGetLastError();
+}
 
 cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream) {
   const int64_t rows = p.pairs * 64 * diff_vec_tiles((p.L + 63) / 64);

@@ -250,7 +250,9 @@ void free_device(bsa_lut* lut) {
   if (lut->d_row_ptr) cudaFree(lut->d_row_ptr);
   if (lut->d_row_idx) cudaFree(lut->d_row_idx);
   if (lut->d_list) cudaFree(lut->d_list);
-  lut->d_list = nullptr;
+  if (lut->d_col_ptr) cudaFree(lut->d_col_ptr);
+  if (lut->d_diag_t) cudaFree(lut->d_diag_t);
+  lut->d_list = lut->d_col_ptr = lut->d_diag_t = nullptr;
   lut->d_row_ptr = lut->d_row_idx = nullptr;
   for (int o = 0; o < 2; ++o) {
     if (lut->d_items_t[o]) cudaFree(lut->d_items_t[o]);
@@ -494,7 +496,10 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
       return BSA_ERR_ALLOC;
     }
     const size_t nr = std::max<size_t>(lut->row_idx.size(), 1) * 4;
+    const size_t ncp = lut->col_ptr.size() * 4, ndt = lut->diag_pos_t.size() * 4;
     if (cudaMalloc(&lut->d_row_idx, nr) != cudaSuccess ||
+        cudaMalloc(&lut->d_col_ptr, ncp) != cudaSuccess ||
+        cudaMalloc(&lut->d_diag_t, ndt) != cudaSuccess ||
         cudaMalloc(&lut->d_items_t[0], ni) != cudaSuccess ||
         cudaMalloc(&lut->d_items_t[1], ni) != cudaSuccess ||
         cudaMalloc(&lut->d_sched_start_t[0], ns) != cudaSuccess ||
@@ -503,9 +508,13 @@ int bsa_lut_upload(bsa_lut* lut, void* stream) {
       cudaGetLastError();
       return BSA_ERR_ALLOC;
     }
-    ok = lut->row_idx.empty() ||
-         cudaMemcpyAsync(lut->d_row_idx, lut->row_idx.data(), lut->row_idx.size() * 4,
-                         cudaMemcpyHostToDevice, st) == cudaSuccess;
+    ok = (lut->row_idx.empty() ||
+          cudaMemcpyAsync(lut->d_row_idx, lut->row_idx.data(), lut->row_idx.size() * 4,
+                          cudaMemcpyHostToDevice, st) == cudaSuccess) &&
+         cudaMemcpyAsync(lut->d_col_ptr, lut->col_ptr.data(), ncp, cudaMemcpyHostToDevice, st) ==
+             cudaSuccess &&
+         cudaMemcpyAsync(lut->d_diag_t, lut->diag_pos_t.data(), ndt, cudaMemcpyHostToDevice, st) ==
+             cudaSuccess;
     for (int o = 0; o < 2 && ok; ++o)
       ok = (lut->sched_records_t[o].empty() ||
             cudaMemcpyAsync(lut->d_items_t[o], lut->sched_records_t[o].data(),

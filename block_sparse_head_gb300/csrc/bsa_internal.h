@@ -47,6 +47,8 @@ struct bsa_lut {
   int32_t* d_items_t[2] = {nullptr, nullptr};        // records of both column schedules
   int32_t* d_sched_start_t[2] = {nullptr, nullptr};
   int32_t* d_list = nullptr;           // records of items, in work-list order
+  int32_t* d_col_ptr = nullptr;        // column view: col_ptr, diag_pos_t
+  int32_t* d_diag_t = nullptr;
   uint64_t wait_limit_ns = 10000000000ull;
   int expire_site = 0;  // bsa_debug_expire_wait
 };
@@ -206,20 +208,38 @@ constexpr int kDiffVecFloats = 328;
 __host__ __device__ inline int diff_vec_tiles(int tiles) { return (tiles + 1) & ~1; }
 
 struct DiffBwdParams : DiffList {
-  const int4* items;         // dK/dV walk: the plain backward's column work list (else null)
-  const int32_t* cta_start;
-  const int32_t* col_idx;    // dQ: key blocks of each row; dK/dV: query blocks of each column
+  const int32_t* col_idx;    // key blocks of each row
+  const int32_t* col_ptr;    // column view: [heads * nb + 1], query blocks of each column, and
+  const int32_t* row_idx;    // the place of the diagonal block among them
+  const int32_t* diag_pos;
+  int B, nb, nnz;            // nnz: active blocks of all kv heads
+  int cols;                  // kv heads * nb
   const float* vec;          // row terms
   void* dq;                  // dQ walk: bf16 [B,2H,L,dq]
   float* dlam;               // and fp32 [B,H,L]
   void* dk;                  // dK/dV walk: bf16 [B,Hkv,L,d]
   void* dv;
+  float* parts;              // dV and dK of cut columns: slots of block * 2 d fp32
   int32_t* status;
   float scale_log2, scale;
-  int causal_diag, L;
+  int causal_diag, L, block, d;
   unsigned long long wait_limit_ns;
   int expire_site;
 };
+// The dK/dV walk lays the steps of all columns end to end, (b, column, entry, head of the kv
+// head, half) with the last fastest, and CTA c takes the c-th piece of equal length: whole
+// columns and at most two cut ones.  A cut column's pieces go to slots: 2 c the piece that begins
+// CTA c's share (a column begun earlier), 2 c + 1 the one that ends it.
+constexpr int kDiffShare = 4;  // steps of a share at least
+__host__ __device__ inline long long diff_steps(const DiffBwdParams& p) {
+  return static_cast<long long>(p.B) * p.nnz * p.pairs * p.halves;
+}
+__host__ __device__ inline long long diff_share(const DiffBwdParams& p, int grid) {
+  const long long n = (diff_steps(p) + grid - 1) / grid;
+  return n < kDiffShare ? kDiffShare : n;
+}
+// Joins the pieces of cut columns (in order) and writes the zeros of columns without a block.
+cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, cudaStream_t stream);
 // a, b, x, y: q, dO, k, v (dQ walk) or k, v, q, dO (kv).
 #define BSA_DIFF_BWD(name)                                                                      \
   cudaError_t launch_diff_bwd_##name(bool split, bool kv, const DiffBwdParams& p,               \

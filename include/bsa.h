@@ -316,7 +316,7 @@ int bsa_diff_forward(const void* q, const void* k, const void* v, const float* l
  *           Calls that may overlap on the GPU need one each.
  *   the others as in bsa_diff_forward.
  *
- * Asynchronous; three kernels, a fourth without lam_rows; allocates nothing.  Errors: as
+ * Asynchronous; four kernels, a fifth without lam_rows; allocates nothing.  Errors: as
  * bsa_diff_forward, BSA_ERR_TOO_LARGE (workspace too small).
  */
 int bsa_diff_backward(const void* q, const void* k, const void* v, const float* lam,
@@ -326,9 +326,9 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
                       int d, int dq, int lam_rows, float scale, int block, int causal_diag,
                       void* stream);
 
-/* bsa_diff_workspace -- bytes of workspace that bsa_diff_backward needs.  Errors: BSA_ERR_NULL,
- * BSA_ERR_SHAPE. */
-int bsa_diff_workspace(int B, int H, int L, int64_t* bytes);
+/* bsa_diff_workspace -- bytes of workspace that bsa_diff_backward needs on the current device.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE, BSA_ERR_UNSUPPORTED, BSA_ERR_CUDA. */
+int bsa_diff_workspace(int B, int H, int L, int d, int block, int64_t* bytes);
 
 /*
  * bsa_topk_forward -- top-k token-gather attention with an attention sink, the second

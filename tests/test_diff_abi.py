@@ -69,9 +69,8 @@ def test_backward(lib, lut):
 
 def test_workspace(lib):
     n = ctypes.c_int64()
-    assert lib.bsa_diff_workspace(1, 1, 1, None) == -1
+    assert lib.bsa_diff_workspace(1, 1, 1, 64, 64, None) == -1
     for bad in ((0, 1, 1), (1, 0, 1), (1, 1, 0), (1 << 15, 1 << 15, 1 << 10), (1, 1, 1 << 30)):
-        assert lib.bsa_diff_workspace(*bad, ctypes.byref(n)) == -2
-    assert lib.bsa_diff_workspace(2, 3, 65, ctypes.byref(n)) == 0
-    # row terms of two tiles of 64 (328 numbers each) and one number a row
-    assert n.value == 6 * (2 * 328 + 65) * 4
+        assert lib.bsa_diff_workspace(*bad, 64, 64, ctypes.byref(n)) == -2
+    for bad in ((96, 64), (64, 32)):
+        assert lib.bsa_diff_workspace(1, 1, 1, *bad, ctypes.byref(n)) == -6

@@ -111,6 +111,22 @@ def test_many_items_a_cta():
     _check(q, k, v, lam, do, _layout(4, 25, 73, 0.15), 0.125, 64, True)
 
 
+@pytest.mark.parametrize("block,d,dq", [(64, 64, 64), (128, 128, 64)])
+def test_columns_cut_between_ctas(block, d, dq):
+    """One kv head of eight heads and few, long columns: every column's steps are shared by several
+    CTAs, some of them inside one column for their whole share, columns without a block between."""
+    nb = 14
+    lay = torch.zeros(1, nb, nb, dtype=torch.int32)
+    lay[0, :, 3], lay[0, :, 7], lay[0, 5:9, 10], lay[0, 13, 13] = 1, 1, 1, 1
+    q, k, v, lam, do = _inputs(2, 8, 1, nb * block - 3, d, dq, False, 90)
+    _check(q, k, v, lam, do, lay, 1 / math.sqrt(dq), block, True)
+
+
+def test_layout_without_a_block():
+    q, k, v, lam, do = _inputs(1, 2, 1, 100, 64, 64, False, 91)
+    _check(q, k, v, lam, do, torch.zeros(1, 2, 2, dtype=torch.int32), 0.1, 64, True)
+
+
 def test_repeatable_and_on_another_stream():
     q, k, v, lam, do = _inputs(1, 4, 2, 900, 128, 64, False, 74)
     lay = _layout(2, 8, 75)
@@ -128,7 +144,7 @@ def test_repeatable_and_on_another_stream():
 def test_captured_step_follows_its_inputs():
     q, k, v, lam, do = _inputs(1, 2, 2, 300, 64, 64, False, 76)
     lay = torch.tril(torch.ones(2, 5, 5, dtype=torch.int32))
-    lut, ws = bsa.build_lut(lay, 1), bsa.diff_workspace(1, 2, 300)
+    lut, ws = bsa.build_lut(lay, 1), bsa.diff_workspace(1, 2, 300, 64, 64)
 
     def step():
         out, lse, out2 = bsa.diff_forward(q, k, v, lam, lut, 0.125, 64, True, training=True)
