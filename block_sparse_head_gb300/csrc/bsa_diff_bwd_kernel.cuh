@@ -26,10 +26,12 @@
 //              leave fp32 pieces that bsa_diff_rows.cu joins in order.
 // Queries of d / 2 numbers are laid out over d columns, zero in the other map's half
 // (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
-// Rows past the end of the sequence read as zero and carry lse = +inf, so that their P is 0;
+// Rows past the end of the sequence read as zero and carry -lse = -inf, so that their P is 0;
 // keys past it have K = V = 0 and are not stored.
 // Every wait is bounded (WaitCtl), as in the plain kernels.
 #pragma once
+
+#include <type_traits>
 
 #include "bsa_bwd_kernel.cuh"
 #include "bsa_diff.cuh"
@@ -43,8 +45,8 @@ __device__ __forceinline__ int4 stream_item(const DiffBwdParams& p, int u) {
   return stream_item(static_cast<const DiffList&>(p), u);
 }
 
-// Row terms of 64 queries: two groups of 32, each [lse_0, lse_1 (log2 units), D_0, D_1, lam]
-// of 32 fp32 and 16 bytes of room, so that the two half-warps, which read the same places of
+// Row terms of 64 queries: two groups of 32, each [-lse_0, -lse_1 (log2 units), -D_0, -D_1, -lam]
+// of 32 fp32 (negated: they are added) and 16 bytes of room, so that the two half-warps, which read the same places of
 // different groups, hit different banks.
 constexpr int kDiffVecHalf = 5 * 32 + 4;
 constexpr int kDiffVec = 2 * kDiffVecHalf;
@@ -337,8 +339,8 @@ __device__ __forceinline__ void diff_dq_mma(const DiffBwdParams& p, uint32_t sba
     tc_fence_after();
     diff_issue_first<D, C::kItemPlane, C::kXPlane, C::kXBlkB, BLK>(
         tmem + ((t & 1) ? C::kT1b : C::kT1), a0, x0 + (t % 3) * (C::kXTile >> 4), hi, C::kIdescT1, nblk);
-    // T2 is free once the elementwise warps finished step t-1.
-    if (t >= 1 && !mbar_wait(bar(C::kBarEF), (t - 1) & 1, ctl, kSiteMmaPFull)) break;
+    // T2 is free once the elementwise warps have loaded that of step t-1.
+    if (t >= 1 && !mbar_wait(bar(C::kBarDL), (t - 1) & 1, ctl, kSiteMmaPFull)) break;
     if (!mbar_wait(bar(C::kBarYF + t % 2), (t / 2) & 1, ctl, kSiteMmaStage)) break;
     tc_fence_after();
     diff_issue_first<D, C::kItemPlane, C::kYPlane, C::kXBlkB, BLK>(
@@ -567,8 +569,10 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       continue;
     }
     const float* v = p.vec + (pair * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + (qin & 31);
-    const float lr = v[32 * map], dr = v[64 + 32 * map];
-    const float w = map ? -v[128] : 1.f;
+    // dS = P (w dP - w D) with the row's weight w
+    const float w = map ? v[128] : 1.f, wd = w * v[64 + 32 * map];
+    const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), l2 = f2_pack(v[32 * map], v[32 * map]);
+    const uint64_t w2 = f2_pack(w, w), wd2 = f2_pack(wd, wd);
     const int dpos = p.causal_diag ? is.dpos() : -1;
     const int qblk = qin + (BLK == 128 ? (is.cur.y & 1) * 64 : 0);
     const int nsteps = (cnt + G - 1) / G;
@@ -591,25 +595,36 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rs + 32));
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp));
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp + 32));
-      const int hi = diag ? qblk - kbase : (1 << 30);  // keys after the query: masked
+      warp_arrive(C::kBarDL);  // T2 may now take the next step's dP
+      // Keys behind the query in the diagonal block, and a block that is not there, are masked
+      // (after scaling, so that a negative scale cannot turn -inf into +inf).
+      const int hi = valid ? (diag ? qblk - kbase : 63) : -1;
       uint32_t pk1[32];
-      float sums[4] = {0.f, 0.f, 0.f, 0.f};
+      uint64_t sums[2] = {0ull, 0ull};
+      auto form = [&](auto masked) {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        float ds[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const int cc = 2 * i + u;
-          // masked after scaling, so that a negative scale cannot turn -inf into +inf
-          const float y = mask_outside(__uint_as_float(rs[cc]) * p.scale_log2 - lr, cc, -(1 << 30), hi);
-          const float pe = valid ? ex2_approx(y) : 0.f;
-          const float dp = valid ? __uint_as_float(rp[cc]) : 0.f;
-          sums[cc & 3] = fmaf(pe, dp, sums[cc & 3]);
-          ds[u] = pe * w * (dp - dr);
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t y = f2_fma(f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), c2, l2);
+          float y0 = f2_lo(y), y1 = f2_hi(y);
+          float d0 = __uint_as_float(rp[2 * i]), d1 = __uint_as_float(rp[2 * i + 1]);
+          if constexpr (decltype(masked)::value) {
+            y0 = mask_gt(y0, 2 * i, hi);
+            y1 = mask_gt(y1, 2 * i + 1, hi);
+            d0 = 2 * i > hi ? 0.f : d0;
+            d1 = 2 * i + 1 > hi ? 0.f : d1;
+          }
+          const uint64_t pe = f2_pack(ex2_approx(y0), ex2_approx(y1)), dp = f2_pack(d0, d1);
+          sums[i & 1] = f2_fma(pe, dp, sums[i & 1]);
+          const uint64_t ds = f2_mul(pe, f2_fma(dp, w2, wd2));
+          pk1[i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
         }
-        pk1[i] = pack_bf16x2(ds[0], ds[1]);
-      }
-      rsum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      };
+      if (__any_sync(0xffffffffu, hi < 63))
+        form(std::true_type{});
+      else
+        form(std::false_type{});
+      sums[0] = f2_add(sums[0], sums[1]);
+      rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
       tmem_st_16x32bx2_x32<32>(t1, pk1);
       tmem_st_wait();
       // The previous step's dQ product issued (its issuer cannot fall two phases behind).
@@ -659,6 +674,7 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     return w;
   };
 
+  const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
   DiffKvWalk c;
   c.init(p);
   int dpos = -1;
@@ -680,25 +696,32 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     // formed.  The second map's P is kept with its weight -lam.
     {
       uint32_t pk[16];
+      auto form = [&](auto masked) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float4 l0 = vec[i], l1 = vec[8 + i], lm = vec[32 + i];
-        const float a0[4] = {l0.x, l0.y, l0.z, l0.w}, a1[4] = {l1.x, l1.y, l1.z, l1.w};
-        const float am[4] = {lm.x, lm.y, lm.z, lm.w};
-        float w[4];
+        for (int i = 0; i < 16; ++i) {
+          const float4 l0 = vec[i >> 1], l1 = vec[8 + (i >> 1)], lm = vec[32 + (i >> 1)];
+          auto two = [&](const float4& f) { return i & 1 ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y); };
+          const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(rs[0][2 * i]), __uint_as_float(rs[0][2 * i + 1])), c2, two(l0));
+          const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(rs[1][2 * i]), __uint_as_float(rs[1][2 * i + 1])), c2, two(l1));
+          float a[4] = {f2_lo(y0), f2_hi(y0), f2_lo(y1), f2_hi(y1)};
+          if constexpr (decltype(masked)::value) {
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int cc = 4 * i + u;
-          const float y0 = mask_outside(fmaf(__uint_as_float(rs[0][cc]), p.scale_log2, -a0[u]), cc, lo, 1 << 30);
-          const float y1 = mask_outside(fmaf(__uint_as_float(rs[1][cc]), p.scale_log2, -a1[u]), cc, lo, 1 << 30);
-          const float p0 = ex2_approx(y0), p1 = -am[u] * ex2_approx(y1);
-          rs[0][cc] = __float_as_uint(p0);
-          rs[1][cc] = __float_as_uint(p1);
-          w[u] = p0 + p1;
+            for (int u = 0; u < 4; ++u) a[u] = mask_outside(a[u], 2 * i + (u & 1), lo, 1 << 30);
+          }
+          const uint64_t p0 = f2_pack(ex2_approx(a[0]), ex2_approx(a[1]));
+          const uint64_t p1 = f2_mul(f2_pack(ex2_approx(a[2]), ex2_approx(a[3])), two(lm));
+          rs[0][2 * i] = __float_as_uint(f2_lo(p0));
+          rs[0][2 * i + 1] = __float_as_uint(f2_hi(p0));
+          rs[1][2 * i] = __float_as_uint(f2_lo(p1));
+          rs[1][2 * i + 1] = __float_as_uint(f2_hi(p1));
+          const uint64_t w = f2_add(p0, p1);
+          pk[i] = pack_bf16x2(f2_lo(w), f2_hi(w));
         }
-        pk[2 * i] = pack_bf16x2(w[0], w[1]);
-        pk[2 * i + 1] = pack_bf16x2(w[2], w[3]);
-      }
+      };
+      if (c.x - c.begin == dpos)
+        form(std::true_type{});
+      else
+        form(std::false_type{});
       tmem_st_16x32bx2_x16<16>(t1, pk);
     }
     tmem_st_wait();
@@ -713,15 +736,12 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
 #pragma unroll
       for (int m = 0; m < 2; ++m)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const float4 dd = vec[16 + 8 * m + i];
-          const float a[4] = {dd.x, dd.y, dd.z, dd.w};
-          float w[4];
-#pragma unroll
-          for (int u = 0; u < 4; ++u)
-            w[u] = __uint_as_float(rs[m][4 * i + u]) * (__uint_as_float(rp[4 * i + u]) - a[u]);
-          pk[16 * m + 2 * i] = pack_bf16x2(w[0], w[1]);
-          pk[16 * m + 2 * i + 1] = pack_bf16x2(w[2], w[3]);
+        for (int i = 0; i < 16; ++i) {
+          const float4 dd = vec[16 + 8 * m + (i >> 1)];
+          const uint64_t t = f2_add(f2_pack(__uint_as_float(rp[2 * i]), __uint_as_float(rp[2 * i + 1])),
+                                    i & 1 ? f2_pack(dd.z, dd.w) : f2_pack(dd.x, dd.y));
+          const uint64_t ds = f2_mul(f2_pack(__uint_as_float(rs[m][2 * i]), __uint_as_float(rs[m][2 * i + 1])), t);
+          pk[16 * m + i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
         }
       tmem_st_16x32bx2_x32<32>(t1 + 64, pk);
     }

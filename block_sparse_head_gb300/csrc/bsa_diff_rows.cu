@@ -45,16 +45,16 @@ __global__ void __launch_bounds__(256) bsa_diff_rows_kernel(const DiffRowsParams
     a1 += __shfl_xor_sync(0xffffffffu, a1, w);
   }
   if (!in || lane % R >= 5) return;
-  // Lane i of a row writes term i.  Rows past the end, and rows without an active key, get
-  // lse = +inf: their P is 0.
+  // Lane i of a row writes term i, negated.  Rows past the end, and rows without an active key,
+  // get -lse = -inf: their P is 0.
   const int i = lane % R;
   const float lam = live ? (p.lam_rows ? p.lam[pair * p.L + q] : p.lam[pair % p.H]) : 0.f;
   float x;
   if (i < 2) {
-    x = live ? p.lse[(2 * pair + i) * p.L + q] * kLog2e : INFINITY;
-    if (x == -INFINITY) x = INFINITY;
+    x = live ? p.lse[(2 * pair + i) * p.L + q] * -kLog2e : -INFINITY;
+    if (x == INFINITY) x = -INFINITY;
   } else {
-    x = i == 2 ? fmaf(lam, a1, a0) : i == 3 ? a1 : lam;
+    x = -(i == 2 ? fmaf(lam, a1, a0) : i == 3 ? a1 : lam);
   }
   p.vec[(pair * tiles + (q >> 6)) * kDiffVecFloats + ((q >> 5) & 1) * (kDiffVecFloats / 2) + 32 * i +
         (q & 31)] = x;
