@@ -12,6 +12,7 @@ from .binding import (  # noqa: F401
     backward,
     build_lut,
     cache_append,
+    cache_diff_forward,
     cache_forward,
     cache_resize,
     cache_status,

@@ -35,7 +35,7 @@ EXPORTED = (
     "bsa_build_lut_rect", "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
     "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
     "bsa_cache_forward", "bsa_cache_workspace", "bsa_diff_forward", "bsa_diff_backward",
-    "bsa_diff_workspace",
+    "bsa_diff_workspace", "bsa_cache_diff_forward",
 )
 
 _ACTIVATIONS = {torch.bfloat16: 0, torch.float16: 1}          # BSA_BF16, BSA_FP16
@@ -97,6 +97,8 @@ def load_library():
                                          i64, vp]
         lib.bsa_cache_forward.argtypes = [vp] + [vp] * 8 + [i64] + [ci] * 6 + \
             [i64, i64, ctypes.c_float, vp, vp]
+        lib.bsa_cache_diff_forward.argtypes = [vp] * 10 + [i64] + [ci] * 8 + \
+            [i64, i64, ctypes.c_float, vp, vp]
         lib.bsa_cache_workspace.argtypes = [ci, ci, ci, ci, ctypes.POINTER(i64)]
         lib.bsa_diff_forward.argtypes = [vp] * 8 + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
         lib.bsa_diff_backward.argtypes = [vp] * 14 + [i64] + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
@@ -134,7 +136,7 @@ def load_library():
                      "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
                      "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
                      "bsa_cache_forward", "bsa_cache_workspace", "bsa_diff_forward",
-                     "bsa_diff_backward", "bsa_diff_workspace"):
+                     "bsa_diff_backward", "bsa_diff_workspace", "bsa_cache_diff_forward"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -536,6 +538,15 @@ def cache_status(workspace: torch.Tensor) -> int:
     return int(workspace[:4].view(torch.int32).item())
 
 
+def _cache_args(window, softcap, sinks, heads: int, lut, block, dev: int):
+    """bsa_cache_args as bytes (None: none of them)."""
+    if not ((window is not None and window >= 0) or softcap or sinks is not None or lut is not None):
+        return None
+    return _CACHE_ARGS.pack(-1 if window is None else min(max(-1, int(window)), 2 ** 31 - 1), float(softcap),
+                            0 if sinks is None else _dev_ptr(sinks, "sinks", torch.float32, (heads,), dev),
+                            0 if lut is None else lut.handle.value, 0 if block is None else int(block))
+
+
 def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                   k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
                   kv_len: torch.Tensor, cu_q: torch.Tensor, scale: float, max_q: int | None = None,
@@ -575,12 +586,7 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
                 workspace = cache_workspace(heads, kv_heads, d, max_q)
                 if status is None:
                     status = torch.empty(1, dtype=i32, device=where)
-    args = None
-    if (window is not None and window >= 0) or softcap or sinks is not None or lut is not None:
-        args = _CACHE_ARGS.pack(-1 if window is None else min(max(-1, int(window)), 2 ** 31 - 1), float(softcap),
-                                0 if sinks is None else _dev_ptr(sinks, "sinks", f32, (heads,), dev),
-                                0 if lut is None else lut.handle.value,
-                                0 if block is None else int(block))
+    args = _cache_args(window, softcap, sinks, heads, lut, block, dev)
     ws_bytes = workspace.numel()
     _check(lib.bsa_cache_forward(
         cache, qp, _dev_ptr(block_table, "block_table", i32, (B, max_pages), dev),
@@ -591,6 +597,60 @@ def cache_forward(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
         _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, max_pages, T,
         heads, max_q, _ACTIVATIONS[q.dtype], qt, qh, float(scale), args, _cache_stream(stream, dev)),
         "bsa_cache_forward")
+    return out, lse, status
+
+
+def cache_diff_forward(q: torch.Tensor, lam: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                       k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                       kv_len: torch.Tensor, cu_q: torch.Tensor, scale: float, max_q: int | None = None,
+                       window: int | None = None, softcap: float = 0.0,
+                       sinks: torch.Tensor | None = None, lut: Lut | None = None,
+                       block: int | None = None, out: torch.Tensor | None = None,
+                       lse: torch.Tensor | None = None, status: torch.Tensor | None = None,
+                       workspace: torch.Tensor | None = None, stream=None):
+    """Differential attention of the newest tokens of every request over its cache
+    (bsa_cache_diff_forward): out = O_0 - lam O_1 with cache_forward's O of query heads 2h and
+    2h + 1.  q: bf16 or fp16 [T, 2 * heads, dq], dq = d or (a key half for each map) d / 2 = 64;
+    lam: fp32 [heads] or [T, heads]; sinks [2 * heads]; ``workspace`` from cache_workspace(2 *
+    heads, ...); the rest as in cache_forward.  Returns (out [T, heads, d], lse fp32 [T, 2 *
+    heads], status)."""
+    lib = _lib or load_library()
+    dev, cache, kv_heads, d = _cache_view(k_cache, v_cache, k_scale, v_scale)
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or q.shape[1] % 2:
+        raise ValueError("q must be bf16 or fp16 [T, 2 * heads, dq]")
+    T, heads2, dq = q.shape
+    heads = heads2 // 2
+    qp, qt, qh = _rows_ptr(q, "q", None, dq, dev)
+    if not isinstance(block_table, torch.Tensor) or block_table.dim() != 2:
+        raise ValueError("block_table must be int32 [B, max_pages]")
+    if not isinstance(lam, torch.Tensor) or lam.dim() not in (1, 2):
+        raise ValueError("lam must be fp32 [heads] or [T, heads]")
+    B, max_pages = block_table.shape
+    if lut is not None and block is None:
+        raise ValueError("a lut needs its block")
+    max_q = max(T, 1) if max_q is None else int(max_q)
+    i32, f32 = torch.int32, torch.float32
+    if out is None or lse is None or workspace is None:
+        with _on(stream):
+            where = q.device
+            out = torch.empty(T, heads, d, dtype=q.dtype, device=where) if out is None else out
+            lse = torch.empty(T, heads2, dtype=f32, device=where) if lse is None else lse
+            if workspace is None:
+                workspace = cache_workspace(heads2, kv_heads, d, max_q)
+                if status is None:
+                    status = torch.empty(1, dtype=i32, device=where)
+    rows = lam.dim() == 2
+    ws_bytes = workspace.numel()
+    _check(lib.bsa_cache_diff_forward(
+        cache, qp, _dev_ptr(lam, "lam", f32, (T, heads) if rows else (heads,), dev),
+        _dev_ptr(block_table, "block_table", i32, (B, max_pages), dev),
+        _dev_ptr(kv_len, "kv_len", i32, (B,), dev), _dev_ptr(cu_q, "cu_q", i32, (B + 1,), dev),
+        _dev_ptr(out, "out", q.dtype, (T, heads, d), dev), _dev_ptr(lse, "lse", f32, (T, heads2), dev),
+        None if status is None else _dev_ptr(status, "status", i32, (1,), dev),
+        _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, max_pages, T,
+        heads, dq, max_q, int(rows), _ACTIVATIONS[q.dtype], qt, qh, float(scale),
+        _cache_args(window, softcap, sinks, heads2, lut, block, dev), _cache_stream(stream, dev)),
+        "bsa_cache_diff_forward")
     return out, lse, status
 
 

@@ -417,10 +417,16 @@ __device__ __forceinline__ int atomic_add_acq_rel(int* p, int x) {
   return r;
 }
 
+// The second map's weight for output row (token, head).
+__device__ __forceinline__ float diff_lam(const CacheFwdParams& p, int64_t orow) {
+  return p.lam[p.lam_rows ? orow : orow % (p.Hq >> 1)];
+}
+
 // Rows r0, r0 + step, .. (N of them, fewer at the unit's end) of a cut unit: pieces 0 .. more,
 // the first at the end of CTA root's share, piece i at the start of CTA root + i's.  One warp;
-// the rows' loads overlap.
-template <class A, int D, int R, int N>
+// the rows' loads overlap.  DIFF: pairs of rows r0, r0 + 1, r0 + step, r0 + step + 1, .., both maps
+// of an output row.
+template <class A, int D, int R, int N, bool DIFF>
 __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CacheParts& parts,
                                           const CacheSeg& s, int root, int more, int r0, int step,
                                           int lane) {
@@ -428,7 +434,9 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
   const int rows = s.nq * p.group;
   int64_t row[N];  // of the output
   float top[N], z[N], o[N][E] = {};
-  auto row_of = [&](int j) { return min(r0 + j * step, rows - 1); };
+  static_assert(!DIFF || N % 2 == 0, "pairs of rows");
+  auto place = [&](int j) { return DIFF ? r0 + (j >> 1) * step + (j & 1) : r0 + j * step; };
+  auto row_of = [&](int j) { return min(place(j), rows - 1); };
   auto slot = [&](int i, int j) {
     return static_cast<int64_t>(i == 0 ? 2 * root + 1 : 2 * (root + i)) * R + row_of(j);
   };
@@ -474,17 +482,33 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
   }
 #pragma unroll
   for (int j = 0; j < N; ++j) {
-    if (r0 + j * step >= rows) continue;
+    if (place(j) >= rows) continue;
     const float inv = z[j] == 0.f ? 0.f : 1.f / z[j];
-    uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row[j] * D + lane * E);
-#pragma unroll
-    for (int i = 0; i < E / 2; ++i)
-      dst[i] = float2_to_act<A>(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
     if (lane == 0) p.lse[row[j]] = z[j] == 0.f ? -INFINITY : (top[j] + log2f(z[j])) * kLn2;
+    if constexpr (DIFF) {
+#pragma unroll
+      for (int i = 0; i < E; ++i) o[j][i] *= inv;
+      if ((j & 1) == 0) continue;
+      const int64_t orow = row[j] >> 1;  // Hq is even
+      const float lam = diff_lam(p, orow);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + orow * D + lane * E);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i)
+        dst[i] = float2_to_act<A>(fmaf(-lam, o[j][2 * i], o[j - 1][2 * i]),
+                                  fmaf(-lam, o[j][2 * i + 1], o[j - 1][2 * i + 1]));
+    } else {
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + row[j] * D + lane * E);
+#pragma unroll
+      for (int i = 0; i < E / 2; ++i)
+        dst[i] = float2_to_act<A>(o[j][2 * i] * inv, o[j][2 * i + 1] * inv);
+    }
   }
 }
 
-template <class A, class C, int D, int NT>
+// DIFF: differential attention.  Rows 2i and 2i + 1 of a tile are the two maps of an output row
+// (a unit's rows are its queries times an even number of heads), both in one lane, which stores
+// their difference.
+template <class A, class C, int D, int NT, bool DIFF>
 __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     bsa_cache_decode_kernel(const __grid_constant__ CUtensorMap tm_k,
                             const __grid_constant__ CUtensorMap tm_v, const CacheFwdParams p,
@@ -540,9 +564,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
         const int row = 8 * n + g, qi = group_div(row);
-        if (row < seg.nq * p.group) {
+        // Split queries: the columns of the other map's key half are zero.
+        const bool split = DIFF && p.split;
+        if (row < seg.nq * p.group && !(split && (t >> 1) != (row & 1))) {
           const A* q = static_cast<const A*>(p.q) + (seg.q0 + qi) * p.q_token_stride +
-                       (seg.h * p.group + row - qi * p.group) * p.q_head_stride + t * (16 * KT);
+                       (seg.h * p.group + row - qi * p.group) * p.q_head_stride + t * (16 * KT) -
+                       (split ? (row & 1) * (D / 2) : 0);
 #pragma unroll
           for (int c = 0; c < KT; ++c) {
             const uint4 a = *reinterpret_cast<const uint4*>(q + c * 16);
@@ -875,13 +902,29 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
               }
               const float inv = z == 0.f ? 0.f : f / z;
               uint32_t w[D / 16];
+              int64_t orow = row;
+              if constexpr (DIFF) {
 #pragma unroll
-              for (int j = 0; j < D / 16; ++j)
-                w[j] = float2_to_act<A>(o[n][j][e] * inv, o[n][j][e + 2] * inv);
-              uint4* dst = reinterpret_cast<uint4*>(static_cast<A*>(p.out) + row * D + g * VB);
+                for (int j = 0; j < D / 16; ++j) {
+                  o[n][j][e] *= inv;
+                  o[n][j][e + 2] *= inv;
+                }
+                orow = row >> 1;  // Hq is even
+                const float lam = e == 1 ? diff_lam(p, orow) : 0.f;
 #pragma unroll
-              for (int i = 0; i < D / 64; ++i)
-                dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                for (int j = 0; j < D / 16; ++j)
+                  w[j] = float2_to_act<A>(fmaf(-lam, o[n][j][1], o[n][j][0]), fmaf(-lam, o[n][j][3], o[n][j][2]));
+              } else {
+#pragma unroll
+                for (int j = 0; j < D / 16; ++j)
+                  w[j] = float2_to_act<A>(o[n][j][e] * inv, o[n][j][e + 2] * inv);
+              }
+              if (!DIFF || e == 1) {
+                uint4* dst = reinterpret_cast<uint4*>(static_cast<A*>(p.out) + orow * D + g * VB);
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i)
+                  dst[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              }
               if (g == 0) p.lse[row] = z == 0.f ? -INFINITY : (top + log2f(z)) * kLn2;
             } else {
               float4* dst = reinterpret_cast<float4*>(
@@ -910,8 +953,12 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
       if (!whole_unit) {
         if (err[2]) {
           // At most two rows a warp.
-          if (warp < s.nq * p.group)
-            join_rows<A, D, R, R / W>(p, parts, s, blockIdx.x - s.before, s.before + s.more, warp, W, lane);
+          if constexpr (DIFF) {
+            if (2 * warp < s.nq * p.group)
+              join_rows<A, D, R, 2, true>(p, parts, s, blockIdx.x - s.before, s.before + s.more, 2 * warp, R, lane);
+          } else if (warp < s.nq * p.group) {
+            join_rows<A, D, R, R / W, false>(p, parts, s, blockIdx.x - s.before, s.before + s.more, warp, W, lane);
+          }
         }
         consumer_sync<32 * W>();  // err[2] has been read
       }
@@ -922,11 +969,11 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
   if (tid == 0 && err[0] != 0) atomicMax(p.status != nullptr ? p.status : parts.status, err[0]);
 }
 
-template <class A, class C, int D, int NT>
+template <class A, class C, int D, int NT, bool DIFF>
 cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const CacheFwdParams& p,
                           void* workspace, int sms, cudaStream_t stream) {
   using Cfg = DecodeCfg<D, NT>;
-  auto* kernel = bsa_cache_decode_kernel<A, C, D, NT>;
+  auto* kernel = bsa_cache_decode_kernel<A, C, D, NT, DIFF>;
   static int done[64];
   const cudaError_t e = set_smem_once(kernel, Cfg::kSmemB, done);
   if (e != cudaSuccess) return e;
@@ -934,14 +981,14 @@ cudaError_t launch_decode(const CUtensorMap& k, const CUtensorMap& v, const Cach
   return cudaGetLastError();
 }
 
-template <class C, int D>
+template <class C, int D, bool DIFF>
 cudaError_t launch_decode(bool fp16, int rows, const CUtensorMap& k, const CUtensorMap& v,
                           const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
   if (fp16)
-    return rows <= 8 ? launch_decode<__half, C, D, 1>(k, v, p, workspace, sms, stream)
-                     : launch_decode<__half, C, D, 2>(k, v, p, workspace, sms, stream);
-  return rows <= 8 ? launch_decode<__nv_bfloat16, C, D, 1>(k, v, p, workspace, sms, stream)
-                   : launch_decode<__nv_bfloat16, C, D, 2>(k, v, p, workspace, sms, stream);
+    return rows <= 8 ? launch_decode<__half, C, D, 1, DIFF>(k, v, p, workspace, sms, stream)
+                     : launch_decode<__half, C, D, 2, DIFF>(k, v, p, workspace, sms, stream);
+  return rows <= 8 ? launch_decode<__nv_bfloat16, C, D, 1, DIFF>(k, v, p, workspace, sms, stream)
+                   : launch_decode<__nv_bfloat16, C, D, 2, DIFF>(k, v, p, workspace, sms, stream);
 }
 
 }  // namespace bsa

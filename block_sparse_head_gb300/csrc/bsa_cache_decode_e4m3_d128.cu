@@ -6,7 +6,7 @@ namespace bsa {
 cudaError_t launch_cache_decode_e4m3_d128(bool fp16, int rows, const CUtensorMap& k,
                                          const CUtensorMap& v, const CacheFwdParams& p,
                                          void* workspace, int sms, cudaStream_t stream) {
-  return launch_decode<E4M3, 128>(fp16, rows, k, v, p, workspace, sms, stream);
+  return launch_decode<E4M3, 128, false>(fp16, rows, k, v, p, workspace, sms, stream);
 }
 
 }  // namespace bsa

@@ -150,12 +150,16 @@ int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* byte
   return BSA_OK;
 }
 
-int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* block_table,
-                      const int32_t* kv_len, const int32_t* cu_q, void* out, float* lse,
-                      int32_t* status, void* workspace, int64_t workspace_bytes, int B,
-                      int max_pages, int T, int heads, int max_q, int dtype,
-                      int64_t q_token_stride, int64_t q_head_stride, float scale,
-                      const bsa_cache_args* args, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// heads: query heads.  lam: differential attention (null: not), with queries of dq numbers.
+int cache_forward(const bsa_cache* cache, const void* q, const float* lam, bool lam_rows, int dq,
+                  const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q, void* out,
+                  float* lse, int32_t* status, void* workspace, int64_t workspace_bytes, int B,
+                  int max_pages, int T, int heads, int max_q, int dtype, int64_t q_token_stride,
+                  int64_t q_head_stride, float scale, const bsa_cache_args* args, void* stream) {
   const int bad = check_cache(cache);
   if (bad != BSA_OK) return bad;
   bsa_cache_args x{-1, 0.f, nullptr, nullptr, 0};
@@ -164,6 +168,8 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
       (T > 0 && (q == nullptr || out == nullptr || lse == nullptr)))
     return BSA_ERR_NULL;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_DTYPE;
+  const bool diff = lam != nullptr;
+  if (diff && dq != cache->d && !(cache->d == 128 && dq == 64)) return BSA_ERR_UNSUPPORTED;
   if (B < 1 || T < 0 || T > bsa::kMaxPositions || max_pages < 1 || max_q < 1 ||
       check_heads(heads, cache->kv_heads) != BSA_OK ||
       static_cast<int64_t>(max_pages) * cache->page > bsa::kMaxPositions ||
@@ -173,7 +179,7 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
     return BSA_ERR_UNSUPPORTED;
   if (!aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16) || !aligned(lse, 4) ||
       !aligned(status, 4) || !aligned(block_table, 4) || !aligned(kv_len, 4) ||
-      !aligned(cu_q, 4) || !aligned(x.sinks, 4) || q_token_stride % 8 != 0 ||
+      !aligned(cu_q, 4) || !aligned(x.sinks, 4) || !aligned(lam, 4) || q_token_stride % 8 != 0 ||
       q_head_stride % 8 != 0)
     return BSA_ERR_ALIGN;
   bsa::CacheFwdParams p{};
@@ -220,6 +226,9 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
   p.lse = lse;
   p.status = status;
   p.sinks = x.sinks;
+  p.lam = lam;
+  p.lam_rows = lam_rows;
+  p.split = diff && dq != cache->d;
   p.B = B;
   p.T = T;
   p.Hq = heads;
@@ -246,18 +255,55 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
     if (!bsa::encode_cache(&k, cache->k, tiles, cache->page, cache->d, 1 << p.box_shift) ||
         !bsa::encode_cache(&v, cache->v, tiles, cache->page, cache->d, 1 << p.box_shift))
       return BSA_ERR_CUDA;
-    e = cache->d == 128
-            ? (int8 ? bsa::launch_cache_decode_int8_d128(fp16, rows, k, v, p, workspace, sms, st)
-                    : bsa::launch_cache_decode_e4m3_d128(fp16, rows, k, v, p, workspace, sms, st))
-            : (int8 ? bsa::launch_cache_decode_int8_d64(fp16, rows, k, v, p, workspace, sms, st)
-                    : bsa::launch_cache_decode_e4m3_d64(fp16, rows, k, v, p, workspace, sms, st));
+    using namespace bsa;
+    static constexpr decltype(&launch_cache_decode_int8_d64) kLaunch[2][2][2] = {
+        {{launch_cache_decode_e4m3_d64, launch_cache_decode_e4m3_d128},
+         {launch_cache_decode_int8_d64, launch_cache_decode_int8_d128}},
+        {{launch_cache_decode_diff_e4m3_d64, launch_cache_decode_diff_e4m3_d128},
+         {launch_cache_decode_diff_int8_d64, launch_cache_decode_diff_int8_d128}}};
+    e = kLaunch[diff][int8][cache->d == 128](fp16, rows, k, v, p, workspace, sms, st);
   } else {
-    e = cache->d == 128 ? (int8 ? bsa::launch_cache_tile_int8_d128(fp16, p, workspace, sms, st)
-                                : bsa::launch_cache_tile_e4m3_d128(fp16, p, workspace, sms, st))
-                        : (int8 ? bsa::launch_cache_tile_int8_d64(fp16, p, workspace, sms, st)
-                                : bsa::launch_cache_tile_e4m3_d64(fp16, p, workspace, sms, st));
+    using namespace bsa;
+    static constexpr decltype(&launch_cache_tile_int8_d64) kLaunch[2][2][2] = {
+        {{launch_cache_tile_e4m3_d64, launch_cache_tile_e4m3_d128},
+         {launch_cache_tile_int8_d64, launch_cache_tile_int8_d128}},
+        {{launch_cache_tile_diff_e4m3_d64, launch_cache_tile_diff_e4m3_d128},
+         {launch_cache_tile_diff_int8_d64, launch_cache_tile_diff_int8_d128}}};
+    e = kLaunch[diff][int8][cache->d == 128](fp16, p, workspace, sms, st);
   }
   return e == cudaSuccess ? BSA_OK : BSA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* block_table,
+                      const int32_t* kv_len, const int32_t* cu_q, void* out, float* lse,
+                      int32_t* status, void* workspace, int64_t workspace_bytes, int B,
+                      int max_pages, int T, int heads, int max_q, int dtype,
+                      int64_t q_token_stride, int64_t q_head_stride, float scale,
+                      const bsa_cache_args* args, void* stream) {
+  return cache_forward(cache, q, nullptr, false, 0, block_table, kv_len, cu_q, out, lse, status,
+                       workspace, workspace_bytes, B, max_pages, T, heads, max_q, dtype,
+                       q_token_stride, q_head_stride, scale, args, stream);
+}
+
+int bsa_cache_diff_forward(const bsa_cache* cache, const void* q, const float* lam,
+                           const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q,
+                           void* out, float* lse, int32_t* status, void* workspace,
+                           int64_t workspace_bytes, int B, int max_pages, int T, int heads, int dq,
+                           int max_q, int lam_rows, int dtype, int64_t q_token_stride,
+                           int64_t q_head_stride, float scale, const bsa_cache_args* args,
+                           void* stream) {
+  if (lam == nullptr) return BSA_ERR_NULL;
+  // Two query heads for each output head, an even number for each kv head.
+  if (cache != nullptr &&
+      (heads < 1 || heads > 32767 || cache->kv_heads < 1 || heads % cache->kv_heads != 0))
+    return BSA_ERR_SHAPE;
+  return cache_forward(cache, q, lam, lam_rows != 0, dq, block_table, kv_len, cu_q, out, lse, status,
+                       workspace, workspace_bytes, B, max_pages, T, 2 * heads, max_q, dtype,
+                       q_token_stride, q_head_stride, scale, args, stream);
 }
 
 }  // extern "C"

@@ -361,7 +361,7 @@ __device__ __forceinline__ uint4 load16(const void* ptr) {
 
 // Queries of a tile into fp16, a share of the rows for each of eight warps: 16 bytes a lane, as
 // many rows at once as a warp holds, a few loads in flight.
-template <class A, int D>
+template <class A, int D, bool DIFF>
 __device__ __forceinline__ void tile_queries(const CacheFwdParams& p, const CacheSeg& s, uint8_t* tile,
                                              float* factor, int warp, int lane) {
   constexpr int L = D / 8, RPI = 32 / L;  // lanes of a row, rows at once
@@ -378,8 +378,11 @@ __device__ __forceinline__ void tile_queries(const CacheFwdParams& p, const Cach
     for (int u = 0; u < N; ++u) {
       const int r = first + u * RPI, qi = static_cast<int>((r * p.group_inv) >> 16);
       x[u] = make_uint4(0, 0, 0, 0);
-      if (r < rows)
-        x[u] = *reinterpret_cast<const uint4*>(q + qi * p.q_token_stride + (r - qi * p.group) * p.q_head_stride);
+      // Split queries: the columns of the other map's key half are zero.
+      const bool split = DIFF && p.split;
+      if (r < rows && !(split && c / (L / 2) != (r & 1)))
+        x[u] = *reinterpret_cast<const uint4*>(q + qi * p.q_token_stride + (r - qi * p.group) * p.q_head_stride -
+                                               (split ? (r & 1) * (D / 2) : 0));
     }
 #pragma unroll
     for (int u = 0; u < N; ++u) {
@@ -410,7 +413,7 @@ __device__ __forceinline__ void tile_queries(const CacheFwdParams& p, const Cach
 }
 
 // One side (V: values, else keys) and half the queries; 128 threads.  One piece of code for both.
-template <class A, class C, int D>
+template <class A, class C, int D, bool DIFF>
 __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* smem, const bool V,
                                              volatile int* ctl) {
   using Cfg = TileCfg<D>;
@@ -468,7 +471,7 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
           if (!__all_sync(0xffffffffu, free_q.wait(ctl, kSiteProdKEmpty))) break;
           free_q.advance();
         }
-        tile_queries<A, D>(p, step().seg, smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB,
+        tile_queries<A, D, DIFF>(p, step().seg, smem + Cfg::kOffQ + (item & 1) * Cfg::kTileB,
                            reinterpret_cast<float*>(smem + Cfg::kOffFactor) + (item % Cfg::kItems) * 128,
                            warp + (V ? 4 : 0), lane);
         fence_proxy_async_smem();
@@ -516,7 +519,7 @@ __device__ __forceinline__ void tile_convert(const CacheFwdParams& p, uint8_t* s
 
 // FOLD: positive scale and no soft-cap, so that the scores' factor goes into the exponent's
 // multiplier; else they are transformed first.
-template <class A, int D, bool FOLD>
+template <class A, int D, bool FOLD, bool DIFF>
 __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* smem, uint32_t tmem,
                                              const CacheParts& parts, int* join_flag, volatile int* ctl) {
   using Cfg = TileCfg<D>;
@@ -571,6 +574,32 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       uint32_t r[32];
       tmem_ld_16x32bx2_x32<32>(to + c * 64, r);
       tmem_ld_wait(r);
+      if constexpr (DIFF) {
+        if (whole) {
+          // The row pair's two lanes exchange halves of these columns, and each stores one.
+          const bool odd = lane & 1;
+          const float lam = live ? diff_lam(p, orow >> 1) : 0.f;
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            float y[2];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+              const float a = __uint_as_float(r[2 * i + u]) * f, b = __uint_as_float(r[16 + 2 * i + u]) * f;
+              const float got = __shfl_xor_sync(0xffffffffu, odd ? a : b, 1);
+              y[u] = odd ? fmaf(-lam, b, got) : fmaf(-lam, got, a);
+            }
+            w[i] = float2_to_act<A>(y[0], y[1]);
+          }
+          if (live) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<A*>(p.out) + (orow >> 1) * D + c * 64 + half * 32 +
+                                                  (odd ? 16 : 0));
+            dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+          continue;
+        }
+      }
       if (!live) continue;
       if (whole) {
         uint4* dst = reinterpret_cast<uint4*>(static_cast<A*>(p.out) + orow * D + c * 64 + half * 32);
@@ -611,9 +640,9 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       }
       if (i == 1 && *reinterpret_cast<volatile int*>(join_flag)) {
 #pragma unroll 1
-        for (int r = w8; r < seg.nq * p.group; r += 8 * kJoinRows)
-          join_rows<A, D, R, kJoinRows>(p, parts, seg, blockIdx.x - seg.before, seg.before + seg.more, r, 8,
-                                        lane);
+        for (int r = DIFF ? 2 * w8 : w8; r < seg.nq * p.group; r += 8 * kJoinRows)
+          join_rows<A, D, R, kJoinRows, DIFF>(p, parts, seg, blockIdx.x - seg.before, seg.before + seg.more, r,
+                                              DIFF ? 16 : 8, lane);
       }
     }
     return true;
@@ -781,7 +810,8 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
 
 // ------------------------------------------------------------------------ kernel
 
-template <class A, class C, int D, bool FOLD>
+// DIFF: differential attention.  Rows 2i and 2i + 1 of a tile are the two maps of an output row.
+template <class A, class C, int D, bool FOLD, bool DIFF>
 __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdParams p, void* workspace) {
   using Cfg = TileCfg<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -844,10 +874,10 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
     }
   } else if (warp < 12) {
     setmaxnreg_inc<Cfg::kRegSoft>();
-    tile_softmax<A, D, FOLD>(p, smem, tmem, parts, err + 1, ctl);
+    tile_softmax<A, D, FOLD, DIFF>(p, smem, tmem, parts, err + 1, ctl);
   } else {
     setmaxnreg_dec<Cfg::kRegConv>();
-    tile_convert<A, C, D>(p, smem, warp >= 16, ctl);
+    tile_convert<A, C, D, DIFF>(p, smem, warp >= 16, ctl);
   }
   tc_fence_before();
   __syncthreads();
@@ -860,11 +890,11 @@ __global__ void __launch_bounds__(640, 1) bsa_cache_tile_kernel(const CacheFwdPa
   if (threadIdx.x == 0 && err[0] != 0) atomicMax(p.status != nullptr ? p.status : parts.status, err[0]);
 }
 
-template <class A, class C, int D, bool FOLD>
+template <class A, class C, int D, bool FOLD, bool DIFF>
 cudaError_t launch_tile_as(const CacheFwdParams& p, void* workspace, int sms,
                            cudaStream_t stream) {
   using Cfg = TileCfg<D>;
-  auto* kernel = bsa_cache_tile_kernel<A, C, D, FOLD>;
+  auto* kernel = bsa_cache_tile_kernel<A, C, D, FOLD, DIFF>;
   static int done[64];
   const cudaError_t e = set_smem_once(kernel, Cfg::kLaunchSmem, done);
   if (e != cudaSuccess) return e;
@@ -872,11 +902,11 @@ cudaError_t launch_tile_as(const CacheFwdParams& p, void* workspace, int sms,
   return cudaGetLastError();
 }
 
-template <class A, class C, int D>
+template <class A, class C, int D, bool DIFF>
 cudaError_t launch_tile(const CacheFwdParams& p, void* workspace, int sms, cudaStream_t stream) {
   return p.softcap_log2 == 0.f && p.scale_log2 > 0.f
-             ? launch_tile_as<A, C, D, true>(p, workspace, sms, stream)
-             : launch_tile_as<A, C, D, false>(p, workspace, sms, stream);
+             ? launch_tile_as<A, C, D, true, DIFF>(p, workspace, sms, stream)
+             : launch_tile_as<A, C, D, false, DIFF>(p, workspace, sms, stream);
 }
 
 }  // namespace bsa

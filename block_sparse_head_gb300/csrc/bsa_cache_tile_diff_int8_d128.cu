@@ -1,0 +1,12 @@
+// Tile kernels of differential attention over an int8 cache, head dim 128.
+#include "bsa_cache_tile.cuh"
+
+namespace bsa {
+
+cudaError_t launch_cache_tile_diff_int8_d128(bool fp16, const CacheFwdParams& p, void* workspace,
+                                       int sms, cudaStream_t stream) {
+  return fp16 ? launch_tile<__half, Int8, 128, true>(p, workspace, sms, stream)
+              : launch_tile<__nv_bfloat16, Int8, 128, true>(p, workspace, sms, stream);
+}
+
+}  // namespace bsa

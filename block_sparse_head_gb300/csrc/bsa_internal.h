@@ -364,6 +364,11 @@ struct CacheFwdParams {
   float* lse;                // [T, Hq]
   int32_t* status;           // [1]
   const float* sinks;        // [Hq] or null
+  // Differential attention only: query heads 2h and 2h + 1 are the maps of output head h (out is
+  // [T, Hq / 2, d]), its weight lam[h] or, with lam_rows, lam[token][h]; split: queries have d / 2
+  // numbers, for the first half of a key under map 0 and the second under map 1.
+  const float* lam;
+  int lam_rows, split;
   int B, T, Hq, Hkv, group;  // group = Hq / Hkv
   uint32_t group_inv;        // r / group = r * group_inv >> 16 for r < 256, group <= 128
   int n_pages, max_pages, page_shift;
@@ -394,6 +399,10 @@ BSA_DECODE_LAUNCH(e4m3_d64);
 BSA_DECODE_LAUNCH(e4m3_d128);
 BSA_DECODE_LAUNCH(int8_d64);
 BSA_DECODE_LAUNCH(int8_d128);
+BSA_DECODE_LAUNCH(diff_e4m3_d64);
+BSA_DECODE_LAUNCH(diff_e4m3_d128);
+BSA_DECODE_LAUNCH(diff_int8_d64);
+BSA_DECODE_LAUNCH(diff_int8_d128);
 #undef BSA_DECODE_LAUNCH
 
 // Any number of query rows, in tiles of kTileRows.
@@ -405,6 +414,10 @@ BSA_TILE_LAUNCH(e4m3_d64);
 BSA_TILE_LAUNCH(e4m3_d128);
 BSA_TILE_LAUNCH(int8_d64);
 BSA_TILE_LAUNCH(int8_d128);
+BSA_TILE_LAUNCH(diff_e4m3_d64);
+BSA_TILE_LAUNCH(diff_e4m3_d128);
+BSA_TILE_LAUNCH(diff_int8_d64);
+BSA_TILE_LAUNCH(diff_int8_d128);
 #undef BSA_TILE_LAUNCH
 
 // A cache side [tiles, page, d] of 8-bit numbers for boxes of `rows` rows of one tile,

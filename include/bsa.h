@@ -567,6 +567,33 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
                       int64_t q_token_stride, int64_t q_head_stride, float scale,
                       const bsa_cache_args* args, void* stream);
 
+/*
+ * bsa_cache_diff_forward -- differential attention (bsa_diff_forward) of the newest tokens of
+ * every request over its cache: head h of `heads` has the query heads 2h and 2h + 1, both over
+ * kv head g = h / (heads / kv_heads), and with O_m and lse_m what bsa_cache_forward gives for
+ * query head 2h + m,
+ *
+ *   out[t, h] = O_0 - lam O_1,   lse[t, 2h + m] = lse_m
+ *
+ *   q         device [T, 2 * heads, dq], strides as in bsa_cache_forward.  dq = d, or d / 2 (d =
+ *             128): map m scores the numbers [m * dq, (m + 1) * dq) of a key alone.
+ *   lam       device fp32 [heads], or with lam_rows nonzero [T, heads]; 4-byte aligned.
+ *   out       device [T, heads, d] of dtype;  lse  device fp32 [T, 2 * heads].
+ *   workspace as in bsa_cache_forward, of the size for 2 * heads query heads.
+ *   heads     a multiple of kv_heads, at most 64 times it.
+ *   args      sinks, where given, fp32 [2 * heads].
+ *   the others as in bsa_cache_forward, errors too (BSA_ERR_UNSUPPORTED: also other dq).
+ *
+ * The keys are read once for both maps.
+ */
+int bsa_cache_diff_forward(const bsa_cache* cache, const void* q, const float* lam,
+                           const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q,
+                           void* out, float* lse, int32_t* status, void* workspace,
+                           int64_t workspace_bytes, int B, int max_pages, int T, int heads, int dq,
+                           int max_q, int lam_rows, int dtype, int64_t q_token_stride,
+                           int64_t q_head_stride, float scale, const bsa_cache_args* args,
+                           void* stream);
+
 /* bsa_cache_workspace -- bytes of workspace that bsa_cache_forward needs on the current
  * device, for any batch and any lengths.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE,
  * BSA_ERR_UNSUPPORTED (d), BSA_ERR_CUDA. */

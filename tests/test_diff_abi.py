@@ -74,3 +74,30 @@ def test_workspace(lib):
         assert lib.bsa_diff_workspace(*bad, 64, 64, ctypes.byref(n)) == -2
     for bad in ((96, 64), (64, 32)):
         assert lib.bsa_diff_workspace(1, 1, 1, *bad, ctypes.byref(n)) == -6
+
+
+def test_cache_forward(lib):
+    from block_sparse_head_gb300 import binding
+
+    names = ("q", "lam", "table", "kv_len", "cu_q", "out", "lse", "status", "ws")
+
+    def f(**kw):
+        cache = binding._CACHE.pack(A, A, A, A, 64, kw.get("kv", 2), 64, kw.get("d", 128), 2)
+        ptrs = [kw.get(n, A) for n in names]
+        sizes = [kw.get(n, x) for n, x in (("B", 2), ("max_pages", 4), ("T", 2), ("heads", 4), ("dq", 128), ("max_q", 1),
+                                           ("rows", 0), ("dtype", 0))]
+        return lib.bsa_cache_diff_forward(cache, *ptrs, kw.get("bytes", 1 << 30), *sizes, 256, 256,
+                                          kw.get("scale", 0.1), None, None)
+
+    for n in names:
+        if n != "status":
+            assert f(**{n: None}) == -1, n
+    for n in ("q", "out", "ws"):
+        assert f(**{n: A + 8}) == -5, n
+    for n in ("lam", "lse", "status", "table"):
+        assert f(**{n: A + 2}) == -5, n
+    for kw, want in [(dict(dq=32), -6), (dict(dq=256), -6), (dict(d=64, dq=32), -6), (dict(d=64), -6), (dict(heads=3), -2),
+                     (dict(heads=0), -2), (dict(heads=-4), -2), (dict(heads=130, kv=2), -2), (dict(heads=1 << 30), -2),
+                     (dict(dtype=2), -4), (dict(T=-1), -2), (dict(B=0), -2), (dict(max_q=0), -2),
+                     (dict(scale=float("inf")), -6)]:
+        assert f(**kw) == want, kw
