@@ -9,6 +9,7 @@ from .binding import (  # noqa: F401
     BSA_ORDER_GROUPED,
     BsaError,
     Lut,
+    RotaryTable,
     backward,
     build_lut,
     cache_append,
@@ -24,5 +25,7 @@ from .binding import (  # noqa: F401
     forward_ext,
     library_path,
     load_library,
+    rotary,
+    rotary_table,
     topk_forward,
 )

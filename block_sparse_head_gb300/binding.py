@@ -35,7 +35,7 @@ EXPORTED = (
     "bsa_build_lut_rect", "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
     "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
     "bsa_cache_forward", "bsa_cache_workspace", "bsa_diff_forward", "bsa_diff_backward",
-    "bsa_diff_workspace", "bsa_cache_diff_forward",
+    "bsa_diff_workspace", "bsa_cache_diff_forward", "bsa_rotary_table", "bsa_rotary",
 )
 
 _ACTIVATIONS = {torch.bfloat16: 0, torch.float16: 1}          # BSA_BF16, BSA_FP16
@@ -103,6 +103,8 @@ def load_library():
         lib.bsa_diff_forward.argtypes = [vp] * 8 + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
         lib.bsa_diff_backward.argtypes = [vp] * 14 + [i64] + [ci] * 7 + [ctypes.c_float, ci, ci, vp]
         lib.bsa_diff_workspace.argtypes = [ci] * 5 + [ctypes.POINTER(i64)]
+        lib.bsa_rotary_table.argtypes = [vp, vp, ci, vp]
+        lib.bsa_rotary.argtypes = [vp, vp]
         lib.bsa_lut_export_csc.argtypes = [vp, vp, vp, vp]
         lib.bsa_backward.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float,
@@ -136,7 +138,8 @@ def load_library():
                      "bsa_lut_kv_blocks", "bsa_forward_ext", "bsa_lut_export_csc",
                      "bsa_backward", "bsa_topk_forward", "bsa_cache_resize", "bsa_cache_append",
                      "bsa_cache_forward", "bsa_cache_workspace", "bsa_diff_forward",
-                     "bsa_diff_backward", "bsa_diff_workspace", "bsa_cache_diff_forward"):
+                     "bsa_diff_backward", "bsa_diff_workspace", "bsa_cache_diff_forward",
+                     "bsa_rotary_table", "bsa_rotary"):
             getattr(lib, name).restype = ctypes.c_int
         _lib = lib
         return lib
@@ -742,6 +745,106 @@ def diff_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
         int(len(lam_shape) == 3), float(scale), int(block), int(bool(causal_diag)),
         _cache_stream(stream, dev)), "bsa_diff_backward")
     return dq, dk, dv, dlam
+
+
+_ROTARY_ARGS = struct.Struct("@PPi4x6qPPi4x6qP2qP8i")  # bsa_rotary_args
+_PAIRINGS = {"half": 0, "adjacent": 1}
+
+
+class RotaryTable:
+    """Frequencies and axes of the pairs of a head (rotary_table), on one device."""
+
+    def __init__(self, data: torch.Tensor, pairs: int, axes: int):
+        self.data, self.pairs, self.axes = data, pairs, axes
+
+
+def rotary_table(inv_freq, axis=None) -> RotaryTable:
+    """Table of rotary's pairs on the current device (bsa_rotary_table).  inv_freq: the pairs'
+    frequencies in radians per position, as numbers of 64 bits (1 to 128 of them, at most 1e6 in
+    magnitude); axis: the axis of each, 0 to 7 (None: all 0).  A ladder over all pairs whose rungs
+    are dealt to three axes, or a ladder for each axis: both are lists of these."""
+    lib = _lib or load_library()
+    f = np.ascontiguousarray(inv_freq, np.float64)
+    if f.ndim != 1 or f.size == 0:
+        raise ValueError("inv_freq must be a list of frequencies")
+    a = np.zeros(f.size, np.int32)
+    if axis is not None:
+        given = np.asarray(axis)
+        if given.shape != f.shape or given.dtype.kind not in "iu":
+            raise ValueError("axis must have a whole number for each frequency")
+        a[:] = np.clip(given, -1, 8)  # out of range stays so: the library refuses it
+    host = np.zeros((f.size, 2), np.uint64)
+    _check(lib.bsa_rotary_table(f.ctypes.data, a.ctypes.data, int(f.size), host.ctypes.data), "bsa_rotary_table")
+    dev = torch.device("cuda", torch.cuda.current_device())
+    return RotaryTable(torch.from_numpy(host.view(np.int64)).to(dev), int(f.size), int(a.max()) + 1)
+
+
+def _rotary_side(x, out, name: str, B: int, L: int, d: int, dtype, packed: bool, dev: int):
+    """Fields of bsa_rotary_side for q or k and its output (None: left out)."""
+    if x is None:
+        return (0, 0, 0, 0, 0, 0, 0, 0, 0)
+    fields, heads = [], x.shape[1]
+    for t, what in ((x, name), (out, name + "_out")):
+        shape = (L, heads, d) if packed else (B, heads, L, d)
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+            raise ValueError(f"{what} must be a {dtype} CUDA tensor of shape {shape}")
+        if t.get_device() != dev:
+            raise ValueError(f"{what} is on {t.device}, not on the current device")
+        st = t.stride()
+        if st[-1] != 1 and t.numel() > 0:
+            raise ValueError(f"{what}: the last dimension must be contiguous")
+        # The stride of a dimension of one is never used, whatever the tensor says.
+        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
+        fields.append((t.data_ptr(), *((0, st[1], st[0]) if packed else (st[0], st[1], st[2]))))
+    (p, *si), (q, *so) = fields
+    return (p, q, heads, *si, *so)
+
+
+def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: RotaryTable,
+           pairing: str = "half", inverse: bool = False, q_out: torch.Tensor | None = None,
+           k_out: torch.Tensor | None = None, stream=None):
+    """Turns the pairs of q's and k's heads by their positions (bsa_rotary), one launch.  q, k:
+    bf16 or fp16 [B, H, L, d] as the layout's calls take them, or packed [T, heads, d] as the
+    cache's do, any strides that are multiples of 8 with d contiguous; k may be None.  positions:
+    int32 [axes, L] (packed: [axes, T]) or [axes, B, L], last dimension contiguous, with the axes
+    of ``table``.  ``pairing``: "half" (numbers i and i + pairs) or "adjacent" (2i and 2i + 1);
+    ``inverse`` turns back, which is the gradient.  q_out and k_out may be q and k.  Returns (q, k)
+    turned (k None without one)."""
+    lib = _lib or load_library()
+    dev = _this_device(q, "q")
+    if q.dtype not in _ACTIVATIONS or q.dim() not in (3, 4):
+        raise ValueError("q must be bf16 or fp16 [B, H, L, d] or [T, heads, d]")
+    packed = q.dim() == 3
+    B, L, d = (1, q.shape[0], q.shape[2]) if packed else (q.shape[0], q.shape[2], q.shape[3])
+    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != q.dim()):
+        raise ValueError("k must have as many dimensions as q")
+    if not isinstance(table, RotaryTable):
+        raise ValueError("table must come from rotary_table")
+    if pairing not in _PAIRINGS:
+        raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}")
+    if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or \
+            positions.get_device() != dev:
+        raise ValueError("positions must be an int32 tensor on the current device")
+    if positions.shape not in ((table.axes, L), (table.axes, B, L)):
+        raise ValueError(f"positions has shape {tuple(positions.shape)}, expected "
+                         f"{(table.axes, L)} or {(table.axes, B, L)}")
+    if positions.stride(-1) != 1 and L > 1:
+        raise ValueError("positions: the last dimension must be contiguous")
+    if table.data.get_device() != dev:
+        raise ValueError(f"table is on {table.data.device}, not on the current device")
+    if q_out is None or (k is not None and k_out is None):
+        with _on(stream):
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+            if k is not None and k_out is None:
+                k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
+    ps = positions.stride()
+    _check(lib.bsa_rotary(_ROTARY_ARGS.pack(
+        *_rotary_side(q, q_out, "q", B, L, d, q.dtype, packed, dev),
+        *_rotary_side(k, k_out, "k", B, L, d, q.dtype, packed, dev), positions.data_ptr(), ps[0],
+        ps[1] if positions.dim() == 3 and B > 1 else 0, table.data.data_ptr(), table.pairs, table.axes,
+        _PAIRINGS[pairing], int(bool(inverse)), B, L, d, _ACTIVATIONS[q.dtype]), _cache_stream(stream, dev)),
+        "bsa_rotary")
+    return q_out, None if k is None else k_out
 
 
 def forward_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lut: Lut, scale: float,

@@ -29,6 +29,7 @@ SOURCES = [
     "bsa_cache_append.cu",
     "bsa_diff_host.cpp",
     "bsa_diff_rows.cu",
+    "bsa_rotary.cu",
 ] + [f"bsa_diff_{k}_b{b}_d{d}.cu" for k in ("fwd", "bwd") for b in (64, 128) for d in (64, 128)] + [f"bsa_cache_{k}_{c}_d{d}.cu" for k in ("decode", "tile")
      for c in ("e4m3", "int8", "diff_e4m3", "diff_int8")
      for d in (64, 128)] + [f"bsa_fwd_q{qb}_k{kb}_d{d}.cu" for qb, kb in ((64, 64), (128, 128), (64, 128), (128, 64))

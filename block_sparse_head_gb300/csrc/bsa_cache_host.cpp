@@ -154,8 +154,8 @@ int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* byte
 
 namespace {
 
-// heads: query heads.  lam: differential attention (null: not), with queries of dq numbers.
-int cache_forward(const bsa_cache* cache, const void* q, const float* lam, bool lam_rows, int dq,
+// heads: query heads.  diff: differential attention with queries of dq numbers.
+int cache_forward(const bsa_cache* cache, const void* q, bool diff, const float* lam, bool lam_rows, int dq,
                   const int32_t* block_table, const int32_t* kv_len, const int32_t* cu_q, void* out,
                   float* lse, int32_t* status, void* workspace, int64_t workspace_bytes, int B,
                   int max_pages, int T, int heads, int max_q, int dtype, int64_t q_token_stride,
@@ -165,10 +165,9 @@ int cache_forward(const bsa_cache* cache, const void* q, const float* lam, bool 
   bsa_cache_args x{-1, 0.f, nullptr, nullptr, 0};
   if (args != nullptr) x = *args;
   if (block_table == nullptr || kv_len == nullptr || cu_q == nullptr || workspace == nullptr ||
-      (T > 0 && (q == nullptr || out == nullptr || lse == nullptr)))
+      (T > 0 && (q == nullptr || out == nullptr || lse == nullptr || (diff && lam == nullptr))))
     return BSA_ERR_NULL;
   if (dtype != BSA_BF16 && dtype != BSA_FP16) return BSA_ERR_DTYPE;
-  const bool diff = lam != nullptr;
   if (diff && dq != cache->d && !(cache->d == 128 && dq == 64)) return BSA_ERR_UNSUPPORTED;
   if (B < 1 || T < 0 || T > bsa::kMaxPositions || max_pages < 1 || max_q < 1 ||
       check_heads(heads, cache->kv_heads) != BSA_OK ||
@@ -284,7 +283,7 @@ int bsa_cache_forward(const bsa_cache* cache, const void* q, const int32_t* bloc
                       int max_pages, int T, int heads, int max_q, int dtype,
                       int64_t q_token_stride, int64_t q_head_stride, float scale,
                       const bsa_cache_args* args, void* stream) {
-  return cache_forward(cache, q, nullptr, false, 0, block_table, kv_len, cu_q, out, lse, status,
+  return cache_forward(cache, q, false, nullptr, false, 0, block_table, kv_len, cu_q, out, lse, status,
                        workspace, workspace_bytes, B, max_pages, T, heads, max_q, dtype,
                        q_token_stride, q_head_stride, scale, args, stream);
 }
@@ -296,12 +295,11 @@ int bsa_cache_diff_forward(const bsa_cache* cache, const void* q, const float* l
                            int max_q, int lam_rows, int dtype, int64_t q_token_stride,
                            int64_t q_head_stride, float scale, const bsa_cache_args* args,
                            void* stream) {
-  if (lam == nullptr) return BSA_ERR_NULL;
   // Two query heads for each output head, an even number for each kv head.
   if (cache != nullptr &&
       (heads < 1 || heads > 32767 || cache->kv_heads < 1 || heads % cache->kv_heads != 0))
     return BSA_ERR_SHAPE;
-  return cache_forward(cache, q, lam, lam_rows != 0, dq, block_table, kv_len, cu_q, out, lse, status,
+  return cache_forward(cache, q, true, lam, lam_rows != 0, dq, block_table, kv_len, cu_q, out, lse, status,
                        workspace, workspace_bytes, B, max_pages, T, 2 * heads, max_q, dtype,
                        q_token_stride, q_head_stride, scale, args, stream);
 }

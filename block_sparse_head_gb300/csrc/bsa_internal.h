@@ -424,6 +424,27 @@ BSA_TILE_LAUNCH(diff_int8_d128);
 // swizzled over their whole row (128 or 64 bytes).  false: the encoder refused.
 bool encode_cache(CUtensorMap* map, const void* base, int64_t tiles, int page, int d, int rows);
 
+// Rotary positions: q (side 0) and k (side 1); heads 0: that side is left out.
+struct RotarySide {
+  const void* in;
+  void* out;
+  int heads;
+  int64_t in_batch, in_head, in_token;  // strides in elements
+  int64_t out_batch, out_head, out_token;
+};
+struct RotaryParams {
+  RotarySide side[2];
+  const int32_t* positions;
+  const bsa_rotary_pair* table;
+  int64_t pos_axis, pos_batch;
+  int B, L, d, pairs, axes, half, inverse;
+  // set by launch_rotary
+  int heads;                             // of both sides
+  int pieces;                            // of a row, one a thread
+  int tokens, token_shift, tiles, hsubs; // tokens of a CTA (a power of two), its heads at once
+};
+cudaError_t launch_rotary(RotaryParams p, bool fp16, int sms, cudaStream_t stream);
+
 // One-CTA kernel whose only wait never completes; it must give up after limit_ns.
 cudaError_t launch_wait_selftest(int32_t* status, uint64_t limit_ns, cudaStream_t stream);
 

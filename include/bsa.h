@@ -600,6 +600,73 @@ int bsa_cache_diff_forward(const bsa_cache* cache, const void* q, const float* l
 int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* bytes);
 
 /*
+ * ---------------------------------------------------------------- rotary positions
+ *
+ * bsa_rotary -- turns the pairs of numbers of every query and key head by their positions, on
+ * one axis (text) or several (time, height and width of images and video), in one launch for q
+ * and k: what the attention calls above take.  Pair i (numbers i and i + pairs, or 2i and 2i + 1)
+ * of token t lies on axis a_i with frequency f_i,
+ *
+ *   angle = positions[a_i][b][t] * f_i
+ *   (x, y) -> (x cos angle - y sin angle, x sin angle + y cos angle)
+ *
+ * and with `inverse` by -angle, which is also the gradient of the turn.  Numbers behind the last
+ * pair (2 * pairs < d) are copied.  Angles are exact before their sine and cosine are taken in
+ * fp32, for any 32-bit position; results are rounded once.
+ */
+
+/* One pair of a table: its frequency in turns per position, a 64-bit binary fraction (two's
+ * complement), and its axis. */
+typedef struct bsa_rotary_pair {
+  uint64_t turns;
+  int32_t axis;
+  int32_t reserved;
+} bsa_rotary_pair;
+
+/* bsa_rotary_table -- fills a host table (to be copied to the device, 16-byte aligned) from
+ * frequencies in radians per position.
+ *   inv_freq  host, pairs numbers, |f| <= 1e6;  axis  host, each 0 to 7, or NULL: all 0.
+ *   pairs     1 to 128.
+ * Errors: BSA_ERR_NULL, BSA_ERR_SHAPE (pairs, axis), BSA_ERR_UNSUPPORTED (a frequency). */
+int bsa_rotary_table(const double* inv_freq, const int32_t* axis, int pairs, bsa_rotary_pair* table);
+
+enum {
+  BSA_ROTARY_HALF = 0,    /* numbers i and i + pairs are a pair */
+  BSA_ROTARY_ADJACENT = 1 /* numbers 2i and 2i + 1 are          */
+};
+
+/* q or k: number x of token t of head h of batch entry b at b * batch + h * head + t * token + x
+ * of `in` (and likewise of `out`); strides in elements, multiples of 8 (the stride of a dimension
+ * of one is not used).  `out` may be `in` with the same strides; else they do not overlap. */
+typedef struct bsa_rotary_side {
+  const void* in;  /* device, dtype, 16-byte aligned */
+  void* out;       /* the same                       */
+  int heads;       /* 0: this side is left out       */
+  int64_t in_batch, in_head, in_token;
+  int64_t out_batch, out_head, out_token;
+} bsa_rotary_side;
+
+typedef struct bsa_rotary_args {
+  bsa_rotary_side q, k;
+  const int32_t* positions; /* device int32: of axis a, batch entry b, token t at
+                               a * pos_axis + b * pos_batch + t (pos_batch 0: all the same) */
+  int64_t pos_axis, pos_batch;
+  const bsa_rotary_pair* table; /* device [pairs]; its axes are below `axes`              */
+  int pairs;                /* 2 * pairs <= d                                             */
+  int axes;                 /* 1 to 8                                                     */
+  int pairing;              /* BSA_ROTARY_*                                               */
+  int inverse;
+  int B, L;                 /* batch entries, tokens of each (0: nothing to do)           */
+  int d;                    /* numbers of a head: a multiple of 8, at most 256            */
+  int dtype;                /* BSA_BF16 or BSA_FP16                                       */
+} bsa_rotary_args;
+
+/* Asynchronous, one kernel launch, allocates nothing.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE,
+ * BSA_ERR_DTYPE, BSA_ERR_ALIGN, BSA_ERR_UNSUPPORTED (pairing, in place with other strides),
+ * BSA_ERR_CUDA. */
+int bsa_rotary(const bsa_rotary_args* args, void* stream);
+
+/*
  * bsa_device_status -- synchronize `stream`, read and clear the LUT's device status
  * word.  Returns BSA_OK, or BSA_ERR_DEVICE_TIMEOUT if a bounded wait inside a
  * kernel gave up since the last check (the kernel then skipped the remaining work

@@ -225,6 +225,12 @@ def test_a_serving_step():
         assert np.all(np.abs(lse[:n].double().cpu().numpy() - rl) <= delta + 2.0 ** -20 * (1 + np.abs(rl)))
 
 
+def test_no_tokens():
+    c = DiffCase([40], [0], 4, 2, pad=0, seed=13)
+    out, lse = c.run(max_q=1)
+    assert out.shape == (0, 4, 128) and lse.shape == (0, 8)
+
+
 def test_refusals():
     c = DiffCase([40], [1], 4, 2, seed=11)
     for bad in (dict(q=c.q[:, :3]), dict(q=c.q.float()), dict(q=c.q.cpu()), dict(q=c.q[0]), dict(lam=c.lam.double()),
