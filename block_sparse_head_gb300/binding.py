@@ -633,27 +633,33 @@ def cache_diff_forward(q: torch.Tensor, lam: torch.Tensor, k_cache: torch.Tensor
         raise ValueError("a lut needs its block")
     max_q = max(T, 1) if max_q is None else int(max_q)
     i32, f32 = torch.int32, torch.float32
+    out_ptr = None if out is None else _dev_ptr(out, "out", q.dtype, (T, heads, d), dev)
+    lse_ptr = None if lse is None else _dev_ptr(lse, "lse", f32, (T, heads2), dev)
     if out is None or lse is None or workspace is None:
         with _on(stream):
             where = q.device
-            out = torch.empty(T, heads, d, dtype=q.dtype, device=where) if out is None else out
-            lse = torch.empty(T, heads2, dtype=f32, device=where) if lse is None else lse
+            if out is None:
+                out = torch.empty((T, heads, d), dtype=q.dtype, device=where)
+                out_ptr = out.data_ptr()
+            if lse is None:
+                lse = torch.empty((T, heads2), dtype=f32, device=where)
+                lse_ptr = lse.data_ptr()
             if workspace is None:
                 workspace = cache_workspace(heads2, kv_heads, d, max_q)
                 if status is None:
                     status = torch.empty(1, dtype=i32, device=where)
     rows = lam.dim() == 2
     ws_bytes = workspace.numel()
-    _check(lib.bsa_cache_diff_forward(
+    rc = lib.bsa_cache_diff_forward(
         cache, qp, _dev_ptr(lam, "lam", f32, (T, heads) if rows else (heads,), dev),
         _dev_ptr(block_table, "block_table", i32, (B, max_pages), dev),
-        _dev_ptr(kv_len, "kv_len", i32, (B,), dev), _dev_ptr(cu_q, "cu_q", i32, (B + 1,), dev),
-        _dev_ptr(out, "out", q.dtype, (T, heads, d), dev), _dev_ptr(lse, "lse", f32, (T, heads2), dev),
+        _dev_ptr(kv_len, "kv_len", i32, (B,), dev), _dev_ptr(cu_q, "cu_q", i32, (B + 1,), dev), out_ptr, lse_ptr,
         None if status is None else _dev_ptr(status, "status", i32, (1,), dev),
         _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, max_pages, T,
-        heads, dq, max_q, int(rows), _ACTIVATIONS[q.dtype], qt, qh, float(scale),
-        _cache_args(window, softcap, sinks, heads2, lut, block, dev), _cache_stream(stream, dev)),
-        "bsa_cache_diff_forward")
+        heads, dq, max_q, rows, _ACTIVATIONS[q.dtype], qt, qh, scale,
+        _cache_args(window, softcap, sinks, heads2, lut, block, dev), _cache_stream(stream, dev))
+    if rc:
+        raise BsaError(rc, "bsa_cache_diff_forward")
     return out, lse, status
 
 
@@ -685,20 +691,27 @@ def diff_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.T
     lib = _lib or load_library()
     dev, B, H, kv, L, d, dq, lam_shape = _diff_shapes(q, k, lam)
     bf16, f32 = torch.bfloat16, torch.float32
-    shape = (B, H, L, d)
+    shape, keys = (B, H, L, d), (B, kv, L, d)
+    out_ptr = None if out is None else _dev_ptr(out, "out", bf16, shape, dev)
+    lse_ptr = None if lse is None else _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev)
+    out2_ptr = None if out2 is None else _dev_ptr(out2, "out2", bf16, shape, dev)
     if out is None or lse is None or (training and out2 is None):
         with _on(stream):
-            out = torch.empty(shape, dtype=bf16, device=q.device) if out is None else out
-            lse = torch.empty(B, 2 * H, L, dtype=f32, device=q.device) if lse is None else lse
+            if out is None:
+                out = torch.empty(shape, dtype=bf16, device=q.device)
+                out_ptr = out.data_ptr()
+            if lse is None:
+                lse = torch.empty((B, 2 * H, L), dtype=f32, device=q.device)
+                lse_ptr = lse.data_ptr()
             if training and out2 is None:
-                out2 = torch.empty(shape, dtype=bf16, device=q.device)
-    _check(lib.bsa_diff_forward(
-        _dev_ptr(q, "q", bf16, (B, 2 * H, L, dq), dev), _dev_ptr(k, "k", bf16, (B, kv, L, d), dev),
-        _dev_ptr(v, "v", bf16, (B, kv, L, d), dev), _dev_ptr(lam, "lam", f32, lam_shape, dev), lut.handle,
-        _dev_ptr(out, "out", bf16, shape, dev), _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev),
-        None if out2 is None else _dev_ptr(out2, "out2", bf16, shape, dev), B, H, kv, L, d, dq,
-        int(len(lam_shape) == 3), float(scale), int(block), int(bool(causal_diag)),
-        _cache_stream(stream, dev)), "bsa_diff_forward")
+                out2 = torch.empty_like(out)
+                out2_ptr = out2.data_ptr()
+    status = lib.bsa_diff_forward(
+        _dev_ptr(q, "q", bf16, q.shape, dev), _dev_ptr(k, "k", bf16, keys, dev), _dev_ptr(v, "v", bf16, keys, dev),
+        _dev_ptr(lam, "lam", f32, lam_shape, dev), lut.handle, out_ptr, lse_ptr, out2_ptr, B, H, kv, L, d, dq,
+        len(lam_shape) == 3, scale, block, bool(causal_diag), _cache_stream(stream, dev))
+    if status:
+        raise BsaError(status, "bsa_diff_forward")
     return out, lse, out2
 
 
@@ -724,26 +737,38 @@ def diff_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
     lib = _lib or load_library()
     dev, B, H, kv, L, d, n, lam_shape = _diff_shapes(q, k, lam)
     bf16, f32 = torch.bfloat16, torch.float32
-    if dq is None or dk is None or dv is None or dlam is None or workspace is None:
-        with _on(stream):
-            where = q.device
-            dq = torch.empty(q.shape, dtype=bf16, device=where) if dq is None else dq
-            dk = torch.empty(k.shape, dtype=bf16, device=where) if dk is None else dk
-            dv = torch.empty(k.shape, dtype=bf16, device=where) if dv is None else dv
-            dlam = torch.empty(lam_shape, dtype=f32, device=where) if dlam is None else dlam
-            workspace = diff_workspace(B, H, L, d, block) if workspace is None else workspace
     rows, keys = (B, H, L, d), (B, kv, L, d)
-    ws_bytes = workspace.numel()
-    _check(lib.bsa_diff_backward(
-        _dev_ptr(q, "q", bf16, (B, 2 * H, L, n), dev), _dev_ptr(k, "k", bf16, keys, dev),
-        _dev_ptr(v, "v", bf16, keys, dev), _dev_ptr(lam, "lam", f32, lam_shape, dev),
-        _dev_ptr(out, "out", bf16, rows, dev), _dev_ptr(out2, "out2", bf16, rows, dev),
-        _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev), _dev_ptr(dout, "dout", bf16, rows, dev),
-        lut.handle, _dev_ptr(dq, "dq", bf16, (B, 2 * H, L, n), dev), _dev_ptr(dk, "dk", bf16, keys, dev),
-        _dev_ptr(dv, "dv", bf16, keys, dev), _dev_ptr(dlam, "dlam", f32, lam_shape, dev),
-        _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, H, kv, L, d, n,
-        int(len(lam_shape) == 3), float(scale), int(block), int(bool(causal_diag)),
-        _cache_stream(stream, dev)), "bsa_diff_backward")
+    q_ptr, k_ptr = _dev_ptr(q, "q", bf16, q.shape, dev), _dev_ptr(k, "k", bf16, keys, dev)
+    v_ptr, lam_ptr = _dev_ptr(v, "v", bf16, keys, dev), _dev_ptr(lam, "lam", f32, lam_shape, dev)
+    given = [None if t is None else _dev_ptr(t, name, like.dtype, like.shape, dev)
+             for t, name, like in ((dq, "dq", q), (dk, "dk", k), (dv, "dv", v), (dlam, "dlam", lam))]
+    if workspace is not None:
+        ws_bytes = workspace.numel()
+        ws_ptr = _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev)
+    if workspace is None or None in given:
+        with _on(stream):
+            if dq is None:
+                dq = torch.empty_like(q)
+                given[0] = dq.data_ptr()
+            if dk is None:
+                dk = torch.empty_like(k)
+                given[1] = dk.data_ptr()
+            if dv is None:
+                dv = torch.empty_like(v)
+                given[2] = dv.data_ptr()
+            if dlam is None:
+                dlam = torch.empty_like(lam)
+                given[3] = dlam.data_ptr()
+            if workspace is None:
+                workspace = diff_workspace(B, H, L, d, block)
+                ws_bytes, ws_ptr = workspace.numel(), workspace.data_ptr()
+    status = lib.bsa_diff_backward(
+        q_ptr, k_ptr, v_ptr, lam_ptr, _dev_ptr(out, "out", bf16, rows, dev), _dev_ptr(out2, "out2", bf16, rows, dev),
+        _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev), _dev_ptr(dout, "dout", bf16, rows, dev), lut.handle, *given,
+        ws_ptr, ws_bytes, B, H, kv, L, d, n, len(lam_shape) == 3, scale, block, bool(causal_diag),
+        _cache_stream(stream, dev))
+    if status:
+        raise BsaError(status, "bsa_diff_backward")
     return dq, dk, dv, dlam
 
 
@@ -779,25 +804,24 @@ def rotary_table(inv_freq, axis=None) -> RotaryTable:
     return RotaryTable(torch.from_numpy(host.view(np.int64)).to(dev), int(f.size), int(a.max()) + 1)
 
 
-def _rotary_side(x, out, name: str, B: int, L: int, d: int, dtype, packed: bool, dev: int):
-    """Fields of bsa_rotary_side for q or k and its output (None: left out)."""
-    if x is None:
-        return (0, 0, 0, 0, 0, 0, 0, 0, 0)
-    fields, heads = [], x.shape[1]
-    for t, what in ((x, name), (out, name + "_out")):
-        shape = (L, heads, d) if packed else (B, heads, L, d)
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
-            raise ValueError(f"{what} must be a {dtype} CUDA tensor of shape {shape}")
-        if t.get_device() != dev:
-            raise ValueError(f"{what} is on {t.device}, not on the current device")
-        st = t.stride()
-        if st[-1] != 1 and t.numel() > 0:
-            raise ValueError(f"{what}: the last dimension must be contiguous")
-        # The stride of a dimension of one is never used, whatever the tensor says.
-        st = [s if n > 1 else 0 for s, n in zip(st, shape)]
-        fields.append((t.data_ptr(), *((0, st[1], st[0]) if packed else (st[0], st[1], st[2]))))
-    (p, *si), (q, *so) = fields
-    return (p, q, heads, *si, *so)
+def _rotary_rows(t, name: str, dtype, shape, dev: int):
+    """(pointer, batch, head and token strides) of q, k or an output of rotary's."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape:
+        raise ValueError(f"{name} must be a {dtype} CUDA tensor of shape {tuple(shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} is on {t.device}, not on the current device")
+    if len(shape) == 3:
+        (token, head, one), batch = t.stride(), 0
+        tokens, heads, _ = shape
+    else:
+        batch, head, token, one = t.stride()
+        many, heads, tokens, _ = shape
+        if many == 1:
+            batch = 0
+    if one != 1 and t.numel() > 0:
+        raise ValueError(f"{name}: the last dimension must be contiguous")
+    # The stride of a dimension of one is never used, whatever the tensor says.
+    return t.data_ptr(), batch, head if heads > 1 else 0, token if tokens > 1 else 0
 
 
 def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, table: RotaryTable,
@@ -837,13 +861,21 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, tab
             q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
             if k is not None and k_out is None:
                 k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-    ps = positions.stride()
-    _check(lib.bsa_rotary(_ROTARY_ARGS.pack(
-        *_rotary_side(q, q_out, "q", B, L, d, q.dtype, packed, dev),
-        *_rotary_side(k, k_out, "k", B, L, d, q.dtype, packed, dev), positions.data_ptr(), ps[0],
-        ps[1] if positions.dim() == 3 and B > 1 else 0, table.data.data_ptr(), table.pairs, table.axes,
-        _PAIRINGS[pairing], int(bool(inverse)), B, L, d, _ACTIVATIONS[q.dtype]), _cache_stream(stream, dev)),
-        "bsa_rotary")
+    ps, shape, dtype = positions.stride(), q.shape, q.dtype
+    qi, q0, q1, q2 = _rotary_rows(q, "q", dtype, shape, dev)
+    qo, q3, q4, q5 = _rotary_rows(q_out, "q_out", dtype, shape, dev)
+    ki = k0 = k1 = k2 = ko = k3 = k4 = k5 = k_heads = 0
+    if k is not None:
+        k_heads = k.shape[1]
+        shape = (L, k_heads, d) if packed else (B, k_heads, L, d)
+        ki, k0, k1, k2 = _rotary_rows(k, "k", dtype, shape, dev)
+        ko, k3, k4, k5 = _rotary_rows(k_out, "k_out", dtype, shape, dev)
+    status = lib.bsa_rotary(_ROTARY_ARGS.pack(
+        qi, qo, q.shape[1], q0, q1, q2, q3, q4, q5, ki, ko, k_heads, k0, k1, k2, k3, k4, k5, positions.data_ptr(),
+        ps[0], ps[1] if positions.dim() == 3 and B > 1 else 0, table.data.data_ptr(), table.pairs, table.axes,
+        _PAIRINGS[pairing], bool(inverse), B, L, d, _ACTIVATIONS[dtype]), _cache_stream(stream, dev))
+    if status:
+        raise BsaError(status, "bsa_rotary")
     return q_out, None if k is None else k_out
 
 

@@ -198,9 +198,8 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   if (launch(dq != d, false, p, tq, tdo32, tk, tv, std::min(p.n, sms), st) != cudaSuccess)
     return BSA_ERR_CUDA;
   if (launch(dq != d, true, p, tk, tv, tq, tdo64, sms, st) != cudaSuccess ||
-      bsa::launch_diff_join(p, sms, st) != cudaSuccess)
+      bsa::launch_diff_join(p, sms, lam_rows ? nullptr : dlam, H, st) != cudaSuccess)
     return BSA_ERR_CUDA;
-  if (!lam_rows && bsa::launch_diff_lam(rows, dlam, B, H, L, st) != cudaSuccess) return BSA_ERR_CUDA;
   return BSA_OK;
 }
 

@@ -60,33 +60,44 @@ __global__ void __launch_bounds__(256) bsa_diff_rows_kernel(const DiffRowsParams
         (q & 31)] = x;
 }
 
-// One CTA a head; fp64 sums in a fixed order.
-__global__ void __launch_bounds__(256) bsa_diff_lam_kernel(const float* __restrict__ rows,
-                                                           float* __restrict__ dlam, int B, int H,
-                                                           int L) {
+// dlam[h] = sum over b and rows of rows[b, h, :], by one CTA in fp64 and a fixed order.
+__device__ void sum_lam(const float* rows, float* dlam, int B, int H, int h, int L) {
   __shared__ double part[8];
   double s = 0.0;
   for (int b = 0; b < B; ++b) {
-    const float* r = rows + (static_cast<int64_t>(b) * H + blockIdx.x) * L;
-    for (int i = threadIdx.x; i < L; i += 256) s += static_cast<double>(r[i]);
+    const float* r = rows + (static_cast<int64_t>(b) * H + h) * L;
+    float x[8];
+    for (int i = threadIdx.x; i < L; i += 8 * 256) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u) x[u] = i + 256 * u < L ? r[i + 256 * u] : 0.f;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) s += static_cast<double>(x[u]);
+    }
   }
 #pragma unroll
   for (int w = 16; w >= 1; w /= 2) s += __shfl_xor_sync(0xffffffffu, s, w);
+  __syncthreads();  // the head before has read its parts
   if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = s;
   __syncthreads();
   if (threadIdx.x == 0) {
     for (int w = 1; w < 8; ++w) s += part[w];
-    dlam[blockIdx.x] = static_cast<float>(s);
+    dlam[h] = static_cast<float>(s);
   }
 }
 
 // Block x < grid of the dK/dV walk: the column cut at the start of CTA x's share, if CTA x - 1 has
 // its first piece, is the sum of its pieces in the CTAs' order.  Blocks behind: the zeros of
-// columns without an active block.  y: a share of the column's rows.
-__global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams p, int grid) {
+// columns without an active block.  y: a share of the column's rows; and, behind the last share,
+// the weight's gradient of heads x, x + gridDim.x, .. (where it is one number a head).
+__global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams p, int grid, int shares,
+                                                            float* dlam, int H) {
+  if (static_cast<int>(blockIdx.y) == shares) {
+    for (int h = blockIdx.x; h < H; h += gridDim.x) sum_lam(p.dlam, dlam, p.B, H, h, p.L);
+    return;
+  }
   const int d = p.d, lanes = d / 2;  // threads of a row, four numbers of dV | dK each
   const int r0 = threadIdx.x / lanes, at = threadIdx.x % lanes * 4;
-  const int rows = p.block / gridDim.y, step = 256 / lanes;
+  const int rows = p.block / shares, step = 256 / lanes;
   auto store = [&](int b, int col, int row, float4 x) {
     const int kv = col / p.nb, key = (col - kv * p.nb) * p.block + row;
     if (key >= p.L) return;
@@ -140,9 +151,10 @@ __global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams 
 
 }  // namespace
 
-cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, cudaStream_t stream) {
+cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, float* dlam, int H, cudaStream_t stream) {
   const int more = static_cast<int>(std::min<long long>(64, static_cast<long long>(p.B) * p.cols));
-  bsa_diff_join_kernel<<<dim3(grid + more, 8), 256, 0, stream>>>(p, grid);
+  constexpr int kShares = 8;
+  bsa_diff_join_kernel<<<dim3(grid + more, kShares + (dlam != nullptr)), 256, 0, stream>>>(p, grid, kShares, dlam, H);
   return cudaGetLastError();
 }
 
@@ -155,11 +167,6 @@ cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream) {
     bsa_diff_rows_kernel<128><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
   else
     bsa_diff_rows_kernel<64><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
-  return cudaGetLastError();
-}
-
-cudaError_t launch_diff_lam(const float* rows, float* dlam, int B, int H, int L, cudaStream_t stream) {
-  bsa_diff_lam_kernel<<<H, 256, 0, stream>>>(rows, dlam, B, H, L);
   return cudaGetLastError();
 }
 

@@ -238,8 +238,9 @@ __host__ __device__ inline long long diff_share(const DiffBwdParams& p, int grid
   const long long n = (diff_steps(p) + grid - 1) / grid;
   return n < kDiffShare ? kDiffShare : n;
 }
-// Joins the pieces of cut columns (in order) and writes the zeros of columns without a block.
-cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, cudaStream_t stream);
+// Joins the pieces of cut columns (in order) and writes the zeros of columns without a block; sums
+// the rows of dlam to one number a head where dlam is not null.
+cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, float* dlam, int H, cudaStream_t stream);
 // a, b, x, y: q, dO, k, v (dQ walk) or k, v, q, dO (kv).
 #define BSA_DIFF_BWD(name)                                                                      \
   cudaError_t launch_diff_bwd_##name(bool split, bool kv, const DiffBwdParams& p,               \
@@ -263,8 +264,6 @@ struct DiffRowsParams {
   int H, L, d, lam_rows;
 };
 cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream);
-// dlam[h] = sum over b and rows of rows[b, h, :], in a fixed order.
-cudaError_t launch_diff_lam(const float* rows, float* dlam, int B, int H, int L, cudaStream_t stream);
 
 // [heads, L, d] bf16 as four dimensions: 64 columns, rows, d/64 column halves, heads.  The box
 // is 64 columns x rows x halves of one head, 128-byte swizzled; rows past L read as zero.
