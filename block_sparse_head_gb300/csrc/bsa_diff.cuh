@@ -20,21 +20,29 @@ __device__ __forceinline__ int2 stream_range(const DiffList& p) {
   return make_int2(0, full + (((full & 1) ? grid - 1 - c : c) < rest ? 1 : 0));
 }
 
-// Sub-item u of this CTA as a device record {b * H + h, first query / 64, first col_idx entry,
-// nnz | (dpos + 1) << 16}.
-__device__ __forceinline__ int4 stream_item(const DiffList& p, int u) {
+__device__ __forceinline__ unsigned diff_place(int u) {
   const int grid = gridDim.x, c = blockIdx.x;
-  const unsigned k = u * grid + ((u & 1) ? grid - 1 - c : c);
-  const unsigned per = p.pairs * p.halves, item = k / per, rest = k - item * per;
-  const unsigned half = rest / p.pairs, pair = rest - half * p.pairs;
-  const int4 r = p.list[item];
-  return make_int4(r.x * p.pairs + pair, r.y * p.halves + half, r.z, r.w);
+  return u * grid + ((u & 1) ? grid - 1 - c : c);
+}
+__device__ __forceinline__ int4 stream_item(const DiffList& p, int u) {
+  return p.list[diff_place(u) / static_cast<unsigned>(p.pairs * p.halves)];
+}
+// Sub-item u of this CTA as a record {b * H + h, first query / 64, first col_idx entry, nnz |
+// (dpos + 1) << 16}, from its item's.
+__device__ __forceinline__ int4 stream_place(const DiffList& p, int u, const int4& r) {
+  if (r.w < 0) return r;  // the end
+  const unsigned rest = diff_place(u) % static_cast<unsigned>(p.pairs * p.halves);
+  const unsigned half = rest / p.pairs;
+  return make_int4(r.x * p.pairs + (rest - half * p.pairs), r.y * p.halves + half, r.z, r.w);
 }
 __device__ __forceinline__ int2 stream_range(const DiffFwdParams& p) {
   return stream_range(static_cast<const DiffList&>(p));
 }
 __device__ __forceinline__ int4 stream_item(const DiffFwdParams& p, int u) {
   return stream_item(static_cast<const DiffList&>(p), u);
+}
+__device__ __forceinline__ int4 stream_place(const DiffFwdParams& p, int u, const int4& r) {
+  return stream_place(static_cast<const DiffList&>(p), u, r);
 }
 
 }  // namespace bsa

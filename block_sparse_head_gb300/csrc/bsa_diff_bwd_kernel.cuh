@@ -22,7 +22,7 @@
 //              E2 = dS^T 128.  acc1 += E1 Y = dV,  acc2 += E2 X = dK / scale: the sum over maps
 //              and heads stays in TMEM.  A column's steps are its entries times heads times
 //              halves, and columns differ widely (a global one is seen by every row), so that
-//              the CTAs share the steps, not the columns out (diff_share): a share's cut columns
+//              the CTAs share the steps, not the columns out: a share's cut columns
 //              leave fp32 pieces that bsa_diff_rows.cu joins in order.
 // Queries of d / 2 numbers are laid out over d columns, zero in the other map's half
 // (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
@@ -43,6 +43,9 @@ __device__ __forceinline__ int2 stream_range(const DiffBwdParams& p) {
 }
 __device__ __forceinline__ int4 stream_item(const DiffBwdParams& p, int u) {
   return stream_item(static_cast<const DiffList&>(p), u);
+}
+__device__ __forceinline__ int4 stream_place(const DiffBwdParams& p, int u, const int4& r) {
+  return stream_place(static_cast<const DiffList&>(p), u, r);
 }
 
 // Row terms of 64 queries: two groups of 32, each [-lse_0, -lse_1 (log2 units), -D_0, -D_1, -lam]
@@ -96,7 +99,7 @@ struct DiffBwdCfg {
   static constexpr uint32_t kIdescAcc = idesc_bf16_f32(kRows, D, false, true);  // B MN-major
 };
 
-// This CTA's steps of the dK/dV walk (see diff_share), a column's end loaded one column ahead.
+// This CTA's steps of the dK/dV walk (see DiffBwdParams), a column's end loaded one column ahead.
 struct DiffKvWalk {
   long long left;    // steps still to go, this one among them
   int per;           // steps of a column's entry: heads of the kv head times halves
@@ -107,23 +110,15 @@ struct DiffKvWalk {
     return c < p.cols ? p.col_ptr[c + 1] : 0;
   }
   __device__ __forceinline__ void init(const DiffBwdParams& p) {
-    const long long total = diff_steps(p), share = diff_share(p, gridDim.x);
-    const long long at = blockIdx.x * share;
-    left = total - at < share ? total - at : share;
+    const long long at = blockIdx.x * p.share;
+    left = p.steps - at < p.share ? p.steps - at : p.share;
     if (left <= 0) return;
     per = p.pairs * p.halves;
-    const long long entry = at / per;
+    const long long entry = diff_div(at, per);
     rest = static_cast<int>(at - entry * per);
-    b = static_cast<int>(entry / p.nnz);
+    b = static_cast<int>(diff_div(entry, p.nnz));
     x = static_cast<int>(entry - static_cast<long long>(b) * p.nnz);
-    // the column with col_ptr[col] <= x < col_ptr[col + 1]
-    int lo = 0, hi = p.cols - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi) >> 1;
-      if (p.col_ptr[mid + 1] > x) hi = mid;
-      else lo = mid + 1;
-    }
-    col = lo;
+    col = diff_column(p, x);
     begin = p.col_ptr[col];
     end = p.col_ptr[col + 1];
     next_end = end_of(p, col + 1);
@@ -831,6 +826,7 @@ __global__ void __launch_bounds__(DiffBwdCfg<BLK, D, KV>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, p.expire_site};
+  wait_before();
   if (warp == 0) {
     if (lane == 0) {
       if constexpr (KV) diff_kv_producer<BLK, D, SPLIT>(p, &tm_a, &tm_b, &tm_x, &tm_y, sbase, ctl);
@@ -867,8 +863,7 @@ cudaError_t launch_diff_bwd(const DiffBwdParams& p, const CUtensorMap& a, const 
   static int done[64] = {0};
   const cudaError_t e = set_smem_once(kernel, C::kLaunchSmem, done);
   if (e != cudaSuccess) return e;
-  kernel<<<grid, C::kThreads, C::kLaunchSmem, stream>>>(a, b, x, y, p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(grid), C::kThreads, C::kLaunchSmem, stream, a, b, x, y, p);
 }
 
 }  // namespace bsa

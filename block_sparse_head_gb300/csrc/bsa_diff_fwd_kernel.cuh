@@ -4,8 +4,8 @@
 // A work item is 64 queries of one head, both maps as 128 rows (bsa_diff.cuh): row 32 w + 16 m
 // + r is query 16 w + r under map m, so that the two rows of a query sit 16 lanes apart in one
 // warp's TMEM lanes.  Everything up to the epilogue is the plain forward's pipeline at 128 query
-// rows (bsa_fwd_kernel.cuh: roles, barriers, S buffers, register split): warp 0 loads, warp 1
-// issues S = Q K^T, warp 2 O += P V, softmax warps 4-7 hold the rows of map 0 and 8-11 those of
+// rows (bsa_fwd_kernel.cuh: roles, barriers, S buffers, register split): warp 0 loads keys and
+// values, warp 3 queries, warp 1 issues S = Q K^T, warp 2 O += P V, softmax warps 4-7 hold the rows of map 0 and 8-11 those of
 // map 1 (each with its own running maximum and sum), and the epilogue warps read O out, divide
 // each row by its sum, exchange halves of the columns with the lane 16 away and store
 // O_0 - lam O_1 (and, for a training step, O_1, which the backward needs).
@@ -18,15 +18,53 @@
 
 namespace bsa {
 
-// ----------------------------------------------------------------- producer
+// The plain forward's layout of shared memory and barriers, with barriers of their own for Q.
+template <int KB, int D>
+struct DiffFwdCfg : FwdCfg<128, KB, D> {
+  using Base = FwdCfg<128, KB, D>;
+  static constexpr int kBarQF = Base::kNumBars;       // [2] Q of an item landed
+  static constexpr int kBarQE = Base::kNumBars + 2;   // [2] the item's last S complete
+  static constexpr int kNumBars = Base::kNumBars + 4;
+  static constexpr int kBarBytes = 256;
+  static_assert(kNumBars * 8 + 8 <= kBarBytes, "barrier area");
+  static constexpr int kOffStats = Base::kOffBar + kBarBytes;
+  static constexpr int kSmemBytes = kOffStats + 128 * 8 + 1024;  // + align slack
+  static_assert(kSmemBytes <= 232448, "shared memory budget");
+  static constexpr int kLaunchSmem = kSmemBytes > 120 * 1024 ? kSmemBytes : 120 * 1024;
+};
 
+// ---------------------------------------------------------------- producers
+
+// Queries, by a warp of their own: an item's are eight or sixteen copies, which would hold up the
+// keys', and go out as soon as the item before the last has had its last product.
 template <int KB, int D, bool SPLIT>
-__device__ __forceinline__ void diff_producer(const DiffFwdParams& p, const CUtensorMap* tm_q,
-                                              const CUtensorMap* tm_k, const CUtensorMap* tm_v,
-                                              uint32_t sbase, const WaitCtl& ctl) {
-  using C = FwdCfg<128, KB, D>;
+__device__ __forceinline__ void diff_query_producer(const DiffFwdParams& p, const CUtensorMap* tm_q,
+                                                    uint32_t sbase, const WaitCtl& ctl) {
+  using C = DiffFwdCfg<KB, D>;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  int n = 0;  // items armed
+  ItemStream is;
+  for (is.init<true>(p); !is.done(); is.next<true>(p), ++n) {
+    if (n >= 2 && !mbar_wait_inl(bar(C::kBarQE + (n & 1)), ((n - 2) / 2) & 1, ctl, kSiteProdKEmpty)) break;
+    const uint32_t fb = bar(C::kBarQF + (n & 1)), qd = sbase + C::kOffQ + (n & 1) * C::kQTile;
+    mbar_arrive_expect_tx(fb, SPLIT ? C::kQTile / 2 : C::kQTile);
+#pragma unroll
+    for (int w = 0; w < 4; ++w)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+#pragma unroll
+        for (int z = 0; z < (SPLIT ? 1 : D / 64); ++z)
+          tma_load_4d(qd + (SPLIT ? m : z) * C::kQRegion + (32 * w + 16 * m) * 128, tm_q, fb, 0,
+                      is.cur.y * 64 + 16 * w, z, 2 * is.cur.x + m);
+  }
+  for (int j = (n > 2 ? n - 2 : 0); j < n; ++j) mbar_drain_wait(bar(C::kBarQF + (j & 1)), (j / 2) & 1);
+}
+
+template <int KB, int D>
+__device__ __forceinline__ void diff_producer(const DiffFwdParams& p, const CUtensorMap* tm_k,
+                                              const CUtensorMap* tm_v, uint32_t sbase, const WaitCtl& ctl) {
+  using C = DiffFwdCfg<KB, D>;
   constexpr int G = C::kG;
-  constexpr int kQBytes = SPLIT ? C::kQTile / 2 : C::kQTile;  // loaded; the rest stays zero
   auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
   struct StepKeys {
     int col[G];
@@ -51,17 +89,11 @@ __device__ __forceinline__ void diff_producer(const DiffFwdParams& p, const CUte
   for (int t = 0;; ++t) {
     StepKeys r0{};
     r0.nblk = 0;
-    bool first = false;
-    int pair = 0, q64 = 0, qb = 0;
     if (c.valid()) {
       r0.nblk = c.nblk();
-      pair = c.is.cur.x;
-      r0.head = pair / p.pairs;
+      r0.head = c.is.cur.x / p.pairs;
 #pragma unroll
       for (int g = 0; g < G; ++g) r0.col[g] = colv[g];
-      first = (c.s == 0);
-      q64 = c.is.cur.y;
-      qb = c.is.n % C::kNQ;
       c.advance(p);
       fetch_cols();  // the next step's columns, consumed one iteration later
     } else {
@@ -69,25 +101,12 @@ __device__ __forceinline__ void diff_producer(const DiffFwdParams& p, const CUte
       if (nsteps == 0 || t >= nsteps + 2) break;
     }
     if (r0.nblk > 0) {
-      // K slot and Q tile free: as in the plain forward's producer.
-      int j = (t >= 3) ? t - 3 : -1;
-      if (first) j = max(j, t - 2);
+      // K slot t % 3 held K(t-3), read by S(t-3).
       static_assert(C::kNQ == 2 && C::kNK == 3, "slot reuse is tied to the S buffers");
-      if (j >= 0 && !mbar_wait_inl(bar(C::kBarSF + j % 3), (j / 3) & 1, ctl, kSiteProdKEmpty)) break;
+      if (t >= 3 && !mbar_wait_inl(bar(C::kBarSF + t % 3), ((t - 3) / 3) & 1, ctl, kSiteProdKEmpty)) break;
       const uint32_t fb = bar(C::kBarKF + t % 3);
-      mbar_arrive_expect_tx(fb, (first ? kQBytes : 0) + r0.nblk * C::kBlkB);
+      mbar_arrive_expect_tx(fb, r0.nblk * C::kBlkB);
       ++nk;
-      if (first) {
-        const uint32_t qd = sbase + C::kOffQ + qb * C::kQTile;
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-#pragma unroll
-            for (int z = 0; z < (SPLIT ? 1 : D / 64); ++z)
-              tma_load_4d(qd + (SPLIT ? m : z) * C::kQRegion + (32 * w + 16 * m) * 128, tm_q, fb, 0,
-                          q64 * 64 + 16 * w, z, 2 * pair + m);
-      }
       const uint32_t kdst = sbase + C::kOffK + (t % 3) * C::kKVTile;
 #pragma unroll
       for (int g = 0; g < G; ++g)
@@ -117,12 +136,62 @@ __device__ __forceinline__ void diff_producer(const DiffFwdParams& p, const CUte
     mbar_drain_wait(bar(C::kBarVF + j % 3), (j / 3) & 1);
 }
 
+// -------------------------------------------------------------- S issuer
+
+// S(t) = Q K(t)^T into S[t % 3], as in the plain forward.
+template <int KB, int D>
+__device__ __forceinline__ void diff_mma_s(const DiffFwdParams& p, uint32_t sbase, uint32_t tmem,
+                                           const WaitCtl& ctl) {
+  using C = DiffFwdCfg<KB, D>;
+  constexpr int G = C::kG;
+  auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
+  const MmaDescs<128, KB, D> md(sbase);
+  StepCursor<G> c;
+  c.init(p);
+  for (int t = 0; c.valid(); ++t) {
+    const int nblk = c.nblk(), n = c.is.n;
+    const bool first = c.s == 0, last = c.s == c.nsteps - 1;
+    c.advance(p);
+    if (first && !mbar_wait_inl(bar(C::kBarQF + (n & 1)), (n / 2) & 1, ctl, kSiteMmaStage)) break;
+    if (!mbar_wait_inl(bar(C::kBarKF + t % 3), (t / 3) & 1, ctl, kSiteMmaStage)) break;
+    // S[t % 3] was last read by PV(t-3).
+    if (t >= 3 && !mbar_wait_inl(bar(C::kBarPVD + t % 3), ((t - 3) / 3) & 1, ctl, kSiteMmaPvDone)) break;
+    tc_fence_after();
+    const uint32_t sb = tmem + (t % 3) * 128;
+    const uint32_t qlo = md.q0 + (n & 1) * (C::kQTile >> 4);
+    const uint32_t klo = md.k0 + (t % 3) * (C::kKVTile >> 4);
+    auto s_mmas = [&](int nb) {
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const uint32_t qa = qlo + (((kk >> 2) * C::kQRegion + (kk & 3) * 32) >> 4);
+        const uint32_t kb = klo + (((kk >> 2) * C::kHalfB + (kk & 3) * 32) >> 4);
+        if (KB == 128) {
+          tc_mma_ss_lh(sb, qa, md.hi, kb, md.hi, C::kIdescS, kk > 0 ? 1u : 0u);
+        } else {
+#pragma unroll
+          for (int g = 0; g < nb; ++g)
+            tc_mma_ss_lh(sb + g * KB, qa, md.hi, kb + ((g * C::kBlkB) >> 4), md.hi, C::kIdescS1,
+                         kk > 0 ? 1u : 0u);
+        }
+      }
+    };
+    if (KB == 64 && nblk > 1)  // a branch between two MMAs slows their issue
+      s_mmas(2);
+    else
+      s_mmas(1);
+    tc_commit(bar(C::kBarSF + t % 3));
+    if (last) tc_commit(bar(C::kBarQE + (n & 1)));
+  }
+  tc_commit(bar(C::kBarDrainS));
+  mbar_drain_wait(bar(C::kBarDrainS), 0);
+}
+
 // ------------------------------------------------------------------ softmax
 
 template <int KB, int D>
 __device__ __forceinline__ void diff_softmax(const DiffFwdParams& p, uint32_t sbase, uint8_t* smem,
                                              uint32_t tmem, const WaitCtl& ctl) {
-  using C = FwdCfg<128, KB, D>;
+  using C = DiffFwdCfg<KB, D>;
   constexpr int G = C::kG;
   constexpr int NC = 64;  // score columns per thread
   constexpr int NA = 8;   // independent max chains
@@ -163,6 +232,8 @@ __device__ __forceinline__ void diff_softmax(const DiffFwdParams& p, uint32_t sb
   for (is.init<true>(p); ok && !is.done(); is.next<true>(p)) {
     const int nnz = is.nnz();
     const int dpos = p.causal_diag ? is.dpos() : -1;  // position of the diagonal block in the row
+    // Position of a block that the end of the sequence cuts: only the last one can be.
+    const int cut = ragged && p.col_idx[is.cur.z + nnz - 1] == p.L / KB ? nnz - 1 : -1;
     // The query's place in its layout block: block 128 has two tiles.
     const int qblk = qin + (KB == 128 ? (is.cur.y & 1) * 64 : 0);
     const int nsteps = (nnz + G - 1) / G;
@@ -174,10 +245,7 @@ __device__ __forceinline__ void diff_softmax(const DiffFwdParams& p, uint32_t sb
       // Last key of this half's 64 that the row sees: before the diagonal's end and the sequence's.
       int lim = NC - 1;
       if (valid && ((KB == 128) ? s : s * 2 + half) == dpos) lim = min(lim, qblk - kbase);
-      if (ragged && valid) {  // the load overlaps the S wait
-        const int col = p.col_idx[is.cur.z + s * G + (KB == 64 ? half : 0)];
-        lim = min(lim, p.L - 1 - col * KB - kbase);
-      }
+      if (valid && ((KB == 128) ? s : s * 2 + half) == cut) lim = min(lim, (p.L - 1) % KB - kbase);
       if (!valid) lim = -1;
       const uint32_t ts = tl + (g % 3) * 128;
       if (__all_sync(0xffffffffu, s_next)) {
@@ -291,7 +359,7 @@ template <int KB, int D>
 __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t sbase,
                                               const uint8_t* smem, uint32_t tmem,
                                               const WaitCtl& ctl) {
-  using C = FwdCfg<128, KB, D>;
+  using C = DiffFwdCfg<KB, D>;
   constexpr int G = C::kG;
   constexpr int HC = D / 2;  // output columns of each of a query's two lanes
   constexpr float kLn2 = 0.6931471805599453f;
@@ -315,11 +383,11 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
     if (lane == 0) mbar_arrive(bar(b));
   };
   // 32 columns as bf16: whole sectors where the bases allow it.
-  auto store32 = [&](__nv_bfloat16* dst, const uint32_t (&w)[16]) {
+  auto store32 = [&](__nv_bfloat16* dst, const uint32_t (&w)[16], unsigned gap) {
     if (v8) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) {
-        __nanosleep(C::kStoreGapNs);  // a burst of stores stalls the softmax warps
+        __nanosleep(gap);  // a burst of stores stalls the softmax warps
         st_global_v8(dst + 16 * q, w[8 * q], w[8 * q + 1], w[8 * q + 2], w[8 * q + 3], w[8 * q + 4],
                      w[8 * q + 5], w[8 * q + 6], w[8 * q + 7]);
       }
@@ -344,8 +412,8 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
         const uint32_t zero[16] = {};
 #pragma unroll
         for (int c = 0; c < HC / 32; ++c) {
-          store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, zero);
-          if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, zero);
+          store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, zero, 0);
+          if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, zero, 0);
         }
         *lse = -INFINITY;
       }
@@ -384,11 +452,12 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
         w2[c][i] = pack_bf16x2(o2[0], o2[1]);
       }
     }
+    const unsigned gap = is.nx1.w < 0 ? 0 : C::kStoreGapNs;  // none behind the last item
     if (live) {
 #pragma unroll
       for (int c = 0; c < HC / 32; ++c) {
-        store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, w[c]);
-        if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, w2[c]);
+        store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, w[c], gap);
+        if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, w2[c], gap);
       }
     }
     if (live) *lse = (ml.y > 0.f) ? (ml.x + log2f(ml.y)) * kLn2 : -INFINITY;
@@ -398,10 +467,10 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
 // ------------------------------------------------------------------- kernel
 
 template <int KB, int D, bool SPLIT>
-__global__ void __launch_bounds__(FwdCfg<128, KB, D>::kThreads, 1)
+__global__ void __launch_bounds__(DiffFwdCfg<KB, D>::kThreads, 1)
     bsa_diff_fwd_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                         const __grid_constant__ CUtensorMap tm_v, const DiffFwdParams p) {
-  using C = FwdCfg<128, KB, D>;
+  using C = DiffFwdCfg<KB, D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -425,6 +494,10 @@ __global__ void __launch_bounds__(FwdCfg<128, KB, D>::kThreads, 1)
     mbar_init(bar(C::kBarOFree), 4);
     mbar_init(bar(C::kBarStFull), 4 * C::kNumWG);
     mbar_init(bar(C::kBarStFree), 4);
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(bar(C::kBarQF + x), 1);
+      mbar_init(bar(C::kBarQE + x), 1);
+    }
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -447,15 +520,18 @@ __global__ void __launch_bounds__(FwdCfg<128, KB, D>::kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   const WaitCtl ctl{abort_flag, p.status, p.wait_limit_ns, p.expire_site};
+  wait_before();
 
   if (warp < C::kSoftWarp) {
     setmaxnreg_dec<C::kRegCtl>();
     if (warp == 0) {
-      if (lane == 0) diff_producer<KB, D, SPLIT>(p, &tm_q, &tm_k, &tm_v, sbase, ctl);
+      if (lane == 0) diff_producer<KB, D>(p, &tm_k, &tm_v, sbase, ctl);
     } else if (warp == 1) {
-      if (lane == 0) fwd_mma_s<128, KB, D>(p, sbase, tmem, ctl);
+      if (lane == 0) diff_mma_s<KB, D>(p, sbase, tmem, ctl);
     } else if (warp == 2) {
       if (lane == 0) fwd_mma_pv<128, KB, D>(p, sbase, tmem, ctl);
+    } else {
+      if (lane == 0) diff_query_producer<KB, D, SPLIT>(p, &tm_q, sbase, ctl);
     }
   } else if (warp < C::kEpiWarp) {
     setmaxnreg_inc<C::kRegSoft>();
@@ -477,7 +553,7 @@ __global__ void __launch_bounds__(FwdCfg<128, KB, D>::kThreads, 1)
 template <int KB, int D, bool SPLIT>
 cudaError_t launch_diff_fwd(const DiffFwdParams& p, const CUtensorMap& q, const CUtensorMap& k,
                             const CUtensorMap& v, int grid, cudaStream_t stream) {
-  using C = FwdCfg<128, KB, D>;
+  using C = DiffFwdCfg<KB, D>;
   static_assert(C::kEpi && C::kSplitRegs, "roles");
   auto* kernel = bsa_diff_fwd_kernel<KB, D, SPLIT>;
   static int done[64] = {0}, split_ok[64] = {0};
@@ -495,8 +571,7 @@ cudaError_t launch_diff_fwd(const DiffFwdParams& p, const CUtensorMap& q, const 
     if (fa.numRegs != C::kLaunchRegs) return cudaErrorInvalidConfiguration;
     if (dev >= 0 && dev < 64) split_ok[dev] = 1;
   }
-  kernel<<<grid, C::kThreads, C::kLaunchSmem, stream>>>(q, k, v, p);
-  return cudaGetLastError();
+  return launch_after(kernel, dim3(grid), C::kThreads, C::kLaunchSmem, stream, q, k, v, p);
 }
 
 }  // namespace bsa

@@ -178,6 +178,8 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   p.nb = lut->nb;
   p.nnz = lut->nnz_total;
   p.cols = lut->H * lut->nb;
+  p.steps = static_cast<int64_t>(B) * p.nnz * p.pairs * p.halves;
+  p.share = std::max<int64_t>((p.steps + sms - 1) / sms, bsa::kDiffShare);
   p.vec = r.vec;
   p.parts = reinterpret_cast<float*>(ws + parts.parts);
   p.dq = dq_out;

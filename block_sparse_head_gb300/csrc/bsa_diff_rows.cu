@@ -1,7 +1,5 @@
 // bsa_diff_rows.cu -- the small kernels of differential attention's backward: the row terms
 // before its walks, the joining of cut columns and the sum of the weight's gradient after them.
-#include <algorithm>
-
 #include <cuda_bf16.h>
 
 #include "bsa_internal.h"
@@ -16,6 +14,7 @@ template <int D>
 __global__ void __launch_bounds__(256) bsa_diff_rows_kernel(const DiffRowsParams p) {
   constexpr int R = D / 8;
   constexpr float kLog2e = 1.4426950408889634f;
+  wait_before();
   const int lane = threadIdx.x & 31;
   const int tiles = diff_vec_tiles((p.L + 63) / 64);
   const int64_t r = static_cast<int64_t>(blockIdx.x) * (256 / R) + threadIdx.x / R;
@@ -91,6 +90,7 @@ __device__ void sum_lam(const float* rows, float* dlam, int B, int H, int h, int
 // the weight's gradient of heads x, x + gridDim.x, .. (where it is one number a head).
 __global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams p, int grid, int shares,
                                                             float* dlam, int H) {
+  wait_before();
   if (static_cast<int>(blockIdx.y) == shares) {
     for (int h = blockIdx.x; h < H; h += gridDim.x) sum_lam(p.dlam, dlam, p.B, H, h, p.L);
     return;
@@ -109,29 +109,33 @@ __global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams 
   };
   const int row0 = blockIdx.y * rows;
   if (static_cast<int>(blockIdx.x) >= grid) {
-    const long long n = static_cast<long long>(p.B) * p.cols;
-    for (long long i = blockIdx.x - grid; i < n; i += gridDim.x - grid) {
-      const int b = static_cast<int>(i / p.cols), col = static_cast<int>(i - static_cast<long long>(b) * p.cols);
-      if (p.col_ptr[col] != p.col_ptr[col + 1]) continue;
-      for (int r = r0; r < rows; r += step) store(b, col, row0 + r, make_float4(0.f, 0.f, 0.f, 0.f));
+    // 256 columns a block, a thread each.
+    __shared__ int empty[256], n;
+    if (threadIdx.x == 0) n = 0;
+    __syncthreads();
+    const long long mine = (blockIdx.x - grid) * 256ll + threadIdx.x;
+    const int col = static_cast<int>(mine % p.cols);
+    if (mine < static_cast<long long>(p.B) * p.cols && p.col_ptr[col] == p.col_ptr[col + 1])
+      empty[atomicAdd(&n, 1)] = threadIdx.x;
+    __syncthreads();
+    for (int i = 0; i < n; ++i) {
+      const long long it = (blockIdx.x - grid) * 256ll + empty[i];
+      const int b = static_cast<int>(it / p.cols);
+      for (int r = r0; r < rows; r += step)
+        store(b, static_cast<int>(it - static_cast<long long>(b) * p.cols), row0 + r, make_float4(0.f, 0.f, 0.f, 0.f));
     }
     return;
   }
-  const long long total = diff_steps(p), share = diff_share(p, grid), start = blockIdx.x * share;
-  if (blockIdx.x == 0 || start >= total) return;
+  const long long start = blockIdx.x * p.share;
+  if (blockIdx.x == 0 || start >= p.steps) return;
   const int per = p.pairs * p.halves;
-  const long long entry = start / per;
-  const int b = static_cast<int>(entry / p.nnz);
+  const long long entry = diff_div(start, per);
+  const int b = static_cast<int>(diff_div(entry, p.nnz));
   const long long base = static_cast<long long>(b) * p.nnz;
   const int x = static_cast<int>(entry - base);
-  int lo = 0, hi = p.cols - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi) >> 1;
-    if (p.col_ptr[mid + 1] > x) hi = mid;
-    else lo = mid + 1;
-  }
+  const int lo = diff_column(p, x);
   const long long first = (base + p.col_ptr[lo]) * per, end = (base + p.col_ptr[lo + 1]) * per;
-  const int root = static_cast<int>(first / share), last = static_cast<int>((end - 1) / share);
+  const int root = static_cast<int>(diff_div(first, p.share)), last = static_cast<int>(diff_div(end - 1, p.share));
   if (first == start || root != static_cast<int>(blockIdx.x) - 1) return;
   const int64_t slot = static_cast<int64_t>(p.block) * 2 * d;
   for (int r = r0; r < rows; r += step) {
@@ -152,10 +156,10 @@ __global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams 
 }  // namespace
 
 cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, float* dlam, int H, cudaStream_t stream) {
-  const int more = static_cast<int>(std::min<long long>(64, static_cast<long long>(p.B) * p.cols));
-  constexpr int kShares = 8;
-  bsa_diff_join_kernel<<<dim3(grid + more, kShares + (dlam != nullptr)), 256, 0, stream>>>(p, grid, kShares, dlam, H);
-  return cudaGetLastError();
+  const int more = static_cast<int>((static_cast<long long>(p.B) * p.cols + 255) / 256);
+  const int shares = p.block * p.d / 512;  // a thread has one row
+  return launch_after(bsa_diff_join_kernel, dim3(grid + more, shares + (dlam != nullptr)), 256, 0, stream, p, grid,
+                      shares, dlam, H);
 }
 
 cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream) {
@@ -163,11 +167,8 @@ cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream) {
   const int per = 256 / (p.d / 8);
   const int64_t grid = (rows + per - 1) / per;
   if (grid > 0x7FFFFFFF) return cudaErrorInvalidValue;
-  if (p.d == 128)
-    bsa_diff_rows_kernel<128><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
-  else
-    bsa_diff_rows_kernel<64><<<static_cast<unsigned>(grid), 256, 0, stream>>>(p);
-  return cudaGetLastError();
+  auto* kernel = p.d == 128 ? bsa_diff_rows_kernel<128> : bsa_diff_rows_kernel<64>;
+  return launch_after(kernel, dim3(static_cast<unsigned>(grid)), 256, 0, stream, p);
 }
 
 }  // namespace bsa

@@ -166,7 +166,8 @@ __device__ __forceinline__ int step_blocks(int nnz, int s) {
   return rem < G ? rem : G;
 }
 
-// This CTA's share [x, y) of a work list, and its item u.
+// This CTA's share [x, y) of a work list, its item u as the list has it, and what becomes of that
+// when it is the current one (the load that stream_item begins is not waited for before).
 template <class P>
 __device__ __forceinline__ int2 stream_range(const P& p) {
   return make_int2(p.cta_start[blockIdx.x], p.cta_start[blockIdx.x + 1]);
@@ -174,6 +175,10 @@ __device__ __forceinline__ int2 stream_range(const P& p) {
 template <class P>
 __device__ __forceinline__ int4 stream_item(const P& p, int u) {
   return p.items[u];
+}
+template <class P>
+__device__ __forceinline__ int4 stream_place(const P&, int, const int4& item) {
+  return item;
 }
 
 // The CTA's share of the work list: items[cta_start[c] .. cta_start[c+1]) for CTA c, as
@@ -191,7 +196,7 @@ struct ItemStream {
   int4 nx2;
 
   // P: any kernel-argument struct with `items` and `cta_start` (forward or backward), or one
-  // with overloads of stream_range and stream_item of its own.
+  // with overloads of stream_range, stream_item and stream_place of its own.
   template <class P>
   __device__ __forceinline__ int4 fetch(const P& p, int u) const {
     return u < end ? stream_item(p, u) : make_int4(0, 0, 0, -1);
@@ -201,7 +206,7 @@ struct ItemStream {
   __device__ __forceinline__ void next(const P& p) {
     for (;;) {
       ++t;
-      cur = nx1;
+      cur = stream_place(p, t, nx1);
       nx1 = nx2;
       nx2 = fetch(p, t + 2);
       if (cur.w > 0) ++n;
@@ -366,8 +371,8 @@ struct MmaDescs {
 };
 
 // S(t) = Q K(t)^T into S[t % 3].
-template <int QB, int KB, int D, class P>
-__device__ __forceinline__ void fwd_mma_s(const P& p, uint32_t sbase, uint32_t tmem,
+template <int QB, int KB, int D>
+__device__ __forceinline__ void fwd_mma_s(const FwdParams& p, uint32_t sbase, uint32_t tmem,
                                           const WaitCtl& ctl) {
   using C = FwdCfg<QB, KB, D>;
   constexpr int G = C::kG;

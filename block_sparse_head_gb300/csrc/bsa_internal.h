@@ -213,6 +213,7 @@ struct DiffBwdParams : DiffList {
   const int32_t* row_idx;    // the place of the diagonal block among them
   const int32_t* diag_pos;
   int B, nb, nnz;            // nnz: active blocks of all kv heads
+  long long steps, share;    // of the dK/dV walk, and of one of its CTAs
   int cols;                  // kv heads * nb
   const float* vec;          // row terms
   void* dq;                  // dQ walk: bf16 [B,2H,L,dq]
@@ -230,14 +231,51 @@ struct DiffBwdParams : DiffList {
 // head, half) with the last fastest, and CTA c takes the c-th piece of equal length: whole
 // columns and at most two cut ones.  A cut column's pieces go to slots: 2 c the piece that begins
 // CTA c's share (a column begun earlier), 2 c + 1 the one that ends it.
-constexpr int kDiffShare = 4;  // steps of a share at least
-__host__ __device__ inline long long diff_steps(const DiffBwdParams& p) {
-  return static_cast<long long>(p.B) * p.nnz * p.pairs * p.halves;
+constexpr int kDiffShare = 2;  // steps of a share at least
+#ifdef __CUDACC__
+// a / b for a >= 0, b > 0, in 32 bits where they suffice (a 64-bit division takes several times
+// as long, and these stand in the way of the first load).
+__device__ __forceinline__ long long diff_div(long long a, long long b) {
+  return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
 }
-__host__ __device__ inline long long diff_share(const DiffBwdParams& p, int grid) {
-  const long long n = (diff_steps(p) + grid - 1) / grid;
-  return n < kDiffShare ? kDiffShare : n;
+// The column with col_ptr[col] <= x < col_ptr[col + 1].  Seven places are looked at at once: the
+// loads of one round wait for one trip to memory together.
+__device__ __forceinline__ int diff_column(const DiffBwdParams& p, int x) {
+  int lo = 0, n = p.cols;  // in [lo, lo + n)
+  while (n > 1) {
+    const int step = (n + 7) >> 3;
+    int c = 0;
+#pragma unroll
+    for (int i = 1; i < 8; ++i)
+      if (i * step < n && p.col_ptr[lo + i * step] <= x) c = i;
+    lo += c * step;
+    n = min(step, n - c * step);
+  }
+  return lo;
 }
+
+// Waits until the kernels before this one in the stream have finished and their writes are seen
+// (launch_after); every thread that reads what they wrote, before it does.
+__device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Launches a kernel that calls wait_before in every thread, so that its launch overlaps the end of
+// the kernel before it (a backward of 2,999 tokens in four kernels: 90 -> 81 us).  None of them lets
+// the next one begin early (griddepcontrol.launch_dependents): with an SM's whole shared memory each
+// they could only take turns, and long ones lost 3 %.
+template <class... P, class... A>
+cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A&&... args) {
+  cudaLaunchAttribute attr{};
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
+}
+#endif
 // Joins the pieces of cut columns (in order) and writes the zeros of columns without a block; sums
 // the rows of dlam to one number a head where dlam is not null.
 cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, float* dlam, int H, cudaStream_t stream);
