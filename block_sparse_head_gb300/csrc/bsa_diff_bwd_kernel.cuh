@@ -72,14 +72,15 @@ struct DiffBwdCfg {
   static constexpr int kXBlkB = kXBlk * D * 2;
   static constexpr int kYTile = (KV ? 64 : 128) * D * 2;
   static constexpr int kYPlane = (KV ? 64 : BLK) * 128;
-  static constexpr int kNX = KV ? 2 : 3;
+  static constexpr int kNX = 3;             // X slots (dK/dV: stages of X, Y and the row terms)
+  static constexpr int kNY = KV ? 3 : 2;
   static constexpr int kOffA = 0;
   static constexpr int kOffB = kItemTile;
   static constexpr int kOffX = 2 * kItemTile;
   static constexpr int kOffY = kOffX + kNX * kXTile;
   static constexpr int kVecB = kDiffVec * 4;
-  static constexpr int kOffVec = kOffY + 2 * kYTile;
-  static constexpr int kOffBar = kOffVec + (KV ? 2 * kVecB : 0);
+  static constexpr int kOffVec = kOffY + kNY * kYTile;
+  static constexpr int kOffBar = kOffVec + (KV ? kNX * kVecB : 0);
   // barriers: as in the plain backward
   static constexpr int kBarIF = 0, kBarIE = 1, kBarXF = 2, kBarXE = 5, kBarYF = 8, kBarYE = 10;
   static constexpr int kBarTF = 12, kBarEF = 13, kBarAD = 14, kBarAR = 16, kBarDrain = 17;
@@ -255,14 +256,14 @@ __device__ __forceinline__ void diff_kv_producer(const DiffBwdParams& p, const C
       tma_load_4d(sbase + C::kOffA, tm_k, fb, 0, key0, 0, head);
     }
     c.advance(p);
-    // Stage t % 2 held step t-2, read by its dV and dK products.
-    if (t >= 2 && !mbar_wait(bar(C::kBarXE + t % 2), ((t - 2) / 2) & 1, ctl, kSiteProdVEmpty)) break;
-    const uint32_t fb = bar(C::kBarXF + t % 2);
+    // Stage t % 3 held step t-3, read by its dV and dK products.
+    if (t >= 3 && !mbar_wait(bar(C::kBarXE + t % 3), ((t - 3) / 3) & 1, ctl, kSiteProdVEmpty)) break;
+    const uint32_t fb = bar(C::kBarXF + t % 3);
     mbar_arrive_expect_tx(fb, (SPLIT ? C::kXTile / 2 : C::kXTile) + C::kYTile + C::kVecB);
-    diff_load_q<D, SPLIT>(sbase + C::kOffX + (t % 2) * C::kXTile, tm_q, fb, q64 * 64, pair);
-    tma_load_4d(sbase + C::kOffY + (t % 2) * C::kYTile, tm_do, fb, 0, q64 * 64, 0, pair);
+    diff_load_q<D, SPLIT>(sbase + C::kOffX + (t % 3) * C::kXTile, tm_q, fb, q64 * 64, pair);
+    tma_load_4d(sbase + C::kOffY + (t % 3) * C::kYTile, tm_do, fb, 0, q64 * 64, 0, pair);
     // A block's second half may lie past the sequence; the row terms have room for it.
-    bulk_load(sbase + C::kOffVec + (t % 2) * C::kVecB,
+    bulk_load(sbase + C::kOffVec + (t % 3) * C::kVecB,
               p.vec + (static_cast<int64_t>(pair) * diff_vec_tiles(tiles) + q64) * kDiffVec, C::kVecB, fb);
     if (item_first) {
       // B (V) after the step's tiles: the previous item's last T2 completes later.
@@ -276,7 +277,7 @@ __device__ __forceinline__ void diff_kv_producer(const DiffBwdParams& p, const C
       ++nv;
     }
   }
-  for (int j = (t > 2 ? t - 2 : 0); j < t; ++j) mbar_drain_wait(bar(C::kBarXF + j % 2), (j / 2) & 1);
+  for (int j = (t > 3 ? t - 3 : 0); j < t; ++j) mbar_drain_wait(bar(C::kBarXF + j % 3), (j / 3) & 1);
   if (n >= 0) mbar_drain_wait(bar(C::kBarIF), n & 1);
   if (nv > 0) mbar_drain_wait(bar(C::kBarIFV), (nv - 1) & 1);
 }
@@ -367,6 +368,7 @@ __device__ __forceinline__ void diff_dq_mma2(const DiffBwdParams& p, uint32_t sb
     c.advance(p);
     if (first) ++n;
     if (!mbar_wait(bar(C::kBarEF), u & 1, ctl, kSiteMmaPFull)) break;
+    mbar_arrive(bar(C::kBarQI));
     if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
     tc_fence_after();
     const uint32_t te = tmem + ((u & 1) ? C::kT1b : C::kT1), xs = x0 + (u % 3) * (C::kXTile >> 4);
@@ -382,17 +384,15 @@ __device__ __forceinline__ void diff_dq_mma2(const DiffBwdParams& p, uint32_t sb
     }
     tc_commit(bar(C::kBarAD + (u & 1)));
     tc_commit(bar(C::kBarXE + u % 3));
-    mbar_arrive(bar(C::kBarQI));
   }
   tc_commit(bar(C::kBarDrain2));
   mbar_drain_wait(bar(C::kBarDrain2), 0);
 }
 
-// dK/dV walk: T1 and T2.  T1(t) is the region at 0 on even steps and at 128 on odd ones, T2(t)
-// the other's first columns.  Per step: T2(t) over T1(t-1) once the products of t-1 have read
-// E1 and E2 there; T1(t+1) over T2(t) once every elementwise warp has loaded it and the dV
-// product of t has been issued (so that E1 of t+1 cannot complete before the other thread has
-// waited for E1 of t).
+// dK/dV walk: T1 and T2.  Steps alternate between two regions of 128 columns.  T1(t) fills one;
+// once every elementwise warp has loaded it, T2(t) goes into its second half; E1(t) and then E2(t)
+// (over T2(t)) are written there as well.  So T1(t+1) needs the products of t-1 only, and runs
+// while the warps are at step t.  Per step, here: T2(t), then T1(t+1).
 template <int BLK, int D>
 __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sbase, uint32_t tmem,
                                             const WaitCtl& ctl) {
@@ -406,7 +406,7 @@ __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sba
   const uint32_t y0 = static_cast<uint32_t>(sdesc_sw128(sbase + C::kOffY, 16, 1024));
   auto issue1 = [&](int t) {
     diff_issue_first<D, C::kItemPlane, C::kXPlane, 0, 128>(tmem + ((t & 1) ? C::kT2 : C::kT1), a0,
-                                                           x0 + (t % 2) * (C::kXTile >> 4), hi,
+                                                           x0 + (t % 3) * (C::kXTile >> 4), hi,
                                                            C::kIdescT1, 1);
   };
   DiffKvWalk c;
@@ -424,22 +424,23 @@ __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sba
       if (last) tc_commit(bar(C::kBarIE));
     }
     for (int t = 0; ok; ++t) {
-      if (t > 0 && !mbar_wait(bar(C::kBarAD), (t - 1) & 1, ctl, kSiteMmaPvDone)) break;
       if (first && !mbar_wait(bar(C::kBarIFV), n & 1, ctl, kSiteMmaStage)) break;
+      if (!mbar_wait(bar(C::kBarDL), t & 1, ctl, kSiteMmaPFull)) break;
       tc_fence_after();
       diff_issue_first<D, C::kItemPlane, C::kYPlane, 0, 64>(
-          tmem + ((t & 1) ? C::kT1 : C::kT2), b0, y0 + (t % 2) * (C::kYTile >> 4), hi, C::kIdescT2,
-          1);  // dP^T = V dO^T
+          tmem + ((t & 1) ? C::kT2 : C::kT1) + 64, b0, y0 + (t % 3) * (C::kYTile >> 4), hi,
+          C::kIdescT2, 1);  // dP^T = V dO^T
       tc_commit(bar(C::kBarDF));
       if (last) tc_commit(bar(C::kBarIEV));
       if (!c.valid()) break;
       first = c.first;
       last = c.last();
       c.advance(p);
-      if (!mbar_wait(bar(C::kBarDL), t & 1, ctl, kSiteMmaPFull)) break;
-      if (!mbar_wait(bar(C::kBarVI), t & 1, ctl, kSiteMmaPFull)) break;
       if (first && !mbar_wait(bar(C::kBarIF), (n + 1) & 1, ctl, kSiteMmaStage)) break;
-      if (!mbar_wait(bar(C::kBarXF + (t + 1) % 2), ((t + 1) / 2) & 1, ctl, kSiteMmaStage)) break;
+      if (!mbar_wait(bar(C::kBarXF + (t + 1) % 3), ((t + 1) / 3) & 1, ctl, kSiteMmaStage)) break;
+      // Two barriers, by region: the next phase of this one is step t+1's own.
+      if (t >= 1 && !mbar_wait(bar(C::kBarAD + ((t + 1) & 1)), ((t - 1) / 2) & 1, ctl, kSiteMmaPvDone))
+        break;
       tc_fence_after();
       issue1(t + 1);
       tc_commit(bar(C::kBarTF));
@@ -474,18 +475,18 @@ __device__ __forceinline__ void diff_kv_mma2(const DiffBwdParams& p, uint32_t sb
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
-      tc_mma_ts_lh(tmem + C::kAcc1, t1 + kk * 8, y0 + (t % 2) * (C::kYTile >> 4) + ((kk * 16 * 128) >> 4),
+      tc_mma_ts_lh(tmem + C::kAcc1, t1 + kk * 8, y0 + (t % 3) * (C::kYTile >> 4) + ((kk * 16 * 128) >> 4),
                    hi, C::kIdescAcc, (first && kk == 0) ? 0u : 1u);
-    mbar_arrive(bar(C::kBarVI));
     if (!mbar_wait(bar(C::kBarEF), t & 1, ctl, kSiteMmaPFull)) break;
+    mbar_arrive(bar(C::kBarVI));
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
       tc_mma_ts_lh(tmem + C::kAcc2, t1 + 64 + kk * 8,
-                   x0 + (t % 2) * (C::kXTile >> 4) + ((kk * 16 * 128) >> 4), hi, C::kIdescAcc,
+                   x0 + (t % 3) * (C::kXTile >> 4) + ((kk * 16 * 128) >> 4), hi, C::kIdescAcc,
                    (first && kk == 0) ? 0u : 1u);
-    tc_commit(bar(C::kBarAD));
-    tc_commit(bar(C::kBarXE + t % 2));
+    tc_commit(bar(C::kBarAD + (t & 1)));
+    tc_commit(bar(C::kBarXE + t % 3));
   }
   tc_commit(bar(C::kBarDrain2));
   mbar_drain_wait(bar(C::kBarDrain2), 0);
@@ -622,7 +623,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
       tmem_st_16x32bx2_x32<32>(t1, pk1);
       tmem_st_wait();
-      // The previous step's dQ product issued (its issuer cannot fall two phases behind).
+      // The issuer of the dQ products has seen the previous step's E: it cannot fall two phases behind.
       if (g >= 1 && !wait_bar(C::kBarQI, (g - 1) & 1, kSiteSoftSFull)) {
         ok = false;
         break;
@@ -675,11 +676,10 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
   int dpos = -1;
   for (int g = 0; c.valid(); ++g) {
     const uint32_t t1 = tl + ((g & 1) ? C::kT2 : C::kT1);
-    const uint32_t t2 = tl + ((g & 1) ? C::kT1 : C::kT2);
     if (c.first && p.causal_diag) dpos = p.diag_pos[c.col];
     // Of this half's 32 queries those before the key are masked in the diagonal block.
     const int lo = (c.x - c.begin == dpos) ? row - 64 * (c.rest % C::kHalves) - 32 * half : -(1 << 30);
-    const float4* vec = reinterpret_cast<const float4*>(smem + C::kOffVec + (g % 2) * C::kVecB +
+    const float4* vec = reinterpret_cast<const float4*>(smem + C::kOffVec + (g % 3) * C::kVecB +
                                                         half * (kDiffVecHalf * 4));
     if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) break;
     uint32_t rs[2][32];  // S^T, then P^T, of each map
@@ -687,6 +687,7 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     tmem_ld_16x32bx2_x32<64>(t1 + 32, rs[1]);
     tmem_ld_wait(rs[0]);
     tmem_ld_wait(rs[1]);
+    warp_arrive(C::kBarDL);  // T2 may go over the second half
     // E1 = P_0^T - lam P_1^T, handed over on its own so that dV's product runs while dS^T is
     // formed.  The second map's P is kept with its weight -lam.
     {
@@ -720,12 +721,14 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
       tmem_st_16x32bx2_x16<16>(t1, pk);
     }
     tmem_st_wait();
+    // The issuer that waits for E1 and E2 in turn has seen E2 of the step before: it cannot fall two
+    // phases behind.
+    if (g >= 1 && !wait_bar(C::kBarVI, (g - 1) & 1, kSiteSoftSFull)) break;
     warp_arrive(C::kBarEF1);
     if (!wait_bar(C::kBarDF, g & 1, kSiteSoftSFull)) break;
     uint32_t rp[32];  // dP^T
-    tmem_ld_16x32bx2_x32<32>(t2, rp);
+    tmem_ld_16x32bx2_x32<32>(t1 + 64, rp);
     tmem_ld_wait(rp);
-    warp_arrive(C::kBarDL);  // T2 may now take the next step's S^T
     {
       uint32_t pk[32];
 #pragma unroll
@@ -745,7 +748,7 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     const bool whole = c.head && c.tail();
     if (c.last()) {
       // The piece is complete once its last step's products are.
-      if (!wait_bar(C::kBarAD, g & 1, kSiteSoftItemDone)) break;
+      if (!wait_bar(C::kBarAD + (g & 1), (g / 2) & 1, kSiteSoftItemDone)) break;
       const int kv = c.col / p.nb, key = (c.col - kv * p.nb) * BLK + row;
       if (whole) {
         uint32_t pk[D / 4], pk2[D / 4];

@@ -138,26 +138,39 @@ __global__ void __launch_bounds__(256) bsa_diff_join_kernel(const DiffBwdParams 
   const int root = static_cast<int>(diff_div(first, p.share)), last = static_cast<int>(diff_div(end - 1, p.share));
   if (first == start || root != static_cast<int>(blockIdx.x) - 1) return;
   const int64_t slot = static_cast<int64_t>(p.block) * 2 * d;
-  for (int r = r0; r < rows; r += step) {
-    const float* src = p.parts + (row0 + r) * (2 * d) + at;
-    float4 sum = *reinterpret_cast<const float4*>(src + (2 * static_cast<int64_t>(root) + 1) * slot);
-#pragma unroll 4
-    for (int i = root + 1; i <= last; ++i) {
-      const float4 y = *reinterpret_cast<const float4*>(src + 2 * static_cast<int64_t>(i) * slot);
-      sum.x += y.x;
-      sum.y += y.y;
-      sum.z += y.z;
-      sum.w += y.w;
-    }
-    store(b, lo, row0 + r, sum);
+  // Two rows a thread, four pieces at once: their loads wait together.
+  const float* src = p.parts + (row0 + r0) * (2 * d) + at;
+  float4 sum[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+    sum[u] = *reinterpret_cast<const float4*>(src + u * step * 2 * d + (2 * static_cast<int64_t>(root) + 1) * slot);
+  for (int i = root + 1; i <= last; i += 4) {
+    float4 y[4][2];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+        y[j][u] = i + j <= last ? *reinterpret_cast<const float4*>(src + u * step * 2 * d + 2 * static_cast<int64_t>(i + j) * slot)
+                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        sum[u].x += y[j][u].x;
+        sum[u].y += y[j][u].y;
+        sum[u].z += y[j][u].z;
+        sum[u].w += y[j][u].w;
+      }
   }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) store(b, lo, row0 + r0 + u * step, sum[u]);
 }
 
 }  // namespace
 
 cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, float* dlam, int H, cudaStream_t stream) {
   const int more = static_cast<int>((static_cast<long long>(p.B) * p.cols + 255) / 256);
-  const int shares = p.block * p.d / 512;  // a thread has one row
+  const int shares = p.block * p.d / 1024;  // a thread has two rows
   return launch_after(bsa_diff_join_kernel, dim3(grid + more, shares + (dlam != nullptr)), 256, 0, stream, p, grid,
                       shares, dlam, H);
 }
