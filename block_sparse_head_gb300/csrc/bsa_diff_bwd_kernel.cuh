@@ -6,8 +6,8 @@
 //     dV = (P_0 - lam P_1)^T dO,   dlam = -D_1.
 // K, V and their gradients are shared by both maps and by the heads of a kv head.
 //
-// The row terms and the sums at the end are bsa_diff_rows.cu's; the two walks here are dQ over the
-// layout's rows and dK and dV over its columns.
+// The row terms are bsa_diff_rows.cu's; the two walks here are dQ over the layout's rows and dK and
+// dV over its columns.
 // Both are the plain backward's pipelines (bsa_bwd_kernel.cuh: roles, barriers, TMEM regions) on tiles of 64 queries with both maps as 128 rows, row 64 a + 32 m + r being query
 // 32 a + r under map m:
 //   dQ walk    item: such a tile, A = its Q, B = its dO (each row twice).  Step: 128 keys,
@@ -22,8 +22,8 @@
 //              E2 = dS^T 128.  acc1 += E1 Y = dV,  acc2 += E2 X = dK / scale: the sum over maps
 //              and heads stays in TMEM.  A column's steps are its entries times heads times
 //              halves, and columns differ widely (a global one is seen by every row), so that
-//              the CTAs share the steps, not the columns out: a share's cut columns
-//              leave fp32 pieces that bsa_diff_rows.cu joins in order.
+//              the CTAs share the steps, not the columns out: of a column that
+//              is cut, each CTA but the last one there leaves an fp32 piece, which that one joins.
 // Queries of d / 2 numbers are laid out over d columns, zero in the other map's half
 // (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
 // Rows past the end of the sequence read as zero and carry -lse = -inf, so that their P is 0;
@@ -492,6 +492,28 @@ __device__ __forceinline__ void diff_kv_mma2(const DiffBwdParams& p, uint32_t sb
   mbar_drain_wait(bar(C::kBarDrain2), 0);
 }
 
+// dlam[h], by the second issuing warp of CTA h, h + grid, .. before its first product is due: the
+// sums of 16 rows that the dQ walk left, added in fp64 and a fixed order.
+__device__ __forceinline__ void diff_sum_lam(const DiffBwdParams& p, int lane) {
+  const int per = 4 * diff_vec_tiles((p.L + 63) / 64), live = 4 * ((p.L + 63) / 64);
+  for (int h = blockIdx.x; h < p.H; h += gridDim.x) {
+    double s = 0.0;
+    for (int b = 0; b < p.B; ++b) {
+      const float* x = p.lam_sums + (static_cast<int64_t>(b) * p.H + h) * per;
+      for (int i = lane; i < live; i += 8 * 32) {
+        float y[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) y[u] = i + 32 * u < live ? x[i + 32 * u] : 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u) s += static_cast<double>(y[u]);
+      }
+    }
+#pragma unroll
+    for (int w = 16; w >= 1; w /= 2) s += __shfl_xor_sync(0xffffffffu, s, w);
+    if (lane == 0) p.dlam[h] = static_cast<float>(s);
+  }
+}
+
 // ----------------------------------------------------------- elementwise warps
 
 template <int BLK, int D, bool SPLIT>
@@ -536,6 +558,20 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
                        pk[16 * c + 4 * i + 3]);
     }
   };
+  // dlam of the second map's rows: one number each, or (one weight a head) sums of 16 rows, which
+  // the dK/dV walk's kernel adds up.
+  auto store_lam = [&](int64_t pair, int tile, float x) {
+    if (map == 0) return;
+    if (p.lam_rows) {
+      const int q = tile * 64 + qin;
+      if (half == 0 && q < p.L) p.dlam[pair * p.L + q] = x;
+      return;
+    }
+    if (tile * 64 + qin >= p.L) x = 0.f;
+#pragma unroll
+    for (int k = 1; k < 16; k *= 2) x += __shfl_xor_sync(0xffffffffu, x, k);
+    if (lane == 0) p.lam_sums[(pair * tiles + tile) * 4 + (qin >> 4)] = x;
+  };
   // The previous item's accumulator goes out at the next item's first step, once that step's E
   // is handed over.
   bool pending = false;
@@ -561,7 +597,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     if (cnt == 0) {
       const uint32_t zero[D / 4] = {};
       store_dq(pair, q, zero);
-      if (map == 1 && half == 0 && q < p.L) p.dlam[pair * p.L + q] = 0.f;
+      store_lam(pair, is.cur.y, 0.f);
       continue;
     }
     const float* v = p.vec + (pair * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + (qin & 31);
@@ -636,7 +672,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     }
     if (!ok) break;
     rsum += __shfl_xor_sync(0xffffffffu, rsum, 16);
-    if (map == 1 && half == 0 && q < p.L) p.dlam[pair * p.L + q] = -rsum;
+    store_lam(pair, is.cur.y, -rsum);
     pending = true;
     ppair = pair;
     pq = q;
@@ -761,19 +797,87 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
           store_row_bf16<D>(static_cast<__nv_bfloat16*>(p.dk) + orow * D, 0, half, pk2);
         }
       } else {
-        // dV and dK as they are: this thread's 32-column groups, one after another.
-        float* slot = p.parts + (2 * static_cast<int64_t>(blockIdx.x) + (c.head ? 1 : 0)) * (BLK * 2 * D) +
-                      row * (2 * D) + half * 32;
+        // A cut column.  Its pieces lie in the CTAs root .. end; this warp's rows of them meet on
+        // their own.  Who finds all others' pieces there adds them to what it holds; else it leaves
+        // its own, and joins them if another has been as late.  The sum goes in the CTAs' order in
+        // any case.
+        const long long base = static_cast<long long>(c.b) * p.nnz;
+        const int root = static_cast<int>(diff_div((base + c.begin) * c.per, p.share));
+        const int end = static_cast<int>(diff_div((base + c.end) * c.per - 1, p.share));
+        const int me = blockIdx.x;
+        int* count = p.count + root * C::kEwWarps + ((threadIdx.x >> 5) - 2);
+        // A piece is laid out as its readers, the same warps elsewhere, take it: lanes side by side.
+        auto piece = [&](int i, int g) {
+          const int64_t slot = i == root ? 2 * static_cast<int64_t>(root) + 1 : 2 * static_cast<int64_t>(i);
+          return reinterpret_cast<float4*>(p.parts) + slot * (BLK * 2 * D / 4) +
+                 (((threadIdx.x >> 5) - 2) * (D / 32) + g) * (8 * 32) + lane;
+        };
+        const int64_t orow = static_cast<int64_t>(c.b * (p.cols / p.nb) + kv) * p.L + key;
+        // Columns 64 g + 32 half .. of dV | dK: the pieces' sum (own: this CTA's) to bf16.
+        auto sum_pieces = [&](int g, const uint32_t* own) {
+          float4 x[8];
+#pragma unroll
+          for (int u = 0; u < 8; ++u) x[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+          for (int i = root; i <= end; ++i) {
+            float4 y[8];
+            if (own != nullptr && i == me) {
+#pragma unroll
+              for (int u = 0; u < 8; ++u)
+                y[u] = make_float4(__uint_as_float(own[4 * u]), __uint_as_float(own[4 * u + 1]),
+                                   __uint_as_float(own[4 * u + 2]), __uint_as_float(own[4 * u + 3]));
+            } else {
+              const float4* from = piece(i, g);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) y[u] = __ldcg(from + 32 * u);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+              x[u].x += y[u].x;
+              x[u].y += y[u].y;
+              x[u].z += y[u].z;
+              x[u].w += y[u].w;
+            }
+          }
+          if (key >= p.L) return;
+          const bool is_k = g >= D / 64;
+          const float f = is_k ? p.scale : 1.f;
+          __nv_bfloat16* out = static_cast<__nv_bfloat16*>(is_k ? p.dk : p.dv) + orow * D +
+                               (is_k ? g - D / 64 : g) * 64 + half * 32;
+#pragma unroll
+          for (int u = 0; u < 4; ++u)
+            reinterpret_cast<uint4*>(out)[u] =
+                make_uint4(pack_bf16x2(x[2 * u].x * f, x[2 * u].y * f), pack_bf16x2(x[2 * u].z * f, x[2 * u].w * f),
+                           pack_bf16x2(x[2 * u + 1].x * f, x[2 * u + 1].y * f),
+                           pack_bf16x2(x[2 * u + 1].z * f, x[2 * u + 1].w * f));
+        };
+        int there = 0;
+        if (lane == 0) there = load_acquire(count);
+        const bool late = __shfl_sync(0xffffffffu, there, 0) == end - root;
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t r[32];
           load_o32(tl + C::kAcc1, i, r);
           tmem_ld_wait(r);
           if (i == D / 32 - 1) warp_arrive(C::kBarAR);
+          if (late) {
+            sum_pieces(i, r);
+          } else {
+            float4* to = piece(me, i);
 #pragma unroll
-          for (int u = 0; u < 8; ++u)
-            *reinterpret_cast<uint4*>(slot + 64 * i + 4 * u) =
-                make_uint4(r[4 * u], r[4 * u + 1], r[4 * u + 2], r[4 * u + 3]);
+            for (int u = 0; u < 8; ++u)
+              to[32 * u] = make_float4(__uint_as_float(r[4 * u]), __uint_as_float(r[4 * u + 1]),
+                                       __uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3]));
+          }
+        }
+        if (!late) {
+          __threadfence();
+          __syncwarp();
+          if (lane == 0) there = add_acq_rel(count, 1);
+          if (__shfl_sync(0xffffffffu, there, 0) == end - root) {
+            __threadfence();
+#pragma unroll 1
+            for (int i = 0; i < D / 32; ++i) sum_pieces(i, nullptr);
+          }
         }
       }
     }
@@ -841,6 +945,8 @@ __global__ void __launch_bounds__(DiffBwdCfg<BLK, D, KV>::kThreads, 1)
       else diff_dq_mma<BLK, D>(p, sbase, tmem, ctl);
     }
   } else if (warp == C::kMma2Warp) {
+    if constexpr (KV)
+      if (!p.lam_rows) diff_sum_lam(p, lane);
     if (lane == 0) {
       if constexpr (KV) diff_kv_mma2<BLK, D>(p, sbase, tmem, ctl);
       else diff_dq_mma2<BLK, D>(p, sbase, tmem, ctl);

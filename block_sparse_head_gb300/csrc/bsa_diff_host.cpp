@@ -53,13 +53,17 @@ auto pick(int block, int d, F64_64 a, F64_128 b, F128_64 c, F128_128 e) {
   return block == 64 ? (d == 64 ? a : b) : (d == 64 ? c : e);
 }
 
-// The workspace: row terms, the pieces of cut columns (two a CTA), rows of dlam.
+// The workspace: row terms, the pieces of cut columns (two a CTA), sums of dlam, counts.
+constexpr int kCounts = 8;  // of a CTA: one a warp
+
 struct Parts {
-  int64_t parts, rows, bytes;  // offsets
+  int64_t parts, sums, count, bytes;  // offsets
   Parts(int B, int H, int L, int d, int block, int sms) {
-    parts = static_cast<int64_t>(B) * H * bsa::diff_vec_tiles((L + 63) / 64) * bsa::kDiffVecFloats * 4;
-    rows = parts + static_cast<int64_t>(sms) * 2 * block * 2 * d * 4;
-    bytes = rows + static_cast<int64_t>(B) * H * L * 4;
+    const int64_t tiles = static_cast<int64_t>(B) * H * bsa::diff_vec_tiles((L + 63) / 64);
+    parts = tiles * bsa::kDiffVecFloats * 4;
+    sums = parts + static_cast<int64_t>(sms) * 2 * block * 2 * d * 4;
+    count = sums + tiles * 16;
+    bytes = count + static_cast<int64_t>(sms) * kCounts * 4;
   }
 };
 
@@ -165,9 +169,7 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   r.L = L;
   r.d = d;
   r.lam_rows = lam_rows != 0;
-  if (bsa::launch_diff_rows(r, st) != cudaSuccess) return BSA_ERR_CUDA;
   char* ws = static_cast<char*>(workspace);
-  float* rows = lam_rows ? dlam : reinterpret_cast<float*>(ws + parts.rows);
   bsa::DiffBwdParams p{};
   fill_list(p, lut, H / kv_heads, block);
   p.col_idx = lut->d_col_idx;
@@ -182,8 +184,12 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   p.share = std::max<int64_t>((p.steps + sms - 1) / sms, bsa::kDiffShare);
   p.vec = r.vec;
   p.parts = reinterpret_cast<float*>(ws + parts.parts);
+  p.count = reinterpret_cast<int*>(ws + parts.count);
   p.dq = dq_out;
-  p.dlam = rows;
+  p.dlam = dlam;
+  p.lam_sums = reinterpret_cast<float*>(ws + parts.sums);
+  p.lam_rows = lam_rows != 0;
+  p.H = H;
   p.dk = dk;
   p.dv = dv;
   p.status = lut->d_status;
@@ -197,10 +203,9 @@ int bsa_diff_backward(const void* q, const void* k, const void* v, const float* 
   p.expire_site = lut->expire_site;
   auto* launch = pick(block, d, bsa::launch_diff_bwd_b64_d64, bsa::launch_diff_bwd_b64_d128,
                       bsa::launch_diff_bwd_b128_d64, bsa::launch_diff_bwd_b128_d128);
-  if (launch(dq != d, false, p, tq, tdo32, tk, tv, std::min(p.n, sms), st) != cudaSuccess)
-    return BSA_ERR_CUDA;
-  if (launch(dq != d, true, p, tk, tv, tq, tdo64, sms, st) != cudaSuccess ||
-      bsa::launch_diff_join(p, sms, lam_rows ? nullptr : dlam, H, st) != cudaSuccess)
+  if (bsa::launch_diff_rows(r, p, sms * kCounts, st) != cudaSuccess ||
+      launch(dq != d, false, p, tq, tdo32, tk, tv, std::min(p.n, sms), st) != cudaSuccess ||
+      launch(dq != d, true, p, tk, tv, tq, tdo64, sms, st) != cudaSuccess)
     return BSA_ERR_CUDA;
   return BSA_OK;
 }

@@ -217,13 +217,16 @@ struct DiffBwdParams : DiffList {
   int cols;                  // kv heads * nb
   const float* vec;          // row terms
   void* dq;                  // dQ walk: bf16 [B,2H,L,dq]
-  float* dlam;               // and fp32 [B,H,L]
+  float* dlam;               // fp32 [B,H,L] (lam_rows; written by the dQ walk) or [H] (dK/dV walk)
+  float* lam_sums;           // without lam_rows: [B*H][diff_vec_tiles][4], sums of 16 rows
   void* dk;                  // dK/dV walk: bf16 [B,Hkv,L,d]
   void* dv;
   float* parts;              // dV and dK of cut columns: slots of block * 2 d fp32
+  int* count;                // [CTAs][8]: pieces there of the column cut at a CTA's end, a count a
+                             // warp; zero at the start (bsa_diff_rows.cu)
   int32_t* status;
   float scale_log2, scale;
-  int causal_diag, L, block, d;
+  int causal_diag, lam_rows, H, L, block, d;
   unsigned long long wait_limit_ns;
   int expire_site;
 };
@@ -276,9 +279,6 @@ cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem,
   return cudaLaunchKernelEx(&cfg, kernel, static_cast<P>(args)...);
 }
 #endif
-// Joins the pieces of cut columns (in order) and writes the zeros of columns without a block; sums
-// the rows of dlam to one number a head where dlam is not null.
-cudaError_t launch_diff_join(const DiffBwdParams& p, int grid, float* dlam, int H, cudaStream_t stream);
 // a, b, x, y: q, dO, k, v (dQ walk) or k, v, q, dO (kv).
 #define BSA_DIFF_BWD(name)                                                                      \
   cudaError_t launch_diff_bwd_##name(bool split, bool kv, const DiffBwdParams& p,               \
@@ -301,7 +301,8 @@ struct DiffRowsParams {
   int64_t pairs;     // B * H
   int H, L, d, lam_rows;
 };
-cudaError_t launch_diff_rows(const DiffRowsParams& p, cudaStream_t stream);
+// Row terms; the counts of b to zero, dk and dv of columns without a block, too.  counts: of them.
+cudaError_t launch_diff_rows(const DiffRowsParams& p, const DiffBwdParams& b, int counts, cudaStream_t stream);
 
 // [heads, L, d] bf16 as four dimensions: 64 columns, rows, d/64 column halves, heads.  The box
 // is 64 columns x rows x halves of one head, 128-byte swizzled; rows past L read as zero.

@@ -316,7 +316,7 @@ int bsa_diff_forward(const void* q, const void* k, const void* v, const float* l
  *           Calls that may overlap on the GPU need one each.
  *   the others as in bsa_diff_forward.
  *
- * Asynchronous; four kernels; allocates nothing.  Errors: as
+ * Asynchronous; three kernels; allocates nothing.  Errors: as
  * bsa_diff_forward, BSA_ERR_TOO_LARGE (workspace too small).
  */
 int bsa_diff_backward(const void* q, const void* k, const void* v, const float* lam,
