@@ -656,7 +656,7 @@ def cache_diff_forward(q: torch.Tensor, lam: torch.Tensor, k_cache: torch.Tensor
         _dev_ptr(kv_len, "kv_len", i32, (B,), dev), _dev_ptr(cu_q, "cu_q", i32, (B + 1,), dev), out_ptr, lse_ptr,
         None if status is None else _dev_ptr(status, "status", i32, (1,), dev),
         _dev_ptr(workspace, "workspace", torch.uint8, (ws_bytes,), dev), ws_bytes, B, max_pages, T,
-        heads, dq, max_q, rows, _ACTIVATIONS[q.dtype], qt, qh, scale,
+        heads, dq, max_q, rows, _ACTIVATIONS[q.dtype], qt, qh, float(scale),
         _cache_args(window, softcap, sinks, heads2, lut, block, dev), _cache_stream(stream, dev))
     if rc:
         raise BsaError(rc, "bsa_cache_diff_forward")
@@ -709,7 +709,7 @@ def diff_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.T
     status = lib.bsa_diff_forward(
         _dev_ptr(q, "q", bf16, q.shape, dev), _dev_ptr(k, "k", bf16, keys, dev), _dev_ptr(v, "v", bf16, keys, dev),
         _dev_ptr(lam, "lam", f32, lam_shape, dev), lut.handle, out_ptr, lse_ptr, out2_ptr, B, H, kv, L, d, dq,
-        len(lam_shape) == 3, scale, block, bool(causal_diag), _cache_stream(stream, dev))
+        len(lam_shape) == 3, float(scale), int(block), bool(causal_diag), _cache_stream(stream, dev))
     if status:
         raise BsaError(status, "bsa_diff_forward")
     return out, lse, out2
@@ -765,7 +765,7 @@ def diff_backward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.
     status = lib.bsa_diff_backward(
         q_ptr, k_ptr, v_ptr, lam_ptr, _dev_ptr(out, "out", bf16, rows, dev), _dev_ptr(out2, "out2", bf16, rows, dev),
         _dev_ptr(lse, "lse", f32, (B, 2 * H, L), dev), _dev_ptr(dout, "dout", bf16, rows, dev), lut.handle, *given,
-        ws_ptr, ws_bytes, B, H, kv, L, d, n, len(lam_shape) == 3, scale, block, bool(causal_diag),
+        ws_ptr, ws_bytes, B, H, kv, L, d, n, len(lam_shape) == 3, float(scale), int(block), bool(causal_diag),
         _cache_stream(stream, dev))
     if status:
         raise BsaError(status, "bsa_diff_backward")

@@ -12,8 +12,8 @@
 // 32 a + r under map m:
 //   dQ walk    item: such a tile, A = its Q, B = its dO (each row twice).  Step: 128 keys,
 //              X = K, Y = V.  T1 = A X^T, T2 = B Y^T, E = dS, acc += E X.  The row sums of
-//              P_1 dP, in fp32 throughout, give dlam (D_1 from the bf16 O_1 would carry its
-//              rounding).
+//              P_m dP, in fp32 throughout, are D_m without the rounding of the bf16 outputs:
+//              they give dlam, and the dK/dV walk takes them instead of the row terms' D.
 //   dK/dV walk item: a key block, A = K, B = V (rows: keys).  Step: 64 queries of one head of
 //              the kv head, X = Q of both maps (128 rows), Y = dO (64 rows).  T1 = A X^T (128
 //              columns), T2 = B Y^T (64 columns, for both maps).  A thread's 64 columns of T1
@@ -651,10 +651,34 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
           pk1[i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
         }
       };
-      if (__any_sync(0xffffffffu, hi < 63))
+      if (nsteps == 1) {
+        // All of the row is here: D from P dP itself instead of from the rounded outputs, whose
+        // error is largest in rows of few keys.
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t y = f2_fma(f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), c2, l2);
+          const float p0 = ex2_approx(mask_gt(f2_lo(y), 2 * i, hi)), p1 = ex2_approx(mask_gt(f2_hi(y), 2 * i + 1, hi));
+          rs[2 * i] = __float_as_uint(p0);
+          rs[2 * i + 1] = __float_as_uint(p1);
+          if (2 * i > hi) rp[2 * i] = 0u;
+          if (2 * i + 1 > hi) rp[2 * i + 1] = 0u;
+          sums[i & 1] = f2_fma(f2_pack(p0, p1), f2_pack(__uint_as_float(rp[2 * i]), __uint_as_float(rp[2 * i + 1])), sums[i & 1]);
+        }
+        const uint64_t both = f2_add(sums[0], sums[1]);
+        float all = f2_lo(both) + f2_hi(both);
+        all += __shfl_xor_sync(0xffffffffu, all, 16);
+        const uint64_t wd1 = f2_pack(-w * all, -w * all);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          const uint64_t ds = f2_mul(f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
+                                     f2_fma(f2_pack(__uint_as_float(rp[2 * i]), __uint_as_float(rp[2 * i + 1])), w2, wd1));
+          pk1[i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
+        }
+      } else if (__any_sync(0xffffffffu, hi < 63)) {
         form(std::true_type{});
-      else
+      } else {
         form(std::false_type{});
+      }
       sums[0] = f2_add(sums[0], sums[1]);
       rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
       tmem_st_16x32bx2_x32<32>(t1, pk1);
@@ -673,6 +697,9 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     if (!ok) break;
     rsum += __shfl_xor_sync(0xffffffffu, rsum, 16);
     store_lam(pair, is.cur.y, -rsum);
+    // For the dK/dV walk, which comes after this one.
+    if (half == 0)
+      p.vec[(pair * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + 64 + 32 * map + (qin & 31)] = -rsum;
     pending = true;
     ppair = pair;
     pq = q;

@@ -215,7 +215,7 @@ struct DiffBwdParams : DiffList {
   int B, nb, nnz;            // nnz: active blocks of all kv heads
   long long steps, share;    // of the dK/dV walk, and of one of its CTAs
   int cols;                  // kv heads * nb
-  const float* vec;          // row terms
+  float* vec;                // row terms; the dQ walk writes the D of its rows anew
   void* dq;                  // dQ walk: bf16 [B,2H,L,dq]
   float* dlam;               // fp32 [B,H,L] (lam_rows; written by the dQ walk) or [H] (dK/dV walk)
   float* lam_sums;           // without lam_rows: [B*H][diff_vec_tiles][4], sums of 16 rows
