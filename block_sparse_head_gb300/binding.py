@@ -400,6 +400,20 @@ def _this_device(t, name: str) -> int:
     return dev
 
 
+# torch.cuda.current_device() without its look whether CUDA has been initialised: the callers have
+# a tensor there.
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _device_of(t, name: str) -> int:
+    """_this_device for the calls whose host time counts most."""
+    if isinstance(t, torch.Tensor):
+        dev = t.get_device()
+        if dev >= 0 and dev == _current_device():
+            return dev
+    return _this_device(t, name)
+
+
 def _dev_ptr(t, name: str, dtype, shape, dev: int) -> int:
     """Pointer of a contiguous tensor of this type and shape on device dev."""
     try:
@@ -443,7 +457,7 @@ def _on(stream):
 
 def _cache_view(k_cache, v_cache, k_scale, v_scale):
     """(device, bsa_cache as bytes, kv_heads, d)."""
-    dev = _this_device(k_cache, "k_cache")
+    dev = _device_of(k_cache, "k_cache")
     kind = _CACHE_TYPES.get(k_cache.dtype)
     if kind is None or k_cache.dim() != 4:
         raise ValueError("k_cache must be float8_e4m3fn or int8 [pages, kv_heads, page, d]")
@@ -665,16 +679,18 @@ def cache_diff_forward(q: torch.Tensor, lam: torch.Tensor, k_cache: torch.Tensor
 
 def _diff_shapes(q, k, lam):
     """(device, B, H, kv_heads, L, d, dq, shape of lam) of a differential attention call."""
-    dev = _this_device(q, "q")
+    dev = _device_of(q, "q")
     if q.dim() != 4 or q.shape[1] % 2:
         raise ValueError("q must be bf16 [B, 2H, L, dq]")
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be bf16 [B, kv_heads, L, d]")
     B, H2, L, dq = q.shape
+    _, kv, _, d = k.shape
     H = H2 // 2
-    if not isinstance(lam, torch.Tensor) or lam.dim() not in (1, 3):
+    rows = lam.dim() if isinstance(lam, torch.Tensor) else 0
+    if rows != 1 and rows != 3:
         raise ValueError("lam must be fp32 [H] or [B, H, L]")
-    return dev, B, H, k.shape[1], L, k.shape[3], dq, (H,) if lam.dim() == 1 else (B, H, L)
+    return dev, B, H, kv, L, d, dq, (H,) if rows == 1 else (B, H, L)
 
 
 def diff_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lam: torch.Tensor, lut: Lut,
@@ -835,33 +851,44 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, tab
     ``inverse`` turns back, which is the gradient.  q_out and k_out may be q and k.  Returns (q, k)
     turned (k None without one)."""
     lib = _lib or load_library()
-    dev = _this_device(q, "q")
-    if q.dtype not in _ACTIVATIONS or q.dim() not in (3, 4):
+    dev = _device_of(q, "q")
+    dtype, shape = q.dtype, q.shape
+    kind = _ACTIVATIONS.get(dtype)
+    packed = len(shape) == 3
+    if kind is None or not (packed or len(shape) == 4):
         raise ValueError("q must be bf16 or fp16 [B, H, L, d] or [T, heads, d]")
-    packed = q.dim() == 3
-    B, L, d = (1, q.shape[0], q.shape[2]) if packed else (q.shape[0], q.shape[2], q.shape[3])
-    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != q.dim()):
+    if packed:
+        B, (L, heads, d) = 1, shape
+    else:
+        B, heads, L, d = shape
+    if k is not None and (not isinstance(k, torch.Tensor) or k.dim() != len(shape)):
         raise ValueError("k must have as many dimensions as q")
     if not isinstance(table, RotaryTable):
         raise ValueError("table must come from rotary_table")
-    if pairing not in _PAIRINGS:
+    pair = _PAIRINGS.get(pairing)
+    if pair is None:
         raise ValueError(f"pairing must be one of {tuple(_PAIRINGS)}")
     if not isinstance(positions, torch.Tensor) or positions.dtype is not torch.int32 or \
             positions.get_device() != dev:
         raise ValueError("positions must be an int32 tensor on the current device")
-    if positions.shape not in ((table.axes, L), (table.axes, B, L)):
+    axes = table.axes
+    if positions.shape == (axes, L):
+        pos_axis, one = positions.stride()
+        pos_batch = 0
+    elif positions.shape == (axes, B, L):
+        pos_axis, pos_batch, one = positions.stride()
+    else:
         raise ValueError(f"positions has shape {tuple(positions.shape)}, expected "
-                         f"{(table.axes, L)} or {(table.axes, B, L)}")
-    if positions.stride(-1) != 1 and L > 1:
+                         f"{(axes, L)} or {(axes, B, L)}")
+    if one != 1 and L > 1:
         raise ValueError("positions: the last dimension must be contiguous")
     if table.data.get_device() != dev:
         raise ValueError(f"table is on {table.data.device}, not on the current device")
     if q_out is None or (k is not None and k_out is None):
         with _on(stream):
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device) if q_out is None else q_out
+            q_out = torch.empty(shape, dtype=dtype, device=q.device) if q_out is None else q_out
             if k is not None and k_out is None:
                 k_out = torch.empty(k.shape, dtype=k.dtype, device=q.device)
-    ps, shape, dtype = positions.stride(), q.shape, q.dtype
     qi, q0, q1, q2 = _rotary_rows(q, "q", dtype, shape, dev)
     qo, q3, q4, q5 = _rotary_rows(q_out, "q_out", dtype, shape, dev)
     ki = k0 = k1 = k2 = ko = k3 = k4 = k5 = k_heads = 0
@@ -871,9 +898,9 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor, tab
         ki, k0, k1, k2 = _rotary_rows(k, "k", dtype, shape, dev)
         ko, k3, k4, k5 = _rotary_rows(k_out, "k_out", dtype, shape, dev)
     status = lib.bsa_rotary(_ROTARY_ARGS.pack(
-        qi, qo, q.shape[1], q0, q1, q2, q3, q4, q5, ki, ko, k_heads, k0, k1, k2, k3, k4, k5, positions.data_ptr(),
-        ps[0], ps[1] if positions.dim() == 3 and B > 1 else 0, table.data.data_ptr(), table.pairs, table.axes,
-        _PAIRINGS[pairing], bool(inverse), B, L, d, _ACTIVATIONS[dtype]), _cache_stream(stream, dev))
+        qi, qo, heads, q0, q1, q2, q3, q4, q5, ki, ko, k_heads, k0, k1, k2, k3, k4, k5, positions.data_ptr(),
+        pos_axis, pos_batch, table.data.data_ptr(), table.pairs, axes, pair, bool(inverse), B, L, d, kind),
+        _cache_stream(stream, dev))
     if status:
         raise BsaError(status, "bsa_rotary")
     return q_out, None if k is None else k_out
