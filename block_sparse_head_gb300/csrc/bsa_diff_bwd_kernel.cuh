@@ -604,7 +604,8 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     // dS = P (w dP - w D) with the row's weight w
     const float w = map ? v[128] : 1.f, wd = w * v[64 + 32 * map];
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), l2 = f2_pack(v[32 * map], v[32 * map]);
-    const uint64_t w2 = f2_pack(w, w), wd2 = f2_pack(wd, wd);
+    const uint64_t w2 = f2_pack(w, w);
+    uint64_t wd2 = f2_pack(wd, wd);
     const int dpos = p.causal_diag ? is.dpos() : -1;
     const int qblk = qin + (BLK == 128 ? (is.cur.y & 1) * 64 : 0);
     const int nsteps = (cnt + G - 1) / G;
@@ -654,31 +655,17 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       if (nsteps == 1) {
         // All of the row is here: D from P dP itself instead of from the rounded outputs, whose
         // error is largest in rows of few keys.
+        float all = 0.f;
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint64_t y = f2_fma(f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), c2, l2);
-          const float p0 = ex2_approx(mask_gt(f2_lo(y), 2 * i, hi)), p1 = ex2_approx(mask_gt(f2_hi(y), 2 * i + 1, hi));
-          rs[2 * i] = __float_as_uint(p0);
-          rs[2 * i + 1] = __float_as_uint(p1);
-          if (2 * i > hi) rp[2 * i] = 0u;
-          if (2 * i + 1 > hi) rp[2 * i + 1] = 0u;
-          sums[i & 1] = f2_fma(f2_pack(p0, p1), f2_pack(__uint_as_float(rp[2 * i]), __uint_as_float(rp[2 * i + 1])), sums[i & 1]);
-        }
-        const uint64_t both = f2_add(sums[0], sums[1]);
-        float all = f2_lo(both) + f2_hi(both);
+        for (int c = 0; c < 64; ++c)
+          if (c <= hi) all = fmaf(ex2_approx(fmaf(__uint_as_float(rs[c]), p.scale_log2, f2_lo(l2))), __uint_as_float(rp[c]), all);
         all += __shfl_xor_sync(0xffffffffu, all, 16);
-        const uint64_t wd1 = f2_pack(-w * all, -w * all);
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint64_t ds = f2_mul(f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])),
-                                     f2_fma(f2_pack(__uint_as_float(rp[2 * i]), __uint_as_float(rp[2 * i + 1])), w2, wd1));
-          pk1[i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
-        }
-      } else if (__any_sync(0xffffffffu, hi < 63)) {
-        form(std::true_type{});
-      } else {
-        form(std::false_type{});
+        wd2 = f2_pack(-w * all, -w * all);
       }
+      if (__any_sync(0xffffffffu, hi < 63))
+        form(std::true_type{});
+      else
+        form(std::false_type{});
       sums[0] = f2_add(sums[0], sums[1]);
       rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
       tmem_st_16x32bx2_x32<32>(t1, pk1);

@@ -242,11 +242,7 @@ __device__ __forceinline__ void diff_softmax(const DiffFwdParams& p, uint32_t sb
     for (int s = 0; s < nsteps; ++s, ++g) {
       const int nblk = step_blocks<G>(nnz, s);
       const bool valid = (KB == 128) || (half < nblk);
-      // Last key of this half's 64 that the row sees: before the diagonal's end and the sequence's.
-      int lim = NC - 1;
-      if (valid && ((KB == 128) ? s : s * 2 + half) == dpos) lim = min(lim, qblk - kbase);
-      if (valid && ((KB == 128) ? s : s * 2 + half) == cut) lim = min(lim, (p.L - 1) % KB - kbase);
-      if (!valid) lim = -1;
+      const int blk = (KB == 128) ? s : s * 2 + half;  // the half's place in the row
       const uint32_t ts = tl + (g % 3) * 128;
       if (__all_sync(0xffffffffu, s_next)) {
         tc_fence_after();
@@ -271,7 +267,11 @@ __device__ __forceinline__ void diff_softmax(const DiffFwdParams& p, uint32_t sb
 #pragma unroll
         for (int c = 0; c < NC; ++c) x[c] *= p.scale_log2;
       }
-      if (lim < NC - 1) {
+      if (!valid || blk == dpos || blk == cut) {  // KB = 128: the same for the whole warp
+        // Last key of this half's 64 that the row sees: before the diagonal's and the sequence's end.
+        int lim = valid ? NC - 1 : -1;
+        if (blk == dpos) lim = min(lim, qblk - kbase);
+        if (blk == cut) lim = min(lim, (p.L - 1) % KB - kbase);
 #pragma unroll
         for (int c = 0; c < NC; ++c) x[c] = mask_gt(x[c], c, lim);
       }

@@ -43,7 +43,7 @@ struct Piece<2> {
 };
 template <>
 struct Piece<1> {
-  using T = uint16_t;
+  using T = unsigned short;
 };
 
 template <class A>
@@ -108,8 +108,8 @@ __global__ void __launch_bounds__(kThreads, 3) bsa_rotary_kernel(const RotaryPar
       const uint16_t* from = static_cast<const uint16_t*>(side.in) + b * side.in_batch + hh * side.in_head +
                              t * side.in_token + x0;
       to[j] = static_cast<uint16_t*>(side.out) + b * side.out_batch + hh * side.out_head + t * side.out_token + x0;
-      a[j] = *reinterpret_cast<const T*>(from);
-      if (HALF && turns) z[j] = *reinterpret_cast<const T*>(from + p.pairs);
+      a[j] = __ldcs(reinterpret_cast<const T*>(from));
+      if (HALF && turns) z[j] = __ldcs(reinterpret_cast<const T*>(from + p.pairs));
     }
 #pragma unroll
     for (int j = 0; j < kRows; ++j) {
@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 3) bsa_rotary_kernel(const RotaryPar
             x[i] = from_float<A>(fmaf(f, c[i], -g * s[i]));
             y[i] = from_float<A>(fmaf(f, s[i], g * c[i]));
           }
-          *reinterpret_cast<T*>(to[j] + p.pairs) = z[j];
+          __stcs(reinterpret_cast<T*>(to[j] + p.pairs), z[j]);
         }
       } else {
 #pragma unroll
@@ -135,7 +135,7 @@ __global__ void __launch_bounds__(kThreads, 3) bsa_rotary_kernel(const RotaryPar
           x[2 * i + 1] = from_float<A>(fmaf(f, s[i], g * c[i]));
         }
       }
-      *reinterpret_cast<T*>(to[j]) = a[j];
+      __stcs(reinterpret_cast<T*>(to[j]), a[j]);
     }
   }
 }
