@@ -58,8 +58,11 @@ static_assert(kDiffVec == kDiffVecFloats, "workspace");
 template <int BLK, int D, bool KV>
 struct DiffBwdCfg {
   static constexpr int kRows = KV ? BLK : 128;         // rows of an item tile
-  static constexpr int kNumWG = kRows / 64;            // elementwise warpgroups
-  static constexpr int kEwWarps = 4 * kNumWG;
+  static constexpr int kEwWarps = 8;                   // elementwise warps
+  // Those of one step: eight for 128 rows; for 64 rows (dK/dV, block 64) four, and the two groups
+  // take steps in turn.
+  static constexpr int kStepWarps = kRows / 16;
+  static constexpr int kGroups = kEwWarps / kStepWarps;
   static constexpr int kMma2Warp = 2 + kEwWarps;
   static constexpr int kThreads = 32 * (3 + kEwWarps);
   static constexpr int kG = KV ? 1 : 128 / BLK;        // key blocks of a step (dQ walk)
@@ -81,18 +84,32 @@ struct DiffBwdCfg {
   static constexpr int kVecB = kDiffVec * 4;
   static constexpr int kOffVec = kOffY + kNY * kYTile;
   static constexpr int kOffBar = kOffVec + (KV ? kNX * kVecB : 0);
-  // barriers: as in the plain backward
-  static constexpr int kBarIF = 0, kBarIE = 1, kBarXF = 2, kBarXE = 5, kBarYF = 8, kBarYE = 10;
-  static constexpr int kBarTF = 12, kBarEF = 13, kBarAD = 14, kBarAR = 16, kBarDrain = 17;
-  static constexpr int kBarEF1 = 18, kBarDF = 19, kBarDL = 20, kBarIFV = 21, kBarIEV = 22;
-  static constexpr int kBarVI = 23, kBarDrain2 = 24, kBarQI = 25, kNumBars = 26;
+  // barriers
+  static constexpr int kBarIF = 0;     // item tiles landed (dK/dV: A's)
+  static constexpr int kBarIE = 1;     // item tiles free (dK/dV: A's)
+  static constexpr int kBarXF = 2;     // [3] X landed (dK/dV: X, Y and the row terms)
+  static constexpr int kBarXE = 5;     // [3] X free
+  static constexpr int kBarYF = 8;     // [2] dQ: Y landed
+  static constexpr int kBarYE = 10;    // [2] dQ: Y free
+  // By the step's parity, so that one who waits for a step's phase (the second issuer, a group of
+  // warps) cannot miss it: the next one needs that step's second products.
+  static constexpr int kBarTF = 12;    // [2] T1 (dQ: and T2) computed
+  static constexpr int kBarDF = 14;    // [2] dK/dV: T2 computed
+  static constexpr int kBarEF1 = 16;   // [2] dK/dV: E1 written (a step's warps)
+  static constexpr int kBarEF = 18;    // [2] E (E2) written (a step's warps)
+  static constexpr int kBarAD = 20;    // [2] a step's second products done
+  static constexpr int kBarDL = 22;    // dQ: T2 loaded; dK/dV: T1 loaded (a step's warps)
+  static constexpr int kBarAR = 23;    // accumulators read out (a step's warps)
+  static constexpr int kBarIFV = 24;   // dK/dV: item tile B landed
+  static constexpr int kBarIEV = 25;   // dK/dV: item tile B free
+  static constexpr int kBarDrain = 26, kBarDrain2 = 27, kNumBars = 28;
   static constexpr int kBarBytes = 256;
   static_assert(kNumBars * 8 + 8 <= kBarBytes && kOffBar % 8 == 0 && kOffVec % 16 == 0, "barrier area");
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
   static_assert(kSmemBytes <= 232448, "shared memory budget");
   static constexpr int kLaunchSmem = kSmemBytes > 120 * 1024 ? kSmemBytes : 120 * 1024;
-  // TMEM columns, as in the plain backward.  dQ: T1 at 0 or 256, T2 at 128, acc at 384.  dK/dV:
-  // T1 and T2 (its first 64 columns) swap between 0 and 128; E1 and E2 over T1.
+  // TMEM columns.  dQ: T1 at 0 or 256 (E over it), T2 at 128, acc at 384.  dK/dV: a step's T1 at 0
+  // or 128, T2 (and E2) over its second half, E1 over its first; acc at 256.
   static constexpr int kT1 = 0, kT2 = 128, kT1b = 256;
   static constexpr int kAcc1 = KV ? 256 : 384, kAcc2 = 256 + D;
   static constexpr uint32_t kIdescT1 = idesc_bf16_f32(kRows, KV ? 128 : BLK, false, false);
@@ -341,7 +358,7 @@ __device__ __forceinline__ void diff_dq_mma(const DiffBwdParams& p, uint32_t sba
     tc_fence_after();
     diff_issue_first<D, C::kItemPlane, C::kYPlane, C::kXBlkB, BLK>(
         tmem + C::kT2, b0, y0 + (t % 2) * (C::kYTile >> 4), hi, C::kIdescT2, nblk);
-    tc_commit(bar(C::kBarTF));
+    tc_commit(bar(C::kBarTF + (t & 1)));
     tc_commit(bar(C::kBarYE + t % 2));
     if (last) tc_commit(bar(C::kBarIE));
   }
@@ -367,8 +384,7 @@ __device__ __forceinline__ void diff_dq_mma2(const DiffBwdParams& p, uint32_t sb
     const bool first = c.s == 0;
     c.advance(p);
     if (first) ++n;
-    if (!mbar_wait(bar(C::kBarEF), u & 1, ctl, kSiteMmaPFull)) break;
-    mbar_arrive(bar(C::kBarQI));
+    if (!mbar_wait(bar(C::kBarEF + (u & 1)), (u / 2) & 1, ctl, kSiteMmaPFull)) break;
     if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
     tc_fence_after();
     const uint32_t te = tmem + ((u & 1) ? C::kT1b : C::kT1), xs = x0 + (u % 3) * (C::kXTile >> 4);
@@ -430,7 +446,7 @@ __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sba
       diff_issue_first<D, C::kItemPlane, C::kYPlane, 0, 64>(
           tmem + ((t & 1) ? C::kT2 : C::kT1) + 64, b0, y0 + (t % 3) * (C::kYTile >> 4), hi,
           C::kIdescT2, 1);  // dP^T = V dO^T
-      tc_commit(bar(C::kBarDF));
+      tc_commit(bar(C::kBarDF + (t & 1)));
       if (last) tc_commit(bar(C::kBarIEV));
       if (!c.valid()) break;
       first = c.first;
@@ -443,7 +459,7 @@ __device__ __forceinline__ void diff_kv_mma(const DiffBwdParams& p, uint32_t sba
         break;
       tc_fence_after();
       issue1(t + 1);
-      tc_commit(bar(C::kBarTF));
+      tc_commit(bar(C::kBarTF + ((t + 1) & 1)));
       if (last) tc_commit(bar(C::kBarIE));
       if (first) ++n;
     }
@@ -470,15 +486,14 @@ __device__ __forceinline__ void diff_kv_mma2(const DiffBwdParams& p, uint32_t sb
     c.advance(p);
     if (first) ++n;
     const uint32_t t1 = tmem + ((t & 1) ? C::kT2 : C::kT1);
-    if (!mbar_wait(bar(C::kBarEF1), t & 1, ctl, kSiteMmaPFull)) break;
+    if (!mbar_wait(bar(C::kBarEF1 + (t & 1)), (t / 2) & 1, ctl, kSiteMmaPFull)) break;
     if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < 4; ++kk)
       tc_mma_ts_lh(tmem + C::kAcc1, t1 + kk * 8, y0 + (t % 3) * (C::kYTile >> 4) + ((kk * 16 * 128) >> 4),
                    hi, C::kIdescAcc, (first && kk == 0) ? 0u : 1u);
-    if (!mbar_wait(bar(C::kBarEF), t & 1, ctl, kSiteMmaPFull)) break;
-    mbar_arrive(bar(C::kBarVI));
+    if (!mbar_wait(bar(C::kBarEF + (t & 1)), (t / 2) & 1, ctl, kSiteMmaPFull)) break;
     tc_fence_after();
 #pragma unroll
     for (int kk = 0; kk < 8; ++kk)
@@ -614,7 +629,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       const int nblk = step_blocks<G>(cnt, s);
       const bool valid = (BLK == 128) || (half < nblk);
       const bool diag = valid && (((BLK == 128) ? s : s * 2 + half) == dpos);
-      if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) {
+      if (!wait_bar(C::kBarTF + (g & 1), (g / 2) & 1, kSiteSoftSFull)) {
         ok = false;
         break;
       }
@@ -670,12 +685,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
       tmem_st_16x32bx2_x32<32>(t1, pk1);
       tmem_st_wait();
-      // The issuer of the dQ products has seen the previous step's E: it cannot fall two phases behind.
-      if (g >= 1 && !wait_bar(C::kBarQI, (g - 1) & 1, kSiteSoftSFull)) {
-        ok = false;
-        break;
-      }
-      warp_arrive(C::kBarEF);
+      warp_arrive(C::kBarEF + (g & 1));
       if (s == 0 && pending && !read_pending()) {
         ok = false;
         break;
@@ -703,6 +713,8 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
   using C = DiffBwdCfg<BLK, D, true>;
   auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
   const int wg = ((threadIdx.x >> 5) - 2) >> 2;
+  const int group = C::kGroups == 2 ? wg : 0;  // takes steps group, group + kGroups, ..
+  const int gwarp = ((threadIdx.x >> 5) - 2) % C::kStepWarps;
   const int wq = (threadIdx.x >> 5) & 3;
   const int lane = threadIdx.x & 31;
   const int half = lane >> 4;
@@ -723,15 +735,19 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
   const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
   DiffKvWalk c;
   c.init(p);
-  int dpos = -1;
-  for (int g = 0; c.valid(); ++g) {
+  if (group == 1 && c.valid()) c.advance(p);
+  int dpos = -1, dcol = -1;  // the diagonal block's place in column dcol
+  for (int g = group; c.valid(); g += C::kGroups) {
     const uint32_t t1 = tl + ((g & 1) ? C::kT2 : C::kT1);
-    if (c.first && p.causal_diag) dpos = p.diag_pos[c.col];
+    if (c.col != dcol && p.causal_diag) {
+      dcol = c.col;
+      dpos = p.diag_pos[dcol];
+    }
     // Of this half's 32 queries those before the key are masked in the diagonal block.
     const int lo = (c.x - c.begin == dpos) ? row - 64 * (c.rest % C::kHalves) - 32 * half : -(1 << 30);
     const float4* vec = reinterpret_cast<const float4*>(smem + C::kOffVec + (g % 3) * C::kVecB +
                                                         half * (kDiffVecHalf * 4));
-    if (!wait_bar(C::kBarTF, g & 1, kSiteSoftSFull)) break;
+    if (!wait_bar(C::kBarTF + (g & 1), (g / 2) & 1, kSiteSoftSFull)) break;
     uint32_t rs[2][32];  // S^T, then P^T, of each map
     tmem_ld_16x32bx2_x32<64>(t1, rs[0]);
     tmem_ld_16x32bx2_x32<64>(t1 + 32, rs[1]);
@@ -771,11 +787,8 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
       tmem_st_16x32bx2_x16<16>(t1, pk);
     }
     tmem_st_wait();
-    // The issuer that waits for E1 and E2 in turn has seen E2 of the step before: it cannot fall two
-    // phases behind.
-    if (g >= 1 && !wait_bar(C::kBarVI, (g - 1) & 1, kSiteSoftSFull)) break;
-    warp_arrive(C::kBarEF1);
-    if (!wait_bar(C::kBarDF, g & 1, kSiteSoftSFull)) break;
+    warp_arrive(C::kBarEF1 + (g & 1));
+    if (!wait_bar(C::kBarDF + (g & 1), (g / 2) & 1, kSiteSoftSFull)) break;
     uint32_t rp[32];  // dP^T
     tmem_ld_16x32bx2_x32<32>(t1 + 64, rp);
     tmem_ld_wait(rp);
@@ -794,7 +807,7 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
       tmem_st_16x32bx2_x32<32>(t1 + 64, pk);
     }
     tmem_st_wait();
-    warp_arrive(C::kBarEF);
+    warp_arrive(C::kBarEF + (g & 1));
     const bool whole = c.head && c.tail();
     if (c.last()) {
       // The piece is complete once its last step's products are.
@@ -819,12 +832,12 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
         const int root = static_cast<int>(diff_div((base + c.begin) * c.per, p.share));
         const int end = static_cast<int>(diff_div((base + c.end) * c.per - 1, p.share));
         const int me = blockIdx.x;
-        int* count = p.count + root * C::kEwWarps + ((threadIdx.x >> 5) - 2);
+        int* count = p.count + root * C::kEwWarps + gwarp;
         // A piece is laid out as its readers, the same warps elsewhere, take it: lanes side by side.
         auto piece = [&](int i, int g) {
           const int64_t slot = i == root ? 2 * static_cast<int64_t>(root) + 1 : 2 * static_cast<int64_t>(i);
           return reinterpret_cast<float4*>(p.parts) + slot * (BLK * 2 * D / 4) +
-                 (((threadIdx.x >> 5) - 2) * (D / 32) + g) * (8 * 32) + lane;
+                 (gwarp * (D / 32) + g) * (8 * 32) + lane;
         };
         const int64_t orow = static_cast<int64_t>(c.b * (p.cols / p.nb) + kv) * p.L + key;
         // Columns 64 g + 32 half .. of dV | dK: the pieces' sum (own: this CTA's) to bf16.
@@ -895,7 +908,9 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
         }
       }
     }
-    c.advance(p);
+#pragma unroll
+    for (int i = 0; i < C::kGroups; ++i)
+      if (c.valid()) c.advance(p);
   }
   tmem_st_wait();
 }
@@ -920,9 +935,9 @@ __global__ void __launch_bounds__(DiffBwdCfg<BLK, D, KV>::kThreads, 1)
   if (threadIdx.x == 0) {
     auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
     for (int i = 0; i < C::kNumBars; ++i)
-      mbar_init(bar(i), (i == C::kBarEF || i == C::kBarAR || i == C::kBarEF1 || i == C::kBarDL)
-                           ? C::kEwWarps
-                           : 1);
+      mbar_init(bar(i), (i >= C::kBarEF1 && i < C::kBarEF + 2) || i == C::kBarAR || i == C::kBarDL
+                            ? C::kStepWarps
+                            : 1);
     *abort_flag = 0;
     fence_mbar_init();
   }
