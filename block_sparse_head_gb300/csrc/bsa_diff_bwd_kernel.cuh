@@ -102,7 +102,9 @@ struct DiffBwdCfg {
   static constexpr int kBarAR = 23;    // accumulators read out (a step's warps)
   static constexpr int kBarIFV = 24;   // dK/dV: item tile B landed
   static constexpr int kBarIEV = 25;   // dK/dV: item tile B free
-  static constexpr int kBarDrain = 26, kBarDrain2 = 27, kNumBars = 28;
+  static constexpr int kBarDrain = 26, kBarDrain2 = 27;
+  static constexpr int kBarQI = 28;    // dQ: a step's E taken by the second issuer
+  static constexpr int kNumBars = 29;
   static constexpr int kBarBytes = 256;
   static_assert(kNumBars * 8 + 8 <= kBarBytes && kOffBar % 8 == 0 && kOffVec % 16 == 0, "barrier area");
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
@@ -385,6 +387,7 @@ __device__ __forceinline__ void diff_dq_mma2(const DiffBwdParams& p, uint32_t sb
     c.advance(p);
     if (first) ++n;
     if (!mbar_wait(bar(C::kBarEF + (u & 1)), (u / 2) & 1, ctl, kSiteMmaPFull)) break;
+    mbar_arrive(bar(C::kBarQI));
     if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
     tc_fence_after();
     const uint32_t te = tmem + ((u & 1) ? C::kT1b : C::kT1), xs = x0 + (u % 3) * (C::kXTile >> 4);
@@ -590,8 +593,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
   // The previous item's accumulator goes out at the next item's first step, once that step's E
   // is handed over.
   bool pending = false;
-  int64_t ppair = 0;
-  int pq = 0, pg = 0;  // its query and last step
+  int ppair = 0, pq = 0, pg = 0;  // its query and last step
   auto read_pending = [&]() -> bool {
     if (!wait_bar(C::kBarAD + (pg & 1), (pg / 2) & 1, kSiteSoftItemDone)) return false;
     uint32_t pk[D / 4];
@@ -607,7 +609,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
   ItemStream is;
   for (is.init<false>(p); ok && !is.done(); is.next<false>(p)) {
     const int cnt = is.nnz();
-    const int64_t pair = is.cur.x;
+    const int pair = is.cur.x;
     const int q = is.cur.y * 64 + qin;
     if (cnt == 0) {
       const uint32_t zero[D / 4] = {};
@@ -615,7 +617,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       store_lam(pair, is.cur.y, 0.f);
       continue;
     }
-    const float* v = p.vec + (pair * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + (qin & 31);
+    const float* v = p.vec + (static_cast<int64_t>(pair) * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + (qin & 31);
     // dS = P (w dP - w D) with the row's weight w
     const float w = map ? v[128] : 1.f, wd = w * v[64 + 32 * map];
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), l2 = f2_pack(v[32 * map], v[32 * map]);
@@ -685,6 +687,12 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
       tmem_st_16x32bx2_x32<32>(t1, pk1);
       tmem_st_wait();
+      // The second issuer has taken the previous step's E.  Nothing depends on this wait; without it
+      // the walk is 1 to 3 % slower (8,192 tokens: 199 us, 197 with it).
+      if (g >= 1 && !wait_bar(C::kBarQI, (g - 1) & 1, kSiteSoftSFull)) {
+        ok = false;
+        break;
+      }
       warp_arrive(C::kBarEF + (g & 1));
       if (s == 0 && pending && !read_pending()) {
         ok = false;
@@ -696,7 +704,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     store_lam(pair, is.cur.y, -rsum);
     // For the dK/dV walk, which comes after this one.
     if (half == 0)
-      p.vec[(pair * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + 64 + 32 * map + (qin & 31)] = -rsum;
+      p.vec[(static_cast<int64_t>(pair) * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + 64 + 32 * map + (qin & 31)] = -rsum;
     pending = true;
     ppair = pair;
     pq = q;
