@@ -236,8 +236,15 @@ int bsa_rotary(const bsa_rotary_args* a, void* stream) {
       if (n % 8 != 0) return BSA_ERR_ALIGN;
     if (s.in == s.out && (s.in_batch != s.out_batch || s.in_head != s.out_head || s.in_token != s.out_token))
       return BSA_ERR_UNSUPPORTED;
+    // Rows that share a place would be written by several threads.
+    if ((a->B > 1 && s.out_batch == 0) || (s.heads > 1 && s.out_head == 0) || (a->L > 1 && s.out_token == 0))
+      return BSA_ERR_UNSUPPORTED;
     p.side[i] = {s.in, s.out, s.heads, s.in_batch, s.in_head, s.in_token, s.out_batch, s.out_head, s.out_token};
   }
+  // One side's output over the other side's tensors: turned twice, or read after it was turned.
+  if (a->q.heads > 0 && a->k.heads > 0 &&
+      (a->q.out == a->k.out || a->q.out == a->k.in || a->k.out == a->q.in))
+    return BSA_ERR_UNSUPPORTED;
   p.positions = a->positions;
   p.table = a->table;
   p.pos_axis = a->pos_axis;

@@ -637,7 +637,8 @@ enum {
 
 /* q or k: number x of token t of head h of batch entry b at b * batch + h * head + t * token + x
  * of `in` (and likewise of `out`); strides in elements, multiples of 8 (the stride of a dimension
- * of one is not used).  `out` may be `in` with the same strides; else they do not overlap. */
+ * of one is not used).  `out` may be `in` with the same strides; else they do not overlap, nor do
+ * two numbers of an output, nor one side's output and the other side's tensors. */
 typedef struct bsa_rotary_side {
   const void* in;  /* device, dtype, 16-byte aligned */
   void* out;       /* the same                       */
@@ -662,8 +663,8 @@ typedef struct bsa_rotary_args {
 } bsa_rotary_args;
 
 /* Asynchronous, one kernel launch, allocates nothing.  Errors: BSA_ERR_NULL, BSA_ERR_SHAPE,
- * BSA_ERR_DTYPE, BSA_ERR_ALIGN, BSA_ERR_UNSUPPORTED (pairing, in place with other strides),
- * BSA_ERR_CUDA. */
+ * BSA_ERR_DTYPE, BSA_ERR_ALIGN, BSA_ERR_UNSUPPORTED (pairing, in place with other strides, an
+ * output of stride 0, one side's output where the other side's tensors begin), BSA_ERR_CUDA. */
 int bsa_rotary(const bsa_rotary_args* args, void* stream);
 
 /*

@@ -13,6 +13,7 @@ import torch
 import block_sparse_head_gb300 as bsa
 from oracle import bsa_oracle_cache as oc
 from test_gpu_cache import LENS, Case, _stored, ints
+from test_gpu_cache_abort import Call
 
 pytestmark = pytest.mark.gpu
 
@@ -223,6 +224,28 @@ def test_a_serving_step():
         tol = 2.0 ** -8 * np.abs(ref) + each[:, 0::2] + ln * each[:, 1::2]
         assert np.all(np.abs(out[:n].double().cpu().numpy() - ref) <= tol)
         assert np.all(np.abs(lse[:n].double().cpu().numpy() - rl) <= delta + 2.0 ** -20 * (1 + np.abs(rl)))
+
+
+class DiffCall(Call):
+    """test_gpu_cache_abort's calls, as two maps of G / 2 heads a kv head."""
+
+    def __call__(self, status=None):
+        lam = torch.linspace(0.1, 0.9, self.q.shape[1] // 2, device="cuda")
+        out, lse, _ = bsa.cache_diff_forward(self.q, lam, self.kc, self.vc, self.ks, self.vs, self.table, self.lens,
+                                             self.cu, self.scale, max_q=self.n, lut=self.lut, block=128,
+                                             workspace=self.ws, status=status)
+        return out, lse
+
+
+@pytest.mark.parametrize("site", [6, 16])
+@pytest.mark.parametrize("G,n,d", [(4, 1, 128), (4, 4, 128), (10, 1, 64)])
+def test_decode_wait_gives_up(G, n, d, site):
+    DiffCall([3000, 130, 9000, 257] * 8, n, G, 4, d).check_site(site)
+
+
+@pytest.mark.parametrize("site,others", [(6, [1, 2, 7, 9]), (7, [1, 2, 6, 8, 9, 11, 12]), (17, [17])])
+def test_tile_role_is_missing(site, others):
+    DiffCall([6000, 300, 20000, 1290], 200, 4, 4, 128).check_site(site, [0x10000 | x for x in others], ways=1)
 
 
 def test_no_tokens():

@@ -141,6 +141,66 @@ def test_repeatable_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+def test_two_streams_at_once():
+    """Forwards and backwards on two streams that share the LUT, with nothing between them: the
+    same bits as one after another."""
+    lut = bsa.build_lut(_layout(2, 8, 75), 1)
+    sets = [_inputs(1, 8, 2, 1000, 128, 128, rows, 76 + rows) for rows in (False, True)]
+
+    def step(t, **kw):
+        q, k, v, lam, do = t
+        out, lse, out2 = bsa.diff_forward(q, k, v, lam, lut, 0.1, 128, True, training=True, **kw)
+        return (out, lse, out2) + bsa.diff_backward(q, k, v, lam, out, out2, lse, do, lut, 0.1, 128, True, **kw)
+
+    want = [step(t) for t in sets]
+    torch.cuda.synchronize()
+    sides = [torch.cuda.Stream() for _ in sets]
+    got = [[step(t, stream=s) for t, s in zip(sets, sides)] for _ in range(6)]
+    torch.cuda.synchronize()
+    assert lut.device_status()[0] == 0
+    for both in got:
+        for a, b in zip(both, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
+
+
+def test_offsets_behind_32_bits():
+    """More than 2^31 numbers of queries; the last heads and the first against calls of them alone.
+    dk and dv are summed in fp32 in another order there: within one rounding of each other."""
+    L, H, d, block = 65536, 132, 128, 128
+    nb = L // block
+    lay = torch.zeros(1, nb, nb, dtype=torch.int32)
+    lay[0, torch.arange(nb), torch.arange(nb)] = 1
+    lay[0, nb - 1, 0] = 1
+    luts = [bsa.build_lut(lay.expand(n, nb, nb).contiguous(), 1) for n in (H, 1)]
+    g = torch.Generator(device="cuda").manual_seed(92)
+
+    def rows(n):
+        t = torch.empty(1, n, L, d, dtype=torch.bfloat16, device="cuda")
+        for h in range(n):
+            t[0, h] = torch.randn(L, d, generator=g, device="cuda")
+        return t
+
+    q, k, v, do = rows(2 * H), rows(H), rows(H), rows(H)
+    assert q.numel() > 2 ** 31
+    lam = torch.rand(1, H, L, generator=g, device="cuda")
+    out, lse, out2 = bsa.diff_forward(q, k, v, lam, luts[0], 0.1, block, True, training=True)
+    grads = bsa.diff_backward(q, k, v, lam, out, out2, lse, do, luts[0], 0.1, block, True)
+    assert luts[0].device_status()[0] == 0
+    for h in (0, H - 1):
+        one = [t[:, h:h + 1].contiguous() for t in (k, v, lam, do)]
+        qh = q[:, 2 * h:2 * h + 2].contiguous()
+        o, s, o2 = bsa.diff_forward(qh, *one[:3], luts[1], 0.1, block, True, training=True)
+        gr = bsa.diff_backward(qh, *one[:3], o, o2, s, one[3], luts[1], 0.1, block, True)
+        assert torch.equal(out[:, h:h + 1], o) and torch.equal(out2[:, h:h + 1], o2)
+        assert torch.equal(lse[:, 2 * h:2 * h + 2], s) and torch.equal(grads[0][:, 2 * h:2 * h + 2], gr[0])
+        assert torch.equal(grads[3][:, h:h + 1], gr[3])
+        for a, b in ((grads[1], gr[1]), (grads[2], gr[2])):
+            a, b = a[:, h:h + 1].float(), b.float()
+            # One bf16 step, at most 2^-7 of the value, and the order of the sums: at most four
+            # steps of eight accumulations, each off by 2^-23 of a sum of at most 256 terms below 10.
+            assert torch.all((a - b).abs() <= 2.0 ** -7 * torch.maximum(a.abs(), b.abs()) + 32 * 2560 * 2.0 ** -23)
+
+
 def test_captured_step_follows_its_inputs():
     q, k, v, lam, do = _inputs(1, 2, 2, 300, 64, 64, False, 76)
     lay = torch.tril(torch.ones(2, 5, 5, dtype=torch.int32))

@@ -189,6 +189,39 @@ def test_streams_and_capture():
     assert all(torch.equal(a, b) for a, b in zip(held, bsa.rotary(q, k, pos, table)))
 
 
+def test_offsets_behind_32_bits():
+    """More than 2^31 numbers of queries: the last tokens of the last head against a call of them
+    alone, in place and not."""
+    L, d, n = 270_000, 128, 70
+    q = torch.empty(1, 64, L, d, dtype=torch.bfloat16, device="cuda")
+    assert q.numel() > 2 ** 31
+    g = torch.Generator().manual_seed(15)
+    tail = torch.randn(1, 2, n, d, generator=g).to(torch.bfloat16).cuda()
+    q[:, -2:, -n:] = tail
+    q[:, 0, :n] = tail[:, 0]
+    pos = torch.arange(L, dtype=torch.int32).cuda()[None]
+    table = bsa.rotary_table(_ladder(64, 1)[0])
+    want = bsa.rotary(tail, None, pos[:, -n:].contiguous(), table)[0]
+    first = bsa.rotary(tail[:, :1].contiguous(), None, pos[:, :n].contiguous(), table)[0]
+    for out in (None, q):
+        got = bsa.rotary(q, None, pos, table, q_out=out)[0]
+        assert torch.equal(got[:, -2:, -n:], want) and torch.equal(got[:, :1, :n], first)
+        del got
+
+
+def test_queries_that_are_the_keys():
+    """q and k one tensor: turned into two outputs; in place it is refused."""
+    q = torch.randn(1, 2, 9, 64, device="cuda").to(torch.bfloat16)
+    pos = torch.arange(9, dtype=torch.int32).cuda()[None]
+    table = bsa.rotary_table(_ladder(32, 1)[0])
+    a, b = bsa.rotary(q, q, pos, table)
+    assert torch.equal(a, b) and torch.equal(a, bsa.rotary(q, None, pos, table)[0])
+    with pytest.raises(bsa.BsaError):
+        bsa.rotary(q, q, pos, table, q_out=q, k_out=q)
+    with pytest.raises(bsa.BsaError):
+        bsa.rotary(q, None, pos, table, q_out=q[:, :1].expand(1, 2, 9, 64))
+
+
 def test_no_tokens():
     table = bsa.rotary_table([1.0])
     q = torch.empty(0, 4, 64, dtype=torch.float16, device="cuda")

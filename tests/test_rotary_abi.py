@@ -80,3 +80,20 @@ def test_arguments(lib):
     assert lib.bsa_rotary(None, None) == -1
     # nothing to do: no device is asked for
     assert f(L=0) == 0 and f(B=0) == 0 and f(H=0, Hk=0) == 0 and f(H=0, q=0, qo=0, L=0) == 0
+
+
+def test_outputs_that_share_places_are_refused(lib):
+    """Queries that are the keys too, turned in place (twice, or read after the turn), and outputs
+    whose rows are one row."""
+    names = ["q", "qo", "H", "qb", "qh", "qt", "qob", "qoh", "qot", "k", "ko", "Hk", "kb", "kh", "kt", "kob", "koh",
+             "kot", "pos", "pa", "pb", "table", "pairs", "axes", "pairing", "inverse", "B", "L", "d", "dtype"]
+    C, D, E = A + 4096, A + 8192, A + 12288
+    good = dict(zip(names, [A, C, 4, 4096, 512, 64, 4096, 512, 64, D, E, 2, 4096, 512, 64, 4096, 512, 64, A, 8,
+                            0, A, 32, 1, 0, 0, 2, 8, 64, 0]))
+
+    def f(**kw):
+        return lib.bsa_rotary(binding._ROTARY_ARGS.pack(*{**good, **kw}.values()), None)
+
+    for kw in (dict(q=D, qo=D, ko=D), dict(ko=C), dict(k=A, qo=A), dict(q=D, ko=D), dict(qob=0), dict(qoh=0), dict(qot=0),
+               dict(kob=0), dict(koh=0), dict(kot=0)):
+        assert f(**kw) == -6, kw
