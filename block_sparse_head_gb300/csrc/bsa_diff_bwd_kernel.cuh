@@ -8,8 +8,9 @@
 //
 // The row terms are bsa_diff_rows.cu's; the two walks here are dQ over the layout's rows and dK and
 // dV over its columns.
-// Both are the plain backward's pipelines (bsa_bwd_kernel.cuh: roles, barriers, TMEM regions) on tiles of 64 queries with both maps as 128 rows, row 64 a + 32 m + r being query
-// 32 a + r under map m:
+// Both are the plain backward's pipelines (bsa_bwd_kernel.cuh: roles, barriers, TMEM regions) on
+// tiles of 64 queries with both maps as 128 rows, row 64 a + 32 m + r being query 32 a + r under
+// map m:
 //   dQ walk    item: such a tile, A = its Q, B = its dO (each row twice).  Step: 128 keys,
 //              X = K, Y = V.  T1 = A X^T, T2 = B Y^T, E = dS, acc += E X.  The row sums of
 //              P_m dP, in fp32 throughout, are D_m without the rounding of the bf16 outputs:
@@ -28,7 +29,23 @@
 // (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
 // Rows past the end of the sequence read as zero and carry -lse = -inf, so that their P is 0;
 // keys past it have K = V = 0 and are not stored.
-// Every wait is bounded (WaitCtl), as in the plain kernels.
+// P, dS and their combinations are rounded to bf16 for their products; scores, dP, D, the sums
+// over keys, rows, maps and heads and dlam's sum are fp32 or more, and each gradient is rounded
+// once.  Every wait is bounded (WaitCtl), as in the plain kernels.
+//
+// Bound: the chain of a step, products -> TMEM loads -> exponentials and dS -> TMEM stores ->
+// products; the tensor pipe works 49 % of the time in both walks.  Timing copies without one part
+// each: no row terms -1 %, no exponentials -2 %, a quarter of the first products -14 %, of the
+// second ones -7 %.
+// Measured (dQ + dK/dV): 16 heads of 128 on 4 kv heads, 8,192 tokens, block 128, a band and a
+// stride: 196 + 207 us, 1,050 TFLOP/s (0.55 of a cuBLAS bf16 product; 0.37 without the scores and
+// dP that the second walk computes again); 2 x 8 heads of 64, 2,999 tokens, block 64, a window and
+// a global block: 29 + 37 us; 2 x 2 heads, 333 tokens: 10 + 17 us, one CTA's way.  What counted, at the first: columns' steps shared by the CTAs (whole
+// columns: 510 and 230 us); packed fp32 arithmetic, masks only in the blocks that need them, dP's
+// buffer released once it is loaded (dQ 232 -> 192); cut columns joined by the last CTA there
+// rather than by a kernel of their own (15 to 30 us); three stages of queries and dP over the
+// scores' second half, so that the next scores run ahead (dK/dV 218 -> 209); at block 64 two
+// groups of warps in turn (41 -> 37).
 #pragma once
 
 #include <type_traits>
@@ -49,8 +66,8 @@ __device__ __forceinline__ int4 stream_place(const DiffBwdParams& p, int u, cons
 }
 
 // Row terms of 64 queries: two groups of 32, each [-lse_0, -lse_1 (log2 units), -D_0, -D_1, -lam]
-// of 32 fp32 (negated: they are added) and 16 bytes of room, so that the two half-warps, which read the same places of
-// different groups, hit different banks.
+// of 32 fp32 (negated: they are added) and 16 bytes of room, so that the two half-warps, which
+// read the same places of different groups, hit different banks.
 constexpr int kDiffVecHalf = 5 * 32 + 4;
 constexpr int kDiffVec = 2 * kDiffVecHalf;
 static_assert(kDiffVec == kDiffVecFloats, "workspace");

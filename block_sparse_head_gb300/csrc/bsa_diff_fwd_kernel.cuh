@@ -5,13 +5,25 @@
 // + r is query 16 w + r under map m, so that the two rows of a query sit 16 lanes apart in one
 // warp's TMEM lanes.  Everything up to the epilogue is the plain forward's pipeline at 128 query
 // rows (bsa_fwd_kernel.cuh: roles, barriers, S buffers, register split): warp 0 loads keys and
-// values, warp 3 queries, warp 1 issues S = Q K^T, warp 2 O += P V, softmax warps 4-7 hold the rows of map 0 and 8-11 those of
-// map 1 (each with its own running maximum and sum), and the epilogue warps read O out, divide
-// each row by its sum, exchange halves of the columns with the lane 16 away and store
-// O_0 - lam O_1 (and, for a training step, O_1, which the backward needs).
+// values, warp 3 queries, warp 1 issues S = Q K^T, warp 2 O += P V, softmax warps 4-7 hold the
+// rows of map 0 and 8-11 those of map 1 (each with its own running maximum and sum), and the
+// epilogue warps read O out, divide each row by its sum, exchange halves of the columns with the
+// lane 16 away and store O_0 - lam O_1 (and, for a training step, O_1, which the backward needs).
+//
+// P is rounded to bf16 for its product, as in the plain forward; maxima, sums, O and the
+// difference of the maps are fp32, and out is rounded once.
 //
 // Bound: as the plain forward the softmax warps' chain of TMEM loads, maxima and exponentials;
 // a step of 128 keys is 128 x 128 scores whichever map they belong to.
+// Measured: 16 heads of 128 on 4 kv heads, 16,384 tokens, block 128, a band and a stride: 281 us,
+// 1,275 TFLOP/s (0.67 of a cuBLAS bf16 product; the plain forward on 32 such heads takes 260);
+// 8,192 tokens 127 us; 8 heads of 64 twice, 2,999 tokens, block 64, a window and a global block:
+// 25 us; 4 heads of 64, 512 tokens: 10 us, an item's way.  In the first the tensor pipe works
+// half the time, the exponentials' unit a quarter, and one instruction fetch in six misses its
+// cache.  What counted: both maps in one tile rather than two passes over the keys; queries by a
+// warp of their own, an item ahead (306 us with the keys' warp); O released before the output's
+// stores, which are spaced out (316); masks tested once a warp (286); items dealt forwards and
+// backwards in turn (3 % against dealing forwards).
 #pragma once
 
 #include "bsa_diff.cuh"

@@ -9,7 +9,8 @@ namespace {
 
 // Per query: D_1 = sum dO O_1, D_0 = sum dO out + lam D_1 (out = O_0 - lam O_1), the two lse in
 // log2 units and lam, laid out as the kernels read them.  Bound: memory, 6 d bytes a query.
-// D / 8 lanes a row, 16-byte loads.
+// D / 8 lanes a row, 16-byte loads.  Measured: 16 heads of 128, 8,192 tokens 20 us, 5.0 TB/s; 2 x
+// 8 heads of 64, 2,999 tokens 5 us; 2 x 2 heads, 333 tokens 2.5 us, the launch.
 // Blocks behind the rows' write zeros: the counts, and the gradients of columns without an active
 // block, 256 columns a block.
 template <int D>

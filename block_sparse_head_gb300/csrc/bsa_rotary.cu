@@ -11,7 +11,11 @@
 //     walks the heads of q and k with it, so that sines and cosines stay in registers: 8 of them
 //     for all heads.  Few tokens: the heads are split over threads and CTAs, which then each
 //     work them out.
-//   * Loads of kRows heads are in flight at once.
+//   * Loads of kRows heads are in flight at once (2, 6 and 8 of them measured the same or worse),
+//     all reads and writes streaming, since no number is used twice (59 -> 58 us, 110 -> 109).
+// Measured: 32 + 8 heads of 128, 16,384 tokens 58 us, 5.8 TB/s (0.85 of a copy); 2 x 20,280 tokens
+// of 16 + 16 heads, adjacent pairs on three axes, 109 us, 6.1 TB/s; 64 packed tokens 3.8 us, the
+// launch and two dependent loads (a call takes the host four times that).
 #include <cmath>
 
 #include <cuda_bf16.h>

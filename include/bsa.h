@@ -718,8 +718,9 @@ int bsa_set_wait_limit(bsa_lut* lut, uint64_t ns);
  * their counterparts: 1 and 2 the producer's item and step slots free, 6 tiles landed,
  * 7 the elementwise warps' operands written (or the accumulators read out), 8 a TMEM
  * region free, 9 the elementwise warps waiting for a product, 12 an item's last
- * products done.  bsa_cache_forward with this LUT takes the knob as well and reports
- * in its own status word.  For few query rows (heads / kv_heads * max_q <= 16): 1 producer,
+ * products done; bsa_diff_forward and bsa_diff_backward use them for theirs.
+ * bsa_cache_forward and bsa_cache_diff_forward with this LUT take the knob as well and report
+ * in their own status word.  For few query rows (heads / kv_heads * max_q <= 16): 1 producer,
  * stage free; 2 values' copier, stage announced; 6 consumers, stage landed; 16 consumers,
  * joining a segment.  For more rows the knob ends one role at once (6 the issuer of the S
  * products, 7 of the PV products, 17 the look-ups; others have no effect), and the other roles'
