@@ -7,8 +7,8 @@
 // rows (bsa_fwd_kernel.cuh: roles, barriers, S buffers, register split): warp 0 loads keys and
 // values, warp 3 queries, warp 1 issues S = Q K^T, warp 2 O += P V, softmax warps 4-7 hold the
 // rows of map 0 and 8-11 those of map 1 (each with its own running maximum and sum), and the
-// epilogue warps read O out, divide each row by its sum, exchange halves of the columns with the
-// lane 16 away and store O_0 - lam O_1 (and, for a training step, O_1, which the backward needs).
+// epilogue warps read O out, half the columns of both of a query's rows a lane, divide them by
+// their sums and store O_0 - lam O_1 (and, for a training step, O_1, which the backward needs).
 //
 // P is rounded to bf16 for its product, as in the plain forward; maxima, sums, O and the
 // difference of the maps are fp32, and out is rounded once.
@@ -373,12 +373,12 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
                                               const WaitCtl& ctl) {
   using C = DiffFwdCfg<KB, D>;
   constexpr int G = C::kG;
-  constexpr int HC = D / 2;  // output columns of each of a query's two lanes
+  constexpr int HC = D / 2;  // output columns of each of a query's two lanes, 16 apart
   constexpr float kLn2 = 0.6931471805599453f;
   auto bar = [&](int i) { return sbase + C::kOffBar + 8 * i; };
   const int wq = (threadIdx.x >> 5) & 3;
   const int lane = threadIdx.x & 31;
-  const int map = lane >> 4;
+  const int half = lane >> 4;  // of the query's columns; and the map whose lse this lane stores
   const int qin = wq * 16 + (lane & 15);
   const uint32_t to = tmem + (static_cast<uint32_t>(wq * 32) << 16) + C::kOCol;
   const float2* stats = reinterpret_cast<const float2*>(smem + C::kOffStats);
@@ -417,35 +417,36 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
     const int q = is.cur.y * 64 + qin;
     const bool live = q < p.L;
     const int64_t pair = is.cur.x;
-    const int64_t orow = (pair * p.L + q) * D + map * HC;  // this lane's first output number
-    float* lse = p.lse + (2 * pair + map) * p.L + q;
+    const int64_t orow = (pair * p.L + q) * D + half * HC;  // this lane's first output number
+    float* lse = p.lse + (2 * pair + half) * p.L + q;
     if (nnz == 0) {
       if (live) {
-        const uint32_t zero[16] = {};
-#pragma unroll
-        for (int c = 0; c < HC / 32; ++c) {
-          store32(static_cast<__nv_bfloat16*>(p.out) + orow + 32 * c, zero, 0);
-          if (p.out2 != nullptr) store32(static_cast<__nv_bfloat16*>(p.out2) + orow + 32 * c, zero, 0);
+#pragma unroll 1
+        for (int c = 0; c < HC; c += 8) {
+          const uint4 zero = make_uint4(0, 0, 0, 0);
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + orow + c) = zero;
+          if (p.out2 != nullptr) *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out2) + orow + c) = zero;
         }
         *lse = -INFINITY;
       }
       continue;
     }
     float lam = 0.f;
-    if (live) lam = p.lam_rows ? p.lam[pair * p.L + q] : p.lam[pair % p.H];
+    if (live) lam = p.lam_rows ? p.lam[pair * p.L + q] : p.lam[static_cast<unsigned>(is.cur.x) % p.H];
     const int gl = g + (nnz + G - 1) / G - 1;  // the item's last step
     g = gl + 1;
     if (!wait_bar(C::kBarStFull, is.n & 1, kSiteEpiStats)) break;
-    const float2 ml = stats[wq * 32 + lane];
+    const float2 ml0 = stats[wq * 32 + (lane & 15)], ml1 = stats[wq * 32 + 16 + (lane & 15)];
+    const float2 ml = half ? ml1 : ml0;
     warp_arrive(C::kBarStFree);
     if (!wait_bar(C::kBarPVD + gl % 3, (gl / 3) & 1, kSiteSoftItemDone)) break;
-    const float inv = (ml.y > 0.f) ? 1.f / ml.y : 0.f;
+    const float inv0 = (ml0.y > 0.f) ? 1.f / ml0.y : 0.f, inv1 = (ml1.y > 0.f) ? 1.f / ml1.y : 0.f;
     uint32_t w[HC / 32][16], w2[HC / 32][16];
 #pragma unroll
     for (int c = 0; c < HC / 32; ++c) {
-      uint32_t r0[32], r1[32];  // of this lane's row: the columns that lanes 0-15 and 16-31 store
-      tmem_ld_32x32b_x32(to + 32 * c, r0);
-      tmem_ld_32x32b_x32(to + HC + 32 * c, r1);
+      uint32_t r0[32], r1[32];  // this lane's columns of its query's two rows
+      tmem_ld_16x32bx2_x32<HC>(to + 32 * c, r0);
+      tmem_ld_16x32bx2_x32<HC>(to + (16u << 16) + 32 * c, r1);
       tmem_ld_wait(r0);
       tmem_ld_wait(r1);
       if (c == HC / 32 - 1) warp_arrive(C::kBarOFree);  // O may be overwritten now
@@ -454,11 +455,8 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
         float o[2], o2[2];
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const float a = __uint_as_float(r0[2 * i + u]) * inv, b = __uint_as_float(r1[2 * i + u]) * inv;
-          const float got = __shfl_xor_sync(0xffffffffu, map ? a : b, 16);
-          const float first = map ? got : a, second = map ? b : got;
-          o[u] = fmaf(-lam, second, first);
-          o2[u] = second;
+          o2[u] = __uint_as_float(r1[2 * i + u]) * inv1;
+          o[u] = fmaf(-lam, o2[u], __uint_as_float(r0[2 * i + u]) * inv0);
         }
         w[c][i] = pack_bf16x2(o[0], o[1]);
         w2[c][i] = pack_bf16x2(o2[0], o2[1]);
