@@ -12,6 +12,14 @@
 
 namespace bsa {
 
+// u / by for u below 2^31, with mul = ceil(2^(31 + shift) / by) and 2^shift >= by: mul * by passes
+// 2^(31 + shift) by less than 2^shift, so that the product is off by less than 1 / by.  The roles
+// that walk the list divide two to four times an item or step; divisions proper were 11 KB of code in
+// the forward, where code is short of cache (bsa_diff_fwd_kernel.cuh).
+__device__ __forceinline__ unsigned diff_over(unsigned u, uint32_t mul, int shift) {
+  return __umulhi(2 * u, mul) >> shift;
+}
+
 // CTA c's u-th sub-item of the work list (descending cost): c, 2G - 1 - c, 2G + c, ... of the
 // list of items times pairs times halves, forwards and backwards in turn.
 __device__ __forceinline__ int2 stream_range(const DiffList& p) {
@@ -25,15 +33,17 @@ __device__ __forceinline__ unsigned diff_place(int u) {
   return u * grid + ((u & 1) ? grid - 1 - c : c);
 }
 __device__ __forceinline__ int4 stream_item(const DiffList& p, int u) {
-  return p.list[diff_place(u) / static_cast<unsigned>(p.pairs * p.halves)];
+  return p.list[diff_over(diff_place(u), p.each_mul, p.each_shift)];
 }
 // Sub-item u of this CTA as a record {b * H + h, first query / 64, first col_idx entry, nnz |
 // (dpos + 1) << 16}, from its item's.
 __device__ __forceinline__ int4 stream_place(const DiffList& p, int u, const int4& r) {
   if (r.w < 0) return r;  // the end
-  const unsigned rest = diff_place(u) % static_cast<unsigned>(p.pairs * p.halves);
-  const unsigned half = rest / p.pairs;
-  return make_int4(r.x * p.pairs + (rest - half * p.pairs), r.y * p.halves + half, r.z, r.w);
+  const unsigned at = diff_place(u), item = diff_over(at, p.each_mul, p.each_shift);
+  int pair = at - item * (p.pairs * p.halves);
+  const int half = pair >= p.pairs ? 1 : 0;
+  pair -= half * p.pairs;
+  return make_int4(r.x * p.pairs + pair, r.y * p.halves + half, r.z, r.w);
 }
 __device__ __forceinline__ int2 stream_range(const DiffFwdParams& p) {
   return stream_range(static_cast<const DiffList&>(p));

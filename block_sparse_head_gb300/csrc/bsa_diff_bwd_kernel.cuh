@@ -219,7 +219,7 @@ __device__ __forceinline__ void diff_dq_producer(const DiffBwdParams& p, const C
   int nx = 0, ny = 0;  // steps whose X (Y) copies were armed
   for (int t = 0; c.valid(); ++t) {
     const int nblk = c.nblk();
-    const int pair = c.is.cur.x, q0 = c.is.cur.y * 64, head = pair / p.pairs;
+    const int pair = c.is.cur.x, q0 = c.is.cur.y * 64, head = diff_over(pair, p.pairs_mul, p.pairs_shift);
     int cols[G];
 #pragma unroll
     for (int g = 0; g < G; ++g) cols[g] = (g < nblk) ? p.col_idx[c.is.cur.z + c.s * G + g] : 0;

@@ -15,12 +15,14 @@
 //
 // Bound: as the plain forward the softmax warps' chain of TMEM loads, maxima and exponentials;
 // a step of 128 keys is 128 x 128 scores whichever map they belong to.
-// Measured: 16 heads of 128 on 4 kv heads, 16,384 tokens, block 128, a band and a stride: 281 us,
-// 1,275 TFLOP/s (0.67 of a cuBLAS bf16 product; the plain forward on 32 such heads takes 260);
-// 8,192 tokens 127 us; 8 heads of 64 twice, 2,999 tokens, block 64, a window and a global block:
-// 25 us; 4 heads of 64, 512 tokens: 10 us, an item's way.  In the first the tensor pipe works
-// half the time, the exponentials' unit a quarter, and one instruction fetch in six misses its
-// cache.  What counted: both maps in one tile rather than two passes over the keys; queries by a
+// Measured: 16 heads of 128 on 4 kv heads, 16,384 tokens, block 128, a band and a stride: 260 us,
+// 1,375 TFLOP/s (0.72 of a cuBLAS bf16 product; the plain forward on 32 such heads takes 260);
+// 8,192 tokens 112 us; 8 heads of 64 twice, 2,999 tokens, block 64, a window and a global block:
+// 22 us; 4 heads of 64, 512 tokens: 7 us, an item's way.  The roles' loops together pass the
+// instruction cache, and the SMs of a GPC share the one behind it, which was busy 75 % of the time:
+// code that an item or a step runs counts twice.  Without it (an epilogue whose lanes read both
+// rows of a query instead of exchanging columns, in packed arithmetic, list places by products
+// instead of divisions, the queries' copies in a loop) 82 KB became 62 and 282 us 260.  What counted: both maps in one tile rather than two passes over the keys; queries by a
 // warp of their own, an item ahead (306 us with the keys' warp); O released before the output's
 // stores, which are spaced out (316); masks tested once a warp (286); items dealt forwards and
 // backwards in turn (3 % against dealing forwards).
@@ -60,7 +62,7 @@ __device__ __forceinline__ void diff_query_producer(const DiffFwdParams& p, cons
     if (n >= 2 && !mbar_wait_inl(bar(C::kBarQE + (n & 1)), ((n - 2) / 2) & 1, ctl, kSiteProdKEmpty)) break;
     const uint32_t fb = bar(C::kBarQF + (n & 1)), qd = sbase + C::kOffQ + (n & 1) * C::kQTile;
     mbar_arrive_expect_tx(fb, SPLIT ? C::kQTile / 2 : C::kQTile);
-#pragma unroll
+#pragma unroll 1
     for (int w = 0; w < 4; ++w)
 #pragma unroll
       for (int m = 0; m < 2; ++m)
@@ -103,7 +105,7 @@ __device__ __forceinline__ void diff_producer(const DiffFwdParams& p, const CUte
     r0.nblk = 0;
     if (c.valid()) {
       r0.nblk = c.nblk();
-      r0.head = c.is.cur.x / p.pairs;
+      r0.head = diff_over(c.is.cur.x, p.pairs_mul, p.pairs_shift);
 #pragma unroll
       for (int g = 0; g < G; ++g) r0.col[g] = colv[g];
       c.advance(p);
@@ -440,7 +442,9 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
     const float2 ml = half ? ml1 : ml0;
     warp_arrive(C::kBarStFree);
     if (!wait_bar(C::kBarPVD + gl % 3, (gl / 3) & 1, kSiteSoftItemDone)) break;
-    const float inv0 = (ml0.y > 0.f) ? 1.f / ml0.y : 0.f, inv1 = (ml1.y > 0.f) ? 1.f / ml1.y : 0.f;
+    auto twice = [](float x) { return f2_pack(x, x); };
+    const uint64_t inv0 = twice((ml0.y > 0.f) ? 1.f / ml0.y : 0.f), weight = twice(-lam);
+    const uint64_t inv1 = twice((ml1.y > 0.f) ? 1.f / ml1.y : 0.f);
     uint32_t w[HC / 32][16], w2[HC / 32][16];
 #pragma unroll
     for (int c = 0; c < HC / 32; ++c) {
@@ -452,14 +456,11 @@ __device__ __forceinline__ void diff_epilogue(const DiffFwdParams& p, uint32_t s
       if (c == HC / 32 - 1) warp_arrive(C::kBarOFree);  // O may be overwritten now
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        float o[2], o2[2];
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          o2[u] = __uint_as_float(r1[2 * i + u]) * inv1;
-          o[u] = fmaf(-lam, o2[u], __uint_as_float(r0[2 * i + u]) * inv0);
-        }
-        w[c][i] = pack_bf16x2(o[0], o[1]);
-        w2[c][i] = pack_bf16x2(o2[0], o2[1]);
+        const uint64_t a = f2_pack(__uint_as_float(r0[2 * i]), __uint_as_float(r0[2 * i + 1]));
+        const uint64_t b = f2_pack(__uint_as_float(r1[2 * i]), __uint_as_float(r1[2 * i + 1]));
+        const uint64_t o2 = f2_mul(b, inv1), o = f2_fma(o2, weight, f2_mul(a, inv0));
+        w[c][i] = pack_bf16x2(f2_lo(o), f2_hi(o));
+        w2[c][i] = pack_bf16x2(f2_lo(o2), f2_hi(o2));
       }
     }
     const unsigned gap = is.nx1.w < 0 ? 0 : C::kStoreGapNs;  // none behind the last item

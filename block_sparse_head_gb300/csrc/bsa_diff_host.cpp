@@ -46,6 +46,13 @@ void fill_list(bsa::DiffList& p, const bsa_lut* lut, int pairs, int block) {
   p.pairs = pairs;
   p.halves = block / 64;
   p.n = lut->n_items * pairs * p.halves;
+  auto over = [](int by, uint32_t& mul, int& shift) {
+    shift = 0;
+    while ((1ll << shift) < by) ++shift;
+    mul = static_cast<uint32_t>(((1ull << (31 + shift)) + by - 1) / by);
+  };
+  over(pairs * p.halves, p.each_mul, p.each_shift);
+  over(pairs, p.pairs_mul, p.pairs_shift);
 }
 
 template <class F64_64, class F64_128, class F128_64, class F128_128>

@@ -175,6 +175,9 @@ struct DiffList {
   int n;               // sub-items: n_items * pairs * halves
   int pairs;           // heads of a kv head
   int halves;          // block / 64
+  // Division by pairs * halves, and by pairs (diff_over).
+  uint32_t each_mul, pairs_mul;
+  int each_shift, pairs_shift;
 };
 
 struct DiffFwdParams : DiffList {
