@@ -38,17 +38,17 @@
 // each: no row terms -1 %, no exponentials -2 %, a quarter of the first products -14 %, of the
 // second ones -7 %.
 // Measured (dQ + dK/dV): 16 heads of 128 on 4 kv heads, 8,192 tokens, block 128, a band and a
-// stride: 196 + 207 us, 1,050 TFLOP/s (0.55 of a cuBLAS bf16 product; 0.37 without the scores and
-// dP that the second walk computes again); 2 x 8 heads of 64, 2,999 tokens, block 64, a window and
-// a global block: 29 + 37 us; 2 x 2 heads, 333 tokens: 10 + 17 us, one CTA's way.  What counted, at the first: columns' steps shared by the CTAs (whole
-// columns: 510 and 230 us); packed fp32 arithmetic, masks only in the blocks that need them, dP's
-// buffer released once it is loaded (dQ 232 -> 192); cut columns joined by the last CTA there
-// rather than by a kernel of their own (15 to 30 us); three stages of queries and dP over the
-// scores' second half, so that the next scores run ahead (dK/dV 218 -> 209); at block 64 two
-// groups of warps in turn (41 -> 37).
+// stride: 181 + 205 us, 1,100 TFLOP/s (0.58 of a cuBLAS bf16 product; 0.39 without the scores and
+// dP that the second walk computes again); 2 x 8 heads of 64, 2,999 tokens, block 64, a window
+// and a global block: 27 + 37 us; 2 x 2 heads, 333 tokens: 10 + 16 us, one CTA's way.  What
+// counted, at the first: columns' steps shared by the CTAs (whole columns: 510 and 230 us);
+// packed fp32 arithmetic, masks only in the blocks that need them, dP's buffer released once it
+// is loaded (dQ 232 -> 192); cut columns joined by the last CTA there rather than by a kernel of
+// their own (15 to 30 us); three stages of queries and dP over the scores' second half, so that
+// the next scores run ahead (dK/dV 218 -> 209); at block 64 two groups of warps in turn (41 ->
+// 37); masks as a pass of their own instead of a second copy of a step's code, which competes for
+// the instruction cache (dQ 196 -> 181, dK/dV 207 -> 205).
 #pragma once
-
-#include <type_traits>
 
 #include "bsa_bwd_kernel.cuh"
 #include "bsa_diff.cuh"
@@ -119,9 +119,7 @@ struct DiffBwdCfg {
   static constexpr int kBarAR = 23;    // accumulators read out (a step's warps)
   static constexpr int kBarIFV = 24;   // dK/dV: item tile B landed
   static constexpr int kBarIEV = 25;   // dK/dV: item tile B free
-  static constexpr int kBarDrain = 26, kBarDrain2 = 27;
-  static constexpr int kBarQI = 28;    // dQ: a step's E taken by the second issuer
-  static constexpr int kNumBars = 29;
+  static constexpr int kBarDrain = 26, kBarDrain2 = 27, kNumBars = 28;
   static constexpr int kBarBytes = 256;
   static_assert(kNumBars * 8 + 8 <= kBarBytes && kOffBar % 8 == 0 && kOffVec % 16 == 0, "barrier area");
   static constexpr int kSmemBytes = kOffBar + kBarBytes + 1024;
@@ -230,7 +228,7 @@ __device__ __forceinline__ void diff_dq_producer(const DiffBwdParams& p, const C
       mbar_arrive_expect_tx(fb, (SPLIT ? C::kItemTile / 2 : C::kItemTile) + C::kItemTile);
       ++n;
       diff_load_q<D, SPLIT>(sbase + C::kOffA, tm_q, fb, q0, pair);
-#pragma unroll
+#pragma unroll 1
       for (int a = 0; a < 2; ++a)
 #pragma unroll
         for (int m = 0; m < 2; ++m)
@@ -277,9 +275,13 @@ __device__ __forceinline__ void diff_kv_producer(const DiffBwdParams& p, const C
   const int tiles = (p.L + 63) / 64;
   int n = -1, t = 0;  // pieces whose A was armed; steps armed
   int nv = 0;         // pieces whose B was armed
+  int head = 0, key0 = 0;
   for (; c.valid(); ++t) {
-    const int kv = c.col / p.nb, head = c.b * (p.cols / p.nb) + kv;
-    const int key0 = (c.col - kv * p.nb) * BLK;
+    if (c.first) {
+      const int kv = c.col / p.nb;
+      head = c.b * (p.cols / p.nb) + kv;
+      key0 = (c.col - kv * p.nb) * BLK;
+    }
     const int pair = head * p.pairs + c.rest / C::kHalves;
     const int q64 = p.row_idx[c.x] * C::kHalves + c.rest % C::kHalves;
     const bool item_first = c.first;
@@ -404,7 +406,6 @@ __device__ __forceinline__ void diff_dq_mma2(const DiffBwdParams& p, uint32_t sb
     c.advance(p);
     if (first) ++n;
     if (!mbar_wait(bar(C::kBarEF + (u & 1)), (u / 2) & 1, ctl, kSiteMmaPFull)) break;
-    mbar_arrive(bar(C::kBarQI));
     if (first && n > 0 && !mbar_wait(bar(C::kBarAR), (n - 1) & 1, ctl, kSiteMmaPFull)) break;
     tc_fence_after();
     const uint32_t te = tmem + ((u & 1) ? C::kT1b : C::kT1), xs = x0 + (u % 3) * (C::kXTile >> 4);
@@ -634,7 +635,8 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       store_lam(pair, is.cur.y, 0.f);
       continue;
     }
-    const float* v = p.vec + (static_cast<int64_t>(pair) * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + (qin & 31);
+    float* v = p.vec + (static_cast<int64_t>(pair) * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf +
+               (qin & 31);
     // dS = P (w dP - w D) with the row's weight w
     const float w = map ? v[128] : 1.f, wd = w * v[64 + 32 * map];
     const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2), l2 = f2_pack(v[32 * map], v[32 * map]);
@@ -663,53 +665,45 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp));
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp + 32));
       warp_arrive(C::kBarDL);  // T2 may now take the next step's dP
-      // Keys behind the query in the diagonal block, and a block that is not there, are masked
-      // (after scaling, so that a negative scale cannot turn -inf into +inf).
+      // Keys behind the query in the diagonal block, and a block that is not there, are masked: after
+      // the exponentials, so that the steps without a mask run no second copy of the code.
       const int hi = valid ? (diag ? qblk - kbase : 63) : -1;
-      uint32_t pk1[32];
-      uint64_t sums[2] = {0ull, 0ull};
-      auto form = [&](auto masked) {
-#pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          const uint64_t y = f2_fma(f2_pack(__uint_as_float(rs[2 * i]), __uint_as_float(rs[2 * i + 1])), c2, l2);
-          float y0 = f2_lo(y), y1 = f2_hi(y);
-          float d0 = __uint_as_float(rp[2 * i]), d1 = __uint_as_float(rp[2 * i + 1]);
-          if constexpr (decltype(masked)::value) {
-            y0 = mask_gt(y0, 2 * i, hi);
-            y1 = mask_gt(y1, 2 * i + 1, hi);
-            d0 = 2 * i > hi ? 0.f : d0;
-            d1 = 2 * i + 1 > hi ? 0.f : d1;
-          }
-          const uint64_t pe = f2_pack(ex2_approx(y0), ex2_approx(y1)), dp = f2_pack(d0, d1);
-          sums[i & 1] = f2_fma(pe, dp, sums[i & 1]);
-          const uint64_t ds = f2_mul(pe, f2_fma(dp, w2, wd2));
-          pk1[i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
-        }
+      auto pair_of = [](const uint32_t (&r)[64], int i) {
+        return f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
       };
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {  // P, over the scores
+        const uint64_t y = f2_fma(pair_of(rs, i), c2, l2);
+        rs[2 * i] = __float_as_uint(ex2_approx(f2_lo(y)));
+        rs[2 * i + 1] = __float_as_uint(ex2_approx(f2_hi(y)));
+      }
+      if (__any_sync(0xffffffffu, hi < 63)) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c) {
+          rs[c] = c > hi ? 0u : rs[c];
+          rp[c] = c > hi ? 0u : rp[c];
+        }
+      }
+      uint64_t sums[4] = {0ull, 0ull, 0ull, 0ull};
+#pragma unroll
+      for (int i = 0; i < 32; ++i) sums[i & 3] = f2_fma(pair_of(rs, i), pair_of(rp, i), sums[i & 3]);
+      sums[0] = f2_add(f2_add(sums[0], sums[1]), f2_add(sums[2], sums[3]));
+      const float part = f2_lo(sums[0]) + f2_hi(sums[0]);
+      rsum += part;
       if (nsteps == 1) {
         // All of the row is here: D from P dP itself instead of from the rounded outputs, whose
         // error is largest in rows of few keys.
-        float all = 0.f;
-#pragma unroll
-        for (int c = 0; c < 64; ++c)
-          if (c <= hi) all = fmaf(ex2_approx(fmaf(__uint_as_float(rs[c]), p.scale_log2, f2_lo(l2))), __uint_as_float(rp[c]), all);
-        all += __shfl_xor_sync(0xffffffffu, all, 16);
-        wd2 = f2_pack(-w * all, -w * all);
+        const float all = -w * (part + __shfl_xor_sync(0xffffffffu, part, 16));
+        wd2 = f2_pack(all, all);
       }
-      if (__any_sync(0xffffffffu, hi < 63))
-        form(std::true_type{});
-      else
-        form(std::false_type{});
-      sums[0] = f2_add(sums[0], sums[1]);
-      rsum += f2_lo(sums[0]) + f2_hi(sums[0]);
+      uint32_t pk1[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        const uint64_t ds = f2_mul(pair_of(rs, i), f2_fma(pair_of(rp, i), w2, wd2));
+        pk1[i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
+      }
       tmem_st_16x32bx2_x32<32>(t1, pk1);
       tmem_st_wait();
-      // The second issuer has taken the previous step's E.  Nothing depends on this wait; without it
-      // the walk is 1 to 3 % slower (8,192 tokens: 199 us, 197 with it).
-      if (g >= 1 && !wait_bar(C::kBarQI, (g - 1) & 1, kSiteSoftSFull)) {
-        ok = false;
-        break;
-      }
       warp_arrive(C::kBarEF + (g & 1));
       if (s == 0 && pending && !read_pending()) {
         ok = false;
@@ -720,8 +714,7 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     rsum += __shfl_xor_sync(0xffffffffu, rsum, 16);
     store_lam(pair, is.cur.y, -rsum);
     // For the dK/dV walk, which comes after this one.
-    if (half == 0)
-      p.vec[(static_cast<int64_t>(pair) * tiles + is.cur.y) * kDiffVec + (qin >> 5) * kDiffVecHalf + 64 + 32 * map + (qin & 31)] = -rsum;
+    if (half == 0) v[64 + 32 * map] = -rsum;
     pending = true;
     ppair = pair;
     pq = q;
@@ -757,6 +750,9 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     return w;
   };
 
+  auto pair_of = [](const uint32_t (&r)[32], int i) {
+    return f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
+  };
   const uint64_t c2 = f2_pack(p.scale_log2, p.scale_log2);
   DiffKvWalk c;
   c.init(p);
@@ -783,32 +779,31 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
     // formed.  The second map's P is kept with its weight -lam.
     {
       uint32_t pk[16];
-      auto form = [&](auto masked) {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float4 l0 = vec[i >> 1], l1 = vec[8 + (i >> 1)], lm = vec[32 + (i >> 1)];
+        auto two = [&](const float4& f) { return i & 1 ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y); };
+        const uint64_t y0 = f2_fma(pair_of(rs[0], i), c2, two(l0)), y1 = f2_fma(pair_of(rs[1], i), c2, two(l1));
+        const uint64_t p1 = f2_mul(f2_pack(ex2_approx(f2_lo(y1)), ex2_approx(f2_hi(y1))), two(lm));
+        const uint64_t p0 = f2_pack(ex2_approx(f2_lo(y0)), ex2_approx(f2_hi(y0)));
+        rs[0][2 * i] = __float_as_uint(f2_lo(p0));
+        rs[0][2 * i + 1] = __float_as_uint(f2_hi(p0));
+        rs[1][2 * i] = __float_as_uint(f2_lo(p1));
+        rs[1][2 * i + 1] = __float_as_uint(f2_hi(p1));
+        const uint64_t w = f2_add(p0, p1);
+        pk[i] = pack_bf16x2(f2_lo(w), f2_hi(w));
+      }
+      if (c.x - c.begin == dpos) {
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+#pragma unroll
+          for (int i = 0; i < 32; ++i) rs[m][i] = i < lo ? 0u : rs[m][i];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          const float4 l0 = vec[i >> 1], l1 = vec[8 + (i >> 1)], lm = vec[32 + (i >> 1)];
-          auto two = [&](const float4& f) { return i & 1 ? f2_pack(f.z, f.w) : f2_pack(f.x, f.y); };
-          const uint64_t y0 = f2_fma(f2_pack(__uint_as_float(rs[0][2 * i]), __uint_as_float(rs[0][2 * i + 1])), c2, two(l0));
-          const uint64_t y1 = f2_fma(f2_pack(__uint_as_float(rs[1][2 * i]), __uint_as_float(rs[1][2 * i + 1])), c2, two(l1));
-          float a[4] = {f2_lo(y0), f2_hi(y0), f2_lo(y1), f2_hi(y1)};
-          if constexpr (decltype(masked)::value) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) a[u] = mask_outside(a[u], 2 * i + (u & 1), lo, 1 << 30);
-          }
-          const uint64_t p0 = f2_pack(ex2_approx(a[0]), ex2_approx(a[1]));
-          const uint64_t p1 = f2_mul(f2_pack(ex2_approx(a[2]), ex2_approx(a[3])), two(lm));
-          rs[0][2 * i] = __float_as_uint(f2_lo(p0));
-          rs[0][2 * i + 1] = __float_as_uint(f2_hi(p0));
-          rs[1][2 * i] = __float_as_uint(f2_lo(p1));
-          rs[1][2 * i + 1] = __float_as_uint(f2_hi(p1));
-          const uint64_t w = f2_add(p0, p1);
+          const uint64_t w = f2_add(pair_of(rs[0], i), pair_of(rs[1], i));
           pk[i] = pack_bf16x2(f2_lo(w), f2_hi(w));
         }
-      };
-      if (c.x - c.begin == dpos)
-        form(std::true_type{});
-      else
-        form(std::false_type{});
+      }
       tmem_st_16x32bx2_x16<16>(t1, pk);
     }
     tmem_st_wait();
@@ -824,9 +819,8 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
           const float4 dd = vec[16 + 8 * m + (i >> 1)];
-          const uint64_t t = f2_add(f2_pack(__uint_as_float(rp[2 * i]), __uint_as_float(rp[2 * i + 1])),
-                                    i & 1 ? f2_pack(dd.z, dd.w) : f2_pack(dd.x, dd.y));
-          const uint64_t ds = f2_mul(f2_pack(__uint_as_float(rs[m][2 * i]), __uint_as_float(rs[m][2 * i + 1])), t);
+          const uint64_t t = f2_add(pair_of(rp, i), i & 1 ? f2_pack(dd.z, dd.w) : f2_pack(dd.x, dd.y));
+          const uint64_t ds = f2_mul(pair_of(rs[m], i), t);
           pk[16 * m + i] = pack_bf16x2(f2_lo(ds), f2_hi(ds));
         }
       tmem_st_16x32bx2_x32<32>(t1 + 64, pk);
