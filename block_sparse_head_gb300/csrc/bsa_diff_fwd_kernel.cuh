@@ -342,7 +342,7 @@ __device__ __forceinline__ void diff_softmax(const DiffFwdParams& p, uint32_t sb
       if (s > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         ok = wait_bar(C::kBarPVD + (g - 1) % 3, ((g - 1) / 3) & 1, kSiteSoftPvDone);
         if (!ok) break;
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t r[32];
           load_o32(to, c, r);

