@@ -434,7 +434,6 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
   const int rows = s.nq * p.group;
   int64_t row[N];  // of the output
   float top[N], z[N], o[N][E] = {};
-  float lam[DIFF ? N / 2 : 1];  // read ahead of the pieces
   static_assert(!DIFF || N % 2 == 0, "pairs of rows");
   auto place = [&](int j) { return DIFF ? r0 + (j >> 1) * step + (j & 1) : r0 + j * step; };
   auto row_of = [&](int j) { return min(place(j), rows - 1); };
@@ -448,7 +447,6 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
     row[j] = static_cast<int64_t>(s.q0 + qi) * p.Hq + head;
     z[j] = p.sinks != nullptr ? p.sinks[head] * kLog2e : -INFINITY;
     top[j] = z[j];
-    if constexpr (DIFF) lam[j >> 1] = diff_lam(p, row[j] >> 1, head >> 1);
   }
 #pragma unroll 1
   for (int i = lane; i <= more; i += 32)
@@ -493,7 +491,8 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
       if ((j & 1) == 0) continue;
       const int64_t orow = row[j] >> 1;  // Hq is even
       uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<A*>(p.out) + orow * D + lane * E);
-      const float w = -lam[j >> 1];
+      // Read here: kept from the start it cost the tile kernel 5 % in registers.
+      const float w = -diff_lam(p, orow, static_cast<int>(orow % (p.Hq >> 1)));
 #pragma unroll
       for (int i = 0; i < E / 2; ++i)
         dst[i] = float2_to_act<A>(fmaf(w, o[j][2 * i], o[j - 1][2 * i]),
