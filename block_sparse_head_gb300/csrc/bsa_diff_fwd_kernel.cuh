@@ -15,18 +15,19 @@
 //
 // Bound: as the plain forward the softmax warps' chain of TMEM loads, maxima and exponentials;
 // a step of 128 keys is 128 x 128 scores whichever map they belong to.
-// Measured: 16 heads of 128 on 4 kv heads, 16,384 tokens, block 128, a band and a stride: 260 us,
-// 1,375 TFLOP/s (0.72 of a cuBLAS bf16 product; the plain forward on 32 such heads takes 260);
-// 8,192 tokens 112 us; 8 heads of 64 twice, 2,999 tokens, block 64, a window and a global block:
-// 22 us; 4 heads of 64, 512 tokens: 7 us, an item's way.  The roles' loops together pass the
-// instruction cache, and the SMs of a GPC share the one behind it, which was busy 75 % of the
-// time: code that an item or a step runs counts twice.  Without it (an epilogue whose lanes read
-// both rows of a query instead of exchanging columns, in packed arithmetic, list places by
-// products instead of divisions, the queries' copies in a loop) 82 KB became 62 and 282 us 260.
+// Measured: 16 heads of 128 on 4 kv heads, 16,384 tokens, block 128, a band and a stride: 255 us,
+// 1,400 TFLOP/s (0.74 of a cuBLAS bf16 product; the plain forward on 32 such heads takes 255 too);
+// 8,192 tokens 109 us; 2 x 8 heads of 64, 2,999 tokens, block 64, a window and a global block: 21
+// us; 4 heads of 64, 512 tokens: 6.6 us, an item's way.  The tensor pipe works 59 % of the time,
+// the exponentials' unit 30 %.
 // What counted: both maps in one tile rather than two passes over the keys; queries by a warp of
 // their own, an item ahead (306 us with the keys' warp); O released before the output's stores,
 // which are spaced out (316); masks tested once a warp (286); items dealt forwards and backwards
-// in turn (3 % against dealing forwards).
+// in turn (3 % against dealing forwards).  And the size of the code: the roles' loops together
+// passed the instruction cache, and the SMs of a GPC share the one behind it, which was busy 75 %
+// of the time.  An epilogue whose lanes read both rows of a query instead of exchanging columns,
+// in packed arithmetic, list places by products instead of divisions, the queries' copies in a
+// loop and waits of one loop made 59 KB of 82, and 255 us of 282.
 #pragma once
 
 #include "bsa_diff.cuh"
