@@ -28,7 +28,7 @@
 // Queries of d / 2 numbers are laid out over d columns, zero in the other map's half
 // (bsa_diff.cuh): E2 X then puts each map's dK into its own columns.
 // Rows past the end of the sequence read as zero and carry -lse = -inf, so that their P is 0;
-// keys past it have K = V = 0 and are not stored.
+// keys past it have K = V = 0: the dQ walk masks them, the dK/dV walk does not store them.
 // P, dS and their combinations are rounded to bf16 for their products; scores, dP, D, the sums
 // over keys, rows, maps and heads and dlam's sum are fp32 or more, and each gradient is rounded
 // once.  Every wait is bounded (WaitCtl), as in the plain kernels.
@@ -38,7 +38,7 @@
 // each: no row terms -1 %, no exponentials -2 %, a quarter of the first products -14 %, of the
 // second ones -7 %.
 // Measured (dQ + dK/dV): 16 heads of 128 on 4 kv heads, 8,192 tokens, block 128, a band and a
-// stride: 181 + 205 us, 1,100 TFLOP/s (0.58 of a cuBLAS bf16 product; 0.39 without the scores and
+// stride: 185 + 205 us, 1,090 TFLOP/s (0.58 of a cuBLAS bf16 product; 0.39 without the scores and
 // dP that the second walk computes again); 2 x 8 heads of 64, 2,999 tokens, block 64, a window
 // and a global block: 27 + 37 us; 2 x 2 heads, 333 tokens: 10 + 16 us, one CTA's way.  What
 // counted, at the first: columns' steps shared by the CTAs (whole columns: 510 and 230 us);
@@ -47,7 +47,8 @@
 // their own (15 to 30 us); three stages of queries and dP over the scores' second half, so that
 // the next scores run ahead (dK/dV 218 -> 209); at block 64 two groups of warps in turn (41 ->
 // 37); masks as a pass of their own instead of a second copy of a step's code, which competes for
-// the instruction cache (dQ 196 -> 181, dK/dV 207 -> 205).
+// the instruction cache (dQ 196 -> 181, dK/dV 207 -> 205); the
+// end of the sequence masked in the dQ walk costs 4 us of these (dQ 185).
 #pragma once
 
 #include "bsa_bwd_kernel.cuh"
@@ -643,13 +644,16 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
     const uint64_t w2 = f2_pack(w, w);
     uint64_t wd2 = f2_pack(wd, wd);
     const int dpos = p.causal_diag ? is.dpos() : -1;
+    // Does the end of the sequence cut the last block?  Keys behind the end score 0, and exp(0 - lse)
+    // may be more than fp32 holds.
+    const bool cut = p.L % BLK != 0 && p.col_idx[is.cur.z + cnt - 1] == p.L / BLK;
     const int qblk = qin + (BLK == 128 ? (is.cur.y & 1) * 64 : 0);
     const int nsteps = (cnt + G - 1) / G;
     float rsum = 0.f;  // of P dP
     for (int s = 0; s < nsteps; ++s, ++g) {
       const int nblk = step_blocks<G>(cnt, s);
       const bool valid = (BLK == 128) || (half < nblk);
-      const bool diag = valid && (((BLK == 128) ? s : s * 2 + half) == dpos);
+      const int place = (BLK == 128) ? s : s * 2 + half;
       if (!wait_bar(C::kBarTF + (g & 1), (g / 2) & 1, kSiteSoftSFull)) {
         ok = false;
         break;
@@ -665,9 +669,11 @@ __device__ __forceinline__ void diff_dq_elementwise(const DiffBwdParams& p, uint
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp));
       tmem_ld_wait(*reinterpret_cast<uint32_t(*)[32]>(rp + 32));
       warp_arrive(C::kBarDL);  // T2 may now take the next step's dP
-      // Keys behind the query in the diagonal block, and a block that is not there, are masked: after
-      // the exponentials, so that the steps without a mask run no second copy of the code.
-      const int hi = valid ? (diag ? qblk - kbase : 63) : -1;
+      // Keys behind the query in the diagonal block or behind the end, and a block that is not there,
+      // are masked: after the exponentials, so that the steps without a mask run no second copy of
+      // the code.
+      int hi = valid ? (place == dpos ? qblk - kbase : 63) : -1;
+      if (cut && place == cnt - 1) hi = min(hi, (p.L - 1) % BLK - kbase);
       auto pair_of = [](const uint32_t (&r)[64], int i) {
         return f2_pack(__uint_as_float(r[2 * i]), __uint_as_float(r[2 * i + 1]));
       };

@@ -105,6 +105,17 @@ def test_scales_and_a_growing_maximum(scale):
     _check(q, k, v, lam, do, torch.tril(torch.ones(1, 9, 9, dtype=torch.int32)), scale, block, True)
 
 
+@pytest.mark.parametrize("block,d,dq", KINDS)
+@pytest.mark.parametrize("L", [100, 200])
+def test_scores_far_below_zero(block, d, dq, L):
+    """Every score near -130, the last block cut by the sequence's end and seen by all rows: places
+    behind the end score 0 there, and exp(0 - lse) is more than fp32 holds."""
+    nb = -(-L // block)
+    q, k, v, lam, do = _inputs(1, 2, 1, L, d, dq, True, 94 + L + block + d + dq)
+    q, k = (0.05 * q.float() - 1.0).to(torch.bfloat16), (0.05 * k.float() + 1.0).to(torch.bfloat16)
+    _check(q, k, v, lam, do, torch.ones(1, nb, nb, dtype=torch.int32), 130.0 / dq, block, False)
+
+
 def test_many_items_a_cta():
     """More work items than SMs in every walk, so that CTAs change items several times."""
     q, k, v, lam, do = _inputs(2, 8, 4, 1600, 64, 64, True, 72)
