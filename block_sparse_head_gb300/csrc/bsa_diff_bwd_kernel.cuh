@@ -47,8 +47,8 @@
 // their own (15 to 30 us); three stages of queries and dP over the scores' second half, so that
 // the next scores run ahead (dK/dV 218 -> 209); at block 64 two groups of warps in turn (41 ->
 // 37); masks as a pass of their own instead of a second copy of a step's code, which competes for
-// the instruction cache (dQ 196 -> 181, dK/dV 207 -> 205); the
-// end of the sequence masked in the dQ walk costs 4 us of these (dQ 185).
+// the instruction cache (dQ 196 -> 181, dK/dV 207 -> 205); the end of the sequence masked in the
+// dQ walk costs 4 us of these (dQ 185).
 #pragma once
 
 #include "bsa_bwd_kernel.cuh"
