@@ -973,6 +973,7 @@ __global__ void __launch_bounds__(DiffBwdCfg<BLK, D, KV>::kThreads, 1)
     tma_prefetch_desc(&tm_y);
   }
   if (warp == 1) {
+    wait_before();  // TMEM is not held across it (launch_after)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }

@@ -520,6 +520,7 @@ __global__ void __launch_bounds__(DiffFwdCfg<KB, D>::kThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   if (warp == 1) {
+    wait_before();  // TMEM is not held across it (launch_after)
     tmem_alloc(smem_u32(tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }

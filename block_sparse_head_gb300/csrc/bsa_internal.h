@@ -264,9 +264,13 @@ __device__ __forceinline__ int diff_column(const DiffBwdParams& p, int x) {
 // (launch_after); every thread that reads what they wrote, before it does.
 __device__ __forceinline__ void wait_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 // Launches a kernel that calls wait_before in every thread, so that its launch overlaps the end of
-// the kernel before it (a backward of 2,999 tokens in four kernels: 90 -> 81 us).  None of them lets
-// the next one begin early (griddepcontrol.launch_dependents): with an SM's whole shared memory each
-// they could only take turns, and long ones lost 3 %.
+// the kernel before it (measured on a backward of 2,999 tokens that had a fourth kernel: 90 -> 81
+// us).  None of them lets the next one begin early (griddepcontrol.launch_dependents): with an SM's
+// whole shared memory each they could only take turns, and long ones lost 3 %.
+// The kernel before may be anyone's, and may have let this one begin while its own blocks have yet
+// to allocate their TMEM: a block that held TMEM across wait_before, which has no limit, would wait
+// for one that waits for the TMEM.  So the allocating warp calls wait_before first; barriers,
+// descriptors and shared memory are set up before it.
 template <class... P, class... A>
 cudaError_t launch_after(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, A&&... args) {
   cudaLaunchAttribute attr{};
