@@ -902,9 +902,7 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
                            pack_bf16x2(x[2 * u + 1].x * f, x[2 * u + 1].y * f),
                            pack_bf16x2(x[2 * u + 1].z * f, x[2 * u + 1].w * f));
         };
-        int there = 0;
-        if (lane == 0) there = load_acquire(count);
-        const bool late = __shfl_sync(0xffffffffu, there, 0) == end - root;
+        const bool late = warp_load_acquire(count, lane) == end - root;
 #pragma unroll 1
         for (int i = 0; i < D / 32; ++i) {
           uint32_t r[32];
@@ -921,15 +919,9 @@ __device__ __forceinline__ void diff_kv_elementwise(const DiffBwdParams& p, uint
                                        __uint_as_float(r[4 * u + 2]), __uint_as_float(r[4 * u + 3]));
           }
         }
-        if (!late) {
-          __threadfence();
-          __syncwarp();
-          if (lane == 0) there = add_acq_rel(count, 1);
-          if (__shfl_sync(0xffffffffu, there, 0) == end - root) {
-            __threadfence();
+        if (!late && warp_add_acq_rel(count, 1, lane) == end - root) {
 #pragma unroll 1
-            for (int i = 0; i < D / 32; ++i) sum_pieces(i, nullptr);
-          }
+          for (int i = 0; i < D / 32; ++i) sum_pieces(i, nullptr);
         }
       }
     }

@@ -263,6 +263,21 @@ __device__ __forceinline__ int add_acq_rel(int* p, int x) {
   asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;" : "=r"(r) : "l"(p), "r"(x) : "memory");
   return r;
 }
+// The two for a whole warp: its earlier writes are announced, and all its lanes see what lane 0 is
+// told of.  The warp barriers carry the order between lane 0 and the others; a shuffle would not.
+__device__ __forceinline__ int warp_load_acquire(const int* p, int lane) {
+  int r = 0;
+  if (lane == 0) r = load_acquire(p);
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, r, 0);
+}
+__device__ __forceinline__ int warp_add_acq_rel(int* p, int x, int lane) {
+  int r = 0;
+  __syncwarp();
+  if (lane == 0) r = add_acq_rel(p, x);
+  __syncwarp();
+  return __shfl_sync(0xffffffffu, r, 0);
+}
 
 // ------------------------------------------------------------------- tcgen05
 

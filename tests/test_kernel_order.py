@@ -45,3 +45,18 @@ def test_no_tmem_is_held_across_the_wait_for_the_kernel_before():
                 warp = body[body.rindex("if (warp ==", 0, body.index("tmem_alloc(")):]
                 assert "wait_before();" in _body(warp, 0)
     assert kernels == 2  # the differential forward and backward
+
+
+def test_a_warp_learns_of_other_blocks_writes_behind_a_barrier():
+    """One lane's acquire orders the other lanes' loads only through a barrier between them: whoever
+    asks a count for a warp uses the wrappers that have it, or a barrier of the block."""
+    text = _sources()
+    ptx = text["bsa_ptx.cuh"]
+    for name, asked in (("warp_load_acquire", "load_acquire("), ("warp_add_acq_rel", "add_acq_rel(")):
+        body = _body(ptx, ptx.index(f"int {name}("))
+        ask, tell = body.index(asked), body.index("__shfl_sync")
+        assert "__syncwarp();" in body[ask:tell], name
+        if name == "warp_add_acq_rel":  # the other lanes' writes before lane 0 announces them
+            assert "__syncwarp();" in body[:ask]
+    for call in re.findall(r"\w*(?:load_acquire|add_acq_rel)\(", text["bsa_diff_bwd_kernel.cuh"]):
+        assert call.startswith("warp_"), call
