@@ -2,11 +2,11 @@
 // by (position on the pair's axis) x (the pair's frequency).  See include/bsa.h.
 //
 // Bound: memory, each number read and written once.
-//   * The angle: the table holds frequencies in turns per position as 64-bit binary fractions, so
-//     that the 64-bit product with an integer position, which wraps at whole turns, is the angle
-//     exactly, however far the position; its top 32 bits give sincospif's argument to 2^-32 turns.
-//     (An fp32 product would be off by 2^-24 of the angle: at position 2^20 all of a radian's
-//     fourth digit.)
+//   * The angle: the table holds frequencies in turns per position as 64-bit binary fractions, each
+//     within 2^-64 turns, and the 64-bit product with an integer position, which wraps at whole
+//     turns, adds nothing to that: at position 2^31 it is within 2^-33 turns of the angle.  Its top
+//     32 bits are rounded to fp32 for sincospif, by 2^-25 half-turns at most: 1e-7 radians in all.  (An fp32 product would be off by 2^-24 of the angle: at position 2^20 all of a
+//     radian's fourth digit.)
 //   * A thread keeps one token and one piece of its row (8 numbers, or 8 and their partners) and
 //     walks the heads of q and k with it, so that sines and cosines stay in registers: 8 of them
 //     for all heads.  Few tokens: the heads are split over threads and CTAs, which then each
@@ -206,12 +206,19 @@ int bsa_rotary_table(const double* inv_freq, const int32_t* axis, int pairs, bsa
     if (!std::isfinite(inv_freq[i]) || std::fabs(inv_freq[i]) > 1e6) return BSA_ERR_UNSUPPORTED;
     if (axis != nullptr && (axis[i] < 0 || axis[i] > 7)) return BSA_ERR_SHAPE;
   }
+  // 2 pi to 2^-106 of its size, as a sum of two doubles.
+  constexpr double kTwoPi = 6.283185307179586, kTwoPiLow = 2.4492935982947064e-16;
   for (int i = 0; i < pairs; ++i) {
-    // Turns per position, to [-1/2, 1/2], as a 64-bit fraction (1/2 and -1/2 are the same).
-    const double turns = inv_freq[i] / 6.283185307179586;
+    // Turns per position as a 64-bit fraction, which wraps at whole turns.  The quotient comes in two
+    // doubles too, the second from the remainder that a fused multiply-add leaves exact (Dekker): one
+    // alone is off by 2^-54 of up to 160,000 turns, which 2^31 positions make 0.1 radians.  The first
+    // one's part behind whole turns, in [-1/2, 1/2], is exact; 2^64 takes 1/2 no more (-1/2 is the same).
+    const double turns = inv_freq[i] / kTwoPi;
+    const double more = std::fma(-turns, kTwoPiLow, std::fma(-turns, kTwoPi, inv_freq[i])) / kTwoPi;
     double f = turns - std::nearbyint(turns);
     if (f >= 0.5) f -= 1.0;
-    table[i].turns = static_cast<uint64_t>(static_cast<int64_t>(std::ldexp(f, 63))) << 1;
+    table[i].turns = static_cast<uint64_t>(std::llrint(std::ldexp(f, 64))) +
+                     static_cast<uint64_t>(std::llrint(std::ldexp(more, 64)));
     table[i].axis = axis == nullptr ? 0 : axis[i];
     table[i].reserved = 0;
   }

@@ -611,12 +611,13 @@ int bsa_cache_workspace(int heads, int kv_heads, int d, int max_q, int64_t* byte
  *   (x, y) -> (x cos angle - y sin angle, x sin angle + y cos angle)
  *
  * and with `inverse` by -angle, which is also the gradient of the turn.  Numbers behind the last
- * pair (2 * pairs < d) are copied.  Angles are exact before their sine and cosine are taken in
- * fp32, for any 32-bit position; results are rounded once.
+ * pair (2 * pairs < d) are copied.  Sine and cosine are taken in fp32 of an angle that is within
+ * 1e-7 radians, for any frequency that a table may have and any 32-bit position; results are rounded
+ * once.
  */
 
 /* One pair of a table: its frequency in turns per position, a 64-bit binary fraction (two's
- * complement), and its axis. */
+ * complement; within 2^-64 where bsa_rotary_table makes it), and its axis. */
 typedef struct bsa_rotary_pair {
   uint64_t turns;
   int32_t axis;

@@ -5,6 +5,7 @@ and the sine and cosine are good to 2^-22, so a result is off by at most 5e-7 (|
 its rounding, eps / 2 of its size."""
 
 import math
+from fractions import Fraction
 
 import numpy as np
 import pytest
@@ -167,6 +168,26 @@ def test_relative_positions_only():
         s.append(a[0, 0].double() @ b[0, 0].double().T)
     # each turned number is rounded by 2^-11: 128 products of numbers of size about one
     assert (s[0] - s[1]).abs().max() < 4 * 2.0 ** -11 * 128 ** 0.5 * 3
+
+
+@pytest.mark.parametrize("pairing", ["half", "adjacent"])
+def test_large_frequencies_at_far_positions(pairing):
+    """Frequencies up to the largest that a table takes, at the ends of 32 bits: the angle as an exact
+    fraction, so that the bound at the top holds here as for a ladder below one."""
+    f = [1e6, -1e6, 123456.789, 1e3, 12.5, 1.0, 1e5 * math.pi, 777.7]
+    pos = [2 ** 31 - 1, -2 ** 31, 2 ** 31 - 2, -123456789, 1 << 30, 1]
+    g = torch.Generator().manual_seed(16)
+    x = torch.randn(1, 2, len(pos), 16, generator=g).to(torch.float16).cuda()
+    got = bsa.rotary(x, None, torch.tensor([pos], dtype=torch.int32).cuda(), bsa.rotary_table(f), pairing=pairing)[0]
+    two_pi = Fraction("6.28318530717958647692528676655900576839433879875021164194989")
+    before = x.double().cpu().numpy()
+    want = before.copy()
+    for i, w in enumerate(f):
+        a, b = (i, i + len(f)) if pairing == "half" else (2 * i, 2 * i + 1)
+        for t, at in enumerate(pos):
+            turned = (before[:, :, t, a] + 1j * before[:, :, t, b]) * np.exp(1j * float((Fraction(w) * at) % two_pi))
+            want[:, :, t, a], want[:, :, t, b] = turned.real, turned.imag
+    _within(got, before, want, len(f), pairing)
 
 
 def test_streams_and_capture():

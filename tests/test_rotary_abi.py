@@ -42,6 +42,21 @@ def test_table_is_the_fraction_of_a_turn(lib):
         assert off <= abs(Fraction(x) / TWO_PI) / 2 ** 51 + Fraction(1, 2 ** 62), x
 
 
+def test_table_is_within_a_place_of_its_64_bits(lib):
+    """The largest frequencies too, whose turns have 18 bits before the point: two roundings to 2^-64,
+    half a place each, and the second double's own (2^-53 of 2^-36 turns, 2^-106 of 2 pi: nothing)."""
+    r = np.random.default_rng(3)
+    f = [1e6, -1e6, 999999.9, 123456.789, 1e3, 1.0, -1.0, math.pi, -3 * math.pi, 1e5 * math.pi, 5e-324, 1e-30, 0.0,
+         -0.0] + (10.0 ** r.uniform(-12, 6, 500) * r.choice([-1, 1], 500)).tolist() + \
+        [10000.0 ** (-i / 64) for i in range(64)]
+    for at in range(0, len(f), 128):
+        status, out = _table(lib, f[at:at + 128])
+        assert status == 0
+        for x, t in zip(f[at:], out[:, 0]):
+            off = (Fraction(int(t), 2 ** 64) - Fraction(x) / TWO_PI) % 1
+            assert min(off, 1 - off) <= Fraction(1, 2 ** 64) + Fraction(1, 2 ** 80), x
+
+
 def test_table_axes_and_refusals(lib):
     status, out = _table(lib, [1.0, 0.5, 0.25], [2, 0, 7])
     assert status == 0
