@@ -245,11 +245,12 @@ int bsa_rotary(const bsa_rotary_args* a, void* stream) {
     if (!aligned(s.in, 16) || !aligned(s.out, 16)) return BSA_ERR_ALIGN;
     for (int64_t n : {s.in_batch, s.in_head, s.in_token, s.out_batch, s.out_head, s.out_token})
       if (n % 8 != 0) return BSA_ERR_ALIGN;
-    if (s.in == s.out && (s.in_batch != s.out_batch || s.in_head != s.out_head || s.in_token != s.out_token))
-      return BSA_ERR_UNSUPPORTED;
-    // Rows that share a place would be written by several threads.
-    if ((a->B > 1 && s.out_batch == 0) || (s.heads > 1 && s.out_head == 0) || (a->L > 1 && s.out_token == 0))
-      return BSA_ERR_UNSUPPORTED;
+    // Of the dimensions that have more than one place: in place with other strides, and rows that share a
+    // place, which several threads would write.
+    const bool many[3] = {a->B > 1, s.heads > 1, a->L > 1};
+    const int64_t from[3] = {s.in_batch, s.in_head, s.in_token}, to[3] = {s.out_batch, s.out_head, s.out_token};
+    for (int j = 0; j < 3; ++j)
+      if (many[j] && (to[j] == 0 || (s.in == s.out && from[j] != to[j]))) return BSA_ERR_UNSUPPORTED;
     p.side[i] = {s.in, s.out, s.heads, s.in_batch, s.in_head, s.in_token, s.out_batch, s.out_head, s.out_token};
   }
   // One side's output over the other side's tensors: turned twice, or read after it was turned.

@@ -637,9 +637,10 @@ enum {
 };
 
 /* q or k: number x of token t of head h of batch entry b at b * batch + h * head + t * token + x
- * of `in` (and likewise of `out`); strides in elements, multiples of 8 (the stride of a dimension
- * of one is not used).  `out` may be `in` with the same strides; else they do not overlap, nor do
- * two numbers of an output, nor one side's output and the other side's tensors. */
+ * of `in` (and likewise of `out`); strides in elements, all of them multiples of 8 (that of a
+ * dimension of one too, though nothing else is asked of it).  `out` may be `in` with the same strides;
+ * else they do not overlap, nor do two numbers of an output, nor one side's output and the other
+ * side's tensors. */
 typedef struct bsa_rotary_side {
   const void* in;  /* device, dtype, 16-byte aligned */
   void* out;       /* the same                       */

@@ -112,3 +112,22 @@ def test_outputs_that_share_places_are_refused(lib):
     for kw in (dict(q=D, qo=D, ko=D), dict(ko=C), dict(k=A, qo=A), dict(q=D, ko=D), dict(qob=0), dict(qoh=0), dict(qot=0),
                dict(kob=0), dict(koh=0), dict(kot=0)):
         assert f(**kw) == -6, kw
+
+
+def test_strides_of_dimensions_of_one_are_not_compared(lib):
+    """In place, queries of one batch entry, head or token whose unused strides differ between input and
+    output: the check goes on to the keys, which have no pointer here.  With two of them it ends at the
+    queries."""
+    names = ["q", "qo", "H", "qb", "qh", "qt", "qob", "qoh", "qot", "k", "ko", "Hk", "kb", "kh", "kt", "kob", "koh",
+             "kot", "pos", "pa", "pb", "table", "pairs", "axes", "pairing", "inverse", "B", "L", "d", "dtype"]
+    good = dict(zip(names, [A, A, 2, 4096, 512, 64, 4096, 512, 64, 0, 0, 2, 4096, 512, 64, 4096, 512, 64, A, 8,
+                            0, A, 32, 1, 0, 0, 2, 2, 64, 0]))
+
+    def f(**kw):
+        return lib.bsa_rotary(binding._ROTARY_ARGS.pack(*{**good, **kw}.values()), None)
+
+    assert f() == -1
+    for size, stride in (("B", "qob"), ("H", "qoh"), ("L", "qot")):
+        for other in (8192, 0):
+            assert f(**{stride: other}) == -6, stride
+            assert f(**{size: 1, stride: other}) == -1, stride
