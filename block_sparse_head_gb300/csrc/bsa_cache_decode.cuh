@@ -406,17 +406,6 @@ __device__ __forceinline__ void decode_values(const CUtensorMap* tm_v, uint8_t* 
   }
 }
 
-// Adds and returns what was there; the warp's earlier writes (after a __syncwarp) are seen by
-// whoever sees the sum, and this thread sees the others'.
-__device__ __forceinline__ int atomic_add_acq_rel(int* p, int x) {
-  int r;
-  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], %2;"
-               : "=r"(r)
-               : "l"(p), "r"(x)
-               : "memory");
-  return r;
-}
-
 // The second map's weight for output row orow = (token, head), of query heads 2 head, 2 head + 1.
 __device__ __forceinline__ float diff_lam(const CacheFwdParams& p, int64_t orow, int head) {
   return p.lam[p.lam_rows ? orow : head];
@@ -1014,7 +1003,7 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
           if (lane == 0) {
             int* count = parts.count + (blockIdx.x - s.before);
             const int pieces = s.before + 1 + s.more;
-            const bool join_now = atomic_add_acq_rel(count, 1) == pieces - 1;
+            const bool join_now = add_acq_rel(count, 1) == pieces - 1;
             if (join_now) *count = 0;  // as the next call wants it
             err[2] = join_now;
           }

@@ -634,7 +634,7 @@ __device__ __forceinline__ void tile_softmax(const CacheFwdParams& p, uint8_t* s
       if (i == 0 && w8 == 0 && lane == 0) {
         __threadfence();
         int* count = parts.count + (blockIdx.x - seg.before);
-        const bool now = atomic_add_acq_rel(count, 1) == seg.before + seg.more;
+        const bool now = add_acq_rel(count, 1) == seg.before + seg.more;
         if (now) *count = 0;
         *join_flag = now;
       }
