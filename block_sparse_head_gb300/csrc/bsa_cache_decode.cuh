@@ -495,11 +495,11 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
   }
 }
 
-// The same for 32 columns of one output row of differential attention, for units of many pieces:
-// a lone warp's instructions are what a join costs, so that a row's columns go to several warps.
+// The same for 32 columns of one output row of differential attention, for units of few rows: a
+// lone warp's instructions are what a join costs, so that a row's columns go to several warps.
 // Half-warp m has map m, a lane two columns.  Pieces come in blocks, lane i holding the maximum and
 // the sum of the block's piece i; a block's loads are all in flight at once (ten: sixteen spill).
-// One request of 1,000 tokens 10.4 us, 14.0 with two warps of two whole rows each.
+// One request of 1,000 tokens: 10.6 us, 14.0 with two warps of two whole rows each.
 template <class A, int D, int R>
 __device__ __forceinline__ void join_pair(const CacheFwdParams& p, const CacheParts& parts,
                                           const CacheSeg& s, int root, int more, int pair, int col,
@@ -1012,10 +1012,16 @@ __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
       consumer_sync<32 * W>();  // the join buffer is free again
       if (!whole_unit) {
         if (err[2]) {
-          // At most two rows a warp.
+          // join_rows: at most two rows a warp.  Differential attention: join_pair where a warp gets no
+          // more than two of its pieces of columns, whatever the number of partial results.  Eight kv
+          // heads, B requests of 2,048 tokens, 19 / 5 / 1.6 partial results a unit (B = 1, 4, 12),
+          // join_pair against join_rows: 4 rows of d = 128 13.3 / 14.5 / 18.7 us against 17.6 / 16.7 /
+          // 19.6; 8 rows 15.7 / 15.2 / 19.6 against 17.7 / 16.3 / 19.6; 16 rows of d = 64 17.2 / 17.1 /
+          // 21.9 against 19.0 / 18.0 / 21.9; 16 rows of d = 128 22.8 / 21.4 / 28.1 against 20.2 / 20.1 /
+          // 26.6.
           if constexpr (DIFF) {
             const int root = blockIdx.x - s.before, more = s.before + s.more, rows = s.nq * p.group;
-            if (more >= 4) {
+            if constexpr (R * (D / 64) <= 2 * W) {
               for (int i = warp; i < rows * (D / 64); i += W)
                 join_pair<A, D, R>(p, parts, s, root, more, i / (D / 32), 32 * (i % (D / 32)), lane);
             } else if (2 * warp < rows) {

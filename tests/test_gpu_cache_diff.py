@@ -141,6 +141,14 @@ def test_cut_units_are_joined(news):
     DiffCase([6000], news, 8, 1, True, rows=False, seed=8).check()
 
 
+@pytest.mark.parametrize("B", [30, 60, 100])
+@pytest.mark.parametrize("n,d", [(1, 128), (4, 128), (4, 64)])
+def test_units_cut_into_few_pieces(B, n, d):
+    """One to five partial results a unit, of 4 rows and of 16."""
+    DiffCase([900 - 7 * i for i in range(B)], [n] * B, 4, 1, d=d, page=32, seed=B + n + d).check(
+        max_q=n, sinks=torch.randn(4, device="cuda"))
+
+
 @pytest.mark.parametrize("news", [[3, 1, 2], [70, 1, 20]])
 def test_more_queries_than_tokens(news):
     c = DiffCase([2, 0, 0], news, 4, 2, seed=6)
