@@ -152,6 +152,115 @@ def test_repeatable_and_on_another_stream():
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("block,d,dq", [(64, 64, 64), (128, 128, 128), (64, 128, 64)])
+@pytest.mark.parametrize("rows", [False, True])
+def test_weights_far_from_one(block, d, dq, rows):
+    """|lam| from 2 to 30, of both signs: D_0 = <dO, out> + lam D_1 is the small difference of large
+    numbers, whose roundings the bounds count."""
+    L = 9 * block - 5
+    q, k, v, lam, do = _inputs(1, 4, 2, L, d, dq, rows, 97 + block + d + dq)
+    lam = torch.where(lam > 0.4, 2.0 + 28.0 * lam.clamp(0, 1), -2.0 - 20.0 * lam.abs())
+    _check(q, k, v, lam, do, torch.tril(torch.ones(2, 9, 9, dtype=torch.int32)), 1 / math.sqrt(dq), block, True)
+
+
+@pytest.mark.parametrize("block", [64, 128])
+def test_key_halves_of_a_long_sequence(block):
+    nb = -(-2999 // block)
+    q, k, v, lam, do = _inputs(1, 4, 2, 2999, 128, 64, True, 98 + block)
+    _check(q, k, v, lam, do, torch.tril(_layout(2, nb, 99, 0.3)), 0.125, block, True)
+
+
+def test_a_key_half_that_is_not_finite_spoils_its_block_alone():
+    """NaN and infinity among the numbers of one map's key half and of a value: rows that see their
+    block may be lost, the others keep their bits, gradients of other blocks' keys too."""
+    block, L = 64, 6 * 64
+    q, k, v, lam, do = _inputs(1, 2, 1, L, 128, 64, True, 101)
+    lay = torch.zeros(1, 6, 6, dtype=torch.int32)
+    lay[0, :, 0], lay[0, 3, 2], lay[0, torch.arange(6), torch.arange(6)] = 1, 1, 1
+    lay[0, 5, 5] = 0
+    lut = bsa.build_lut(lay, 1)
+
+    def step(k, v):
+        out, lse, out2 = bsa.diff_forward(q, k, v, lam, lut, 0.125, block, True, training=True)
+        return (out, lse, out2) + bsa.diff_backward(q, k, v, lam, out, out2, lse, do, lut, 0.125, block, True)
+
+    want = step(k, v)
+    kb, vb = k.clone(), v.clone()
+    kb[0, 0, 2 * block + 5, 70], kb[0, 0, 2 * block + 9, 3], vb[0, 0, 2 * block + 7, 11] = math.nan, math.inf, -math.inf
+    got = step(kb, vb)
+    assert lut.device_status()[0] == 0
+    keep = torch.ones(L, dtype=torch.bool, device="cuda")
+    for row in (2, 3):  # rows that see block 2
+        keep[row * block:(row + 1) * block] = False
+    for a, b in zip(got[:4] + got[6:], want[:4] + want[6:]):
+        assert torch.equal(a[:, :, keep], b[:, :, keep])
+    for a, b in zip(got[4:6], want[4:6]):  # keys that only rows without block 2 see
+        for c in (1, 4, 5):
+            assert torch.equal(a[:, :, c * block:(c + 1) * block], b[:, :, c * block:(c + 1) * block])
+
+
+def test_captured_behind_a_memset_and_another_stream():
+    """The graph's node before the first kernel is no kernel, and the second call has two of them
+    before it, one of another stream."""
+    q, k, v, lam, do = _inputs(1, 2, 2, 500, 64, 64, False, 102)
+    lut = bsa.build_lut(torch.tril(torch.ones(2, 8, 8, dtype=torch.int32)), 1)
+    source = [t.clone() for t in (q, v, do)]
+
+    def step(side=None):
+        q.zero_()
+        here = torch.cuda.current_stream()
+        if side is not None:
+            side.wait_stream(here)
+            with torch.cuda.stream(side):
+                v.copy_(source[1])
+                v.mul_(0.5)
+        else:
+            v.copy_(source[1])
+            v.mul_(0.5)
+        q.copy_(source[0])
+        q.mul_(2.0)
+        if side is not None:
+            here.wait_stream(side)
+        out, lse, out2 = bsa.diff_forward(q, k, v, lam, lut, 0.125, 64, True, training=True)
+        do.zero_()
+        first = bsa.diff_backward(q, k, v, lam, out, out2, lse, do, lut, 0.125, 64, True)
+        do.copy_(source[2])
+        return (out, lse, out2) + first + bsa.diff_backward(q, k, v, lam, out, out2, lse, do, lut, 0.125, 64, True)
+
+    want = [t.clone() for t in step()]
+    side, other = torch.cuda.Stream(), torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side), torch.cuda.graph(graph, stream=side):
+        held = step(other)
+    for _ in range(3):
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip(held, want):
+            assert torch.equal(a, b)
+
+
+def test_behind_a_library_product():
+    """Kernels of other libraries right before and behind each call, on one stream."""
+    lut = bsa.build_lut(_layout(2, 8, 75), 1)
+    q, k, v, lam, do = _inputs(1, 8, 2, 1000, 128, 128, True, 103)
+    a = torch.randn(4096, 4096, device="cuda", dtype=torch.bfloat16)
+
+    def step(product):
+        product()
+        out, lse, out2 = bsa.diff_forward(q, k, v, lam, lut, 0.1, 128, True, training=True)
+        product()
+        got = (out, lse, out2) + bsa.diff_backward(q, k, v, lam, out, out2, lse, do, lut, 0.1, 128, True)
+        product()
+        return got
+
+    want = step(lambda: None)
+    for _ in range(20):
+        for x, y in zip(step(lambda: a @ a), want):
+            assert torch.equal(x, y)
+    assert lut.device_status()[0] == 0
+
+
 def test_two_streams_at_once():
     """Forwards and backwards on two streams that share the LUT, with nothing between them: the
     same bits as one after another."""
