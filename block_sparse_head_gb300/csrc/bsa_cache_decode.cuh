@@ -499,7 +499,7 @@ __device__ __forceinline__ void join_rows(const CacheFwdParams& p, const CachePa
 // lone warp's instructions are what a join costs, so that a row's columns go to several warps.
 // Half-warp m has map m, a lane two columns.  Pieces come in blocks, lane i holding the maximum and
 // the sum of the block's piece i; a block's loads are all in flight at once (ten: sixteen spill).
-// One request of 1,000 tokens: 10.6 us, 14.0 with two warps of two whole rows each.
+// One request of 1,000 tokens: 10.9 us, 14.0 with two warps of two whole rows each.
 template <class A, int D, int R>
 __device__ __forceinline__ void join_pair(const CacheFwdParams& p, const CacheParts& parts,
                                           const CacheSeg& s, int root, int more, int pair, int col,
@@ -555,9 +555,9 @@ __device__ __forceinline__ void join_pair(const CacheFwdParams& p, const CachePa
 // (a unit's rows are its queries times an even number of heads), both in one lane, which stores
 // their difference.  Keys and values are read once for both; queries of d / 2 numbers are loaded
 // into their map's half of a row of zeros.  Measured, 16 heads of two maps, 8 kv heads, d = 128,
-// e4m3: 64 requests of 2,048 to 8,192 tokens 112 us, 5.9 TB/s (plain attention of 32 heads 111); 16
+// e4m3: 64 requests of 2,048 to 8,192 tokens 113 us, 5.9 TB/s (plain attention of 32 heads 111); 16
 // requests of 4 queries, window 1,000, int8, pages of 16, key halves 24 us; one request of 1,000
-// tokens 10.6 us.
+// tokens 10.9 us.
 template <class A, class C, int D, int NT, bool DIFF>
 __global__ void __launch_bounds__(DecodeCfg<D, NT>::kThreads, 1)
     bsa_cache_decode_kernel(const __grid_constant__ CUtensorMap tm_k,

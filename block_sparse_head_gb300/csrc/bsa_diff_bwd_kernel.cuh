@@ -34,9 +34,9 @@
 // once.  Every wait is bounded (WaitCtl), as in the plain kernels.
 //
 // Bound: the chain of a step, products -> TMEM loads -> exponentials and dS -> TMEM stores ->
-// products; the tensor pipe works 49 % of the time in both walks.  Timing copies without one part
-// each: no row terms -1 %, no exponentials -2 %, a quarter of the first products -14 %, of the
-// second ones -7 %.
+// products; the tensor pipe works 52 % of the dQ walk's time and 49 % of the other's.  Timing copies
+// without one part each: no row terms -1 %, no exponentials -2 %, a quarter of the first products
+// -14 %, of the second ones -7 %.
 // Measured (dQ + dK/dV): 16 heads of 128 on 4 kv heads, 8,192 tokens, block 128, a band and a
 // stride: 185 + 205 us, 1,090 TFLOP/s (0.58 of a cuBLAS bf16 product; 0.39 without the scores and
 // dP that the second walk computes again); 2 x 8 heads of 64, 2,999 tokens, block 64, a window

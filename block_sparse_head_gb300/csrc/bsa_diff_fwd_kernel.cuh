@@ -18,7 +18,7 @@
 // Measured: 16 heads of 128 on 4 kv heads, 16,384 tokens, block 128, a band and a stride: 255 us,
 // 1,400 TFLOP/s (0.74 of a cuBLAS bf16 product; the plain forward on 32 such heads takes 255 too);
 // 8,192 tokens 109 us; 2 x 8 heads of 64, 2,999 tokens, block 64, a window and a global block: 21
-// us; 4 heads of 64, 512 tokens: 6.6 us, an item's way.  The tensor pipe works 59 % of the time,
+// us; 4 heads of 64, 512 tokens: 6.8 us, an item's way.  The tensor pipe works 59 % of the time,
 // the exponentials' unit 30 %.
 // What counted: both maps in one tile rather than two passes over the keys; queries by a warp of
 // their own, an item ahead (306 us with the keys' warp); O released before the output's stores,
